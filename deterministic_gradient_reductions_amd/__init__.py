@@ -15,9 +15,20 @@ Functions (same names as the C ABI):
     det_grouped_wgrad_acc(main_grad, G, X, offs, cfg=None, atomic=False)
     det_grouped_dbias(dbias, dA, offs, cfg=None, atomic=False)
     det_topk_canonicalize(ids, logits, ids_out, logits_out, probs)
+    det_router_balance(logits, ids, offs, counts, prob_sum, loss, coeff=1.0, score="softmax")
+    det_router_balance_bwd(dlogits, logits, offs, counts, dloss, topk, coeff=1.0, score="softmax")
+    det_topk_distill(logits, ids, teacher, loss, lse, tau=1.0)
+    det_topk_distill_bwd(dlogits, logits, ids, teacher, lse, dloss, tau=1.0)
+    det_block_norm(x, f, y, gate=, w_post=, alpha=, w_pre=, h=, rstd_post=, rstd_pre=, eps=1e-6)
+    det_block_norm_bwd(dy, x, f, dx, df, dh=, gate=, w_post=, alpha=, w_pre=, rstd_post=, rstd_pre=, dgate=,
+                       dw_post=, dalpha=, dw_pre=)
 Every function accepts ``ws=`` (a Workspace or a uint8 device tensor) and
 ``stream=`` (a torch.cuda.Stream); by default a cached per-stream workspace
-and torch's current stream are used.
+and torch's current stream are used. The router balance, distillation and block
+norm functions take no cached workspace: without ``ws=`` they allocate one from
+torch's caching allocator on the call's stream (so it is safe inside a graph
+capture), and without ``stream=`` they use the current stream of the tensors'
+device, whichever device is current.
 """
 from __future__ import annotations
 
@@ -32,7 +43,9 @@ __all__ = [
     "det_grouped_wgrad_acc", "det_grouped_wgrad_acc_workspace_size", "det_grouped_wgrad_acc_bf16",
     "det_grouped_wgrad_acc_bf16_workspace_size", "det_grouped_dbias",
     "det_grouped_dbias_workspace_size", "det_topk_canonicalize", "det_workspace_init", "det_detmath_eval", "det_mfma_eval",
-    "det_mfma_rate", "DET_OK", "DET_ERR_INVALID_ARG", "DET_ERR_UNSUPPORTED", "DET_ERR_WORKSPACE", "DET_ERR_OVERLAP", "DET_ERR_HIP",
+    "det_mfma_rate", "det_router_balance", "det_router_balance_bwd", "det_router_balance_workspace_size",
+    "det_topk_distill", "det_topk_distill_bwd", "det_topk_distill_workspace_size", "det_block_norm",
+    "det_block_norm_bwd", "det_block_norm_bwd_workspace_size", "DET_OK", "DET_ERR_INVALID_ARG", "DET_ERR_UNSUPPORTED", "DET_ERR_WORKSPACE", "DET_ERR_OVERLAP", "DET_ERR_HIP",
 ]
 
 DET_OK, DET_ERR_INVALID_ARG, DET_ERR_UNSUPPORTED, DET_ERR_WORKSPACE, DET_ERR_OVERLAP, DET_ERR_HIP = 0, -1, -2, -3, -4, -5
@@ -74,6 +87,7 @@ _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _INT = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F64 = ctypes.c_double
 
 _SIGS = {
     "det_abi_version": ([], _INT),
@@ -114,6 +128,19 @@ _SIGS = {
                                                    ctypes.POINTER(_SZ)], _INT),
     "det_grouped_wgrad_acc_bf16": ([_P, _I64, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _I64, _I64,
                                     ctypes.POINTER(WgradCfg), _P, _SZ, _P], _INT),
+    "det_router_balance_workspace_size": ([_I64, _I64, _I64, _I64, ctypes.POINTER(_SZ)], _INT),
+    "det_router_balance": ([_P, _I64, _INT, _P, _I64, _I64, _I64, _I64, _P, _I64, _INT, _F64, _P, _P, _P, _P, _SZ, _P],
+                           _INT),
+    "det_router_balance_bwd": ([_P, _I64, _P, _I64, _INT, _I64, _I64, _I64, _P, _I64, _P, _P, _INT, _F64, _P], _INT),
+    "det_topk_distill_workspace_size": ([_I64, _I64, _I64, ctypes.POINTER(_SZ)], _INT),
+    "det_topk_distill": ([_P, _I64, _INT, _P, _I64, _P, _I64, _INT, _I64, _I64, _I64, _F64, _P, _P, _P, _SZ, _P], _INT),
+    "det_topk_distill_bwd": ([_P, _I64, _P, _I64, _INT, _P, _I64, _P, _I64, _INT, _I64, _I64, _I64, _F64, _P, _P, _P],
+                             _INT),
+    "det_block_norm": ([_P, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _P, _INT, _I64, _I64, _F64, _P, _I64, _P, _I64, _P,
+                        _P, _P], _INT),
+    "det_block_norm_bwd_workspace_size": ([_I64, _I64, ctypes.POINTER(_SZ)], _INT),
+    "det_block_norm_bwd": ([_P, _I64] * 5 + [_I64] + [_P] * 5 + [_INT, _I64, _I64] + [_P, _I64] * 3 +
+                           [_P] * 4 + [_SZ, _P], _INT),
 }
 
 _lib = None
@@ -511,3 +538,247 @@ def det_mfma_rate(ops, out, blocks: int, iters: int, stream=None) -> None:
     if not (ops.is_contiguous() and out.is_contiguous()):
         raise ValueError("ops and out must be contiguous")
     _check(lib().det_mfma_rate(_ptr(ops), ops.numel(), _ptr(out), out.numel(), blocks, iters, _stream_handle(stream)))
+
+
+# ------------------------------------------ router balance, distillation, block norms
+_DTYPE_CODES = {}
+
+
+def _float_code(t, name: str) -> int:
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.bfloat16: DET_BF16, torch.float32: DET_F32})
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+    return code
+
+
+def _rows(t, name: str, shape, dtype=None) -> int:
+    """Check a 2-D tensor's shape, dtype and unit column stride; return its row stride in elements."""
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have unit innermost stride" % name)
+    return t.stride(0) if shape[0] > 1 else max(shape[1], 1)
+
+
+def _flat(t, name: str, shape, dtype) -> None:
+    """Check a contiguous tensor's shape and dtype."""
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+class _Launch:
+    """The device, stream and workspace of one call: every tensor on one GPU, that GPU current during the
+    call, the workspace allocated on the call's stream (freed to that stream's pool when the call returns)."""
+
+    def __init__(self, tensors, need, ws, stream):
+        import torch
+        dev = tensors[0].device
+        for t in tensors:
+            if t is not None and (t.device != dev or not t.is_cuda):
+                raise ValueError("all tensors must be on one GPU, got %s and %s" % (dev, t.device))
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
+        self.stream = ctypes.c_void_p(stream.cuda_stream)
+        self.keep, self.ws, self.nbytes = ws, ctypes.c_void_p(0), 0
+        if isinstance(ws, Workspace):
+            if ws._buf.device != dev:
+                raise ValueError("the workspace is on %s, the tensors on %s" % (ws._buf.device, dev))
+            self.ws, self.nbytes = ctypes.c_void_p(ws.ptr), ws.nbytes
+        elif ws is not None:
+            if ws.device != dev or not ws.is_contiguous():
+                raise ValueError("the workspace must be a contiguous tensor on %s" % dev)
+            self.ws, self.nbytes = ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size()
+        elif need:
+            if stream == torch.cuda.current_stream(dev):
+                self.keep = torch.empty(need + 256, dtype=torch.uint8, device=dev)
+            else:
+                with torch.cuda.stream(stream):
+                    self.keep = torch.empty(need + 256, dtype=torch.uint8, device=dev)
+            self.ws, self.nbytes = ctypes.c_void_p((self.keep.data_ptr() + 255) // 256 * 256), need
+        self.other = dev if dev.index != torch.cuda.current_device() else None
+
+    def call(self, fn, *args) -> None:
+        if self.other is None:
+            _check(fn(*args))
+        else:
+            import torch
+            with torch.cuda.device(self.other):
+                _check(fn(*args))
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score_code(score) -> int:
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid', got %r" % (score,))
+    return _SCORES[score]
+
+
+def det_router_balance_workspace_size(T: int, E: int, K: int, S: int) -> int:
+    n = _SZ()
+    _check(lib().det_router_balance_workspace_size(T, E, K, S, ctypes.byref(n)))
+    return n.value
+
+
+def det_router_balance(logits, ids, offs, counts, prob_sum, loss, coeff: float = 1.0, score: str = "softmax", ws=None,
+                       stream=None) -> None:
+    """loss[s] = coeff * E / (K * N_s^2) * sum_e counts[s, e] * prob_sum[s, e] over the tokens
+    offs[s] <= t < offs[s + 1]. logits bf16 or float32 [T, E], ids int32 [T, K], offs int32 [S + 1]; overwrites
+    counts int32 [S, E], prob_sum float32 [S, E] and loss float32 [S]."""
+    import torch
+    code, sc = _float_code(logits, "logits"), _score_code(score)
+    if logits.dim() != 2 or ids.dim() != 2 or offs.dim() != 1 or offs.numel() < 1:
+        raise ValueError("need logits [T, E], ids [T, K] and offs [S + 1]")
+    T, E = logits.shape
+    K, S = ids.shape[1], offs.numel() - 1
+    ld = _rows(logits, "logits", (T, E))
+    ids_ld = _rows(ids, "ids", (T, K), torch.int32)
+    _flat(offs, "offs", (S + 1,), torch.int32)
+    _flat(counts, "counts", (S, E), torch.int32)
+    _flat(prob_sum, "prob_sum", (S, E), torch.float32)
+    _flat(loss, "loss", (S,), torch.float32)
+    need = det_router_balance_workspace_size(T, E, K, S)
+    c = _Launch((logits, ids, offs, counts, prob_sum, loss), need, ws, stream)
+    c.call(lib().det_router_balance, _ptr(logits), ld, code, _ptr(ids), ids_ld, T, E, K, _ptr(offs), S, sc,
+           float(coeff), _ptr(counts), _ptr(prob_sum), _ptr(loss), c.ws, c.nbytes, c.stream)
+
+
+def det_router_balance_bwd(dlogits, logits, offs, counts, dloss, topk: int, coeff: float = 1.0, score: str = "softmax",
+                           stream=None) -> None:
+    """dlogits = the gradient of sum_s dloss[s] * loss[s] of det_router_balance (rows of tokens in a sequence are
+    overwritten, the others left as they were). counts int32 [S, E], dloss float32 [S], topk = K."""
+    import torch
+    code, sc = _float_code(logits, "logits"), _score_code(score)
+    if logits.dim() != 2 or offs.dim() != 1 or offs.numel() < 1:
+        raise ValueError("need logits [T, E] and offs [S + 1]")
+    T, E = logits.shape
+    S = offs.numel() - 1
+    ld = _rows(logits, "logits", (T, E))
+    ld_d = _rows(dlogits, "dlogits", (T, E), logits.dtype)
+    _flat(offs, "offs", (S + 1,), torch.int32)
+    _flat(counts, "counts", (S, E), torch.int32)
+    _flat(dloss, "dloss", (S,), torch.float32)
+    c = _Launch((dlogits, logits, offs, counts, dloss), 0, None, stream)
+    c.call(lib().det_router_balance_bwd, _ptr(dlogits), ld_d, _ptr(logits), ld, code, T, E, int(topk), _ptr(offs), S,
+           _ptr(counts), _ptr(dloss), sc, float(coeff), c.stream)
+
+
+def det_topk_distill_workspace_size(T: int, V: int, K: int) -> int:
+    n = _SZ()
+    _check(lib().det_topk_distill_workspace_size(T, V, K, ctypes.byref(n)))
+    return n.value
+
+
+def _distill_operands(logits, ids, teacher):
+    import torch
+    code, t_code = _float_code(logits, "logits"), _float_code(teacher, "teacher")
+    if logits.dim() != 2 or ids.dim() != 2:
+        raise ValueError("need logits [T, V], ids and teacher [T, K]")
+    T, V = logits.shape
+    K = ids.shape[1]
+    return (_ptr(logits), _rows(logits, "logits", (T, V)), code, _ptr(ids), _rows(ids, "ids", (T, K), torch.int32),
+            _ptr(teacher), _rows(teacher, "teacher", (T, K)), t_code, T, V, K)
+
+
+def det_topk_distill(logits, ids, teacher, loss, lse, tau: float = 1.0, ws=None, stream=None) -> None:
+    """loss[t] = KL(teacher's top K || student) at temperature tau, lse[t] = logsumexp(logits[t] / tau).
+    logits bf16 or float32 [T, V]; ids int32 [T, K] (outside [0, V): unused slots); teacher bf16 or float32 [T, K]
+    logits; overwrites loss and lse float32 [T]."""
+    import torch
+    ops = _distill_operands(logits, ids, teacher)
+    T, V, K = ops[-3:]
+    _flat(loss, "loss", (T,), torch.float32)
+    _flat(lse, "lse", (T,), torch.float32)
+    need = det_topk_distill_workspace_size(T, V, K)
+    c = _Launch((logits, ids, teacher, loss, lse), need, ws, stream)
+    c.call(lib().det_topk_distill, *ops, float(tau), _ptr(loss), _ptr(lse), c.ws, c.nbytes, c.stream)
+
+
+def det_topk_distill_bwd(dlogits, logits, ids, teacher, lse, dloss, tau: float = 1.0, stream=None) -> None:
+    """dlogits = the gradient of sum_t dloss[t] * loss[t] of det_topk_distill (overwritten; a row whose dloss is 0 or
+    that has no teacher mass is zeros). lse float32 [T] from the forward, dloss float32 [T]."""
+    import torch
+    ops = _distill_operands(logits, ids, teacher)
+    T, V, _ = ops[-3:]
+    ld_d = _rows(dlogits, "dlogits", (T, V), logits.dtype)
+    _flat(lse, "lse", (T,), torch.float32)
+    _flat(dloss, "dloss", (T,), torch.float32)
+    c = _Launch((dlogits, logits, ids, teacher, lse, dloss), 0, None, stream)
+    c.call(lib().det_topk_distill_bwd, _ptr(dlogits), ld_d, *ops, float(tau), _ptr(lse), _ptr(dloss), c.stream)
+
+
+def _norm_row(t, name, T, cols, dtype):
+    return (_ptr(None), 0) if t is None else (_ptr(t), _rows(t, name, (T, cols), dtype))
+
+
+def _norm_vec(t, name, n):
+    import torch
+    if t is not None:
+        _flat(t, name, (n,), torch.float32)
+    return _ptr(t)
+
+
+def _gate_cols(gate, D: int) -> int:
+    if gate is None:
+        return 0
+    if gate.dim() != 2 or gate.shape[1] not in (1, D):
+        raise ValueError("gate must be [T, D] or [T, 1]")
+    return gate.shape[1]
+
+
+def det_block_norm(x, f, y, gate=None, w_post=None, alpha=None, w_pre=None, h=None, rstd_post=None, rstd_pre=None,
+                   eps: float = 1e-6, stream=None) -> None:
+    """y = x + alpha * sigmoid(gate) * (w_post * f / rms(f)); h = w_pre * y / rms(y). x, f, y, h bf16 or float32 [T, D],
+    gate [T, D] or [T, 1] of the same dtype, w_post, alpha, w_pre float32 [D]; each of gate, w_post, alpha and w_pre may
+    be left out. Overwrites y, h (with w_pre) and the norms' factors rstd_post (with w_post) and rstd_pre (with w_pre),
+    float32 [T]."""
+    code = _float_code(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [T, D]")
+    (T, D), dt, gc = x.shape, x.dtype, _gate_cols(gate, x.shape[1])
+    args = (*_norm_row(x, "x", T, D, dt), *_norm_row(f, "f", T, D, dt), *_norm_row(gate, "gate", T, gc, dt), gc,
+            _norm_vec(w_post, "w_post", D), _norm_vec(alpha, "alpha", D), _norm_vec(w_pre, "w_pre", D), code, T, D,
+            float(eps), *_norm_row(y, "y", T, D, dt), *_norm_row(h, "h", T, D, dt),
+            _norm_vec(rstd_post, "rstd_post", T), _norm_vec(rstd_pre, "rstd_pre", T))
+    c = _Launch((x, f, y, gate, w_post, alpha, w_pre, h, rstd_post, rstd_pre), 0, None, stream)
+    c.call(lib().det_block_norm, *args, c.stream)
+
+
+def det_block_norm_bwd_workspace_size(T: int, D: int) -> int:
+    n = _SZ()
+    _check(lib().det_block_norm_bwd_workspace_size(T, D, ctypes.byref(n)))
+    return n.value
+
+
+def det_block_norm_bwd(dy, x, f, dx, df, dh=None, gate=None, w_post=None, alpha=None, w_pre=None, rstd_post=None,
+                       rstd_pre=None, dgate=None, dw_post=None, dalpha=None, dw_pre=None, ws=None,
+                       stream=None) -> None:
+    """The gradients of det_block_norm from dy and dh: overwrites dx, df and dgate, accumulates the parameter gradients
+    dw_post, dalpha, dw_pre (float32 [D]) in a fixed order. The optional arguments are given as in the forward, each
+    with its gradient; x may be None without w_pre."""
+    code = _float_code(dy, "dy")
+    if dy.dim() != 2:
+        raise ValueError("dy must be [T, D]")
+    (T, D), dt, gc = dy.shape, dy.dtype, _gate_cols(gate, dy.shape[1])
+    args = (*_norm_row(dy, "dy", T, D, dt), *_norm_row(dh, "dh", T, D, dt), *_norm_row(x, "x", T, D, dt),
+            *_norm_row(f, "f", T, D, dt), *_norm_row(gate, "gate", T, gc, dt), gc, _norm_vec(w_post, "w_post", D),
+            _norm_vec(alpha, "alpha", D), _norm_vec(w_pre, "w_pre", D), _norm_vec(rstd_post, "rstd_post", T),
+            _norm_vec(rstd_pre, "rstd_pre", T), code, T, D, *_norm_row(dx, "dx", T, D, dt),
+            *_norm_row(df, "df", T, D, dt), *_norm_row(dgate, "dgate", T, gc, dt), _norm_vec(dw_post, "dw_post", D),
+            _norm_vec(dalpha, "dalpha", D), _norm_vec(dw_pre, "dw_pre", D))
+    need = 0 if w_post is None and alpha is None and w_pre is None else det_block_norm_bwd_workspace_size(T, D)
+    c = _Launch((dy, x, f, dx, df, dh, gate, w_post, alpha, w_pre, rstd_post, rstd_pre, dgate, dw_post, dalpha, dw_pre),
+                need, ws, stream)
+    c.call(lib().det_block_norm_bwd, *args, c.ws, c.nbytes, c.stream)

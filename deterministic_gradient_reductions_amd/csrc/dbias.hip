@@ -28,77 +28,13 @@
 // read once (4 bytes per tile and column, 1/64 of dA's bytes at block_m 128);
 // dbias is read and written once. The tile kernel is HBM-bound.
 #include "common.hpp"
+#include "segtiles.hpp"
 
 namespace detgrad {
 namespace {
 
 // Columns per workgroup: 64 lanes x CPL (8, 4 or 2 columns per lane, one
 // 16-, 8- or 4-byte load per row), the configuration's block_n.
-
-// Inclusive scans over the 64 lanes on DPP (row shifts by 1, 2, 4, 8, then
-// the last lane of row 0 into rows 1 and 3 and of row 1 into rows 2 and 3);
-// lanes without a source read 0, the identity of both (the values are >= 0).
-template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ uint32_t dpp_src(uint32_t v) {
-  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROW_MASK, 0xF, false));
-}
-__device__ __forceinline__ uint32_t scan_add(uint32_t v) {
-  v += dpp_src<0x111, 0xF>(v); v += dpp_src<0x112, 0xF>(v); v += dpp_src<0x114, 0xF>(v);
-  v += dpp_src<0x118, 0xF>(v); v += dpp_src<0x142, 0xA>(v); v += dpp_src<0x143, 0xC>(v);
-  return v;
-}
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint32_t scan_max(uint32_t v) {
-  v = umax(v, dpp_src<0x111, 0xF>(v)); v = umax(v, dpp_src<0x112, 0xF>(v)); v = umax(v, dpp_src<0x114, 0xF>(v));
-  v = umax(v, dpp_src<0x118, 0xF>(v)); v = umax(v, dpp_src<0x142, 0xA>(v)); v = umax(v, dpp_src<0x143, 0xC>(v));
-  return v;
-}
-// the value of the lane below, `fill` in lane 0 (DPP wave_shr:1 with the fill
-// as the old value; computed with every lane active, never under a branch)
-__device__ __forceinline__ uint32_t from_lane_below(uint32_t v, uint32_t fill) {
-  return static_cast<uint32_t>(
-      __builtin_amdgcn_update_dpp(static_cast<int>(fill), static_cast<int>(v), 0x138, 0xF, 0xF, false));
-}
-__device__ __forceinline__ uint32_t lane_value(uint32_t v, int j) {
-  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), j));
-}
-__device__ __forceinline__ uint32_t clamp_off(int32_t o, uint32_t M) {
-  const uint32_t v = o < 0 ? 0u : static_cast<uint32_t>(o);
-  return v < M ? v : M;
-}
-
-// Expert tile table, computed by every workgroup from the device offsets:
-// b_e = min(M, max(0, offs[0..e])) (clamped monotone), tiles_e =
-// ceil((b_{e+1} - b_e) / block_m), tile_start_e = sum of tiles before e.
-// Returns the expert of global tile t (false past the last tile) and its rows.
-__device__ bool tile_of(const int32_t* __restrict__ offs, int E, uint32_t M, int log_bm, uint32_t t, int& e_out,
-                        uint32_t& r0, uint32_t& r1) {
-  const int lane = threadIdx.x & 63;
-  const uint32_t bm = 1u << log_bm;
-  uint32_t run_b = clamp_off(offs[0], M);  // b of the first expert of the chunk
-  uint32_t run_t = 0;                      // tiles before the chunk
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    // b_{e+1}: running max of the offsets (lanes past E repeat offs[E])
-    const uint32_t b1 = umax(scan_max(clamp_off(offs[e < E ? e + 1 : E], M)), run_b);
-    const uint32_t b0 = from_lane_below(b1, run_b);
-    const uint32_t nt = (e < E && b1 > b0) ? (b1 - b0 + bm - 1) >> log_bm : 0u;
-    const uint32_t incl = scan_add(nt);
-    const uint32_t first = run_t + incl - nt;
-    const uint64_t hit = __ballot(e < E && t >= first && t < first + nt);
-    if (hit) {
-      const int j = __builtin_ctzll(hit);
-      e_out = e0 + j;
-      r0 = lane_value(b0, j) + ((t - lane_value(first, j)) << log_bm);
-      const uint32_t hi = lane_value(b1, j);
-      r1 = r0 + bm < hi ? r0 + bm : hi;
-      return true;
-    }
-    run_t += lane_value(incl, 63);
-    run_b = lane_value(b1, 63);
-  }
-  return false;
-}
 
 // One row of a lane's CPL columns as CPL / 2 words (two bf16 each).
 template <int CPL>
@@ -177,17 +113,7 @@ __global__ __launch_bounds__(256) void dbias_tile_kernel(const uint16_t* __restr
   // tile run side by side, so the workgroups in flight read whole rows)
   const uint32_t cb = blockIdx.x % ncb;
   if (!ATOMIC && blockIdx.x == 0 && wave == 0) {
-    uint32_t run_b = 0, run_t = 0;
-    for (int e0 = 0; e0 <= E; e0 += 64) {
-      const int ee = e0 + lane;
-      const uint32_t b = umax(scan_max(clamp_off(ee <= E ? offs[ee] : 0, Mu)), run_b);  // b_ee
-      const uint32_t bp = from_lane_below(b, e0 == 0 ? b : run_b);                     // b_{ee-1}
-      const uint32_t nt = (ee >= 1 && ee <= E && b > bp) ? (b - bp + BM - 1) / BM : 0u;  // tiles of expert ee-1
-      const uint32_t incl = scan_add(nt);
-      if (ee <= E) tstart[ee] = static_cast<int32_t>(run_t + incl);  // tiles of experts before ee
-      run_t += lane_value(incl, 63);
-      run_b = lane_value(b, 63);
-    }
+    write_tile_table(offs, E, Mu, LOG_BM, tstart);
   }
   const uint32_t t = blockIdx.x / ncb;
   int e;

@@ -1,0 +1,374 @@
+// det_topk_distill / det_topk_distill_bwd: distillation from a teacher's top
+// logits, per token t over a vocabulary of V words.
+//
+//   x = z / tau,  lse = log sum_v exp(x_v)
+//   q = softmax of teacher / tau over the valid slots (0 <= id < V)
+//   loss = sum_k q_k (log q_k - x[id_k] + lse)          (slots with q_k = 0 add nothing)
+//   dz_v = dloss / tau (exp(x_v - lse) - sum of q_k over the slots with id_k = v)
+//
+// A row without teacher mass (no valid slot, or only -inf there) has loss 0 and
+// a zero gradient row, and so has a row whose dloss is 0, whatever its logits.
+//
+// Forward: one pass over the row with a running maximum and sum per lane
+// (rescaled when the maximum grows), joined over the lanes, the waves and, when
+// the call has few rows, the workgroups that share a row, always in one fixed
+// order. Backward: dz of a piece of the row is written in one streaming pass,
+// then the workgroup rewrites the at most K elements that a teacher slot names.
+// Both are bound by the logits' bytes.
+#include "rowops.hpp"
+
+namespace detgrad {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kStep = kThreads * 8;  // elements one workgroup takes per access
+constexpr int kMaxK = 1024;
+
+// Running (maximum, sum of exp(x - maximum)) in units of z, c = log2(e) / tau.
+struct MaxSum {
+  float m, s;
+};
+
+__device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// m stays -inf until an element above -inf is seen; its factor is then taken
+// against 0, and every exp(-inf) is 0.
+__device__ __forceinline__ float finite_ref(float m) { return m == -__builtin_inff() ? 0.0f : m; }
+
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
+  const float m = fmaxf(a.m, b.m), r = finite_ref(m);
+  return {m, a.s * pow2((a.m - r) * c) + b.s * pow2((b.m - r) * c)};
+}
+
+__device__ __forceinline__ MaxSum wave_join(MaxSum a, float c) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const MaxSum o{__shfl_xor(a.m, d), __shfl_xor(a.s, d)};
+    a = join(a, o, c);
+  }
+  return a;
+}
+
+// Adds 8 N elements: their own sum first (a short tree of chains), then the
+// running sum, so the running chain is one add per 8 N elements long.
+template <int N>
+__device__ __forceinline__ void push(MaxSum& a, const float (&v)[N][8], float c) {
+  float m = a.m;
+#pragma unroll
+  for (int u = 0; u < N; ++u)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, v[u][j]);
+  const float r = finite_ref(m);
+  float s[4] = {};
+#pragma unroll
+  for (int u = 0; u < N; ++u)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j & 3] += pow2((v[u][j] - r) * c);
+  a = {m, a.s * pow2((a.m - r) * c) + ((s[0] + s[1]) + (s[2] + s[3]))};
+}
+
+// The teacher's softmax over the valid slots of one row, by one wave: t_k / tau
+// is at most m (0 if no valid slot is above -inf), sum = sum exp(t_k / tau - m).
+struct Teacher {
+  float m, sum;
+};
+template <typename TT>
+__device__ __forceinline__ Teacher teacher_row(const int32_t* __restrict__ ids, const TT* __restrict__ t, int K,
+                                               int64_t V, float it) {
+  const int lane = threadIdx.x & 63;
+  float m = -__builtin_inff();
+  for (int k = lane; k < K; k += 64)
+    if (ids[k] >= 0 && ids[k] < V) m = fmaxf(m, to_f32(t[k]) * it);
+  m = finite_ref(lanes_max<64>(m));
+  float s = 0.0f;
+  for (int k = lane; k < K; k += 64)
+    if (ids[k] >= 0 && ids[k] < V) s += exp_e(to_f32(t[k]) * it - m);
+  return {m, lanes_sum<64>(s)};
+}
+
+// loss and lse of a row from its (maximum, sum), by one wave.
+template <typename T, typename TT>
+__device__ __forceinline__ void finish_row(MaxSum a, const T* __restrict__ z, const int32_t* __restrict__ ids,
+                                           const TT* __restrict__ t, int K, int64_t V, float it,
+                                           float* __restrict__ loss, float* __restrict__ lse) {
+  const int lane = threadIdx.x & 63;
+  const float l = a.m * it + logf(a.s);
+  const Teacher q = teacher_row(ids, t, K, V, it);
+  float tot = 0.0f;
+  const float inv = 1.0f / q.sum, logsum = logf(q.sum);
+  for (int k = lane; k < K; k += 64) {
+    const int32_t id = ids[k];
+    if (id < 0 || id >= V) continue;
+    const float d = to_f32(t[k]) * it - q.m, qk = exp_e(d) * inv;
+    // (a NaN q_k or an empty row's 0 / 0 does not take the q_k = 0 way out)
+    if (q.sum != 0.0f && qk != 0.0f) tot += qk * ((d - logsum) - (to_f32(z[id]) * it - l));
+  }
+  tot = lanes_sum<64>(tot);
+  if (lane == 0) {
+    *loss = tot;
+    *lse = l;
+  }
+}
+
+// Workgroup b: piece b % n_split of row b / n_split, columns [c0, c0 + piece).
+template <typename T, typename TT>
+__global__ __launch_bounds__(kThreads) void distill_fwd_kernel(const T* __restrict__ z, int64_t ld, int64_t V,
+                                                               const int32_t* __restrict__ ids, int64_t ids_ld,
+                                                               const TT* __restrict__ teacher, int64_t t_ld, int K,
+                                                               float it, int n_split, int64_t piece,
+                                                               MaxSum* __restrict__ slots, float* __restrict__ loss,
+                                                               float* __restrict__ lse) {
+  constexpr int U = 4;
+  __shared__ MaxSum part[kWaves];
+  const int64_t row = blockIdx.x / n_split, c0 = (blockIdx.x % n_split) * piece;
+  const int64_t c1 = c0 + piece < V ? c0 + piece : V;
+  const T* p = z + row * ld;
+  const float c = it * kLog2e;
+  MaxSum a{-__builtin_inff(), 0.0f};
+  int64_t i = c0;
+  for (; i + U * kStep <= c1; i += U * kStep) {
+    Raw8<T> raw[U];
+    float v[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u].load(p + i + u * kStep + threadIdx.x * 8);
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u].get(v[u]);
+    push<U>(a, v, c);
+  }
+  for (; i < c1; i += kStep) {
+    float v[1][8];
+    const int64_t k = i + threadIdx.x * 8;
+    load8(p + k, c1 - k, -__builtin_inff(), v[0]);
+    push<1>(a, v, c);
+  }
+  a = wave_join(a, c);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  a = join(join(part[0], part[1], c), join(part[2], part[3], c), c);
+  if (n_split > 1) {
+    if (threadIdx.x == 0) slots[blockIdx.x] = a;
+    return;
+  }
+  finish_row(a, p, ids + row * ids_ld, teacher + row * t_ld, K, V, it, loss + row, lse + row);
+}
+
+// One wave per row joins the row's slots.
+template <typename T, typename TT>
+__global__ __launch_bounds__(64) void distill_join_kernel(const T* __restrict__ z, int64_t ld, int64_t V,
+                                                          const int32_t* __restrict__ ids, int64_t ids_ld,
+                                                          const TT* __restrict__ teacher, int64_t t_ld, int K,
+                                                          float it, int n_split, const MaxSum* __restrict__ slots,
+                                                          float* __restrict__ loss, float* __restrict__ lse) {
+  const int64_t row = blockIdx.x;
+  const float c = it * kLog2e;
+  MaxSum a{-__builtin_inff(), 0.0f};
+  for (int i = threadIdx.x; i < n_split; i += 64) a = join(a, slots[row * n_split + i], c);
+  a = wave_join(a, c);
+  finish_row(a, z + row * ld, ids + row * ids_ld, teacher + row * t_ld, K, V, it, loss + row, lse + row);
+}
+
+template <typename T, typename TT>
+__global__ __launch_bounds__(kThreads) void distill_bwd_kernel(T* __restrict__ dz, int64_t ld_d,
+                                                               const T* __restrict__ z, int64_t ld, int64_t V,
+                                                               const int32_t* __restrict__ ids, int64_t ids_ld,
+                                                               const TT* __restrict__ teacher, int64_t t_ld, int K,
+                                                               float it, int n_split, int64_t piece,
+                                                               const float* __restrict__ lse,
+                                                               const float* __restrict__ dloss) {
+  constexpr int U = 4;
+  __shared__ int32_t s_id[kMaxK];  // the valid slots' ids inside the piece, -1 for the others
+  __shared__ float s_q[kMaxK];
+  const int64_t row = blockIdx.x / n_split, c0 = (blockIdx.x % n_split) * piece;
+  const int64_t c1 = c0 + piece < V ? c0 + piece : V;
+  const T* p = z + row * ld;
+  T* o = dz + row * ld_d;
+  const int32_t* id = ids + row * ids_ld;
+  const TT* t = teacher + row * t_ld;
+  const Teacher q = teacher_row(id, t, K, V, it);
+  const float a = dloss[row] * it, l = lse[row];
+  const bool live = a != 0.0f && q.sum != 0.0f;  // the same for the whole workgroup
+  if (!live) {
+    const float zero[8] = {};
+    for (int64_t i = c0 + threadIdx.x * 8; i < c1; i += kStep) store8(o + i, c1 - i, zero);
+    return;
+  }
+  for (int k = threadIdx.x; k < K; k += kThreads) {
+    const int32_t v = id[k];
+    const bool in = v >= c0 && v < c1;
+    s_id[k] = in ? v : -1;
+    s_q[k] = in ? exp_e(to_f32(t[k]) * it - q.m) / q.sum : 0.0f;
+  }
+  int64_t i = c0;
+  for (; i + U * kStep <= c1; i += U * kStep) {
+    Raw8<T> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u].load(p + i + u * kStep + threadIdx.x * 8);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float v[8];
+      raw[u].get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = a * exp_e(v[j] * it - l);
+      store8_full(o + i + u * kStep + threadIdx.x * 8, v);
+    }
+  }
+  for (; i < c1; i += kStep) {
+    float v[8];
+    const int64_t k = i + threadIdx.x * 8;
+    load8(p + k, c1 - k, 0.0f, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = a * exp_e(v[j] * it - l);
+    store8(o + k, c1 - k, v);
+  }
+  __syncthreads();  // the piece's stores come before the rewrites below, the LDS slots are complete
+  for (int k = threadIdx.x; k < K; k += kThreads) {
+    const int32_t v = s_id[k];
+    if (v < 0) continue;
+    bool first = true;
+    for (int j = 0; j < k; ++j) first = first && s_id[j] != v;
+    if (!first) continue;  // the first slot of a repeated id sums them all, in slot order
+    float m = s_q[k];
+    for (int j = k + 1; j < K; ++j)
+      if (s_id[j] == v) m += s_q[j];
+    o[v] = from_f32<T>(a * (exp_e(to_f32(p[v]) * it - l) - m));
+  }
+}
+
+// Pieces per row, from the shape alone: one when the rows alone give every
+// compute unit several workgroups, else enough for about 2048 workgroups, with
+// pieces of whole steps of the workgroup, four at least.
+struct Split {
+  int n;
+  int64_t piece;
+};
+Split split_of(int64_t T, int64_t V) {
+  int64_t n = T >= 1024 || T == 0 ? 1 : ceil_div(2048, T);
+  const int64_t most = ceil_div(V, 4 * kStep);
+  if (n > most) n = most;
+  if (n < 1) n = 1;
+  const int64_t piece = align_up(ceil_div(V, n), kStep);
+  return {static_cast<int>(ceil_div(V, piece)), piece};
+}
+
+int check_args(const char* what, int dtype, int t_dtype, int64_t T, int64_t V, int64_t K, double tau) {
+  if (int s = check_float_dtype(what, dtype)) return s;
+  if (int s = check_float_dtype(what, t_dtype)) return s;
+  if (T < 0 || K < 0) return set_error(DET_ERR_INVALID_ARG, "%s: T and K must be >= 0", what);
+  if (V < 1) return set_error(DET_ERR_INVALID_ARG, "%s: V must be >= 1", what);
+  if (K > kMaxK) return set_error(DET_ERR_UNSUPPORTED, "%s: K must be <= %d, got %lld", what, kMaxK, (long long)K);
+  if (V > 0x7FFFFFFF - 65536 || T > 0x7FFFFFFF)
+    return set_error(DET_ERR_UNSUPPORTED, "%s: T and V must be < 2^31 - 65536", what);
+  if (!(tau >= 1e-6 && tau <= 1e6))
+    return set_error(DET_ERR_INVALID_ARG, "%s: tau must lie in [1e-6, 1e6], got %g", what, tau);
+  const Split s = split_of(T, V);
+  if (T * s.n > 0x7FFFFFFF) return set_error(DET_ERR_UNSUPPORTED, "%s: problem too large", what);
+  return DET_OK;
+}
+int check_ld(const char* what, const char* name, int64_t ld, int64_t n, int64_t T) {
+  if (ld < n) return set_error(DET_ERR_INVALID_ARG, "%s: row stride of %s < %lld", what, name, (long long)n);
+  if (ld > (int64_t(1) << 44) / T) return set_error(DET_ERR_UNSUPPORTED, "%s: %s is too large", what, name);
+  return DET_OK;
+}
+
+size_t ws_bytes_for(int64_t T, int64_t V) {
+  const Split s = split_of(T, V);
+  return T == 0 || s.n == 1 ? 0 : DET_WS_HEADER_BYTES + align_up(static_cast<size_t>(T * s.n) * sizeof(MaxSum), 256);
+}
+
+template <typename T, typename TT>
+void launch_fwd(const void* z, int64_t ld, int64_t V, const int32_t* ids, int64_t ids_ld, const void* t, int64_t t_ld,
+                int64_t rows, int64_t K, float it, float* loss, float* lse, MaxSum* slots, hipStream_t st) {
+  const Split s = split_of(rows, V);
+  hipLaunchKernelGGL((distill_fwd_kernel<T, TT>), dim3(static_cast<uint32_t>(rows * s.n)), dim3(kThreads), 0, st,
+                     static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n,
+                     s.piece, slots, loss, lse);
+  if (s.n > 1)
+    hipLaunchKernelGGL((distill_join_kernel<T, TT>), dim3(static_cast<uint32_t>(rows)), dim3(64), 0, st,
+                       static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n,
+                       slots, loss, lse);
+}
+template <typename T, typename TT>
+void launch_bwd(void* dz, int64_t ld_d, const void* z, int64_t ld, int64_t V, const int32_t* ids, int64_t ids_ld,
+                const void* t, int64_t t_ld, int64_t rows, int64_t K, float it, const float* lse, const float* dloss,
+                hipStream_t st) {
+  const Split s = split_of(rows, V);
+  hipLaunchKernelGGL((distill_bwd_kernel<T, TT>), dim3(static_cast<uint32_t>(rows * s.n)), dim3(kThreads), 0, st,
+                     static_cast<T*>(dz), ld_d, static_cast<const T*>(z), ld, V, ids, ids_ld,
+                     static_cast<const TT*>(t), t_ld, (int)K, it, s.n, s.piece, lse, dloss);
+}
+
+}  // namespace
+}  // namespace detgrad
+
+using namespace detgrad;
+
+#define DET_DISTILL_BY_TYPE(F, ...)                                                              \
+  if (dtype == DET_BF16) {                                                                       \
+    if (teacher_dtype == DET_BF16) F<uint16_t, uint16_t>(__VA_ARGS__);                           \
+    else F<uint16_t, float>(__VA_ARGS__);                                                        \
+  } else {                                                                                       \
+    if (teacher_dtype == DET_BF16) F<float, uint16_t>(__VA_ARGS__);                              \
+    else F<float, float>(__VA_ARGS__);                                                           \
+  }
+
+extern "C" int det_topk_distill_workspace_size(int64_t T, int64_t V, int64_t K, size_t* bytes) {
+  if (!bytes) return set_error(DET_ERR_INVALID_ARG, "topk_distill: bytes is NULL");
+  if (int s = check_args("topk_distill", DET_BF16, DET_BF16, T, V, K, 1.0)) return s;
+  *bytes = ws_bytes_for(T, V);
+  return ok();
+}
+
+extern "C" int det_topk_distill(const void* logits, int64_t ld, int dtype, const int32_t* ids, int64_t ids_ld,
+                                const void* teacher, int64_t teacher_ld, int teacher_dtype, int64_t T, int64_t V,
+                                int64_t K, double tau, float* loss, float* lse, void* ws, size_t ws_bytes,
+                                void* stream) {
+  const char* what = "topk_distill";
+  if (int s = check_args(what, dtype, teacher_dtype, T, V, K, tau)) return s;
+  if (T == 0) return ok();
+  if (!logits || !loss || !lse || (K && (!ids || !teacher)))
+    return set_error(DET_ERR_INVALID_ARG, "%s: NULL pointer", what);
+  if (int s = check_ld(what, "logits", ld, V, T)) return s;
+  if (int s = check_ld(what, "ids", ids_ld, K, T)) return s;
+  if (int s = check_ld(what, "teacher", teacher_ld, K, T)) return s;
+  const size_t need = ws_bytes_for(T, V);
+  if (int s = check_workspace(ws, ws_bytes, need)) return s;
+  const Buf outs[] = {{"loss", range1d(loss, T * 4)},
+                      {"lse", range1d(lse, T * 4)},
+                      {"the workspace", range1d(need ? ws : nullptr, ws_bytes)}};
+  const Buf ins[] = {{"logits", range2d(logits, T, V, ld, dtype_size(dtype))},
+                     {"ids", range2d(ids, T, K, ids_ld, 4)},
+                     {"teacher", range2d(teacher, T, K, teacher_ld, dtype_size(teacher_dtype))}};
+  if (int s = check_overlaps(what, outs, 3, ins, 3)) return s;
+  auto* slots = need ? reinterpret_cast<MaxSum*>(static_cast<char*>(ws) + DET_WS_HEADER_BYTES) : nullptr;
+  const float it = static_cast<float>(1.0 / tau);
+  DET_DISTILL_BY_TYPE(launch_fwd, logits, ld, V, ids, ids_ld, teacher, teacher_ld, T, K, it, loss, lse, slots,
+                      as_stream(stream))
+  return check_launch("det_topk_distill");
+}
+
+extern "C" int det_topk_distill_bwd(void* dlogits, int64_t ld_d, const void* logits, int64_t ld, int dtype,
+                                    const int32_t* ids, int64_t ids_ld, const void* teacher, int64_t teacher_ld,
+                                    int teacher_dtype, int64_t T, int64_t V, int64_t K, double tau, const float* lse,
+                                    const float* dloss, void* stream) {
+  const char* what = "topk_distill_bwd";
+  if (int s = check_args(what, dtype, teacher_dtype, T, V, K, tau)) return s;
+  if (T == 0) return ok();
+  if (!dlogits || !logits || !lse || !dloss || (K && (!ids || !teacher)))
+    return set_error(DET_ERR_INVALID_ARG, "%s: NULL pointer", what);
+  if (int s = check_ld(what, "dlogits", ld_d, V, T)) return s;
+  if (int s = check_ld(what, "logits", ld, V, T)) return s;
+  if (int s = check_ld(what, "ids", ids_ld, K, T)) return s;
+  if (int s = check_ld(what, "teacher", teacher_ld, K, T)) return s;
+  const Buf outs[] = {{"dlogits", range2d(dlogits, T, V, ld_d, dtype_size(dtype))}};
+  const Buf ins[] = {{"logits", range2d(logits, T, V, ld, dtype_size(dtype))},
+                     {"ids", range2d(ids, T, K, ids_ld, 4)},
+                     {"teacher", range2d(teacher, T, K, teacher_ld, dtype_size(teacher_dtype))},
+                     {"lse", range1d(lse, T * 4)},
+                     {"dloss", range1d(dloss, T * 4)}};
+  if (int s = check_overlaps(what, outs, 1, ins, 5)) return s;
+  const float it = static_cast<float>(1.0 / tau);
+  DET_DISTILL_BY_TYPE(launch_bwd, dlogits, ld_d, logits, ld, V, ids, ids_ld, teacher, teacher_ld, T, K, it, lse, dloss,
+                      as_stream(stream))
+  return check_launch("det_topk_distill_bwd");
+}

@@ -1,0 +1,167 @@
+// Row-wise building blocks of the loss and norm kernels: eight consecutive
+// elements per lane and access, exponentials, and sums across lanes.
+//
+// Rows may start at any element: the 16-byte accesses go through
+// __builtin_memcpy with the element's own alignment, which this target turns
+// into one global_load/store_dwordx4 (its global memory accesses need no
+// alignment), so odd widths and odd strides take the same path.
+#pragma once
+
+#include "common.hpp"
+
+namespace detgrad {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Element types: uint16_t holds bf16 bits, float is float32.
+__device__ __forceinline__ float to_f32(uint16_t b) { return bf16_to_f32(b); }
+__device__ __forceinline__ float to_f32(float f) { return f; }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+// bf16 by round to nearest even, NaN kept (the target's conversion instruction)
+template <>
+__device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+
+// Eight elements as they are in memory (16 bytes of bf16, 32 of float32).
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  u32x4 w;
+  __device__ __forceinline__ void load(const uint16_t* p) { __builtin_memcpy(&w, p, 16); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    __builtin_memcpy(&a, p, 16);
+    __builtin_memcpy(&b, p + 4, 16);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  }
+};
+
+// v = the elements p[0..7]; those at or past n (n <= 0: all of them) are `fill`
+// and are not read.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int64_t n, float fill, float (&v)[8]) {
+  if (n >= 8) {
+    Raw8<T> r;
+    r.load(p);
+    r.get(v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : fill;
+  }
+}
+
+__device__ __forceinline__ void store8_full(float* p, const float (&v)[8]) {
+  const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+  __builtin_memcpy(p, &a, 16);
+  __builtin_memcpy(p + 4, &b, 16);
+}
+__device__ __forceinline__ void store8_full(uint16_t* p, const float (&v)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = static_cast<uint32_t>(from_f32<uint16_t>(v[2 * i])) |
+           (static_cast<uint32_t>(from_f32<uint16_t>(v[2 * i + 1])) << 16);
+  __builtin_memcpy(p, &w, 16);
+}
+
+// p[0..min(n, 8)) = v, rounded once to the element type.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int64_t n, const float (&v)[8]) {
+  if (n >= 8) {
+    store8_full(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = from_f32<T>(v[i]);
+  }
+}
+
+constexpr float kLog2e = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
+
+// exp(x) within about 1.5 units in the last place: x log2(e) = k + f with k
+// whole, f from two fused steps against a two-word log2(e) (so the reduction's
+// error does not grow with |x|), then the hardware's 2^f scaled by 2^k.
+// exp(-inf) = 0, NaN stays NaN, results below 2^-149 are 0.
+__device__ __forceinline__ float exp_e(float x) {
+  const float k = __builtin_rintf(x * kLog2e);
+  const float f = __builtin_fmaf(x, kLog2eLo, __builtin_fmaf(x, kLog2e, -k));
+  const float y = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), static_cast<int>(k));
+  return x < -104.0f ? 0.0f : (x > 89.0f ? __builtin_inff() : y);
+}
+
+// Sum / maximum over groups of W consecutive lanes (W a power of two); every
+// lane of a group ends with the group's value, added in one fixed tree.
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (W >= 2) v = v + dpp_mov<DPP_XOR1>(v);
+  if constexpr (W >= 4) v = v + dpp_mov<DPP_XOR2>(v);
+  if constexpr (W >= 8) v = v + dpp_mov<DPP_HALF_MIRROR>(v);
+  if constexpr (W >= 16) v = v + dpp_mov<DPP_MIRROR>(v);
+  if constexpr (W >= 32) v = v + __shfl_xor(v, 16);
+  if constexpr (W >= 64) v = v + __shfl_xor(v, 32);
+  return v;
+}
+template <int W>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (W >= 2) v = fmaxf(v, dpp_mov<DPP_XOR1>(v));
+  if constexpr (W >= 4) v = fmaxf(v, dpp_mov<DPP_XOR2>(v));
+  if constexpr (W >= 8) v = fmaxf(v, dpp_mov<DPP_HALF_MIRROR>(v));
+  if constexpr (W >= 16) v = fmaxf(v, dpp_mov<DPP_MIRROR>(v));
+  if constexpr (W >= 32) v = fmaxf(v, __shfl_xor(v, 16));
+  if constexpr (W >= 64) v = fmaxf(v, __shfl_xor(v, 32));
+  return v;
+}
+
+// ------------------------------------------------------------------ host side
+// One buffer of a call, for the overlap check.
+struct Buf {
+  const char* name;
+  Range r;
+};
+
+// No output may overlap an input, another output or the workspace.
+inline int check_overlaps(const char* what, const Buf* outs, int n_out, const Buf* ins, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (overlaps(outs[i].r, ins[j].r))
+        return set_error(DET_ERR_OVERLAP, "%s: %s overlaps %s", what, outs[i].name, ins[j].name);
+    for (int j = i + 1; j < n_out; ++j)
+      if (overlaps(outs[i].r, outs[j].r))
+        return set_error(DET_ERR_OVERLAP, "%s: %s overlaps %s", what, outs[i].name, outs[j].name);
+  }
+  return DET_OK;
+}
+
+inline int check_float_dtype(const char* what, int dtype) {
+  if (dtype != DET_BF16 && dtype != DET_F32)
+    return set_error(DET_ERR_INVALID_ARG, "%s: dtype must be DET_BF16 or DET_F32, got %d", what, dtype);
+  return DET_OK;
+}
+inline size_t dtype_size(int dtype) { return dtype == DET_BF16 ? 2 : 4; }
+
+}  // namespace detgrad

@@ -65,6 +65,8 @@ typedef enum {
 
 typedef enum { DET_BF16 = 0, DET_F32 = 1 } det_dtype;
 
+typedef enum { DET_SCORE_SOFTMAX = 0, DET_SCORE_SIGMOID = 1 } det_score;
+
 /* ABI version of the loaded library (DET_ABI_VERSION). */
 int det_abi_version(void);
 
@@ -390,6 +392,145 @@ int det_grouped_wgrad_acc_bf16(uint16_t* main_grad, int64_t ld_e, int64_t ld_m, 
  * deterministic by construction and has no atomic arm. */
 int det_topk_canonicalize(const int32_t* ids, const float* logits, int64_t Q, int64_t K, int64_t ld,
                           int32_t* ids_out, float* logits_out, float* probs, int64_t ld_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * det_router_balance: the router's load-balancing loss, the per-expert counts
+ * and score sums it is made of, per segment of tokens (the sequences of a
+ * packed batch; one segment gives the loss of the whole batch).
+ * Megatron-LM PR #7441 (DSv4 deterministic mode) names the fused aux loss's
+ * cross-block float atomics as a source of run-to-run variation; here every
+ * float sum has one order.
+ *
+ *   p[t]         = softmax(logits[t]) (DET_SCORE_SOFTMAX), or
+ *                  sigmoid(logits[t]) / sum_e sigmoid(logits[t][e]) (DET_SCORE_SIGMOID)
+ *   counts[s][e] = slots (t, k), t in segment s, with ids[t][k] == e
+ *   prob_sum[s][e] = sum of p[t][e] over the tokens t of segment s
+ *   loss[s]      = coeff * E / (K * N_s^2) * sum_e counts[s][e] * prob_sum[s][e]
+ *
+ * N_s = the segment's tokens. Segment s owns the tokens [b_s, b_{s+1}), b =
+ * offs clamped to [0, T] and made non-decreasing (read on the device only);
+ * tokens of no segment are not read. Ids outside [0, E) are not counted; an id
+ * given twice counts twice. A token whose logits are all -inf has p = 0; a NaN
+ * or +inf logit makes its row's p NaN. An empty segment has zeros.
+ * The outputs are overwritten, not accumulated. Sums over tokens are float32
+ * per tile (the tile by a rule on T and E) and float64 across tiles, in tile
+ * order: the same bits from run to run.
+ *
+ * logits: [T, E], row stride ld >= E elements of any alignment, dtype DET_BF16
+ *         or DET_F32; E <= 1024. ids: [T, K] int32, row stride ids_ld >= K;
+ *         T * K < 2^31. offs: [S + 1] int32, S <= 65535.
+ * counts: [S, E] int32, prob_sum: [S, E], loss: [S] float32, contiguous.
+ * ws:     det_router_balance_workspace_size() bytes. Its header is neither
+ *         read nor written, so it needs no det_workspace_init().
+ * No atomic arm. */
+int det_router_balance_workspace_size(int64_t T, int64_t E, int64_t K, int64_t S, size_t* bytes);
+int det_router_balance(const void* logits, int64_t ld, int dtype, const int32_t* ids, int64_t ids_ld, int64_t T,
+                       int64_t E, int64_t K, const int32_t* offs, int64_t S, int score, double coeff, int32_t* counts,
+                       float* prob_sum, float* loss, void* ws, size_t ws_bytes, void* stream);
+
+/* det_router_balance_bwd: the gradient of sum_s dloss[s] * loss[s] with respect
+ * to the logits (counts are constants):
+ *
+ *   d[t][e] = dloss[s] * coeff * E / (K * N_s^2) * p_e * (counts[s][e] - sum_j p_j counts[s][j])
+ *             (times 1 - sigmoid(logits[t][e]) for DET_SCORE_SIGMOID)
+ *
+ * computed in float32 and rounded once to dtype; rows of tokens in a segment
+ * are overwritten, the other rows of dlogits are left as they were. counts:
+ * [S, E] int32, the forward's or (data-parallel ranks) their sum, with N_s
+ * still this call's tokens. dloss: [S] float32. dlogits: [T, E], row stride
+ * ld_d >= E, not overlapping an input. No workspace. */
+int det_router_balance_bwd(void* dlogits, int64_t ld_d, const void* logits, int64_t ld, int dtype, int64_t T, int64_t E,
+                           int64_t K, const int32_t* offs, int64_t S, const int32_t* counts, const float* dloss,
+                           int score, double coeff, void* stream);
+
+/* ------------------------------------------------------------------------
+ * det_topk_distill: distillation from a teacher's top logits: the
+ * Kullback-Leibler divergence of the student's distribution over the whole
+ * vocabulary from the teacher's over its K given words (renormalised), per
+ * token; the full-vocabulary counterpart of det_indexer_dk's loss.
+ *
+ *   x = logits[t] / tau,  lse[t] = log sum_v exp(x_v)
+ *   q = softmax of teacher[t] / tau over the valid slots (0 <= ids[t][k] < V)
+ *   loss[t] = sum_k q_k * (log q_k - x[ids[t][k]] + lse[t])
+ *
+ * Slots with q_k = 0 add nothing, and invalid slots are not read beyond their
+ * id. A token with no valid slot, or with only -inf there, has loss 0 (its lse
+ * is still written). An id given twice is two slots. Logits of -inf (masked
+ * words) have probability 0. loss and lse are overwritten, not accumulated; no
+ * factor tau^2 is applied. The running maximum and sum are float32, joined in
+ * one order given by T and V: the same bits from run to run.
+ *
+ * logits: [T, V], row stride ld >= V elements of any alignment, DET_BF16 or
+ *         DET_F32. ids: [T, K] int32, K <= 1024. teacher: [T, K], DET_BF16 or
+ *         DET_F32. Row strides ids_ld, teacher_ld >= K. loss, lse: [T] float32.
+ * tau in [1e-6, 1e6].
+ * ws:     det_topk_distill_workspace_size() bytes (0 when one workgroup takes a
+ *         whole row); its header is neither read nor written.
+ * No atomic arm. */
+int det_topk_distill_workspace_size(int64_t T, int64_t V, int64_t K, size_t* bytes);
+int det_topk_distill(const void* logits, int64_t ld, int dtype, const int32_t* ids, int64_t ids_ld,
+                     const void* teacher, int64_t teacher_ld, int teacher_dtype, int64_t T, int64_t V, int64_t K,
+                     double tau, float* loss, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* det_topk_distill_bwd: the gradient of sum_t dloss[t] * loss[t] with respect
+ * to the logits:
+ *
+ *   dlogits[t][v] = dloss[t] / tau * (exp(x_v - lse[t]) - sum of q_k over the slots with ids[t][k] == v)
+ *
+ * computed in float32 (repeated ids in slot order) and rounded once to dtype;
+ * overwritten. A token without teacher mass, or whose dloss is 0, gets a row of
+ * zeros whatever its logits are. lse: [T] float32, the forward's. dlogits:
+ * [T, V], row stride ld_d >= V, not overlapping an input. No workspace. */
+int det_topk_distill_bwd(void* dlogits, int64_t ld_d, const void* logits, int64_t ld, int dtype, const int32_t* ids,
+                         int64_t ids_ld, const void* teacher, int64_t teacher_ld, int teacher_dtype, int64_t T,
+                         int64_t V, int64_t K, double tau, const float* lse, const float* dloss, void* stream);
+
+/* ------------------------------------------------------------------------
+ * det_block_norm: the boundary between two residual blocks in one pass: the
+ * norm after a block with its gate and residual scale, the residual sum, and
+ * the norm before the next block. Root-mean-square norms over D channels.
+ *
+ *   n = w_post * f / sqrt(mean(f^2) + eps)         (w_post NULL: n = f)
+ *   y = x + alpha * sigmoid(gate) * n              (alpha NULL, gate NULL: a factor of 1)
+ *   h = w_pre * y / sqrt(mean(y^2) + eps)          (w_pre NULL: no h)
+ *
+ * in float32 (h from y before its rounding), each output rounded once.
+ * x, f, y, h: [T, D] of dtype (DET_BF16 or DET_F32), row strides >= D elements
+ * of any alignment; D <= 16384. gate: [T, gate_cols], gate_cols = D (a gate per
+ * channel) or 1 (per token). w_post, alpha, w_pre: [D] float32. rstd_post,
+ * rstd_pre: [T] float32, the factors 1 / sqrt(mean + eps), for the backward;
+ * given exactly when w_post, w_pre are (and h when w_pre is). Outputs are
+ * overwritten and overlap no input and no other output. No workspace. */
+int det_block_norm(const void* x, int64_t x_ld, const void* f, int64_t f_ld, const void* gate, int64_t gate_ld,
+                   int64_t gate_cols, const float* w_post, const float* alpha, const float* w_pre, int dtype, int64_t T,
+                   int64_t D, double eps, void* y, int64_t y_ld, void* h, int64_t h_ld, float* rstd_post,
+                   float* rstd_pre, void* stream);
+
+/* det_block_norm_bwd: all gradients of det_block_norm from dy and dh (the
+ * gradients of y and h), with y recomputed from x, f and the forward's factors:
+ *
+ *   D = dy + rstd_pre * (u - yh * mean(u * yh)),  yh = y * rstd_pre, u = w_pre * dh   (w_pre NULL: D = dy)
+ *   dx = D,  dn = D * alpha * sigmoid(gate),  fh = f * rstd_post (w_post NULL: fh = f)
+ *   dgate = dn * n * (1 - sigmoid(gate))          (summed over the row for gate_cols = 1)
+ *   df = rstd_post * (w_post * dn - fh * mean(w_post * dn * fh))   (w_post NULL: df = dn)
+ *   dw_pre += sum_t dh * yh,  dalpha += sum_t D * sigmoid(gate) * n,  dw_post += sum_t dn * fh
+ *
+ * dx, df, dgate (dtype, overwritten) have the layouts of x, f, gate; the
+ * parameter gradients ([D] float32) accumulate like every reduction here:
+ * out <- RN32(out + total), with a workgroup's rows (b, b + G, ... for a G
+ * given by T and D) added in order and the workgroups' slots in one fixed
+ * order, in float32. dh, rstd_pre, dw_pre are given exactly when w_pre is,
+ * rstd_post, dw_post when w_post is, dalpha when alpha is, dgate when gate is;
+ * x may be NULL without w_pre. T = 0 leaves every output unchanged.
+ * ws: det_block_norm_bwd_workspace_size() bytes when any of w_post, alpha,
+ *     w_pre is given; its header is neither read nor written. */
+int det_block_norm_bwd_workspace_size(int64_t T, int64_t D, size_t* bytes);
+int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t dh_ld, const void* x, int64_t x_ld,
+                       const void* f, int64_t f_ld, const void* gate, int64_t gate_ld, int64_t gate_cols,
+                       const float* w_post, const float* alpha, const float* w_pre, const float* rstd_post,
+                       const float* rstd_pre, int dtype, int64_t T, int64_t D, void* dx, int64_t dx_ld, void* df,
+                       int64_t df_ld, void* dgate, int64_t dgate_ld, float* dw_post, float* dalpha, float* dw_pre,
+                       void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Diagnostics (tests only). det_detmath_eval evaluates the device versions of

@@ -88,6 +88,49 @@ MANIFEST = {
         "atomic": None,
         "graph": ["test_gpu_graph.py::test_topk"],
     },
+    # against float64 within derived tolerances, not against a bit model of the float32 sequence
+    "det_router_balance": {
+        "cite": "Megatron-LM PR #7441 (DSv4), the router aux loss's float atomics",
+        "replay": ["test_gpu_router_balance.py::test_replay_under_load_with_poisoned_workspaces"],
+        "parity": ["test_gpu_router_balance.py::test_sizes"],
+        "atomic": None,
+        "graph": ["test_gpu_router_balance.py::test_graph_replays_and_two_streams"],
+    },
+    "det_router_balance_bwd": {
+        "cite": "Megatron-LM PR #7441 (DSv4), the router aux loss's float atomics",
+        "replay": ["test_gpu_router_balance.py::test_replay_under_load_with_poisoned_workspaces"],
+        "parity": ["test_gpu_router_balance.py::test_sizes", "test_gpu_router_balance.py::test_gradient_against_differences"],
+        "atomic": None,
+        "graph": ["test_gpu_router_balance.py::test_graph_replays_and_two_streams"],
+    },
+    "det_topk_distill": {
+        "cite": "the full-vocabulary counterpart of the clipped-KL indexer loss (no page)",
+        "replay": ["test_gpu_topk_distill.py::test_replay_under_load_with_poisoned_workspaces"],
+        "parity": ["test_gpu_topk_distill.py::test_sizes"],
+        "atomic": None,
+        "graph": ["test_gpu_topk_distill.py::test_graph_replays_and_two_streams"],
+    },
+    "det_topk_distill_bwd": {
+        "cite": "the full-vocabulary counterpart of the clipped-KL indexer loss (no page)",
+        "replay": ["test_gpu_topk_distill.py::test_replay_under_load_with_poisoned_workspaces"],
+        "parity": ["test_gpu_topk_distill.py::test_sizes", "test_gpu_topk_distill.py::test_gradient_against_differences"],
+        "atomic": None,
+        "graph": ["test_gpu_topk_distill.py::test_graph_replays_and_two_streams"],
+    },
+    "det_block_norm": {
+        "cite": "the column sums of the gate page's pattern, for a block's norms (no page)",
+        "replay": ["test_gpu_block_norm.py::test_replay_under_load_with_poisoned_workspaces"],
+        "parity": ["test_gpu_block_norm.py::test_sizes"],
+        "atomic": None,
+        "graph": ["test_gpu_block_norm.py::test_graph_replays_and_two_streams"],
+    },
+    "det_block_norm_bwd": {
+        "cite": "the column sums of the gate page's pattern, for a block's norms (no page)",
+        "replay": ["test_gpu_block_norm.py::test_replay_under_load_with_poisoned_workspaces"],
+        "parity": ["test_gpu_block_norm.py::test_sizes", "test_gpu_block_norm.py::test_gradients_against_differences"],
+        "atomic": None,
+        "graph": ["test_gpu_block_norm.py::test_graph_replays_and_two_streams"],
+    },
 }
 
 # declared functions that are sizes, set-up or diagnostics rather than accumulating entry points
