@@ -33,6 +33,7 @@ device, whichever device is current.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -541,80 +542,106 @@ def det_mfma_rate(ops, out, blocks: int, iters: int, stream=None) -> None:
 
 
 # ------------------------------------------ router balance, distillation, block norms
-_DTYPE_CODES = {}
+# These calls are short on the GPU, so their checks read each tensor's attributes once and
+# pass plain integers to the library.
+_ctx = None
 
 
-def _float_code(t, name: str) -> int:
-    if not _DTYPE_CODES:
+class _Context:
+    """torch names the calls below use, looked up once."""
+
+    def __init__(self):
         import torch
-        _DTYPE_CODES.update({torch.bfloat16: DET_BF16, torch.float32: DET_F32})
-    code = _DTYPE_CODES.get(t.dtype)
+        self.torch, self.f32, self.i32, self.u8 = torch, torch.float32, torch.int32, torch.uint8
+        self.codes = {torch.bfloat16: DET_BF16, torch.float32: DET_F32}
+        # torch.cuda.current_stream() builds a Stream object (2.6 us); the raw handle takes 0.05 us
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda i: torch.cuda.current_stream(i).cuda_stream)
+        self.device = torch.cuda.current_device
+
+
+def _context() -> _Context:
+    global _ctx
+    if _ctx is None:
+        _ctx = _Context()
+    return _ctx
+
+
+def _code(c, t, name: str) -> int:
+    code = c.codes.get(t.dtype)
     if code is None:
         raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
     return code
 
 
-def _rows(t, name: str, shape, dtype=None) -> int:
-    """Check a 2-D tensor's shape, dtype and unit column stride; return its row stride in elements."""
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError("%s must have unit innermost stride" % name)
-    return t.stride(0) if shape[0] > 1 else max(shape[1], 1)
-
-
-def _flat(t, name: str, shape, dtype) -> None:
-    """Check a contiguous tensor's shape and dtype."""
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
+def _bad(t, name: str, shape, dtype, dev: int, layout: str) -> None:
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.get_device() != dev:
+        raise ValueError("all tensors must be on one GPU, but %s is on %s" % (name, t.device))
+    raise ValueError("%s must %s" % (name, layout))
 
 
-class _Launch:
-    """The device, stream and workspace of one call: every tensor on one GPU, that GPU current during the
-    call, the workspace allocated on the call's stream (freed to that stream's pool when the call returns)."""
+def _rows(t, name: str, shape, dtype, dev: int) -> int:
+    """Check a 2-D tensor with unit column stride; return its row stride in elements."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
+        st = t.stride()
+        if st[1] == 1 or shape[1] <= 1:
+            return st[0] if shape[0] > 1 else max(shape[1], 1)
+    _bad(t, name, shape, dtype, dev, "have unit innermost stride")
 
-    def __init__(self, tensors, need, ws, stream):
-        import torch
-        dev = tensors[0].device
-        for t in tensors:
-            if t is not None and (t.device != dev or not t.is_cuda):
-                raise ValueError("all tensors must be on one GPU, got %s and %s" % (dev, t.device))
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
-        self.stream = ctypes.c_void_p(stream.cuda_stream)
-        self.keep, self.ws, self.nbytes = ws, ctypes.c_void_p(0), 0
-        if isinstance(ws, Workspace):
-            if ws._buf.device != dev:
-                raise ValueError("the workspace is on %s, the tensors on %s" % (ws._buf.device, dev))
-            self.ws, self.nbytes = ctypes.c_void_p(ws.ptr), ws.nbytes
-        elif ws is not None:
-            if ws.device != dev or not ws.is_contiguous():
-                raise ValueError("the workspace must be a contiguous tensor on %s" % dev)
-            self.ws, self.nbytes = ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size()
-        elif need:
-            if stream == torch.cuda.current_stream(dev):
-                self.keep = torch.empty(need + 256, dtype=torch.uint8, device=dev)
-            else:
-                with torch.cuda.stream(stream):
-                    self.keep = torch.empty(need + 256, dtype=torch.uint8, device=dev)
-            self.ws, self.nbytes = ctypes.c_void_p((self.keep.data_ptr() + 255) // 256 * 256), need
-        self.other = dev if dev.index != torch.cuda.current_device() else None
 
-    def call(self, fn, *args) -> None:
-        if self.other is None:
-            _check(fn(*args))
-        else:
-            import torch
-            with torch.cuda.device(self.other):
-                _check(fn(*args))
+def _flat(t, name: str, shape, dtype, dev: int) -> int:
+    """Check a contiguous tensor; return its address."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _bad(t, name, shape, dtype, dev, "be contiguous")
+
+
+def _stream_on(c, dev: int, stream) -> int:
+    """The raw handle of the call's stream: the given one, or the current stream of the tensors' device."""
+    if dev < 0:
+        raise ValueError("all tensors must be on one GPU, got CPU tensors")
+    if stream is None:
+        return c.raw_stream(dev)
+    if stream.device.index != dev:
+        raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, dev))
+    return stream.cuda_stream
+
+
+def _scratch(c, need: int, ws, dev: int, stream, raw: int):
+    """(address, bytes, owner) of the call's workspace: the caller's, or one from the caching allocator on the
+    call's stream (returned to that stream's pool when the owner goes)."""
+    if ws is not None:
+        buf = ws._buf if isinstance(ws, Workspace) else ws
+        if buf.get_device() != dev or not buf.is_contiguous():
+            raise ValueError("the workspace must be contiguous and on cuda:%d" % dev)
+        return (ws.ptr, ws.nbytes, ws) if buf is not ws else (ws.data_ptr(), ws.numel() * ws.element_size(), ws)
+    if need == 0:
+        return None, 0, None
+    torch = c.torch
+    if stream is None or raw == c.raw_stream(dev):
+        buf = torch.empty(need + 256, dtype=c.u8, device=dev)
+    else:
+        with torch.cuda.stream(stream):
+            buf = torch.empty(need + 256, dtype=c.u8, device=dev)
+    return (buf.data_ptr() + 255) // 256 * 256, need, buf
+
+
+def _run(c, dev: int, fn, *args) -> None:
+    if c.device() == dev:
+        status = fn(*args)
+    else:
+        with c.torch.cuda.device(dev):
+            status = fn(*args)
+    if status != DET_OK:
+        _check(status)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -626,6 +653,7 @@ def _score_code(score) -> int:
     return _SCORES[score]
 
 
+@functools.lru_cache(maxsize=256)
 def det_router_balance_workspace_size(T: int, E: int, K: int, S: int) -> int:
     n = _SZ()
     _check(lib().det_router_balance_workspace_size(T, E, K, S, ctypes.byref(n)))
@@ -637,97 +665,90 @@ def det_router_balance(logits, ids, offs, counts, prob_sum, loss, coeff: float =
     """loss[s] = coeff * E / (K * N_s^2) * sum_e counts[s, e] * prob_sum[s, e] over the tokens
     offs[s] <= t < offs[s + 1]. logits bf16 or float32 [T, E], ids int32 [T, K], offs int32 [S + 1]; overwrites
     counts int32 [S, E], prob_sum float32 [S, E] and loss float32 [S]."""
-    import torch
-    code, sc = _float_code(logits, "logits"), _score_code(score)
-    if logits.dim() != 2 or ids.dim() != 2 or offs.dim() != 1 or offs.numel() < 1:
+    c = _context()
+    code, sc = _code(c, logits, "logits"), _score_code(score)
+    if logits.dim() != 2 or ids.dim() != 2 or offs.dim() != 1 or offs.shape[0] < 1:
         raise ValueError("need logits [T, E], ids [T, K] and offs [S + 1]")
-    T, E = logits.shape
-    K, S = ids.shape[1], offs.numel() - 1
-    ld = _rows(logits, "logits", (T, E))
-    ids_ld = _rows(ids, "ids", (T, K), torch.int32)
-    _flat(offs, "offs", (S + 1,), torch.int32)
-    _flat(counts, "counts", (S, E), torch.int32)
-    _flat(prob_sum, "prob_sum", (S, E), torch.float32)
-    _flat(loss, "loss", (S,), torch.float32)
-    need = det_router_balance_workspace_size(T, E, K, S)
-    c = _Launch((logits, ids, offs, counts, prob_sum, loss), need, ws, stream)
-    c.call(lib().det_router_balance, _ptr(logits), ld, code, _ptr(ids), ids_ld, T, E, K, _ptr(offs), S, sc,
-           float(coeff), _ptr(counts), _ptr(prob_sum), _ptr(loss), c.ws, c.nbytes, c.stream)
+    T, E = shape = logits.shape
+    K, S, dev = ids.shape[1], offs.shape[0] - 1, logits.get_device()
+    ld = _rows(logits, "logits", shape, logits.dtype, dev)
+    ids_ld = _rows(ids, "ids", (T, K), c.i32, dev)
+    p = (_flat(offs, "offs", (S + 1,), c.i32, dev), _flat(counts, "counts", (S, E), c.i32, dev),
+         _flat(prob_sum, "prob_sum", (S, E), c.f32, dev), _flat(loss, "loss", (S,), c.f32, dev))
+    raw = _stream_on(c, dev, stream)
+    wp, wn, keep = _scratch(c, det_router_balance_workspace_size(T, E, K, S), ws, dev, stream, raw)
+    _run(c, dev, lib().det_router_balance, logits.data_ptr(), ld, code, ids.data_ptr(), ids_ld, T, E, K, p[0], S, sc,
+         coeff, p[1], p[2], p[3], wp, wn, raw)
 
 
 def det_router_balance_bwd(dlogits, logits, offs, counts, dloss, topk: int, coeff: float = 1.0, score: str = "softmax",
                            stream=None) -> None:
     """dlogits = the gradient of sum_s dloss[s] * loss[s] of det_router_balance (rows of tokens in a sequence are
     overwritten, the others left as they were). counts int32 [S, E], dloss float32 [S], topk = K."""
-    import torch
-    code, sc = _float_code(logits, "logits"), _score_code(score)
-    if logits.dim() != 2 or offs.dim() != 1 or offs.numel() < 1:
+    c = _context()
+    code, sc = _code(c, logits, "logits"), _score_code(score)
+    if logits.dim() != 2 or offs.dim() != 1 or offs.shape[0] < 1:
         raise ValueError("need logits [T, E] and offs [S + 1]")
-    T, E = logits.shape
-    S = offs.numel() - 1
-    ld = _rows(logits, "logits", (T, E))
-    ld_d = _rows(dlogits, "dlogits", (T, E), logits.dtype)
-    _flat(offs, "offs", (S + 1,), torch.int32)
-    _flat(counts, "counts", (S, E), torch.int32)
-    _flat(dloss, "dloss", (S,), torch.float32)
-    c = _Launch((dlogits, logits, offs, counts, dloss), 0, None, stream)
-    c.call(lib().det_router_balance_bwd, _ptr(dlogits), ld_d, _ptr(logits), ld, code, T, E, int(topk), _ptr(offs), S,
-           _ptr(counts), _ptr(dloss), sc, float(coeff), c.stream)
+    T, E = shape = logits.shape
+    S, dev = offs.shape[0] - 1, logits.get_device()
+    ld = _rows(logits, "logits", shape, logits.dtype, dev)
+    ld_d = _rows(dlogits, "dlogits", shape, logits.dtype, dev)
+    po, pc = _flat(offs, "offs", (S + 1,), c.i32, dev), _flat(counts, "counts", (S, E), c.i32, dev)
+    pl = _flat(dloss, "dloss", (S,), c.f32, dev)
+    raw = _stream_on(c, dev, stream)
+    _run(c, dev, lib().det_router_balance_bwd, dlogits.data_ptr(), ld_d, logits.data_ptr(), ld, code, T, E, topk, po,
+         S, pc, pl, sc, coeff, raw)
 
 
+@functools.lru_cache(maxsize=256)
 def det_topk_distill_workspace_size(T: int, V: int, K: int) -> int:
     n = _SZ()
     _check(lib().det_topk_distill_workspace_size(T, V, K, ctypes.byref(n)))
     return n.value
 
 
-def _distill_operands(logits, ids, teacher):
-    import torch
-    code, t_code = _float_code(logits, "logits"), _float_code(teacher, "teacher")
+def _distill_operands(c, logits, ids, teacher):
+    code, t_code = _code(c, logits, "logits"), _code(c, teacher, "teacher")
     if logits.dim() != 2 or ids.dim() != 2:
         raise ValueError("need logits [T, V], ids and teacher [T, K]")
-    T, V = logits.shape
-    K = ids.shape[1]
-    return (_ptr(logits), _rows(logits, "logits", (T, V)), code, _ptr(ids), _rows(ids, "ids", (T, K), torch.int32),
-            _ptr(teacher), _rows(teacher, "teacher", (T, K)), t_code, T, V, K)
+    T, V = shape = logits.shape
+    K, dev = ids.shape[1], logits.get_device()
+    return dev, (logits.data_ptr(), _rows(logits, "logits", shape, logits.dtype, dev), code,
+                 ids.data_ptr(), _rows(ids, "ids", (T, K), c.i32, dev),
+                 teacher.data_ptr(), _rows(teacher, "teacher", (T, K), teacher.dtype, dev), t_code, T, V, K)
 
 
 def det_topk_distill(logits, ids, teacher, loss, lse, tau: float = 1.0, ws=None, stream=None) -> None:
     """loss[t] = KL(teacher's top K || student) at temperature tau, lse[t] = logsumexp(logits[t] / tau).
     logits bf16 or float32 [T, V]; ids int32 [T, K] (outside [0, V): unused slots); teacher bf16 or float32 [T, K]
     logits; overwrites loss and lse float32 [T]."""
-    import torch
-    ops = _distill_operands(logits, ids, teacher)
+    c = _context()
+    dev, ops = _distill_operands(c, logits, ids, teacher)
     T, V, K = ops[-3:]
-    _flat(loss, "loss", (T,), torch.float32)
-    _flat(lse, "lse", (T,), torch.float32)
-    need = det_topk_distill_workspace_size(T, V, K)
-    c = _Launch((logits, ids, teacher, loss, lse), need, ws, stream)
-    c.call(lib().det_topk_distill, *ops, float(tau), _ptr(loss), _ptr(lse), c.ws, c.nbytes, c.stream)
+    pl, pe = _flat(loss, "loss", (T,), c.f32, dev), _flat(lse, "lse", (T,), c.f32, dev)
+    raw = _stream_on(c, dev, stream)
+    wp, wn, keep = _scratch(c, det_topk_distill_workspace_size(T, V, K), ws, dev, stream, raw)
+    _run(c, dev, lib().det_topk_distill, *ops, tau, pl, pe, wp, wn, raw)
 
 
 def det_topk_distill_bwd(dlogits, logits, ids, teacher, lse, dloss, tau: float = 1.0, stream=None) -> None:
     """dlogits = the gradient of sum_t dloss[t] * loss[t] of det_topk_distill (overwritten; a row whose dloss is 0 or
     that has no teacher mass is zeros). lse float32 [T] from the forward, dloss float32 [T]."""
-    import torch
-    ops = _distill_operands(logits, ids, teacher)
-    T, V, _ = ops[-3:]
-    ld_d = _rows(dlogits, "dlogits", (T, V), logits.dtype)
-    _flat(lse, "lse", (T,), torch.float32)
-    _flat(dloss, "dloss", (T,), torch.float32)
-    c = _Launch((dlogits, logits, ids, teacher, lse, dloss), 0, None, stream)
-    c.call(lib().det_topk_distill_bwd, _ptr(dlogits), ld_d, *ops, float(tau), _ptr(lse), _ptr(dloss), c.stream)
+    c = _context()
+    dev, ops = _distill_operands(c, logits, ids, teacher)
+    T = ops[-3]
+    ld_d = _rows(dlogits, "dlogits", logits.shape, logits.dtype, dev)
+    pe, pl = _flat(lse, "lse", (T,), c.f32, dev), _flat(dloss, "dloss", (T,), c.f32, dev)
+    raw = _stream_on(c, dev, stream)
+    _run(c, dev, lib().det_topk_distill_bwd, dlogits.data_ptr(), ld_d, *ops, tau, pe, pl, raw)
 
 
-def _norm_row(t, name, T, cols, dtype):
-    return (_ptr(None), 0) if t is None else (_ptr(t), _rows(t, name, (T, cols), dtype))
+def _opt_rows(t, name: str, shape, dtype, dev: int) -> int:
+    return 0 if t is None else _rows(t, name, shape, dtype, dev)
 
 
-def _norm_vec(t, name, n):
-    import torch
-    if t is not None:
-        _flat(t, name, (n,), torch.float32)
-    return _ptr(t)
+def _opt_flat(t, name: str, shape, dtype, dev: int):
+    return None if t is None else _flat(t, name, shape, dtype, dev)
 
 
 def _gate_cols(gate, D: int) -> int:
@@ -744,18 +765,22 @@ def det_block_norm(x, f, y, gate=None, w_post=None, alpha=None, w_pre=None, h=No
     gate [T, D] or [T, 1] of the same dtype, w_post, alpha, w_pre float32 [D]; each of gate, w_post, alpha and w_pre may
     be left out. Overwrites y, h (with w_pre) and the norms' factors rstd_post (with w_post) and rstd_pre (with w_pre),
     float32 [T]."""
-    code = _float_code(x, "x")
+    c = _context()
+    code = _code(c, x, "x")
     if x.dim() != 2:
         raise ValueError("x must be [T, D]")
-    (T, D), dt, gc = x.shape, x.dtype, _gate_cols(gate, x.shape[1])
-    args = (*_norm_row(x, "x", T, D, dt), *_norm_row(f, "f", T, D, dt), *_norm_row(gate, "gate", T, gc, dt), gc,
-            _norm_vec(w_post, "w_post", D), _norm_vec(alpha, "alpha", D), _norm_vec(w_pre, "w_pre", D), code, T, D,
-            float(eps), *_norm_row(y, "y", T, D, dt), *_norm_row(h, "h", T, D, dt),
-            _norm_vec(rstd_post, "rstd_post", T), _norm_vec(rstd_pre, "rstd_pre", T))
-    c = _Launch((x, f, y, gate, w_post, alpha, w_pre, h, rstd_post, rstd_pre), 0, None, stream)
-    c.call(lib().det_block_norm, *args, c.stream)
+    T, D = sh = x.shape
+    dt, gc, f32, dev = x.dtype, _gate_cols(gate, D), c.f32, x.get_device()
+    args = (x.data_ptr(), _rows(x, "x", sh, dt, dev), _at(f), _opt_rows(f, "f", sh, dt, dev),
+            _at(gate), _opt_rows(gate, "gate", (T, gc), dt, dev), gc, _opt_flat(w_post, "w_post", (D,), f32, dev),
+            _opt_flat(alpha, "alpha", (D,), f32, dev), _opt_flat(w_pre, "w_pre", (D,), f32, dev), code, T, D, eps,
+            _at(y), _opt_rows(y, "y", sh, dt, dev), _at(h), _opt_rows(h, "h", sh, dt, dev),
+            _opt_flat(rstd_post, "rstd_post", (T,), f32, dev), _opt_flat(rstd_pre, "rstd_pre", (T,), f32, dev))
+    raw = _stream_on(c, dev, stream)
+    _run(c, dev, lib().det_block_norm, *args, raw)
 
 
+@functools.lru_cache(maxsize=256)
 def det_block_norm_bwd_workspace_size(T: int, D: int) -> int:
     n = _SZ()
     _check(lib().det_block_norm_bwd_workspace_size(T, D, ctypes.byref(n)))
@@ -768,17 +793,22 @@ def det_block_norm_bwd(dy, x, f, dx, df, dh=None, gate=None, w_post=None, alpha=
     """The gradients of det_block_norm from dy and dh: overwrites dx, df and dgate, accumulates the parameter gradients
     dw_post, dalpha, dw_pre (float32 [D]) in a fixed order. The optional arguments are given as in the forward, each
     with its gradient; x may be None without w_pre."""
-    code = _float_code(dy, "dy")
+    c = _context()
+    code = _code(c, dy, "dy")
     if dy.dim() != 2:
         raise ValueError("dy must be [T, D]")
-    (T, D), dt, gc = dy.shape, dy.dtype, _gate_cols(gate, dy.shape[1])
-    args = (*_norm_row(dy, "dy", T, D, dt), *_norm_row(dh, "dh", T, D, dt), *_norm_row(x, "x", T, D, dt),
-            *_norm_row(f, "f", T, D, dt), *_norm_row(gate, "gate", T, gc, dt), gc, _norm_vec(w_post, "w_post", D),
-            _norm_vec(alpha, "alpha", D), _norm_vec(w_pre, "w_pre", D), _norm_vec(rstd_post, "rstd_post", T),
-            _norm_vec(rstd_pre, "rstd_pre", T), code, T, D, *_norm_row(dx, "dx", T, D, dt),
-            *_norm_row(df, "df", T, D, dt), *_norm_row(dgate, "dgate", T, gc, dt), _norm_vec(dw_post, "dw_post", D),
-            _norm_vec(dalpha, "dalpha", D), _norm_vec(dw_pre, "dw_pre", D))
+    T, D = sh = dy.shape
+    dt, gc, f32, dev, vec, tok = dy.dtype, _gate_cols(gate, D), c.f32, dy.get_device(), (D,), (T,)
+    gs = (T, gc)
+    args = (dy.data_ptr(), _rows(dy, "dy", sh, dt, dev), _at(dh), _opt_rows(dh, "dh", sh, dt, dev),
+            _at(x), _opt_rows(x, "x", sh, dt, dev), _at(f), _opt_rows(f, "f", sh, dt, dev),
+            _at(gate), _opt_rows(gate, "gate", gs, dt, dev), gc, _opt_flat(w_post, "w_post", vec, f32, dev),
+            _opt_flat(alpha, "alpha", vec, f32, dev), _opt_flat(w_pre, "w_pre", vec, f32, dev),
+            _opt_flat(rstd_post, "rstd_post", tok, f32, dev), _opt_flat(rstd_pre, "rstd_pre", tok, f32, dev),
+            code, T, D, _at(dx), _opt_rows(dx, "dx", sh, dt, dev), _at(df), _opt_rows(df, "df", sh, dt, dev),
+            _at(dgate), _opt_rows(dgate, "dgate", gs, dt, dev), _opt_flat(dw_post, "dw_post", vec, f32, dev),
+            _opt_flat(dalpha, "dalpha", vec, f32, dev), _opt_flat(dw_pre, "dw_pre", vec, f32, dev))
+    raw = _stream_on(c, dev, stream)
     need = 0 if w_post is None and alpha is None and w_pre is None else det_block_norm_bwd_workspace_size(T, D)
-    c = _Launch((dy, x, f, dx, df, dh, gate, w_post, alpha, w_pre, rstd_post, rstd_pre, dgate, dw_post, dalpha, dw_pre),
-                need, ws, stream)
-    c.call(lib().det_block_norm_bwd, *args, c.ws, c.nbytes, c.stream)
+    wp, wn, keep = _scratch(c, need, ws, dev, stream, raw)
+    _run(c, dev, lib().det_block_norm_bwd, *args, wp, wn, raw)
