@@ -10,9 +10,10 @@
 // recomputes it in float32 from x and f, so it needs no copy of y.
 //
 //   yh = y rstd_y, u = w_pre dh:  D = dy + rstd_y (u - yh mean(u yh))   (w_pre NULL: D = dy)
-//   dx = D;  dw_pre += sum dh yh;  dalpha += sum D s n
+//   dx = D;  dw_pre += sum dh yh
 //   dn = D alpha s:  dgate = dn n (1 - s)  (its row sum for a gate per token)
-//   fh = f rstd_f:   dw_post += sum dn fh;  df = rstd_f (w_post dn - fh mean(w_post dn fh))   (w_post NULL: df = dn)
+//   fh = f rstd_f:   df = rstd_f (w_post dn - fh mean(w_post dn fh))   (w_post NULL: df = dn)
+//   A = sum D s fh over the tokens:  dw_post += alpha A,  dalpha += w_post A  (one column sum for both)
 //
 // A workgroup owns whole rows, eight (or sixteen) consecutive channels per
 // thread, so a row's sums are a wave tree and one exchange through LDS, and the
@@ -48,7 +49,11 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
   }
 }
 
-__device__ __forceinline__ float sigmoid_f(float g) { return 1.0f / (1.0f + exp_e(-g)); }
+// 1 / (1 + 2^(-g log2 e)) by the hardware's exponential and reciprocal: within
+// (|g| + 3) units in the last place of a float32 sigmoid.
+__device__ __forceinline__ float sigmoid_f(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * kLog2e));
+}
 
 enum GateKind { kGateNone = 0, kGateRow = 1, kGateFull = 2 };
 
@@ -58,13 +63,16 @@ struct NormParams {
   int64_t rows, D;
 };
 
-template <int N>
-__device__ __forceinline__ void load_param(const float* p, int64_t col, int64_t n, float (&v)[N]) {
+// Rows of fewer than eight channels only reach the 64-thread instances.
+template <bool TINY>
+__device__ __forceinline__ void load_param(const float* p, const Cols<TINY>& c, float (&v)[8]) {
   if (p) {
-    load8(p + col, n, 0.0f, v);
+    Raw8<float> r;
+    load_cols(r, p, c);
+    get_cols(r, c, 0.0f, v);
   } else {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = 1.0f;
+    for (int j = 0; j < 8; ++j) v[j] = 1.0f;
   }
 }
 
@@ -79,24 +87,33 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(const T* __restrict__
   __shared__ float buf[2][THREADS / 64];
   const bool post = P.w_post != nullptr, pre = P.w_pre != nullptr;
   float wp[NV][8], wq[NV][8];  // w_post alpha, w_pre
+  Cols<THREADS == 64> c[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t col = (i * THREADS + threadIdx.x) * 8;
+    c[i].set((i * THREADS + threadIdx.x) * 8, static_cast<int>(P.D), THREADS * NV * 8);
     float al[8];
-    load_param(P.w_post, col, P.D - col, wp[i]);
-    load_param(P.alpha, col, P.D - col, al);
-    load_param(P.w_pre, col, P.D - col, wq[i]);
+    load_param(P.w_post, c[i], wp[i]);
+    load_param(P.alpha, c[i], al);
+    load_param(P.w_pre, c[i], wq[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) wp[i][j] *= al[j];
   }
   for (int64_t r = blockIdx.x; r < P.rows; r += gridDim.x) {
     float xv[NV][8], fv[NV][8], gv[NV][8];
+    {
+      Raw8<T> rx[NV], rf[NV], rg[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t col = (i * THREADS + threadIdx.x) * 8;
-      load8(f + r * ld_f + col, P.D - col, 0.0f, fv[i]);
-      load8(x + r * ld_x + col, P.D - col, 0.0f, xv[i]);
-      if (gate_kind == kGateFull) load8(gate + r * ld_g + col, P.D - col, 0.0f, gv[i]);
+      for (int i = 0; i < NV; ++i) {
+        load_cols(rf[i], f + r * ld_f, c[i]);
+        load_cols(rx[i], x + r * ld_x, c[i]);
+        if (gate_kind == kGateFull) load_cols(rg[i], gate + r * ld_g, c[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        get_cols(rf[i], c[i], 0.0f, fv[i]);
+        get_cols(rx[i], c[i], 0.0f, xv[i]);
+        if (gate_kind == kGateFull) rg[i].get(gv[i]);
+      }
     }
     const float s_row = gate_kind == kGateRow ? sigmoid_f(to_f32(gate[r * ld_g])) : 1.0f;
     float rp = 1.0f;
@@ -118,18 +135,16 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(const T* __restrict__
         xv[i][j] += fv[i][j] * rp * wp[i][j] * s;
         q += xv[i][j] * xv[i][j];
       }
-      const int64_t col = (i * THREADS + threadIdx.x) * 8;
-      store8(y + r * ld_y + col, P.D - col, xv[i]);
+      store_cols(y + r * ld_y, c[i], xv[i]);
     }
     if (pre) {
       const float rq = 1.0f / sqrtf(block_sum<THREADS>(q, buf[1]) * P.inv_d + P.eps);
       if (threadIdx.x == 0) rstd_pre[r] = rq;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int64_t col = (i * THREADS + threadIdx.x) * 8;
 #pragma unroll
         for (int j = 0; j < 8; ++j) xv[i][j] = xv[i][j] * rq * wq[i][j];
-        store8(h + r * ld_h + col, P.D - col, xv[i]);
+        store_cols(h + r * ld_h, c[i], xv[i]);
       }
     }
     // with one sum per row the same buffer serves every row
@@ -137,45 +152,128 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(const T* __restrict__
   }
 }
 
-// Rows a workgroup's slot holds: dw_post, dalpha, dw_pre, in this order.
-template <typename T, int THREADS, int NV>
-__global__ __launch_bounds__(THREADS) void norm_bwd_kernel(const T* __restrict__ dy, int64_t ld_dy,
-                                                           const T* __restrict__ dh, int64_t ld_dh,
-                                                           const T* __restrict__ x, int64_t ld_x,
-                                                           const T* __restrict__ f, int64_t ld_f,
-                                                           const T* __restrict__ gate, int64_t ld_g, int gate_kind,
-                                                           NormParams P, const float* __restrict__ rstd_post,
-                                                           const float* __restrict__ rstd_pre, T* __restrict__ dx,
-                                                           int64_t ld_dx, T* __restrict__ df, int64_t ld_df,
-                                                           T* __restrict__ dgate, int64_t ld_dg,
-                                                           float* __restrict__ slots) {
-  __shared__ float buf[2][THREADS / 64];
-  const bool post = P.w_post != nullptr, pre = P.w_pre != nullptr;
-  const bool second = post || gate_kind == kGateRow;  // a second sum over the row is needed
-  float wp[NV][8], al[NV][8], wq[NV][8];
-  float g_post[NV][8] = {}, g_alpha[NV][8] = {}, g_pre[NV][8] = {};
+// One row of the backward's inputs as loaded.
+template <typename T, int NV>
+struct BwdRow {
+  Raw8<T> f[NV], g[NV], x[NV], u[NV], d[NV];
+  float rp, rq, g_row;
+};
+
+template <typename T>
+struct BwdIn {
+  const T *dy, *dh, *x, *f, *gate;
+  int64_t ld_dy, ld_dh, ld_x, ld_f, ld_g;
+  const float *rstd_post, *rstd_pre;
+  int gate_kind;
+};
+
+template <typename T, int NV, bool TINY>
+__device__ __forceinline__ void load_row(BwdRow<T, NV>& R, const BwdIn<T>& I, bool post, bool pre, int64_t r,
+                                         const Cols<TINY> (&c)[NV]) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t col = (i * THREADS + threadIdx.x) * 8;
-    load_param(P.w_post, col, P.D - col, wp[i]);
-    load_param(P.alpha, col, P.D - col, al[i]);
-    load_param(P.w_pre, col, P.D - col, wq[i]);
+    load_cols(R.f[i], I.f + r * I.ld_f, c[i]);
+    if (I.gate_kind == kGateFull) load_cols(R.g[i], I.gate + r * I.ld_g, c[i]);
+    if (pre) {
+      load_cols(R.x[i], I.x + r * I.ld_x, c[i]);
+      load_cols(R.u[i], I.dh + r * I.ld_dh, c[i]);
+    }
+    load_cols(R.d[i], I.dy + r * I.ld_dy, c[i]);
   }
+  R.rp = post ? I.rstd_post[r] : 1.0f;
+  R.rq = pre ? I.rstd_pre[r] : 1.0f;
+  R.g_row = I.gate_kind == kGateRow ? to_f32(I.gate[r * I.ld_g]) : 0.0f;
+}
+
+// A workgroup's slot holds A and dw_pre. The next row's loads are issued as soon
+// as the current row is unpacked (bf16; a float32 row would take twice the
+// registers). The parameters of a thread's channels sit in LDS (each thread
+// reads back what it wrote, 16 bytes per lane side by side), which leaves the
+// registers to the running sums, two rows and four waves per SIMD. For D > 8192
+// a thread has 16 channels: their running sums take the LDS instead, and the
+// parameters are read again for every row.
+template <typename T, int THREADS, int NV>
+__global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormParams P, T* __restrict__ dx,
+                                                              int64_t ld_dx, T* __restrict__ df, int64_t ld_df,
+                                                              T* __restrict__ dgate, int64_t ld_dg,
+                                                              float* __restrict__ slots) {
+  constexpr bool kWide = NV > 1, kAhead = !kWide && sizeof(T) == 2;
+  constexpr int kKept = kWide ? 2 * NV : 3;  // LDS: per thread, kKept sets of eight floats
+  __shared__ float buf[2][THREADS / 64];
+  __shared__ f32x4 kept[kKept][2][THREADS];
+  const bool post = P.w_post != nullptr, pre = P.w_pre != nullptr;
+  const int gate_kind = I.gate_kind;
+  const bool second = post || gate_kind == kGateRow;  // a second sum over the row is needed
+  const float* const params[3] = {P.w_post, P.alpha, P.w_pre};
+  const auto put = [&](int k, const float(&w)[8]) {
+    kept[k][0][threadIdx.x] = f32x4{w[0], w[1], w[2], w[3]};
+    kept[k][1][threadIdx.x] = f32x4{w[4], w[5], w[6], w[7]};
+  };
+  const auto get = [&](int k, float(&w)[8]) {
+    const f32x4 a = kept[k][0][threadIdx.x], b = kept[k][1][threadIdx.x];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = a[j];
+      w[4 + j] = b[j];
+    }
+  };
+  float sum_a[NV][8] = {}, sum_pre[NV][8] = {};  // (wide: in LDS)
+  Cols<THREADS == 64> c[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    c[i].set((i * THREADS + threadIdx.x) * 8, static_cast<int>(P.D), THREADS * NV * 8);
+    if constexpr (kWide) {
+      put(2 * i, sum_a[i]);
+      put(2 * i + 1, sum_pre[i]);
+    }
+  }
+  if constexpr (!kWide) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      float w[8];
+      load_param(params[k], c[0], w);
+      put(k, w);
+    }
+  }
+  const auto param = [&](int k, int i, float(&w)[8]) {
+    if constexpr (kWide)
+      load_param(params[k], c[i], w);
+    else
+      get(k, w);
+  };
+  // sum[j] += a[j] * b[j] for the columns of piece i
+  const auto accumulate = [&](int which, int i, float(&sum)[8], const float(&a)[8], const float(&b)[8]) {
+    float t[8];
+    if constexpr (kWide) get(2 * i + which, t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (kWide)
+        t[j] = __builtin_fmaf(a[j], b[j], t[j]);
+      else
+        sum[j] = __builtin_fmaf(a[j], b[j], sum[j]);
+    }
+    if constexpr (kWide) put(2 * i + which, t);
+  };
+  BwdRow<T, NV> R;
+  if constexpr (kAhead) load_row(R, I, post, pre, blockIdx.x, c);  // the grid has at most `rows` workgroups
+#pragma unroll 1
   for (int64_t r = blockIdx.x; r < P.rows; r += gridDim.x) {
     float d[NV][8], fh[NV][8], s[NV][8], yh[NV][8], u[NV][8];
+    if constexpr (!kAhead) load_row(R, I, post, pre, r, c);
+    const float rp = R.rp, rq = R.rq, s_row = gate_kind == kGateRow ? sigmoid_f(R.g_row) : 1.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t col = (i * THREADS + threadIdx.x) * 8, n = P.D - col;
-      load8(f + r * ld_f + col, n, 0.0f, fh[i]);
-      load8(dy + r * ld_dy + col, n, 0.0f, d[i]);
-      if (gate_kind == kGateFull) load8(gate + r * ld_g + col, n, 0.0f, s[i]);
+      get_cols(R.f[i], c[i], 0.0f, fh[i]);
+      if (gate_kind == kGateFull) R.g[i].get(s[i]);
       if (pre) {
-        load8(x + r * ld_x + col, n, 0.0f, yh[i]);
-        load8(dh + r * ld_dh + col, n, 0.0f, u[i]);
+        get_cols(R.x[i], c[i], 0.0f, yh[i]);
+        get_cols(R.u[i], c[i], 0.0f, u[i]);
       }
+      get_cols(R.d[i], c[i], 0.0f, d[i]);
     }
-    const float s_row = gate_kind == kGateRow ? sigmoid_f(to_f32(gate[r * ld_g])) : 1.0f;
-    const float rp = post ? rstd_post[r] : 1.0f;
+    if constexpr (kAhead) {
+      if (r + gridDim.x < P.rows) load_row(R, I, post, pre, r + gridDim.x, c);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -184,43 +282,50 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(const T* __restrict__
         s[i][j] = gate_kind == kGateFull ? sigmoid_f(s[i][j]) : s_row;
       }
     if (pre) {
-      const float rq = rstd_pre[r];
       float q = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        float wp[8], al[8], wq[8];
+        param(0, i, wp);
+        param(1, i, al);
+        param(2, i, wq);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) yh[i][j] = (yh[i][j] + fh[i][j] * (wp[j] * al[j]) * s[i][j]) * rq;
+        accumulate(1, i, sum_pre[i], u[i], yh[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          yh[i][j] = (yh[i][j] + fh[i][j] * (wp[i][j] * al[i][j]) * s[i][j]) * rq;
-          g_pre[i][j] += u[i][j] * yh[i][j];
-          u[i][j] *= wq[i][j];
-          q += u[i][j] * yh[i][j];
+          const float w = u[i][j] * wq[j];
+          q = __builtin_fmaf(w, yh[i][j], q);
+          d[i][j] = __builtin_fmaf(rq, w, d[i][j]);
         }
-      const float mean = block_sum<THREADS>(q, buf[0]) * P.inv_d;
+      }
+      const float m = rq * (block_sum<THREADS>(q, buf[0]) * P.inv_d);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[i][j] += rq * (u[i][j] - yh[i][j] * mean);
+        for (int j = 0; j < 8; ++j) d[i][j] = __builtin_fmaf(-m, yh[i][j], d[i][j]);
     }
-    // d = the gradient of y; from here u = dn = d alpha s
+    // d = the gradient of y, u = w_post dn
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t col = (i * THREADS + threadIdx.x) * 8;
-      store8(dx + r * ld_dx + col, P.D - col, d[i]);
+      store_cols(dx + r * ld_dx, c[i], d[i]);
+      float wp[8], al[8];
+      param(0, i, wp);
+      param(1, i, al);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[i][j] *= s[i][j];
+      accumulate(0, i, sum_a[i], d[i], fh[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float ds = d[i][j] * s[i][j];
-        g_alpha[i][j] += ds * (fh[i][j] * wp[i][j]);
-        const float dn = ds * al[i][j];
-        g_post[i][j] += dn * fh[i][j];
-        u[i][j] = dn * wp[i][j];
-        q += u[i][j] * fh[i][j];
+        u[i][j] = d[i][j] * (al[j] * wp[j]);
+        q = __builtin_fmaf(u[i][j], fh[i][j], q);
       }
       if (gate_kind == kGateFull) {
         float dg[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) dg[j] = u[i][j] * fh[i][j] * (1.0f - s[i][j]);
-        store8(dgate + r * ld_dg + col, P.D - col, dg);
+        store_cols(dgate + r * ld_dg, c[i], dg);
       }
     }
     if (second) {
@@ -231,51 +336,66 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(const T* __restrict__
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) u[i][j] = rp * (u[i][j] - fh[i][j] * mean);
+          for (int j = 0; j < 8; ++j) u[i][j] = rp * __builtin_fmaf(-mean, fh[i][j], u[i][j]);
       }
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t col = (i * THREADS + threadIdx.x) * 8;
-      store8(df + r * ld_df + col, P.D - col, u[i]);
-    }
+    for (int i = 0; i < NV; ++i) store_cols(df + r * ld_df, c[i], u[i]);
     if (THREADS > 64 && second != pre) __syncthreads();
   }
+  if (!slots) return;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t col = (i * THREADS + threadIdx.x) * 8, n = P.D - col;
-    float* o = slots + static_cast<int64_t>(blockIdx.x) * 3 * P.D + col;
-    if (post) store8(o, n, g_post[i]);
-    if (P.alpha) store8(o + P.D, n, g_alpha[i]);
-    if (pre) store8(o + 2 * P.D, n, g_pre[i]);
+    float* o = slots + static_cast<int64_t>(blockIdx.x) * 2 * P.D;
+    if constexpr (kWide) {
+      get(2 * i, sum_a[i]);
+      get(2 * i + 1, sum_pre[i]);
+    }
+    if (post || P.alpha) store_cols(o, c[i], sum_a[i]);
+    if (pre) store_cols(o + P.D, c[i], sum_pre[i]);
   }
 }
 
-// Workgroup (64 columns, parameter): wave w adds slots w, w + 4, ... in order,
-// the four sums meet left to right, one add into the output.
+// Workgroup (64 columns, sum): wave w of 16 adds slots w, w + 16, ... in order,
+// the waves' sums meet left to right, one add into each output. Sixteen waves
+// with 16 loads each in flight, since a call has few columns and the slots come
+// from other XCDs' L2s.
 struct NormGrads {
-  float* g[3];
+  float *w_post, *alpha, *w_pre;
 };
-__global__ __launch_bounds__(256) void norm_fold_kernel(const float* __restrict__ slots, int n_slots, int64_t D,
-                                                        NormGrads G) {
-  __shared__ float part[4][64];
-  float* out = G.g[blockIdx.y];
-  if (!out) return;
+constexpr int kFoldWaves = 16;
+__global__ __launch_bounds__(64 * kFoldWaves) void norm_fold_kernel(const float* __restrict__ slots, int n_slots,
+                                                                    NormParams P, NormGrads G) {
+  __shared__ float part[kFoldWaves][64];
+  const bool second = blockIdx.y == 1;  // dw_pre
+  if (second ? !G.w_pre : !(G.w_post || G.alpha)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-  const float* p = slots + blockIdx.y * D + col;
+  const int64_t D = P.D, col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  const float* p = slots + blockIdx.y * D + (col < D ? col : 0);
   float t = 0.0f;
-  if (col < D)
-    for (int b = wave; b < n_slots; b += 64) {
-      float v[16];
+  for (int b = wave; b < n_slots; b += 16 * kFoldWaves) {
+    float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = b + 4 * i < n_slots ? p[static_cast<int64_t>(b + 4 * i) * 3 * D] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) t += v[i];
+    for (int i = 0; i < 16; ++i) {
+      const int k = b + kFoldWaves * i;
+      v[i] = p[static_cast<int64_t>(k < n_slots ? k : wave) * 2 * D];  // (a slot read already, and not added)
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += b + kFoldWaves * i < n_slots ? v[i] : 0.0f;
+  }
   part[wave][lane] = t;
   __syncthreads();
-  if (wave == 0 && col < D) out[col] += ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane];
+  if (wave != 0 || col >= D) return;
+  t = part[0][lane];
+#pragma unroll
+  for (int w = 1; w < kFoldWaves; ++w) t += part[w][lane];
+  if (second) {
+    G.w_pre[col] += t;
+  } else {
+    const float wp = P.w_post ? P.w_post[col] : 1.0f, al = P.alpha ? P.alpha[col] : 1.0f;
+    if (G.w_post) G.w_post[col] += t * al;
+    if (G.alpha) G.alpha[col] += t * wp;
+  }
 }
 
 int threads_for(int64_t D) {
@@ -286,14 +406,14 @@ int threads_for(int64_t D) {
 
 // Workgroups of a launch: every compute unit's 2048 threads, twice over for the
 // forward (no per-workgroup cost beyond the parameters), once for the backward,
-// whose every workgroup writes a slot of 12 bytes per channel.
+// whose every workgroup writes a slot of 8 bytes per channel.
 int64_t groups_for(int64_t T, int64_t D, bool bwd) {
   const int64_t g = 256 * (2048 / threads_for(D)) * (bwd ? 1 : 2) / (bwd && D > 512 ? 2 : 1);
   return T < g ? T : g;
 }
 size_t ws_bytes_for(int64_t T, int64_t D) {
   return T == 0 || D == 0 ? 0
-                          : DET_WS_HEADER_BYTES + align_up(static_cast<size_t>(groups_for(T, D, true) * 3 * D) * 4, 256);
+                          : DET_WS_HEADER_BYTES + align_up(static_cast<size_t>(groups_for(T, D, true) * 2 * D) * 4, 256);
 }
 
 int check_sizes(const char* what, int64_t T, int64_t D) {
@@ -435,11 +555,14 @@ extern "C" int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh,
   const dim3 grid(static_cast<uint32_t>(groups));
   const hipStream_t st = as_stream(stream);
   auto* slots = need ? reinterpret_cast<float*>(static_cast<char*>(ws) + DET_WS_HEADER_BYTES) : nullptr;
-#define DET_NORM_BWD(E)                                                                                               \
-  DET_NORM_LAUNCH(norm_bwd_kernel, E, static_cast<const E*>(dy), dy_ld, static_cast<const E*>(dh), dh_ld,             \
-                  static_cast<const E*>(x), x_ld, static_cast<const E*>(f), f_ld, static_cast<const E*>(gate), gate_ld, \
-                  kind, P, rstd_post, rstd_pre, static_cast<E*>(dx), dx_ld, static_cast<E*>(df), df_ld,               \
-                  static_cast<E*>(dgate), dgate_ld, slots)
+#define DET_NORM_BWD(E)                                                                                              \
+  {                                                                                                                  \
+    const BwdIn<E> I{static_cast<const E*>(dy), static_cast<const E*>(dh), static_cast<const E*>(x),                 \
+                     static_cast<const E*>(f),  static_cast<const E*>(gate), dy_ld, dh_ld, x_ld, f_ld, gate_ld,      \
+                     rstd_post, rstd_pre, kind};                                                                     \
+    DET_NORM_LAUNCH(norm_bwd_kernel, E, I, P, static_cast<E*>(dx), dx_ld, static_cast<E*>(df), df_ld,                \
+                    static_cast<E*>(dgate), dgate_ld, slots)                                                         \
+  }
   if (dtype == DET_BF16) {
     DET_NORM_BWD(uint16_t)
   } else {
@@ -447,7 +570,7 @@ extern "C" int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh,
   }
 #undef DET_NORM_BWD
   if (need)
-    hipLaunchKernelGGL(norm_fold_kernel, dim3(static_cast<uint32_t>(ceil_div(D, 64)), 3), dim3(256), 0, st, slots,
-                       static_cast<int>(groups), D, NormGrads{{dw_post, dalpha, dw_pre}});
+    hipLaunchKernelGGL(norm_fold_kernel, dim3(static_cast<uint32_t>(ceil_div(D, 64)), 2), dim3(64 * kFoldWaves), 0, st, slots,
+                       static_cast<int>(groups), P, NormGrads{dw_post, dalpha, dw_pre});
   return check_launch("det_block_norm_bwd");
 }

@@ -27,79 +27,102 @@
 namespace detgrad {
 namespace {
 
-constexpr int kFwdThreads = 512, kBwdThreads = 256, kFoldThreads = 1024;
+constexpr int kFwdThreads = 512, kDirectThreads = 1024, kBwdThreads = 256, kFoldThreads = 1024;
 
-__device__ __forceinline__ float log_sigmoid(float z) {
-  const float e = __builtin_amdgcn_exp2f(-fabsf(z) * kLog2e);
-  return fminf(z, 0.0f) - kLn2 * __builtin_amdgcn_logf(1.0f + e);
-}
+// Rows of a lane group whose loads are in flight together.
+constexpr int kAhead = 4, kBwdAhead = 2;
+
+// exp(x) for x <= 0 as 2^(x log2 e): within (|x| + 2) units in the last place,
+// which is below 2^-24 of the row's largest score (its own error is |x| e^x).
+__device__ __forceinline__ float exp_nonpos(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // The row's unnormalised scores e (0 past the row's end and in a row whose
 // logits are all -inf) and 1 / their sum (0 for such a row). z: the logits,
 // -inf past the end.
-template <int LPR, int NI>
-__device__ __forceinline__ float row_scores(const float (&z)[NI][8], bool sigmoid, float (&e)[NI][8], float& sum) {
+//
+// softmax: e = exp(z - max z). sigmoid: with t = exp(-|z|), r = 1 / (1 + t),
+// sigmoid(z) = exp(min(z, 0)) r; e = exp(min(z, 0) - max min(z, 0)) r keeps a
+// row of very negative logits from underflowing, and is sigmoid(z) itself where
+// the row has a logit >= 0. q = sigmoid(-z) for the gradient.
+template <int LPR, int NI, bool SIGMOID, bool GRAD>
+__device__ __forceinline__ float row_scores(const float (&z)[NI][8], float (&e)[NI][8], float (&q)[NI][8]) {
   float m = -__builtin_inff();
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      e[i][j] = sigmoid ? log_sigmoid(z[i][j]) : z[i][j];
-      m = fmaxf(m, e[i][j]);
-    }
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, z[i][j]);
   m = lanes_max<LPR>(m);
+  if (SIGMOID) m = fminf(m, 0.0f);
   m = m == -__builtin_inff() ? 0.0f : m;  // nothing but -inf: every score is exp(-inf) = 0 (and a NaN stays one)
   float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      e[i][j] = exp_e(e[i][j] - m);
-      s += e[i][j];
-    }
-  sum = lanes_sum<LPR>(s);
-  return sum == 0.0f ? 0.0f : 1.0f / sum;
-}
-
-template <typename T, int LPR, int NI>
-__global__ __launch_bounds__(kFwdThreads) void router_tile_kernel(const T* __restrict__ z, int64_t ld, uint32_t rows,
-                                                                  int E, const int32_t* __restrict__ ids,
-                                                                  int64_t ids_ld, int K,
-                                                                  const int32_t* __restrict__ offs, int S, int log_bt,
-                                                                  int sigmoid, float* __restrict__ slot_p,
-                                                                  int32_t* __restrict__ slot_c,
-                                                                  int32_t* __restrict__ table) {
-  constexpr int RPW = 64 / LPR, W = kFwdThreads / 64, COLS = 8 * LPR * NI;
-  __shared__ float part[W][COLS];
-  __shared__ int32_t hist[COLS];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (blockIdx.x == 0 && wave == 0) write_tile_table(offs, S, rows, log_bt, table);
-  int seg;
-  uint32_t r0, r1;
-  if (!tile_of(offs, S, rows, log_bt, blockIdx.x, seg, r0, r1)) return;  // the grid covers the worst case
-  for (int i = threadIdx.x; i < COLS; i += kFwdThreads) hist[i] = 0;
-  __syncthreads();
-  const uint32_t slots = (r1 - r0) * static_cast<uint32_t>(K);  // < 2^31 (checked by the host)
-  for (uint32_t i = threadIdx.x; i < slots; i += kFwdThreads) {
-    const uint32_t r = i / static_cast<uint32_t>(K);
-    const int32_t id = ids[static_cast<int64_t>(r0 + r) * ids_ld + (i - r * K)];
-    if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
-  }
-  float acc[NI][8] = {};
-  const int sub = lane / LPR, l = lane % LPR;
-  for (uint32_t r = r0 + wave * RPW; r < r1; r += W * RPW) {
-    const bool in = r + sub < r1;
-    float v[NI][8], e[NI][8], sum;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int col = (i * LPR + l) * 8;
-      load8(z + static_cast<int64_t>(in ? r + sub : r) * ld + col, in ? E - col : 0, -__builtin_inff(), v[i]);
-    }
-    const float inv = row_scores<LPR, NI>(v, sigmoid, e, sum);
+  if constexpr (SIGMOID) {
+    const bool below = __ballot(m != 0.0f) != 0;  // some row of the wave has only negative logits
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j] += e[i][j] * inv;
+      for (int j = 0; j < 8; ++j) {
+        const float t = exp_nonpos(-fabsf(z[i][j])), r = __builtin_amdgcn_rcpf(1.0f + t), tr = t * r;
+        const bool neg = z[i][j] < 0.0f;
+        e[i][j] = neg ? tr : r;
+        if (GRAD) q[i][j] = neg ? r : tr;
+        if (below) e[i][j] = exp_nonpos(fminf(z[i][j], 0.0f) - m) * r;
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[i][j] = exp_nonpos(z[i][j] - m);
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+    s += ((e[i][0] + e[i][1]) + (e[i][2] + e[i][3])) + ((e[i][4] + e[i][5]) + (e[i][6] + e[i][7]));
+  s = lanes_sum<LPR>(s);
+  return s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
+}
+
+// P of the rows [r0, r1) into part[0][0..E) and their counts into hist (both
+// LDS), by the whole workgroup; ends with the barrier that makes them visible.
+// Lane group g of wave w takes rows r0 + w RPW + g, then every W RPW-th row.
+template <typename T, int LPR, int NI, bool SIGMOID, int THREADS>
+__device__ __forceinline__ void sum_rows(const T* __restrict__ z, int64_t ld, int E, const int32_t* __restrict__ ids,
+                                         int64_t ids_ld, int K, uint32_t r0, uint32_t r1,
+                                         float (&part)[THREADS / 64][8 * LPR * NI], int32_t (&hist)[8 * LPR * NI]) {
+  constexpr int RPW = 64 / LPR, W = THREADS / 64, COLS = 8 * LPR * NI;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int sub = lane / LPR, l = lane % LPR;
+  for (int i = threadIdx.x; i < COLS; i += THREADS) hist[i] = 0;
+  __syncthreads();
+  Cols<LPR == 1> c[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) c[i].set((i * LPR + l) * 8, E, COLS);
+  float acc[NI][8] = {};
+  for (uint32_t r = r0 + wave * RPW; r < r1; r += kAhead * W * RPW) {
+    Raw8<T> raw[kAhead][NI];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const uint32_t row = r + a * W * RPW + sub;  // past the end: the tile's first row again, and not added
+#pragma unroll
+      for (int i = 0; i < NI; ++i) load_cols(raw[a][i], z + static_cast<int64_t>(row < r1 ? row : r0) * ld, c[i]);
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      float v[NI][8], e[NI][8], q[NI][8];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) get_cols(raw[a][i], c[i], -__builtin_inff(), v[i]);
+      const float inv = row_scores<LPR, NI, SIGMOID, false>(v, e, q);
+      if (r + a * W * RPW + sub < r1) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[i][j] = __builtin_fmaf(e[i][j], inv, acc[i][j]);
+      }
+    }
+  }
+  const uint32_t slots = (r1 - r0) * static_cast<uint32_t>(K);  // < 2^31 (checked by the host)
+  for (uint32_t i = threadIdx.x; i < slots; i += THREADS) {
+    const uint32_t r = i / static_cast<uint32_t>(K);
+    const int32_t id = ids[static_cast<int64_t>(r0 + r) * ids_ld + (i - r * K)];
+    if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
   }
 #pragma unroll
   for (int i = 0; i < NI; ++i)
@@ -107,27 +130,97 @@ __global__ __launch_bounds__(kFwdThreads) void router_tile_kernel(const T* __res
     for (int j = 0; j < 8; ++j) {
 #pragma unroll
       for (int d = LPR; d < 64; d <<= 1) acc[i][j] += __shfl_xor(acc[i][j], d);
-      if (sub == 0) part[wave][(i * LPR + l) * 8 + j] = acc[i][j];
+      if (sub == 0 && c[i].own(j)) part[wave][c[i].base + j] = acc[i][j];
     }
   __syncthreads();
-  for (int c = threadIdx.x; c < E; c += kFwdThreads) {
+  for (int c = threadIdx.x; c < E; c += THREADS) {
     float s = part[0][c];
 #pragma unroll
     for (int w = 1; w < W; ++w) s += part[w][c];
-    slot_p[static_cast<int64_t>(blockIdx.x) * E + c] = s;
+    part[0][c] = s;  // column c belongs to this thread alone
+  }
+}
+
+template <typename T, int LPR, int NI, bool SIGMOID>
+__global__ __launch_bounds__(kFwdThreads) void router_tile_kernel(const T* __restrict__ z, int64_t ld, uint32_t rows,
+                                                                  int E, const int32_t* __restrict__ ids,
+                                                                  int64_t ids_ld, int K,
+                                                                  const int32_t* __restrict__ offs, int S, int log_bt,
+                                                                  float* __restrict__ slot_p,
+                                                                  int32_t* __restrict__ slot_c,
+                                                                  int32_t* __restrict__ table) {
+  __shared__ float part[kFwdThreads / 64][8 * LPR * NI];
+  __shared__ int32_t hist[8 * LPR * NI];
+  if (blockIdx.x == 0 && threadIdx.x < 64) write_tile_table(offs, S, rows, log_bt, table);
+  int seg;
+  uint32_t r0, r1;
+  if (!tile_of(offs, S, rows, log_bt, blockIdx.x, seg, r0, r1)) return;  // the grid covers the worst case
+  sum_rows<T, LPR, NI, SIGMOID, kFwdThreads>(z, ld, E, ids, ids_ld, K, r0, r1, part, hist);
+  for (int c = threadIdx.x; c < E; c += kFwdThreads) {
+    slot_p[static_cast<int64_t>(blockIdx.x) * E + c] = part[0][c];
     slot_c[static_cast<int64_t>(blockIdx.x) * E + c] = hist[c];
   }
 }
 
-// b_s for every lane: the running maximum of the clamped offsets up to s.
-__device__ __forceinline__ uint32_t segment_bound(const int32_t* __restrict__ offs, int s, uint32_t rows) {
+// [b_s, b_{s+1}): the running maximum of the clamped offsets, by every wave.
+__device__ __forceinline__ void segment_bounds(const int32_t* __restrict__ offs, int s, uint32_t rows, uint32_t& b0,
+                                               uint32_t& b1) {
+  const uint32_t last = clamp_off(offs[s + 1], rows);
   uint32_t b = 0;
   for (int i = threadIdx.x & 63; i <= s; i += 64) b = umax(b, clamp_off(offs[i], rows));
-  return lane_value(scan_max(b), 63);
+  b0 = lane_value(scan_max(b), 63);
+  b1 = umax(b0, last);
 }
 
 __device__ __forceinline__ double balance_scale(double coeff, int E, int K, uint32_t n) {
   return n == 0 ? 0.0 : coeff * E / (static_cast<double>(K) * n * n);
+}
+
+// A segment's outputs from its sums, by the first E threads' columns: returns
+// nothing; loss = scale sum_e counts P in float64, adjacent tree per wave, waves
+// left to right.
+template <int THREADS>
+__device__ __forceinline__ void write_loss(double term, double scale, float* __restrict__ loss,
+                                           double (&sl)[THREADS / 64]) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) term += __shfl_xor(term, d);
+  if ((threadIdx.x & 63) == 0) sl[threadIdx.x >> 6] = term;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double tot = sl[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 64; ++w) tot += sl[w];
+    *loss = static_cast<float>(scale * tot);
+  }
+}
+
+// The whole forward of a small call in one launch: workgroup s sums all tokens
+// of segment s.
+template <typename T, int LPR, int NI, bool SIGMOID>
+__global__ __launch_bounds__(kDirectThreads) void router_direct_kernel(const T* __restrict__ z, int64_t ld,
+                                                                       uint32_t rows, int E,
+                                                                       const int32_t* __restrict__ ids,
+                                                                       int64_t ids_ld, int K,
+                                                                       const int32_t* __restrict__ offs, double coeff,
+                                                                       float* __restrict__ psum,
+                                                                       int32_t* __restrict__ counts,
+                                                                       float* __restrict__ loss) {
+  __shared__ float part[kDirectThreads / 64][8 * LPR * NI];
+  __shared__ int32_t hist[8 * LPR * NI];
+  __shared__ double sl[kDirectThreads / 64];
+  const int s = blockIdx.x;
+  uint32_t r0, r1;
+  segment_bounds(offs, s, rows, r0, r1);
+  sum_rows<T, LPR, NI, SIGMOID, kDirectThreads>(z, ld, E, ids, ids_ld, K, r0, r1, part, hist);
+  double term = 0.0;
+  const int c = threadIdx.x;  // E <= 1024: one column per thread
+  if (c < E) {
+    const float p = part[0][c];
+    psum[static_cast<int64_t>(s) * E + c] = p;
+    counts[static_cast<int64_t>(s) * E + c] = hist[c];
+    term = static_cast<double>(p) * hist[c];
+  }
+  write_loss<kDirectThreads>(term, balance_scale(coeff, E, K, r1 - r0), loss + s, sl);
 }
 
 // One workgroup per segment: `strips` threads per expert (1024 over E rounded up
@@ -146,20 +239,23 @@ __global__ __launch_bounds__(kFoldThreads) void router_fold_kernel(const float* 
   const int s = blockIdx.x, cols = 1 << log_cols, strips = kFoldThreads >> log_cols;
   const int c = threadIdx.x & (cols - 1), strip = threadIdx.x >> log_cols;
   const int t0 = table[s], t1 = table[s + 1];
+  uint32_t b0, b1;
+  segment_bounds(offs, s, rows, b0, b1);
+  const double scale = balance_scale(coeff, E, K, b1 - b0);
   double p = 0.0;
   int32_t n = 0;
   if (c < E)
-    for (int t = t0 + strip; t < t1; t += 8 * strips) {
-      float v[8];
-      int32_t k[8];
+    for (int t = t0 + strip; t < t1; t += 16 * strips) {
+      float v[16];
+      int32_t k[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 16; ++i) {
         const int tt = t + i * strips;
         v[i] = tt < t1 ? slot_p[static_cast<int64_t>(tt) * E + c] : 0.0f;
         k[i] = tt < t1 ? slot_c[static_cast<int64_t>(tt) * E + c] : 0;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 16; ++i) {
         p += v[i];
         n += k[i];
       }
@@ -177,24 +273,15 @@ __global__ __launch_bounds__(kFoldThreads) void router_fold_kernel(const float* 
     counts[static_cast<int64_t>(s) * E + c] = n;
     term = p * n;
   }
-  for (int d = 1; d < 64; d <<= 1) term += __shfl_xor(term, d);
-  if ((threadIdx.x & 63) == 0) sl[threadIdx.x >> 6] = term;
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    const uint32_t n_s = segment_bound(offs, s + 1, rows) - segment_bound(offs, s, rows);
-    double tot = 0.0;
-    for (int w = 0; w < kFoldThreads / 64; ++w) tot += sl[w];
-    if (threadIdx.x == 0) loss[s] = static_cast<float>(balance_scale(coeff, E, K, n_s) * tot);
-  }
+  write_loss<kFoldThreads>(term, scale, loss + s, sl);
 }
 
-template <typename T, int LPR, int NI>
+template <typename T, int LPR, int NI, bool SIGMOID>
 __global__ __launch_bounds__(kBwdThreads) void router_bwd_kernel(T* __restrict__ dz, int64_t ld_d,
                                                                  const T* __restrict__ z, int64_t ld, uint32_t rows,
                                                                  int E, int K, const int32_t* __restrict__ offs,
                                                                  int S, int log_bt, const int32_t* __restrict__ counts,
-                                                                 const float* __restrict__ dloss, double coeff,
-                                                                 int sigmoid) {
+                                                                 const float* __restrict__ dloss, double coeff) {
   constexpr int RPW = 64 / LPR, W = kBwdThreads / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int seg;
@@ -204,42 +291,50 @@ __global__ __launch_bounds__(kBwdThreads) void router_bwd_kernel(T* __restrict__
   const int sub = lane / LPR, l = lane % LPR;
   // c_e less the mean count: the gradient does not change (sum p = 1), and the
   // difference c_e - sum p c keeps its digits when the experts are nearly balanced
-  const int64_t ref = static_cast<int64_t>(K) * (s1 - s0) / E;
-  float c[NI][8];
+  const int32_t ref = static_cast<int32_t>(static_cast<uint32_t>(K) * (s1 - s0) / static_cast<uint32_t>(E));
+  Cols<LPR == 1> c[NI];
+  float n[NI][8];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+  for (int i = 0; i < NI; ++i) {
+    c[i].set((i * LPR + l) * 8, E, 8 * LPR * NI);
+    Raw8<float> raw;  // whole numbers, moved as bits
+    load_cols(raw, reinterpret_cast<const float*>(counts) + static_cast<int64_t>(seg) * E, c[i]);
+    raw.get(n[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = (i * LPR + l) * 8 + j;
-      c[i][j] = e < E ? static_cast<float>(counts[static_cast<int64_t>(seg) * E + e] - ref) : 0.0f;
+    for (int j = 0; j < 8; ++j) n[i][j] = c[i].own(j) ? static_cast<float>(__float_as_int(n[i][j]) - ref) : 0.0f;
+  }
+  for (uint32_t r = r0 + wave * RPW; r < r1; r += kBwdAhead * W * RPW) {
+    Raw8<T> raw[kBwdAhead][NI];
+#pragma unroll
+    for (int a = 0; a < kBwdAhead; ++a) {
+      const uint32_t row = r + a * W * RPW + sub;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) load_cols(raw[a][i], z + static_cast<int64_t>(row < r1 ? row : r0) * ld, c[i]);
     }
-  for (uint32_t r = r0 + wave * RPW; r < r1; r += W * RPW) {
-    const bool in = r + sub < r1;
-    const int64_t row = in ? r + sub : r;
-    float v[NI][8], e[NI][8], sum;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int col = (i * LPR + l) * 8;
-      load8(z + row * ld + col, in ? E - col : 0, -__builtin_inff(), v[i]);
-    }
-    const float inv = row_scores<LPR, NI>(v, sigmoid, e, sum);
-    float mean = 0.0f;
+    for (int a = 0; a < kBwdAhead; ++a) {
+      const uint32_t row = r + a * W * RPW + sub;
+      float v[NI][8], e[NI][8], q[NI][8];
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+      for (int i = 0; i < NI; ++i) get_cols(raw[a][i], c[i], -__builtin_inff(), v[i]);
+      const float inv = row_scores<LPR, NI, SIGMOID, true>(v, e, q);
+      float mean = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mean += e[i][j] * c[i][j];
-    mean = lanes_sum<LPR>(mean) * inv;
-    const float gi = g * inv;
+      for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int col = (i * LPR + l) * 8;
-      float d[8];
+        for (int j = 0; j < 8; ++j) mean = __builtin_fmaf(e[i][j], n[i][j], mean);
+      mean = lanes_sum<LPR>(mean) * inv;
+      const float gi = g * inv;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        d[j] = gi * e[i][j] * (c[i][j] - mean);
-        if (sigmoid) d[j] = d[j] / (1.0f + exp_e(v[i][j]));
+      for (int i = 0; i < NI; ++i) {
+        float d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          d[j] = gi * e[i][j] * (n[i][j] - mean);
+          if (SIGMOID) d[j] *= q[i][j];
+        }
+        if (row < r1) store_cols(dz + static_cast<int64_t>(row) * ld_d, c[i], d);
       }
-      if (in) store8(dz + row * ld_d + col, E - col, d);
     }
   }
 }
@@ -247,17 +342,23 @@ __global__ __launch_bounds__(kBwdThreads) void router_bwd_kernel(T* __restrict__
 int64_t max_tiles(int64_t T, int64_t S, int log_bt) { return ceil_div(T, int64_t(1) << log_bt) + S; }
 
 // Rows per tile, a power of two from the shape alone: about `target` tiles, but
-// no fewer rows than one step of the workgroup's waves takes.
-int tile_log(int64_t T, int64_t E, int threads, int64_t target) {
+// no fewer rows than the workgroup's waves take in one step of `ahead` rows per
+// lane group.
+int tile_log(int64_t T, int64_t E, int threads, int ahead, int64_t target) {
   int64_t lpr = 1;
   while (lpr * 8 < E && lpr < 64) lpr *= 2;
-  const int64_t step = threads / 64 * (64 / lpr);
+  const int64_t step = threads / 64 * (64 / lpr) * ahead;
   int lg = 0;
   while ((int64_t(1) << lg) < step || (T >> lg) > target) ++lg;
   return lg;
 }
-int fwd_log(int64_t T, int64_t E) { return tile_log(T, E, kFwdThreads, 256); }
-int bwd_log(int64_t T, int64_t E) { return tile_log(T, E, kBwdThreads, 2048); }
+int fwd_log(int64_t T, int64_t E) { return tile_log(T, E, kFwdThreads, kAhead, 512); }
+int bwd_log(int64_t T, int64_t E) { return tile_log(T, E, kBwdThreads, kBwdAhead, 2048); }
+
+// A call whose logits would fill at most 16 steps of one workgroup's lanes is
+// summed by one workgroup per segment: in the worst case (one segment) that
+// costs about what the second launch and its slots would.
+bool direct(int64_t T, int64_t E) { return T * E <= (int64_t(16) << 13); }
 
 struct RouterWs {
   size_t table, p, c, total;
@@ -298,21 +399,29 @@ int check_call(const char* what, int dtype, int score, double coeff, int64_t T, 
 
 using namespace detgrad;
 
-// LPR x NI by E (eight columns per lane): calls F<LPR, NI>.
-#define DET_ROUTER_BY_E(F)    \
-  if (E <= 8) F(1, 1)         \
-  else if (E <= 16) F(2, 1)   \
-  else if (E <= 32) F(4, 1)   \
-  else if (E <= 64) F(8, 1)   \
-  else if (E <= 128) F(16, 1) \
-  else if (E <= 256) F(32, 1) \
-  else if (E <= 512) F(64, 1) \
-  else F(64, 2)
+// LPR x NI by E (eight columns per lane), the element type and the score.
+#define DET_ROUTER_BY_E(F, TYPE, SIG)          \
+  if (E <= 8) { F(TYPE, SIG, 1, 1) }           \
+  else if (E <= 16) { F(TYPE, SIG, 2, 1) }     \
+  else if (E <= 32) { F(TYPE, SIG, 4, 1) }     \
+  else if (E <= 64) { F(TYPE, SIG, 8, 1) }     \
+  else if (E <= 128) { F(TYPE, SIG, 16, 1) }   \
+  else if (E <= 256) { F(TYPE, SIG, 32, 1) }   \
+  else if (E <= 512) { F(TYPE, SIG, 64, 1) }   \
+  else { F(TYPE, SIG, 64, 2) }
+#define DET_ROUTER_DISPATCH(F)                                                 \
+  if (dtype == DET_BF16) {                                                     \
+    if (score == DET_SCORE_SIGMOID) { DET_ROUTER_BY_E(F, uint16_t, true) }     \
+    else { DET_ROUTER_BY_E(F, uint16_t, false) }                               \
+  } else {                                                                     \
+    if (score == DET_SCORE_SIGMOID) { DET_ROUTER_BY_E(F, float, true) }        \
+    else { DET_ROUTER_BY_E(F, float, false) }                                  \
+  }
 
 extern "C" int det_router_balance_workspace_size(int64_t T, int64_t E, int64_t K, int64_t S, size_t* bytes) {
   if (!bytes) return set_error(DET_ERR_INVALID_ARG, "router_balance: bytes is NULL");
   if (int s = check_sizes("router_balance", T, E, K, S)) return s;
-  *bytes = S == 0 ? 0 : layout(T, E, S).total;
+  *bytes = S == 0 || direct(T, E) ? 0 : layout(T, E, S).total;
   return ok();
 }
 
@@ -328,42 +437,44 @@ extern "C" int det_router_balance(const void* logits, int64_t ld, int dtype, con
     return set_error(DET_ERR_INVALID_ARG, "%s: NULL pointer", what);
   if (T && ids_ld < K) return set_error(DET_ERR_INVALID_ARG, "%s: ids row stride < K", what);
   if (T && ids_ld > (int64_t(1) << 44) / T) return set_error(DET_ERR_UNSUPPORTED, "%s: tensor too large", what);
+  const bool one = direct(T, E);
   const RouterWs w = layout(T, E, S);
-  if (int s = check_workspace(ws, ws_bytes, w.total)) return s;
+  if (int s = check_workspace(ws, ws_bytes, one ? 0 : w.total)) return s;
   const size_t es = dtype_size(dtype);
   const Buf outs[] = {{"counts", range1d(counts, S * E * 4)},
                       {"prob_sum", range1d(prob_sum, S * E * 4)},
                       {"loss", range1d(loss, S * 4)},
-                      {"the workspace", range1d(ws, ws_bytes)}};
+                      {"the workspace", range1d(one ? nullptr : ws, ws_bytes)}};
   const Buf ins[] = {{"logits", range2d(logits, T, E, ld, es)},
                      {"ids", range2d(ids, T, K, ids_ld, 4)},
                      {"offs", range1d(offs, (S + 1) * 4)}};
   if (int s = check_overlaps(what, outs, 4, ins, 3)) return s;
   const hipStream_t st = as_stream(stream);
   char* b = static_cast<char*>(ws);
-  auto* table = reinterpret_cast<int32_t*>(b + w.table);
-  auto* sp = reinterpret_cast<float*>(b + w.p);
-  auto* sc = reinterpret_cast<int32_t*>(b + w.c);
+  auto* table = one ? nullptr : reinterpret_cast<int32_t*>(b + w.table);
+  auto* sp = one ? nullptr : reinterpret_cast<float*>(b + w.p);
+  auto* sc = one ? nullptr : reinterpret_cast<int32_t*>(b + w.c);
   const int lg = fwd_log(T, E);
-  const dim3 grid(static_cast<uint32_t>(max_tiles(T, S, lg)));
-  const int sg = score == DET_SCORE_SIGMOID;
-#define DET_ROUTER_FWD(LPR, NI)                                                                                       \
-  {                                                                                                                   \
-    if (dtype == DET_BF16)                                                                                            \
-      hipLaunchKernelGGL((router_tile_kernel<uint16_t, LPR, NI>), grid, dim3(kFwdThreads), 0, st,                     \
-                         static_cast<const uint16_t*>(logits), ld, (uint32_t)T, (int)E, ids, ids_ld, (int)K, offs,    \
-                         (int)S, lg, sg, sp, sc, table);                                                              \
-    else                                                                                                              \
-      hipLaunchKernelGGL((router_tile_kernel<float, LPR, NI>), grid, dim3(kFwdThreads), 0, st,                        \
-                         static_cast<const float*>(logits), ld, (uint32_t)T, (int)E, ids, ids_ld, (int)K, offs,       \
-                         (int)S, lg, sg, sp, sc, table);                                                              \
+  const dim3 grid(static_cast<uint32_t>(one ? S : max_tiles(T, S, lg)));
+#define DET_ROUTER_FWD(TYPE, SIG, LPR, NI)                                                                       \
+  {                                                                                                              \
+    if (one)                                                                                                     \
+      hipLaunchKernelGGL((router_direct_kernel<TYPE, LPR, NI, SIG>), grid, dim3(kDirectThreads), 0, st,          \
+                         static_cast<const TYPE*>(logits), ld, (uint32_t)T, (int)E, ids, ids_ld, (int)K, offs,   \
+                         coeff, prob_sum, counts, loss);                                                         \
+    else                                                                                                         \
+      hipLaunchKernelGGL((router_tile_kernel<TYPE, LPR, NI, SIG>), grid, dim3(kFwdThreads), 0, st,               \
+                         static_cast<const TYPE*>(logits), ld, (uint32_t)T, (int)E, ids, ids_ld, (int)K, offs,   \
+                         (int)S, lg, sp, sc, table);                                                             \
   }
-  DET_ROUTER_BY_E(DET_ROUTER_FWD)
+  DET_ROUTER_DISPATCH(DET_ROUTER_FWD)
 #undef DET_ROUTER_FWD
-  int log_cols = 0;
-  while ((1 << log_cols) < E) ++log_cols;
-  hipLaunchKernelGGL(router_fold_kernel, dim3(static_cast<uint32_t>(S)), dim3(kFoldThreads), 0, st, sp, sc, table, offs,
-                     (uint32_t)T, (int)E, (int)K, log_cols, coeff, prob_sum, counts, loss);
+  if (!one) {
+    int log_cols = 0;
+    while ((1 << log_cols) < E) ++log_cols;
+    hipLaunchKernelGGL(router_fold_kernel, dim3(static_cast<uint32_t>(S)), dim3(kFoldThreads), 0, st, sp, sc, table,
+                       offs, (uint32_t)T, (int)E, (int)K, log_cols, coeff, prob_sum, counts, loss);
+  }
   return check_launch("det_router_balance");
 }
 
@@ -387,19 +498,11 @@ extern "C" int det_router_balance_bwd(void* dlogits, int64_t ld_d, const void* l
   const hipStream_t st = as_stream(stream);
   const int lg = bwd_log(T, E);
   const dim3 grid(static_cast<uint32_t>(max_tiles(T, S, lg)));
-  const int sg = score == DET_SCORE_SIGMOID;
-#define DET_ROUTER_BWD(LPR, NI)                                                                                       \
-  {                                                                                                                   \
-    if (dtype == DET_BF16)                                                                                            \
-      hipLaunchKernelGGL((router_bwd_kernel<uint16_t, LPR, NI>), grid, dim3(kBwdThreads), 0, st,                      \
-                         static_cast<uint16_t*>(dlogits), ld_d, static_cast<const uint16_t*>(logits), ld,             \
-                         (uint32_t)T, (int)E, (int)K, offs, (int)S, lg, counts, dloss, coeff, sg);                    \
-    else                                                                                                              \
-      hipLaunchKernelGGL((router_bwd_kernel<float, LPR, NI>), grid, dim3(kBwdThreads), 0, st,                         \
-                         static_cast<float*>(dlogits), ld_d, static_cast<const float*>(logits), ld, (uint32_t)T,      \
-                         (int)E, (int)K, offs, (int)S, lg, counts, dloss, coeff, sg);                                 \
-  }
-  DET_ROUTER_BY_E(DET_ROUTER_BWD)
+#define DET_ROUTER_BWD(TYPE, SIG, LPR, NI)                                                                       \
+  hipLaunchKernelGGL((router_bwd_kernel<TYPE, LPR, NI, SIG>), grid, dim3(kBwdThreads), 0, st,                    \
+                     static_cast<TYPE*>(dlogits), ld_d, static_cast<const TYPE*>(logits), ld, (uint32_t)T,       \
+                     (int)E, (int)K, offs, (int)S, lg, counts, dloss, coeff);
+  DET_ROUTER_DISPATCH(DET_ROUTER_BWD)
 #undef DET_ROUTER_BWD
   return check_launch("det_router_balance_bwd");
 }

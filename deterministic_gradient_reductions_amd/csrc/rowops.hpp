@@ -37,6 +37,12 @@ template <>
 struct Raw8<uint16_t> {
   u32x4 w;
   __device__ __forceinline__ void load(const uint16_t* p) { __builtin_memcpy(&w, p, 16); }
+  __device__ __forceinline__ void load_short(const uint16_t* p, int n) {  // n in [1, 8): the last element repeats
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = static_cast<uint32_t>(p[2 * i < n ? 2 * i : n - 1]) |
+             (static_cast<uint32_t>(p[2 * i + 1 < n ? 2 * i + 1 : n - 1]) << 16);
+  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -51,6 +57,13 @@ struct Raw8<float> {
   __device__ __forceinline__ void load(const float* p) {
     __builtin_memcpy(&a, p, 16);
     __builtin_memcpy(&b, p + 4, 16);
+  }
+  __device__ __forceinline__ void load_short(const float* p, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = p[i < n ? i : n - 1];
+      b[i] = p[i + 4 < n ? i + 4 : n - 1];
+    }
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
@@ -101,6 +114,53 @@ __device__ __forceinline__ void store8(T* p, int64_t n, const float (&v)[8]) {
   }
 }
 
+// A lane's eight columns of rows of N elements, chosen so that the lane's load is
+// one unconditional access inside the row (loads under a branch would be waited
+// for one by one): columns base .. base + 7, of which those in [lo, hi) are the
+// lane's own. The lane that would cross the row's end moves back to N - 8 and
+// leaves the columns it shares with its neighbour alone; a lane past the end
+// (lo = 8) owns none and reads the row's start. Rows of N < 8 elements, which
+// only instances with TINY meet, are loaded element by element.
+template <bool TINY>
+struct Cols {
+  int base, lo, hi;
+  bool all;  // every lane of the launch owns eight columns (the same everywhere)
+  __device__ __forceinline__ bool own(int j) const { return j >= lo && (!TINY || j < hi); }
+  // col: the lane's first column, a multiple of 8; cover: the columns of all lanes
+  __device__ __forceinline__ void set(int col, int N, int cover) {
+    all = N == cover;
+    hi = TINY && N < 8 ? N : 8;
+    base = col + 8 <= N ? col : (col < N && hi == 8 ? N - 8 : 0);
+    lo = col < N ? col - base : 8;
+  }
+};
+template <typename T, bool TINY>
+__device__ __forceinline__ void load_cols(Raw8<T>& r, const T* row, const Cols<TINY>& c) {
+  if (TINY && c.hi < 8)  // (the same for every lane)
+    r.load_short(row, c.hi);
+  else
+    r.load(row + c.base);
+}
+// v = the loaded values, `fill` in columns that are not the lane's own
+template <typename T, bool TINY>
+__device__ __forceinline__ void get_cols(const Raw8<T>& r, const Cols<TINY>& c, float fill, float (&v)[8]) {
+  r.get(v);
+  if (!c.all) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c.own(j) ? v[j] : fill;
+  }
+}
+template <typename T, bool TINY>
+__device__ __forceinline__ void store_cols(T* row, const Cols<TINY>& c, const float (&v)[8]) {
+  if (c.all || (c.lo == 0 && (!TINY || c.hi == 8))) {
+    store8_full(row + c.base, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c.own(j)) row[c.base + j] = from_f32<T>(v[j]);
+  }
+}
+
 constexpr float kLog2e = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
 
 // exp(x) within about 1.5 units in the last place: x log2(e) = k + f with k
@@ -114,6 +174,21 @@ __device__ __forceinline__ float exp_e(float x) {
   return x < -104.0f ? 0.0f : (x > 89.0f ? __builtin_inff() : y);
 }
 
+// The lane swaps of a value with itself give every lane the copies of both
+// partners at distance 16 or 32 (a from the lower, b from the upper), on the
+// VALU instead of through LDS; every lane of the wave must be active.
+struct Halves {
+  float a, b;
+};
+__device__ __forceinline__ Halves halves16(float v) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return {__uint_as_float(p[0]), __uint_as_float(p[1])};
+}
+__device__ __forceinline__ Halves halves32(float v) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return {__uint_as_float(p[0]), __uint_as_float(p[1])};
+}
+
 // Sum / maximum over groups of W consecutive lanes (W a power of two); every
 // lane of a group ends with the group's value, added in one fixed tree.
 template <int W>
@@ -122,8 +197,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
   if constexpr (W >= 4) v = v + dpp_mov<DPP_XOR2>(v);
   if constexpr (W >= 8) v = v + dpp_mov<DPP_HALF_MIRROR>(v);
   if constexpr (W >= 16) v = v + dpp_mov<DPP_MIRROR>(v);
-  if constexpr (W >= 32) v = v + __shfl_xor(v, 16);
-  if constexpr (W >= 64) v = v + __shfl_xor(v, 32);
+  if constexpr (W >= 32) {
+    const Halves h = halves16(v);
+    v = h.a + h.b;
+  }
+  if constexpr (W >= 64) {
+    const Halves h = halves32(v);
+    v = h.a + h.b;
+  }
   return v;
 }
 template <int W>
@@ -132,8 +213,14 @@ __device__ __forceinline__ float lanes_max(float v) {
   if constexpr (W >= 4) v = fmaxf(v, dpp_mov<DPP_XOR2>(v));
   if constexpr (W >= 8) v = fmaxf(v, dpp_mov<DPP_HALF_MIRROR>(v));
   if constexpr (W >= 16) v = fmaxf(v, dpp_mov<DPP_MIRROR>(v));
-  if constexpr (W >= 32) v = fmaxf(v, __shfl_xor(v, 16));
-  if constexpr (W >= 64) v = fmaxf(v, __shfl_xor(v, 32));
+  if constexpr (W >= 32) {
+    const Halves h = halves16(v);
+    v = fmaxf(h.a, h.b);
+  }
+  if constexpr (W >= 64) {
+    const Halves h = halves32(v);
+    v = fmaxf(h.a, h.b);
+  }
   return v;
 }
 

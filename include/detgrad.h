@@ -513,7 +513,7 @@ int det_block_norm(const void* x, int64_t x_ld, const void* f, int64_t f_ld, con
  *   dx = D,  dn = D * alpha * sigmoid(gate),  fh = f * rstd_post (w_post NULL: fh = f)
  *   dgate = dn * n * (1 - sigmoid(gate))          (summed over the row for gate_cols = 1)
  *   df = rstd_post * (w_post * dn - fh * mean(w_post * dn * fh))   (w_post NULL: df = dn)
- *   dw_pre += sum_t dh * yh,  dalpha += sum_t D * sigmoid(gate) * n,  dw_post += sum_t dn * fh
+ *   dw_pre += sum_t dh * yh;  with A = sum_t D * sigmoid(gate) * fh:  dw_post += alpha * A,  dalpha += w_post * A
  *
  * dx, df, dgate (dtype, overwritten) have the layouts of x, f, gate; the
  * parameter gradients ([D] float32) accumulate like every reduction here:

@@ -86,7 +86,8 @@ def check(T, E, K, dtype, offs, score, seed=0, ld=None, shift=0, z=None, coeff=0
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("T,E,K", [(1, 1, 1), (1, 8, 2), (7, 3, 2), (33, 16, 4), (100, 31, 1), (257, 64, 6),
                                    (64, 65, 8), (301, 128, 4), (129, 200, 3), (515, 256, 8), (90, 511, 5),
-                                   (70, 512, 2), (40, 513, 2), (35, 1000, 7), (9, 1024, 16), (3000, 17, 2)])
+                                   (70, 512, 2), (40, 513, 2), (35, 1000, 7), (9, 1024, 16), (3000, 17, 2), (8300, 16, 2), (700, 250, 3), (500, 500, 2),
+                                   (300, 700, 4), (2100, 72, 2), (17000, 8, 1), (1300, 128, 2), (4200, 32, 1)])
 def test_sizes(T, E, K, dtype, score):
     check(T, E, K, dtype, [0, T], score, seed=T + E)
 
@@ -230,6 +231,7 @@ def test_replay_under_load_with_poisoned_workspaces():
     z, ids = make(5000, 96, 4, BF, 12)
     z, ids, od = z.cuda(), ids.cuda(), offsets(0, 700, 2900, 4990)
     n = dg.det_router_balance_workspace_size(5000, 96, 4, 3)
+    assert n > 0
     first, load = None, SideLoad(mib=64, iters=4)
     for fill in (0, 255, 127, 1, 255, 3, 0, 90):
         ws = torch.full((n + 256,), fill, dtype=torch.uint8, device="cuda")

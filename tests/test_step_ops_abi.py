@@ -23,7 +23,7 @@ def run(fn, defaults, **kw):
     return getattr(dg.lib(), fn)(*{**defaults, **kw}.values())
 
 
-ROUTER = dict(logits=A[0], ld=64, dtype=0, ids=A[1], ids_ld=4, T=100, E=64, K=4, offs=A[2], S=2, score=0, coeff=0.01,
+ROUTER = dict(logits=A[0], ld=64, dtype=0, ids=A[1], ids_ld=4, T=100000, E=64, K=4, offs=A[2], S=2, score=0, coeff=0.01,
               counts=A[3], prob_sum=A[4], loss=A[5], ws=A[6], ws_bytes=BIG, stream=None)
 ROUTER_BWD = dict(dlogits=A[0], ld_d=64, logits=A[1], ld=64, dtype=0, T=100, E=64, K=4, offs=A[2], S=2, counts=A[3],
                   dloss=A[4], score=0, coeff=0.01, stream=None)
@@ -113,12 +113,13 @@ def test_empty_problems_touch_nothing():
 
 def test_workspace_sizes():
     assert dg.det_router_balance_workspace_size(100, 64, 4, 0) == 0
-    assert dg.det_router_balance_workspace_size(0, 64, 4, 2) > 256
+    assert dg.det_router_balance_workspace_size(100, 64, 4, 2) == 0     # a workgroup per sequence
+    assert dg.det_router_balance_workspace_size(100000, 64, 4, 2) > 256 + 2 * 64 * 8
     assert dg.det_topk_distill_workspace_size(0, 1000, 4) == 0
     assert dg.det_topk_distill_workspace_size(2000, 131072, 4) == 0     # a workgroup per row
     assert dg.det_topk_distill_workspace_size(3, 131072, 4) >= 256 + 3 * 8 * 2
     assert dg.det_block_norm_bwd_workspace_size(0, 64) == 0
-    assert dg.det_block_norm_bwd_workspace_size(1, 64) >= 256 + 3 * 64 * 4
+    assert dg.det_block_norm_bwd_workspace_size(1, 64) >= 256 + 2 * 64 * 4
     n = ctypes.c_size_t()
     L = dg.lib()
     assert L.det_router_balance_workspace_size(100, 64, 4, 2, None) == INVALID
