@@ -10,21 +10,25 @@
 // a zero gradient row, and so has a row whose dloss is 0, whatever its logits.
 //
 // Forward: one pass over the row with a running maximum and sum per lane
-// (rescaled when the maximum grows), joined over the lanes, the waves and, when
-// the call has few rows, the workgroups that share a row, always in one fixed
+// (rescaled when the maximum grows), joined over the lanes, the waves and, for
+// few very long rows, the workgroups that share a row, always in one fixed
 // order. Backward: dz of a piece of the row is written in one streaming pass,
 // then the workgroup rewrites the at most K elements that a teacher slot names.
-// Both are bound by the logits' bytes.
+// The slots' words and logits are fetched into LDS while the row streams.
+// Both are bound by the logits' bytes; the backward takes the rows in reverse
+// order, so that after a forward it first meets the rows still cached.
 #include "rowops.hpp"
 
 namespace detgrad {
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kStep = kThreads * 8;  // elements one workgroup takes per access
 constexpr int kMaxK = 1024;
+constexpr int kUnroll = 4;  // 16-byte loads of a lane in flight together
 
-// Running (maximum, sum of exp(x - maximum)) in units of z, c = log2(e) / tau.
+// Everything below is in units of log2: x2 = x log2(e) = c z with
+// c = log2(e) / tau, formed by one fused step against the reference, so only
+// the difference is rounded. MaxSum: the reference m (a rounded maximum of c z)
+// and s = sum of 2^(c z - m).
 struct MaxSum {
   float m, s;
 };
@@ -32,19 +36,19 @@ struct MaxSum {
 __device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // m stays -inf until an element above -inf is seen; its factor is then taken
-// against 0, and every exp(-inf) is 0.
+// against 0, and every 2^-inf is 0.
 __device__ __forceinline__ float finite_ref(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
   const float m = fmaxf(a.m, b.m), r = finite_ref(m);
-  return {m, a.s * pow2((a.m - r) * c) + b.s * pow2((b.m - r) * c)};
+  return {m, a.s * pow2(a.m - r) + b.s * pow2(b.m - r)};
 }
 
-__device__ __forceinline__ MaxSum wave_join(MaxSum a, float c) {
+__device__ __forceinline__ MaxSum wave_join(MaxSum a) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const MaxSum o{__shfl_xor(a.m, d), __shfl_xor(a.s, d)};
-    a = join(a, o, c);
+    a = join(a, o);
   }
   return a;
 }
@@ -53,55 +57,70 @@ __device__ __forceinline__ MaxSum wave_join(MaxSum a, float c) {
 // running sum, so the running chain is one add per 8 N elements long.
 template <int N>
 __device__ __forceinline__ void push(MaxSum& a, const float (&v)[N][8], float c) {
-  float m = a.m;
+  float m = -__builtin_inff();
 #pragma unroll
   for (int u = 0; u < N; ++u)
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = fmaxf(m, v[u][j]);
+  m = fmaxf(a.m, m * c);
   const float r = finite_ref(m);
   float s[4] = {};
 #pragma unroll
   for (int u = 0; u < N; ++u)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j & 3] += pow2((v[u][j] - r) * c);
-  a = {m, a.s * pow2((a.m - r) * c) + ((s[0] + s[1]) + (s[2] + s[3]))};
+    for (int j = 0; j < 8; ++j) s[j & 3] += pow2(__builtin_fmaf(v[u][j], c, -r));
+  a = {m, a.s * pow2(a.m - r) + ((s[0] + s[1]) + (s[2] + s[3]))};
 }
 
-// The teacher's softmax over the valid slots of one row, by one wave: t_k / tau
-// is at most m (0 if no valid slot is above -inf), sum = sum exp(t_k / tau - m).
+// A row's teacher slots in LDS: the word, teacher / tau (-inf for an invalid
+// slot, which has no weight either way) and the student's z / tau.
+struct Slots {
+  int32_t id[kMaxK];
+  float t[kMaxK], x[kMaxK];
+};
+// Slots k of the row with lo <= id < hi get their student logit (others 0); a
+// slot outside [0, V) gets the word -1.
+template <typename T, typename TT, int THREADS>
+__device__ __forceinline__ void fetch_slots(Slots& S, const int32_t* __restrict__ ids, const TT* __restrict__ t, int K,
+                                            int64_t V, float it, const T* __restrict__ z, int64_t lo, int64_t hi) {
+  for (int k = threadIdx.x; k < K; k += THREADS) {
+    const int32_t id = ids[k];
+    const float tk = to_f32(t[k]);
+    const bool valid = id >= 0 && id < V, in = id >= lo && id < hi;
+    const float x = to_f32(z[in ? id : lo]);
+    S.id[k] = valid ? id : -1;
+    S.t[k] = valid ? tk * it : -__builtin_inff();
+    S.x[k] = in ? x * it : 0.0f;
+  }
+}
+
+// The teacher's softmax over the valid slots, by one wave: t is at most m (0 if
+// no slot is above -inf), sum = sum exp(t - m); 0 for a row without mass.
 struct Teacher {
   float m, sum;
 };
-template <typename TT>
-__device__ __forceinline__ Teacher teacher_row(const int32_t* __restrict__ ids, const TT* __restrict__ t, int K,
-                                               int64_t V, float it) {
+__device__ __forceinline__ Teacher teacher_row(const Slots& S, int K) {
   const int lane = threadIdx.x & 63;
   float m = -__builtin_inff();
-  for (int k = lane; k < K; k += 64)
-    if (ids[k] >= 0 && ids[k] < V) m = fmaxf(m, to_f32(t[k]) * it);
+  for (int k = lane; k < K; k += 64) m = fmaxf(m, S.t[k]);
   m = finite_ref(lanes_max<64>(m));
   float s = 0.0f;
-  for (int k = lane; k < K; k += 64)
-    if (ids[k] >= 0 && ids[k] < V) s += exp_e(to_f32(t[k]) * it - m);
+  for (int k = lane; k < K; k += 64) s += exp_e(S.t[k] - m);
   return {m, lanes_sum<64>(s)};
 }
 
-// loss and lse of a row from its (maximum, sum), by one wave.
-template <typename T, typename TT>
-__device__ __forceinline__ void finish_row(MaxSum a, const T* __restrict__ z, const int32_t* __restrict__ ids,
-                                           const TT* __restrict__ t, int K, int64_t V, float it,
-                                           float* __restrict__ loss, float* __restrict__ lse) {
+// loss and lse of a row from its (reference, sum), by one wave.
+__device__ __forceinline__ void finish_row(MaxSum a, const Slots& S, int K, float* __restrict__ loss,
+                                           float* __restrict__ lse) {
   const int lane = threadIdx.x & 63;
-  const float l = a.m * it + logf(a.s);
-  const Teacher q = teacher_row(ids, t, K, V, it);
+  const float l = a.m * kLn2 + logf(a.s);
+  const Teacher q = teacher_row(S, K);
   float tot = 0.0f;
   const float inv = 1.0f / q.sum, logsum = logf(q.sum);
   for (int k = lane; k < K; k += 64) {
-    const int32_t id = ids[k];
-    if (id < 0 || id >= V) continue;
-    const float d = to_f32(t[k]) * it - q.m, qk = exp_e(d) * inv;
+    const float d = S.t[k] - q.m, qk = exp_e(d) * inv;
     // (a NaN q_k or an empty row's 0 / 0 does not take the q_k = 0 way out)
-    if (q.sum != 0.0f && qk != 0.0f) tot += qk * ((d - logsum) - (to_f32(z[id]) * it - l));
+    if (q.sum != 0.0f && qk != 0.0f) tot += qk * ((d - logsum) - (S.x[k] - l));
   }
   tot = lanes_sum<64>(tot);
   if (lane == 0) {
@@ -111,19 +130,21 @@ __device__ __forceinline__ void finish_row(MaxSum a, const T* __restrict__ z, co
 }
 
 // Workgroup b: piece b % n_split of row b / n_split, columns [c0, c0 + piece).
-template <typename T, typename TT>
-__global__ __launch_bounds__(kThreads) void distill_fwd_kernel(const T* __restrict__ z, int64_t ld, int64_t V,
-                                                               const int32_t* __restrict__ ids, int64_t ids_ld,
-                                                               const TT* __restrict__ teacher, int64_t t_ld, int K,
-                                                               float it, int n_split, int64_t piece,
-                                                               MaxSum* __restrict__ slots, float* __restrict__ loss,
-                                                               float* __restrict__ lse) {
-  constexpr int U = 4;
+template <typename T, typename TT, int THREADS>
+__global__ __launch_bounds__(THREADS) void distill_fwd_kernel(const T* __restrict__ z, int64_t ld, int64_t V,
+                                                              const int32_t* __restrict__ ids, int64_t ids_ld,
+                                                              const TT* __restrict__ teacher, int64_t t_ld, int K,
+                                                              float it, int n_split, int64_t piece,
+                                                              MaxSum* __restrict__ slots, float* __restrict__ loss,
+                                                              float* __restrict__ lse) {
+  constexpr int U = kUnroll, kWaves = THREADS / 64, kStep = THREADS * 8;
   __shared__ MaxSum part[kWaves];
+  __shared__ Slots S;
   const int64_t row = blockIdx.x / n_split, c0 = (blockIdx.x % n_split) * piece;
   const int64_t c1 = c0 + piece < V ? c0 + piece : V;
   const T* p = z + row * ld;
   const float c = it * kLog2e;
+  if (n_split == 1) fetch_slots<T, TT, THREADS>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, it, p, 0, V);
   MaxSum a{-__builtin_inff(), 0.0f};
   int64_t i = c0;
   for (; i + U * kStep <= c1; i += U * kStep) {
@@ -141,64 +162,71 @@ __global__ __launch_bounds__(kThreads) void distill_fwd_kernel(const T* __restri
     load8(p + k, c1 - k, -__builtin_inff(), v[0]);
     push<1>(a, v, c);
   }
-  a = wave_join(a, c);
+  a = wave_join(a);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
   __syncthreads();
   if (threadIdx.x >= 64) return;
-  a = join(join(part[0], part[1], c), join(part[2], part[3], c), c);
+  a = part[threadIdx.x % kWaves];  // every wave's value once in each group of kWaves lanes
+#pragma unroll
+  for (int d = 1; d < kWaves; d <<= 1) {
+    const MaxSum o{__shfl_xor(a.m, d), __shfl_xor(a.s, d)};
+    a = join(a, o);
+  }
   if (n_split > 1) {
     if (threadIdx.x == 0) slots[blockIdx.x] = a;
     return;
   }
-  finish_row(a, p, ids + row * ids_ld, teacher + row * t_ld, K, V, it, loss + row, lse + row);
+  finish_row(a, S, K, loss + row, lse + row);
 }
 
-// One wave per row joins the row's slots.
+// One workgroup per row joins the row's slots.
 template <typename T, typename TT>
-__global__ __launch_bounds__(64) void distill_join_kernel(const T* __restrict__ z, int64_t ld, int64_t V,
-                                                          const int32_t* __restrict__ ids, int64_t ids_ld,
-                                                          const TT* __restrict__ teacher, int64_t t_ld, int K,
-                                                          float it, int n_split, const MaxSum* __restrict__ slots,
-                                                          float* __restrict__ loss, float* __restrict__ lse) {
+__global__ __launch_bounds__(256) void distill_join_kernel(const T* __restrict__ z, int64_t ld, int64_t V,
+                                                           const int32_t* __restrict__ ids, int64_t ids_ld,
+                                                           const TT* __restrict__ teacher, int64_t t_ld, int K,
+                                                           float it, int n_split, const MaxSum* __restrict__ slots,
+                                                           float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ Slots S;
   const int64_t row = blockIdx.x;
-  const float c = it * kLog2e;
+  fetch_slots<T, TT, 256>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, it, z + row * ld, 0, V);
   MaxSum a{-__builtin_inff(), 0.0f};
-  for (int i = threadIdx.x; i < n_split; i += 64) a = join(a, slots[row * n_split + i], c);
-  a = wave_join(a, c);
-  finish_row(a, z + row * ld, ids + row * ids_ld, teacher + row * t_ld, K, V, it, loss + row, lse + row);
+  for (int i = threadIdx.x & 63; i < n_split; i += 64) a = join(a, slots[row * n_split + i]);
+  a = wave_join(a);
+  __syncthreads();
+  if (threadIdx.x < 64) finish_row(a, S, K, loss + row, lse + row);
 }
 
+constexpr int kBwdThreads = 256;
 template <typename T, typename TT>
-__global__ __launch_bounds__(kThreads) void distill_bwd_kernel(T* __restrict__ dz, int64_t ld_d,
-                                                               const T* __restrict__ z, int64_t ld, int64_t V,
-                                                               const int32_t* __restrict__ ids, int64_t ids_ld,
-                                                               const TT* __restrict__ teacher, int64_t t_ld, int K,
-                                                               float it, int n_split, int64_t piece,
-                                                               const float* __restrict__ lse,
-                                                               const float* __restrict__ dloss) {
-  constexpr int U = 4;
-  __shared__ int32_t s_id[kMaxK];  // the valid slots' ids inside the piece, -1 for the others
-  __shared__ float s_q[kMaxK];
-  const int64_t row = blockIdx.x / n_split, c0 = (blockIdx.x % n_split) * piece;
+__global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict__ dz, int64_t ld_d,
+                                                                  const T* __restrict__ z, int64_t ld, int64_t V,
+                                                                  const int32_t* __restrict__ ids, int64_t ids_ld,
+                                                                  const TT* __restrict__ teacher, int64_t t_ld, int K,
+                                                                  float it, int n_split, int64_t piece,
+                                                                  const float* __restrict__ lse,
+                                                                  const float* __restrict__ dloss) {
+  constexpr int U = kUnroll, kStep = kBwdThreads * 8;
+  __shared__ Slots S;
+  const uint32_t b = gridDim.x - 1 - blockIdx.x;
+  const int64_t row = b / n_split, c0 = (b % n_split) * piece;
   const int64_t c1 = c0 + piece < V ? c0 + piece : V;
   const T* p = z + row * ld;
   T* o = dz + row * ld_d;
-  const int32_t* id = ids + row * ids_ld;
-  const TT* t = teacher + row * t_ld;
-  const Teacher q = teacher_row(id, t, K, V, it);
+  fetch_slots<T, TT, kBwdThreads>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, it, p, c0, c1);
   const float a = dloss[row] * it, l = lse[row];
-  const bool live = a != 0.0f && q.sum != 0.0f;  // the same for the whole workgroup
-  if (!live) {
+  __syncthreads();
+  const Teacher q = teacher_row(S, K);  // the same in every wave
+  if (a == 0.0f || q.sum == 0.0f) {
     const float zero[8] = {};
     for (int64_t i = c0 + threadIdx.x * 8; i < c1; i += kStep) store8(o + i, c1 - i, zero);
     return;
   }
-  for (int k = threadIdx.x; k < K; k += kThreads) {
-    const int32_t v = id[k];
-    const bool in = v >= c0 && v < c1;
-    s_id[k] = in ? v : -1;
-    s_q[k] = in ? exp_e(to_f32(t[k]) * it - q.m) / q.sum : 0.0f;
-  }
+  // a exp(x - lse), x - lse rounded once; the root of the exponential twice, since the hardware's 2^y has no
+  // results below 2^-126 and a may be large
+  const auto grad = [&](float v) {
+    const float h = pow2(__builtin_fmaf(v, it, -l) * (0.5f * kLog2e));
+    return a * h * h;
+  };
   int64_t i = c0;
   for (; i + U * kStep <= c1; i += U * kStep) {
     Raw8<T> raw[U];
@@ -209,7 +237,7 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(T* __restrict__ d
       float v[8];
       raw[u].get(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = a * exp_e(v[j] * it - l);
+      for (int j = 0; j < 8; ++j) v[j] = grad(v[j]);
       store8_full(o + i + u * kStep + threadIdx.x * 8, v);
     }
   }
@@ -218,37 +246,48 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(T* __restrict__ d
     const int64_t k = i + threadIdx.x * 8;
     load8(p + k, c1 - k, 0.0f, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = a * exp_e(v[j] * it - l);
+    for (int j = 0; j < 8; ++j) v[j] = grad(v[j]);
     store8(o + k, c1 - k, v);
   }
-  __syncthreads();  // the piece's stores come before the rewrites below, the LDS slots are complete
-  for (int k = threadIdx.x; k < K; k += kThreads) {
-    const int32_t v = s_id[k];
-    if (v < 0) continue;
+  // every slot's q in place of its t (each thread its own), the piece's stores before the rewrites
+  for (int k = threadIdx.x; k < K; k += kBwdThreads) S.t[k] = exp_e(S.t[k] - q.m) / q.sum;
+  __syncthreads();
+  for (int k = threadIdx.x; k < K; k += kBwdThreads) {
+    const int32_t v = S.id[k];
+    if (v < c0 || v >= c1) continue;
     bool first = true;
-    for (int j = 0; j < k; ++j) first = first && s_id[j] != v;
+    for (int j = 0; j < k; ++j) first = first && S.id[j] != v;
     if (!first) continue;  // the first slot of a repeated id sums them all, in slot order
-    float m = s_q[k];
+    float m = S.t[k];
     for (int j = k + 1; j < K; ++j)
-      if (s_id[j] == v) m += s_q[j];
-    o[v] = from_f32<T>(a * (exp_e(to_f32(p[v]) * it - l) - m));
+      if (S.id[j] == v) m += S.t[j];
+    o[v] = from_f32<T>(a * (exp_e(S.x[k] - l) - m));
   }
 }
 
-// Pieces per row, from the shape alone: one when the rows alone give every
-// compute unit several workgroups, else enough for about 2048 workgroups, with
-// pieces of whole steps of the workgroup, four at least.
+// Workgroups and pieces per row, from the shape alone.
+// Forward: a workgroup of 256 threads per row when the rows alone fill the
+// compute units, of 1024 below that; a second workgroup for a row costs a
+// second launch and pays only past 2^18 elements.
+// Backward: pieces of four steps of the workgroup or more, about 2048 of them
+// when there are few rows (no second launch is needed).
 struct Split {
   int n;
   int64_t piece;
 };
-Split split_of(int64_t T, int64_t V) {
-  int64_t n = T >= 1024 || T == 0 ? 1 : ceil_div(2048, T);
-  const int64_t most = ceil_div(V, 4 * kStep);
-  if (n > most) n = most;
-  if (n < 1) n = 1;
-  const int64_t piece = align_up(ceil_div(V, n), kStep);
+Split split_into(int64_t V, int64_t n, int64_t step) {
+  const int64_t piece = align_up(ceil_div(V, n < 1 ? 1 : n), step);
   return {static_cast<int>(ceil_div(V, piece)), piece};
+}
+int fwd_threads(int64_t T) { return T >= 512 ? 256 : 1024; }
+Split fwd_split(int64_t T, int64_t V) {
+  const int64_t most = ceil_div(V, int64_t(1) << 18), want = T >= 256 || T == 0 ? 1 : ceil_div(512, T);
+  return split_into(V, want < most ? want : most, fwd_threads(T) * 8);
+}
+Split bwd_split(int64_t T, int64_t V) {
+  const int64_t step = kBwdThreads * 8, most = ceil_div(V, 4 * step);
+  const int64_t want = T >= 1024 || T == 0 ? 1 : ceil_div(2048, T);
+  return split_into(V, want < most ? want : most, step);
 }
 
 int check_args(const char* what, int dtype, int t_dtype, int64_t T, int64_t V, int64_t K, double tau) {
@@ -261,8 +300,7 @@ int check_args(const char* what, int dtype, int t_dtype, int64_t T, int64_t V, i
     return set_error(DET_ERR_UNSUPPORTED, "%s: T and V must be < 2^31 - 65536", what);
   if (!(tau >= 1e-6 && tau <= 1e6))
     return set_error(DET_ERR_INVALID_ARG, "%s: tau must lie in [1e-6, 1e6], got %g", what, tau);
-  const Split s = split_of(T, V);
-  if (T * s.n > 0x7FFFFFFF) return set_error(DET_ERR_UNSUPPORTED, "%s: problem too large", what);
+  if (T * (bwd_split(T, V).n + fwd_split(T, V).n) > 0x7FFFFFFF) return set_error(DET_ERR_UNSUPPORTED, "%s: problem too large", what);
   return DET_OK;
 }
 int check_ld(const char* what, const char* name, int64_t ld, int64_t n, int64_t T) {
@@ -272,19 +310,23 @@ int check_ld(const char* what, const char* name, int64_t ld, int64_t n, int64_t 
 }
 
 size_t ws_bytes_for(int64_t T, int64_t V) {
-  const Split s = split_of(T, V);
+  const Split s = fwd_split(T, V);
   return T == 0 || s.n == 1 ? 0 : DET_WS_HEADER_BYTES + align_up(static_cast<size_t>(T * s.n) * sizeof(MaxSum), 256);
 }
 
 template <typename T, typename TT>
 void launch_fwd(const void* z, int64_t ld, int64_t V, const int32_t* ids, int64_t ids_ld, const void* t, int64_t t_ld,
                 int64_t rows, int64_t K, float it, float* loss, float* lse, MaxSum* slots, hipStream_t st) {
-  const Split s = split_of(rows, V);
-  hipLaunchKernelGGL((distill_fwd_kernel<T, TT>), dim3(static_cast<uint32_t>(rows * s.n)), dim3(kThreads), 0, st,
-                     static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n,
-                     s.piece, slots, loss, lse);
+  const Split s = fwd_split(rows, V);
+  const dim3 grid(static_cast<uint32_t>(rows * s.n));
+  if (fwd_threads(rows) == 256)
+    hipLaunchKernelGGL((distill_fwd_kernel<T, TT, 256>), grid, dim3(256), 0, st, static_cast<const T*>(z), ld, V, ids,
+                       ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n, s.piece, slots, loss, lse);
+  else
+    hipLaunchKernelGGL((distill_fwd_kernel<T, TT, 1024>), grid, dim3(1024), 0, st, static_cast<const T*>(z), ld, V, ids,
+                       ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n, s.piece, slots, loss, lse);
   if (s.n > 1)
-    hipLaunchKernelGGL((distill_join_kernel<T, TT>), dim3(static_cast<uint32_t>(rows)), dim3(64), 0, st,
+    hipLaunchKernelGGL((distill_join_kernel<T, TT>), dim3(static_cast<uint32_t>(rows)), dim3(256), 0, st,
                        static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n,
                        slots, loss, lse);
 }
@@ -292,8 +334,8 @@ template <typename T, typename TT>
 void launch_bwd(void* dz, int64_t ld_d, const void* z, int64_t ld, int64_t V, const int32_t* ids, int64_t ids_ld,
                 const void* t, int64_t t_ld, int64_t rows, int64_t K, float it, const float* lse, const float* dloss,
                 hipStream_t st) {
-  const Split s = split_of(rows, V);
-  hipLaunchKernelGGL((distill_bwd_kernel<T, TT>), dim3(static_cast<uint32_t>(rows * s.n)), dim3(kThreads), 0, st,
+  const Split s = bwd_split(rows, V);
+  hipLaunchKernelGGL((distill_bwd_kernel<T, TT>), dim3(static_cast<uint32_t>(rows * s.n)), dim3(kBwdThreads), 0, st,
                      static_cast<T*>(dz), ld_d, static_cast<const T*>(z), ld, V, ids, ids_ld,
                      static_cast<const TT*>(t), t_ld, (int)K, it, s.n, s.piece, lse, dloss);
 }

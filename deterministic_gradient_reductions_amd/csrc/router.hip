@@ -29,23 +29,29 @@ namespace {
 
 constexpr int kFwdThreads = 512, kDirectThreads = 1024, kBwdThreads = 256, kFoldThreads = 1024;
 
-// Rows of a lane group whose loads are in flight together.
-constexpr int kAhead = 4, kBwdAhead = 2;
+// Rows of a lane group whose loads are in flight together (half as many where a
+// lane holds sixteen columns).
+constexpr int fwd_ahead(int ni) { return 2 / ni; }
+constexpr int bwd_ahead(int ni) { return 2 / ni; }
+
+template <bool B>
+struct Const {
+  static constexpr bool value = B;
+};
 
 // exp(x) for x <= 0 as 2^(x log2 e): within (|x| + 2) units in the last place,
 // which is below 2^-24 of the row's largest score (its own error is |x| e^x).
 __device__ __forceinline__ float exp_nonpos(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
-// The row's unnormalised scores e (0 past the row's end and in a row whose
-// logits are all -inf) and 1 / their sum (0 for such a row). z: the logits,
-// -inf past the end.
+// A row's scores. softmax: e = exp(z - max z). sigmoid: with t = exp(-|z|),
+// r = 1 / (1 + t), sigmoid(z) = exp(min(z, 0)) r; e = exp(min(z, 0) - max
+// min(z, 0)) r keeps a row of very negative logits from underflowing (LOW), and
+// is sigmoid(z) itself where the row has a logit >= 0.
 //
-// softmax: e = exp(z - max z). sigmoid: with t = exp(-|z|), r = 1 / (1 + t),
-// sigmoid(z) = exp(min(z, 0)) r; e = exp(min(z, 0) - max min(z, 0)) r keeps a
-// row of very negative logits from underflowing, and is sigmoid(z) itself where
-// the row has a logit >= 0. q = sigmoid(-z) for the gradient.
-template <int LPR, int NI, bool SIGMOID, bool GRAD>
-__device__ __forceinline__ float row_scores(const float (&z)[NI][8], float (&e)[NI][8], float (&q)[NI][8]) {
+// row_ref: the maximum taken out of the exponents; 0 for a row of nothing but
+// -inf, whose scores are then all exp(-inf) = 0 (and a NaN stays one).
+template <int LPR, int NI, bool SIGMOID>
+__device__ __forceinline__ float row_ref(const float (&z)[NI][8]) {
   float m = -__builtin_inff();
 #pragma unroll
   for (int i = 0; i < NI; ++i)
@@ -53,31 +59,57 @@ __device__ __forceinline__ float row_scores(const float (&z)[NI][8], float (&e)[
     for (int j = 0; j < 8; ++j) m = fmaxf(m, z[i][j]);
   m = lanes_max<LPR>(m);
   if (SIGMOID) m = fminf(m, 0.0f);
-  m = m == -__builtin_inff() ? 0.0f : m;  // nothing but -inf: every score is exp(-inf) = 0 (and a NaN stays one)
+  return m == -__builtin_inff() ? 0.0f : m;
+}
+// The unnormalised scores e (0 in columns of -inf) and 1 / their sum (0 for a
+// row without any); q = sigmoid(-z) for the gradient.
+template <int LPR, int NI, bool SIGMOID, bool LOW, bool GRAD>
+__device__ __forceinline__ float row_scores(const float (&z)[NI][8], float m, float (&e)[NI][8], float (&q)[NI][8]) {
   float s = 0.0f;
-  if constexpr (SIGMOID) {
-    const bool below = __ballot(m != 0.0f) != 0;  // some row of the wave has only negative logits
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+  for (int i = 0; i < NI; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (SIGMOID) {
         const float t = exp_nonpos(-fabsf(z[i][j])), r = __builtin_amdgcn_rcpf(1.0f + t), tr = t * r;
         const bool neg = z[i][j] < 0.0f;
-        e[i][j] = neg ? tr : r;
+        e[i][j] = LOW ? exp_nonpos(fminf(z[i][j], 0.0f) - m) * r : (neg ? tr : r);
         if (GRAD) q[i][j] = neg ? r : tr;
-        if (below) e[i][j] = exp_nonpos(fminf(z[i][j], 0.0f) - m) * r;
+      } else {
+        e[i][j] = exp_nonpos(z[i][j] - m);
       }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) e[i][j] = exp_nonpos(z[i][j] - m);
-  }
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
+    }
     s += ((e[i][0] + e[i][1]) + (e[i][2] + e[i][3])) + ((e[i][4] + e[i][5]) + (e[i][6] + e[i][7]));
+  }
   s = lanes_sum<LPR>(s);
   return s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
+}
+
+// The next rows of a wave's lane groups, `AHEAD` per group, W RPW apart, loaded
+// together; those past r1 repeat row r0 (and are not used).
+template <typename T, int LPR, int NI, int AHEAD>
+__device__ __forceinline__ void load_rows(const T* __restrict__ z, int64_t ld, uint32_t r, uint32_t step, uint32_t r0,
+                                          uint32_t r1, const Cols<LPR == 1> (&c)[NI], float (&v)[AHEAD][NI][8]) {
+  Raw8<T> raw[AHEAD][NI];
+#pragma unroll
+  for (int a = 0; a < AHEAD; ++a) {
+    const uint32_t row = r + a * step < r1 ? r + a * step : r0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) load_cols(raw[a][i], z + static_cast<int64_t>(row) * ld, c[i]);
+  }
+#pragma unroll
+  for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+    for (int i = 0; i < NI; ++i) raw[a][i].get(v[a][i]);
+  if (!c[0].all) {
+    keep_branch();
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[a][i][j] = c[i].own(j) ? v[a][i][j] : -__builtin_inff();
+  }
 }
 
 // P of the rows [r0, r1) into part[0][0..E) and their counts into hist (both
@@ -87,7 +119,7 @@ template <typename T, int LPR, int NI, bool SIGMOID, int THREADS>
 __device__ __forceinline__ void sum_rows(const T* __restrict__ z, int64_t ld, int E, const int32_t* __restrict__ ids,
                                          int64_t ids_ld, int K, uint32_t r0, uint32_t r1,
                                          float (&part)[THREADS / 64][8 * LPR * NI], int32_t (&hist)[8 * LPR * NI]) {
-  constexpr int RPW = 64 / LPR, W = THREADS / 64, COLS = 8 * LPR * NI;
+  constexpr int RPW = 64 / LPR, W = THREADS / 64, COLS = 8 * LPR * NI, kAhead = fwd_ahead(NI);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int sub = lane / LPR, l = lane % LPR;
   for (int i = threadIdx.x; i < COLS; i += THREADS) hist[i] = 0;
@@ -97,32 +129,45 @@ __device__ __forceinline__ void sum_rows(const T* __restrict__ z, int64_t ld, in
   for (int i = 0; i < NI; ++i) c[i].set((i * LPR + l) * 8, E, COLS);
   float acc[NI][8] = {};
   for (uint32_t r = r0 + wave * RPW; r < r1; r += kAhead * W * RPW) {
-    Raw8<T> raw[kAhead][NI];
+    float v[kAhead][NI][8], m[kAhead];
+    load_rows<T, LPR, NI, kAhead>(z, ld, r + sub, W * RPW, r0, r1, c, v);
+    bool low = false;
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const uint32_t row = r + a * W * RPW + sub;  // past the end: the tile's first row again, and not added
-#pragma unroll
-      for (int i = 0; i < NI; ++i) load_cols(raw[a][i], z + static_cast<int64_t>(row < r1 ? row : r0) * ld, c[i]);
+      m[a] = row_ref<LPR, NI, SIGMOID>(v[a]);
+      low = low || m[a] != 0.0f;
     }
+    const auto add = [&](auto is_low) {
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      float v[NI][8], e[NI][8], q[NI][8];
+      for (int a = 0; a < kAhead; ++a) {
+        float e[NI][8], q[NI][8];
+        float inv = row_scores<LPR, NI, SIGMOID, decltype(is_low)::value, false>(v[a], m[a], e, q);
+        if (r + sub + a * W * RPW < r1) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) get_cols(raw[a][i], c[i], -__builtin_inff(), v[i]);
-      const float inv = row_scores<LPR, NI, SIGMOID, false>(v, e, q);
-      if (r + a * W * RPW + sub < r1) {
+          for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc[i][j] = __builtin_fmaf(e[i][j], inv, acc[i][j]);
+            for (int j = 0; j < 8; ++j) acc[i][j] = __builtin_fmaf(e[i][j], inv, acc[i][j]);
+        }
       }
+    };
+    if (SIGMOID && __ballot(low) != 0) {
+      keep_branch();
+      add(Const<true>{});
+    } else {
+      add(Const<false>{});
     }
   }
   const uint32_t slots = (r1 - r0) * static_cast<uint32_t>(K);  // < 2^31 (checked by the host)
-  for (uint32_t i = threadIdx.x; i < slots; i += THREADS) {
-    const uint32_t r = i / static_cast<uint32_t>(K);
-    const int32_t id = ids[static_cast<int64_t>(r0 + r) * ids_ld + (i - r * K)];
-    if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
+  for (uint32_t i = threadIdx.x; i < slots; i += 4 * THREADS) {
+    int32_t id[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t at = i + k * THREADS < slots ? i + k * THREADS : i, r = at / static_cast<uint32_t>(K);
+      id[k] = ids[static_cast<int64_t>(r0 + r) * ids_ld + (at - r * K)];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * THREADS < slots && id[k] >= 0 && id[k] < E) atomicAdd(&hist[id[k]], 1);
   }
 #pragma unroll
   for (int i = 0; i < NI; ++i)
@@ -244,22 +289,23 @@ __global__ __launch_bounds__(kFoldThreads) void router_fold_kernel(const float* 
   const double scale = balance_scale(coeff, E, K, b1 - b0);
   double p = 0.0;
   int32_t n = 0;
-  if (c < E)
-    for (int t = t0 + strip; t < t1; t += 16 * strips) {
-      float v[16];
-      int32_t k[16];
+  const int cc = c < E ? c : 0;
+  for (int t = t0 + strip; t < t1; t += 16 * strips) {
+    float v[16];
+    int32_t k[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int tt = t + i * strips;
-        v[i] = tt < t1 ? slot_p[static_cast<int64_t>(tt) * E + c] : 0.0f;
-        k[i] = tt < t1 ? slot_c[static_cast<int64_t>(tt) * E + c] : 0;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        p += v[i];
-        n += k[i];
-      }
+    for (int i = 0; i < 16; ++i) {  // past the last tile: the strip's first one again, and not added
+      const int64_t at = static_cast<int64_t>(t + i * strips < t1 ? t + i * strips : t) * E + cc;
+      v[i] = slot_p[at];
+      k[i] = slot_c[at];
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const bool in = t + i * strips < t1;
+      p += in ? v[i] : 0.0f;
+      n += in ? k[i] : 0;
+    }
+  }
   sp[threadIdx.x] = p;
   sc[threadIdx.x] = n;
   __syncthreads();
@@ -282,7 +328,7 @@ __global__ __launch_bounds__(kBwdThreads) void router_bwd_kernel(T* __restrict__
                                                                  int E, int K, const int32_t* __restrict__ offs,
                                                                  int S, int log_bt, const int32_t* __restrict__ counts,
                                                                  const float* __restrict__ dloss, double coeff) {
-  constexpr int RPW = 64 / LPR, W = kBwdThreads / 64;
+  constexpr int RPW = 64 / LPR, W = kBwdThreads / 64, kBwdAhead = bwd_ahead(NI);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int seg;
   uint32_t r0, r1, s0, s1;
@@ -304,37 +350,44 @@ __global__ __launch_bounds__(kBwdThreads) void router_bwd_kernel(T* __restrict__
     for (int j = 0; j < 8; ++j) n[i][j] = c[i].own(j) ? static_cast<float>(__float_as_int(n[i][j]) - ref) : 0.0f;
   }
   for (uint32_t r = r0 + wave * RPW; r < r1; r += kBwdAhead * W * RPW) {
-    Raw8<T> raw[kBwdAhead][NI];
+    float v[kBwdAhead][NI][8], m[kBwdAhead];
+    load_rows<T, LPR, NI, kBwdAhead>(z, ld, r + sub, W * RPW, r0, r1, c, v);
+    bool low = false;
 #pragma unroll
     for (int a = 0; a < kBwdAhead; ++a) {
-      const uint32_t row = r + a * W * RPW + sub;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) load_cols(raw[a][i], z + static_cast<int64_t>(row < r1 ? row : r0) * ld, c[i]);
+      m[a] = row_ref<LPR, NI, SIGMOID>(v[a]);
+      low = low || m[a] != 0.0f;
     }
+    const auto write = [&](auto is_low) {
 #pragma unroll
-    for (int a = 0; a < kBwdAhead; ++a) {
-      const uint32_t row = r + a * W * RPW + sub;
-      float v[NI][8], e[NI][8], q[NI][8];
+      for (int a = 0; a < kBwdAhead; ++a) {
+        const uint32_t row = r + sub + a * W * RPW;
+        float e[NI][8], q[NI][8];
+        const float inv = row_scores<LPR, NI, SIGMOID, decltype(is_low)::value, true>(v[a], m[a], e, q);
+        float mean = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) get_cols(raw[a][i], c[i], -__builtin_inff(), v[i]);
-      const float inv = row_scores<LPR, NI, SIGMOID, true>(v, e, q);
-      float mean = 0.0f;
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+          for (int j = 0; j < 8; ++j) mean = __builtin_fmaf(e[i][j], n[i][j], mean);
+        mean = lanes_sum<LPR>(mean) * inv;
+        const float gi = g * inv;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mean = __builtin_fmaf(e[i][j], n[i][j], mean);
-      mean = lanes_sum<LPR>(mean) * inv;
-      const float gi = g * inv;
+        for (int i = 0; i < NI; ++i) {
+          float d[8];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        float d[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          d[j] = gi * e[i][j] * (n[i][j] - mean);
-          if (SIGMOID) d[j] *= q[i][j];
+          for (int j = 0; j < 8; ++j) {
+            d[j] = gi * e[i][j] * (n[i][j] - mean);
+            if (SIGMOID) d[j] *= q[i][j];
+          }
+          if (row < r1) store_cols(dz + static_cast<int64_t>(row) * ld_d, c[i], d);
         }
-        if (row < r1) store_cols(dz + static_cast<int64_t>(row) * ld_d, c[i], d);
       }
+    };
+    if (SIGMOID && __ballot(low) != 0) {
+      keep_branch();
+      write(Const<true>{});
+    } else {
+      write(Const<false>{});
     }
   }
 }
@@ -344,16 +397,16 @@ int64_t max_tiles(int64_t T, int64_t S, int log_bt) { return ceil_div(T, int64_t
 // Rows per tile, a power of two from the shape alone: about `target` tiles, but
 // no fewer rows than the workgroup's waves take in one step of `ahead` rows per
 // lane group.
-int tile_log(int64_t T, int64_t E, int threads, int ahead, int64_t target) {
+int tile_log(int64_t T, int64_t E, int threads, int (*ahead)(int), int64_t target) {
   int64_t lpr = 1;
   while (lpr * 8 < E && lpr < 64) lpr *= 2;
-  const int64_t step = threads / 64 * (64 / lpr) * ahead;
+  const int64_t step = threads / 64 * (64 / lpr) * ahead(E > 512 ? 2 : 1);
   int lg = 0;
   while ((int64_t(1) << lg) < step || (T >> lg) > target) ++lg;
   return lg;
 }
-int fwd_log(int64_t T, int64_t E) { return tile_log(T, E, kFwdThreads, kAhead, 512); }
-int bwd_log(int64_t T, int64_t E) { return tile_log(T, E, kBwdThreads, kBwdAhead, 2048); }
+int fwd_log(int64_t T, int64_t E) { return tile_log(T, E, kFwdThreads, fwd_ahead, 1024); }
+int bwd_log(int64_t T, int64_t E) { return tile_log(T, E, kBwdThreads, bwd_ahead, 2048); }
 
 // A call whose logits would fill at most 16 steps of one workgroup's lanes is
 // summed by one workgroup per segment: in the worst case (one segment) that

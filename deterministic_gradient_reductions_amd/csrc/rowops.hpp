@@ -114,6 +114,10 @@ __device__ __forceinline__ void store8(T* p, int64_t n, const float (&v)[8]) {
   }
 }
 
+// In a block under a condition that is the same for all lanes and seldom true:
+// keeps the compiler from computing the block always and selecting.
+__device__ __forceinline__ void keep_branch() { asm volatile(""); }
+
 // A lane's eight columns of rows of N elements, chosen so that the lane's load is
 // one unconditional access inside the row (loads under a branch would be waited
 // for one by one): columns base .. base + 7, of which those in [lo, hi) are the
@@ -146,6 +150,7 @@ template <typename T, bool TINY>
 __device__ __forceinline__ void get_cols(const Raw8<T>& r, const Cols<TINY>& c, float fill, float (&v)[8]) {
   r.get(v);
   if (!c.all) {
+    keep_branch();
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = c.own(j) ? v[j] : fill;
   }

@@ -27,8 +27,8 @@ ROUTER = dict(logits=A[0], ld=64, dtype=0, ids=A[1], ids_ld=4, T=100000, E=64, K
               counts=A[3], prob_sum=A[4], loss=A[5], ws=A[6], ws_bytes=BIG, stream=None)
 ROUTER_BWD = dict(dlogits=A[0], ld_d=64, logits=A[1], ld=64, dtype=0, T=100, E=64, K=4, offs=A[2], S=2, counts=A[3],
                   dloss=A[4], score=0, coeff=0.01, stream=None)
-DISTILL = dict(logits=A[0], ld=30000, dtype=0, ids=A[1], ids_ld=8, teacher=A[2], teacher_ld=8, teacher_dtype=1, T=10,
-               V=30000, K=8, tau=1.0, loss=A[3], lse=A[4], ws=A[5], ws_bytes=BIG, stream=None)
+DISTILL = dict(logits=A[0], ld=300000, dtype=0, ids=A[1], ids_ld=8, teacher=A[2], teacher_ld=8, teacher_dtype=1, T=10,
+               V=300000, K=8, tau=1.0, loss=A[3], lse=A[4], ws=A[5], ws_bytes=BIG, stream=None)
 DISTILL_BWD = dict(dlogits=A[0], ld_d=30000, logits=A[1], ld=30000, dtype=0, ids=A[2], ids_ld=8, teacher=A[3],
                    teacher_ld=8, teacher_dtype=1, T=10, V=30000, K=8, tau=1.0, lse=A[4], dloss=A[5], stream=None)
 NORM = dict(x=A[0], x_ld=64, f=A[1], f_ld=64, gate=A[2], gate_ld=64, gate_cols=64, w_post=A[3], alpha=A[4], w_pre=A[5],
@@ -57,7 +57,7 @@ CASES = [
     ("det_router_balance_bwd", ROUTER_BWD, OVERLAP, [dict(dlogits=A[1]), dict(counts=FAR), dict(dloss=FAR)]),
     ("det_topk_distill", DISTILL, INVALID, [dict(T=-1), dict(V=0), dict(K=-1), dict(dtype=2), dict(teacher_dtype=2),
                                             dict(tau=0.0), dict(tau=-1.0), dict(tau=float("nan")),
-                                            dict(tau=float("inf")), dict(tau=1e-9), dict(ld=29999), dict(ids_ld=7),
+                                            dict(tau=float("inf")), dict(tau=1e-9), dict(ld=299999), dict(ids_ld=7),
                                             dict(teacher_ld=7), dict(logits=None), dict(ids=None), dict(teacher=None),
                                             dict(loss=None), dict(lse=None)]),
     ("det_topk_distill", DISTILL, UNSUPPORTED, [dict(K=1025, ids_ld=1025, teacher_ld=1025), dict(V=1 << 31, ld=1 << 31),
@@ -117,7 +117,8 @@ def test_workspace_sizes():
     assert dg.det_router_balance_workspace_size(100000, 64, 4, 2) > 256 + 2 * 64 * 8
     assert dg.det_topk_distill_workspace_size(0, 1000, 4) == 0
     assert dg.det_topk_distill_workspace_size(2000, 131072, 4) == 0     # a workgroup per row
-    assert dg.det_topk_distill_workspace_size(3, 131072, 4) >= 256 + 3 * 8 * 2
+    assert dg.det_topk_distill_workspace_size(3, 131072, 4) == 0
+    assert dg.det_topk_distill_workspace_size(3, 300000, 4) >= 256 + 3 * 8 * 2
     assert dg.det_block_norm_bwd_workspace_size(0, 64) == 0
     assert dg.det_block_norm_bwd_workspace_size(1, 64) >= 256 + 2 * 64 * 4
     n = ctypes.c_size_t()
