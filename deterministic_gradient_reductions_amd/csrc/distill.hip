@@ -23,7 +23,9 @@ namespace detgrad {
 namespace {
 
 constexpr int kMaxK = 1024;
-constexpr int kUnroll = 4;  // 16-byte loads of a lane in flight together
+// 16-byte loads of a lane in flight together: in the main loop, and in the loop
+// that takes most of what is left.
+constexpr int kUnroll = 8, kUnrollRest = 2;
 
 // Everything below is in units of log2: x2 = x log2(e) = c z with
 // c = log2(e) / tau, formed by one fused step against the reference, so only
@@ -31,6 +33,11 @@ constexpr int kUnroll = 4;  // 16-byte loads of a lane in flight together
 // and s = sum of 2^(c z - m).
 struct MaxSum {
   float m, s;
+};
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
 };
 
 __device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -137,7 +144,7 @@ __global__ __launch_bounds__(THREADS) void distill_fwd_kernel(const T* __restric
                                                               float it, int n_split, int64_t piece,
                                                               MaxSum* __restrict__ slots, float* __restrict__ loss,
                                                               float* __restrict__ lse) {
-  constexpr int U = kUnroll, kWaves = THREADS / 64, kStep = THREADS * 8;
+  constexpr int kWaves = THREADS / 64, kStep = THREADS * 8;
   __shared__ MaxSum part[kWaves];
   __shared__ Slots S;
   const int64_t row = blockIdx.x / n_split, c0 = (blockIdx.x % n_split) * piece;
@@ -147,15 +154,20 @@ __global__ __launch_bounds__(THREADS) void distill_fwd_kernel(const T* __restric
   if (n_split == 1) fetch_slots<T, TT, THREADS>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, it, p, 0, V);
   MaxSum a{-__builtin_inff(), 0.0f};
   int64_t i = c0;
-  for (; i + U * kStep <= c1; i += U * kStep) {
-    Raw8<T> raw[U];
-    float v[U][8];
+  const auto stream = [&](auto unroll) {
+    constexpr int U = decltype(unroll)::value;
+    for (; i + U * kStep <= c1; i += U * kStep) {
+      Raw8<T> raw[U];
+      float v[U][8];
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u].load(p + i + u * kStep + threadIdx.x * 8);
+      for (int u = 0; u < U; ++u) raw[u].load(p + i + u * kStep + threadIdx.x * 8);
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u].get(v[u]);
-    push<U>(a, v, c);
-  }
+      for (int u = 0; u < U; ++u) raw[u].get(v[u]);
+      push<U>(a, v, c);
+    }
+  };
+  stream(Int<kUnroll>{});
+  stream(Int<kUnrollRest>{});
   for (; i < c1; i += kStep) {
     float v[1][8];
     const int64_t k = i + threadIdx.x * 8;
@@ -197,7 +209,7 @@ __global__ __launch_bounds__(256) void distill_join_kernel(const T* __restrict__
 }
 
 constexpr int kBwdThreads = 256;
-template <typename T, typename TT>
+template <typename T, typename TT, bool PAST>
 __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict__ dz, int64_t ld_d,
                                                                   const T* __restrict__ z, int64_t ld, int64_t V,
                                                                   const int32_t* __restrict__ ids, int64_t ids_ld,
@@ -205,7 +217,7 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
                                                                   float it, int n_split, int64_t piece,
                                                                   const float* __restrict__ lse,
                                                                   const float* __restrict__ dloss) {
-  constexpr int U = kUnroll, kStep = kBwdThreads * 8;
+  constexpr int kStep = kBwdThreads * 8;
   __shared__ Slots S;
   const uint32_t b = gridDim.x - 1 - blockIdx.x;
   const int64_t row = b / n_split, c0 = (b % n_split) * piece;
@@ -228,19 +240,24 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
     return a * h * h;
   };
   int64_t i = c0;
-  for (; i + U * kStep <= c1; i += U * kStep) {
-    Raw8<T> raw[U];
+  const auto stream = [&](auto unroll) {
+    constexpr int U = decltype(unroll)::value;
+    for (; i + U * kStep <= c1; i += U * kStep) {
+      Raw8<T> raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u].load(p + i + u * kStep + threadIdx.x * 8);
+      for (int u = 0; u < U; ++u) raw[u].load(p + i + u * kStep + threadIdx.x * 8);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float v[8];
-      raw[u].get(v);
+      for (int u = 0; u < U; ++u) {
+        float v[8];
+        raw[u].get(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = grad(v[j]);
-      store8_full(o + i + u * kStep + threadIdx.x * 8, v);
+        for (int j = 0; j < 8; ++j) v[j] = grad(v[j]);
+        store8_full<PAST>(o + i + u * kStep + threadIdx.x * 8, v);
+      }
     }
-  }
+  };
+  stream(Int<kUnroll>{});
+  stream(Int<kUnrollRest>{});
   for (; i < c1; i += kStep) {
     float v[8];
     const int64_t k = i + threadIdx.x * 8;
@@ -335,9 +352,15 @@ void launch_bwd(void* dz, int64_t ld_d, const void* z, int64_t ld, int64_t V, co
                 const void* t, int64_t t_ld, int64_t rows, int64_t K, float it, const float* lse, const float* dloss,
                 hipStream_t st) {
   const Split s = bwd_split(rows, V);
-  hipLaunchKernelGGL((distill_bwd_kernel<T, TT>), dim3(static_cast<uint32_t>(rows * s.n)), dim3(kBwdThreads), 0, st,
-                     static_cast<T*>(dz), ld_d, static_cast<const T*>(z), ld, V, ids, ids_ld,
-                     static_cast<const TT*>(t), t_ld, (int)K, it, s.n, s.piece, lse, dloss);
+  const dim3 grid(static_cast<uint32_t>(rows * s.n));
+  if (2 * rows * V * static_cast<int64_t>(sizeof(T)) > kCacheBytes)
+    hipLaunchKernelGGL((distill_bwd_kernel<T, TT, true>), grid, dim3(kBwdThreads), 0, st, static_cast<T*>(dz), ld_d,
+                       static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n,
+                       s.piece, lse, dloss);
+  else
+    hipLaunchKernelGGL((distill_bwd_kernel<T, TT, false>), grid, dim3(kBwdThreads), 0, st, static_cast<T*>(dz), ld_d,
+                       static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n,
+                       s.piece, lse, dloss);
 }
 
 }  // namespace

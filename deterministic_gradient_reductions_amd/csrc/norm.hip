@@ -76,7 +76,7 @@ __device__ __forceinline__ void load_param(const float* p, const Cols<TINY>& c, 
   }
 }
 
-template <typename T, int THREADS, int NV>
+template <typename T, int THREADS, int NV, bool PAST>
 __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(const T* __restrict__ x, int64_t ld_x,
                                                            const T* __restrict__ f, int64_t ld_f,
                                                            const T* __restrict__ gate, int64_t ld_g, int gate_kind,
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(const T* __restrict__
         xv[i][j] += fv[i][j] * rp * wp[i][j] * s;
         q += xv[i][j] * xv[i][j];
       }
-      store_cols(y + r * ld_y, c[i], xv[i]);
+      store_cols<PAST>(y + r * ld_y, c[i], xv[i]);
     }
     if (pre) {
       const float rq = 1.0f / sqrtf(block_sum<THREADS>(q, buf[1]) * P.inv_d + P.eps);
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(const T* __restrict__
       for (int i = 0; i < NV; ++i) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) xv[i][j] = xv[i][j] * rq * wq[i][j];
-        store_cols(h + r * ld_h, c[i], xv[i]);
+        store_cols<PAST>(h + r * ld_h, c[i], xv[i]);
       }
     }
     // with one sum per row the same buffer serves every row
@@ -192,7 +192,7 @@ __device__ __forceinline__ void load_row(BwdRow<T, NV>& R, const BwdIn<T>& I, bo
 // registers to the running sums, two rows and four waves per SIMD. For D > 8192
 // a thread has 16 channels: their running sums take the LDS instead, and the
 // parameters are read again for every row.
-template <typename T, int THREADS, int NV>
+template <typename T, int THREADS, int NV, bool PAST>
 __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormParams P, T* __restrict__ dx,
                                                               int64_t ld_dx, T* __restrict__ df, int64_t ld_df,
                                                               T* __restrict__ dgate, int64_t ld_dg,
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormPa
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      store_cols(dx + r * ld_dx, c[i], d[i]);
+      store_cols<PAST>(dx + r * ld_dx, c[i], d[i]);
       float wp[8], al[8];
       param(0, i, wp);
       param(1, i, al);
@@ -325,7 +325,7 @@ __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormPa
         float dg[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) dg[j] = u[i][j] * fh[i][j] * (1.0f - s[i][j]);
-        store_cols(dgate + r * ld_dg, c[i], dg);
+        store_cols<PAST>(dgate + r * ld_dg, c[i], dg);
       }
     }
     if (second) {
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormPa
       }
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) store_cols(df + r * ld_df, c[i], u[i]);
+    for (int i = 0; i < NV; ++i) store_cols<PAST>(df + r * ld_df, c[i], u[i]);
     if (THREADS > 64 && second != pre) __syncthreads();
   }
   if (!slots) return;
@@ -404,11 +404,20 @@ int threads_for(int64_t D) {
   return t;
 }
 
-// Workgroups of a launch: every compute unit's 2048 threads, twice over for the
-// forward (no per-workgroup cost beyond the parameters), once for the backward,
-// whose every workgroup writes a slot of 8 bytes per channel.
+// Workgroups of a launch, from the shape alone. Enough to fill the compute units
+// (forward: their 2048 threads twice over; backward: the 1024 threads its
+// registers allow), but where the tokens are few, few enough that a workgroup
+// walks three rows (forward: its parameters are loaded once) or six (backward:
+// every workgroup also writes a slot of 8 bytes per channel, which the fold
+// reads). Measured at 3001 x 1407 float32: 16 + 21 + 5.5 us against 17 + 21.5 +
+// 7.5 with all workgroups; at 8192 x 4096 bf16 the forward takes 53 us with
+// 2048 workgroups and 57 with 512.
 int64_t groups_for(int64_t T, int64_t D, bool bwd) {
-  const int64_t g = 256 * (2048 / threads_for(D)) * (bwd ? 1 : 2) / (bwd && D > 512 ? 2 : 1);
+  const int64_t full = bwd ? 256 * (1024 / threads_for(D)) : 512 * (2048 / threads_for(D));
+  const int64_t few = bwd ? 512 : 1024, rows = bwd ? 6 : 3;
+  int64_t g = ceil_div(T, rows);
+  if (g < few) g = few;
+  if (g > full) g = full;
   return T < g ? T : g;
 }
 size_t ws_bytes_for(int64_t T, int64_t D) {
@@ -434,14 +443,20 @@ int check_ld(const char* what, const char* name, const void* p, int64_t ld, int6
 
 using namespace detgrad;
 
-#define DET_NORM_LAUNCH(KERNEL, T, ...)                                                                            \
-  switch (D > 8192 ? 2048 : threads_for(D)) {                                                                      \
-    case 64: hipLaunchKernelGGL((KERNEL<T, 64, 1>), grid, dim3(64), 0, st, __VA_ARGS__); break;                    \
-    case 128: hipLaunchKernelGGL((KERNEL<T, 128, 1>), grid, dim3(128), 0, st, __VA_ARGS__); break;                 \
-    case 256: hipLaunchKernelGGL((KERNEL<T, 256, 1>), grid, dim3(256), 0, st, __VA_ARGS__); break;                 \
-    case 512: hipLaunchKernelGGL((KERNEL<T, 512, 1>), grid, dim3(512), 0, st, __VA_ARGS__); break;                 \
-    case 1024: hipLaunchKernelGGL((KERNEL<T, 1024, 1>), grid, dim3(1024), 0, st, __VA_ARGS__); break;              \
-    default: hipLaunchKernelGGL((KERNEL<T, 1024, 2>), grid, dim3(1024), 0, st, __VA_ARGS__); break;                \
+#define DET_NORM_CASE(KERNEL, T, THREADS, NV, ...)                                                          \
+  if (past)                                                                                                 \
+    hipLaunchKernelGGL((KERNEL<T, THREADS, NV, true>), grid, dim3(THREADS), 0, st, __VA_ARGS__);            \
+  else                                                                                                      \
+    hipLaunchKernelGGL((KERNEL<T, THREADS, NV, false>), grid, dim3(THREADS), 0, st, __VA_ARGS__);           \
+  break;
+#define DET_NORM_LAUNCH(KERNEL, T, ...)                     \
+  switch (D > 8192 ? 2048 : threads_for(D)) {               \
+    case 64: DET_NORM_CASE(KERNEL, T, 64, 1, __VA_ARGS__)   \
+    case 128: DET_NORM_CASE(KERNEL, T, 128, 1, __VA_ARGS__) \
+    case 256: DET_NORM_CASE(KERNEL, T, 256, 1, __VA_ARGS__) \
+    case 512: DET_NORM_CASE(KERNEL, T, 512, 1, __VA_ARGS__) \
+    case 1024: DET_NORM_CASE(KERNEL, T, 1024, 1, __VA_ARGS__) \
+    default: DET_NORM_CASE(KERNEL, T, 1024, 2, __VA_ARGS__) \
   }
 
 extern "C" int det_block_norm(const void* x, int64_t x_ld, const void* f, int64_t f_ld, const void* gate,
@@ -479,6 +494,7 @@ extern "C" int det_block_norm(const void* x, int64_t x_ld, const void* f, int64_
   const NormParams P{w_post, alpha, w_pre, static_cast<float>(eps), static_cast<float>(1.0 / D), T, D};
   const int kind = !gate ? kGateNone : (gate_cols == D ? kGateFull : kGateRow);
   const dim3 grid(static_cast<uint32_t>(groups_for(T, D, false)));
+  const bool past = T * D * static_cast<int64_t>(dtype_size(dtype)) * (3 + (kind == kGateFull) + (h != nullptr)) > kCacheBytes;
   const hipStream_t st = as_stream(stream);
 #define DET_NORM_FWD(E)                                                                                             \
   DET_NORM_LAUNCH(norm_fwd_kernel, E, static_cast<const E*>(x), x_ld, static_cast<const E*>(f), f_ld,               \
@@ -553,6 +569,7 @@ extern "C" int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh,
   const int kind = !gate ? kGateNone : (gate_cols == D ? kGateFull : kGateRow);
   const int64_t groups = groups_for(T, D, true);
   const dim3 grid(static_cast<uint32_t>(groups));
+  const bool past = T * D * static_cast<int64_t>(dtype_size(dtype)) * (4 + 2 * (kind == kGateFull) + 2 * pre) > kCacheBytes;
   const hipStream_t st = as_stream(stream);
   auto* slots = need ? reinterpret_cast<float*>(static_cast<char*>(ws) + DET_WS_HEADER_BYTES) : nullptr;
 #define DET_NORM_BWD(E)                                                                                              \

@@ -88,35 +88,50 @@ __device__ __forceinline__ void load8(const T* p, int64_t n, float fill, float (
   }
 }
 
+// In a block under a condition that is the same for all lanes and seldom true:
+// keeps the compiler from computing the block always and selecting.
+__device__ __forceinline__ void keep_branch() { asm volatile(""); }
+
+// Stores of eight elements. PAST: past the caches, for calls whose tensors
+// together are larger than they are: the reader of such an output would not find
+// it there anyway, and dirty lines would be written back among other reads.
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+template <bool PAST>
 __device__ __forceinline__ void store8_full(float* p, const float (&v)[8]) {
   const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-  __builtin_memcpy(p, &a, 16);
-  __builtin_memcpy(p + 4, &b, 16);
+  if constexpr (PAST) {
+    __builtin_nontemporal_store(a, reinterpret_cast<f32x4_a4*>(p));
+    __builtin_nontemporal_store(b, reinterpret_cast<f32x4_a4*>(p + 4));
+  } else {
+    __builtin_memcpy(p, &a, 16);
+    __builtin_memcpy(p + 4, &b, 16);
+  }
 }
+template <bool PAST>
 __device__ __forceinline__ void store8_full(uint16_t* p, const float (&v)[8]) {
   u32x4 w;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     w[i] = static_cast<uint32_t>(from_f32<uint16_t>(v[2 * i])) |
            (static_cast<uint32_t>(from_f32<uint16_t>(v[2 * i + 1])) << 16);
-  __builtin_memcpy(p, &w, 16);
+  if constexpr (PAST)
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_a2*>(p));
+  else
+    __builtin_memcpy(p, &w, 16);
 }
 
 // p[0..min(n, 8)) = v, rounded once to the element type.
 template <typename T>
 __device__ __forceinline__ void store8(T* p, int64_t n, const float (&v)[8]) {
   if (n >= 8) {
-    store8_full(p, v);
+    store8_full<false>(p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < n) p[i] = from_f32<T>(v[i]);
   }
 }
-
-// In a block under a condition that is the same for all lanes and seldom true:
-// keeps the compiler from computing the block always and selecting.
-__device__ __forceinline__ void keep_branch() { asm volatile(""); }
 
 // A lane's eight columns of rows of N elements, chosen so that the lane's load is
 // one unconditional access inside the row (loads under a branch would be waited
@@ -155,10 +170,10 @@ __device__ __forceinline__ void get_cols(const Raw8<T>& r, const Cols<TINY>& c, 
     for (int j = 0; j < 8; ++j) v[j] = c.own(j) ? v[j] : fill;
   }
 }
-template <typename T, bool TINY>
+template <bool PAST = false, typename T, bool TINY>
 __device__ __forceinline__ void store_cols(T* row, const Cols<TINY>& c, const float (&v)[8]) {
   if (c.all || (c.lo == 0 && (!TINY || c.hi == 8))) {
-    store8_full(row + c.base, v);
+    store8_full<PAST>(row + c.base, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -230,6 +245,10 @@ __device__ __forceinline__ float lanes_max(float v) {
 }
 
 // ------------------------------------------------------------------ host side
+// Size of the last-level cache: calls whose large tensors together exceed it
+// store their outputs past the caches.
+constexpr int64_t kCacheBytes = int64_t(256) << 20;
+
 // One buffer of a call, for the overlap check.
 struct Buf {
   const char* name;
