@@ -239,7 +239,11 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
     const float h = pow2(__builtin_fmaf(v, it, -l) * (0.5f * kLog2e));
     return a * h * h;
   };
-  int64_t i = c0;
+  // up to the first 128-byte line of dz one element per thread, so that a wave's stores fill whole lines (rows of
+  // an odd V start anywhere)
+  const int64_t lead = (-reinterpret_cast<uintptr_t>(o + c0) & 127) / sizeof(T), head = lead < c1 - c0 ? lead : c1 - c0;
+  int64_t i = c0 + head;
+  if (threadIdx.x < head) o[c0 + threadIdx.x] = from_f32<T>(grad(to_f32(p[c0 + threadIdx.x])));
   const auto stream = [&](auto unroll) {
     constexpr int U = decltype(unroll)::value;
     for (; i + U * kStep <= c1; i += U * kStep) {
@@ -353,7 +357,7 @@ void launch_bwd(void* dz, int64_t ld_d, const void* z, int64_t ld, int64_t V, co
                 hipStream_t st) {
   const Split s = bwd_split(rows, V);
   const dim3 grid(static_cast<uint32_t>(rows * s.n));
-  if (2 * rows * V * static_cast<int64_t>(sizeof(T)) > kCacheBytes)
+  if (past_caches(rows * V * static_cast<int64_t>(sizeof(T))))
     hipLaunchKernelGGL((distill_bwd_kernel<T, TT, true>), grid, dim3(kBwdThreads), 0, st, static_cast<T*>(dz), ld_d,
                        static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n,
                        s.piece, lse, dloss);

@@ -494,7 +494,7 @@ extern "C" int det_block_norm(const void* x, int64_t x_ld, const void* f, int64_
   const NormParams P{w_post, alpha, w_pre, static_cast<float>(eps), static_cast<float>(1.0 / D), T, D};
   const int kind = !gate ? kGateNone : (gate_cols == D ? kGateFull : kGateRow);
   const dim3 grid(static_cast<uint32_t>(groups_for(T, D, false)));
-  const bool past = T * D * static_cast<int64_t>(dtype_size(dtype)) * (3 + (kind == kGateFull) + (h != nullptr)) > kCacheBytes;
+  const bool past = past_caches(T * D * static_cast<int64_t>(dtype_size(dtype)) * (h ? 2 : 1));
   const hipStream_t st = as_stream(stream);
 #define DET_NORM_FWD(E)                                                                                             \
   DET_NORM_LAUNCH(norm_fwd_kernel, E, static_cast<const E*>(x), x_ld, static_cast<const E*>(f), f_ld,               \
@@ -569,7 +569,7 @@ extern "C" int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh,
   const int kind = !gate ? kGateNone : (gate_cols == D ? kGateFull : kGateRow);
   const int64_t groups = groups_for(T, D, true);
   const dim3 grid(static_cast<uint32_t>(groups));
-  const bool past = T * D * static_cast<int64_t>(dtype_size(dtype)) * (4 + 2 * (kind == kGateFull) + 2 * pre) > kCacheBytes;
+  const bool past = past_caches(T * D * static_cast<int64_t>(dtype_size(dtype)) * (kind == kGateFull ? 3 : 2));
   const hipStream_t st = as_stream(stream);
   auto* slots = need ? reinterpret_cast<float*>(static_cast<char*>(ws) + DET_WS_HEADER_BYTES) : nullptr;
 #define DET_NORM_BWD(E)                                                                                              \

@@ -92,9 +92,9 @@ __device__ __forceinline__ void load8(const T* p, int64_t n, float fill, float (
 // keeps the compiler from computing the block always and selecting.
 __device__ __forceinline__ void keep_branch() { asm volatile(""); }
 
-// Stores of eight elements. PAST: past the caches, for calls whose tensors
-// together are larger than they are: the reader of such an output would not find
-// it there anyway, and dirty lines would be written back among other reads.
+// Stores of eight elements. PAST: past the caches, for outputs larger than they
+// are: their reader would not find them there anyway, and their dirty lines
+// would be written back among other reads.
 typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 template <bool PAST>
@@ -245,9 +245,14 @@ __device__ __forceinline__ float lanes_max(float v) {
 }
 
 // ------------------------------------------------------------------ host side
-// Size of the last-level cache: calls whose large tensors together exceed it
-// store their outputs past the caches.
+// Size of the last-level cache: calls whose outputs together reach it store them
+// past the caches. Measured with the distillation's backward: 4096 x 32768 bf16
+// (256 MiB of dz) 92 us against 119 with ordinary stores, in a step that then
+// reads other logits. Smaller outputs are 5 % faster to store that way as well,
+// but the kernel that reads them next loses more: at 128 MiB of dz 3 us gained, 37
+// lost by a reduction over dz that took 295.
 constexpr int64_t kCacheBytes = int64_t(256) << 20;
+inline bool past_caches(int64_t out_bytes) { return out_bytes >= kCacheBytes; }
 
 // One buffer of a call, for the overlap check.
 struct Buf {
