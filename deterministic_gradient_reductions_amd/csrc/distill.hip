@@ -208,23 +208,22 @@ __global__ __launch_bounds__(256) void distill_join_kernel(const T* __restrict__
   if (threadIdx.x < 64) finish_row(a, S, K, loss + row, lse + row);
 }
 
-constexpr int kBwdThreads = 256;
-template <typename T, typename TT, bool PAST>
-__global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict__ dz, int64_t ld_d,
+template <typename T, typename TT, int THREADS, bool PAST>
+__global__ __launch_bounds__(THREADS) void distill_bwd_kernel(T* __restrict__ dz, int64_t ld_d,
                                                                   const T* __restrict__ z, int64_t ld, int64_t V,
                                                                   const int32_t* __restrict__ ids, int64_t ids_ld,
                                                                   const TT* __restrict__ teacher, int64_t t_ld, int K,
                                                                   float it, int n_split, int64_t piece,
                                                                   const float* __restrict__ lse,
                                                                   const float* __restrict__ dloss) {
-  constexpr int kStep = kBwdThreads * 8;
+  constexpr int kStep = THREADS * 8;
   __shared__ Slots S;
   const uint32_t b = gridDim.x - 1 - blockIdx.x;
   const int64_t row = b / n_split, c0 = (b % n_split) * piece;
   const int64_t c1 = c0 + piece < V ? c0 + piece : V;
   const T* p = z + row * ld;
   T* o = dz + row * ld_d;
-  fetch_slots<T, TT, kBwdThreads>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, it, p, c0, c1);
+  fetch_slots<T, TT, THREADS>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, it, p, c0, c1);
   const float a = dloss[row] * it, l = lse[row];
   __syncthreads();
   const Teacher q = teacher_row(S, K);  // the same in every wave
@@ -271,9 +270,9 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
     store8(o + k, c1 - k, v);
   }
   // every slot's q in place of its t (each thread its own), the piece's stores before the rewrites
-  for (int k = threadIdx.x; k < K; k += kBwdThreads) S.t[k] = exp_e(S.t[k] - q.m) / q.sum;
+  for (int k = threadIdx.x; k < K; k += THREADS) S.t[k] = exp_e(S.t[k] - q.m) / q.sum;
   __syncthreads();
-  for (int k = threadIdx.x; k < K; k += kBwdThreads) {
+  for (int k = threadIdx.x; k < K; k += THREADS) {
     const int32_t v = S.id[k];
     if (v < c0 || v >= c1) continue;
     bool first = true;
@@ -287,28 +286,36 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
 }
 
 // Workgroups and pieces per row, from the shape alone.
-// Forward: a workgroup of 256 threads per row when the rows alone fill the
-// compute units, of 1024 below that; a second workgroup for a row costs a
-// second launch and pays only past 2^18 elements.
-// Backward: pieces of four steps of the workgroup or more, about 2048 of them
-// when there are few rows (no second launch is needed).
+//
+// Threads of a workgroup that streams `len` elements: as many as still make two
+// turns of the main loop. Backward at 8192 x 131072 bf16 (a step with its
+// forward): 1182 us with 256 threads, 1154 with 512, 1122 with 1024; at 4096 x
+// 32768: 143, 144, 151; at 1021 pieces of 18432: 58, 75, 76.
+int stream_threads(int64_t len) {
+  const int64_t turn = 8 * kUnroll;
+  return len >= 2 * 1024 * turn ? 1024 : (len >= 2 * 512 * turn ? 512 : 256);
+}
 struct Split {
-  int n;
+  int n, threads;
   int64_t piece;
 };
-Split split_into(int64_t V, int64_t n, int64_t step) {
+Split split_into(int64_t V, int64_t n, int64_t step, int threads) {
   const int64_t piece = align_up(ceil_div(V, n < 1 ? 1 : n), step);
-  return {static_cast<int>(ceil_div(V, piece)), piece};
+  return {static_cast<int>(ceil_div(V, piece)), threads ? threads : stream_threads(piece < V ? piece : V), piece};
 }
-int fwd_threads(int64_t T) { return T >= 512 ? 256 : 1024; }
+// Forward: a workgroup per row, of 1024 threads when the rows alone leave
+// compute units idle; a second workgroup for a row costs a second launch and pays
+// only past 2^18 elements (three rows of 131072 float32: 8 us in one launch; 3.8
+// and 3.2 us, and 4 us more of the host's time, in two).
 Split fwd_split(int64_t T, int64_t V) {
   const int64_t most = ceil_div(V, int64_t(1) << 18), want = T >= 256 || T == 0 ? 1 : ceil_div(512, T);
-  return split_into(V, want < most ? want : most, fwd_threads(T) * 8);
+  return split_into(V, want < most ? want : most, 8192, T >= 512 ? 0 : 1024);
 }
+// Backward: pieces of 8192 elements or more, about 2048 of them when there are
+// few rows (no second launch is needed).
 Split bwd_split(int64_t T, int64_t V) {
-  const int64_t step = kBwdThreads * 8, most = ceil_div(V, 4 * step);
-  const int64_t want = T >= 1024 || T == 0 ? 1 : ceil_div(2048, T);
-  return split_into(V, want < most ? want : most, step);
+  const int64_t most = ceil_div(V, 8192), want = T >= 1024 || T == 0 ? 1 : ceil_div(2048, T);
+  return split_into(V, want < most ? want : most, 2048, 0);
 }
 
 int check_args(const char* what, int dtype, int t_dtype, int64_t T, int64_t V, int64_t K, double tau) {
@@ -340,12 +347,13 @@ void launch_fwd(const void* z, int64_t ld, int64_t V, const int32_t* ids, int64_
                 int64_t rows, int64_t K, float it, float* loss, float* lse, MaxSum* slots, hipStream_t st) {
   const Split s = fwd_split(rows, V);
   const dim3 grid(static_cast<uint32_t>(rows * s.n));
-  if (fwd_threads(rows) == 256)
-    hipLaunchKernelGGL((distill_fwd_kernel<T, TT, 256>), grid, dim3(256), 0, st, static_cast<const T*>(z), ld, V, ids,
-                       ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n, s.piece, slots, loss, lse);
-  else
-    hipLaunchKernelGGL((distill_fwd_kernel<T, TT, 1024>), grid, dim3(1024), 0, st, static_cast<const T*>(z), ld, V, ids,
-                       ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n, s.piece, slots, loss, lse);
+#define DET_DISTILL_FWD(THREADS)                                                                                      \
+  hipLaunchKernelGGL((distill_fwd_kernel<T, TT, THREADS>), grid, dim3(THREADS), 0, st, static_cast<const T*>(z), ld, V, \
+                     ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n, s.piece, slots, loss, lse)
+  if (s.threads == 256) DET_DISTILL_FWD(256);
+  else if (s.threads == 512) DET_DISTILL_FWD(512);
+  else DET_DISTILL_FWD(1024);
+#undef DET_DISTILL_FWD
   if (s.n > 1)
     hipLaunchKernelGGL((distill_join_kernel<T, TT>), dim3(static_cast<uint32_t>(rows)), dim3(256), 0, st,
                        static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n,
@@ -357,14 +365,22 @@ void launch_bwd(void* dz, int64_t ld_d, const void* z, int64_t ld, int64_t V, co
                 hipStream_t st) {
   const Split s = bwd_split(rows, V);
   const dim3 grid(static_cast<uint32_t>(rows * s.n));
-  if (past_caches(rows * V * static_cast<int64_t>(sizeof(T))))
-    hipLaunchKernelGGL((distill_bwd_kernel<T, TT, true>), grid, dim3(kBwdThreads), 0, st, static_cast<T*>(dz), ld_d,
-                       static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n,
-                       s.piece, lse, dloss);
-  else
-    hipLaunchKernelGGL((distill_bwd_kernel<T, TT, false>), grid, dim3(kBwdThreads), 0, st, static_cast<T*>(dz), ld_d,
-                       static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n,
-                       s.piece, lse, dloss);
+  const bool past = past_caches(rows * V * static_cast<int64_t>(sizeof(T)));
+#define DET_DISTILL_BWD(THREADS, PAST)                                                                              \
+  hipLaunchKernelGGL((distill_bwd_kernel<T, TT, THREADS, PAST>), grid, dim3(THREADS), 0, st, static_cast<T*>(dz),   \
+                     ld_d, static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, \
+                     s.n, s.piece, lse, dloss)
+  if (s.threads == 256) {
+    if (past) DET_DISTILL_BWD(256, true);
+    else DET_DISTILL_BWD(256, false);
+  } else if (s.threads == 512) {
+    if (past) DET_DISTILL_BWD(512, true);
+    else DET_DISTILL_BWD(512, false);
+  } else {
+    if (past) DET_DISTILL_BWD(1024, true);
+    else DET_DISTILL_BWD(1024, false);
+  }
+#undef DET_DISTILL_BWD
 }
 
 }  // namespace

@@ -67,7 +67,7 @@ def check(T, V, K, dtype, t_dtype=F32, tau=1.0, seed=0, ld=None, shift=0, data=N
 
 @pytest.mark.parametrize("dtype,t_dtype", [(BF, F32), (F32, BF)])
 @pytest.mark.parametrize("T,V,K", [(1, 1, 1), (3, 2, 1), (4, 7, 3), (5, 8, 16), (9, 255, 8), (6, 2047, 64),
-                                   (7, 2048, 65), (3, 8192, 5), (4, 8193, 130), (5, 16385, 1024), (2, 50001, 33), (2, 262145, 40), (3, 600001, 7), (600, 3001, 9), (513, 1000, 300),
+                                   (7, 2048, 65), (3, 8192, 5), (4, 8193, 130), (5, 16385, 1024), (2, 50001, 33), (2, 262145, 40), (3, 600001, 7), (600, 3001, 9), (513, 1000, 300), (520, 66001, 5), (516, 131101, 3),
                                    (1, 131072, 1), (1030, 300, 4)])
 def test_sizes(T, V, K, dtype, t_dtype):
     check(T, V, K, dtype, t_dtype, tau=1.0 if T % 2 else 2.5, seed=T * 7 + V)

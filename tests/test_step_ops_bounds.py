@@ -93,24 +93,25 @@ def test_router_tiles_cover_every_token_once(T, E, offs):
         assert np.array_equal(seen, inside)
 
 
-def split_into(V, n, step):
+def split_into(V, n, step, threads):
     piece = cdiv(cdiv(V, max(n, 1)), step) * step
-    return cdiv(V, piece), piece
+    length = min(piece, V)
+    t = threads or (1024 if length >= 131072 else 512 if length >= 65536 else 256)
+    return t, cdiv(V, piece), piece
 
 
 def fwd_split(T, V):
-    threads = 256 if T >= 512 else 1024
     want = 1 if T >= 256 or T == 0 else cdiv(512, T)
-    return threads, *split_into(V, min(want, cdiv(V, 1 << 18)), threads * 8)
+    return split_into(V, min(want, cdiv(V, 1 << 18)), 8192, 0 if T >= 512 else 1024)
 
 
 def bwd_split(T, V):
     want = 1 if T >= 1024 or T == 0 else cdiv(2048, T)
-    return 256, *split_into(V, min(want, cdiv(V, 4 * 2048)), 2048)
+    return split_into(V, min(want, cdiv(V, 8192)), 2048, 0)
 
 
 @pytest.mark.parametrize("T,V", [(1, 1), (3, 131072), (3, 600001), (1021, 50001), (2000, 2049), (7, 8193), (1, 262145),
-                                 (300, 16384), (600, 7)])
+                                 (300, 16384), (600, 7), (5000, 70001), (5000, 140001)])
 @pytest.mark.parametrize("phase", [0, 2, 14, 126])
 def test_distill_pieces_cover_every_word_once(T, V, phase):
     """The pieces of a row, the lead to a 128-byte line (backward, bf16 at byte `phase` of a line), the loops of eight,
