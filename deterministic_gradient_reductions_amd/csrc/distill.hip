@@ -328,7 +328,10 @@ int check_args(const char* what, int dtype, int t_dtype, int64_t T, int64_t V, i
     return set_error(DET_ERR_UNSUPPORTED, "%s: T and V must be < 2^31 - 65536", what);
   if (!(tau >= 1e-6 && tau <= 1e6))
     return set_error(DET_ERR_INVALID_ARG, "%s: tau must lie in [1e-6, 1e6], got %g", what, tau);
-  if (T * (bwd_split(T, V).n + fwd_split(T, V).n) > 0x7FFFFFFF) return set_error(DET_ERR_UNSUPPORTED, "%s: problem too large", what);
+  // a launch has at most 2^32 - 1 threads
+  if (T * fwd_split(T, V).n > 0xFFFFFFFF / 1024 && T * fwd_split(T, V).n * fwd_split(T, V).threads > 0xFFFFFFFF)
+    return set_error(DET_ERR_UNSUPPORTED, "%s: problem too large", what);
+  if (T * bwd_split(T, V).n > 0xFFFFFFFF / 1024 && T * bwd_split(T, V).n * bwd_split(T, V).threads > 0xFFFFFFFF) return set_error(DET_ERR_UNSUPPORTED, "%s: problem too large", what);
   return DET_OK;
 }
 int check_ld(const char* what, const char* name, int64_t ld, int64_t n, int64_t T) {
@@ -418,13 +421,14 @@ extern "C" int det_topk_distill(const void* logits, int64_t ld, int dtype, const
   if (int s = check_ld(what, "teacher", teacher_ld, K, T)) return s;
   const size_t need = ws_bytes_for(T, V);
   if (int s = check_workspace(ws, ws_bytes, need)) return s;
+  const size_t es = dtype_size(dtype), ts = dtype_size(teacher_dtype);
   const Buf outs[] = {{"loss", range1d(loss, T * 4)},
                       {"lse", range1d(lse, T * 4)},
                       {"the workspace", range1d(need ? ws : nullptr, ws_bytes)}};
-  const Buf ins[] = {{"logits", range2d(logits, T, V, ld, dtype_size(dtype))},
+  const Buf ins[] = {{"logits", range2d(logits, T, V, ld, es), es},
                      {"ids", range2d(ids, T, K, ids_ld, 4)},
-                     {"teacher", range2d(teacher, T, K, teacher_ld, dtype_size(teacher_dtype))}};
-  if (int s = check_overlaps(what, outs, 3, ins, 3)) return s;
+                     {"teacher", range2d(teacher, T, K, teacher_ld, ts), ts}};
+  if (int s = check_buffers(what, outs, 3, ins, 3)) return s;
   auto* slots = need ? reinterpret_cast<MaxSum*>(static_cast<char*>(ws) + DET_WS_HEADER_BYTES) : nullptr;
   const float it = static_cast<float>(1.0 / tau);
   DET_DISTILL_BY_TYPE(launch_fwd, logits, ld, V, ids, ids_ld, teacher, teacher_ld, T, K, it, loss, lse, slots,
@@ -445,13 +449,14 @@ extern "C" int det_topk_distill_bwd(void* dlogits, int64_t ld_d, const void* log
   if (int s = check_ld(what, "logits", ld, V, T)) return s;
   if (int s = check_ld(what, "ids", ids_ld, K, T)) return s;
   if (int s = check_ld(what, "teacher", teacher_ld, K, T)) return s;
-  const Buf outs[] = {{"dlogits", range2d(dlogits, T, V, ld_d, dtype_size(dtype))}};
-  const Buf ins[] = {{"logits", range2d(logits, T, V, ld, dtype_size(dtype))},
+  const size_t es = dtype_size(dtype), ts = dtype_size(teacher_dtype);
+  const Buf outs[] = {{"dlogits", range2d(dlogits, T, V, ld_d, es), es}};
+  const Buf ins[] = {{"logits", range2d(logits, T, V, ld, es), es},
                      {"ids", range2d(ids, T, K, ids_ld, 4)},
-                     {"teacher", range2d(teacher, T, K, teacher_ld, dtype_size(teacher_dtype))},
+                     {"teacher", range2d(teacher, T, K, teacher_ld, ts), ts},
                      {"lse", range1d(lse, T * 4)},
                      {"dloss", range1d(dloss, T * 4)}};
-  if (int s = check_overlaps(what, outs, 1, ins, 5)) return s;
+  if (int s = check_buffers(what, outs, 1, ins, 5)) return s;
   const float it = static_cast<float>(1.0 / tau);
   DET_DISTILL_BY_TYPE(launch_bwd, dlogits, ld_d, logits, ld, V, ids, ids_ld, teacher, teacher_ld, T, K, it, lse, dloss,
                       as_stream(stream))

@@ -29,6 +29,10 @@ namespace {
 
 constexpr int kFwdThreads = 512, kDirectThreads = 1024, kBwdThreads = 256, kFoldThreads = 1024;
 
+// Offsets of up to this many groups of 64 segments are fetched together where
+// the offsets are scanned.
+constexpr int kScanBatch = 8;
+
 // Rows of a lane group whose loads are in flight together (half as many where a
 // lane holds sixteen columns).
 constexpr int fwd_ahead(int ni) { return 2 / ni; }
@@ -198,8 +202,8 @@ __global__ __launch_bounds__(kFwdThreads) void router_tile_kernel(const T* __res
   __shared__ int32_t hist[8 * LPR * NI];
   if (blockIdx.x == 0 && threadIdx.x < 64) write_tile_table(offs, S, rows, log_bt, table);
   int seg;
-  uint32_t r0, r1;
-  if (!tile_of(offs, S, rows, log_bt, blockIdx.x, seg, r0, r1)) return;  // the grid covers the worst case
+  uint32_t r0, r1, s0, s1;
+  if (!segment_tile<kScanBatch>(offs, S, rows, log_bt, blockIdx.x, seg, r0, r1, s0, s1)) return;  // the grid covers the worst case
   sum_rows<T, LPR, NI, SIGMOID, kFwdThreads>(z, ld, E, ids, ids_ld, K, r0, r1, part, hist);
   for (int c = threadIdx.x; c < E; c += kFwdThreads) {
     slot_p[static_cast<int64_t>(blockIdx.x) * E + c] = part[0][c];
@@ -212,7 +216,17 @@ __device__ __forceinline__ void segment_bounds(const int32_t* __restrict__ offs,
                                                uint32_t& b1) {
   const uint32_t last = clamp_off(offs[s + 1], rows);
   uint32_t b = 0;
-  for (int i = threadIdx.x & 63; i <= s; i += 64) b = umax(b, clamp_off(offs[i], rows));
+  for (int i = 0; i <= s; i += 64 * kScanBatch) {
+    uint32_t v[kScanBatch] = {};
+#pragma unroll
+    for (int k = 0; k < kScanBatch; ++k) {
+      if (k > 0 && i + 64 * k > s) break;  // (the same for every lane)
+      const int at = i + 64 * k + static_cast<int>(threadIdx.x & 63);
+      v[k] = clamp_off(offs[at <= s ? at : s], rows);
+    }
+#pragma unroll
+    for (int k = 0; k < kScanBatch; ++k) b = umax(b, v[k]);
+  }
   b0 = lane_value(scan_max(b), 63);
   b1 = umax(b0, last);
 }
@@ -278,6 +292,7 @@ __global__ __launch_bounds__(kFoldThreads) void router_fold_kernel(const float* 
                                                                    float* __restrict__ psum,
                                                                    int32_t* __restrict__ counts,
                                                                    float* __restrict__ loss) {
+  constexpr int kRound = 16;  // slots of a strip in flight together
   __shared__ double sp[kFoldThreads];
   __shared__ int32_t sc[kFoldThreads];
   __shared__ double sl[kFoldThreads / 64];
@@ -290,17 +305,17 @@ __global__ __launch_bounds__(kFoldThreads) void router_fold_kernel(const float* 
   double p = 0.0;
   int32_t n = 0;
   const int cc = c < E ? c : 0;
-  for (int t = t0 + strip; t < t1; t += 16 * strips) {
-    float v[16];
-    int32_t k[16];
+  for (int t = t0 + strip; t < t1; t += kRound * strips) {
+    float v[kRound];
+    int32_t k[kRound];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {  // past the last tile: the strip's first one again, and not added
+    for (int i = 0; i < kRound; ++i) {  // past the last tile: the strip's first one again, and not added
       const int64_t at = static_cast<int64_t>(t + i * strips < t1 ? t + i * strips : t) * E + cc;
       v[i] = slot_p[at];
       k[i] = slot_c[at];
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kRound; ++i) {
       const bool in = t + i * strips < t1;
       p += in ? v[i] : 0.0f;
       n += in ? k[i] : 0;
@@ -332,7 +347,7 @@ __global__ __launch_bounds__(kBwdThreads) void router_bwd_kernel(T* __restrict__
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int seg;
   uint32_t r0, r1, s0, s1;
-  if (!segment_tile(offs, S, rows, log_bt, blockIdx.x, seg, r0, r1, s0, s1)) return;
+  if (!segment_tile<kScanBatch>(offs, S, rows, log_bt, blockIdx.x, seg, r0, r1, s0, s1)) return;
   const float g = static_cast<float>(balance_scale(coeff, E, K, s1 - s0) * dloss[seg]);
   const int sub = lane / LPR, l = lane % LPR;
   // c_e less the mean count: the gradient does not change (sum p = 1), and the
@@ -498,10 +513,10 @@ extern "C" int det_router_balance(const void* logits, int64_t ld, int dtype, con
                       {"prob_sum", range1d(prob_sum, S * E * 4)},
                       {"loss", range1d(loss, S * 4)},
                       {"the workspace", range1d(one ? nullptr : ws, ws_bytes)}};
-  const Buf ins[] = {{"logits", range2d(logits, T, E, ld, es)},
+  const Buf ins[] = {{"logits", range2d(logits, T, E, ld, es), es},
                      {"ids", range2d(ids, T, K, ids_ld, 4)},
                      {"offs", range1d(offs, (S + 1) * 4)}};
-  if (int s = check_overlaps(what, outs, 4, ins, 3)) return s;
+  if (int s = check_buffers(what, outs, 4, ins, 3)) return s;
   const hipStream_t st = as_stream(stream);
   char* b = static_cast<char*>(ws);
   auto* table = one ? nullptr : reinterpret_cast<int32_t*>(b + w.table);
@@ -542,12 +557,12 @@ extern "C" int det_router_balance_bwd(void* dlogits, int64_t ld_d, const void* l
   if (!dlogits || !logits || !offs || !counts || !dloss)
     return set_error(DET_ERR_INVALID_ARG, "%s: NULL pointer", what);
   const size_t es = dtype_size(dtype);
-  const Buf outs[] = {{"dlogits", range2d(dlogits, T, E, ld_d, es)}};
-  const Buf ins[] = {{"logits", range2d(logits, T, E, ld, es)},
+  const Buf outs[] = {{"dlogits", range2d(dlogits, T, E, ld_d, es), es}};
+  const Buf ins[] = {{"logits", range2d(logits, T, E, ld, es), es},
                      {"offs", range1d(offs, (S + 1) * 4)},
                      {"counts", range1d(counts, S * E * 4)},
                      {"dloss", range1d(dloss, S * 4)}};
-  if (int s = check_overlaps(what, outs, 1, ins, 4)) return s;
+  if (int s = check_buffers(what, outs, 1, ins, 4)) return s;
   const hipStream_t st = as_stream(stream);
   const int lg = bwd_log(T, E);
   const dim3 grid(static_cast<uint32_t>(max_tiles(T, S, lg)));

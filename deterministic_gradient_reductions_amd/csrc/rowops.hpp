@@ -254,14 +254,21 @@ __device__ __forceinline__ float lanes_max(float v) {
 constexpr int64_t kCacheBytes = int64_t(256) << 20;
 inline bool past_caches(int64_t out_bytes) { return out_bytes >= kCacheBytes; }
 
-// One buffer of a call, for the overlap check.
+// One buffer of a call and the size of its elements.
 struct Buf {
   const char* name;
   Range r;
+  size_t elem = 4;
 };
 
-// No output may overlap an input, another output or the workspace.
-inline int check_overlaps(const char* what, const Buf* outs, int n_out, const Buf* ins, int n_in) {
+// Every buffer starts on a border of its element type, and no output overlaps an
+// input, another output or the workspace.
+inline int check_buffers(const char* what, const Buf* outs, int n_out, const Buf* ins, int n_in) {
+  for (int i = 0; i < n_out + n_in; ++i) {
+    const Buf& b = i < n_out ? outs[i] : ins[i - n_out];
+    if (b.r.lo % b.elem)
+      return set_error(DET_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", what, b.name);
+  }
   for (int i = 0; i < n_out; ++i) {
     for (int j = 0; j < n_in; ++j)
       if (overlaps(outs[i].r, ins[j].r))

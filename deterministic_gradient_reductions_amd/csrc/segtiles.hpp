@@ -43,33 +43,46 @@ __device__ __forceinline__ uint32_t clamp_off(int32_t o, uint32_t M) {
 // b_e = min(M, max(0, offs[0..e])) (clamped monotone), tiles_e =
 // ceil((b_{e+1} - b_e) / block_m), tile_start_e = sum of tiles before e.
 // Returns the segment of global tile t (false past the last tile), the tile's
-// rows [r0, r1) and the segment's rows [s0, s1).
-__device__ inline bool segment_tile(const int32_t* __restrict__ offs, int E, uint32_t M, int log_bm, uint32_t t,
-                                    int& e_out, uint32_t& r0, uint32_t& r1, uint32_t& s0, uint32_t& s1) {
+// rows [r0, r1) and the segment's rows [s0, s1). BATCH groups of 64 offsets are
+// fetched together (one group at a time suffices for a few experts).
+template <int BATCH>
+__device__ __forceinline__ bool segment_tile(const int32_t* __restrict__ offs, int E, uint32_t M, int log_bm,
+                                             uint32_t t, int& e_out, uint32_t& r0, uint32_t& r1, uint32_t& s0,
+                                             uint32_t& s1) {
   const int lane = threadIdx.x & 63;
   const uint32_t bm = 1u << log_bm;
   uint32_t run_b = clamp_off(offs[0], M);  // b of the first segment of the chunk
   uint32_t run_t = 0;                      // tiles before the chunk
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    // b_{e+1}: running max of the offsets (lanes past E repeat offs[E])
-    const uint32_t b1 = umax(scan_max(clamp_off(offs[e < E ? e + 1 : E], M)), run_b);
-    const uint32_t b0 = from_lane_below(b1, run_b);
-    const uint32_t nt = (e < E && b1 > b0) ? (b1 - b0 + bm - 1) >> log_bm : 0u;
-    const uint32_t incl = scan_add(nt);
-    const uint32_t first = run_t + incl - nt;
-    const uint64_t hit = __ballot(e < E && t >= first && t < first + nt);
-    if (hit) {
-      const int j = __builtin_ctzll(hit);
-      e_out = e0 + j;
-      s0 = lane_value(b0, j);
-      s1 = lane_value(b1, j);
-      r0 = s0 + ((t - lane_value(first, j)) << log_bm);
-      r1 = s1 - r0 > bm ? r0 + bm : s1;
-      return true;
+  for (int e1 = 0; e1 < E; e1 += 64 * BATCH) {
+    uint32_t next[BATCH];  // the clamped offsets e + 1 (lanes past E repeat offs[E])
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (BATCH > 1 && k > 0 && e1 + 64 * k >= E) break;
+      const int e = e1 + 64 * k + lane;
+      next[k] = clamp_off(offs[e < E ? e + 1 : E], M);
     }
-    run_t += lane_value(incl, 63);
-    run_b = lane_value(b1, 63);
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (BATCH > 1 && e1 + 64 * k >= E) break;
+      const int e0 = e1 + 64 * k, e = e0 + lane;
+      const uint32_t b1 = umax(scan_max(next[k]), run_b);  // b_{e+1}: running max of the offsets
+      const uint32_t b0 = from_lane_below(b1, run_b);
+      const uint32_t nt = (e < E && b1 > b0) ? (b1 - b0 + bm - 1) >> log_bm : 0u;
+      const uint32_t incl = scan_add(nt);
+      const uint32_t first = run_t + incl - nt;
+      const uint64_t hit = __ballot(e < E && t >= first && t < first + nt);
+      if (hit) {
+        const int j = __builtin_ctzll(hit);
+        e_out = e0 + j;
+        s0 = lane_value(b0, j);
+        s1 = lane_value(b1, j);
+        r0 = s0 + ((t - lane_value(first, j)) << log_bm);
+        r1 = s1 - r0 > bm ? r0 + bm : s1;
+        return true;
+      }
+      run_t += lane_value(incl, 63);
+      run_b = lane_value(b1, 63);
+    }
   }
   return false;
 }
@@ -78,7 +91,7 @@ __device__ inline bool segment_tile(const int32_t* __restrict__ offs, int E, uin
 __device__ inline bool tile_of(const int32_t* __restrict__ offs, int E, uint32_t M, int log_bm, uint32_t t, int& e_out,
                                uint32_t& r0, uint32_t& r1) {
   uint32_t s0, s1;
-  return segment_tile(offs, E, M, log_bm, t, e_out, r0, r1, s0, s1);
+  return segment_tile<1>(offs, E, M, log_bm, t, e_out, r0, r1, s0, s1);
 }
 
 // The tile table [E+1] for a fold kernel: table[e] = tiles of the segments before

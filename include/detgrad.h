@@ -411,13 +411,14 @@ int det_topk_canonicalize(const int32_t* ids, const float* logits, int64_t Q, in
  * offs clamped to [0, T] and made non-decreasing (read on the device only);
  * tokens of no segment are not read. Ids outside [0, E) are not counted; an id
  * given twice counts twice. A token whose logits are all -inf has p = 0; a NaN
- * or +inf logit makes its row's p NaN. An empty segment has zeros.
+ * logit, or with the softmax a logit of +inf, makes its row's p NaN. Scores below
+ * 2^-126 of the row's largest are 0. An empty segment has zeros.
  * The outputs are overwritten, not accumulated. Sums over tokens are float32
  * per tile (the tile by a rule on T and E) and float64 across tiles, in tile
  * order: the same bits from run to run.
  *
- * logits: [T, E], row stride ld >= E elements of any alignment, dtype DET_BF16
- *         or DET_F32; E <= 1024. ids: [T, K] int32, row stride ids_ld >= K;
+ * logits: [T, E], row stride ld >= E elements (rows may start at any element),
+ *         dtype DET_BF16 or DET_F32; E <= 1024. ids: [T, K] int32, row stride ids_ld >= K;
  *         T * K < 2^31. offs: [S + 1] int32, S <= 65535.
  * counts: [S, E] int32, prob_sum: [S, E], loss: [S] float32, contiguous.
  * ws:     det_router_balance_workspace_size() bytes. Its header is neither
@@ -460,8 +461,8 @@ int det_router_balance_bwd(void* dlogits, int64_t ld_d, const void* logits, int6
  * factor tau^2 is applied. The running maximum and sum are float32, joined in
  * one order given by T and V: the same bits from run to run.
  *
- * logits: [T, V], row stride ld >= V elements of any alignment, DET_BF16 or
- *         DET_F32. ids: [T, K] int32, K <= 1024. teacher: [T, K], DET_BF16 or
+ * logits: [T, V], row stride ld >= V elements (rows may start at any element),
+ *         DET_BF16 or DET_F32. ids: [T, K] int32, K <= 1024. teacher: [T, K], DET_BF16 or
  *         DET_F32. Row strides ids_ld, teacher_ld >= K. loss, lse: [T] float32.
  * tau in [1e-6, 1e6].
  * ws:     det_topk_distill_workspace_size() bytes (0 when one workgroup takes a
@@ -496,7 +497,7 @@ int det_topk_distill_bwd(void* dlogits, int64_t ld_d, const void* logits, int64_
  *
  * in float32 (h from y before its rounding), each output rounded once.
  * x, f, y, h: [T, D] of dtype (DET_BF16 or DET_F32), row strides >= D elements
- * of any alignment; D <= 16384. gate: [T, gate_cols], gate_cols = D (a gate per
+ * (rows may start at any element); D <= 16384. gate: [T, gate_cols], gate_cols = D (a gate per
  * channel) or 1 (per token). w_post, alpha, w_pre: [D] float32. rstd_post,
  * rstd_pre: [T] float32, the factors 1 / sqrt(mean + eps), for the backward;
  * given exactly when w_post, w_pre are (and h when w_pre is). Outputs are

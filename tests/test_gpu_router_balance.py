@@ -110,6 +110,7 @@ def test_many_segments():
     g = torch.Generator().manual_seed(3)
     cuts = torch.randint(0, 2001, (700,), generator=g).sort().values.tolist()
     check(2000, 24, 2, BF, [0] + cuts + [2000], "softmax", seed=4)
+    check(700, 400, 2, F32, [0] * 650 + list(range(0, 700, 2)) + [700], "softmax", seed=5)   # tiles of several workgroups
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])

@@ -47,6 +47,12 @@ CASES = [
                                              dict(offs=None), dict(counts=None), dict(prob_sum=None), dict(loss=None)]),
     ("det_router_balance", ROUTER, UNSUPPORTED, [dict(E=1025, ld=1025), dict(S=65536), dict(K=65537, ids_ld=65537),
                                                  dict(T=1 << 29, K=4), dict(ld=1 << 60), dict(ids_ld=1 << 60)]),
+    ("det_router_balance", ROUTER, INVALID, [dict(logits=P(A[0].value + 1)), dict(ids=P(A[1].value + 2)),
+                                             dict(counts=P(A[3].value + 1)), dict(loss=P(A[5].value + 2))]),
+    ("det_topk_distill_bwd", DISTILL_BWD, INVALID, [dict(dlogits=P(A[0].value + 1)), dict(teacher=P(A[3].value + 2))]),
+    ("det_topk_distill", DISTILL, UNSUPPORTED, [dict(T=1 << 24, V=8, ld=8)]),
+    ("det_block_norm", NORM, INVALID, [dict(x=P(A[0].value + 1)), dict(w_pre=P(A[5].value + 2))]),
+    ("det_block_norm_bwd", NORM_BWD, INVALID, [dict(dgate=P(A[12].value + 1)), dict(dw_pre=P(A[15].value + 2))]),
     ("det_router_balance", ROUTER, WORKSPACE, [dict(ws=None), dict(ws=P(A[6].value + 16)), dict(ws_bytes=300)]),
     ("det_router_balance", ROUTER, OVERLAP, [dict(counts=FAR), dict(loss=FAR), dict(prob_sum=A[3]), dict(loss=A[1]),
                                              dict(ws=A[0]), dict(counts=A[2]), dict(loss=A[6])]),
