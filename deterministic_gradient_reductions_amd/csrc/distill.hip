@@ -23,9 +23,10 @@ namespace detgrad {
 namespace {
 
 constexpr int kMaxK = 1024;
-// 16-byte loads of a lane in flight together: in the main loop, and in the loop
-// that takes most of what is left.
-constexpr int kUnroll = 8, kUnrollRest = 2;
+// 16-byte loads of a lane in flight together: in the forward's main loop, in the
+// loop that takes most of what is left, in the backward's.
+constexpr int kUnroll = 8, kUnrollRest = 2, kBwdUnroll = 4;
+constexpr int kBwdThreads = 256;
 
 // Everything below is in units of log2: x2 = x log2(e) = c z with
 // c = log2(e) / tau, formed by one fused step against the reference, so only
@@ -208,22 +209,26 @@ __global__ __launch_bounds__(256) void distill_join_kernel(const T* __restrict__
   if (threadIdx.x < 64) finish_row(a, S, K, loss + row, lse + row);
 }
 
-template <typename T, typename TT, int THREADS, bool PAST>
-__global__ __launch_bounds__(THREADS) void distill_bwd_kernel(T* __restrict__ dz, int64_t ld_d,
+template <typename T, typename TT, bool PAST>
+__global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict__ dz, int64_t ld_d,
                                                                   const T* __restrict__ z, int64_t ld, int64_t V,
                                                                   const int32_t* __restrict__ ids, int64_t ids_ld,
                                                                   const TT* __restrict__ teacher, int64_t t_ld, int K,
                                                                   float it, int n_split, int64_t piece,
                                                                   const float* __restrict__ lse,
                                                                   const float* __restrict__ dloss) {
-  constexpr int kStep = THREADS * 8;
+  constexpr int kStep = kBwdThreads * 8;
   __shared__ Slots S;
   const uint32_t b = gridDim.x - 1 - blockIdx.x;
-  const int64_t row = b / n_split, c0 = (b % n_split) * piece;
-  const int64_t c1 = c0 + piece < V ? c0 + piece : V;
+  const int64_t row = b / n_split, at = (b % n_split) * piece;
   const T* p = z + row * ld;
   T* o = dz + row * ld_d;
-  fetch_slots<T, TT, THREADS>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, it, p, c0, c1);
+  // The pieces start on 128-byte lines of dz, so that a wave's stores fill whole lines (rows of an odd V start
+  // anywhere); the first takes the `lead` elements before the first line too, one per thread.
+  const int64_t first = (-reinterpret_cast<uintptr_t>(o) & 127) / sizeof(T), lead = first < V ? first : V;
+  const int64_t c0 = at ? lead + at : 0, c1 = lead + at + piece < V ? lead + at + piece : V;
+  if (c0 >= c1) return;
+  fetch_slots<T, TT, kBwdThreads>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, it, p, c0, c1);
   const float a = dloss[row] * it, l = lse[row];
   __syncthreads();
   const Teacher q = teacher_row(S, K);  // the same in every wave
@@ -238,11 +243,8 @@ __global__ __launch_bounds__(THREADS) void distill_bwd_kernel(T* __restrict__ dz
     const float h = pow2(__builtin_fmaf(v, it, -l) * (0.5f * kLog2e));
     return a * h * h;
   };
-  // up to the first 128-byte line of dz one element per thread, so that a wave's stores fill whole lines (rows of
-  // an odd V start anywhere)
-  const int64_t lead = (-reinterpret_cast<uintptr_t>(o + c0) & 127) / sizeof(T), head = lead < c1 - c0 ? lead : c1 - c0;
-  int64_t i = c0 + head;
-  if (threadIdx.x < head) o[c0 + threadIdx.x] = from_f32<T>(grad(to_f32(p[c0 + threadIdx.x])));
+  int64_t i = lead + at;
+  if (at == 0 && threadIdx.x < lead) o[threadIdx.x] = from_f32<T>(grad(to_f32(p[threadIdx.x])));
   const auto stream = [&](auto unroll) {
     constexpr int U = decltype(unroll)::value;
     for (; i + U * kStep <= c1; i += U * kStep) {
@@ -259,7 +261,7 @@ __global__ __launch_bounds__(THREADS) void distill_bwd_kernel(T* __restrict__ dz
       }
     }
   };
-  stream(Int<kUnroll>{});
+  stream(Int<kBwdUnroll>{});
   stream(Int<kUnrollRest>{});
   for (; i < c1; i += kStep) {
     float v[8];
@@ -270,9 +272,9 @@ __global__ __launch_bounds__(THREADS) void distill_bwd_kernel(T* __restrict__ dz
     store8(o + k, c1 - k, v);
   }
   // every slot's q in place of its t (each thread its own), the piece's stores before the rewrites
-  for (int k = threadIdx.x; k < K; k += THREADS) S.t[k] = exp_e(S.t[k] - q.m) / q.sum;
+  for (int k = threadIdx.x; k < K; k += kBwdThreads) S.t[k] = exp_e(S.t[k] - q.m) / q.sum;
   __syncthreads();
-  for (int k = threadIdx.x; k < K; k += THREADS) {
+  for (int k = threadIdx.x; k < K; k += kBwdThreads) {
     const int32_t v = S.id[k];
     if (v < c0 || v >= c1) continue;
     bool first = true;
@@ -286,36 +288,34 @@ __global__ __launch_bounds__(THREADS) void distill_bwd_kernel(T* __restrict__ dz
 }
 
 // Workgroups and pieces per row, from the shape alone.
-//
-// Threads of a workgroup that streams `len` elements: as many as still make two
-// turns of the main loop. Backward at 8192 x 131072 bf16 (a step with its
-// forward): 1182 us with 256 threads, 1154 with 512, 1122 with 1024; at 4096 x
-// 32768: 143, 144, 151; at 1021 pieces of 18432: 58, 75, 76.
-int stream_threads(int64_t len) {
-  const int64_t turn = 8 * kUnroll;
-  return len >= 2 * 1024 * turn ? 1024 : (len >= 2 * 512 * turn ? 512 : 256);
-}
 struct Split {
   int n, threads;
   int64_t piece;
 };
 Split split_into(int64_t V, int64_t n, int64_t step, int threads) {
   const int64_t piece = align_up(ceil_div(V, n < 1 ? 1 : n), step);
-  return {static_cast<int>(ceil_div(V, piece)), threads ? threads : stream_threads(piece < V ? piece : V), piece};
+  return {static_cast<int>(ceil_div(V, piece)), threads, piece};
 }
-// Forward: a workgroup per row, of 1024 threads when the rows alone leave
-// compute units idle; a second workgroup for a row costs a second launch and pays
-// only past 2^18 elements (three rows of 131072 float32: 8 us in one launch; 3.8
-// and 3.2 us, and 4 us more of the host's time, in two).
+// Forward: a workgroup per row. 1024 threads when the rows alone leave compute
+// units idle, else as many as still make two turns of the main loop (in a step
+// at 8192 x 131072 bf16 17 us less with 1024 than with 256, at 4096 x 32768 12 us
+// more). A second workgroup for a row costs a second launch and pays only past
+// 2^18 elements (three rows of 131072 float32: 8 us in one launch; 3.8 and 3.2 us,
+// and 4 us more of the host's time, in two).
 Split fwd_split(int64_t T, int64_t V) {
+  const int64_t turn = 8 * kUnroll;
+  const int threads = T < 512 || V >= 2 * 1024 * turn ? 1024 : (V >= 2 * 512 * turn ? 512 : 256);
   const int64_t most = ceil_div(V, int64_t(1) << 18), want = T >= 256 || T == 0 ? 1 : ceil_div(512, T);
-  return split_into(V, want < most ? want : most, 8192, T >= 512 ? 0 : 1024);
+  return split_into(V, want < most ? want : most, 8192, threads);
 }
-// Backward: pieces of 8192 elements or more, about 2048 of them when there are
-// few rows (no second launch is needed).
-Split bwd_split(int64_t T, int64_t V) {
-  const int64_t most = ceil_div(V, 8192), want = T >= 1024 || T == 0 ? 1 : ceil_div(2048, T);
-  return split_into(V, want < most ? want : most, 2048, 0);
+// Backward: pieces of one turn of the main loop (8192 elements), or of 64
+// elements per teacher slot where that is more, since every piece reads the slots.
+// The workgroups in flight then cover one stretch of memory, which the memory
+// serves faster than a workgroup per row: a step at 4096 x 32768 bf16 takes 136 us
+// against 143, at 8192 x 131072 1100 us against 1182 (and 1102 with 1024 threads).
+Split bwd_split(int64_t V, int64_t K) {
+  const int64_t turn = 8 * kBwdThreads * kBwdUnroll, piece = align_up(64 * K > turn ? 64 * K : turn, turn);
+  return {static_cast<int>(ceil_div(V, piece)), kBwdThreads, piece};
 }
 
 int check_args(const char* what, int dtype, int t_dtype, int64_t T, int64_t V, int64_t K, double tau) {
@@ -329,9 +329,9 @@ int check_args(const char* what, int dtype, int t_dtype, int64_t T, int64_t V, i
   if (!(tau >= 1e-6 && tau <= 1e6))
     return set_error(DET_ERR_INVALID_ARG, "%s: tau must lie in [1e-6, 1e6], got %g", what, tau);
   // a launch has at most 2^32 - 1 threads
-  if (T * fwd_split(T, V).n > 0xFFFFFFFF / 1024 && T * fwd_split(T, V).n * fwd_split(T, V).threads > 0xFFFFFFFF)
+  if (T * fwd_split(T, V).n > 0xFFFFFFFF / fwd_split(T, V).threads)
     return set_error(DET_ERR_UNSUPPORTED, "%s: problem too large", what);
-  if (T * bwd_split(T, V).n > 0xFFFFFFFF / 1024 && T * bwd_split(T, V).n * bwd_split(T, V).threads > 0xFFFFFFFF) return set_error(DET_ERR_UNSUPPORTED, "%s: problem too large", what);
+  if (T * bwd_split(V, K).n > 0xFFFFFFFF / kBwdThreads) return set_error(DET_ERR_UNSUPPORTED, "%s: problem too large", what);
   return DET_OK;
 }
 int check_ld(const char* what, const char* name, int64_t ld, int64_t n, int64_t T) {
@@ -366,23 +366,14 @@ template <typename T, typename TT>
 void launch_bwd(void* dz, int64_t ld_d, const void* z, int64_t ld, int64_t V, const int32_t* ids, int64_t ids_ld,
                 const void* t, int64_t t_ld, int64_t rows, int64_t K, float it, const float* lse, const float* dloss,
                 hipStream_t st) {
-  const Split s = bwd_split(rows, V);
+  const Split s = bwd_split(V, K);
   const dim3 grid(static_cast<uint32_t>(rows * s.n));
-  const bool past = past_caches(rows * V * static_cast<int64_t>(sizeof(T)));
-#define DET_DISTILL_BWD(THREADS, PAST)                                                                              \
-  hipLaunchKernelGGL((distill_bwd_kernel<T, TT, THREADS, PAST>), grid, dim3(THREADS), 0, st, static_cast<T*>(dz),   \
-                     ld_d, static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, \
-                     s.n, s.piece, lse, dloss)
-  if (s.threads == 256) {
-    if (past) DET_DISTILL_BWD(256, true);
-    else DET_DISTILL_BWD(256, false);
-  } else if (s.threads == 512) {
-    if (past) DET_DISTILL_BWD(512, true);
-    else DET_DISTILL_BWD(512, false);
-  } else {
-    if (past) DET_DISTILL_BWD(1024, true);
-    else DET_DISTILL_BWD(1024, false);
-  }
+#define DET_DISTILL_BWD(PAST)                                                                                        \
+  hipLaunchKernelGGL((distill_bwd_kernel<T, TT, PAST>), grid, dim3(kBwdThreads), 0, st, static_cast<T*>(dz), ld_d,   \
+                     static_cast<const T*>(z), ld, V, ids, ids_ld, static_cast<const TT*>(t), t_ld, (int)K, it, s.n, \
+                     s.piece, lse, dloss)
+  if (past_caches(rows * V * static_cast<int64_t>(sizeof(T)))) DET_DISTILL_BWD(true);
+  else DET_DISTILL_BWD(false);
 #undef DET_DISTILL_BWD
 }
 

@@ -74,7 +74,8 @@ def test_sizes(T, V, K, dtype, t_dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("V,ld,shift", [(1001, 1001, 1), (1001, 1013, 3), (20000, 20001, 7), (20001, 20001, 0)])
+@pytest.mark.parametrize("V,ld,shift", [(1001, 1001, 1), (1001, 1013, 3), (20000, 20001, 7), (20001, 20001, 0),
+                                        (8200, 8201, 5), (16450, 16451, 33)])
 def test_strides_and_unaligned_rows(V, ld, shift, dtype):
     check(6, V, 20, dtype, dtype, tau=0.7, seed=2, ld=ld, shift=shift)
 

@@ -51,6 +51,7 @@ CASES = [
                                              dict(counts=P(A[3].value + 1)), dict(loss=P(A[5].value + 2))]),
     ("det_topk_distill_bwd", DISTILL_BWD, INVALID, [dict(dlogits=P(A[0].value + 1)), dict(teacher=P(A[3].value + 2))]),
     ("det_topk_distill", DISTILL, UNSUPPORTED, [dict(T=1 << 24, V=8, ld=8)]),
+    ("det_topk_distill_bwd", DISTILL_BWD, UNSUPPORTED, [dict(T=1 << 24, V=8, ld=8, ld_d=8)]),
     ("det_block_norm", NORM, INVALID, [dict(x=P(A[0].value + 1)), dict(w_pre=P(A[5].value + 2))]),
     ("det_block_norm_bwd", NORM_BWD, INVALID, [dict(dgate=P(A[12].value + 1)), dict(dw_pre=P(A[15].value + 2))]),
     ("det_router_balance", ROUTER, WORKSPACE, [dict(ws=None), dict(ws=P(A[6].value + 16)), dict(ws_bytes=300)]),

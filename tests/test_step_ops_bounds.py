@@ -93,51 +93,61 @@ def test_router_tiles_cover_every_token_once(T, E, offs):
         assert np.array_equal(seen, inside)
 
 
-def split_into(V, n, step, threads):
-    piece = cdiv(cdiv(V, max(n, 1)), step) * step
-    length = min(piece, V)
-    t = threads or (1024 if length >= 131072 else 512 if length >= 65536 else 256)
-    return t, cdiv(V, piece), piece
-
-
 def fwd_split(T, V):
+    threads = 1024 if T < 512 or V >= 131072 else 512 if V >= 65536 else 256
     want = 1 if T >= 256 or T == 0 else cdiv(512, T)
-    return split_into(V, min(want, cdiv(V, 1 << 18)), 8192, 0 if T >= 512 else 1024)
-
-
-def bwd_split(T, V):
-    want = 1 if T >= 1024 or T == 0 else cdiv(2048, T)
-    return split_into(V, min(want, cdiv(V, 8192)), 2048, 0)
+    n = max(1, min(want, cdiv(V, 1 << 18)))
+    piece = cdiv(cdiv(V, n), 8192) * 8192
+    return threads, cdiv(V, piece), piece
 
 
 @pytest.mark.parametrize("T,V", [(1, 1), (3, 131072), (3, 600001), (1021, 50001), (2000, 2049), (7, 8193), (1, 262145),
                                  (300, 16384), (600, 7), (5000, 70001), (5000, 140001)])
+def test_distill_forward_pieces_cover_every_word_once(T, V):
+    threads, n, piece = fwd_split(T, V)
+    assert n >= 1 and (n - 1) * piece < V <= n * piece
+    step = threads * 8
+    seen = np.zeros(V, int)
+    for k in range(n):
+        i, c1 = k * piece, min(V, (k + 1) * piece)
+        for u in (8, 2):
+            while i + u * step <= c1:
+                seen[i:i + u * step] += 1
+                i += u * step
+        while i < c1:
+            seen[i:min(i + step, c1)] += 1
+            i += step
+    assert (seen == 1).all()
+
+
+@pytest.mark.parametrize("V", [1, 5, 63, 64, 65, 8191, 8192, 8193, 8255, 8256, 8257, 50001, 131072, 131100])
 @pytest.mark.parametrize("phase", [0, 2, 14, 126])
-def test_distill_pieces_cover_every_word_once(T, V, phase):
-    """The pieces of a row, the lead to a 128-byte line (backward, bf16 at byte `phase` of a line), the loops of eight,
-    two and one accesses."""
-    for bwd in (False, True):
-        threads, n, piece = bwd_split(T, V) if bwd else fwd_split(T, V)
-        assert n >= 1 and (n - 1) * piece < V <= n * piece
-        step = threads * 8
-        seen = np.zeros(V, int)
-        for k in range(n):
-            c0, c1 = k * piece, min(V, (k + 1) * piece)
-            i = c0
-            if bwd:
-                lead = (-(phase + c0 * 2) % 128) // 2
-                head = min(lead, c1 - c0)
-                assert head <= threads
-                seen[c0:c0 + head] += 1
-                i += head
-            for u in (8, 2):
-                while i + u * step <= c1:
-                    seen[i:i + u * step] += 1
-                    i += u * step
-            while i < c1:
-                seen[i:min(i + step, c1)] += 1
-                i += step
-        assert (seen == 1).all()
+@pytest.mark.parametrize("K", [0, 64, 128, 129, 1024])
+def test_distill_backward_pieces_cover_every_word_once(V, phase, K):
+    """Pieces from the first 128-byte line of dz (bf16, the row starting at byte `phase` of a line), the lead with the
+    first; the loops of four, two and one accesses."""
+    piece = cdiv(max(64 * K, 8192), 8192) * 8192
+    step = 2048
+    lead = min((-phase % 128) // 2, V)
+    assert lead <= 256
+    seen = np.zeros(V, int)
+    for k in range(cdiv(V, piece)):
+        at = k * piece
+        c0, c1 = (lead + at if at else 0), min(lead + at + piece, V)
+        if c0 >= c1:
+            continue
+        i = lead + at
+        if at == 0:
+            seen[:lead] += 1
+        for u in (4, 2):
+            while i + u * step <= c1:
+                assert (phase // 2 + i) % 64 == 0
+                seen[i:i + u * step] += 1
+                i += u * step
+        while i < c1:
+            seen[i:min(i + step, c1)] += 1
+            i += step
+    assert (seen == 1).all()
 
 
 def groups_for(T, D, bwd):
