@@ -117,6 +117,29 @@ __device__ __forceinline__ Teacher teacher_row(const Slots& S, int K) {
   return {m, lanes_sum<64>(s)};
 }
 
+// Moves the slots whose words lie in [lo, hi) to the front, in slot order, with
+// their q in place of t; by one wave, with no other reading S.t or S.x. Returns
+// their number.
+__device__ __forceinline__ int gather_slots(Slots& S, int K, Teacher q, int64_t lo, int64_t hi) {
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+  for (int k0 = 0; k0 < K; k0 += 64) {
+    const int k = k0 + lane < K ? k0 + lane : K - 1;
+    const int32_t id = S.id[k];
+    const float t = S.t[k], x = S.x[k];
+    const bool in = k0 + lane < K && id >= lo && id < hi;
+    const uint64_t mask = __ballot(in);
+    const int to = n + __popcll(mask & ((uint64_t(1) << lane) - 1));  // <= k0 + lane: only slots already read
+    if (in) {
+      S.id[to] = id;
+      S.t[to] = exp_e(t - q.m) / q.sum;
+      S.x[to] = x;
+    }
+    n += __popcll(mask);
+  }
+  return n;
+}
+
 // loss and lse of a row from its (reference, sum), by one wave.
 __device__ __forceinline__ void finish_row(MaxSum a, const Slots& S, int K, float* __restrict__ loss,
                                            float* __restrict__ lse) {
@@ -219,6 +242,7 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
                                                                   const float* __restrict__ dloss) {
   constexpr int kStep = kBwdThreads * 8;
   __shared__ Slots S;
+  __shared__ int n_slots;
   const uint32_t b = gridDim.x - 1 - blockIdx.x;
   const int64_t row = b / n_split, at = (b % n_split) * piece;
   const T* p = z + row * ld;
@@ -236,6 +260,11 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
     const float zero[8] = {};
     for (int64_t i = c0 + threadIdx.x * 8; i < c1; i += kStep) store8(o + i, c1 - i, zero);
     return;
+  }
+  __syncthreads();  // every wave has its q
+  if (threadIdx.x < 64) {
+    const int n = gather_slots(S, K, q, c0, c1);
+    if (threadIdx.x == 0) n_slots = n;
   }
   // a exp(x - lse), x - lse rounded once; the root of the exponential twice, since the hardware's 2^y has no
   // results below 2^-126 and a may be large
@@ -271,19 +300,19 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
     for (int j = 0; j < 8; ++j) v[j] = grad(v[j]);
     store8(o + k, c1 - k, v);
   }
-  // every slot's q in place of its t (each thread its own), the piece's stores before the rewrites
-  for (int k = threadIdx.x; k < K; k += kBwdThreads) S.t[k] = exp_e(S.t[k] - q.m) / q.sum;
-  __syncthreads();
-  for (int k = threadIdx.x; k < K; k += kBwdThreads) {
+  __syncthreads();  // the piece's stores come before the rewrites
+  const int n = n_slots;
+  for (int k = threadIdx.x; k < n; k += kBwdThreads) {
     const int32_t v = S.id[k];
-    if (v < c0 || v >= c1) continue;
     bool first = true;
-    for (int j = 0; j < k; ++j) first = first && S.id[j] != v;
-    if (!first) continue;  // the first slot of a repeated id sums them all, in slot order
-    float m = S.t[k];
-    for (int j = k + 1; j < K; ++j)
-      if (S.id[j] == v) m += S.t[j];
-    o[v] = from_f32<T>(a * (exp_e(S.x[k] - l) - m));
+    float m = 0.0f;  // the q of the word's slots, in slot order
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const bool same = S.id[j] == v;
+      first = first && !(same && j < k);
+      m += same ? S.t[j] : 0.0f;
+    }
+    if (first) o[v] = from_f32<T>(a * (exp_e(S.x[k] - l) - m));  // the first slot of a repeated word writes it
   }
 }
 
