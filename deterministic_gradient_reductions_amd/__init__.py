@@ -557,7 +557,7 @@ class _Context:
         # torch.cuda.current_stream() builds a Stream object (2.6 us); the raw handle takes 0.05 us
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda i: torch.cuda.current_stream(i).cuda_stream)
-        self.device = torch.cuda.current_device
+        self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _context() -> _Context:
@@ -584,17 +584,21 @@ def _bad(t, name: str, shape, dtype, dev: int, layout: str) -> None:
     raise ValueError("%s must %s" % (name, layout))
 
 
-def _rows(t, name: str, shape, dtype, dev: int) -> int:
-    """Check a 2-D tensor with unit column stride; return its row stride in elements."""
+def _rows(t, name: str, shape, dtype, dev: int):
+    """Check a 2-D tensor with unit column stride (or None); return its address and row stride in elements."""
+    if t is None:
+        return None, 0
     if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
         st = t.stride()
         if st[1] == 1 or shape[1] <= 1:
-            return st[0] if shape[0] > 1 else max(shape[1], 1)
+            return t.data_ptr(), st[0] if shape[0] > 1 else max(shape[1], 1)
     _bad(t, name, shape, dtype, dev, "have unit innermost stride")
 
 
-def _flat(t, name: str, shape, dtype, dev: int) -> int:
-    """Check a contiguous tensor; return its address."""
+def _flat(t, name: str, shape, dtype, dev: int):
+    """Check a contiguous tensor (or None); return its address."""
+    if t is None:
+        return None
     if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     _bad(t, name, shape, dtype, dev, "be contiguous")
@@ -640,10 +644,6 @@ def _run(c, dev: int, fn, *args) -> None:
         _check(status)
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
@@ -671,14 +671,12 @@ def det_router_balance(logits, ids, offs, counts, prob_sum, loss, coeff: float =
         raise ValueError("need logits [T, E], ids [T, K] and offs [S + 1]")
     T, E = shape = logits.shape
     K, S, dev = ids.shape[1], offs.shape[0] - 1, logits.get_device()
-    ld = _rows(logits, "logits", shape, logits.dtype, dev)
-    ids_ld = _rows(ids, "ids", (T, K), c.i32, dev)
+    rows = *_rows(logits, "logits", shape, logits.dtype, dev), code, *_rows(ids, "ids", (T, K), c.i32, dev)
     p = (_flat(offs, "offs", (S + 1,), c.i32, dev), _flat(counts, "counts", (S, E), c.i32, dev),
          _flat(prob_sum, "prob_sum", (S, E), c.f32, dev), _flat(loss, "loss", (S,), c.f32, dev))
     raw = _stream_on(c, dev, stream)
     wp, wn, keep = _scratch(c, det_router_balance_workspace_size(T, E, K, S), ws, dev, stream, raw)
-    _run(c, dev, lib().det_router_balance, logits.data_ptr(), ld, code, ids.data_ptr(), ids_ld, T, E, K, p[0], S, sc,
-         coeff, p[1], p[2], p[3], wp, wn, raw)
+    _run(c, dev, lib().det_router_balance, *rows, T, E, K, p[0], S, sc, coeff, p[1], p[2], p[3], wp, wn, raw)
 
 
 def det_router_balance_bwd(dlogits, logits, offs, counts, dloss, topk: int, coeff: float = 1.0, score: str = "softmax",
@@ -691,13 +689,11 @@ def det_router_balance_bwd(dlogits, logits, offs, counts, dloss, topk: int, coef
         raise ValueError("need logits [T, E] and offs [S + 1]")
     T, E = shape = logits.shape
     S, dev = offs.shape[0] - 1, logits.get_device()
-    ld = _rows(logits, "logits", shape, logits.dtype, dev)
-    ld_d = _rows(dlogits, "dlogits", shape, logits.dtype, dev)
+    rows = *_rows(dlogits, "dlogits", shape, logits.dtype, dev), *_rows(logits, "logits", shape, logits.dtype, dev)
     po, pc = _flat(offs, "offs", (S + 1,), c.i32, dev), _flat(counts, "counts", (S, E), c.i32, dev)
     pl = _flat(dloss, "dloss", (S,), c.f32, dev)
     raw = _stream_on(c, dev, stream)
-    _run(c, dev, lib().det_router_balance_bwd, dlogits.data_ptr(), ld_d, logits.data_ptr(), ld, code, T, E, topk, po,
-         S, pc, pl, sc, coeff, raw)
+    _run(c, dev, lib().det_router_balance_bwd, *rows, code, T, E, topk, po, S, pc, pl, sc, coeff, raw)
 
 
 @functools.lru_cache(maxsize=256)
@@ -713,9 +709,8 @@ def _distill_operands(c, logits, ids, teacher):
         raise ValueError("need logits [T, V], ids and teacher [T, K]")
     T, V = shape = logits.shape
     K, dev = ids.shape[1], logits.get_device()
-    return dev, (logits.data_ptr(), _rows(logits, "logits", shape, logits.dtype, dev), code,
-                 ids.data_ptr(), _rows(ids, "ids", (T, K), c.i32, dev),
-                 teacher.data_ptr(), _rows(teacher, "teacher", (T, K), teacher.dtype, dev), t_code, T, V, K)
+    return dev, (*_rows(logits, "logits", shape, logits.dtype, dev), code, *_rows(ids, "ids", (T, K), c.i32, dev),
+                 *_rows(teacher, "teacher", (T, K), teacher.dtype, dev), t_code, T, V, K)
 
 
 def det_topk_distill(logits, ids, teacher, loss, lse, tau: float = 1.0, ws=None, stream=None) -> None:
@@ -737,18 +732,10 @@ def det_topk_distill_bwd(dlogits, logits, ids, teacher, lse, dloss, tau: float =
     c = _context()
     dev, ops = _distill_operands(c, logits, ids, teacher)
     T = ops[-3]
-    ld_d = _rows(dlogits, "dlogits", logits.shape, logits.dtype, dev)
+    out = _rows(dlogits, "dlogits", logits.shape, logits.dtype, dev)
     pe, pl = _flat(lse, "lse", (T,), c.f32, dev), _flat(dloss, "dloss", (T,), c.f32, dev)
     raw = _stream_on(c, dev, stream)
-    _run(c, dev, lib().det_topk_distill_bwd, dlogits.data_ptr(), ld_d, *ops, tau, pe, pl, raw)
-
-
-def _opt_rows(t, name: str, shape, dtype, dev: int) -> int:
-    return 0 if t is None else _rows(t, name, shape, dtype, dev)
-
-
-def _opt_flat(t, name: str, shape, dtype, dev: int):
-    return None if t is None else _flat(t, name, shape, dtype, dev)
+    _run(c, dev, lib().det_topk_distill_bwd, *out, *ops, tau, pe, pl, raw)
 
 
 def _gate_cols(gate, D: int) -> int:
@@ -771,11 +758,12 @@ def det_block_norm(x, f, y, gate=None, w_post=None, alpha=None, w_pre=None, h=No
         raise ValueError("x must be [T, D]")
     T, D = sh = x.shape
     dt, gc, f32, dev = x.dtype, _gate_cols(gate, D), c.f32, x.get_device()
-    args = (x.data_ptr(), _rows(x, "x", sh, dt, dev), _at(f), _opt_rows(f, "f", sh, dt, dev),
-            _at(gate), _opt_rows(gate, "gate", (T, gc), dt, dev), gc, _opt_flat(w_post, "w_post", (D,), f32, dev),
-            _opt_flat(alpha, "alpha", (D,), f32, dev), _opt_flat(w_pre, "w_pre", (D,), f32, dev), code, T, D, eps,
-            _at(y), _opt_rows(y, "y", sh, dt, dev), _at(h), _opt_rows(h, "h", sh, dt, dev),
-            _opt_flat(rstd_post, "rstd_post", (T,), f32, dev), _opt_flat(rstd_pre, "rstd_pre", (T,), f32, dev))
+    vec, tok = (D,), (T,)
+    args = (*_rows(x, "x", sh, dt, dev), *_rows(f, "f", sh, dt, dev), *_rows(gate, "gate", (T, gc), dt, dev), gc,
+            _flat(w_post, "w_post", vec, f32, dev), _flat(alpha, "alpha", vec, f32, dev),
+            _flat(w_pre, "w_pre", vec, f32, dev), code, T, D, eps, *_rows(y, "y", sh, dt, dev),
+            *_rows(h, "h", sh, dt, dev), _flat(rstd_post, "rstd_post", tok, f32, dev),
+            _flat(rstd_pre, "rstd_pre", tok, f32, dev))
     raw = _stream_on(c, dev, stream)
     _run(c, dev, lib().det_block_norm, *args, raw)
 
@@ -800,14 +788,13 @@ def det_block_norm_bwd(dy, x, f, dx, df, dh=None, gate=None, w_post=None, alpha=
     T, D = sh = dy.shape
     dt, gc, f32, dev, vec, tok = dy.dtype, _gate_cols(gate, D), c.f32, dy.get_device(), (D,), (T,)
     gs = (T, gc)
-    args = (dy.data_ptr(), _rows(dy, "dy", sh, dt, dev), _at(dh), _opt_rows(dh, "dh", sh, dt, dev),
-            _at(x), _opt_rows(x, "x", sh, dt, dev), _at(f), _opt_rows(f, "f", sh, dt, dev),
-            _at(gate), _opt_rows(gate, "gate", gs, dt, dev), gc, _opt_flat(w_post, "w_post", vec, f32, dev),
-            _opt_flat(alpha, "alpha", vec, f32, dev), _opt_flat(w_pre, "w_pre", vec, f32, dev),
-            _opt_flat(rstd_post, "rstd_post", tok, f32, dev), _opt_flat(rstd_pre, "rstd_pre", tok, f32, dev),
-            code, T, D, _at(dx), _opt_rows(dx, "dx", sh, dt, dev), _at(df), _opt_rows(df, "df", sh, dt, dev),
-            _at(dgate), _opt_rows(dgate, "dgate", gs, dt, dev), _opt_flat(dw_post, "dw_post", vec, f32, dev),
-            _opt_flat(dalpha, "dalpha", vec, f32, dev), _opt_flat(dw_pre, "dw_pre", vec, f32, dev))
+    args = (*_rows(dy, "dy", sh, dt, dev), *_rows(dh, "dh", sh, dt, dev), *_rows(x, "x", sh, dt, dev),
+            *_rows(f, "f", sh, dt, dev), *_rows(gate, "gate", gs, dt, dev), gc, _flat(w_post, "w_post", vec, f32, dev),
+            _flat(alpha, "alpha", vec, f32, dev), _flat(w_pre, "w_pre", vec, f32, dev),
+            _flat(rstd_post, "rstd_post", tok, f32, dev), _flat(rstd_pre, "rstd_pre", tok, f32, dev), code, T, D,
+            *_rows(dx, "dx", sh, dt, dev), *_rows(df, "df", sh, dt, dev), *_rows(dgate, "dgate", gs, dt, dev),
+            _flat(dw_post, "dw_post", vec, f32, dev), _flat(dalpha, "dalpha", vec, f32, dev),
+            _flat(dw_pre, "dw_pre", vec, f32, dev))
     raw = _stream_on(c, dev, stream)
     need = 0 if w_post is None and alpha is None and w_pre is None else det_block_norm_bwd_workspace_size(T, D)
     wp, wn, keep = _scratch(c, need, ws, dev, stream, raw)
