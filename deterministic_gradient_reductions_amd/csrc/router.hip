@@ -7,10 +7,10 @@
 //   loss[s]      = coeff E / (K N_s^2) sum_e counts[s][e] P[s][e]
 //   dz[t][e]     = dloss[s] coeff E / (K N_s^2) p_e (c_e - sum_j p_j c_j)   [(1 - sigmoid(z_e)) for the sigmoid score]
 //
-// Layout: a row of E logits sits in LPR lanes of eight consecutive columns (one
-// or two 16-byte loads per lane), 64 / LPR rows per wave and step, so the
-// softmax's maximum and sum are a few lane exchanges and every lane keeps the
-// running P of its own columns in registers.
+// Layout: a row of E logits sits in LPR lanes of NI times eight consecutive
+// columns, 64 / LPR rows per wave and step, so a row's maximum and sums are a few
+// lane exchanges (for two times eight columns per lane half as many as for eight)
+// and every lane keeps the running P of its own columns in registers.
 //
 // Order of P (no atomics): a tile of rows of one segment belongs to one
 // workgroup; lane group g of wave w adds its rows of the tile in ascending
@@ -38,54 +38,71 @@ constexpr int kScanBatch = 8;
 constexpr int fwd_ahead(int ni) { return 2 / ni; }
 constexpr int bwd_ahead(int ni) { return 2 / ni; }
 
-template <bool B>
-struct Const {
-  static constexpr bool value = B;
-};
-
 // exp(x) for x <= 0 as 2^(x log2 e): within (|x| + 2) units in the last place,
 // which is below 2^-24 of the row's largest score (its own error is |x| e^x).
 __device__ __forceinline__ float exp_nonpos(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
-// A row's scores. softmax: e = exp(z - max z). sigmoid: with t = exp(-|z|),
-// r = 1 / (1 + t), sigmoid(z) = exp(min(z, 0)) r; e = exp(min(z, 0) - max
-// min(z, 0)) r keeps a row of very negative logits from underflowing (LOW), and
-// is sigmoid(z) itself where the row has a logit >= 0.
-//
-// row_ref: the maximum taken out of the exponents; 0 for a row of nothing but
-// -inf, whose scores are then all exp(-inf) = 0 (and a NaN stays one).
-template <int LPR, int NI, bool SIGMOID>
-__device__ __forceinline__ float row_ref(const float (&z)[NI][8]) {
+// The maximum taken out of a row's exponents; 0 for a row of nothing but -inf,
+// whose scores are then all exp(-inf) = 0 (and a NaN stays one).
+template <int LPR, int NI>
+__device__ __forceinline__ float row_max(const float (&z)[NI][8]) {
   float m = -__builtin_inff();
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = fmaxf(m, z[i][j]);
   m = lanes_max<LPR>(m);
-  if (SIGMOID) m = fminf(m, 0.0f);
   return m == -__builtin_inff() ? 0.0f : m;
 }
-// The unnormalised scores e (0 in columns of -inf) and 1 / their sum (0 for a
-// row without any); q = sigmoid(-z) for the gradient.
-template <int LPR, int NI, bool SIGMOID, bool LOW, bool GRAD>
-__device__ __forceinline__ float row_scores(const float (&z)[NI][8], float m, float (&e)[NI][8], float (&q)[NI][8]) {
+template <int LPR, int NI>
+__device__ __forceinline__ float row_sum(const float (&e)[NI][8]) {
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if constexpr (SIGMOID) {
-        const float t = exp_nonpos(-fabsf(z[i][j])), r = __builtin_amdgcn_rcpf(1.0f + t), tr = t * r;
-        const bool neg = z[i][j] < 0.0f;
-        e[i][j] = LOW ? exp_nonpos(fminf(z[i][j], 0.0f) - m) * r : (neg ? tr : r);
-        if (GRAD) q[i][j] = neg ? r : tr;
-      } else {
-        e[i][j] = exp_nonpos(z[i][j] - m);
-      }
-    }
+  for (int i = 0; i < NI; ++i)
     s += ((e[i][0] + e[i][1]) + (e[i][2] + e[i][3])) + ((e[i][4] + e[i][5]) + (e[i][6] + e[i][7]));
+  return lanes_sum<LPR>(s);
+}
+
+// A row's unnormalised scores e (0 in columns of -inf) and 1 / their sum (0 for
+// a row without any); q = sigmoid(-z) for the gradient.
+// softmax: e = exp(z - max z). sigmoid: e = 1 / (1 + t), q = t e with t =
+// exp(-z), which needs no maximum; a row whose scores nearly vanish (every logit
+// far below 0) takes e = exp(min(z, 0) - max min(z, 0)) / (1 + exp(-|z|)) instead,
+// the same scores times a common factor.
+template <int LPR, int NI, bool SIGMOID, bool GRAD>
+__device__ __forceinline__ float row_scores(const float (&z)[NI][8], float (&e)[NI][8], float (&q)[NI][8]) {
+  float s;
+  if constexpr (SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = __builtin_amdgcn_exp2f(z[i][j] * -kLog2e);
+        e[i][j] = __builtin_amdgcn_rcpf(1.0f + t);
+        if (GRAD) q[i][j] = fminf(t, 0x1p126f) * e[i][j];  // (t = inf: e = 0, and q does not matter)
+      }
+    s = row_sum<LPR, NI>(e);
+    if (__ballot(s < 0x1p-64f) != 0) {  // (lanes of other rows get the same scores again)
+      keep_branch();
+      const float m = fminf(row_max<LPR, NI>(z), 0.0f);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float t = exp_nonpos(-fabsf(z[i][j])), r = __builtin_amdgcn_rcpf(1.0f + t);
+          e[i][j] = exp_nonpos(fminf(z[i][j], 0.0f) - m) * r;
+          if (GRAD) q[i][j] = z[i][j] < 0.0f ? r : t * r;
+        }
+      s = row_sum<LPR, NI>(e);
+    }
+  } else {
+    const float m = row_max<LPR, NI>(z);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[i][j] = exp_nonpos(z[i][j] - m);
+    s = row_sum<LPR, NI>(e);
   }
-  s = lanes_sum<LPR>(s);
   return s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
 }
 
@@ -133,32 +150,18 @@ __device__ __forceinline__ void sum_rows(const T* __restrict__ z, int64_t ld, in
   for (int i = 0; i < NI; ++i) c[i].set((i * LPR + l) * 8, E, COLS);
   float acc[NI][8] = {};
   for (uint32_t r = r0 + wave * RPW; r < r1; r += kAhead * W * RPW) {
-    float v[kAhead][NI][8], m[kAhead];
+    float v[kAhead][NI][8];
     load_rows<T, LPR, NI, kAhead>(z, ld, r + sub, W * RPW, r0, r1, c, v);
-    bool low = false;
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      m[a] = row_ref<LPR, NI, SIGMOID>(v[a]);
-      low = low || m[a] != 0.0f;
-    }
-    const auto add = [&](auto is_low) {
+      float e[NI][8], q[NI][8];
+      const float inv = row_scores<LPR, NI, SIGMOID, false>(v[a], e, q);
+      if (r + sub + a * W * RPW < r1) {
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        float e[NI][8], q[NI][8];
-        float inv = row_scores<LPR, NI, SIGMOID, decltype(is_low)::value, false>(v[a], m[a], e, q);
-        if (r + sub + a * W * RPW < r1) {
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-          for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i][j] = __builtin_fmaf(e[i][j], inv, acc[i][j]);
-        }
+          for (int j = 0; j < 8; ++j) acc[i][j] = __builtin_fmaf(e[i][j], inv, acc[i][j]);
       }
-    };
-    if (SIGMOID && __ballot(low) != 0) {
-      keep_branch();
-      add(Const<true>{});
-    } else {
-      add(Const<false>{});
     }
   }
   const uint32_t slots = (r1 - r0) * static_cast<uint32_t>(K);  // < 2^31 (checked by the host)
@@ -365,44 +368,29 @@ __global__ __launch_bounds__(kBwdThreads) void router_bwd_kernel(T* __restrict__
     for (int j = 0; j < 8; ++j) n[i][j] = c[i].own(j) ? static_cast<float>(__float_as_int(n[i][j]) - ref) : 0.0f;
   }
   for (uint32_t r = r0 + wave * RPW; r < r1; r += kBwdAhead * W * RPW) {
-    float v[kBwdAhead][NI][8], m[kBwdAhead];
+    float v[kBwdAhead][NI][8];
     load_rows<T, LPR, NI, kBwdAhead>(z, ld, r + sub, W * RPW, r0, r1, c, v);
-    bool low = false;
 #pragma unroll
     for (int a = 0; a < kBwdAhead; ++a) {
-      m[a] = row_ref<LPR, NI, SIGMOID>(v[a]);
-      low = low || m[a] != 0.0f;
-    }
-    const auto write = [&](auto is_low) {
+      const uint32_t row = r + sub + a * W * RPW;
+      float e[NI][8], q[NI][8];
+      const float inv = row_scores<LPR, NI, SIGMOID, true>(v[a], e, q);
+      float mean = 0.0f;
 #pragma unroll
-      for (int a = 0; a < kBwdAhead; ++a) {
-        const uint32_t row = r + sub + a * W * RPW;
-        float e[NI][8], q[NI][8];
-        const float inv = row_scores<LPR, NI, SIGMOID, decltype(is_low)::value, true>(v[a], m[a], e, q);
-        float mean = 0.0f;
+      for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+        for (int j = 0; j < 8; ++j) mean = __builtin_fmaf(e[i][j], n[i][j], mean);
+      const float gi = g * inv, gm = lanes_sum<LPR>(mean) * inv * gi;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) mean = __builtin_fmaf(e[i][j], n[i][j], mean);
-        mean = lanes_sum<LPR>(mean) * inv;
-        const float gi = g * inv;
+      for (int i = 0; i < NI; ++i) {
+        float d[8];
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          float d[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            d[j] = gi * e[i][j] * (n[i][j] - mean);
-            if (SIGMOID) d[j] *= q[i][j];
-          }
-          if (row < r1) store_cols(dz + static_cast<int64_t>(row) * ld_d, c[i], d);
+        for (int j = 0; j < 8; ++j) {
+          d[j] = e[i][j] * __builtin_fmaf(n[i][j], gi, -gm);
+          if (SIGMOID) d[j] *= q[i][j];
         }
+        if (row < r1) store_cols(dz + static_cast<int64_t>(row) * ld_d, c[i], d);
       }
-    };
-    if (SIGMOID && __ballot(low) != 0) {
-      keep_branch();
-      write(Const<true>{});
-    } else {
-      write(Const<false>{});
     }
   }
 }
@@ -413,15 +401,16 @@ int64_t max_tiles(int64_t T, int64_t S, int log_bt) { return ceil_div(T, int64_t
 // no fewer rows than the workgroup's waves take in one step of `ahead` rows per
 // lane group.
 int tile_log(int64_t T, int64_t E, int threads, int (*ahead)(int), int64_t target) {
+  const int64_t ni = E > 16 ? 2 : 1;
   int64_t lpr = 1;
-  while (lpr * 8 < E && lpr < 64) lpr *= 2;
-  const int64_t step = threads / 64 * (64 / lpr) * ahead(E > 512 ? 2 : 1);
+  while (lpr * ni * 8 < E) lpr *= 2;
+  const int64_t step = threads / 64 * (64 / lpr) * ahead(ni);
   int lg = 0;
   while ((int64_t(1) << lg) < step || (T >> lg) > target) ++lg;
   return lg;
 }
-int fwd_log(int64_t T, int64_t E) { return tile_log(T, E, kFwdThreads, fwd_ahead, 1024); }
-int bwd_log(int64_t T, int64_t E) { return tile_log(T, E, kBwdThreads, bwd_ahead, 2048); }
+int fwd_log(int64_t T, int64_t E) { return tile_log(T, E, kFwdThreads, fwd_ahead, 512); }
+int bwd_log(int64_t T, int64_t E) { return tile_log(T, E, kBwdThreads, bwd_ahead, 1024); }
 
 // A call whose logits would fill at most 16 steps of one workgroup's lanes is
 // summed by one workgroup per segment: in the worst case (one segment) that
@@ -467,15 +456,15 @@ int check_call(const char* what, int dtype, int score, double coeff, int64_t T, 
 
 using namespace detgrad;
 
-// LPR x NI by E (eight columns per lane), the element type and the score.
+// LPR x NI by E (eight columns per lane and NI), the element type and the score.
 #define DET_ROUTER_BY_E(F, TYPE, SIG)          \
   if (E <= 8) { F(TYPE, SIG, 1, 1) }           \
   else if (E <= 16) { F(TYPE, SIG, 2, 1) }     \
-  else if (E <= 32) { F(TYPE, SIG, 4, 1) }     \
-  else if (E <= 64) { F(TYPE, SIG, 8, 1) }     \
-  else if (E <= 128) { F(TYPE, SIG, 16, 1) }   \
-  else if (E <= 256) { F(TYPE, SIG, 32, 1) }   \
-  else if (E <= 512) { F(TYPE, SIG, 64, 1) }   \
+  else if (E <= 32) { F(TYPE, SIG, 2, 2) }     \
+  else if (E <= 64) { F(TYPE, SIG, 4, 2) }     \
+  else if (E <= 128) { F(TYPE, SIG, 8, 2) }    \
+  else if (E <= 256) { F(TYPE, SIG, 16, 2) }   \
+  else if (E <= 512) { F(TYPE, SIG, 32, 2) }   \
   else { F(TYPE, SIG, 64, 2) }
 #define DET_ROUTER_DISPATCH(F)                                                 \
   if (dtype == DET_BF16) {                                                     \

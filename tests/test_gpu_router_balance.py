@@ -137,6 +137,17 @@ def test_masked_experts_and_rows(score):
     ref64.assert_close(dz, wd, wm, 150, "dlogits")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [7, 24, 300])
+def test_rows_of_very_negative_logits(score, E):
+    """Rows whose sigmoids underflow (-150 and below) keep their ratios, beside ordinary rows of the same wave."""
+    z, _ = make(40, E, 2, F32, 3)
+    z[::3] -= 150.0
+    z[1::6] -= 1000.0
+    z[5, 0] = -40.0
+    check(40, E, 2, F32, [0, 13, 40], score, z=z)
+
+
 def test_nan_and_infinity_stay_in_their_row_and_outside_rows_are_not_read():
     z, ids = make(60, 24, 2, F32, 2)
     z[0] = math.nan          # before the first segment

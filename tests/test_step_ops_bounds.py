@@ -29,10 +29,10 @@ def check_cols(N, lanes, tiny):
 
 
 def router_lanes(E):
-    lpr = 1
-    while lpr * 8 < E and lpr < 64:
+    lpr, ni = 1, 2 if E > 16 else 1
+    while lpr * ni * 8 < E:
         lpr *= 2
-    return lpr, 2 if E > 512 else 1
+    return lpr, ni
 
 
 def test_router_columns():
@@ -74,7 +74,7 @@ def test_router_tiles_cover_every_token_once(T, E, offs):
     """segment_tile over the launch's worst-case grid, and every lane group's rows of a tile."""
     b = clamp_bounds(offs, T)
     S = len(b) - 1
-    for threads, ahead, target in ((512, 2, 1024), (256, 2, 2048)):
+    for threads, ahead, target in ((512, 2, 512), (256, 2, 1024)):
         lg = tile_log(T, E, threads, ahead, target)
         grid = cdiv(T, 1 << lg) + S
         tiles = [(s, r) for s in range(S) for r in range(b[s], b[s + 1], 1 << lg)]
