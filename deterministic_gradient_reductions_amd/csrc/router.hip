@@ -19,8 +19,11 @@
 // slots in float64, in tile order per strip and the strips in order. Counts are
 // whole numbers, so their LDS atomics have one result.
 //
-// Both kernels are bound by reading the logits (and writing dz), and at small
-// sizes by the launches.
+// Bytes: the logits once per direction, dz once. Measured at 65536 x 256 bf16
+// with sigmoid scores, 16 segments: tiles 13.6 us (33.5 MB read; the vector units
+// busy for 6.6), fold 5.7, backward 15.7 (67 MB; busy for 9.2): at this size the
+// chain offsets -> rows -> sums -> slots still costs as much as the bytes (14 us in
+// all at the rate of a copy), and small calls are bound by their launches.
 #include "rowops.hpp"
 #include "segtiles.hpp"
 
@@ -399,7 +402,8 @@ int64_t max_tiles(int64_t T, int64_t S, int log_bt) { return ceil_div(T, int64_t
 
 // Rows per tile, a power of two from the shape alone: about `target` tiles, but
 // no fewer rows than the workgroup's waves take in one step of `ahead` rows per
-// lane group.
+// lane group. A step at 65536 x 256 takes 33.2 us with 512 and 1024 tiles (forward,
+// backward), 34.5 with 256 and 1024, 36.2 with 1024 and 2048, 35.9 with 512 and 512.
 int tile_log(int64_t T, int64_t E, int threads, int (*ahead)(int), int64_t target) {
   const int64_t ni = E > 16 ? 2 : 1;
   int64_t lpr = 1;
@@ -414,7 +418,8 @@ int bwd_log(int64_t T, int64_t E) { return tile_log(T, E, kBwdThreads, bwd_ahead
 
 // A call whose logits would fill at most 16 steps of one workgroup's lanes is
 // summed by one workgroup per segment: in the worst case (one segment) that
-// costs about what the second launch and its slots would.
+// costs about what the second launch and its slots would (48 x 8 in three
+// segments: 5.6 us on the GPU in one launch, 4.6 + 5.8 in two).
 bool direct(int64_t T, int64_t E) { return T * E <= (int64_t(16) << 13); }
 
 struct RouterWs {

@@ -5,9 +5,12 @@
  * workgroup writes its own FP32 partial sums into per-tile slots, and the slots
  * are then reduced in a fixed canonical order on the caller's stream
  * (Megatron-LM PR #8244, description; cudnn-frontend PR #521, first commit).
- * Every entry point takes an `atomic` flag: 0 runs the deterministic route,
- * 1 runs the non-deterministic comparison route that adds the same tile
- * partials into the output with hardware float atomics.
+ * Every accumulating reduction takes an `atomic` flag: 0 runs the deterministic
+ * route, 1 runs the non-deterministic comparison route that adds the same tile
+ * partials into the output with hardware float atomics. The losses and norms of
+ * a training step (det_router_balance, det_topk_distill, det_block_norm and
+ * their _bwd calls) have the deterministic route only; their sums have one
+ * order too, and their outputs are overwritten but for the parameter gradients.
  *
  * Conventions for every entry point
  * ---------------------------------
