@@ -244,6 +244,42 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(g[0], a["dw_post"]) and torch.equal(g[1], a["dalpha"]) and torch.equal(g[2], a["dw_pre"])
 
 
+@pytest.mark.parametrize("dtype,T,D", [(BF, 8200, 8192), (F32, 12001, 3001)])
+def test_outputs_past_the_caches(dtype, T, D):
+    """Outputs larger than the last-level cache are stored another way: every row has the bits of a small call, and the
+    parameter gradients agree with float64 column sums of the call's own rows."""
+    assert 2 * T * D * torch.finfo(dtype).bits // 8 >= 256 << 20
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def rows(n):
+        return torch.randn(n, D, device="cuda", dtype=dtype, generator=g)
+    d = dict(x=rows(T), f=rows(T), gate=rows(T), dy=rows(T), dh=rows(T),
+             **{k: 1 + 0.1 * torch.randn(D, device="cuda", generator=g) for k in ("w_post", "alpha", "w_pre")})
+    o = fwd(d)
+    r = bwd(d, o)
+    for a in range(0, T, 1499):
+        e = {k: v[a:a + 5] if v.dim() == 2 else v for k, v in d.items()}
+        p = fwd(e)
+        assert all(torch.equal(p[k], o[k][a:a + 5]) for k in o), a
+        q = bwd(e, p)
+        assert all(torch.equal(q[k], r[k][a:a + 5]) for k in ("dx", "df", "dgate")), a
+    # dw_pre = sum dh yh from the stored y (off by half a step each) and the call's factors
+    yh = o["y"].double() * o["rstd_pre"].double()[:, None]
+    want, mag = (d["dh"].double() * yh).sum(0), (d["dh"].double() * yh).abs().sum(0)
+    tol = (ref64.HALF_STEP[dtype] + 400 * ref64.U) * mag
+    assert bool(((r["dw_pre"].double() - want).abs() <= tol).all())
+
+
+def test_backward_without_x():
+    """x enters the backward only through the second norm."""
+    h = make(40, 150, F32, pre=False, seed=20)
+    d = dev(h)
+    o = fwd(d)
+    want = bwd(d, o)
+    got = bwd(dict(d, x=None), o)
+    assert all(v is None or torch.equal(v, got[k]) for k, v in want.items())
+
+
 def test_replay_under_load_with_poisoned_workspaces():
     d = dev(make(3000, 640, BF, gate="row", seed=11))
     n = dg.det_block_norm_bwd_workspace_size(3000, 640)

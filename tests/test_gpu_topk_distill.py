@@ -193,6 +193,25 @@ def test_rows_past_32_bit_offsets():
     ref64.assert_close(dz, wd, wdm, n, "dlogits")
 
 
+@pytest.mark.parametrize("dtype,T,V", [(BF, 1030, 131072), (F32, 700, 100003)])
+def test_gradients_past_the_caches(dtype, T, V):
+    """A gradient larger than the last-level cache is stored another way: every row has the bits of a small call."""
+    assert T * V * torch.finfo(dtype).bits // 8 >= 256 << 20
+    g = torch.Generator(device="cuda").manual_seed(1)
+    z = torch.randn(T, V, device="cuda", dtype=dtype, generator=g)
+    ids = torch.randint(-1, V, (T, 40), device="cuda", dtype=torch.int32, generator=g)
+    t, dl = torch.randn(T, 40, device="cuda", generator=g), torch.randn(T, device="cuda", generator=g)
+    lse = torch.logsumexp(z.float(), 1)
+    dz = torch.full_like(z, 9.0)
+    dg.det_topk_distill_bwd(dz, z, ids, t, lse, dl)
+    for r in range(0, T, 101):
+        part = torch.full_like(z[r:r + 7], 5.0)
+        n = part.shape[0]
+        dg.det_topk_distill_bwd(part, z[r:r + 7], ids[r:r + 7], t[r:r + 7], lse[r:r + 7].contiguous(),
+                                dl[r:r + 7].contiguous())
+        assert torch.equal(dz[r:r + n], part), r
+
+
 @pytest.mark.parametrize("T", [3, 1100])
 def test_replay_under_load_with_poisoned_workspaces(T):
     V = 700001 if T == 3 else 3000
