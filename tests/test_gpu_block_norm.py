@@ -118,6 +118,15 @@ def test_every_combination_of_parts(gate, post, alpha, pre):
     check(5, 1030, BF, gate=gate, post=post, alpha=alpha, pre=pre, seed=2)
 
 
+@pytest.mark.parametrize("gate,post,alpha,pre", [("none", True, False, True), ("row", False, True, True),
+                                                 ("full", True, True, False), ("row", True, True, True),
+                                                 ("none", False, False, False), ("full", False, False, True)])
+def test_wide_rows(gate, post, alpha, pre):
+    """More than 8192 channels: sixteen per thread, one workgroup walking several rows."""
+    check(5, 8200, F32, gate=gate, post=post, alpha=alpha, pre=pre, seed=3)
+    check(600, 9001, BF, gate=gate, post=post, alpha=alpha, pre=pre, seed=4, ld_extra=3, shift=1)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("gate", ["row", "full"])
 def test_strides_and_unaligned_rows(gate, dtype):
