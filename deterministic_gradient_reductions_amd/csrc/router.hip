@@ -151,6 +151,18 @@ __device__ __forceinline__ void sum_rows(const T* __restrict__ z, int64_t ld, in
   Cols<LPR == 1> c[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) c[i].set((i * LPR + l) * 8, E, COLS);
+  // the ids of slots i, i + THREADS, ... (past the last: the first again, and not counted); the first round's are
+  // fetched ahead of the rows
+  const uint32_t slots = (r1 - r0) * static_cast<uint32_t>(K);  // < 2^31 (checked by the host)
+  int32_t id[4];
+  const auto fetch_ids = [&](uint32_t i) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t at = i + k * THREADS < slots ? i + k * THREADS : i, r = at / static_cast<uint32_t>(K);
+      id[k] = ids[static_cast<int64_t>(r0 + r) * ids_ld + (at - r * K)];
+    }
+  };
+  if (threadIdx.x < slots) fetch_ids(threadIdx.x);
   float acc[NI][8] = {};
   for (uint32_t r = r0 + wave * RPW; r < r1; r += kAhead * W * RPW) {
     float v[kAhead][NI][8];
@@ -167,14 +179,8 @@ __device__ __forceinline__ void sum_rows(const T* __restrict__ z, int64_t ld, in
       }
     }
   }
-  const uint32_t slots = (r1 - r0) * static_cast<uint32_t>(K);  // < 2^31 (checked by the host)
   for (uint32_t i = threadIdx.x; i < slots; i += 4 * THREADS) {
-    int32_t id[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t at = i + k * THREADS < slots ? i + k * THREADS : i, r = at / static_cast<uint32_t>(K);
-      id[k] = ids[static_cast<int64_t>(r0 + r) * ids_ld + (at - r * K)];
-    }
+    if (i >= 4 * THREADS) fetch_ids(i);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (i + k * THREADS < slots && id[k] >= 0 && id[k] < E) atomicAdd(&hist[id[k]], 1);

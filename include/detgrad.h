@@ -424,8 +424,9 @@ int det_topk_canonicalize(const int32_t* ids, const float* logits, int64_t Q, in
  *         dtype DET_BF16 or DET_F32; E <= 1024. ids: [T, K] int32, row stride ids_ld >= K;
  *         T * K < 2^31. offs: [S + 1] int32, S <= 65535.
  * counts: [S, E] int32, prob_sum: [S, E], loss: [S] float32, contiguous.
- * ws:     det_router_balance_workspace_size() bytes. Its header is neither
- *         read nor written, so it needs no det_workspace_init().
+ * ws:     det_router_balance_workspace_size() bytes (0 for small T * E). Its
+ *         header is neither read nor written, so it needs no
+ *         det_workspace_init().
  * No atomic arm. */
 int det_router_balance_workspace_size(int64_t T, int64_t E, int64_t K, int64_t S, size_t* bytes);
 int det_router_balance(const void* logits, int64_t ld, int dtype, const int32_t* ids, int64_t ids_ld, int64_t T,
