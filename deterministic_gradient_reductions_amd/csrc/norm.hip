@@ -191,8 +191,9 @@ __device__ __forceinline__ void load_row(BwdRow<T, NV>& R, const BwdIn<T>& I, bo
 // registers). The parameters of a thread's channels sit in LDS (each thread
 // reads back what it wrote, 16 bytes per lane side by side), which leaves the
 // registers to the running sums, two rows and four waves per SIMD. For D > 8192
-// a thread has 16 channels: their running sums take the LDS instead, and the
-// parameters are read again for every row.
+// a thread has 16 channels: their running sums take the LDS instead, the
+// parameters are read again for every row, and part of the row still spills
+// (4096 x 16384 bf16: 479 us, 2.2 TB/s, against 113 us at D = 8192).
 template <typename T, int THREADS, int NV, bool PAST>
 __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormParams P, T* __restrict__ dx,
                                                               int64_t ld_dx, T* __restrict__ df, int64_t ld_df,
@@ -411,8 +412,8 @@ int threads_for(int64_t D) {
 // walks three rows (forward: its parameters are loaded once) or six (backward:
 // every workgroup also writes a slot of 8 bytes per channel, which the fold
 // reads). Measured at 3001 x 1407 float32: 16 + 21 + 5.5 us against 17 + 21.5 +
-// 7.5 with all workgroups; at 8192 x 4096 bf16 the forward takes 53 us with
-// 2048 workgroups and 57 with 512.
+// 7.5 with all workgroups; at 8192 x 4096 bf16 (inputs in the caches) the forward
+// takes 53 us with 2048 workgroups and 57 with 512.
 int64_t groups_for(int64_t T, int64_t D, bool bwd) {
   const int64_t full = bwd ? 256 * (1024 / threads_for(D)) : 512 * (2048 / threads_for(D));
   const int64_t few = bwd ? 512 : 1024, rows = bwd ? 6 : 3;
