@@ -304,3 +304,17 @@ def test_graph_replays_and_two_streams():
             outs.append(bufs)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want))
+
+
+def test_a_tensor_on_the_host_is_refused():
+    z, ids = make(8, 6, 2, F32, 1)
+    with pytest.raises(ValueError, match="ids"):
+        fwd(z.cuda(), ids, offsets(0, 8))
+    with pytest.raises(ValueError, match="offs"):
+        fwd(z.cuda(), ids.cuda(), torch.tensor([0, 8], dtype=torch.int32))
+    small = torch.zeros(64, dtype=torch.uint8, device="cuda")
+    big, big_ids = make(20000, 32, 2, F32, 1)
+    with pytest.raises(dg.DetError, match="workspace"):
+        fwd(big.cuda(), big_ids.cuda(), offsets(0, 20000), ws=small)
+    with pytest.raises(ValueError, match="workspace"):
+        fwd(big.cuda(), big_ids.cuda(), offsets(0, 20000), ws=small.cpu())
