@@ -28,11 +28,20 @@ constexpr int kMaxK = 1024;
 // loop that takes most of what is left, in the backward's.
 constexpr int kUnroll = 8, kUnrollRest = 2, kBwdUnroll = 4;
 constexpr int kBwdThreads = 256;
+// A float32 lse of 2^14 or more in size is off by up to 2^-10, and so is p taken
+// from it (half a step of bf16 is 2^-8); at the type's range nothing of log s is
+// left in it. The backward forms such a row's maximum and sum again.
+constexpr float kFarLse = 0x1p14f;
 
 // Everything below is in units of log2: x2 = x log2(e) = c z with
 // c = log2(e) / tau, formed by one fused step against the reference, so only
-// the difference is rounded. MaxSum: the reference m (a rounded maximum of c z)
-// and s = sum of 2^(c z - m).
+// the difference is rounded. MaxSum: the reference m (a rounded maximum of c z,
+// at least kLow) and s = sum of 2^(c z - m). m is off from the true maximum by up
+// to 2^-25 |m|, which cancels as long as it is small: where |m| reaches 2^20 it
+// could take s past float32. So a lane that has met nothing but masked words (-inf,
+// the type's lowest value, -1e30) stays at kLow, against which they count 0, and a
+// row whose own reference is out of (kLow, -kLow) is summed another way (far_row).
+constexpr float kLow = -0x1p20f;
 struct MaxSum {
   float m, s;
 };
@@ -44,18 +53,18 @@ struct Int {
 
 __device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// m stays -inf until an element above -inf is seen; its factor is then taken
-// against 0, and every 2^-inf is 0.
-__device__ __forceinline__ float finite_ref(float m) { return m == -__builtin_inff() ? 0.0f : m; }
+__device__ __forceinline__ bool is_far(MaxSum a) { return !(a.m > kLow && a.m < -kLow); }
 
 __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
-  const float m = fmaxf(a.m, b.m), r = finite_ref(m);
-  return {m, a.s * pow2(a.m - r) + b.s * pow2(b.m - r)};
+  const float m = fmaxf(a.m, b.m);
+  return {m, a.s * pow2(a.m - m) + b.s * pow2(b.m - m)};
 }
 
-__device__ __forceinline__ MaxSum wave_join(MaxSum a) {
+// Over groups of W lanes.
+template <int W>
+__device__ __forceinline__ MaxSum lanes_join(MaxSum a) {
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
+  for (int d = 1; d < W; d <<= 1) {
     const MaxSum o{__shfl_xor(a.m, d), __shfl_xor(a.s, d)};
     a = join(a, o);
   }
@@ -72,17 +81,69 @@ __device__ __forceinline__ void push(MaxSum& a, const float (&v)[N][8], float c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = fmaxf(m, v[u][j]);
   m = fmaxf(a.m, m * c);
-  const float r = finite_ref(m);
   float s[4] = {};
 #pragma unroll
   for (int u = 0; u < N; ++u)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j & 3] += pow2(__builtin_fmaf(v[u][j], c, -r));
-  a = {m, a.s * pow2(a.m - r) + ((s[0] + s[1]) + (s[2] + s[3]))};
+    for (int j = 0; j < 8; ++j) s[j & 3] += pow2(__builtin_fmaf(v[u][j], c, -m));
+  a = {m, a.s * pow2(a.m - m) + ((s[0] + s[1]) + (s[2] + s[3]))};
 }
 
-// A row's teacher slots in LDS: the word, teacher / tau (-inf for an invalid
-// slot, which has no weight either way) and the student's z / tau.
+// What turns a logit of the row into x - lse: (c (z - z0) - m) ln 2 - log s, whose
+// first part is one fused step, so log s is not lost where |lse| is large. z0 = 0
+// but for far rows. (A masked word's c z may leave float32 where its z / tau does
+// not: that is then the whole of the difference.)
+struct Norm {
+  float z0, m, logs;
+  __device__ __forceinline__ float log_p(float z, float it) const {
+    const float d = __builtin_fmaf(z - z0, it * kLog2e, -m);
+    return (d == -__builtin_inff() ? (z - z0) * it - m * kLn2 : d * kLn2) - logs;
+  }
+};
+
+// The same for a row whose reference is far from 0 (every logit masked by a large
+// negative number, or one large positive one), by the whole workgroup in two
+// passes over the row: the maximum of z itself, then the sum against it. Rows of
+// nothing but -inf and rows with +inf come here too and keep the values that the
+// formulas give them. `part` has one float per wave.
+template <typename T, int THREADS>
+__device__ __forceinline__ Norm far_row(const T* __restrict__ p, int64_t V, float c, float* part) {
+  constexpr int kWaves = THREADS / 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  keep_branch();
+  float m = -__builtin_inff();
+  for (int64_t i = threadIdx.x * 8; i < V; i += THREADS * 8) {
+    float v[8];
+    load8(p + i, V - i, -__builtin_inff(), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, v[j]);
+  }
+  m = lanes_max<64>(m);
+  __syncthreads();
+  if (lane == 0) part[wave] = m;
+  __syncthreads();
+  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, part[w]);
+  const float r = m == -__builtin_inff() ? 0.0f : m;
+  float s = 0.0f;
+  for (int64_t i = threadIdx.x * 8; i < V; i += THREADS * 8) {
+    float v[8];
+    load8(p + i, V - i, -__builtin_inff(), v);
+    float t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t += pow2((v[j] - r) * c);
+    s += t;
+  }
+  s = lanes_sum<64>(s);
+  __syncthreads();
+  if (lane == 0) part[wave] = s;
+  __syncthreads();
+  s = part[0];
+  for (int w = 1; w < kWaves; ++w) s += part[w];
+  return {m, 0.0f, logf(s)};
+}
+
+// A row's teacher slots in LDS: the word, the teacher's logit (-inf for an invalid
+// slot, which has no weight either way) and the student's.
 struct Slots {
   int32_t id[kMaxK];
   float t[kMaxK], x[kMaxK];
@@ -91,37 +152,38 @@ struct Slots {
 // slot outside [0, V) gets the word -1.
 template <typename T, typename TT, int THREADS>
 __device__ __forceinline__ void fetch_slots(Slots& S, const int32_t* __restrict__ ids, const TT* __restrict__ t, int K,
-                                            int64_t V, float it, const T* __restrict__ z, int64_t lo, int64_t hi) {
+                                            int64_t V, const T* __restrict__ z, int64_t lo, int64_t hi) {
   for (int k = threadIdx.x; k < K; k += THREADS) {
     const int32_t id = ids[k];
     const float tk = to_f32(t[k]);
     const bool valid = id >= 0 && id < V, in = id >= lo && id < hi;
     const float x = to_f32(z[in ? id : lo]);
     S.id[k] = valid ? id : -1;
-    S.t[k] = valid ? tk * it : -__builtin_inff();
-    S.x[k] = in ? x * it : 0.0f;
+    S.t[k] = valid ? tk : -__builtin_inff();
+    S.x[k] = in ? x : 0.0f;
   }
 }
 
 // The teacher's softmax over the valid slots, by one wave: t is at most m (0 if
-// no slot is above -inf), sum = sum exp(t - m); 0 for a row without mass.
+// no slot is above -inf), sum = sum exp((t - m) / tau); 0 for a row without mass.
 struct Teacher {
   float m, sum;
 };
-__device__ __forceinline__ Teacher teacher_row(const Slots& S, int K) {
+__device__ __forceinline__ Teacher teacher_row(const Slots& S, int K, float it) {
   const int lane = threadIdx.x & 63;
   float m = -__builtin_inff();
   for (int k = lane; k < K; k += 64) m = fmaxf(m, S.t[k]);
-  m = finite_ref(lanes_max<64>(m));
+  m = lanes_max<64>(m);
+  m = m == -__builtin_inff() ? 0.0f : m;
   float s = 0.0f;
-  for (int k = lane; k < K; k += 64) s += exp_e(S.t[k] - m);
+  for (int k = lane; k < K; k += 64) s += exp_e((S.t[k] - m) * it);
   return {m, lanes_sum<64>(s)};
 }
 
 // Moves the slots whose words lie in [lo, hi) to the front, in slot order, with
 // their q in place of t; by one wave, with no other reading S.t or S.x. Returns
 // their number.
-__device__ __forceinline__ int gather_slots(Slots& S, int K, Teacher q, int64_t lo, int64_t hi) {
+__device__ __forceinline__ int gather_slots(Slots& S, int K, Teacher q, float it, int64_t lo, int64_t hi) {
   const int lane = threadIdx.x & 63;
   int n = 0;
   for (int k0 = 0; k0 < K; k0 += 64) {
@@ -133,7 +195,7 @@ __device__ __forceinline__ int gather_slots(Slots& S, int K, Teacher q, int64_t 
     const int to = n + __popcll(mask & ((uint64_t(1) << lane) - 1));  // <= k0 + lane: only slots already read
     if (in) {
       S.id[to] = id;
-      S.t[to] = exp_e(t - q.m) / q.sum;
+      S.t[to] = exp_e((t - q.m) * it) / q.sum;
       S.x[to] = x;
     }
     n += __popcll(mask);
@@ -141,23 +203,22 @@ __device__ __forceinline__ int gather_slots(Slots& S, int K, Teacher q, int64_t 
   return n;
 }
 
-// loss and lse of a row from its (reference, sum), by one wave.
-__device__ __forceinline__ void finish_row(MaxSum a, const Slots& S, int K, float* __restrict__ loss,
-                                           float* __restrict__ lse) {
+// loss and lse of a row, by one wave.
+__device__ __forceinline__ void finish_row(const Norm& n, const Slots& S, int K, float it,
+                                           float* __restrict__ loss, float* __restrict__ lse) {
   const int lane = threadIdx.x & 63;
-  const float l = a.m * kLn2 + logf(a.s);
-  const Teacher q = teacher_row(S, K);
+  const Teacher q = teacher_row(S, K, it);
   float tot = 0.0f;
   const float inv = 1.0f / q.sum, logsum = logf(q.sum);
   for (int k = lane; k < K; k += 64) {
-    const float d = S.t[k] - q.m, qk = exp_e(d) * inv;
+    const float d = (S.t[k] - q.m) * it, qk = exp_e(d) * inv;
     // (a NaN q_k or an empty row's 0 / 0 does not take the q_k = 0 way out)
-    if (q.sum != 0.0f && qk != 0.0f) tot += qk * ((d - logsum) - (S.x[k] - l));
+    if (q.sum != 0.0f && qk != 0.0f) tot += qk * ((d - logsum) - n.log_p(S.x[k], it));
   }
   tot = lanes_sum<64>(tot);
   if (lane == 0) {
     *loss = tot;
-    *lse = l;
+    *lse = __builtin_fmaf(n.z0, it, n.m * kLn2) + n.logs;
   }
 }
 
@@ -171,13 +232,14 @@ __global__ __launch_bounds__(THREADS) void distill_fwd_kernel(const T* __restric
                                                               float* __restrict__ lse) {
   constexpr int kWaves = THREADS / 64, kStep = THREADS * 8;
   __shared__ MaxSum part[kWaves];
+  __shared__ float far_part[kWaves];
   __shared__ Slots S;
   const int64_t row = blockIdx.x / n_split, c0 = (blockIdx.x % n_split) * piece;
   const int64_t c1 = c0 + piece < V ? c0 + piece : V;
   const T* p = z + row * ld;
   const float c = it * kLog2e;
-  if (n_split == 1) fetch_slots<T, TT, THREADS>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, it, p, 0, V);
-  MaxSum a{-__builtin_inff(), 0.0f};
+  if (n_split == 1) fetch_slots<T, TT, THREADS>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, p, 0, V);
+  MaxSum a{kLow, 0.0f};
   int64_t i = c0;
   const auto stream = [&](auto unroll) {
     constexpr int U = decltype(unroll)::value;
@@ -199,21 +261,17 @@ __global__ __launch_bounds__(THREADS) void distill_fwd_kernel(const T* __restric
     load8(p + k, c1 - k, -__builtin_inff(), v[0]);
     push<1>(a, v, c);
   }
-  a = wave_join(a);
+  a = lanes_join<64>(a);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
   __syncthreads();
-  if (threadIdx.x >= 64) return;
-  a = part[threadIdx.x % kWaves];  // every wave's value once in each group of kWaves lanes
-#pragma unroll
-  for (int d = 1; d < kWaves; d <<= 1) {
-    const MaxSum o{__shfl_xor(a.m, d), __shfl_xor(a.s, d)};
-    a = join(a, o);
-  }
+  a = lanes_join<kWaves>(part[threadIdx.x % kWaves]);  // every wave's value once in each group of kWaves lanes
   if (n_split > 1) {
     if (threadIdx.x == 0) slots[blockIdx.x] = a;
     return;
   }
-  finish_row(a, S, K, loss + row, lse + row);
+  Norm n{0.0f, a.m, logf(a.s)};
+  if (is_far(a)) n = far_row<T, THREADS>(p, V, c, far_part);  // (the same in every wave)
+  if (threadIdx.x < 64) finish_row(n, S, K, it, loss + row, lse + row);
 }
 
 // One workgroup per row joins the row's slots.
@@ -224,13 +282,18 @@ __global__ __launch_bounds__(256) void distill_join_kernel(const T* __restrict__
                                                            float it, int n_split, const MaxSum* __restrict__ slots,
                                                            float* __restrict__ loss, float* __restrict__ lse) {
   __shared__ Slots S;
+  __shared__ float far_part[4];
   const int64_t row = blockIdx.x;
-  fetch_slots<T, TT, 256>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, it, z + row * ld, 0, V);
-  MaxSum a{-__builtin_inff(), 0.0f};
+  const T* p = z + row * ld;
+  const float c = it * kLog2e;
+  fetch_slots<T, TT, 256>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, p, 0, V);
+  MaxSum a{kLow, 0.0f};
   for (int i = threadIdx.x & 63; i < n_split; i += 64) a = join(a, slots[row * n_split + i]);
-  a = wave_join(a);
+  a = lanes_join<64>(a);
   __syncthreads();
-  if (threadIdx.x < 64) finish_row(a, S, K, loss + row, lse + row);
+  Norm n{0.0f, a.m, logf(a.s)};
+  if (is_far(a)) n = far_row<T, 256>(p, V, c, far_part);
+  if (threadIdx.x < 64) finish_row(n, S, K, it, loss + row, lse + row);
 }
 
 template <typename T, typename TT, bool PAST>
@@ -244,6 +307,7 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
   constexpr int kStep = kBwdThreads * 8;
   __shared__ Slots S;
   __shared__ int n_slots;
+  __shared__ float far_part[kBwdThreads / 64];
   const uint32_t b = gridDim.x - 1 - blockIdx.x;
   const int64_t row = b / n_split, at = (b % n_split) * piece;
   const T* p = z + row * ld;
@@ -253,10 +317,10 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
   const int64_t first = (-reinterpret_cast<uintptr_t>(o) & 127) / sizeof(T), lead = first < V ? first : V;
   const int64_t c0 = at ? lead + at : 0, c1 = lead + at + piece < V ? lead + at + piece : V;
   if (c0 >= c1) return;
-  fetch_slots<T, TT, kBwdThreads>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, it, p, c0, c1);
+  fetch_slots<T, TT, kBwdThreads>(S, ids + row * ids_ld, teacher + row * t_ld, K, V, p, c0, c1);
   const float a = dloss[row] * it, l = lse[row];
   __syncthreads();
-  const Teacher q = teacher_row(S, K);  // the same in every wave
+  const Teacher q = teacher_row(S, K, it);  // the same in every wave
   if (a == 0.0f || q.sum == 0.0f) {
     const float zero[8] = {};
     for (int64_t i = c0 + threadIdx.x * 8; i < c1; i += kStep) store8(o + i, c1 - i, zero);
@@ -264,7 +328,7 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
   }
   __syncthreads();  // every wave has its q
   if (threadIdx.x < 64) {
-    const int n = gather_slots(S, K, q, c0, c1);
+    const int n = gather_slots(S, K, q, it, c0, c1);
     if (threadIdx.x == 0) n_slots = n;
   }
   // a exp(x - lse), x - lse rounded once; the root of the exponential twice, since the hardware's 2^y has no
@@ -274,7 +338,16 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
     return a * h * h;
   };
   int64_t i = lead + at;
-  if (at == 0 && threadIdx.x < lead) o[threadIdx.x] = from_f32<T>(grad(to_f32(p[threadIdx.x])));
+  const bool far = !(fabsf(l) < kFarLse);  // (the same for the whole workgroup)
+  Norm norm{0.0f, 0.0f, 0.0f};
+  if (far) {
+    norm = far_row<T, kBwdThreads>(p, V, it * kLog2e, far_part);
+    for (int64_t k = c0 + threadIdx.x; k < c1; k += kBwdThreads)
+      o[k] = from_f32<T>(a * exp_e(norm.log_p(to_f32(p[k]), it)));
+    i = c1;
+  } else if (at == 0 && threadIdx.x < lead) {
+    o[threadIdx.x] = from_f32<T>(grad(to_f32(p[threadIdx.x])));
+  }
   const auto stream = [&](auto unroll) {
     constexpr int U = decltype(unroll)::value;
     for (; i + U * kStep <= c1; i += U * kStep) {
@@ -313,7 +386,8 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(T* __restrict_
       first = first && !(same && j < k);
       m += same ? S.t[j] : 0.0f;
     }
-    if (first) o[v] = from_f32<T>(a * (exp_e(S.x[k] - l) - m));  // the first slot of a repeated word writes it
+    const float lp = far ? norm.log_p(S.x[k], it) : __builtin_fmaf(S.x[k], it, -l);
+    if (first) o[v] = from_f32<T>(a * (exp_e(lp) - m));  // the first slot of a repeated word writes it
   }
 }
 

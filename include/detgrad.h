@@ -458,17 +458,22 @@ int det_router_balance_bwd(void* dlogits, int64_t ld_d, const void* logits, int6
  *   q = softmax of teacher[t] / tau over the valid slots (0 <= ids[t][k] < V)
  *   loss[t] = sum_k q_k * (log q_k - x[ids[t][k]] + lse[t])
  *
- * Slots with q_k = 0 add nothing, and invalid slots are not read beyond their
- * id. A token with no valid slot, or with only -inf there, has loss 0 (its lse
- * is still written). An id given twice is two slots. Logits of -inf (masked
- * words) have probability 0. loss and lse are overwritten, not accumulated; no
- * factor tau^2 is applied. The running maximum and sum are float32, joined in
- * one order given by T and V: the same bits from run to run.
+ * Slots with q_k = 0 add nothing, and the teacher's value in an invalid slot does
+ * not matter. A token with no valid slot, or with only -inf there, has loss 0 (its
+ * lse is still written). An id given twice is two slots. Logits of -inf (masked
+ * words) have probability 0, and so have those of large negative numbers beside
+ * ordinary ones; a token with nothing but such numbers keeps the formula's finite
+ * loss, with an lse rounded to float32 (infinite where x leaves float32). A logit
+ * of NaN or +inf, or a teacher with mass against nothing but -inf, makes a NaN
+ * loss. loss and lse are overwritten, not accumulated; no factor tau^2 is applied.
+ * The running maximum and sum are float32, joined in one order given by T and V:
+ * the same bits from run to run.
  *
  * logits: [T, V], row stride ld >= V elements (rows may start at any element),
  *         DET_BF16 or DET_F32. ids: [T, K] int32, K <= 1024. teacher: [T, K], DET_BF16 or
  *         DET_F32. Row strides ids_ld, teacher_ld >= K. loss, lse: [T] float32.
- * tau in [1e-6, 1e6].
+ * tau in [1e-6, 1e6]. T < 2^22, or 2^24 with V < 65536 (the backward: T times the
+ * row's pieces of 8192 words < 2^24).
  * ws:     det_topk_distill_workspace_size() bytes (0 when one workgroup takes a
  *         whole row); its header is neither read nor written.
  * No atomic arm. */
@@ -484,8 +489,10 @@ int det_topk_distill(const void* logits, int64_t ld, int dtype, const int32_t* i
  *
  * computed in float32 (repeated ids in slot order) and rounded once to dtype;
  * overwritten. A token without teacher mass, or whose dloss is 0, gets a row of
- * zeros whatever its logits are. lse: [T] float32, the forward's. dlogits:
- * [T, V], row stride ld_d >= V, not overlapping an input. No workspace. */
+ * zeros whatever its logits are. lse: [T] float32, the forward's; where it is
+ * 2^14 or more in size, and so has lost the digits of the sum, it is formed again
+ * from the logits. dlogits: [T, V], row stride ld_d >= V, not overlapping an
+ * input. No workspace. */
 int det_topk_distill_bwd(void* dlogits, int64_t ld_d, const void* logits, int64_t ld, int dtype, const int32_t* ids,
                          int64_t ids_ld, const void* teacher, int64_t teacher_ld, int teacher_dtype, int64_t T,
                          int64_t V, int64_t K, double tau, const float* lse, const float* dloss, void* stream);
