@@ -56,6 +56,17 @@ __device__ __forceinline__ float sigmoid_f(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * kLog2e));
 }
 
+// The backward needs s = sigmoid(g) and 1 - s with all their digits (1 - s formed
+// from a rounded s has lost 1e-4 of its value at g = 9 and all of it from g = 17
+// on), in one register: the smaller of the two, t / (1 + t) with t = exp(-|g|), with
+// g's sign. The other is 1 less it.
+__device__ __forceinline__ float gate_code(float g) {
+  const float t = __builtin_amdgcn_exp2f(-fabsf(g) * kLog2e);
+  return copysignf(t * __builtin_amdgcn_rcpf(1.0f + t), g);
+}
+__device__ __forceinline__ float gate_open(float w) { return __float_as_int(w) < 0 ? -w : 1.0f - w; }
+__device__ __forceinline__ float gate_shut(float w) { return __float_as_int(w) < 0 ? 1.0f + w : w; }
+
 enum GateKind { kGateNone = 0, kGateRow = 1, kGateFull = 2 };
 
 struct NormParams {
@@ -165,16 +176,20 @@ struct BwdIn {
   const T *dy, *dh, *x, *f, *gate;
   int64_t ld_dy, ld_dh, ld_x, ld_f, ld_g;
   const float *rstd_post, *rstd_pre;
-  int gate_kind;
+  bool row_gate;  // one gate per token
 };
 
-template <typename T, int NV, bool TINY>
+// Calls whose outputs pass the caches wait for f before the other tensors are asked
+// for: fewer streams of memory open at once (8192 x 4096 float32: 224 us against
+// 239, 16384 x 8192 bf16: 397 against 401; smaller calls lose 2 us at 3001 x 1407).
+template <bool FULL, bool PAST, typename T, int NV, bool TINY>
 __device__ __forceinline__ void load_row(BwdRow<T, NV>& R, const BwdIn<T>& I, bool post, bool pre, int64_t r,
                                          const Cols<TINY> (&c)[NV]) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     load_cols(R.f[i], I.f + r * I.ld_f, c[i]);
-    if (I.gate_kind == kGateFull) load_cols(R.g[i], I.gate + r * I.ld_g, c[i]);
+    if constexpr (PAST) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (FULL) load_cols(R.g[i], I.gate + r * I.ld_g, c[i]);
     if (pre) {
       load_cols(R.x[i], I.x + r * I.ld_x, c[i]);
       load_cols(R.u[i], I.dh + r * I.ld_dh, c[i]);
@@ -183,30 +198,29 @@ __device__ __forceinline__ void load_row(BwdRow<T, NV>& R, const BwdIn<T>& I, bo
   }
   R.rp = post ? I.rstd_post[r] : 1.0f;
   R.rq = pre ? I.rstd_pre[r] : 1.0f;
-  R.g_row = I.gate_kind == kGateRow ? to_f32(I.gate[r * I.ld_g]) : 0.0f;
+  R.g_row = I.row_gate ? to_f32(I.gate[r * I.ld_g]) : 0.0f;
 }
 
 // A workgroup's slot holds A and dw_pre. The next row's loads are issued as soon
 // as the current row is unpacked (bf16; a float32 row would take twice the
 // registers). The parameters of a thread's channels sit in LDS (each thread
 // reads back what it wrote, 16 bytes per lane side by side), which leaves the
-// registers to the running sums, two rows and four waves per SIMD. For D > 8192
+// registers to the running sums, two rows and four waves per SIMD. FULL: a gate
+// per channel (else one per token or none, and no register holds one). For D > 8192
 // a thread has 16 channels: their running sums take the LDS instead, the
 // parameters are read again for every row, and part of the row still spills
-// (4096 x 16384 bf16: 479 us, 2.2 TB/s, against 113 us at D = 8192).
-template <typename T, int THREADS, int NV, bool PAST>
+// (4096 x 16384 bf16: 382 us, 2.8 TB/s, against 5.4 at 16384 x 8192).
+template <typename T, int THREADS, int NV, bool PAST, bool FULL>
 __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormParams P, T* __restrict__ dx,
                                                               int64_t ld_dx, T* __restrict__ df, int64_t ld_df,
                                                               T* __restrict__ dgate, int64_t ld_dg,
                                                               float* __restrict__ slots) {
   constexpr bool kWide = NV > 1, kAhead = !kWide && sizeof(T) == 2;
-  constexpr int kKept = kWide ? 2 * NV : 3;  // LDS: per thread, kKept sets of eight floats
+  constexpr int kKept = 2 * NV;  // LDS: per thread, kKept sets of eight floats
   __shared__ float buf[2][THREADS / 64];
   __shared__ f32x4 kept[kKept][2][THREADS];
   const bool post = P.w_post != nullptr, pre = P.w_pre != nullptr;
-  const int gate_kind = I.gate_kind;
-  const bool second = post || gate_kind == kGateRow;  // a second sum over the row is needed
-  const float* const params[3] = {P.w_post, P.alpha, P.w_pre};
+  const bool second = post || I.row_gate;  // a second sum over the row is needed
   const auto put = [&](int k, const float(&w)[8]) {
     kept[k][0][threadIdx.x] = f32x4{w[0], w[1], w[2], w[3]};
     kept[k][1][threadIdx.x] = f32x4{w[4], w[5], w[6], w[7]};
@@ -229,17 +243,27 @@ __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormPa
       put(2 * i + 1, sum_pre[i]);
     }
   }
+  // parameters of piece i: 0 = w_post alpha, 1 = w_pre
+  const auto load_params = [&](int k, int i, float(&w)[8]) {
+    load_param(k == 0 ? P.w_post : P.w_pre, c[i], w);
+    if (k == 0) {
+      float al[8];
+      load_param(P.alpha, c[i], al);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] *= al[j];
+    }
+  };
   if constexpr (!kWide) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < 2; ++k) {
       float w[8];
-      load_param(params[k], c[0], w);
+      load_params(k, 0, w);
       put(k, w);
     }
   }
   const auto param = [&](int k, int i, float(&w)[8]) {
     if constexpr (kWide)
-      load_param(params[k], c[i], w);
+      load_params(k, i, w);
     else
       get(k, w);
   };
@@ -257,16 +281,17 @@ __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormPa
     if constexpr (kWide) put(2 * i + which, t);
   };
   BwdRow<T, NV> R;
-  if constexpr (kAhead) load_row(R, I, post, pre, blockIdx.x, c);  // the grid has at most `rows` workgroups
+  if constexpr (kAhead) load_row<FULL, PAST>(R, I, post, pre, blockIdx.x, c);  // the grid has at most `rows` workgroups
 #pragma unroll 1
   for (int64_t r = blockIdx.x; r < P.rows; r += gridDim.x) {
-    float d[NV][8], fh[NV][8], s[NV][8], yh[NV][8], u[NV][8];
-    if constexpr (!kAhead) load_row(R, I, post, pre, r, c);
-    const float rp = R.rp, rq = R.rq, s_row = gate_kind == kGateRow ? sigmoid_f(R.g_row) : 1.0f;
+    float d[NV][8], fh[NV][8], g[NV][8], yh[NV][8], u[NV][8];
+    if constexpr (!kAhead) load_row<FULL, PAST>(R, I, post, pre, r, c);
+    const float rp = R.rp, rq = R.rq;
+    const float w_row = I.row_gate ? gate_code(R.g_row) : 0.0f, s_row = gate_open(w_row);  // (no gate: 1)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       get_cols(R.f[i], c[i], 0.0f, fh[i]);
-      if (gate_kind == kGateFull) R.g[i].get(s[i]);
+      if (FULL) R.g[i].get(g[i]);
       if (pre) {
         get_cols(R.x[i], c[i], 0.0f, yh[i]);
         get_cols(R.u[i], c[i], 0.0f, u[i]);
@@ -274,25 +299,25 @@ __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormPa
       get_cols(R.d[i], c[i], 0.0f, d[i]);
     }
     if constexpr (kAhead) {
-      if (r + gridDim.x < P.rows) load_row(R, I, post, pre, r + gridDim.x, c);
+      if (r + gridDim.x < P.rows) load_row<FULL, PAST>(R, I, post, pre, r + gridDim.x, c);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         fh[i][j] *= rp;
-        s[i][j] = gate_kind == kGateFull ? sigmoid_f(s[i][j]) : s_row;
+        if (FULL) g[i][j] = gate_code(g[i][j]);
       }
     if (pre) {
       float q = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float wp[8], al[8], wq[8];
+        float wp[8], wq[8];
         param(0, i, wp);
-        param(1, i, al);
-        param(2, i, wq);
+        param(1, i, wq);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) yh[i][j] = (yh[i][j] + fh[i][j] * (wp[j] * al[j]) * s[i][j]) * rq;
+        for (int j = 0; j < 8; ++j)
+          yh[i][j] = (yh[i][j] + fh[i][j] * wp[j] * (FULL ? gate_open(g[i][j]) : s_row)) * rq;
         accumulate(1, i, sum_pre[i], u[i], yh[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -312,27 +337,29 @@ __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormPa
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       store_cols<PAST>(dx + r * ld_dx, c[i], d[i]);
-      float wp[8], al[8];
+      float wp[8];
       param(0, i, wp);
-      param(1, i, al);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[i][j] *= s[i][j];
+      for (int j = 0; j < 8; ++j) {
+        if (FULL) asm volatile("" : "+v"(g[i][j]));  // s is formed again, not kept since its first use (registers)
+        d[i][j] *= FULL ? gate_open(g[i][j]) : s_row;
+      }
       accumulate(0, i, sum_a[i], d[i], fh[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        u[i][j] = d[i][j] * (al[j] * wp[j]);
+        u[i][j] = d[i][j] * wp[j];
         q = __builtin_fmaf(u[i][j], fh[i][j], q);
       }
-      if (gate_kind == kGateFull) {
+      if constexpr (FULL) {
         float dg[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dg[j] = u[i][j] * fh[i][j] * (1.0f - s[i][j]);
+        for (int j = 0; j < 8; ++j) dg[j] = u[i][j] * fh[i][j] * gate_shut(g[i][j]);
         store_cols<PAST>(dgate + r * ld_dg, c[i], dg);
       }
     }
     if (second) {
       const float tot = block_sum<THREADS>(q, buf[1]);
-      if (gate_kind == kGateRow && threadIdx.x == 0) dgate[r * ld_dg] = from_f32<T>(tot * (1.0f - s_row));
+      if (I.row_gate && threadIdx.x == 0) dgate[r * ld_dg] = from_f32<T>(tot * gate_shut(w_row));
       if (post) {
         const float mean = tot * P.inv_d;
 #pragma unroll
@@ -445,20 +472,30 @@ int check_ld(const char* what, const char* name, const void* p, int64_t ld, int6
 
 using namespace detgrad;
 
-#define DET_NORM_CASE(KERNEL, T, THREADS, NV, ...)                                                          \
-  if (past)                                                                                                 \
-    hipLaunchKernelGGL((KERNEL<T, THREADS, NV, true>), grid, dim3(THREADS), 0, st, __VA_ARGS__);            \
-  else                                                                                                      \
-    hipLaunchKernelGGL((KERNEL<T, THREADS, NV, false>), grid, dim3(THREADS), 0, st, __VA_ARGS__);           \
+#define DET_NORM_FWD_KERNEL(T, THREADS, NV, ...)                                                                 \
+  if (past)                                                                                                      \
+    hipLaunchKernelGGL((norm_fwd_kernel<T, THREADS, NV, true>), grid, dim3(THREADS), 0, st, __VA_ARGS__);        \
+  else                                                                                                           \
+    hipLaunchKernelGGL((norm_fwd_kernel<T, THREADS, NV, false>), grid, dim3(THREADS), 0, st, __VA_ARGS__);       \
   break;
-#define DET_NORM_LAUNCH(KERNEL, T, ...)                     \
-  switch (D > 8192 ? 2048 : threads_for(D)) {               \
-    case 64: DET_NORM_CASE(KERNEL, T, 64, 1, __VA_ARGS__)   \
-    case 128: DET_NORM_CASE(KERNEL, T, 128, 1, __VA_ARGS__) \
-    case 256: DET_NORM_CASE(KERNEL, T, 256, 1, __VA_ARGS__) \
-    case 512: DET_NORM_CASE(KERNEL, T, 512, 1, __VA_ARGS__) \
-    case 1024: DET_NORM_CASE(KERNEL, T, 1024, 1, __VA_ARGS__) \
-    default: DET_NORM_CASE(KERNEL, T, 1024, 2, __VA_ARGS__) \
+#define DET_NORM_BWD_KERNEL(T, THREADS, NV, ...)                                                                 \
+  if (past && full)                                                                                              \
+    hipLaunchKernelGGL((norm_bwd_kernel<T, THREADS, NV, true, true>), grid, dim3(THREADS), 0, st, __VA_ARGS__);  \
+  else if (past)                                                                                                 \
+    hipLaunchKernelGGL((norm_bwd_kernel<T, THREADS, NV, true, false>), grid, dim3(THREADS), 0, st, __VA_ARGS__); \
+  else if (full)                                                                                                 \
+    hipLaunchKernelGGL((norm_bwd_kernel<T, THREADS, NV, false, true>), grid, dim3(THREADS), 0, st, __VA_ARGS__); \
+  else                                                                                                           \
+    hipLaunchKernelGGL((norm_bwd_kernel<T, THREADS, NV, false, false>), grid, dim3(THREADS), 0, st, __VA_ARGS__); \
+  break;
+#define DET_NORM_LAUNCH(KERNEL, T, ...)        \
+  switch (D > 8192 ? 2048 : threads_for(D)) {  \
+    case 64: KERNEL(T, 64, 1, __VA_ARGS__)     \
+    case 128: KERNEL(T, 128, 1, __VA_ARGS__)   \
+    case 256: KERNEL(T, 256, 1, __VA_ARGS__)   \
+    case 512: KERNEL(T, 512, 1, __VA_ARGS__)   \
+    case 1024: KERNEL(T, 1024, 1, __VA_ARGS__) \
+    default: KERNEL(T, 1024, 2, __VA_ARGS__)   \
   }
 
 extern "C" int det_block_norm(const void* x, int64_t x_ld, const void* f, int64_t f_ld, const void* gate,
@@ -506,7 +543,7 @@ extern "C" int det_block_norm(const void* x, int64_t x_ld, const void* f, int64_
   const bool past = past_caches(T * D * static_cast<int64_t>(es) * (h ? 2 : 1));
   const hipStream_t st = as_stream(stream);
 #define DET_NORM_FWD(E)                                                                                             \
-  DET_NORM_LAUNCH(norm_fwd_kernel, E, static_cast<const E*>(x), x_ld, static_cast<const E*>(f), f_ld,               \
+  DET_NORM_LAUNCH(DET_NORM_FWD_KERNEL, E, static_cast<const E*>(x), x_ld, static_cast<const E*>(f), f_ld,           \
                   static_cast<const E*>(gate), gate_ld, kind, P, static_cast<E*>(y), y_ld, static_cast<E*>(h), h_ld, \
                   rstd_post, rstd_pre)
   if (dtype == DET_BF16) {
@@ -583,17 +620,18 @@ extern "C" int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh,
   if (int s = check_buffers(what, outs, 7, ins, 10)) return s;
   const NormParams P{w_post, alpha, w_pre, 0.0f, static_cast<float>(1.0 / D), T, D};
   const int kind = !gate ? kGateNone : (gate_cols == D ? kGateFull : kGateRow);
+  const bool full = kind == kGateFull;
   const int64_t groups = groups_for(T, D, true);
   const dim3 grid(static_cast<uint32_t>(groups));
-  const bool past = past_caches(T * D * static_cast<int64_t>(es) * (kind == kGateFull ? 3 : 2));
+  const bool past = past_caches(T * D * static_cast<int64_t>(es) * (full ? 3 : 2));
   const hipStream_t st = as_stream(stream);
   auto* slots = need ? reinterpret_cast<float*>(static_cast<char*>(ws) + DET_WS_HEADER_BYTES) : nullptr;
 #define DET_NORM_BWD(E)                                                                                              \
   {                                                                                                                  \
     const BwdIn<E> I{static_cast<const E*>(dy), static_cast<const E*>(dh), static_cast<const E*>(x),                 \
                      static_cast<const E*>(f),  static_cast<const E*>(gate), dy_ld, dh_ld, x_ld, f_ld, gate_ld,      \
-                     rstd_post, rstd_pre, kind};                                                                     \
-    DET_NORM_LAUNCH(norm_bwd_kernel, E, I, P, static_cast<E*>(dx), dx_ld, static_cast<E*>(df), df_ld,                \
+                     rstd_post, rstd_pre, kind == kGateRow};                                                         \
+    DET_NORM_LAUNCH(DET_NORM_BWD_KERNEL, E, I, P, static_cast<E*>(dx), dx_ld, static_cast<E*>(df), df_ld,            \
                     static_cast<E*>(dgate), dgate_ld, slots)                                                         \
   }
   if (dtype == DET_BF16) {
