@@ -69,9 +69,13 @@ __device__ __forceinline__ float row_sum(const float (&e)[NI][8]) {
 // A row's unnormalised scores e (0 in columns of -inf) and 1 / their sum (0 for
 // a row without any); q = sigmoid(-z) for the gradient.
 // softmax: e = exp(z - max z). sigmoid: e = 1 / (1 + t), q = t e with t =
-// exp(-z), which needs no maximum; a row whose scores nearly vanish (every logit
-// far below 0) takes e = exp(min(z, 0) - max min(z, 0)) / (1 + exp(-|z|)) instead,
-// the same scores times a common factor.
+// exp(-z), which needs no maximum; a row whose scores sum to less than kLowSum
+// (every logit below -14) takes e = exp(min(z, 0) - max min(z, 0)) / (1 + exp(-|z|))
+// instead, the same scores times a common factor. In any other row the largest
+// score is at least 2^-30, so what the first form drops (scores below 2^-126) is
+// below 2^-96 of it. The choice is the row's own, not its wave's: a row has the
+// same bits whatever rows it is computed beside.
+constexpr float kLowSum = 0x1p-20f;
 template <int LPR, int NI, bool SIGMOID, bool GRAD>
 __device__ __forceinline__ float row_scores(const float (&z)[NI][8], float (&e)[NI][8], float (&q)[NI][8]) {
   float s;
@@ -85,17 +89,19 @@ __device__ __forceinline__ float row_scores(const float (&z)[NI][8], float (&e)[
         if (GRAD) q[i][j] = fminf(t, 0x1p126f) * e[i][j];  // (t = inf: e = 0, and q does not matter)
       }
     s = row_sum<LPR, NI>(e);
-    if (__ballot(s < 0x1p-64f) != 0) {  // (lanes of other rows get the same scores again)
+    if (__ballot(s < kLowSum) != 0) {
       keep_branch();
       const float m = fminf(row_max<LPR, NI>(z), 0.0f);
+      if (s < kLowSum) {  // (the same for the row's lanes)
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float t = exp_nonpos(-fabsf(z[i][j])), r = __builtin_amdgcn_rcpf(1.0f + t);
-          e[i][j] = exp_nonpos(fminf(z[i][j], 0.0f) - m) * r;
-          if (GRAD) q[i][j] = z[i][j] < 0.0f ? r : t * r;
-        }
+          for (int j = 0; j < 8; ++j) {
+            const float t = exp_nonpos(-fabsf(z[i][j])), r = __builtin_amdgcn_rcpf(1.0f + t);
+            e[i][j] = exp_nonpos(fminf(z[i][j], 0.0f) - m) * r;
+            if (GRAD) q[i][j] = z[i][j] < 0.0f ? r : t * r;
+          }
+      }
       s = row_sum<LPR, NI>(e);
     }
   } else {

@@ -415,7 +415,8 @@ int det_topk_canonicalize(const int32_t* ids, const float* logits, int64_t Q, in
  * tokens of no segment are not read. Ids outside [0, E) are not counted; an id
  * given twice counts twice. A token whose logits are all -inf has p = 0; a NaN
  * logit, or with the softmax a logit of +inf, makes its row's p NaN. Scores below
- * 2^-126 of the row's largest are 0. An empty segment has zeros.
+ * 2^-126 of the row's largest (with the sigmoid: below 2^-96) may be 0. An empty
+ * segment has zeros. A token's scores and gradient do not depend on other tokens'.
  * The outputs are overwritten, not accumulated. Sums over tokens are float32
  * per tile (the tile by a rule on T and E) and float64 across tiles, in tile
  * order: the same bits from run to run.
