@@ -412,15 +412,19 @@ __global__ __launch_bounds__(kBwdThreads) void router_bwd_kernel(T* __restrict__
 
 int64_t max_tiles(int64_t T, int64_t S, int log_bt) { return ceil_div(T, int64_t(1) << log_bt) + S; }
 
+int columns_per_lane(int64_t E) { return E > 16 ? 16 : 8; }
+int64_t lanes_per_row(int64_t E) {
+  int64_t lpr = 1;
+  while (lpr * columns_per_lane(E) < E) lpr *= 2;
+  return lpr;
+}
+
 // Rows per tile, a power of two from the shape alone: about `target` tiles, but
 // no fewer rows than the workgroup's waves take in one step of `ahead` rows per
 // lane group. A step at 65536 x 256 takes 33.2 us with 512 and 1024 tiles (forward,
 // backward), 34.5 with 256 and 1024, 36.2 with 1024 and 2048, 35.9 with 512 and 512.
 int tile_log(int64_t T, int64_t E, int threads, int (*ahead)(int), int64_t target) {
-  const int64_t ni = E > 16 ? 2 : 1;
-  int64_t lpr = 1;
-  while (lpr * ni * 8 < E) lpr *= 2;
-  const int64_t step = threads / 64 * (64 / lpr) * ahead(ni);
+  const int64_t step = threads / lanes_per_row(E) * ahead(columns_per_lane(E) / 8);
   int lg = 0;
   while ((int64_t(1) << lg) < step || (T >> lg) > target) ++lg;
   return lg;
@@ -428,11 +432,26 @@ int tile_log(int64_t T, int64_t E, int threads, int (*ahead)(int), int64_t targe
 int fwd_log(int64_t T, int64_t E) { return tile_log(T, E, kFwdThreads, fwd_ahead, 512); }
 int bwd_log(int64_t T, int64_t E) { return tile_log(T, E, kBwdThreads, bwd_ahead, 1024); }
 
-// A call whose logits would fill at most 16 steps of one workgroup's lanes is
-// summed by one workgroup per segment: in the worst case (one segment) that
-// costs about what the second launch and its slots would (48 x 8 in three
-// segments: 5.6 us on the GPU in one launch, 4.6 + 5.8 in two).
-bool direct(int64_t T, int64_t E) { return T * E <= (int64_t(16) << 13); }
+// A call is summed by one workgroup per segment, in one launch, where that takes
+// no longer than the second launch and its slots. What such a workgroup does is
+// steps (its lanes' rows at a time, one memory latency each) and slots (LDS atomics
+// on few addresses); the host knows S but not the segments, so a mean segment is
+// held to 4 steps and 8192 slots and the longest possible one to 16 steps, 2^17
+// logits and 32768 slots (16384 x 2, K 2 in one of several segments, the worst of
+// these: 29 us against 19).
+// GPU time of one and of two launches (in a graph; outside, two take 11 us of the
+// host), us, float32:
+//   48 x 8, K 2, S 3        5.3  10.2     2048 x 32, K 4, S 1    11.0   9.6
+//   4096 x 8, K 2, S 1      8.0  10.4     4096 x 32, K 4, S 1    15.9   9.9
+//   8192 x 8, K 2, S 1     11.0  10.3     4096 x 32, K 4, S 8     8.2   9.9
+//   16384 x 8, K 2, S 1    17.7  10.4     256 x 256, K 8, S 1     8.4   8.4
+//   16384 x 8, K 2, S 8     6.7  10.8     512 x 256, K 8, S 1    12.3   8.4
+//   16384 x 8, K 8, S 1    37.9  12.1     65536 x 2, K 2, S 1   100.9  19.4
+bool direct(int64_t T, int64_t E, int64_t K, int64_t S) {
+  const int64_t rows = kDirectThreads / lanes_per_row(E), mean = ceil_div(T, S < 1 ? 1 : S);
+  return ceil_div(mean, rows) <= 4 && mean * K <= 8192 && ceil_div(T, rows) <= 16 && T * E <= 131072 &&
+         T * K <= 32768;
+}
 
 struct RouterWs {
   size_t table, p, c, total;
@@ -495,7 +514,7 @@ using namespace detgrad;
 extern "C" int det_router_balance_workspace_size(int64_t T, int64_t E, int64_t K, int64_t S, size_t* bytes) {
   if (!bytes) return set_error(DET_ERR_INVALID_ARG, "router_balance: bytes is NULL");
   if (int s = check_sizes("router_balance", T, E, K, S)) return s;
-  *bytes = S == 0 || direct(T, E) ? 0 : layout(T, E, S).total;
+  *bytes = S == 0 || direct(T, E, K, S) ? 0 : layout(T, E, S).total;
   return ok();
 }
 
@@ -511,7 +530,7 @@ extern "C" int det_router_balance(const void* logits, int64_t ld, int dtype, con
     return set_error(DET_ERR_INVALID_ARG, "%s: NULL pointer", what);
   if (T && ids_ld < K) return set_error(DET_ERR_INVALID_ARG, "%s: ids row stride < K", what);
   if (T && ids_ld > (int64_t(1) << 44) / T) return set_error(DET_ERR_UNSUPPORTED, "%s: tensor too large", what);
-  const bool one = direct(T, E);
+  const bool one = direct(T, E, K, S);
   const RouterWs w = layout(T, E, S);
   if (int s = check_workspace(ws, ws_bytes, one ? 0 : w.total)) return s;
   const size_t es = dtype_size(dtype);

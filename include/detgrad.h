@@ -418,14 +418,14 @@ int det_topk_canonicalize(const int32_t* ids, const float* logits, int64_t Q, in
  * 2^-126 of the row's largest (with the sigmoid: below 2^-96) may be 0. An empty
  * segment has zeros. A token's scores and gradient do not depend on other tokens'.
  * The outputs are overwritten, not accumulated. Sums over tokens are float32
- * per tile (the tile by a rule on T and E) and float64 across tiles, in tile
+ * per tile (the tile by a rule on T, E, K and S) and float64 across tiles, in tile
  * order: the same bits from run to run.
  *
  * logits: [T, E], row stride ld >= E elements (rows may start at any element),
  *         dtype DET_BF16 or DET_F32; E <= 1024. ids: [T, K] int32, row stride ids_ld >= K;
  *         T * K < 2^31. offs: [S + 1] int32, S <= 65535.
  * counts: [S, E] int32, prob_sum: [S, E], loss: [S] float32, contiguous.
- * ws:     det_router_balance_workspace_size() bytes (0 for small T * E). Its
+ * ws:     det_router_balance_workspace_size() bytes (0 for small calls). Its
  *         header is neither read nor written, so it needs no
  *         det_workspace_init().
  * No atomic arm. */
