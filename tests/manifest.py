@@ -94,7 +94,8 @@ MANIFEST = {
         "replay": ["test_gpu_router_balance.py::test_replay_under_load_with_poisoned_workspaces"],
         "parity": ["test_gpu_router_balance.py::test_sizes"],
         "atomic": None,
-        "graph": ["test_gpu_router_balance.py::test_graph_replays_and_two_streams"],
+        "graph": ["test_gpu_router_balance.py::test_graph_replays_and_two_streams",
+                  "test_gpu_router_workspaces.py::test_workspaces_in_graphs_and_on_two_streams"],
     },
     "det_router_balance_bwd": {
         "cite": "Megatron-LM PR #7441 (DSv4), the router aux loss's float atomics",
