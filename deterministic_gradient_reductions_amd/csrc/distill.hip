@@ -520,9 +520,9 @@ extern "C" int det_topk_distill(const void* logits, int64_t ld, int dtype, const
   const Buf outs[] = {{"loss", range1d(loss, T * 4)},
                       {"lse", range1d(lse, T * 4)},
                       {"the workspace", range1d(need ? ws : nullptr, ws_bytes)}};
-  const Buf ins[] = {{"logits", range2d(logits, T, V, ld, es), es},
-                     {"ids", range2d(ids, T, K, ids_ld, 4)},
-                     {"teacher", range2d(teacher, T, K, teacher_ld, ts), ts}};
+  const Buf ins[] = {buf_rows("logits", logits, T, V, ld, es),
+                     buf_rows("ids", ids, T, K, ids_ld, 4),
+                     buf_rows("teacher", teacher, T, K, teacher_ld, ts)};
   if (int s = check_buffers(what, outs, 3, ins, 3)) return s;
   auto* slots = need ? reinterpret_cast<MaxSum*>(static_cast<char*>(ws) + DET_WS_HEADER_BYTES) : nullptr;
   const float it = static_cast<float>(1.0 / tau);
@@ -545,10 +545,10 @@ extern "C" int det_topk_distill_bwd(void* dlogits, int64_t ld_d, const void* log
   if (int s = check_ld(what, "ids", ids_ld, K, T)) return s;
   if (int s = check_ld(what, "teacher", teacher_ld, K, T)) return s;
   const size_t es = dtype_size(dtype), ts = dtype_size(teacher_dtype);
-  const Buf outs[] = {{"dlogits", range2d(dlogits, T, V, ld_d, es), es}};
-  const Buf ins[] = {{"logits", range2d(logits, T, V, ld, es), es},
-                     {"ids", range2d(ids, T, K, ids_ld, 4)},
-                     {"teacher", range2d(teacher, T, K, teacher_ld, ts), ts},
+  const Buf outs[] = {buf_rows("dlogits", dlogits, T, V, ld_d, es)};
+  const Buf ins[] = {buf_rows("logits", logits, T, V, ld, es),
+                     buf_rows("ids", ids, T, K, ids_ld, 4),
+                     buf_rows("teacher", teacher, T, K, teacher_ld, ts),
                      {"lse", range1d(lse, T * 4)},
                      {"dloss", range1d(dloss, T * 4)}};
   if (int s = check_buffers(what, outs, 1, ins, 5)) return s;

@@ -520,19 +520,15 @@ extern "C" int det_block_norm(const void* x, int64_t x_ld, const void* f, int64_
     int64_t ld, cols;
   } rows[] = {{"x", x, x_ld, D}, {"f", f, f_ld, D}, {"gate", gate, gate_ld, gate_cols}, {"y", y, y_ld, D},
               {"h", h, h_ld, D}};
-  Range rr[5];
+  Buf rr[5];
   for (int i = 0; i < 5; ++i) {
     if (int s = check_ld(what, rows[i].name, rows[i].p, rows[i].ld, rows[i].cols, T)) return s;
-    rr[i] = range2d(rows[i].p, T, rows[i].cols, rows[i].ld, dtype_size(dtype));
+    rr[i] = buf_rows(rows[i].name, rows[i].p, T, rows[i].cols, rows[i].ld, dtype_size(dtype));
   }
-  const size_t es = dtype_size(dtype);
-  const Buf outs[] = {{"y", rr[3], es},
-                      {"h", rr[4], es},
+  const Buf outs[] = {rr[3], rr[4],
                       {"rstd_post", range1d(rstd_post, T * 4)},
                       {"rstd_pre", range1d(rstd_pre, T * 4)}};
-  const Buf ins[] = {{"x", rr[0], es},
-                     {"f", rr[1], es},
-                     {"gate", rr[2], es},
+  const Buf ins[] = {rr[0], rr[1], rr[2],
                      {"w_post", range1d(w_post, D * 4)},
                      {"alpha", range1d(alpha, D * 4)},
                      {"w_pre", range1d(w_pre, D * 4)}};
@@ -540,7 +536,7 @@ extern "C" int det_block_norm(const void* x, int64_t x_ld, const void* f, int64_
   const NormParams P{w_post, alpha, w_pre, static_cast<float>(eps), static_cast<float>(1.0 / D), T, D};
   const int kind = !gate ? kGateNone : (gate_cols == D ? kGateFull : kGateRow);
   const dim3 grid(static_cast<uint32_t>(groups_for(T, D, false)));
-  const bool past = past_caches(T * D * static_cast<int64_t>(es) * (h ? 2 : 1));
+  const bool past = past_caches(T * D * static_cast<int64_t>(dtype_size(dtype)) * (h ? 2 : 1));
   const hipStream_t st = as_stream(stream);
 #define DET_NORM_FWD(E)                                                                                             \
   DET_NORM_LAUNCH(DET_NORM_FWD_KERNEL, E, static_cast<const E*>(x), x_ld, static_cast<const E*>(f), f_ld,           \
@@ -592,26 +588,19 @@ extern "C" int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh,
   } rows[] = {{"dy", dy, dy_ld, D}, {"dh", dh, dh_ld, D}, {"x", x, x_ld, D}, {"f", f, f_ld, D},
               {"gate", gate, gate_ld, gate_cols}, {"dx", dx, dx_ld, D}, {"df", df, df_ld, D},
               {"dgate", dgate, dgate_ld, gate_cols}};
-  Range rr[8];
+  Buf rr[8];
   for (int i = 0; i < 8; ++i) {
     if (int s = check_ld(what, rows[i].name, rows[i].p, rows[i].ld, rows[i].cols, T)) return s;
-    rr[i] = range2d(rows[i].p, T, rows[i].cols, rows[i].ld, dtype_size(dtype));
+    rr[i] = buf_rows(rows[i].name, rows[i].p, T, rows[i].cols, rows[i].ld, dtype_size(dtype));
   }
   const size_t need = post || pre || alpha ? ws_bytes_for(T, D) : 0;
   if (int s = check_workspace(ws, ws_bytes, need)) return s;
-  const size_t es = dtype_size(dtype);
-  const Buf outs[] = {{"dx", rr[5], es},
-                      {"df", rr[6], es},
-                      {"dgate", rr[7], es},
+  const Buf outs[] = {rr[5], rr[6], rr[7],
                       {"dw_post", range1d(dw_post, D * 4)},
                       {"dalpha", range1d(dalpha, D * 4)},
                       {"dw_pre", range1d(dw_pre, D * 4)},
                       {"the workspace", range1d(need ? ws : nullptr, ws_bytes)}};
-  const Buf ins[] = {{"dy", rr[0], es},
-                     {"dh", rr[1], es},
-                     {"x", rr[2], es},
-                     {"f", rr[3], es},
-                     {"gate", rr[4], es},
+  const Buf ins[] = {rr[0], rr[1], rr[2], rr[3], rr[4],
                      {"w_post", range1d(w_post, D * 4)},
                      {"alpha", range1d(alpha, D * 4)},
                      {"w_pre", range1d(w_pre, D * 4)},
@@ -623,7 +612,7 @@ extern "C" int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh,
   const bool full = kind == kGateFull;
   const int64_t groups = groups_for(T, D, true);
   const dim3 grid(static_cast<uint32_t>(groups));
-  const bool past = past_caches(T * D * static_cast<int64_t>(es) * (full ? 3 : 2));
+  const bool past = past_caches(T * D * static_cast<int64_t>(dtype_size(dtype)) * (full ? 3 : 2));
   const hipStream_t st = as_stream(stream);
   auto* slots = need ? reinterpret_cast<float*>(static_cast<char*>(ws) + DET_WS_HEADER_BYTES) : nullptr;
 #define DET_NORM_BWD(E)                                                                                              \

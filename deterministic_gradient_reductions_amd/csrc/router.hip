@@ -538,8 +538,8 @@ extern "C" int det_router_balance(const void* logits, int64_t ld, int dtype, con
                       {"prob_sum", range1d(prob_sum, S * E * 4)},
                       {"loss", range1d(loss, S * 4)},
                       {"the workspace", range1d(one ? nullptr : ws, ws_bytes)}};
-  const Buf ins[] = {{"logits", range2d(logits, T, E, ld, es), es},
-                     {"ids", range2d(ids, T, K, ids_ld, 4)},
+  const Buf ins[] = {buf_rows("logits", logits, T, E, ld, es),
+                     buf_rows("ids", ids, T, K, ids_ld, 4),
                      {"offs", range1d(offs, (S + 1) * 4)}};
   if (int s = check_buffers(what, outs, 4, ins, 3)) return s;
   const hipStream_t st = as_stream(stream);
@@ -582,8 +582,8 @@ extern "C" int det_router_balance_bwd(void* dlogits, int64_t ld_d, const void* l
   if (!dlogits || !logits || !offs || !counts || !dloss)
     return set_error(DET_ERR_INVALID_ARG, "%s: NULL pointer", what);
   const size_t es = dtype_size(dtype);
-  const Buf outs[] = {{"dlogits", range2d(dlogits, T, E, ld_d, es), es}};
-  const Buf ins[] = {{"logits", range2d(logits, T, E, ld, es), es},
+  const Buf outs[] = {buf_rows("dlogits", dlogits, T, E, ld_d, es)};
+  const Buf ins[] = {buf_rows("logits", logits, T, E, ld, es),
                      {"offs", range1d(offs, (S + 1) * 4)},
                      {"counts", range1d(counts, S * E * 4)},
                      {"dloss", range1d(dloss, S * 4)}};

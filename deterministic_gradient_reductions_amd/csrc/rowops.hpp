@@ -253,12 +253,26 @@ __device__ __forceinline__ float lanes_max(float v) {
 constexpr int64_t kCacheBytes = int64_t(256) << 20;
 inline bool past_caches(int64_t out_bytes) { return out_bytes >= kCacheBytes; }
 
-// One buffer of a call and the size of its elements.
+// One buffer of a call, the size of its elements, and for rows with a stride the
+// bytes of a row and from row to row (0: one piece).
 struct Buf {
   const char* name;
   Range r;
-  size_t elem = 4;
+  size_t elem = 4, width = 0, pitch = 0;
 };
+inline Buf buf_rows(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, size_t elem) {
+  return {name, range2d(p, rows, cols, ld, elem), elem, static_cast<size_t>(cols) * elem, static_cast<size_t>(ld) * elem};
+}
+
+// Whether two buffers share a byte. Rows with one stride that take different
+// columns of it (two halves of one [T, 2D] buffer) lie between each other; for
+// other strides the spans decide.
+inline bool overlaps(const Buf& a, const Buf& b) {
+  if (!overlaps(a.r, b.r)) return false;
+  if (a.pitch == 0 || a.pitch != b.pitch) return true;
+  const size_t d = a.r.lo <= b.r.lo ? (b.r.lo - a.r.lo) % a.pitch : (a.pitch - (a.r.lo - b.r.lo) % a.pitch) % a.pitch;
+  return d < a.width || d + b.width > a.pitch;
+}
 
 // Every buffer starts on a border of its element type, and no output overlaps an
 // input, another output or the workspace.
@@ -270,10 +284,10 @@ inline int check_buffers(const char* what, const Buf* outs, int n_out, const Buf
   }
   for (int i = 0; i < n_out; ++i) {
     for (int j = 0; j < n_in; ++j)
-      if (overlaps(outs[i].r, ins[j].r))
+      if (overlaps(outs[i], ins[j]))
         return set_error(DET_ERR_OVERLAP, "%s: %s overlaps %s", what, outs[i].name, ins[j].name);
     for (int j = i + 1; j < n_out; ++j)
-      if (overlaps(outs[i].r, outs[j].r))
+      if (overlaps(outs[i], outs[j]))
         return set_error(DET_ERR_OVERLAP, "%s: %s overlaps %s", what, outs[i].name, outs[j].name);
   }
   return DET_OK;

@@ -513,7 +513,10 @@ int det_topk_distill_bwd(void* dlogits, int64_t ld_d, const void* logits, int64_
  * channel) or 1 (per token). w_post, alpha, w_pre: [D] float32. rstd_post,
  * rstd_pre: [T] float32, the factors 1 / sqrt(mean + eps), for the backward;
  * given exactly when w_post, w_pre are (and h when w_pre is). Outputs are
- * overwritten and overlap no input and no other output. No workspace. */
+ * overwritten and overlap no input and no other output; two column ranges of one
+ * buffer do not overlap if they have one row stride (with different strides the
+ * spans decide), here as in the router's and the distillation's calls. No
+ * workspace. */
 int det_block_norm(const void* x, int64_t x_ld, const void* f, int64_t f_ld, const void* gate, int64_t gate_ld,
                    int64_t gate_cols, const float* w_post, const float* alpha, const float* w_pre, int dtype, int64_t T,
                    int64_t D, double eps, void* y, int64_t y_ld, void* h, int64_t h_ld, float* rstd_post,
