@@ -20,7 +20,7 @@
 // parameters and the parameter gradients' running sums of a thread's channels
 // stay in registers while it walks its rows. The parameter gradients are column
 // sums: workgroup b adds rows b, b + G, b + 2G, ... in order into its own slot
-// (no atomics), a fold adds the slots in a fixed order and once into the output.
+// (no atomics), a fold adds the slots in a fixed order in float64, and once into the output.
 //
 // Both directions are bound by the [T, D] tensors: five read or written forward
 // (8192 x 4096 bf16, a gate per channel: 67 us, 5.0 TB/s), eight backward (16384 x
@@ -385,8 +385,9 @@ __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormPa
   }
 }
 
-// Workgroup (64 columns, sum): wave w of 16 adds slots w, w + 16, ... in order,
-// the waves' sums meet left to right, one add into each output. Sixteen waves
+// Workgroup (64 columns, sum): wave w of 16 adds slots w, w + 16, ... in order in
+// float64, the waves' sums meet left to right, the total (times its parameter) is
+// rounded to float32 once and added into the output. Sixteen waves
 // with 16 loads each in flight, since a call has few columns and the slots come
 // from other XCDs' L2s.
 struct NormGrads {
@@ -395,13 +396,13 @@ struct NormGrads {
 constexpr int kFoldWaves = 16;
 __global__ __launch_bounds__(64 * kFoldWaves) void norm_fold_kernel(const float* __restrict__ slots, int n_slots,
                                                                     NormParams P, NormGrads G) {
-  __shared__ float part[kFoldWaves][64];
+  __shared__ double part[kFoldWaves][64];
   const bool second = blockIdx.y == 1;  // dw_pre
   if (second ? !G.w_pre : !(G.w_post || G.alpha)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t D = P.D, col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
   const float* p = slots + blockIdx.y * D + (col < D ? col : 0);
-  float t = 0.0f;
+  double t = 0.0;
   for (int b = wave; b < n_slots; b += 16 * kFoldWaves) {
     float v[16];
 #pragma unroll
@@ -419,11 +420,11 @@ __global__ __launch_bounds__(64 * kFoldWaves) void norm_fold_kernel(const float*
 #pragma unroll
   for (int w = 1; w < kFoldWaves; ++w) t += part[w][lane];
   if (second) {
-    G.w_pre[col] += t;
+    G.w_pre[col] += static_cast<float>(t);
   } else {
-    const float wp = P.w_post ? P.w_post[col] : 1.0f, al = P.alpha ? P.alpha[col] : 1.0f;
-    if (G.w_post) G.w_post[col] += t * al;
-    if (G.alpha) G.alpha[col] += t * wp;
+    const double wp = P.w_post ? P.w_post[col] : 1.0f, al = P.alpha ? P.alpha[col] : 1.0f;
+    if (G.w_post) G.w_post[col] += static_cast<float>(t * al);
+    if (G.alpha) G.alpha[col] += static_cast<float>(t * wp);
   }
 }
 

@@ -534,8 +534,8 @@ int det_block_norm(const void* x, int64_t x_ld, const void* f, int64_t f_ld, con
  * dx, df, dgate (dtype, overwritten) have the layouts of x, f, gate; the
  * parameter gradients ([D] float32) accumulate like every reduction here:
  * out <- RN32(out + total), with a workgroup's rows (b, b + G, ... for a G
- * given by T and D) added in order and the workgroups' slots in one fixed
- * order, in float32. dh, rstd_pre, dw_pre are given exactly when w_pre is,
+ * given by T and D) added in order in float32 and the workgroups' sums in one
+ * fixed order in float64, the total rounded to float32. dh, rstd_pre, dw_pre are given exactly when w_pre is,
  * rstd_post, dw_post when w_post is, dalpha when alpha is, dgate when gate is;
  * x may be NULL without w_pre. T = 0 leaves every output unchanged.
  * ws: det_block_norm_bwd_workspace_size() bytes when any of w_post, alpha,
