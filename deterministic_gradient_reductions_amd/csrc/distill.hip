@@ -28,10 +28,11 @@ constexpr int kMaxK = 1024;
 // loop that takes most of what is left, in the backward's.
 constexpr int kUnroll = 8, kUnrollRest = 2, kBwdUnroll = 4;
 constexpr int kBwdThreads = 256;
-// A float32 lse of 2^14 or more in size is off by up to 2^-10, and so is p taken
-// from it (half a step of bf16 is 2^-8); at the type's range nothing of log s is
-// left in it. The backward forms such a row's maximum and sum again.
-constexpr float kFarLse = 0x1p14f;
+// A float32 lse below 2^10 in size is off by at most 2^-15, and so is p taken from
+// it. A larger one (every word masked by -1e4, or by the type's lowest value, where
+// nothing of log s is left in it) is not used: the backward forms such a row's
+// maximum and sum again, which costs each of its pieces two reads of the row.
+constexpr float kFarLse = 0x1p10f;
 
 // Everything below is in units of log2: x2 = x log2(e) = c z with
 // c = log2(e) / tau, formed by one fused step against the reference, so only

@@ -491,8 +491,8 @@ int det_topk_distill(const void* logits, int64_t ld, int dtype, const int32_t* i
  * computed in float32 (repeated ids in slot order) and rounded once to dtype;
  * overwritten. A token without teacher mass, or whose dloss is 0, gets a row of
  * zeros whatever its logits are. lse: [T] float32, the forward's; where it is
- * 2^14 or more in size, and so has lost the digits of the sum, it is formed again
- * from the logits. dlogits: [T, V], row stride ld_d >= V, not overlapping an
+ * 2^10 or more in size, and so has lost digits of the sum, it is formed again from
+ * the logits. dlogits: [T, V], row stride ld_d >= V, not overlapping an
  * input. No workspace. */
 int det_topk_distill_bwd(void* dlogits, int64_t ld_d, const void* logits, int64_t ld, int dtype, const int32_t* ids,
                          int64_t ids_ld, const void* teacher, int64_t teacher_ld, int teacher_dtype, int64_t T,

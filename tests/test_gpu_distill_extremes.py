@@ -79,3 +79,21 @@ def test_ordinary_rows_beside_extreme_ones_keep_their_bits():
     want = fwd(*alone)
     got = fwd(z.cuda(), ids.cuda(), t.cuda())
     assert torch.equal(got[0][4:5], want[0]) and torch.equal(got[1][4:5], want[1])
+
+
+@pytest.mark.parametrize("shift", [-1e4, -1100.0, 1100.0, 9000.0])
+def test_rows_far_from_zero_keep_their_digits(shift):
+    """Float32 gradients of rows whose lse has few digits left for log s."""
+    g = torch.Generator().manual_seed(2)
+    z = torch.randn(3, 9001, generator=g) + shift
+    z[2] = shift
+    ids = torch.stack([torch.randperm(9001, generator=g)[:9] for _ in range(3)]).int()
+    t, dl = torch.randn(3, 9, generator=g) * 3, torch.randn(3, generator=g) + 3
+    loss, lse = fwd(z.cuda(), ids.cuda(), t.cuda())
+    dz = torch.zeros_like(z).cuda()
+    dg.det_topk_distill_bwd(dz, z.cuda(), ids.cuda(), t.cuda(), lse, dl.cuda())
+    wl, wm, _, wd, wdm = reference(z, ids, t, dl, 1.0)
+    # the differences to the largest logit are those of an ordinary row
+    n = roundings(z - shift, t, 1.0, 9001)
+    ref64.assert_close(loss, wl, wm, n, "loss")
+    ref64.assert_close(dz, wd, wdm, n, "dlogits")
