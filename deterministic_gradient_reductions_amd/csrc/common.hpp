@@ -1,9 +1,12 @@
 // Shared host and device helpers of libdetgrad (gfx950).
 //
-// Arithmetic rule for every deterministic kernel: IEEE binary32 with
-// round-to-nearest-even, one rounding per + - * /, no contraction (the library
-// is compiled with -ffp-contract=off), no flush of subnormals. bf16 inputs are
-// widened exactly by a 16-bit shift.
+// Arithmetic rule for every kernel that is held to the bits of an oracle (the
+// reductions and the top-k): IEEE binary32 with round-to-nearest-even, one rounding
+// per + - * /, no contraction (the library is compiled with -ffp-contract=off), no
+// flush of subnormals. bf16 inputs are widened exactly by a 16-bit shift. The losses
+// and norms (router, distill, norm) are held to float64 within counted roundings:
+// they fuse where they say so and use the hardware's exponential and reciprocal,
+// which flush results below 2^-126; their order of summation is fixed all the same.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -15,8 +15,8 @@
 // order. Backward: dz of a piece of the row is written in one streaming pass,
 // then the workgroup rewrites the at most K elements that a teacher slot names.
 // The slots' words and logits are fetched into LDS while the row streams.
-// Both are bound by the logits' bytes (8192 x 131072 bf16: forward 354 us, 6.1 TB/s;
-// backward 738 us, 5.8 TB/s); the backward takes the rows in reverse order, so
+// Both are bound by the logits' bytes (8192 x 131072 bf16: forward 359 us, 6.0 TB/s;
+// backward 726 us, 5.9 TB/s); the backward takes the rows in reverse order, so
 // that after a forward it first meets the rows still cached (18 us there).
 #include "rowops.hpp"
 
@@ -404,9 +404,13 @@ Split split_into(int64_t V, int64_t n, int64_t step, int threads) {
 // Forward: a workgroup per row. 1024 threads when the rows alone leave compute
 // units idle, else as many as still make two turns of the main loop (in a step
 // at 8192 x 131072 bf16 17 us less with 1024 than with 256, at 4096 x 32768 12 us
-// more). A second workgroup for a row costs a second launch and pays only past
-// 2^18 elements (three rows of 131072 float32: 8 us in one launch; 3.8 and 3.2 us,
-// and 4 us more of the host's time, in two).
+// more). A second workgroup for a row costs a second launch and a workspace, 11.5 us
+// of wall time at the least, so rows are cut past 2^18 words only. Three float32
+// rows in one launch and in two with pieces of 2^14 words, wall time (GPU time):
+// 131072 words 8.8 (8.8) and 11.5 us (6.4), 151936 9.9 (9.9) and 11.6 (6.4), 262144
+// 13.4 (13.4) and 11.4 (6.4). The pieces of up to 2^18 words taken past the border
+// are longer than they need be: 600001 words take 14.7 us (14.5), 12.0 (6.7) with
+// pieces of 2^14.
 Split fwd_split(int64_t T, int64_t V) {
   const int64_t turn = 8 * kUnroll;
   const int threads = T < 512 || V >= 2 * 1024 * turn ? 1024 : (V >= 2 * 512 * turn ? 512 : 256);

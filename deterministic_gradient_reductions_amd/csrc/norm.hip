@@ -24,7 +24,7 @@
 //
 // Both directions are bound by the [T, D] tensors: five read or written forward
 // (8192 x 4096 bf16, a gate per channel: 67 us, 5.0 TB/s), eight backward (16384 x
-// 8192 bf16: 396 us, 5.4 TB/s, and 6 for the fold).
+// 8192 bf16: 391 us, 5.5 TB/s, and 6.5 for the fold).
 #include "rowops.hpp"
 
 namespace detgrad {
@@ -209,7 +209,7 @@ __device__ __forceinline__ void load_row(BwdRow<T, NV>& R, const BwdIn<T>& I, bo
 // per channel (else one per token or none, and no register holds one). For D > 8192
 // a thread has 16 channels: their running sums take the LDS instead, the
 // parameters are read again for every row, and part of the row still spills
-// (4096 x 16384 bf16: 382 us, 2.8 TB/s, against 5.4 at 16384 x 8192).
+// (4096 x 16384 bf16: 381 us, 2.8 TB/s, against 5.5 at 16384 x 8192).
 template <typename T, int THREADS, int NV, bool PAST, bool FULL>
 __global__ __launch_bounds__(THREADS, 4) void norm_bwd_kernel(BwdIn<T> I, NormParams P, T* __restrict__ dx,
                                                               int64_t ld_dx, T* __restrict__ df, int64_t ld_df,
@@ -439,8 +439,8 @@ int threads_for(int64_t D) {
 // registers allow), but where the tokens are few, few enough that a workgroup
 // walks three rows (forward: its parameters are loaded once) or six (backward:
 // every workgroup also writes a slot of 8 bytes per channel, which the fold
-// reads). Measured at 3001 x 1407 float32: 16 + 21 + 5.5 us against 17 + 21.5 +
-// 7.5 with all workgroups; at 8192 x 4096 bf16 (inputs in the caches) the forward
+// reads). Measured at 3001 x 1407 float32 (inputs in the caches): 16 + 21 + 5.5 us against
+// 17 + 21.5 + 7.5 with all workgroups; at 8192 x 4096 bf16 (inputs in the caches) the forward
 // takes 53 us with 2048 workgroups and 57 with 512.
 int64_t groups_for(int64_t T, int64_t D, bool bwd) {
   const int64_t full = bwd ? 256 * (1024 / threads_for(D)) : 512 * (2048 / threads_for(D));

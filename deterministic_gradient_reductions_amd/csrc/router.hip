@@ -20,9 +20,9 @@
 // whole numbers, so their LDS atomics have one result.
 //
 // Bytes: the logits once per direction, dz once. Measured at 65536 x 256 bf16
-// with sigmoid scores, 16 segments: tiles 13.6 us (33.5 MB read; the vector units
-// busy for 6.6), fold 5.7, backward 15.7 (67 MB; busy for 9.2): at this size the
-// chain offsets -> rows -> sums -> slots still costs as much as the bytes (14 us in
+// with sigmoid scores, 16 segments: tiles 13.5 us (33.5 MB read; the vector units
+// busy for 6.9), fold 5.5, backward 15.9 (67 MB; busy for 9.2): at this size the
+// chain offsets -> rows -> sums -> slots still costs as much as the bytes (13 us in
 // all at the rate of a copy), and small calls are bound by their launches.
 #include "rowops.hpp"
 #include "segtiles.hpp"

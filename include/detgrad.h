@@ -507,7 +507,9 @@ int det_topk_distill_bwd(void* dlogits, int64_t ld_d, const void* logits, int64_
  *   y = x + alpha * sigmoid(gate) * n              (alpha NULL, gate NULL: a factor of 1)
  *   h = w_pre * y / sqrt(mean(y^2) + eps)          (w_pre NULL: no h)
  *
- * in float32 (h from y before its rounding), each output rounded once.
+ * in float32 (h from y before its rounding), each output rounded once. The means
+ * are float32 sums: a row whose squares pass 3.4e38 (values from about 1e19 on) has
+ * a factor of 0.
  * x, f, y, h: [T, D] of dtype (DET_BF16 or DET_F32), row strides >= D elements
  * (rows may start at any element); D <= 16384. gate: [T, gate_cols], gate_cols = D (a gate per
  * channel) or 1 (per token). w_post, alpha, w_pre: [D] float32. rstd_post,
