@@ -22,10 +22,15 @@ Functions (same names as the C ABI):
     det_block_norm(x, f, y, gate=, w_post=, alpha=, w_pre=, h=, rstd_post=, rstd_pre=, eps=1e-6)
     det_block_norm_bwd(dy, x, f, dx, df, dh=, gate=, w_post=, alpha=, w_pre=, rstd_post=, rstd_pre=, dgate=,
                        dw_post=, dalpha=, dw_pre=)
+    det_delta_rule(q, k, v, g, beta, o, offs, initial_state=, final_state=, states=, scale=)
+    det_delta_rule_bwd(do, q, k, v, g, beta, offs, states, dq, dk, dv, dg, dbeta, dfinal_state=, dinitial_state=, scale=)
+    det_delta_rule_step(q, k, v, g, beta, state, o, slots=, scale=)
+    det_qk_norm(q, k, q_out, k_out, w_q=, w_k=, norm="rms", eps=1e-6, pos=, inv_freq=, axis=, pairs="halves")
+    det_qk_norm_bwd(dq_out, dk_out, q, k, dq, dk, w_q=, w_k=, dw_q=, dw_k=, norm=, eps=, pos=, inv_freq=, axis=, pairs=)
 Every function accepts ``ws=`` (a Workspace or a uint8 device tensor) and
 ``stream=`` (a torch.cuda.Stream); by default a cached per-stream workspace
-and torch's current stream are used. The router balance, distillation and block
-norm functions take no cached workspace: without ``ws=`` they allocate one from
+and torch's current stream are used. The router balance, distillation, block
+norm, delta rule and query and key norm functions take no cached workspace: without ``ws=`` they allocate one from
 torch's caching allocator on the call's stream (so it is safe inside a graph
 capture), and without ``stream=`` they use the current stream of the tensors'
 device, whichever device is current.
@@ -46,7 +51,9 @@ __all__ = [
     "det_grouped_dbias_workspace_size", "det_topk_canonicalize", "det_workspace_init", "det_detmath_eval", "det_mfma_eval",
     "det_mfma_rate", "det_router_balance", "det_router_balance_bwd", "det_router_balance_workspace_size",
     "det_topk_distill", "det_topk_distill_bwd", "det_topk_distill_workspace_size", "det_block_norm",
-    "det_block_norm_bwd", "det_block_norm_bwd_workspace_size", "DET_OK", "DET_ERR_INVALID_ARG", "DET_ERR_UNSUPPORTED", "DET_ERR_WORKSPACE", "DET_ERR_OVERLAP", "DET_ERR_HIP",
+    "det_block_norm_bwd", "det_block_norm_bwd_workspace_size", "det_delta_rule", "det_delta_rule_bwd",
+    "det_delta_rule_step", "det_delta_rule_states_shape", "det_delta_rule_workspace_size",
+    "det_delta_rule_bwd_workspace_size", "det_qk_norm", "det_qk_norm_bwd", "det_qk_norm_bwd_workspace_size", "DET_OK", "DET_ERR_INVALID_ARG", "DET_ERR_UNSUPPORTED", "DET_ERR_WORKSPACE", "DET_ERR_OVERLAP", "DET_ERR_HIP",
 ]
 
 DET_OK, DET_ERR_INVALID_ARG, DET_ERR_UNSUPPORTED, DET_ERR_WORKSPACE, DET_ERR_OVERLAP, DET_ERR_HIP = 0, -1, -2, -3, -4, -5
@@ -142,6 +149,21 @@ _SIGS = {
     "det_block_norm_bwd_workspace_size": ([_I64, _I64, ctypes.POINTER(_SZ)], _INT),
     "det_block_norm_bwd": ([_P, _I64] * 5 + [_I64] + [_P] * 5 + [_INT, _I64, _I64] + [_P, _I64] * 3 +
                            [_P] * 4 + [_SZ, _P], _INT),
+    "det_delta_rule_chunks": ([_I64, _I64, _INT, ctypes.POINTER(_I64)], _INT),
+    "det_delta_rule_workspace_size": ([_I64, _I64, _I64, _INT, ctypes.POINTER(_SZ)], _INT),
+    "det_delta_rule": ([_P, _I64, _I64] * 3 + [_P, _I64] * 2 + [_INT] + [_I64] * 5 + [_P, _I64, _F64, _P, _P, _I64, _I64] +
+                       [_P] * 3 + [_SZ, _P], _INT),
+    "det_delta_rule_bwd_workspace_size": ([_I64] * 5 + [_INT, ctypes.POINTER(_SZ)], _INT),
+    "det_delta_rule_bwd": ([_P, _I64, _I64] * 4 + [_P, _I64] * 2 + [_INT] + [_I64] * 5 + [_P, _I64, _F64, _P, _P] +
+                           [_P, _I64, _I64] * 3 + [_P, _I64] * 2 + [_P, _P, _SZ, _P], _INT),
+    "det_delta_rule_step": ([_P, _I64, _I64] * 3 + [_P, _I64] * 2 + [_INT] + [_I64] * 5 + [_F64, _P, _I64, _P] +
+                            [_P, _I64, _I64, _P], _INT),
+    "det_qk_norm": ([_P, _I64, _I64, _I64] * 2 + [_INT, _I64, _I64, _P, _P, _INT, _F64, _P, _I64, _I64, _P, _P, _I64, _INT] +
+                    [_P, _I64, _I64] * 2 + [_P], _INT),
+    "det_qk_norm_bwd_workspace_size": ([_I64] * 4 + [ctypes.POINTER(_SZ)], _INT),
+    "det_qk_norm_bwd": ([_P, _I64, _I64] * 2 + [_P, _I64, _I64, _I64] * 2 +
+                        [_INT, _I64, _I64, _P, _P, _INT, _F64, _P, _I64, _I64, _P, _P, _I64, _INT] + [_P, _I64, _I64] * 2 +
+                        [_P, _P, _P, _SZ, _P], _INT),
 }
 
 _lib = None
@@ -799,3 +821,201 @@ def det_block_norm_bwd(dy, x, f, dx, df, dh=None, gate=None, w_post=None, alpha=
     need = 0 if w_post is None and alpha is None and w_pre is None else det_block_norm_bwd_workspace_size(T, D)
     wp, wn, keep = _scratch(c, need, ws, dev, stream, raw)
     _run(c, dev, lib().det_block_norm_bwd, *args, wp, wn, raw)
+
+
+# ----------------------------------------------- gated delta rule, query and key norms
+def _heads(t, name: str, shape, dtype, dev: int):
+    """Check a [T, heads, dim] tensor with unit innermost stride; return its address, token and head strides."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
+        st = t.stride()
+        if st[2] == 1 or shape[2] <= 1:
+            return t.data_ptr(), st[0], st[1]
+    _bad(t, name, shape, dtype, dev, "have unit innermost stride")
+
+
+def _delta_operands(c, q, k, v, g, beta):
+    code = _code(c, q, "q")
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("need q, k [T, Hk, dk] and v [T, H, dv]")
+    T, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    dt, dev = q.dtype, q.get_device()
+    return dev, (T, Hk, H, dk, dv), (*_heads(q, "q", q.shape, dt, dev), *_heads(k, "k", (T, Hk, dk), dt, dev),
+                                     *_heads(v, "v", (T, H, dv), dt, dev), *_rows(g, "g", (T, H), c.f32, dev),
+                                     *_rows(beta, "beta", (T, H), dt, dev), code, T, Hk, H, dk, dv)
+
+
+def _delta_offs(c, offs, dev: int):
+    if offs.dim() != 1 or offs.shape[0] < 1:
+        raise ValueError("need offs [S + 1]")
+    S = offs.shape[0] - 1
+    return S, _flat(offs, "offs", (S + 1,), c.i32, dev)
+
+
+@functools.lru_cache(maxsize=256)
+def _delta_chunks(T: int, S: int, code: int) -> int:
+    n = _I64()
+    _check(lib().det_delta_rule_chunks(T, S, code, ctypes.byref(n)))
+    return n.value
+
+
+def det_delta_rule_states_shape(q, v, offs):
+    """The shape [chunks, H, dk, dv] of det_delta_rule's states for these q [T, Hk, dk], v [T, H, dv], offs [S + 1]."""
+    return (_delta_chunks(q.shape[0], offs.shape[0] - 1, _code(_context(), q, "q")), v.shape[1], q.shape[2], v.shape[2])
+
+
+@functools.lru_cache(maxsize=256)
+def det_delta_rule_workspace_size(T: int, S: int, H: int, dtype_code: int) -> int:
+    n = _SZ()
+    _check(lib().det_delta_rule_workspace_size(T, S, H, dtype_code, ctypes.byref(n)))
+    return n.value
+
+
+def det_delta_rule(q, k, v, g, beta, o, offs, initial_state=None, final_state=None, states=None, scale=None, ws=None,
+                   stream=None) -> None:
+    """o = the gated delta rule over the sequences offs[s] <= t < offs[s + 1]: S' = exp(g) S, u = beta (v - S'^T k),
+    S = S' + k u^T, o = scale S^T q. q, k bf16 or float32 [T, Hk, dk], v, o [T, H, dv], g float32 [T, H], beta [T, H],
+    offs int32 [S + 1]; initial_state (default: zeros) and final_state float32 [S, H, dk, dv]; states float32 of
+    det_delta_rule_states_shape(), for the backward; scale defaults to dk ** -0.5. Overwrites o, final_state, states."""
+    c = _context()
+    dev, (T, Hk, H, dk, dv), x = _delta_operands(c, q, k, v, g, beta)
+    S, po = _delta_offs(c, offs, dev)
+    code, sh = x[-6], (S, H, dk, dv)
+    p = (_flat(initial_state, "initial_state", sh, c.f32, dev), *_heads(o, "o", (T, H, dv), q.dtype, dev),
+         _flat(final_state, "final_state", sh, c.f32, dev),
+         None if states is None else _flat(states, "states", (_delta_chunks(T, S, code), H, dk, dv), c.f32, dev))
+    raw = _stream_on(c, dev, stream)
+    wp, wn, keep = _scratch(c, det_delta_rule_workspace_size(T, S, H, code), ws, dev, stream, raw)
+    _run(c, dev, lib().det_delta_rule, *x, po, S, max(dk, 1) ** -0.5 if scale is None else scale, *p, wp, wn, raw)
+
+
+@functools.lru_cache(maxsize=256)
+def det_delta_rule_bwd_workspace_size(T: int, S: int, H: int, dk: int, dv: int, dtype_code: int) -> int:
+    n = _SZ()
+    _check(lib().det_delta_rule_bwd_workspace_size(T, S, H, dk, dv, dtype_code, ctypes.byref(n)))
+    return n.value
+
+
+def det_delta_rule_bwd(do, q, k, v, g, beta, offs, states, dq, dk, dv, dg, dbeta, dfinal_state=None, dinitial_state=None,
+                       scale=None, ws=None, stream=None) -> None:
+    """The gradients of det_delta_rule from do and dfinal_state (default: zeros), with the states its forward left:
+    overwrites dq, dk, dv (shapes and type of q, k, v), dg, dbeta ([T, H], the type of q) and dinitial_state (float32
+    [S, H, dk, dv]). scale as in the forward."""
+    c = _context()
+    dev, (T, Hk, H, nk, nv), x = _delta_operands(c, q, k, v, g, beta)
+    S, po = _delta_offs(c, offs, dev)
+    code, sh, dt = x[-6], (S, H, nk, nv), q.dtype
+    po3 = _heads(do, "do", (T, H, nv), dt, dev)
+    p = (_flat(states, "states", (_delta_chunks(T, S, code), H, nk, nv), c.f32, dev),
+         _flat(dfinal_state, "dfinal_state", sh, c.f32, dev), *_heads(dq, "dq", (T, Hk, nk), dt, dev),
+         *_heads(dk, "dk", (T, Hk, nk), dt, dev), *_heads(dv, "dv", (T, H, nv), dt, dev), *_rows(dg, "dg", (T, H), dt, dev),
+         *_rows(dbeta, "dbeta", (T, H), dt, dev), _flat(dinitial_state, "dinitial_state", sh, c.f32, dev))
+    raw = _stream_on(c, dev, stream)
+    wp, wn, keep = _scratch(c, det_delta_rule_bwd_workspace_size(T, S, H, nk, nv, code), ws, dev, stream, raw)
+    _run(c, dev, lib().det_delta_rule_bwd, *po3, *x, po, S, max(nk, 1) ** -0.5 if scale is None else scale, *p, wp, wn, raw)
+
+
+def det_delta_rule_step(q, k, v, g, beta, state, o, slots=None, scale=None, stream=None) -> None:
+    """One token per row through the gated delta rule (see det_delta_rule), against the cache state float32
+    [N, H, dk, dv], updated in place: row b uses state[slots[b]] (slots int32 [B]; None: state[b]). Rows with a slot
+    outside [0, N) touch no state and get zeros; rows with one slot are taken in order. Overwrites o [B, H, dv]."""
+    c = _context()
+    dev, (B, Hk, H, dk, dv), x = _delta_operands(c, q, k, v, g, beta)
+    if state.dim() != 4:
+        raise ValueError("state must be [N, H, dk, dv]")
+    N = state.shape[0]
+    p = (_flat(state, "state", (N, H, dk, dv), c.f32, dev), N, _flat(slots, "slots", (B,), c.i32, dev),
+         *_heads(o, "o", (B, H, dv), q.dtype, dev))
+    raw = _stream_on(c, dev, stream)
+    _run(c, dev, lib().det_delta_rule_step, *x, max(dk, 1) ** -0.5 if scale is None else scale, *p, raw)
+
+
+_NORMS = {"none": 0, "rms": 1, "l2": 2}
+_PAIRS = {"halves": 0, "neighbours": 1}
+
+
+def _qk_operands(c, q, k, names):
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("need %s or %s" % names)
+    if any(t is not None and t.dim() != 3 for t in (q, k)):
+        raise ValueError("%s and %s must be [T, heads, D]" % names)
+    return one, one.shape[0], one.shape[2], one.dtype, _code(c, one, names[0]), one.get_device()
+
+
+def _side(t, name: str, like, T, D, dt, dev):
+    """Address, strides of one of the four q or k tensors of a call, which is there exactly when `like` is."""
+    if like is None:
+        if t is not None:
+            raise ValueError("%s is given without its input" % name)
+        return None, 0, 0
+    if t is None:
+        raise ValueError("%s is missing" % name)
+    return _heads(t, name, (T, like.shape[1], D), dt, dev)
+
+
+def _rotation(c, pos, inv_freq, axis, T: int, dev: int):
+    if (pos is None) != (inv_freq is None):
+        raise ValueError("pos and inv_freq go together")
+    if pos is None:
+        if axis is not None:
+            raise ValueError("axis is given without pos")
+        return None, 0, 0, None, None, 0
+    if inv_freq.dim() != 1 or pos.dim() not in (1, 2):
+        raise ValueError("need pos [T] or [axes, T] and inv_freq [R / 2]")
+    half, A = inv_freq.shape[0], 1 if pos.dim() == 1 else pos.shape[0]
+    pp, ld = (_flat(pos, "pos", (T,), c.i32, dev), T) if pos.dim() == 1 else _rows(pos, "pos", (A, T), c.i32, dev)
+    if A != 1 and axis is None:
+        raise ValueError("several axes need the axis of every pair")
+    return (pp, ld, A, _flat(inv_freq, "inv_freq", (half,), c.f32, dev), _flat(axis, "axis", (half,), c.i32, dev), 2 * half)
+
+
+def _choice(table, value, name: str) -> int:
+    if value not in table:
+        raise ValueError("%s must be one of %s, got %r" % (name, ", ".join(map(repr, table)), value))
+    return table[value]
+
+
+def det_qk_norm(q, k, q_out, k_out, w_q=None, w_k=None, norm: str = "rms", eps: float = 1e-6, pos=None, inv_freq=None,
+                axis=None, pairs: str = "halves", stream=None) -> None:
+    """q_out, k_out = the heads of q [T, Hq, D] and k [T, Hk, D] (bf16 or float32; either may be None) under the norm
+    "rms", "l2" (unit length) or "none", times w_q, w_k (float32 [D] or None), with the first 2 * len(inv_freq) channels
+    turned in pairs by pos * inv_freq. pos int32 [T] or [axes, T], inv_freq float32 [R / 2], axis int32 [R / 2]: the axis
+    of every pair; pairs "halves": (p, p + R / 2), "neighbours": (2p, 2p + 1)."""
+    c = _context()
+    one, T, D, dt, code, dev = _qk_operands(c, q, k, ("q", "k"))
+    xq, xk = _side(q, "q", q, T, D, dt, dev), _side(k, "k", k, T, D, dt, dev)
+    Hq, Hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    rot = _rotation(c, pos, inv_freq, axis, T, dev)
+    args = (*xq, Hq, *xk, Hk, code, T, D, _flat(w_q, "w_q", (D,), c.f32, dev), _flat(w_k, "w_k", (D,), c.f32, dev),
+            _choice(_NORMS, norm, "norm"), eps, *rot, _choice(_PAIRS, pairs, "pairs"),
+            *_side(q_out, "q_out", q, T, D, dt, dev), *_side(k_out, "k_out", k, T, D, dt, dev))
+    raw = _stream_on(c, dev, stream)
+    _run(c, dev, lib().det_qk_norm, *args, raw)
+
+
+@functools.lru_cache(maxsize=256)
+def det_qk_norm_bwd_workspace_size(T: int, Hq: int, Hk: int, D: int) -> int:
+    n = _SZ()
+    _check(lib().det_qk_norm_bwd_workspace_size(T, Hq, Hk, D, ctypes.byref(n)))
+    return n.value
+
+
+def det_qk_norm_bwd(dq_out, dk_out, q, k, dq, dk, w_q=None, w_k=None, dw_q=None, dw_k=None, norm: str = "rms",
+                    eps: float = 1e-6, pos=None, inv_freq=None, axis=None, pairs: str = "halves", ws=None,
+                    stream=None) -> None:
+    """The gradients of det_qk_norm from those of its outputs, with the forward's inputs and arguments: overwrites dq and
+    dk, accumulates dw_q and dw_k (float32 [D], each given exactly when its weights are) in a fixed order."""
+    c = _context()
+    one, T, D, dt, code, dev = _qk_operands(c, q, k, ("q", "k"))
+    Hq, Hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    rot = _rotation(c, pos, inv_freq, axis, T, dev)
+    args = (*_side(dq_out, "dq_out", q, T, D, dt, dev), *_side(dk_out, "dk_out", k, T, D, dt, dev),
+            *_side(q, "q", q, T, D, dt, dev), Hq, *_side(k, "k", k, T, D, dt, dev), Hk, code, T, D,
+            _flat(w_q, "w_q", (D,), c.f32, dev), _flat(w_k, "w_k", (D,), c.f32, dev), _choice(_NORMS, norm, "norm"), eps,
+            *rot, _choice(_PAIRS, pairs, "pairs"), *_side(dq, "dq", q, T, D, dt, dev), *_side(dk, "dk", k, T, D, dt, dev),
+            _flat(dw_q, "dw_q", (D,), c.f32, dev), _flat(dw_k, "dw_k", (D,), c.f32, dev))
+    raw = _stream_on(c, dev, stream)
+    need = 0 if w_q is None and w_k is None else det_qk_norm_bwd_workspace_size(T, Hq, Hk, D)
+    wp, wn, keep = _scratch(c, need, ws, dev, stream, raw)
+    _run(c, dev, lib().det_qk_norm_bwd, *args, wp, wn, raw)

@@ -7,10 +7,11 @@
  * (Megatron-LM PR #8244, description; cudnn-frontend PR #521, first commit).
  * Every accumulating reduction takes an `atomic` flag: 0 runs the deterministic
  * route, 1 runs the non-deterministic comparison route that adds the same tile
- * partials into the output with hardware float atomics. The losses and norms of
- * a training step (det_router_balance, det_topk_distill, det_block_norm and
- * their _bwd calls) have the deterministic route only; their sums have one
- * order too, and their outputs are overwritten but for the parameter gradients.
+ * partials into the output with hardware float atomics. The losses, norms and
+ * token mixers of a step (det_router_balance, det_topk_distill, det_block_norm,
+ * det_delta_rule, det_qk_norm and their _bwd and _step calls) have the
+ * deterministic route only; their sums have one order too, and their outputs are
+ * overwritten but for the parameter gradients.
  *
  * Conventions for every entry point
  * ---------------------------------
@@ -69,6 +70,10 @@ typedef enum {
 typedef enum { DET_BF16 = 0, DET_F32 = 1 } det_dtype;
 
 typedef enum { DET_SCORE_SOFTMAX = 0, DET_SCORE_SIGMOID = 1 } det_score;
+
+typedef enum { DET_NORM_NONE = 0, DET_NORM_RMS = 1, DET_NORM_L2 = 2 } det_norm;
+
+typedef enum { DET_PAIRS_HALVES = 0, DET_PAIRS_NEIGHBOURS = 1 } det_pairs;
 
 /* ABI version of the loaded library (DET_ABI_VERSION). */
 int det_abi_version(void);
@@ -549,6 +554,126 @@ int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t dh
                        const float* rstd_pre, int dtype, int64_t T, int64_t D, void* dx, int64_t dx_ld, void* df,
                        int64_t df_ld, void* dgate, int64_t dgate_ld, float* dw_post, float* dalpha, float* dw_pre,
                        void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * det_delta_rule: the gated delta rule over a packed batch, the recurrence whose
+ * log decays g the gate makes and whose backward makes the dg that det_colsum
+ * reduces. Per sequence and value head, with a state S [dk, dv]:
+ *
+ *   S' = exp(g[t]) S_{t-1},  u = beta[t] (v[t] - S'^T k[t]),  S_t = S' + k[t] u^T,  o[t] = scale S_t^T q[t]
+ *
+ * Sequence s owns the tokens [b_s, b_{s+1}), b = offs clamped to [0, T] and made
+ * non-decreasing (read on the device only); rows of o behind the last sequence are
+ * left as they were. Value head h uses key head h / (H / Hk). It starts from
+ * initial_state[s] (NULL: zeros) and leaves final_state[s] (unless NULL), also for an
+ * empty sequence. states (NULL: not written; needed for the backward) receives the
+ * state in front of every chunk of 64 tokens (DET_F32: 32), counted from each
+ * sequence's first: det_delta_rule_chunks() of [H, dk, dv], of which those past the
+ * last chunk are left as they were.
+ * Computed in chunks on the matrix cores with float32 sums and float32 states:
+ * inputs of DET_F32 and everything that reaches a state are carried in three bf16
+ * words (24 bits), the rest of a DET_BF16 call in two. Any g is allowed; below -1e4
+ * it counts as -1e4 (a decay of 0 either way), -inf included. The recurrence is as
+ * stable as its decays and keys are: with g <= 0, keys of length at most 1 and beta
+ * in [0, 2] no intermediate grows. NaN and infinities spread to what they touch
+ * (and to the rest of their chunk). Every sum has one order: the same bits from run
+ * to run.
+ *
+ * q, k: [T, Hk, dk], v, o: [T, H, dv] of dtype (DET_BF16 or DET_F32), strides of
+ *       tokens (_st) and heads (_sh) in elements: whole tokens that do not overlap
+ *       (a head stride inside the token's) or whole heads; they may start at any
+ *       element. dk, dv <= 128; H a multiple of Hk. g: [T, H] float32, beta: [T, H] of
+ *       dtype, row strides >= H.
+ * offs: [S + 1] int32, S <= 65535. initial_state, final_state: [S, H, dk, dv] float32.
+ * ws:   det_delta_rule_workspace_size() bytes; its header is neither read nor
+ *       written. o, final_state and states overlap nothing else.
+ * No atomic arm. */
+int det_delta_rule_chunks(int64_t T, int64_t S, int dtype, int64_t* chunks);
+int det_delta_rule_workspace_size(int64_t T, int64_t S, int64_t H, int dtype, size_t* bytes);
+int det_delta_rule(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh, const void* v,
+                   int64_t v_st, int64_t v_sh, const float* g, int64_t g_ld, const void* beta, int64_t beta_ld, int dtype,
+                   int64_t T, int64_t Hk, int64_t H, int64_t dk, int64_t dv, const int32_t* offs, int64_t S, double scale,
+                   const float* initial_state, void* o, int64_t o_st, int64_t o_sh, float* final_state, float* states,
+                   void* ws, size_t ws_bytes, void* stream);
+
+/* det_delta_rule_bwd: all gradients of det_delta_rule from d_o and dfinal_state (NULL:
+ * zeros), with the states that its forward left:
+ *
+ *   dq, dk (summed over the value heads of a key head, in order), dv, dg, dbeta and
+ *   dinitial_state (unless NULL)
+ *
+ * overwritten; rows behind the last sequence are left as they were. dq, dk, dv, dg
+ * and dbeta are of dtype (dg is what det_colsum takes next to an a of that type),
+ * dfinal_state and dinitial_state [S, H, dk, dv] float32. A token with g < -104, whose
+ * decay is 0, has dg = 0. dg, dbeta: [T, H], row strides >= H.
+ * ws: det_delta_rule_bwd_workspace_size() bytes; its header is neither read nor
+ *     written. */
+int det_delta_rule_bwd_workspace_size(int64_t T, int64_t S, int64_t H, int64_t dk, int64_t dv, int dtype, size_t* bytes);
+int det_delta_rule_bwd(const void* d_o, int64_t do_st, int64_t do_sh, const void* q, int64_t q_st, int64_t q_sh, const void* k,
+                       int64_t k_st, int64_t k_sh, const void* v, int64_t v_st, int64_t v_sh, const float* g, int64_t g_ld,
+                       const void* beta, int64_t beta_ld, int dtype, int64_t T, int64_t Hk, int64_t H, int64_t dk, int64_t dv,
+                       const int32_t* offs, int64_t S, double scale, const float* states, const float* dfinal_state,
+                       void* dq, int64_t dq_st, int64_t dq_sh, void* dk_out, int64_t dk_st, int64_t dk_sh, void* dv_out,
+                       int64_t dv_st, int64_t dv_sh, void* dg, int64_t dg_ld, void* dbeta, int64_t dbeta_ld,
+                       float* dinitial_state, void* ws, size_t ws_bytes, void* stream);
+
+/* det_delta_rule_step: one token per row of a batch (decoding), against a cache of
+ * N states that is updated in place: row b takes det_delta_rule's step from
+ * state[slots[b]] and leaves it there. slots NULL: row b has state b (B <= N). Rows
+ * whose slot lies outside [0, N) (the padding of a batch) touch no state and get an o
+ * of zeros. Rows that name the same slot are tokens of one sequence, taken in row
+ * order. Float32 throughout but for the inputs and o.
+ * q, k: [B, Hk, dk], v, o: [B, H, dv], g, beta: [B, H], types and strides as above
+ * (each tensor in its own); state: [N, H, dk, dv] float32, contiguous; slots: [B] int32,
+ * B <= 65535. No workspace. */
+int det_delta_rule_step(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh, const void* v,
+                        int64_t v_st, int64_t v_sh, const float* g, int64_t g_ld, const void* beta, int64_t beta_ld,
+                        int dtype, int64_t B, int64_t Hk, int64_t H, int64_t dk, int64_t dv, double scale, float* state,
+                        int64_t N, const int32_t* slots, void* o, int64_t o_st, int64_t o_sh, void* stream);
+
+/* ------------------------------------------------------------------------
+ * det_qk_norm: the norm of every head of queries and keys, its weights and the
+ * rotation by position, in one pass:
+ *
+ *   n = w * x / sqrt(mean(x^2) + eps)     (DET_NORM_L2: the sum in place of the mean; DET_NORM_NONE: n = w * x)
+ *   y_a = n_a cos(t) - n_b sin(t),  y_b = n_b cos(t) + n_a sin(t),  t = pos[axis[p]][token] * inv_freq[p]
+ *
+ * over the pairs p < R / 2 of a head's channels: (p, p + R / 2) for
+ * DET_PAIRS_HALVES, (2p, 2p + 1) for DET_PAIRS_NEIGHBOURS; the channels from R on are
+ * not turned. In float32 (the angles float64), rounded once to dtype. An axis
+ * outside [0, axes) turns its pair by nothing.
+ *
+ * q, q_out: [T, Hq, D], k, k_out: [T, Hk, D] of dtype, strides as in det_delta_rule
+ *     (column ranges of one projection's output, say); D <= 1024, either may have no
+ *     heads (and NULL). w_q, w_k: [D] float32 or NULL (ones). pos: [axes, T] int32, row
+ *     stride pos_ld >= T (any values); inv_freq: [R / 2] float32; axis: [R / 2] int32,
+ *     NULL with one axis. R even, 0 for no rotation. Outputs are overwritten and
+ *     overlap no input and no other output. No workspace. */
+int det_qk_norm(const void* q, int64_t q_st, int64_t q_sh, int64_t Hq, const void* k, int64_t k_st, int64_t k_sh, int64_t Hk,
+                int dtype, int64_t T, int64_t D, const float* w_q, const float* w_k, int norm, double eps, const int32_t* pos,
+                int64_t pos_ld, int64_t axes, const float* inv_freq, const int32_t* axis, int64_t R, int pairs, void* q_out,
+                int64_t qo_st, int64_t qo_sh, void* k_out, int64_t ko_st, int64_t ko_sh, void* stream);
+
+/* det_qk_norm_bwd: all gradients of det_qk_norm from those of q_out and k_out, with the
+ * forward's inputs and arguments: with d the gradient of n (dy turned back), xh = x /
+ * sqrt(mean(x^2) + eps) and u = w d:
+ *
+ *   dx = (u - xh * mean(u * xh)) / sqrt(mean(x^2) + eps)   (DET_NORM_L2: the sum; DET_NORM_NONE: u)
+ *   dw_q, dw_k += sum over tokens and heads of d * xh
+ *
+ * dq, dk are overwritten; dw_q, dw_k ([D] float32, given exactly when w_q, w_k are)
+ * accumulate like every reduction here: a workgroup's rows in float32 in one order
+ * given by T, D and the heads, the workgroups' sums in one order in float64, the
+ * total rounded to float32 and added once.
+ * ws: det_qk_norm_bwd_workspace_size() bytes when w_q or w_k is given; its header is
+ *     neither read nor written. */
+int det_qk_norm_bwd_workspace_size(int64_t T, int64_t Hq, int64_t Hk, int64_t D, size_t* bytes);
+int det_qk_norm_bwd(const void* dq_out, int64_t dqo_st, int64_t dqo_sh, const void* dk_out, int64_t dko_st, int64_t dko_sh,
+                    const void* q, int64_t q_st, int64_t q_sh, int64_t Hq, const void* k, int64_t k_st, int64_t k_sh,
+                    int64_t Hk, int dtype, int64_t T, int64_t D, const float* w_q, const float* w_k, int norm, double eps,
+                    const int32_t* pos, int64_t pos_ld, int64_t axes, const float* inv_freq, const int32_t* axis, int64_t R,
+                    int pairs, void* dq, int64_t dq_st, int64_t dq_sh, void* dk, int64_t dk_st, int64_t dk_sh, float* dw_q,
+                    float* dw_k, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Diagnostics (tests only). det_detmath_eval evaluates the device versions of

@@ -132,8 +132,45 @@ MANIFEST = {
         "atomic": None,
         "graph": ["test_gpu_block_norm.py::test_graph_replays_and_two_streams"],
     },
+    "det_delta_rule": {
+        "cite": "the recurrence whose gate gradient Megatron-LM PR #8244 reduces (no page of its own)",
+        "replay": ["test_gpu_delta_rule.py::test_replay_under_load_with_poisoned_workspaces"],
+        "parity": ["test_gpu_delta_rule.py::test_lengths", "test_gpu_delta_rule.py::test_head_sizes"],
+        "atomic": None,
+        "graph": ["test_gpu_delta_rule.py::test_graph_replays_and_two_streams",
+                  "test_gpu_mixer_step.py::test_step_against_float64_and_in_a_graph"],
+    },
+    "det_delta_rule_bwd": {
+        "cite": "the source of the dg that Megatron-LM PR #8244 reduces (no page of its own)",
+        "replay": ["test_gpu_delta_rule.py::test_replay_under_load_with_poisoned_workspaces"],
+        "parity": ["test_gpu_delta_rule.py::test_lengths", "test_gpu_delta_rule.py::test_gradients_against_differences"],
+        "atomic": None,
+        "graph": ["test_gpu_delta_rule.py::test_graph_replays_and_two_streams"],
+    },
+    "det_delta_rule_step": {
+        "cite": "the recurrence for single tokens (no page)",
+        "replay": ["test_gpu_delta_rule.py::test_step_leaves_other_states_alone_and_replays"],
+        "parity": ["test_gpu_delta_rule.py::test_step_sizes", "test_gpu_delta_rule.py::test_prefill_then_tokens_is_one_longer_prefill"],
+        "atomic": None,
+        "graph": ["test_gpu_delta_rule.py::test_step_leaves_other_states_alone_and_replays"],
+    },
+    "det_qk_norm": {
+        "cite": "the norms in front of the recurrence and of attention (no page)",
+        "replay": ["test_gpu_qk_norm.py::test_replay_under_load_with_poisoned_workspaces"],
+        "parity": ["test_gpu_qk_norm.py::test_head_sizes"],
+        "atomic": None,
+        "graph": ["test_gpu_qk_norm.py::test_graph_replays_and_two_streams"],
+    },
+    "det_qk_norm_bwd": {
+        "cite": "the column sums of the gate page's pattern, for the norms' weights (no page)",
+        "replay": ["test_gpu_qk_norm.py::test_replay_under_load_with_poisoned_workspaces"],
+        "parity": ["test_gpu_qk_norm.py::test_head_sizes", "test_gpu_qk_norm.py::test_gradients_against_differences"],
+        "atomic": None,
+        "graph": ["test_gpu_qk_norm.py::test_graph_replays_and_two_streams"],
+    },
 }
 
 # declared functions that are sizes, set-up or diagnostics rather than accumulating entry points
 NOT_ENTRY_POINTS = {"det_abi_version", "det_last_error", "det_workspace_init", "det_index_add_bad_ids",
-                    "det_colsum_select_cfg", "det_detmath_eval", "det_mfma_eval", "det_mfma_rate"}
+                    "det_colsum_select_cfg", "det_detmath_eval", "det_mfma_eval", "det_mfma_rate",
+                    "det_delta_rule_chunks"}
