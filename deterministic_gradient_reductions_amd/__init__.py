@@ -150,10 +150,10 @@ _SIGS = {
     "det_block_norm_bwd": ([_P, _I64] * 5 + [_I64] + [_P] * 5 + [_INT, _I64, _I64] + [_P, _I64] * 3 +
                            [_P] * 4 + [_SZ, _P], _INT),
     "det_delta_rule_chunks": ([_I64, _I64, _INT, ctypes.POINTER(_I64)], _INT),
-    "det_delta_rule_workspace_size": ([_I64, _I64, _I64, _INT, ctypes.POINTER(_SZ)], _INT),
+    "det_delta_rule_workspace_size": ([_I64] * 6 + [_INT, ctypes.POINTER(_SZ)], _INT),
     "det_delta_rule": ([_P, _I64, _I64] * 3 + [_P, _I64] * 2 + [_INT] + [_I64] * 5 + [_P, _I64, _F64, _P, _P, _I64, _I64] +
                        [_P] * 3 + [_SZ, _P], _INT),
-    "det_delta_rule_bwd_workspace_size": ([_I64] * 5 + [_INT, ctypes.POINTER(_SZ)], _INT),
+    "det_delta_rule_bwd_workspace_size": ([_I64] * 6 + [_INT, ctypes.POINTER(_SZ)], _INT),
     "det_delta_rule_bwd": ([_P, _I64, _I64] * 4 + [_P, _I64] * 2 + [_INT] + [_I64] * 5 + [_P, _I64, _F64, _P, _P] +
                            [_P, _I64, _I64] * 3 + [_P, _I64] * 2 + [_P, _P, _SZ, _P], _INT),
     "det_delta_rule_step": ([_P, _I64, _I64] * 3 + [_P, _I64] * 2 + [_INT] + [_I64] * 5 + [_F64, _P, _I64, _P] +
@@ -865,9 +865,9 @@ def det_delta_rule_states_shape(q, v, offs):
 
 
 @functools.lru_cache(maxsize=256)
-def det_delta_rule_workspace_size(T: int, S: int, H: int, dtype_code: int) -> int:
+def det_delta_rule_workspace_size(T: int, S: int, Hk: int, H: int, dk: int, dv: int, dtype_code: int) -> int:
     n = _SZ()
-    _check(lib().det_delta_rule_workspace_size(T, S, H, dtype_code, ctypes.byref(n)))
+    _check(lib().det_delta_rule_workspace_size(T, S, Hk, H, dk, dv, dtype_code, ctypes.byref(n)))
     return n.value
 
 
@@ -885,14 +885,14 @@ def det_delta_rule(q, k, v, g, beta, o, offs, initial_state=None, final_state=No
          _flat(final_state, "final_state", sh, c.f32, dev),
          None if states is None else _flat(states, "states", (_delta_chunks(T, S, code), H, dk, dv), c.f32, dev))
     raw = _stream_on(c, dev, stream)
-    wp, wn, keep = _scratch(c, det_delta_rule_workspace_size(T, S, H, code), ws, dev, stream, raw)
+    wp, wn, keep = _scratch(c, det_delta_rule_workspace_size(T, S, Hk, H, dk, dv, code), ws, dev, stream, raw)
     _run(c, dev, lib().det_delta_rule, *x, po, S, max(dk, 1) ** -0.5 if scale is None else scale, *p, wp, wn, raw)
 
 
 @functools.lru_cache(maxsize=256)
-def det_delta_rule_bwd_workspace_size(T: int, S: int, H: int, dk: int, dv: int, dtype_code: int) -> int:
+def det_delta_rule_bwd_workspace_size(T: int, S: int, Hk: int, H: int, dk: int, dv: int, dtype_code: int) -> int:
     n = _SZ()
-    _check(lib().det_delta_rule_bwd_workspace_size(T, S, H, dk, dv, dtype_code, ctypes.byref(n)))
+    _check(lib().det_delta_rule_bwd_workspace_size(T, S, Hk, H, dk, dv, dtype_code, ctypes.byref(n)))
     return n.value
 
 
@@ -911,7 +911,7 @@ def det_delta_rule_bwd(do, q, k, v, g, beta, offs, states, dq, dk, dv, dg, dbeta
          *_heads(dk, "dk", (T, Hk, nk), dt, dev), *_heads(dv, "dv", (T, H, nv), dt, dev), *_rows(dg, "dg", (T, H), dt, dev),
          *_rows(dbeta, "dbeta", (T, H), dt, dev), _flat(dinitial_state, "dinitial_state", sh, c.f32, dev))
     raw = _stream_on(c, dev, stream)
-    wp, wn, keep = _scratch(c, det_delta_rule_bwd_workspace_size(T, S, H, nk, nv, code), ws, dev, stream, raw)
+    wp, wn, keep = _scratch(c, det_delta_rule_bwd_workspace_size(T, S, Hk, H, nk, nv, code), ws, dev, stream, raw)
     _run(c, dev, lib().det_delta_rule_bwd, *po3, *x, po, S, max(nk, 1) ** -0.5 if scale is None else scale, *p, wp, wn, raw)
 
 

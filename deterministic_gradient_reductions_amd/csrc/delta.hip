@@ -14,34 +14,93 @@
 // float32 sum over a chunk would lose (two words). g below -1e4 counts as -1e4 (a
 // factor of 0 either way), which keeps -inf out of the differences.
 //
-// Two kernels. The first, all chunks side by side, inverts I + M B (a wave per
-// chunk and head: 16 x 16 diagonal blocks by substitution, the blocks below by
-// float32 matrix instructions). The second walks the chunks of one sequence and
-// value head in order; a wave owns 16 columns of v, so its part of S, R, N, U and O
-// depends on no other wave, and what one product leaves in its registers is the next
-// one's operand. The waves of a workgroup share the fragments of K, Q, K^T, the
-// inverse and P in LDS.
+// Three kernels. Two work on all chunks side by side: one turns K (the backward: Q too)
+// so that tokens are neighbours, and copies what is not of bf16 in whole 16-byte
+// rows; one forms P and the inverse of I + M B (a wave per chunk and head: 16 x 16
+// diagonal blocks by substitution, the blocks below by float32 matrix
+// instructions) and leaves both as fragments. The third walks the chunks of one
+// sequence and value head in order. There a wave owns 16 columns of v, so its part of
+// S, N, U and O depends on no other wave, what one product leaves in its registers is
+// the next one's operand, and the other operands are fragments of 16 bytes per lane,
+// shared by the workgroup through LDS. What is not on the chain of states is formed
+// before it.
 #include "delta.hpp"
 
 namespace detgrad {
 namespace {
 
-// exp(hi + lo) of a difference of two-word sums
-__device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
-  return exp_e((hi_i - hi_j) + (lo_i - lo_j));
+// ------------------------------------------------------------------ turn and copy
+// Workgroup (tile, head): the chunk's rows of x, turned into an image with rows d and
+// places t (`turned`, unless NULL) and copied into padded words (`rows`, unless NULL).
+template <typename T, int DIM>
+__global__ __launch_bounds__(256) void delta_turn_kernel(DeltaSizes z, Heads<const T> x, int heads, int dim,
+                                                         uint16_t* __restrict__ turned, uint16_t* __restrict__ rows) {
+  constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC, KC = C / 32;
+  const uint32_t tile = blockIdx.x;
+  const int h = blockIdx.y;
+  int e;
+  uint32_t r0, r1, s0, s1;
+  if (!segment_tile<1>(z.offs, z.S, static_cast<uint32_t>(z.T), kLogC, tile, e, r0, r1, s0, s1)) return;
+  const int n = static_cast<int>(r1 - r0);
+  const bool whole = dim % 4 == 0;
+  constexpr int kSize = C * DIM * kIn;
+  if (turned) turned += (static_cast<int64_t>(tile) * heads + h) * kSize;
+  for (int id = threadIdx.x; id < C * DIM / 16; id += 256) {
+    const int t = id / (DIM / 4) * 4, d = id % (DIM / 4) * 4;
+    f32x4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = load4(x.row(r0 + (t + j < n ? t + j : 0), h), d, dim, whole);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = t + j < n ? v[j] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    bf16x4 w[kIn][4];  // of row j, then of column j
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        __bf16 y[kIn];
+        split<kIn>(v[j][i], y);
+#pragma unroll
+        for (int p = 0; p < kIn; ++p) w[p][j][i] = y[p];
+      }
+    if (rows)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (t + j < n)
+#pragma unroll
+          for (int p = 0; p < kIn; ++p)
+            __builtin_memcpy(rows + ((static_cast<int64_t>(r0 + t + j) * heads + h) * kIn + p) * DIM + d, &w[p][j], 8);
+    if (turned)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint16_t* to = turned + image_at<KC, kIn>(d + i, t);
+#pragma unroll
+        for (int p = 0; p < kIn; ++p) {
+          const bf16x4 u = {w[p][0][i], w[p][1][i], w[p][2][i], w[p][3][i]};
+          __builtin_memcpy(to + p * kFragElems, &u, 8);
+        }
+      }
+  }
 }
 
+// ------------------------------------------------------------- inverse, P and gates
 constexpr int kPrepWaves = 4;
 
-template <typename T, int DK>
-__global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(DeltaSizes z, Heads<const T> k,
+struct PrepOut {
+  float* gates;
+  uint16_t *inverse, *inverse_t, *p;
+};
+
+// BWD: the inverse's image of both triangles and P transposed (rows j, places i), in the
+// words of the states; else the inverse's and P's of the lower one (rows i, places j).
+template <typename T, int DK, bool BWD>
+__global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSizes z, Rows k, Rows q,
                                                                      const float* __restrict__ g, int64_t g_ld,
                                                                      const T* __restrict__ beta, int64_t beta_ld,
-                                                                     float* __restrict__ inverse, float* __restrict__ gates,
-                                                                     int64_t units) {
-  constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC, RT = C / 16, KS = DK / 32;
+                                                                     PrepOut out, int64_t units) {
+  constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC, RT = C / 16, KC = C / 32, KS = DK / 32;
+  constexpr int kW = kStateWords, kP = BWD ? kStateWords : DeltaType<T>::kOut, kFrags = KC * (KC + 1);
   constexpr int kLd = C + 4;  // 16-byte rows whose starts move through the banks
-  __shared__ float lds[kPrepWaves][C * kLd + 3 * C];
+  __shared__ __align__(16) float lds[kPrepWaves][C * kLd + 3 * C];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kPrepWaves + wave;
   if (unit >= units) return;
@@ -70,59 +129,94 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(DeltaSizes 
     }
     const double last = __shfl(G, C - 1);
     const float h0 = static_cast<float>(G), h1 = static_cast<float>(G - h0);
-    float* out = gates + unit * (kGateRows * C);
+    const float eg = exp_e(h0) * (1.0f + h1), end = __shfl(eg, C - 1);
+    float* to = out.gates + unit * (kGateRows * C);
     if (lane < C) {
       hi[lane] = h0;
       lo[lane] = h1;
       be[lane] = b;
-      out[kGHi * C + lane] = h0;
-      out[kGLo * C + lane] = h1;
-      out[kEG * C + lane] = exp_e(h0) * (1.0f + h1);
+      to[kGHi * C + lane] = h0;
+      to[kGLo * C + lane] = h1;
+      to[kEG * C + lane] = lane < n ? eg : 0.0f;
       const double rest = last - G;
       const float q0 = static_cast<float>(rest);
-      out[kRest * C + lane] = exp_e(q0) * (1.0f + static_cast<float>(rest - q0));
-      out[kBeta * C + lane] = b;
+      to[kRest * C + lane] = exp_e(q0) * (1.0f + static_cast<float>(rest - q0));
+      to[kBeta * C + lane] = b;
+      to[kEnd * C + lane] = end;
     }
   }
   wave_fence();
 
-  // K K^T: fragments straight from memory, eight channels 32 ks + 8 lg .. in a lane
-  f32x4 kk[RT][RT] = {};
+  // K K^T and Q K^T: rows j and columns i (BWD: rows i and columns j)
+  f32x4 kk[RT][RT] = {}, qk[RT][RT] = {};
+  {
+    const uint16_t *pk = k.from(r0, hk), *pq = q.from(r0, hk);
+    uint32_t ok[RT], oq[RT];
 #pragma unroll
-  for (int ks = 0; ks < KS; ++ks) {
-    Frag<kIn> f[RT];
-    const int d = 32 * ks + 8 * lg;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int t = 16 * rt + c;
-      float v[8] = {};
-      if (t < n && d < z.dk) load8(k.row(r0 + t, hk) + d, z.dk - d, 0.0f, v);
-      f[rt] = frag_of<kIn>(f32x4{v[0], v[1], v[2], v[3]}, f32x4{v[4], v[5], v[6], v[7]});
+    for (int i = 0; i < RT; ++i) {
+      const int t = rho(i, c), row = t < n ? t : n - 1;
+      ok[i] = k.lane_off(row);
+      oq[i] = q.lane_off(row);
     }
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int ks = 0; ks < KS; ++ks) {
+      Frag<kIn> fk[RT], fq[RT];
 #pragma unroll
-      for (int j = 0; j <= i; ++j) mm<kIn>(kk[i][j], f[i], f[j]);
+      for (int i = 0; i < RT; ++i) {
+        fk[i] = k.frag<kIn>(pk, ok[i], ks);
+        fq[i] = q.frag<kIn>(pq, oq[i], ks);
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < RT && j / 2 <= i / 2; ++j) {
+          if (BWD) {
+            mm<kIn>(kk[i][j], fk[i], fk[j]);
+            mm<kIn>(qk[i][j], fq[i], fk[j]);
+          } else {
+            mm<kIn>(kk[i][j], fk[j], fk[i]);
+            mm<kIn>(qk[i][j], fk[j], fq[i]);
+          }
+        }
+    }
   }
-  // M B into LDS, rows i, columns j < i
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int j = 0; j <= i; ++j) {
-      const int col = 16 * j + c;
-      const float hj = hi[col], lj = lo[col], bj = be[col];
+    for (int j = 0; j < RT && j / 2 <= i / 2; ++j) {
+      const int col = rho(BWD ? j : i, c), row0 = rho(BWD ? i : j, 4 * lg);
+      const float hc = hi[col], lc = lo[col], bc = be[col];
+      f32x4 m;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * i + 4 * lg + r;
-        a[row * kLd + col] = col < row ? kk[i][j][r] * decay(hi[row], lo[row], hj, lj) * bj : 0.0f;
+        const int row = row0 + r, ti = BWD ? row : col, tj = BWD ? col : row;
+        const float d = BWD ? decay(hi[row], lo[row], hc, lc) : decay(hc, lc, hi[row], lo[row]);
+        m[r] = tj < ti ? kk[i][j][r] * d * (BWD ? bc : be[row]) : 0.0f;
+        qk[i][j][r] = tj <= ti && ti < n ? qk[i][j][r] * d * z.scale : 0.0f;
+      }
+      if (BWD) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[(row0 + r) * kLd + col] = m[r];
+      } else {
+        *reinterpret_cast<f32x4*>(a + col * kLd + row0) = m;
       }
     }
+  {
+    uint16_t* to = out.p + unit * (kFrags * kP * kFragElems);
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int m = 0; m < KC; ++m) {
+        if (BWD && m >= i / 2) image_put<kP>(to, upper_frag<KC>(i, m), frag_of<kP>(qk[2 * m][i], qk[2 * m + 1][i]));
+        if (!BWD && m <= i / 2) image_put<kP>(to, lower_frag(i, m), frag_of<kP>(qk[i][2 * m], qk[i][2 * m + 1]));
+      }
+  }
   wave_fence();
 
   // The inverses of the diagonal blocks: lane group lg takes block lg, lane c its
   // column c, by substitution down the rows.
-  float x[16];
   {
+    float x[16];
     const int blk = lg < RT ? lg : 0;
     const float* p = a + (16 * blk) * kLd + 16 * blk;
 #pragma unroll
@@ -132,8 +226,8 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(DeltaSizes 
       for (int m = 0; m < r; m += 4) {
         const f32x4 w = *reinterpret_cast<const f32x4*>(p + r * kLd + m);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (m + q < r) s = __builtin_fmaf(-w[q], x[m + q], s);
+        for (int u = 0; u < 4; ++u)
+          if (m + u < r) s = __builtin_fmaf(-w[u], x[m + u], s);
       }
       x[r] = s;
     }
@@ -141,15 +235,20 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(DeltaSizes 
     if (lg < RT)
 #pragma unroll
       for (int r = 0; r < 16; ++r) a[(16 * blk + r) * kLd + 16 * blk + c] = x[r];
+    // above the diagonal inside the fragments of 32 places
+#pragma unroll
+    for (int m = 0; m < KC; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) a[(32 * m + 4 * lg + r) * kLd + 32 * m + 16 + c] = 0.0f;
   }
   wave_fence();
 
   // The blocks below, column by column of blocks: X_ij = -X_ii sum_{j <= m < i} (M B)_im X_mj.
-  // Float32 matrix instructions; the place 4 lg + s of the sum is step s of lane group lg.
+  // Float32 matrix instructions; the place 4 lg + s of the sum is step s of lane group
+  // lg. A column of blocks is read no more once it is done, and X takes its place.
   const auto row4 = [&](int i, int j) { return *reinterpret_cast<const f32x4*>(a + (16 * i + c) * kLd + 16 * j + 4 * lg); };
-  float* out = inverse + unit * (C * C);
 #pragma unroll
-  for (int j = 0; j < RT; ++j) {
+  for (int j = 0; j < RT - 1; ++j) {
     f32x4 X[RT];
 #pragma unroll
     for (int r = 0; r < 4; ++r) X[j][r] = a[(16 * j + 4 * lg + r) * kLd + 16 * j + c];
@@ -167,287 +266,277 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(DeltaSizes 
       for (int s = 0; s < 4; ++s) y = __builtin_amdgcn_mfma_f32_16x16x4f32(-u[s], w[s], y, 0, 0, 0);
       X[i] = y;
     }
+    wave_fence();
 #pragma unroll
-    for (int i = j; i < RT; ++i)
+    for (int i = j + 1; i < RT; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) out[(16 * i + 4 * lg + r) * C + 16 * j + c] = X[i][r];
+      for (int r = 0; r < 4; ++r) a[(16 * i + 4 * lg + r) * kLd + 16 * j + c] = X[i][r];
   }
-}
-
-// What the chunk kernel takes and gives.
-template <typename T>
-struct FwdArgs {
-  Heads<const T> q, k, v;
-  Heads<T> o;
-  const float *inverse, *gates, *s0;
-  float *s1, *states;
-};
-
-// Workgroup (x, s): value head x / n_blocks, columns 16 NW (x % n_blocks) .. of sequence s.
-template <typename T, int DK, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T> A, int n_blocks) {
-  constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
-  constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
-  using RowImg = Image<RT, KD, kIn>;   // rows t, places d
-  using ColImg = Image<DT, KC, kIn>;   // rows d, places t
-  using InvImg = Image<RT, KC, kW>;    // rows i, places j
-  using PImg = Image<RT, KC, kOut>;    // rows i, places j
-  constexpr int kK = 0, kQ = kK + RowImg::kBytes, kKT = kQ + RowImg::kBytes, kInv = kKT + ColImg::kBytes,
-                kP = kInv + InvImg::kBytes, kG = kP + PImg::kBytes, kAll = kG + kGateRows * C * 4;
-  __shared__ __align__(16) char lds[kAll];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
-  const int h = blockIdx.x / n_blocks, hk = h / (z.H / z.Hk), v0 = ((blockIdx.x % n_blocks) * NW + wave) * 16;
-  const int s = blockIdx.y;
-  const float* gate = reinterpret_cast<const float*>(lds + kG);
-  uint32_t r0, r1, first;
-  segment_rows(z.offs, s, static_cast<uint32_t>(z.T), kLogC, r0, r1, first);
-
-  // tiles of the images above the diagonal stay zero
-  for (int i = threadIdx.x * 16; i < kG - kInv; i += 64 * NW * 16) *reinterpret_cast<u32x4*>(lds + kInv + i) = u32x4{0, 0, 0, 0};
-
-  // the state's rows 16 i + 4 lg + r, column v0 + c
-  const int col = v0 + c;
-  const bool live = col < z.dv;
-  const int64_t size = static_cast<int64_t>(z.dk) * z.dv, of = (static_cast<int64_t>(s) * z.H + h) * size;
-  f32x4 S[DT];
-#pragma unroll
-  for (int i = 0; i < DT; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int d = 16 * i + 4 * lg + r;
-      S[i][r] = A.s0 && live && d < z.dk ? A.s0[of + static_cast<int64_t>(d) * z.dv + col] : 0.0f;
-    }
-  const auto write_state = [&](float* p) {
-#pragma unroll
-    for (int i = 0; i < DT; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int d = 16 * i + 4 * lg + r;
-        if (live && d < z.dk) p[static_cast<int64_t>(d) * z.dv + col] = S[i][r];
-      }
-  };
-
-  // What a thread brings from memory for a chunk: blocks of four tokens by four channels
-  // of K and Q, of four by four of the inverse, gates, and its own elements of V.
-  constexpr int kThreads = 64 * NW, kRowBlocks = C * DK / 16, kInvBlocks = C * C / 16;
-  constexpr int kNB = (kRowBlocks + kThreads - 1) / kThreads, kNI = (kInvBlocks + kThreads - 1) / kThreads;
-  constexpr int kNG = (kGateRows * C + kThreads - 1) / kThreads;
-  Raw4<T> rk[kNB][4], rq[kNB][4];
-  f32x4 ri[kNI][4];
-  float rg[kNG];
-  T rv[RT][4];
-  const auto fetch = [&](uint32_t t0, int64_t unit) {
-    const int n = r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C;
-#pragma unroll
-    for (int b = 0; b < kNB; ++b) {
-      const int id = b * kThreads + threadIdx.x, t = id / (DK / 4) * 4, d = id % (DK / 4) * 4;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = id < kRowBlocks && t + j < n ? z.dk - d : 0;
-        const int64_t row = m > 0 ? t0 + t + j : t0;
-        rk[b][j].load(A.k.row(row, hk) + d, m);
-        rq[b][j].load(A.q.row(row, hk) + d, m);
-      }
-    }
-    const float* inv = A.inverse + unit * (C * C);
-#pragma unroll
-    for (int b = 0; b < kNI; ++b) {
-      const int id = b * kThreads + threadIdx.x, i = id / (C / 4) * 4, j = id % (C / 4) * 4;
-      if (id < kInvBlocks && j / 16 <= i / 16)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) ri[b][r] = *reinterpret_cast<const f32x4*>(inv + (i + r) * C + j);
-    }
-#pragma unroll
-    for (int b = 0; b < kNG; ++b) {
-      const int id = b * kThreads + threadIdx.x;
-      if (id < kGateRows * C) rg[b] = A.gates[unit * (kGateRows * C) + id];
-    }
+  wave_fence();
+  {
+    uint16_t* to = out.inverse + unit * (kFrags * kW * kFragElems);
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * i + 4 * lg + r;
-        rv[i][r] = live && t < n ? A.v.row(t0 + t, h)[col] : T{};
+      for (int m = 0; m <= i / 2; ++m) {
+        const float* p = a + rho(i, c) * kLd + 32 * m + 8 * lg;
+        image_put<kW>(to, lower_frag(i, m), frag_of<kW>(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4)));
       }
+  }
+  if (BWD) {
+    uint16_t* to = out.inverse_t + unit * (kFrags * kW * kFragElems);
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int m = j / 2; m < KC; ++m) {
+        const float* p = a + (32 * m + 8 * lg) * kLd + rho(j, c);
+        f32x4 x, y;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          x[r] = p[r * kLd];
+          y[r] = p[(4 + r) * kLd];
+        }
+        image_put<kW>(to, upper_frag<KC>(j, m), frag_of<kW>(x, y));
+      }
+  }
+}
+
+// ----------------------------------------------------------------- chain of states
+template <typename T>
+struct FwdArgs {
+  Rows k, q;
+  Heads<const T> v;
+  Heads<T> o;
+  const uint16_t *k_t, *inverse, *p;
+  const float *gates, *s0;
+  float *s1, *states;
+};
+
+// Workgroup (x, s): value head x % H of sequence s; wave w takes the columns
+// 16 (NW (x / H) + w) .. of v. Heads run fastest, so the workgroups of one head, which
+// read the same fragments, meet in one of the eight L2 caches. A chunk's fragments
+// come into LDS while the chunk before is worked on; those of K^T, which are needed
+// last, have one buffer.
+template <typename T, int DK, int NW>
+__global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T> A) {
+  constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
+  constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords, kFrags = KC * (KC + 1);
+  // fragments of a buffer
+  constexpr int nRows = RT * KD * kIn, nInv = kFrags * kW, nP = kFrags * kOut, nGate = (kGateRows * C * 4 + 1023) / 1024,
+                nKT = DT * KC * kIn;
+  constexpr int oQ = nRows, oInv = 2 * nRows, oP = oInv + nInv, oGate = oP + nP, kBuf = (oGate + nGate) * 1024;
+  __shared__ __align__(16) char lds[2 * kBuf + nKT * 1024];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
+  const int h = blockIdx.x % z.H, hk = h / (z.H / z.Hk), v0 = ((blockIdx.x / z.H) * NW + wave) * 16, s = blockIdx.y;
+  const uint32_t lds0 = lds_address(lds);
+  const char* kt_img = lds + 2 * kBuf;
+  uint32_t r0, r1, first;
+  segment_rows(z.offs, s, static_cast<uint32_t>(z.T), kLogC, r0, r1, first);
+
+  // the state's rows rho(i, 4 lg + r), column v0 + c
+  const int col = v0 + c, vcol = col < z.dv ? col : z.dv - 1;
+  const int64_t size = static_cast<int64_t>(z.dk) * z.dv, of = (static_cast<int64_t>(s) * z.H + h) * size;
+  f32x4 S[DT] = {};
+  if (A.s0) {
+    float x[DT][4];
+    load_state<DT>(x, A.s0 + of, z.dk, z.dv, vcol);
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = rho(i, 4 * lg + r) < z.dk ? x[i][r] : 0.0f;
+  }
+  T rv[RT][4];
+  const auto fetch = [&](uint32_t t0, int64_t unit, int buf) {
+    const int last = (r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C) - 1;
+    load_column<RT>(rv, A.v.row(t0, h), A.v.st, vcol, last);
+    const uint32_t to = lds0 + buf * kBuf;
+    fetch_rows<RT, KD, kIn, NW>(to, A.k, t0, last, hk, wave);
+    fetch_rows<RT, KD, kIn, NW>(to + oQ * 1024, A.q, t0, last, hk, wave);
+    fetch_image<nInv, NW>(to + oInv * 1024, A.inverse + unit * (nInv * kFragElems), wave);
+    fetch_image<nP, NW>(to + oP * 1024, A.p + unit * (nP * kFragElems), wave);
+    fetch_image<nGate, NW>(to + oGate * 1024, reinterpret_cast<const uint16_t*>(A.gates + unit * (kGateRows * C)), wave);
   };
 
   int64_t unit = static_cast<int64_t>(first) * z.H + h;
-  if (r0 < r1) fetch(r0, unit);
-  for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H) {
+  int buf = 0;
+  if (r0 < r1) fetch(r0, unit, 0);
+  fetch_done();
+  for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
     const int n = r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C;
-    __syncthreads();  // the last chunk's fragments have been read
-#pragma unroll
-    for (int b = 0; b < kNB; ++b) {
-      const int id = b * kThreads + threadIdx.x, t = id / (DK / 4) * 4, d = id % (DK / 4) * 4;
-      if (id < kRowBlocks) {
-        float x[4][4], y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          rk[b][j].get(x[j]);
-          RowImg::store4(lds + kK, t + j, d, x[j]);
-          rq[b][j].get(y);
-          RowImg::store4(lds + kQ, t + j, d, y);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float w[4] = {x[0][j], x[1][j], x[2][j], x[3][j]};
-          ColImg::store4(lds + kKT, d + j, t, w);
-        }
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < kNI; ++b) {
-      const int id = b * kThreads + threadIdx.x, i = id / (C / 4) * 4, j = id % (C / 4) * 4;
-      if (id < kInvBlocks && j / 16 <= i / 16)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float w[4] = {ri[b][r][0], ri[b][r][1], ri[b][r][2], ri[b][r][3]};
-          InvImg::store4(lds + kInv, i + r, j, w);
-        }
-    }
-#pragma unroll
-    for (int b = 0; b < kNG; ++b) {
-      const int id = b * kThreads + threadIdx.x;
-      if (id < kGateRows * C) reinterpret_cast<float*>(lds + kG)[id] = rg[b];
-    }
     f32x4 R[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) R[i][r] = to_f32(rv[i][r]);
-    __syncthreads();
-    if (t0 + C < r1) fetch(t0 + C, unit + z.H);
-    if (A.states) write_state(A.states + unit * size);
+    __syncthreads();  // this chunk's fragments are there, the last one's have been read
+    fetch_image<nKT, NW>(lds0 + 2 * kBuf, A.k_t + (unit / z.H * z.Hk + hk) * (nKT * kFragElems), wave);
+    if (t0 + C < r1) fetch(t0 + C, unit + z.H, buf ^ 1);
+    if (A.states) store_state<DT>(S, A.states + unit * size, z.dk, z.dv, col);
+    const char* img = lds + buf * kBuf;
+    const float* gate = reinterpret_cast<const float*>(img + oGate * 1024);
 
-    // P, its tiles shared out among the waves: rows j of the result are places of the image
-    for (int p = wave; p < RT * (RT + 1) / 2; p += NW) {
-      int i = 0, j = p;
-      while (j > i) j -= ++i;
-      f32x4 acc{};
-#pragma unroll
-      for (int ks = 0; ks < KD; ++ks)
-        mm<kIn>(acc, RowImg::load(lds + kK, j, ks), RowImg::load(lds + kQ, i, ks));
-      const int row = 16 * i + c;
-      float w[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int m = 16 * j + 4 * lg + r;
-        const float dcy = decay(gate[kGHi * C + row], gate[kGLo * C + row], gate[kGHi * C + m], gate[kGLo * C + m]);
-        w[r] = m <= row ? acc[r] * dcy * z.scale : 0.0f;
-      }
-      PImg::store4(lds + kP, row, 16 * j + 4 * lg, w);
-    }
     // K S0 (rows t, columns v) and its transposed Q S0 (rows v, columns t)
     f32x4 ks0[RT] = {}, o[RT] = {};
 #pragma unroll
     for (int ks = 0; ks < KD; ++ks) {
       const Frag<kW> f = frag_of<kW>(S[2 * ks], S[2 * ks + 1]);
+      Frag<kIn> fk[RT], fq[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        mm<kW>(ks0[i], RowImg::load(lds + kK, i, ks), f);
-        mm<kOut>(o[i], f, RowImg::load(lds + kQ, i, ks));
+        fk[i] = lds_frag<kIn, kIn>(img, i * KD + ks);
+        fq[i] = lds_frag<kIn, kIn>(img + oQ * 1024, i * KD + ks);
       }
+      mm_tiles<kW, 0, RT>(ks0, fk, f);
+      mm_tiles<kOut, 0, RT, true>(o, fq, f);
     }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const f32x4 eg = *reinterpret_cast<const f32x4*>(gate + kEG * C + 16 * i + 4 * lg);
-      const float e_col = gate[kEG * C + 16 * i + c] * z.scale;
+      const f32x4 eg = *reinterpret_cast<const f32x4*>(gate + kEG * C + rho(i, 4 * lg));
+      const float e_col = gate[kEG * C + rho(i, c)] * z.scale;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        R[i][r] = __builtin_fmaf(-eg[r], ks0[i][r], R[i][r]);
-        o[i][r] *= e_col;
-      }
+      for (int r = 0; r < 4; ++r) R[i][r] = __builtin_fmaf(-eg[r], ks0[i][r], R[i][r]);
+      o[i] *= e_col;
     }
     // N, then U = beta N
     f32x4 U[RT] = {};
+    static_for<KC>([&](auto kt) {
+      const Frag<kW> f = frag_of<kW>(R[2 * kt.value], R[2 * kt.value + 1]);
+      Frag<kW> fi[RT];
 #pragma unroll
-    for (int kt = 0; kt < KC; ++kt) {
-      const Frag<kW> f = frag_of<kW>(R[2 * kt], R[2 * kt + 1]);
+      for (int i = 2 * kt.value; i < RT; ++i) fi[i] = lds_frag<kW, kW>(img + oInv * 1024, lower_frag(i, kt.value));
+      mm_tiles<kW, 2 * kt.value, RT>(U, fi, f);
+    });
 #pragma unroll
-      for (int i = 2 * kt; i < RT; ++i) mm<kW>(U[i], InvImg::load(lds + kInv, i, kt), f);
-    }
+    for (int i = 0; i < RT; ++i) U[i] *= *reinterpret_cast<const f32x4*>(gate + kBeta * C + rho(i, 4 * lg));
+    static_for<KC>([&](auto kt) {
+      const Frag<kOut> f = frag_of<kOut>(U[2 * kt.value], U[2 * kt.value + 1]);
+      Frag<kOut> fp[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) U[i] *= *reinterpret_cast<const f32x4*>(gate + kBeta * C + 16 * i + 4 * lg);
-    __syncthreads();  // P is there
-#pragma unroll
-    for (int kt = 0; kt < KC; ++kt) {
-      const Frag<kOut> f = frag_of<kOut>(U[2 * kt], U[2 * kt + 1]);
-#pragma unroll
-      for (int i = 2 * kt; i < RT; ++i) mm<kOut>(o[i], f, PImg::load(lds + kP, i, kt));
-    }
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int t = 16 * i + c;
-      if (t < n) store4(A.o.row(t0 + t, h) + v0 + 4 * lg, z.dv - v0 - 4 * lg, o[i]);
-    }
-    // S1
-    const float el = gate[kEG * C + C - 1];
+      for (int i = 2 * kt.value; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(img + oP * 1024, lower_frag(i, kt.value));
+      mm_tiles<kOut, 2 * kt.value, RT, true>(o, fp, f);
+    });
+    const float el = gate[kEnd * C];
 #pragma unroll
     for (int i = 0; i < DT; ++i) S[i] *= el;
 #pragma unroll
-    for (int kt = 0; kt < KC; ++kt) {
-      const f32x4 w0 = *reinterpret_cast<const f32x4*>(gate + kRest * C + 32 * kt + 4 * lg);
-      const f32x4 w1 = *reinterpret_cast<const f32x4*>(gate + kRest * C + 32 * kt + 16 + 4 * lg);
-      const Frag<kW> f = frag_of<kW>(U[2 * kt] * w0, U[2 * kt + 1] * w1);
+    for (int i = 0; i < RT; ++i) U[i] *= *reinterpret_cast<const f32x4*>(gate + kRest * C + rho(i, 4 * lg));
+    fetch_done();
+    __syncthreads();  // K^T is there, and the next chunk's fragments
 #pragma unroll
-      for (int i = 0; i < DT; ++i) mm<kW>(S[i], ColImg::load(lds + kKT, i, kt), f);
+    for (int i = 0; i < RT; ++i) {
+      const int t = rho(i, c);
+      if (t < n) store4(A.o.row(t0 + t, h) + v0 + 4 * lg, z.dv - v0 - 4 * lg, o[i]);
+    }
+#pragma unroll
+    for (int kt = 0; kt < KC; ++kt) {
+      const Frag<kW> f = frag_of<kW>(U[2 * kt], U[2 * kt + 1]);
+      Frag<kIn> fk[DT];
+#pragma unroll
+      for (int i = 0; i < DT; ++i) fk[i] = lds_frag<kIn, kIn>(kt_img, i * KC + kt);
+      mm_tiles<kW, 0, DT>(S, fk, f);
     }
   }
-  if (A.s1) write_state(A.s1 + of);
+  if (A.s1) store_state<DT>(S, A.s1 + of, z.dk, z.dv, col);
 }
 
-struct Layout {
-  size_t inverse, gates, all;
-};
-Layout layout_of(const DeltaSizes& z, int dtype) {
-  const int64_t C = dtype == DET_BF16 ? 64 : 32, units = delta_tiles(z.T, z.S, dtype) * z.H;
-  Layout l;
-  l.inverse = DET_WS_HEADER_BYTES;
-  l.gates = l.inverse + static_cast<size_t>(units * C * C) * 4;
-  l.all = l.gates + align_up(static_cast<size_t>(units * kGateRows * C) * 4, 256);
-  return l;
+template <typename T, int DIM>
+void launch_turn(const DeltaSizes& z, int dtype, const Heads<const T>& x, int heads, int dim, uint16_t* turned, uint16_t* rows,
+                 hipStream_t st) {
+  if (!turned && !rows) return;
+  const dim3 grid(static_cast<uint32_t>(delta_tiles(z.T, z.S, dtype)), static_cast<uint32_t>(heads));
+  hipLaunchKernelGGL((delta_turn_kernel<T, DIM>), grid, dim3(256), 0, st, z, x, heads, dim, turned, rows);
+}
+
+// Whether the kernels can read a tensor's rows as they are.
+bool as_it_is(const void* p, int64_t st, int64_t sh, int64_t dim) {
+  return dim == delta_pad(dim) && aligned(p, 16) && st % 8 == 0 && sh % 8 == 0 && st < (1 << 24);
+}
+
+template <typename T>
+Rows rows_of(const DeltaSizes& z, int dtype, const void* x, int64_t x_st, int64_t x_sh, int heads, int dim, uint16_t* turned,
+             uint16_t* copy, hipStream_t st) {
+  const bool direct = sizeof(T) == 2 && as_it_is(x, x_st, x_sh, dim);
+  const Heads<const T> h{static_cast<const T*>(x), x_st, x_sh};
+  if (dim <= 64) launch_turn<T, 64>(z, dtype, h, heads, dim, turned, direct ? nullptr : copy, st);
+  else launch_turn<T, 128>(z, dtype, h, heads, dim, turned, direct ? nullptr : copy, st);
+  if (direct) return {static_cast<const uint16_t*>(x), x_st, x_sh, 0};
+  const int pad = delta_pad(dim), words = delta_words(dtype);
+  return {copy, static_cast<int64_t>(heads) * words * pad, static_cast<int64_t>(words) * pad, pad};
 }
 
 template <typename T, int DK>
-void launch_prep(const DeltaSizes& z, const void* k, int64_t k_st, int64_t k_sh, const float* g, int64_t g_ld,
-                 const void* beta, int64_t beta_ld, float* inverse, float* gates, int64_t units, hipStream_t st) {
-  hipLaunchKernelGGL((delta_prep_kernel<T, DK>), dim3(static_cast<uint32_t>(ceil_div(units, kPrepWaves))),
-                     dim3(64 * kPrepWaves), 0, st, z, Heads<const T>{static_cast<const T*>(k), k_st, k_sh}, g, g_ld,
-                     static_cast<const T*>(beta), beta_ld, inverse, gates, units);
+void launch_prep(const DeltaSizes& z, bool bwd, const Rows& k, const Rows& q, const float* g, int64_t g_ld, const void* beta,
+                 int64_t beta_ld, const PrepOut& out, int64_t units, hipStream_t st) {
+  const dim3 grid(static_cast<uint32_t>(ceil_div(units, kPrepWaves)));
+  if (bwd)
+    hipLaunchKernelGGL((delta_prep_kernel<T, DK, true>), grid, dim3(64 * kPrepWaves), 0, st, z, k, q, g, g_ld,
+                       static_cast<const T*>(beta), beta_ld, out, units);
+  else
+    hipLaunchKernelGGL((delta_prep_kernel<T, DK, false>), grid, dim3(64 * kPrepWaves), 0, st, z, k, q, g, g_ld,
+                       static_cast<const T*>(beta), beta_ld, out, units);
+}
+
+template <typename T>
+DeltaPrepared prepare(const DeltaSizes& z, int dtype, bool bwd, const void* q, int64_t q_st, int64_t q_sh, const void* k,
+                      int64_t k_st, int64_t k_sh, const void* d_o, int64_t do_st, int64_t do_sh, const float* g, int64_t g_ld,
+                      const void* beta, int64_t beta_ld, char* ws, const DeltaLayout& l, hipStream_t st) {
+  const auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(ws + o); };
+  DeltaPrepared r{};
+  r.k = rows_of<T>(z, dtype, k, k_st, k_sh, z.Hk, z.dk, at(l.k_t), at(l.k_rows), st);
+  r.q = rows_of<T>(z, dtype, q, q_st, q_sh, z.Hk, z.dk, bwd ? at(l.q_t) : nullptr, at(l.q_rows), st);
+  if (bwd) r.d_o = rows_of<T>(z, dtype, d_o, do_st, do_sh, z.H, z.dv, nullptr, at(l.o_rows), st);
+  const PrepOut out{reinterpret_cast<float*>(ws + l.gates), at(l.inverse), at(l.inverse_t), at(l.p)};
+  const int64_t units = delta_tiles(z.T, z.S, dtype) * z.H;
+  if (z.dk <= 64) launch_prep<T, 64>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, out, units, st);
+  else launch_prep<T, 128>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, out, units, st);
+  return r;
 }
 
 template <typename T, int DK>
 void launch_fwd(const DeltaSizes& z, const FwdArgs<T>& A, hipStream_t st) {
-  // the widest workgroup that still leaves one for each compute unit
-  int nw = 8;
-  while (nw > 1 && (static_cast<int64_t>(z.S) * z.H * ceil_div(z.dv, 16 * nw) < 256 || 16 * nw >= 2 * z.dv)) nw /= 2;
-  const int n_blocks = static_cast<int>(ceil_div(z.dv, 16 * nw));
-  const dim3 grid(static_cast<uint32_t>(z.H * n_blocks), static_cast<uint32_t>(z.S));
-#define DET_DELTA_FWD(NW) \
-  case NW: hipLaunchKernelGGL((delta_fwd_kernel<T, DK, NW>), grid, dim3(64 * NW), 0, st, z, A, n_blocks); break;
-  switch (nw) {
-    DET_DELTA_FWD(1)
-    DET_DELTA_FWD(2)
-    DET_DELTA_FWD(4)
-    DET_DELTA_FWD(8)
-  }
-#undef DET_DELTA_FWD
+  // the waves of a head in one workgroup, which share its L1 cache, where that leaves a
+  // workgroup for each compute unit; else spread out
+  const int64_t chains = static_cast<int64_t>(z.S) * z.H;
+  const int nw = chains >= 256 ? 8 : chains >= 64 ? 4 : 1;
+  const dim3 grid(static_cast<uint32_t>(z.H * ceil_div(z.dv, 16 * nw)), static_cast<uint32_t>(z.S));
+  if (nw == 8) hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 8>), grid, dim3(512), 0, st, z, A);
+  else if (nw == 4) hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 4>), grid, dim3(256), 0, st, z, A);
+  else hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 1>), grid, dim3(64), 0, st, z, A);
 }
 
 }  // namespace
 
-void delta_prepare(const DeltaSizes& z, int dtype, const void* k, int64_t k_st, int64_t k_sh, const float* g, int64_t g_ld,
-                   const void* beta, int64_t beta_ld, float* inverse, float* gates, hipStream_t st) {
-  const int64_t units = delta_tiles(z.T, z.S, dtype) * z.H;
-#define DET_DELTA_PREP(T, DK) launch_prep<T, DK>(z, k, k_st, k_sh, g, g_ld, beta, beta_ld, inverse, gates, units, st)
-  if (dtype == DET_BF16) {
-    if (z.dk <= 64) DET_DELTA_PREP(uint16_t, 64);
-    else DET_DELTA_PREP(uint16_t, 128);
-  } else {
-    if (z.dk <= 64) DET_DELTA_PREP(float, 64);
-    else DET_DELTA_PREP(float, 128);
-  }
-#undef DET_DELTA_PREP
+DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd) {
+  const int64_t C = delta_chunk(dtype), KC = C / 32, tiles = delta_tiles(z.T, z.S, dtype), units = tiles * z.H;
+  const int64_t words = delta_words(dtype), dk = delta_pad(z.dk), dv = delta_pad(z.dv), square = KC * (KC + 1) * kFragElems * 2;
+  const int64_t p_words = bwd ? kStateWords : (dtype == DET_BF16 ? DeltaType<uint16_t>::kOut : DeltaType<float>::kOut);
+  DeltaLayout l{};
+  size_t at = DET_WS_HEADER_BYTES;
+  const auto take = [&](int64_t bytes) {
+    const size_t r = at;
+    at += align_up(static_cast<size_t>(bytes), 256);
+    return r;
+  };
+  l.gates = take(units * kGateRows * C * 4);
+  l.inverse = take(units * square * kStateWords);
+  l.inverse_t = take(bwd ? units * square * kStateWords : 0);
+  l.p = take(units * square * p_words);
+  l.k_t = take(tiles * z.Hk * C * dk * words * 2);
+  l.q_t = take(bwd ? tiles * z.Hk * C * dk * words * 2 : 0);
+  l.k_rows = take(z.T * z.Hk * words * dk * 2);
+  l.q_rows = take(z.T * z.Hk * words * dk * 2);
+  l.o_rows = take(bwd ? z.T * z.H * words * dv * 2 : 0);
+  l.ds = take(bwd ? units * z.dk * z.dv * 4 : 0);
+  l.all = at;
+  return l;
+}
+
+DeltaPrepared delta_prepare(const DeltaSizes& z, int dtype, bool bwd, const void* q, int64_t q_st, int64_t q_sh, const void* k,
+                            int64_t k_st, int64_t k_sh, const void* d_o, int64_t do_st, int64_t do_sh, const float* g,
+                            int64_t g_ld, const void* beta, int64_t beta_ld, char* ws, const DeltaLayout& l, hipStream_t st) {
+  if (dtype == DET_BF16)
+    return prepare<uint16_t>(z, dtype, bwd, q, q_st, q_sh, k, k_st, k_sh, d_o, do_st, do_sh, g, g_ld, beta, beta_ld, ws, l, st);
+  return prepare<float>(z, dtype, bwd, q, q_st, q_sh, k, k_st, k_sh, d_o, do_st, do_sh, g, g_ld, beta, beta_ld, ws, l, st);
 }
 
 int delta_check_sizes(const char* what, int dtype, int64_t T, int64_t S, int64_t Hk, int64_t H, int64_t dk, int64_t dv) {
@@ -493,14 +582,12 @@ extern "C" int det_delta_rule_chunks(int64_t T, int64_t S, int dtype, int64_t* c
   return ok();
 }
 
-extern "C" int det_delta_rule_workspace_size(int64_t T, int64_t S, int64_t H, int dtype, size_t* bytes) {
+extern "C" int det_delta_rule_workspace_size(int64_t T, int64_t S, int64_t Hk, int64_t H, int64_t dk, int64_t dv, int dtype,
+                                             size_t* bytes) {
   if (!bytes) return set_error(DET_ERR_INVALID_ARG, "delta_rule: bytes is NULL");
-  if (int s = delta_check_sizes("delta_rule", dtype, T, S, 1, H, 1, 1)) return s;
-  DeltaSizes z{};
-  z.T = T;
-  z.S = static_cast<int>(S);
-  z.H = static_cast<int>(H);
-  *bytes = T == 0 ? 0 : layout_of(z, dtype).all;
+  if (int s = delta_check_sizes("delta_rule", dtype, T, S, Hk, H, dk, dv)) return s;
+  const DeltaSizes z{T, (int)S, (int)Hk, (int)H, (int)dk, (int)dv, nullptr, 0.0f};
+  *bytes = T == 0 ? 0 : delta_layout(z, dtype, false).all;
   return ok();
 }
 
@@ -526,7 +613,7 @@ extern "C" int det_delta_rule(const void* q, int64_t q_st, int64_t q_sh, const v
   if (T > 0 && (g_ld > (int64_t(1) << 44) / T || beta_ld > (int64_t(1) << 44) / T))
     return set_error(DET_ERR_UNSUPPORTED, "%s: g or beta is too large", what);
   const DeltaSizes z{T, (int)S, (int)Hk, (int)H, (int)dk, (int)dv, offs, static_cast<float>(scale)};
-  const Layout l = layout_of(z, dtype);
+  const DeltaLayout l = delta_layout(z, dtype, false);
   const size_t need = T ? l.all : 0;
   if (int s = check_workspace(ws, ws_bytes, need)) return s;
   const size_t state = static_cast<size_t>(H * dk * dv) * 4;
@@ -540,19 +627,19 @@ extern "C" int det_delta_rule(const void* q, int64_t q_st, int64_t q_sh, const v
                      {"initial_state", range1d(initial_state, S * state)}};
   if (int s = check_buffers(what, outs, 4, ins, 7)) return s;
   const hipStream_t st = as_stream(stream);
-  float *inverse = nullptr, *gates = nullptr;
-  if (T) {
-    inverse = reinterpret_cast<float*>(static_cast<char*>(ws) + l.inverse);
-    gates = reinterpret_cast<float*>(static_cast<char*>(ws) + l.gates);
-    delta_prepare(z, dtype, k, k_st, k_sh, g, g_ld, beta, beta_ld, inverse, gates, st);
-  }
-#define DET_DELTA_FWD(E)                                                                                             \
-  {                                                                                                                  \
-    const FwdArgs<E> A{{static_cast<const E*>(q), q_st, q_sh}, {static_cast<const E*>(k), k_st, k_sh},               \
-                       {static_cast<const E*>(v), v_st, v_sh}, {static_cast<E*>(o), o_st, o_sh},                     \
-                       inverse, gates, initial_state, final_state, states};                                          \
-    if (dk <= 64) launch_fwd<E, 64>(z, A, st);                                                                       \
-    else launch_fwd<E, 128>(z, A, st);                                                                               \
+  char* base = static_cast<char*>(ws);  // (no tokens: nothing there is read)
+  DeltaPrepared r{};
+  if (T)
+    r = delta_prepare(z, dtype, false, q, q_st, q_sh, k, k_st, k_sh, nullptr, 0, 0, g, g_ld, beta, beta_ld, base, l, st);
+#define DET_DELTA_FWD(E)                                                                                            \
+  {                                                                                                                 \
+    const FwdArgs<E> A{r.k, r.q, {static_cast<const E*>(v), v_st, v_sh}, {static_cast<E*>(o), o_st, o_sh},          \
+                       reinterpret_cast<const uint16_t*>(base + l.k_t),                                             \
+                       reinterpret_cast<const uint16_t*>(base + l.inverse),                                         \
+                       reinterpret_cast<const uint16_t*>(base + l.p), reinterpret_cast<const float*>(base + l.gates), \
+                       initial_state, final_state, states};                                                         \
+    if (dk <= 64) launch_fwd<E, 64>(z, A, st);                                                                      \
+    else launch_fwd<E, 128>(z, A, st);                                                                              \
   }
   if (dtype == DET_BF16) DET_DELTA_FWD(uint16_t)
   else DET_DELTA_FWD(float)

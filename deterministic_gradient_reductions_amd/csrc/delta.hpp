@@ -1,5 +1,5 @@
 // Building blocks of the gated delta rule's kernels: 16 x 16 tiles on the matrix
-// cores with operands in one to three bf16 words, and their fragments in LDS.
+// cores with operands in one to three bf16 words, and their fragments in memory.
 //
 // Words. A float32 x is carried into a product as x0 + x1 + x2, x0 = bf16(x), x1 =
 // bf16(x - x0), x2 the rest (both differences are exact): 8 bits of it per word.
@@ -10,12 +10,16 @@
 // input with a float32 state in three.
 //
 // Layout. The instruction takes lane l = 16 g + c as row (A) or column (B) c of its
-// operands with eight of the 32 places of the summed index, and gives it the rows
-// 4 g + r (r = 0..3) of column c of the result. Which eight places a lane group g
-// takes is free as long as A and B agree; here they are 4 g + r and 16 + 4 g + r.
-// Then the results of two tiles, one below the other, are an operand of the next
-// product as they stand, summed over their rows: a chain of products keeps its
-// running operand in registers.
+// operands with the places 8 g .. 8 g + 7 of the summed index (32 of them), and gives it
+// the rows 4 g + r (r = 0..3) of column c of the result. Which token or channel a
+// tile's row stands for is free. Row x of tile i is number
+//
+//   rho(i, x) = 32 (i / 2) + 8 (x / 4) + 4 (i % 2) + x % 4
+//
+// here, so a lane's results of tiles 2m and 2m + 1 are the eight neighbours 32 m + 8 g ..
+// and, as they stand, its places in the next product: a chain of products keeps its
+// running operand in registers, and an operand's fragment from memory is 16 bytes of a
+// row (of K as it is given, say).
 #pragma once
 
 #include "rowops.hpp"
@@ -25,6 +29,26 @@ namespace detgrad {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ constexpr int rho(int tile, int x) {
+  return 32 * (tile >> 1) + 8 * (x >> 2) + 4 * (tile & 1) + (x & 3);
+}
+// and back: the tile and the row in it of a number
+__device__ __forceinline__ constexpr int rho_tile(int n) { return 2 * (n >> 5) + ((n >> 2) & 1); }
+__device__ __forceinline__ constexpr int rho_row(int n) { return 4 * ((n >> 3) & 3) + (n & 3); }
+
+// f(0), f(1), .. f(N - 1) with constant arguments.
+template <int I>
+struct Index {
+  static constexpr int value = I;
+};
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void static_for(const F& f) {
+  if constexpr (I < N) {
+    f(Index<I>{});
+    static_for<N, I + 1>(f);
+  }
+}
 
 template <int NP>
 struct Frag {
@@ -40,6 +64,20 @@ __device__ __forceinline__ void mm(f32x4& acc, const Frag<NA>& a, const Frag<NB>
     for (int i = 0; i < NA; ++i)
       if (s - i >= 0 && s - i < NB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.w[i], b.w[s - i], acc, 0, 0, 0);
 }
+// acc[t] += A[t] B (SWAP: B A[t]) for the tiles t in [FROM, TO), their terms in turn: one
+// after the other would wait for its own result each time.
+template <int P, int FROM, int TO, bool SWAP = false, int N, int NA, int NB>
+__device__ __forceinline__ void mm_tiles(f32x4 (&acc)[N], const Frag<NA> (&a)[N], const Frag<NB>& b) {
+#pragma unroll
+  for (int s = P - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+#pragma unroll
+        for (int t = FROM; t < TO; ++t)
+          acc[t] = SWAP ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.w[s - i], a[t].w[i], acc[t], 0, 0, 0)
+                        : __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t].w[i], b.w[s - i], acc[t], 0, 0, 0);
+}
 
 template <int NP>
 __device__ __forceinline__ void split(float x, __bf16 (&w)[NP]) {
@@ -49,113 +87,113 @@ __device__ __forceinline__ void split(float x, __bf16 (&w)[NP]) {
     if (p + 1 < NP) x -= static_cast<float>(w[p]);
   }
 }
-
-// The fragment whose places are the rows of two results, x above y.
+// The words of two values side by side (one conversion instruction for both).
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 template <int NP>
-__device__ __forceinline__ Frag<NP> frag_of(const f32x4& x, const f32x4& y) {
-  Frag<NP> f;
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&w)[NP]) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    __bf16 a[NP], b[NP];
-    split<NP>(x[r], a);
-    split<NP>(y[r], b);
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      f.w[p][r] = a[p];
-      f.w[p][4 + r] = b[p];
+  for (int p = 0; p < NP; ++p) {
+    const f32x2 v = {x, y};
+    w[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    if (p + 1 < NP) {
+      x -= bf16_lo(w[p]);
+      y -= bf16_hi(w[p]);
     }
   }
+}
+
+// The fragment whose places are the rows of two results (or any eight values).
+template <int NP>
+__device__ __forceinline__ Frag<NP> frag_of(const f32x4& x, const f32x4& y) {
+  uint32_t w[4][NP];
+  split2<NP>(x[0], x[1], w[0]);
+  split2<NP>(x[2], x[3], w[1]);
+  split2<NP>(y[0], y[1], w[2]);
+  split2<NP>(y[2], y[3], w[3]);
+  Frag<NP> f;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) f.w[p] = __builtin_bit_cast(bf16x8, u32x4{w[0][p], w[1][p], w[2][p], w[3][p]});
   return f;
 }
 
-// Fragments of an operand of 16 RT rows (or columns) and 32 KS places in LDS, NP
-// words. A lane's 16 bytes lie side by side for the 16 rows; the lane groups are 272
-// bytes apart and the row tiles a multiple of 256 bytes and 16 more, so that the
-// 8-byte writes of four neighbouring places, rows or columns running over the
-// lanes, spread over the banks.
-template <int RT, int KS, int NP>
-struct Image {
-  static constexpr int kGroup = 272, kFrag = 4 * kGroup, kTile = (KS * kFrag + 239) / 256 * 256 + 16, kWord = RT * kTile;
-  static constexpr int kBytes = NP * kWord;
-  static_assert(kTile >= KS * kFrag && kTile % 16 == 0, "tiles overlap");
-  // row (16 rt + c), places 32 ks + 16 half + 4 g .. + 3
-  static __device__ __forceinline__ int at(int row, int place) {
-    return (row >> 4) * kTile + (place >> 5) * kFrag + ((place >> 2) & 3) * kGroup + (row & 15) * 16 + ((place >> 4) & 1) * 8;
-  }
-  static __device__ __forceinline__ Frag<NP> load(const char* base, int rt, int ks) {
-    const int lane = threadIdx.x & 63;
-    Frag<NP> f;
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-      f.w[p] = *reinterpret_cast<const bf16x8*>(base + p * kWord + rt * kTile + ks * kFrag + (lane >> 4) * kGroup +
-                                                (lane & 15) * 16);
-    return f;
-  }
-  // the places place .. place + 3 (place a multiple of 4) of a row
-  static __device__ __forceinline__ void store4(char* base, int row, int place, const float (&v)[4]) {
-    bf16x4 w[NP];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      __bf16 x[NP];
-      split<NP>(v[j], x);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) w[p][j] = x[p];
-    }
-#pragma unroll
-    for (int p = 0; p < NP; ++p) *reinterpret_cast<bf16x4*>(base + p * kWord + at(row, place)) = w[p];
-  }
-  static __device__ __forceinline__ void store1(char* base, int row, int place, float v) {
-    __bf16 x[NP];
-    split<NP>(v, x);
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-      *reinterpret_cast<__bf16*>(base + p * kWord + at(row, place & ~3) + (place & 3) * 2) = x[p];
-  }
-};
+// The value itself, of which the compiler knows nothing: what is computed from it in a
+// loop stays there. (Moved out, the addresses of a chunk's loads fill the registers.)
+template <typename V>
+__device__ __forceinline__ V here(V x) {  // the same for the wave
+  asm volatile("" : "+s"(x));
+  return x;
+}
+template <typename V>
+__device__ __forceinline__ V here_lane(V x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 
-// Four consecutive elements, those at or past n zero (and not read).
+// A value `off` bytes from `base`, the same for the wave: the address is then a scalar
+// and one register (pointers of the lanes' own take two and 64-bit sums).
+template <typename V>
+__device__ __forceinline__ V load_at(const void* base, uint32_t off) {
+  V v;
+  __builtin_memcpy(&v, static_cast<const char*>(base) + off, sizeof(V));
+  return v;
+}
+
+// Images: fragments one after the other, each NP words of 64 lanes of 16 bytes.
+constexpr int kFragElems = 64 * 8;
+template <int NP, int STORED>
+__device__ __forceinline__ Frag<NP> image_frag(const uint16_t* image, int f) {
+  static_assert(NP <= STORED, "more words than the image has");
+  Frag<NP> r;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) r.w[p] = load_at<bf16x8>(image + (f * STORED + p) * kFragElems, (threadIdx.x & 63) * 16);
+  return r;
+}
+// The same from LDS.
+template <int NP, int STORED>
+__device__ __forceinline__ Frag<NP> lds_frag(const char* image, int f) {
+  static_assert(NP <= STORED, "more words than the image has");
+  Frag<NP> r;
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+    r.w[p] = *reinterpret_cast<const bf16x8*>(image + (f * STORED + p) * 1024 + (threadIdx.x & 63) * 16);
+  return r;
+}
+template <int NP>
+__device__ __forceinline__ void image_put(uint16_t* image, int f, const Frag<NP>& v) {
+#pragma unroll
+  for (int p = 0; p < NP; ++p) __builtin_memcpy(image + (f * NP + p) * kFragElems + (threadIdx.x & 63) * 8, &v.w[p], 16);
+}
+// Where row `row` and place `place` of an operand with KS fragments per row tile lie, in elements (word 0).
+template <int KS, int NP>
+__device__ __forceinline__ int image_at(int row, int place) {
+  return (rho_tile(row) * KS + (place >> 5)) * NP * kFragElems + (16 * ((place >> 3) & 3) + rho_row(row)) * 8 + (place & 7);
+}
+// Square images [C][C] of lower (rows i, places j <= i) or upper (rows j, places i >= j)
+// triangles leave out the fragments that hold nothing else: their numbers.
+__device__ __forceinline__ constexpr int lower_frag(int i, int kt) { return (i >> 1) * ((i >> 1) + 1) + (i & 1) * ((i >> 1) + 1) + kt; }
+template <int KC>
+__device__ __forceinline__ constexpr int upper_frag(int j, int kt) {
+  return 2 * ((j >> 1) * KC - (j >> 1) * ((j >> 1) - 1) / 2) + (j & 1) * (KC - (j >> 1)) + kt - (j >> 1);
+}
+
+// Four consecutive elements at .. at + 3 of a row of n, those behind it zero, loaded
+// without a branch (loads under one would be waited for one by one): whole rows (n a
+// multiple of four, the same for all) in one access, others element by element.
 template <typename T>
-struct Raw4;
-template <>
-struct Raw4<uint16_t> {
-  uint32_t a, b;
-  __device__ __forceinline__ void load(const uint16_t* p, int n) {
-    a = b = 0;
-    if (n >= 4) {
-      uint64_t w;
-      __builtin_memcpy(&w, p, 8);
-      a = static_cast<uint32_t>(w);
-      b = static_cast<uint32_t>(w >> 32);
-    } else if (n > 0) {
-      a = p[0] | (n > 1 ? static_cast<uint32_t>(p[1]) << 16 : 0u);
-      b = n > 2 ? p[2] : 0u;
-    }
-  }
-  __device__ __forceinline__ void get(float (&v)[4]) const {
-    v[0] = bf16_lo(a);
-    v[1] = bf16_hi(a);
-    v[2] = bf16_lo(b);
-    v[3] = bf16_hi(b);
-  }
-};
-template <>
-struct Raw4<float> {
-  f32x4 w;
-  __device__ __forceinline__ void load(const float* p, int n) {
-    w = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (n >= 4) {
-      __builtin_memcpy(&w, p, 16);
-    } else {
+__device__ __forceinline__ f32x4 load4(const T* row, int at, int n, bool whole) {
+  T v[4];
+  if (whole) {
+    __builtin_memcpy(v, row + (at < n ? at : 0), 4 * sizeof(T));
+  } else {
 #pragma unroll
-      for (int j = 0; j < 3; ++j)
-        if (j < n) w[j] = p[j];
-    }
+    for (int j = 0; j < 4; ++j) v[j] = row[at + j < n ? at + j : n - 1];
   }
-  __device__ __forceinline__ void get(float (&v)[4]) const {
+  f32x4 r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = w[j];
-  }
-};
+  for (int j = 0; j < 4; ++j) r[j] = at + j < n ? to_f32(v[j]) : 0.0f;
+  return r;
+}
 // p[0 .. min(n, 4)) = v, rounded once
 __device__ __forceinline__ void store4(float* p, int n, const f32x4& v) {
   if (n >= 4) {
@@ -181,6 +219,40 @@ __device__ __forceinline__ void store4(uint16_t* p, int n, const f32x4& v) {
   }
 }
 
+// Memory to LDS past the registers: lane l brings the 16 bytes at base + off to `lds` + 16 l
+// (base and lds the same for the wave). In assembly, since the compiler makes every
+// read of LDS wait for all such loads, those of a buffer that is only read later
+// too; the wait is fetch_done() and a barrier. It counts only its own loads, of which
+// there are fewer than the hardware counts, so its waits are never too short.
+typedef __attribute__((address_space(3))) void lds_void;
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)p));
+}
+__device__ __forceinline__ void fetch16(uint32_t lds, const void* base, uint32_t off) {
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %2, %3\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
+      : "memory");
+}
+__device__ __forceinline__ void fetch_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// N consecutive fragments of an image, shared out among NW waves.
+template <int N, int NW>
+__device__ __forceinline__ void fetch_image(uint32_t lds, const uint16_t* image, int wave) {
+  const uint32_t off = (threadIdx.x & 63) * 16;
+  wave = here(wave);
+#pragma unroll
+  for (int u = 0; u < (N + NW - 1) / NW; ++u) {
+    const int f = wave + u * NW;
+    if (f < N) fetch16(lds + f * 1024, image + f * kFragElems, off);
+  }
+}
+
 // Writes to LDS of this wave's lanes are seen by its other lanes after this (the
 // wave's LDS accesses run in order; the compiler must not reorder them).
 __device__ __forceinline__ void wave_fence() {
@@ -195,6 +267,116 @@ struct Heads {
   int64_t st, sh;
   __device__ __forceinline__ T* row(int64_t t, int h) const { return p + t * st + h * sh; }
 };
+
+// The elements of a chunk's rows t0 + rho(i, 4 g + r) in one column, `col` elements from
+// `rows` on (row t0 of the head): unconditional loads, the row `last` again behind it.
+template <int RT, typename T>
+__device__ __forceinline__ void load_column(T (&v)[RT][4], const T* rows, int64_t st, int col, int last) {
+  const int g = (here_lane(threadIdx.x) & 63) >> 4;
+  st = here(st);
+  if (last == 16 * RT - 1 && st < (1 << 24)) {  // (the same for all) whole chunks: the rows' distances are uniform
+    const uint32_t off = (8u * g * static_cast<uint32_t>(st) + col) * sizeof(T);
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[i][r] = load_at<T>(rows + rho(i, r) * st, off);
+  } else {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = rho(i, 4 * g + r);
+        v[i][r] = rows[(t < last ? t : last) * st + col];
+      }
+  }
+}
+// The elements d = rho(i, 4 g + r) < dk (others: the first row's) of column col of a [dk, dv] state.
+template <int DT>
+__device__ __forceinline__ void load_state(float (&v)[DT][4], const float* state, int dk, int dv, int col) {
+  const int g = (here_lane(threadIdx.x) & 63) >> 4;
+  dv = here(dv);
+  const uint32_t off = static_cast<uint32_t>(8 * g * dv + col) * 4u;
+  if (dk == 16 * DT) {
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[i][r] = load_at<float>(state + rho(i, r) * dv, off);
+  } else {
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = rho(i, 4 * g + r);
+        v[i][r] = load_at<float>(state, static_cast<uint32_t>((d < dk ? d : 0) * dv + col) * 4u);
+      }
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store_state(const f32x4 (&v)[DT], float* state, int dk, int dv, int col) {
+  const int g = (here_lane(threadIdx.x) & 63) >> 4;
+  dv = here(dv);
+  if (dk == 16 * DT) {
+    if (col < dv)
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<float*>(reinterpret_cast<char*>(state + rho(i, r) * dv) + static_cast<uint32_t>(8 * g * dv + col) * 4u) = v[i][r];
+  } else {
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = rho(i, 4 * g + r);
+        if (col < dv && d < dk) state[d * dv + col] = v[i][r];
+      }
+  }
+}
+
+// The rows of a [T, heads, dim] operand in bf16 words: a bf16 tensor itself where its
+// rows start on 16-byte borders and dim is the kernels' own, else a copy [T, heads, words, dim]
+// padded with zeros.
+struct Rows {
+  const uint16_t* p;
+  int64_t st, sh;
+  int words_at;  // from word to word
+  // the rows from token t of a head on; the places 32 ks + 8 g .. of row t + `row` of them (st < 2^24: see as_it_is)
+  __device__ __forceinline__ const uint16_t* from(int64_t t, int h) const { return p + t * st + h * sh; }
+  __device__ __forceinline__ uint32_t lane_off(int row) const {
+    return (static_cast<uint32_t>(row) * static_cast<uint32_t>(st) + 8u * ((threadIdx.x & 63) >> 4)) * 2u;
+  }
+  template <int NP>
+  __device__ __forceinline__ Frag<NP> frag(const uint16_t* rows, uint32_t off, int ks) const {
+    Frag<NP> f;
+#pragma unroll
+    for (int w = 0; w < NP; ++w) f.w[w] = load_at<bf16x8>(rows + w * words_at + 32 * ks, off);
+    return f;
+  }
+};
+// The fragments of a chunk's rows t0 + rho(i, c) (the last one again behind it) as an image
+// in LDS, tile by tile, KD places of 32 each, NP words; shared out among NW waves. The rows'
+// strides are below 2^24 elements (as_it_is), so that a chunk spans less than 2^32 bytes.
+template <int RT, int KD, int NP, int NW>
+__device__ __forceinline__ void fetch_rows(uint32_t lds, const Rows& x, int64_t t0, int last, int h, int wave) {
+  constexpr int kTile = KD * NP, kAll = RT * kTile;
+  const int c = here_lane(threadIdx.x) & 15;
+  wave = here(wave);
+  const uint16_t* base = x.from(t0, h);
+  uint32_t off[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int t = rho(i, c);
+    off[i] = x.lane_off(t < last ? t : last);
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int u = 0; u < kTile; ++u) {
+      constexpr int kEach = (kAll + NW - 1) / NW;  // neighbours for a wave
+      const int f = i * kTile + u;
+      if (wave == f / kEach) fetch16(lds + f * 1024, base + (u % NP) * x.words_at + 32 * (u / NP), off[i]);
+    }
+}
 
 // Rows [r0, r1) of segment s and the tiles before it, from the clamped offsets (see
 // segment_tile); every lane of the wave active.
@@ -221,7 +403,7 @@ __device__ __forceinline__ void segment_rows(const int32_t* __restrict__ offs, i
 }
 
 // Tokens per chunk, words of an input, words of what only reaches outputs of the
-// input's type. float32 takes half the chunk: its images have three words.
+// input's type. float32 takes half the chunk: its operands have three words.
 template <typename T>
 struct DeltaType;
 template <>
@@ -235,9 +417,15 @@ struct DeltaType<float> {
 // Words of what reaches a float32 state, whose errors stay.
 constexpr int kStateWords = 3;
 
-// What the preparing kernel leaves per (chunk, value head): the inverse [C][C] (its
-// tiles above the diagonal are not written) and five rows of C floats.
-enum GateRow { kGHi = 0, kGLo = 1, kEG = 2, kRest = 3, kBeta = 4, kGateRows = 5 };
+// exp(hi + lo) of a difference of two-word sums
+__device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
+  return exp_e((hi_i - hi_j) + (lo_i - lo_j));
+}
+
+// Rows of C floats that the preparing kernel leaves per (chunk, value head): the running
+// sum G of g in two words, exp(G) and beta (0 behind the sequence's end), exp(G_C - G),
+// and exp(G_C) in every place.
+enum GateRow { kGHi = 0, kGLo = 1, kEG = 2, kRest = 3, kBeta = 4, kEnd = 5, kGateRows = 6 };
 
 // Sizes, and what every kernel of a call is given.
 struct DeltaSizes {
@@ -248,13 +436,25 @@ struct DeltaSizes {
 };
 
 constexpr int kDeltaMaxDim = 128;
-inline int64_t delta_tiles(int64_t T, int64_t S, int dtype) {
-  return (T >> (dtype == DET_BF16 ? DeltaType<uint16_t>::kLogC : DeltaType<float>::kLogC)) + S;
-}
+inline int delta_chunk(int dtype) { return 1 << (dtype == DET_BF16 ? DeltaType<uint16_t>::kLogC : DeltaType<float>::kLogC); }
+inline int delta_words(int dtype) { return dtype == DET_BF16 ? DeltaType<uint16_t>::kIn : DeltaType<float>::kIn; }
+inline int64_t delta_tiles(int64_t T, int64_t S, int dtype) { return T / delta_chunk(dtype) + S; }
+inline int delta_pad(int64_t d) { return d <= 64 ? 64 : 128; }
 
-// Host: launches of the preparing kernel, and the common checks of the calls.
-void delta_prepare(const DeltaSizes& z, int dtype, const void* k, int64_t k_st, int64_t k_sh, const float* g, int64_t g_ld,
-                   const void* beta, int64_t beta_ld, float* inverse, float* gates, hipStream_t st);
+// Where the parts of a workspace lie. The square images: the inverse of I + M B, of both
+// triangles in the backward, and P (transposed in the backward).
+struct DeltaLayout {
+  size_t gates, inverse, inverse_t, p, k_rows, q_rows, o_rows, k_t, q_t, ds, all;
+};
+DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd);
+
+// Host: the kernels that every call begins with, and the common checks of the calls.
+struct DeltaPrepared {
+  Rows k, q, d_o;
+};
+DeltaPrepared delta_prepare(const DeltaSizes& z, int dtype, bool bwd, const void* q, int64_t q_st, int64_t q_sh, const void* k,
+                            int64_t k_st, int64_t k_sh, const void* d_o, int64_t do_st, int64_t do_sh, const float* g,
+                            int64_t g_ld, const void* beta, int64_t beta_ld, char* ws, const DeltaLayout& l, hipStream_t st);
 int delta_check_sizes(const char* what, int dtype, int64_t T, int64_t S, int64_t Hk, int64_t H, int64_t dk, int64_t dv);
 // The buffer of a [T, heads, dim] tensor, or an error where its strides are not those
 // of whole tokens or of whole heads.

@@ -11,513 +11,433 @@
 //        and on the chunk's last row sum(w) + e^G_C <S0, dS1>,   w = rowsum(U * e^(G_C - G) K dS1)
 //   dg = the sums of dG from a row to the chunk's end
 //
-// Nothing is divided by beta or by a decay. Three kernels: the forward's first (the
-// inverses), one that walks a sequence's chunks backwards as the forward's second walks
-// them (16 columns of v per wave, dS in registers; it writes dV and every chunk's
-// dS1), and one for all chunks side by side that forms N, dU and dN of its chunk again
-// and the sums over v and over token pairs. In that one a wave owns 16 columns of v
-// first (N, dN), then tiles of token pairs, then 16 channels of dQ and dK; N, dN and the
-// pair matrices change hands in LDS.
+// Nothing is divided by beta or by a decay. After the forward's two preparing kernels
+// (with P and the inverse transposed too) one kernel walks a sequence's chunks backwards
+// as the forward's walks them (16 columns of v per wave, dS in registers) and writes
+// every chunk's dS1, and one takes all chunks side by side: it forms N, dU and dN of its
+// chunk again and the sums over v and over token pairs. There a wave owns 16 columns of
+// v first (N, dN), then tiles of token pairs, then 16 channels of dQ and dK; N, dN and
+// the pair matrices change hands in LDS as images.
 #include "delta.hpp"
 
 namespace detgrad {
 namespace {
 
-__device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
-  return exp_e((hi_i - hi_j) + (lo_i - lo_j));
-}
 __device__ __forceinline__ f32x4 gate4(const float* gate, int C, int row, int at) {
   return *reinterpret_cast<const f32x4*>(gate + row * C + at);
 }
 
-// The fragment of places 32 ks .. of a row in memory (n elements from p on, zeros behind them).
-template <int NP, typename T>
-__device__ __forceinline__ Frag<NP> row_frag(const T* p, int n, int ks) {
-  const int at = 32 * ks + 4 * ((threadIdx.x & 63) >> 4);
-  Raw4<T> a, b;
-  a.load(p + (n > at ? at : 0), n - at);
-  b.load(p + (n > at + 16 ? at + 16 : 0), n - at - 16);
-  float x[4], y[4];
-  a.get(x);
-  b.get(y);
-  return frag_of<NP>(f32x4{x[0], x[1], x[2], x[3]}, f32x4{y[0], y[1], y[2], y[3]});
-}
-
 template <typename T>
 struct ChainArgs {
-  Heads<const T> q, k, d_o;
-  Heads<T> dv;
-  const float *inverse, *gates, *ds1;
+  Rows k;
+  Heads<const T> d_o;
+  const uint16_t *k_t, *q_t, *inverse_t, *p_t;
+  const float *gates, *ds1;
   float *ds, *ds0;  // every chunk's dS1, the initial state's gradient
 };
 
+// Workgroups, waves and buffers as in the forward's chain; K^T and Q^T have one buffer.
 template <typename T, int DK, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaSizes z, ChainArgs<T> A, int n_blocks) {
+__global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaSizes z, ChainArgs<T> A) {
   constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
-  constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
-  using RowImg = Image<RT, KD, kIn>;  // rows t, places d
-  using ColImg = Image<DT, KC, kIn>;  // rows d, places t
-  using SqImg = Image<RT, KC, kW>;    // rows j, places i: the inverse and P, transposed
-  constexpr int kK = 0, kQ = kK + RowImg::kBytes, kKT = kQ + RowImg::kBytes, kQT = kKT + ColImg::kBytes,
-                kInv = kQT + ColImg::kBytes, kP = kInv + SqImg::kBytes, kG = kP + SqImg::kBytes,
-                kAll = kG + kGateRows * C * 4;
-  __shared__ __align__(16) char lds[kAll];
+  constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords, kFrags = KC * (KC + 1);
+  constexpr int nRows = RT * KD * kIn, nSq = kFrags * kW, nGate = (kGateRows * C * 4 + 1023) / 1024, nT = DT * KC * kIn;
+  constexpr int oInv = nRows, oP = oInv + nSq, oGate = oP + nSq, kBuf = (oGate + nGate) * 1024;
+  __shared__ __align__(16) char lds[2 * kBuf + 2 * nT * 1024];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
-  const int h = blockIdx.x / n_blocks, hk = h / (z.H / z.Hk), v0 = ((blockIdx.x % n_blocks) * NW + wave) * 16;
-  const int s = blockIdx.y;
-  const float* gate = reinterpret_cast<const float*>(lds + kG);
+  const int h = blockIdx.x % z.H, hk = h / (z.H / z.Hk), v0 = ((blockIdx.x / z.H) * NW + wave) * 16, s = blockIdx.y;
+  const uint32_t lds0 = lds_address(lds);
+  const char *kt_img = lds + 2 * kBuf, *qt_img = kt_img + nT * 1024;
   uint32_t r0, r1, first;
   segment_rows(z.offs, s, static_cast<uint32_t>(z.T), kLogC, r0, r1, first);
-  for (int i = threadIdx.x * 16; i < kG - kInv; i += 64 * NW * 16) *reinterpret_cast<u32x4*>(lds + kInv + i) = u32x4{0, 0, 0, 0};
-
-  const int col = v0 + c;
-  const bool live = col < z.dv;
+  const int col = v0 + c, vcol = col < z.dv ? col : z.dv - 1;
   const int64_t size = static_cast<int64_t>(z.dk) * z.dv, of = (static_cast<int64_t>(s) * z.H + h) * size;
-  f32x4 S[DT];
-#pragma unroll
-  for (int i = 0; i < DT; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int d = 16 * i + 4 * lg + r;
-      S[i][r] = A.ds1 && live && d < z.dk ? A.ds1[of + static_cast<int64_t>(d) * z.dv + col] : 0.0f;
-    }
-  const auto write_state = [&](float* p) {
+  f32x4 S[DT] = {};
+  if (A.ds1) {
+    float x[DT][4];
+    load_state<DT>(x, A.ds1 + of, z.dk, z.dv, vcol);
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int d = 16 * i + 4 * lg + r;
-        if (live && d < z.dk) p[static_cast<int64_t>(d) * z.dv + col] = S[i][r];
-      }
-  };
-
-  constexpr int kThreads = 64 * NW, kRowBlocks = C * DK / 16, kInvBlocks = C * C / 16;
-  constexpr int kNB = (kRowBlocks + kThreads - 1) / kThreads, kNI = (kInvBlocks + kThreads - 1) / kThreads;
-  constexpr int kNG = (kGateRows * C + kThreads - 1) / kThreads;
-  Raw4<T> rk[kNB][4], rq[kNB][4];
-  f32x4 ri[kNI][4];
-  float rg[kNG];
+      for (int r = 0; r < 4; ++r) S[i][r] = rho(i, 4 * lg + r) < z.dk ? x[i][r] : 0.0f;
+  }
   T rd[RT][4];
-  const auto fetch = [&](uint32_t t0, int64_t unit) {
-    const int n = r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C;
-#pragma unroll
-    for (int b = 0; b < kNB; ++b) {
-      const int id = b * kThreads + threadIdx.x, t = id / (DK / 4) * 4, d = id % (DK / 4) * 4;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = id < kRowBlocks && t + j < n ? z.dk - d : 0;
-        const int64_t row = m > 0 ? t0 + t + j : t0;
-        rk[b][j].load(A.k.row(row, hk) + (m > 0 ? d : 0), m);
-        rq[b][j].load(A.q.row(row, hk) + (m > 0 ? d : 0), m);
-      }
-    }
-    const float* inv = A.inverse + unit * (C * C);
-#pragma unroll
-    for (int b = 0; b < kNI; ++b) {
-      const int id = b * kThreads + threadIdx.x, i = id / (C / 4) * 4, j = id % (C / 4) * 4;
-      if (id < kInvBlocks && j / 16 <= i / 16)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) ri[b][r] = *reinterpret_cast<const f32x4*>(inv + (i + r) * C + j);
-    }
-#pragma unroll
-    for (int b = 0; b < kNG; ++b) {
-      const int id = b * kThreads + threadIdx.x;
-      if (id < kGateRows * C) rg[b] = A.gates[unit * (kGateRows * C) + id];
-    }
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * i + 4 * lg + r;
-        rd[i][r] = live && t < n ? A.d_o.row(t0 + t, h)[col] : T{};
-      }
+  const auto fetch = [&](uint32_t t0, int64_t unit, int buf) {
+    const int last = (r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C) - 1;
+    load_column<RT>(rd, A.d_o.row(t0, h), A.d_o.st, vcol, last);
+    const uint32_t to = lds0 + buf * kBuf;
+    fetch_rows<RT, KD, kIn, NW>(to, A.k, t0, last, hk, wave);
+    fetch_image<nSq, NW>(to + oInv * 1024, A.inverse_t + unit * (nSq * kFragElems), wave);
+    fetch_image<nSq, NW>(to + oP * 1024, A.p_t + unit * (nSq * kFragElems), wave);
+    fetch_image<nGate, NW>(to + oGate * 1024, reinterpret_cast<const uint16_t*>(A.gates + unit * (kGateRows * C)), wave);
   };
-
   const int chunks = static_cast<int>((r1 - r0 + C - 1) >> kLogC);
-  const auto unit_of = [&](int i) { return (static_cast<int64_t>(first) + i) * z.H + h; };
-  if (chunks) fetch(r0 + ((chunks - 1) << kLogC), unit_of(chunks - 1));
-  for (int ch = chunks - 1; ch >= 0; --ch) {
-    const uint32_t t0 = r0 + (static_cast<uint32_t>(ch) << kLogC);
-    const int n = r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C;
-    __syncthreads();  // the last chunk's fragments have been read
-#pragma unroll
-    for (int b = 0; b < kNB; ++b) {
-      const int id = b * kThreads + threadIdx.x, t = id / (DK / 4) * 4, d = id % (DK / 4) * 4;
-      if (id < kRowBlocks) {
-        float x[4][4], y[4][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          rk[b][j].get(x[j]);
-          RowImg::store4(lds + kK, t + j, d, x[j]);
-          rq[b][j].get(y[j]);
-          RowImg::store4(lds + kQ, t + j, d, y[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float w[4] = {x[0][j], x[1][j], x[2][j], x[3][j]}, u[4] = {y[0][j], y[1][j], y[2][j], y[3][j]};
-          ColImg::store4(lds + kKT, d + j, t, w);
-          ColImg::store4(lds + kQT, d + j, t, u);
-        }
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < kNI; ++b) {
-      const int id = b * kThreads + threadIdx.x, i = id / (C / 4) * 4, j = id % (C / 4) * 4;
-      if (id < kInvBlocks && j / 16 <= i / 16)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float w[4] = {ri[b][0][r], ri[b][1][r], ri[b][2][r], ri[b][3][r]};
-          SqImg::store4(lds + kInv, j + r, i, w);
-        }
-    }
-#pragma unroll
-    for (int b = 0; b < kNG; ++b) {
-      const int id = b * kThreads + threadIdx.x;
-      if (id < kGateRows * C) reinterpret_cast<float*>(lds + kG)[id] = rg[b];
-    }
-    f32x4 dO[RT];
+  const auto start = [&](int ch) { return r0 + (static_cast<uint32_t>(ch) << kLogC); };
+  int64_t unit = (static_cast<int64_t>(first) + chunks - 1) * z.H + h;
+  int buf = 0;
+  if (chunks) fetch(start(chunks - 1), unit, 0);
+  fetch_done();
+  for (int ch = chunks - 1; ch >= 0; --ch, unit -= z.H, buf ^= 1) {
+    f32x4 dU[RT] = {}, dO[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) dO[i][r] = to_f32(rd[i][r]);
-    __syncthreads();
-    if (ch > 0) fetch(t0 - C, unit_of(ch - 1));
-    write_state(A.ds + unit_of(ch) * size);
-
-    // P transposed: rows i of the result are places of the image
-    for (int p = wave; p < RT * (RT + 1) / 2; p += NW) {
-      int i = 0, j = p;
-      while (j > i) j -= ++i;
-      f32x4 acc{};
-#pragma unroll
-      for (int ks = 0; ks < KD; ++ks)
-        mm<kIn>(acc, RowImg::load(lds + kQ, i, ks), RowImg::load(lds + kK, j, ks));
-      const int m = 16 * j + c;
-      float w[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * i + 4 * lg + r;
-        const float dcy = decay(gate[kGHi * C + row], gate[kGLo * C + row], gate[kGHi * C + m], gate[kGLo * C + m]);
-        w[r] = m <= row ? acc[r] * dcy * z.scale : 0.0f;
-      }
-      SqImg::store4(lds + kP, m, 16 * i + 4 * lg, w);
-    }
-    f32x4 dU[RT] = {};
+    __syncthreads();  // this chunk's fragments are there, the last one's have been read
+    const int64_t at = (unit / z.H * z.Hk + hk) * (nT * kFragElems);
+    fetch_image<nT, NW>(lds0 + 2 * kBuf, A.k_t + at, wave);
+    fetch_image<nT, NW>(lds0 + 2 * kBuf + nT * 1024, A.q_t + at, wave);
+    if (ch > 0) fetch(start(ch - 1), unit - z.H, buf ^ 1);
+    store_state<DT>(S, A.ds + unit * size, z.dk, z.dv, col);
+    const char* img = lds + buf * kBuf;
+    const float* gate = reinterpret_cast<const float*>(img + oGate * 1024);
 #pragma unroll
     for (int ks = 0; ks < KD; ++ks) {
       const Frag<kW> f = frag_of<kW>(S[2 * ks], S[2 * ks + 1]);
+      Frag<kIn> fk[RT];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) mm<kW>(dU[i], RowImg::load(lds + kK, i, ks), f);
+      for (int i = 0; i < RT; ++i) fk[i] = lds_frag<kIn, kIn>(img, i * KD + ks);
+      mm_tiles<kW, 0, RT>(dU, fk, f);
     }
 #pragma unroll
-    for (int i = 0; i < RT; ++i) dU[i] *= gate4(gate, C, kRest, 16 * i + 4 * lg);
-    __syncthreads();  // P is there
+    for (int i = 0; i < RT; ++i) dU[i] *= gate4(gate, C, kRest, rho(i, 4 * lg));
+    static_for<KC>([&](auto kt) {
+      constexpr int to = 2 * kt.value + 2;
+      const Frag<kIn> f = frag_of<kIn>(dO[2 * kt.value], dO[2 * kt.value + 1]);
+      Frag<kW> fp[RT];
 #pragma unroll
-    for (int kt = 0; kt < KC; ++kt) {
-      const Frag<kIn> f = frag_of<kIn>(dO[2 * kt], dO[2 * kt + 1]);
-#pragma unroll
-      for (int j = 0; j < RT && j < 2 * kt + 2; ++j) mm<kW>(dU[j], SqImg::load(lds + kP, j, kt), f);
-    }
-#pragma unroll
-    for (int i = 0; i < RT; ++i) dU[i] *= gate4(gate, C, kBeta, 16 * i + 4 * lg);
+      for (int j = 0; j < to; ++j) fp[j] = lds_frag<kW, kW>(img + oP * 1024, upper_frag<KC>(j, kt.value));
+      mm_tiles<kW, 0, to>(dU, fp, f);
+    });
     f32x4 dN[RT] = {};
 #pragma unroll
-    for (int kt = 0; kt < KC; ++kt) {
-      const Frag<kW> f = frag_of<kW>(dU[2 * kt], dU[2 * kt + 1]);
+    for (int i = 0; i < RT; ++i) dU[i] *= gate4(gate, C, kBeta, rho(i, 4 * lg));
+    static_for<KC>([&](auto kt) {
+      constexpr int to = 2 * kt.value + 2;
+      const Frag<kW> f = frag_of<kW>(dU[2 * kt.value], dU[2 * kt.value + 1]);
+      Frag<kW> fi[RT];
 #pragma unroll
-      for (int j = 0; j < RT && j < 2 * kt + 2; ++j) mm<kW>(dN[j], SqImg::load(lds + kInv, j, kt), f);
-    }
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * i + 4 * lg + r;
-        if (live && t < n) A.dv.row(t0 + t, h)[col] = from_f32<T>(dN[i][r]);
-      }
-    const float el = gate[kEG * C + C - 1];
+      for (int j = 0; j < to; ++j) fi[j] = lds_frag<kW, kW>(img + oInv * 1024, upper_frag<KC>(j, kt.value));
+      mm_tiles<kW, 0, to>(dN, fi, f);
+    });
+    const float el = gate[kEnd * C];
 #pragma unroll
     for (int i = 0; i < DT; ++i) S[i] *= el;
 #pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const f32x4 eg = gate4(gate, C, kEG, rho(i, 4 * lg));
+      dO[i] *= eg * z.scale;
+      dN[i] *= -eg;
+    }
+    fetch_done();
+    __syncthreads();  // K^T and Q^T are there, and the next chunk's fragments
+#pragma unroll
     for (int kt = 0; kt < KC; ++kt) {
-      const f32x4 e0 = gate4(gate, C, kEG, 32 * kt + 4 * lg), e1 = gate4(gate, C, kEG, 32 * kt + 16 + 4 * lg);
-      const Frag<kW> fo = frag_of<kW>(dO[2 * kt] * (e0 * z.scale), dO[2 * kt + 1] * (e1 * z.scale));
-      const Frag<kW> fn = frag_of<kW>(-dN[2 * kt] * e0, -dN[2 * kt + 1] * e1);
+      const Frag<kW> fo = frag_of<kW>(dO[2 * kt], dO[2 * kt + 1]), fn = frag_of<kW>(dN[2 * kt], dN[2 * kt + 1]);
+      Frag<kIn> fq[DT], fk[DT];
 #pragma unroll
       for (int i = 0; i < DT; ++i) {
-        mm<kW>(S[i], ColImg::load(lds + kQT, i, kt), fo);
-        mm<kW>(S[i], ColImg::load(lds + kKT, i, kt), fn);
+        fq[i] = lds_frag<kIn, kIn>(qt_img, i * KC + kt);
+        fk[i] = lds_frag<kIn, kIn>(kt_img, i * KC + kt);
       }
+      mm_tiles<kW, 0, DT>(S, fq, fo);
+      mm_tiles<kW, 0, DT>(S, fk, fn);
     }
   }
-  if (A.ds0) write_state(A.ds0 + of);
+  if (A.ds0) store_state<DT>(S, A.ds0 + of, z.dk, z.dv, col);
 }
 
 template <typename T>
 struct GradArgs {
-  Heads<const T> q, k, v, d_o;
-  Heads<T> dq, dk;
+  Rows k, q, d_o_rows;
+  Heads<const T> v, d_o;
+  Heads<T> dq, dk, dv;
   T *dg, *dbeta;
-  const float *g, *inverse, *gates, *states, *ds;
+  const uint16_t *k_t, *q_t, *inverse, *inverse_t, *p_t;
+  const float *g, *gates, *states, *ds;
   int64_t g_ld, dg_ld, dbeta_ld;
 };
 
-// Workgroup (tile, hk): one chunk of one key head, its value heads in turn.
+// No instruction is moved over this: what a step loads is not loaded steps before, in
+// registers that the steps between need.
+__device__ __forceinline__ void step() { __builtin_amdgcn_sched_barrier(0); }
+
+// Pair tile p: tiles i of rows and j of columns of the lower triangle, whole blocks of 32.
+__device__ __forceinline__ void pair_of(int p, int& i, int& j) {
+  i = p < 4 ? p >> 1 : 2 + ((p - 4) >> 2);
+  j = p < 4 ? p & 1 : (p - 4) & 3;
+}
+
+// Workgroup (tile, hk): one chunk of one key head, its value heads in turn. What the
+// products over channels and the chunk's squares need comes to LDS, the rest of a
+// phase's operands to registers all at once, a phase ahead where there is room: the
+// kernel's time goes into memory's latency otherwise (3583 us against ... at 16384
+// tokens of 32 heads, 128 x 128).
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(DeltaSizes z, GradArgs<T> A) {
-  constexpr int kIn = DeltaType<T>::kIn, kW = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
+__global__ __launch_bounds__(4 * (DK > DV ? DK : DV), DK > DV ? DK / 64 : DV / 64) void delta_grad_kernel(DeltaSizes z,
+                                                                                                       GradArgs<T> A) {
+  constexpr int kIn = DeltaType<T>::kIn, kW = DeltaType<T>::kOut, kSW = kStateWords, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int NW = (DK > DV ? DK : DV) / 16, RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, KV = DV / 32;
-  constexpr int kPairs = RT * (RT + 1) / 2, kMine = (kPairs + NW - 1) / NW;  // tiles of token pairs, of a wave
-  using KImg = Image<RT, KD, kIn>;  // rows t, places d
-  using VImg = Image<RT, KV, kW>;   // rows t, places v
-  using SqImg = Image<RT, KC, kW>;
-  // the three square images hold P^T and the inverse both ways, then dP * D both ways and Z + Z^T
-  constexpr int kK = 0, kN = kK + KImg::kBytes, kDN = kN + VImg::kBytes, kA = kDN + VImg::kBytes, kB = kA + SqImg::kBytes,
-                kC = kB + SqImg::kBytes, kG = kC + SqImg::kBytes, kRed = kG + kGateRows * C * 4;
-  constexpr int kPart = NW * C;  // one float per wave and row
-  constexpr int kAll = kRed + (4 * kPart + 3 * kPairs * 16 + NW) * 4;
-  __shared__ __align__(16) char lds[kAll];
-  float* gate = reinterpret_cast<float*>(lds + kG);
-  float *red_b = reinterpret_cast<float*>(lds + kRed), *red_n = red_b + kPart, *red_w = red_n + kPart, *red_q = red_w + kPart;
-  float *row_e = red_q + kPart, *col_e = row_e + kPairs * 16, *col_x = col_e + kPairs * 16, *red_s = col_x + kPairs * 16;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
+  constexpr int kFrags = KC * (KC + 1), kPairs = 2 * kFrags, kMine = (kPairs + NW - 1) / NW;  // pair tiles, of a wave
+  // 1024-byte fragments of the images
+  constexpr int nRows = RT * KD * kIn, nV = RT * KV * kW, nSq = RT * KC * kW, nTri = kFrags * kSW, nGate = (kGateRows * C * 4 + 1023) / 1024;
+  // the pair matrices take the place of the inverses and of P
+  constexpr int nShared = 3 * nSq > 3 * nTri ? 3 * nSq : 3 * nTri;
+  constexpr int oN = nRows, oDN = oN + nV, oS = oDN + nV, oGate = oS + nShared, nAll = oGate + nGate;
+  __shared__ __align__(16) char lds[nAll * 1024];
+  __shared__ float red_b[NW][C], red_n[NW][C], red_q[NW][C], red_s[NW], red_w[NW];
+  __shared__ float row_e[RT][RT][16], col_e[RT][RT][16], col_x[RT][RT][16];
+  const float* gate = reinterpret_cast<const float*>(lds + oGate * 1024);
+  char *img_a = lds + oS * 1024, *img_b = img_a + nSq * 1024, *img_c = img_b + nSq * 1024;
+  const char *inv = img_a, *inv_t = img_a + nTri * 1024, *p_t = inv_t + nTri * 1024;
+  const uint32_t lds0 = lds_address(lds);
+  const int wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tile = blockIdx.x;
   const int hk = blockIdx.y, group = z.H / z.Hk;
   int e;
   uint32_t t0, t1, s0, s1;
   if (!segment_tile<1>(z.offs, z.S, static_cast<uint32_t>(z.T), kLogC, tile, e, t0, t1, s0, s1)) return;
-  const int n = static_cast<int>(t1 - t0);
-  const int64_t size = static_cast<int64_t>(z.dk) * z.dv;
+  const int size = z.dk * z.dv;
+  const bool full = z.dk == DK && z.dv == DV;  // no padded channel
   constexpr int kThreads = 64 * NW;
-
-  // K as an image; the wave's channels of K and Q with tokens as places, in registers
-  for (int id = threadIdx.x; id < C * DK / 4; id += kThreads) {
-    const int t = id / (DK / 4), d = id % (DK / 4) * 4, m = t < n ? z.dk - d : 0;
-    Raw4<T> w;
-    w.load(A.k.row(t0 + (m > 0 ? t : 0), hk) + (m > 0 ? d : 0), m);
-    float x[4];
-    w.get(x);
-    KImg::store4(lds + kK, t, d, x);
-  }
-  Frag<kIn> kT[KC], qT[KC];
-  {
-    const int d = 16 * wave + c;
-#pragma unroll
-    for (int kt = 0; kt < KC; ++kt) {
-      f32x4 a[2], b[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = 32 * kt + 16 * u + 4 * lg + r;
-          const bool in = t < n && d < z.dk;
-          a[u][r] = in ? to_f32(A.k.row(t0 + t, hk)[d]) : 0.0f;
-          b[u][r] = in ? to_f32(A.q.row(t0 + t, hk)[d]) : 0.0f;
-        }
-      kT[kt] = frag_of<kIn>(a[0], a[1]);
-      qT[kt] = frag_of<kIn>(b[0], b[1]);
-    }
-  }
+  fetch_rows<RT, KD, kIn, NW>(lds0, A.k, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
   f32x4 dq[RT] = {}, dk[RT] = {};  // rows d, columns t
 
   for (int h = hk * group; h < (hk + 1) * group; ++h) {
+    const int wave = here(wave_), lane = here_lane(threadIdx.x) & 63, c = lane & 15, lg = lane >> 4;
+    const int n = here(static_cast<int>(t1 - t0));
     const int64_t unit = static_cast<int64_t>(tile) * z.H + h;
+    const float *ps = A.states + unit * size, *pd = A.ds + unit * size;
     __syncthreads();  // the last head's images and sums have been read
-    {
-      const float* inv = A.inverse + unit * (C * C);
-      for (int id = threadIdx.x; id < C * C / 16; id += kThreads) {
-        const int i = id / (C / 4) * 4, j = id % (C / 4) * 4;
-        const bool in = j / 16 <= i / 16;
-        f32x4 x[4] = {};
-        if (in)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x[r] = *reinterpret_cast<const f32x4*>(inv + (i + r) * C + j);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float w[4] = {x[r][0], x[r][1], x[r][2], x[r][3]}, u[4] = {x[0][r], x[1][r], x[2][r], x[3][r]};
-          SqImg::store4(lds + kB, i + r, j, w);
-          SqImg::store4(lds + kC, j + r, i, u);
-        }
-      }
-      for (int id = threadIdx.x; id < kGateRows * C; id += kThreads) gate[id] = A.gates[unit * (kGateRows * C) + id];
-    }
-    __syncthreads();
-
-    // The wave's tiles of token pairs: rows j, columns i.
-    f32x4 P[kMine], M[kMine], D[kMine];
-#pragma unroll
-    for (int m = 0; m < kMine; ++m) {
-      const int p = wave + m * NW;
-      if (p < kPairs) {
-        int i = 0, j = p;
-        while (j > i) j -= ++i;
-        f32x4 qk{}, kk{};
-        const int row = 16 * i + c;
-#pragma unroll
-        for (int ks = 0; ks < KD; ++ks) {
-          const Frag<kIn> kj = KImg::load(lds + kK, j, ks);
-          mm<kIn>(kk, kj, KImg::load(lds + kK, i, ks));
-          mm<kIn>(qk, kj, row_frag<kIn>(A.q.row(t0 + (row < n ? row : 0), hk), row < n ? z.dk : 0, ks));
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int at = 16 * j + 4 * lg + r;
-          const float dcy = decay(gate[kGHi * C + row], gate[kGLo * C + row], gate[kGHi * C + at], gate[kGLo * C + at]);
-          D[m][r] = at <= row ? dcy : 0.0f;
-          P[m][r] = at <= row ? qk[r] * dcy * z.scale : 0.0f;
-          M[m][r] = at < row ? kk[r] * dcy : 0.0f;
-          SqImg::store1(lds + kA, at, row, P[m][r]);  // rows j, places i
-          if (i != j) SqImg::store1(lds + kA, row, at, 0.0f);
-        }
-      }
-    }
-    __syncthreads();
+    fetch_image<nTri, NW>(lds0 + oS * 1024, A.inverse + unit * (nTri * kFragElems), wave);
+    fetch_image<nTri, NW>(lds0 + (oS + nTri) * 1024, A.inverse_t + unit * (nTri * kFragElems), wave);
+    fetch_image<nTri, NW>(lds0 + (oS + 2 * nTri) * 1024, A.p_t + unit * (nTri * kFragElems), wave);
+    fetch_image<nGate, NW>(lds0 + oGate * 1024, reinterpret_cast<const uint16_t*>(A.gates + unit * (kGateRows * C)), wave);
 
     // 16 columns of v: N, dU, dN
+    const int col = 16 * wave + c, vcol = col < z.dv ? col : z.dv - 1;
+    const bool live = col < z.dv;
+    T rv[RT][4], ro[RT][4];
+    float rs[DT][4], rd[DT][4];
     if (wave < DV / 16) {
-      const int col = 16 * wave + c;
-      const bool live = col < z.dv;
-      f32x4 N[RT], dN[RT] = {}, dU[RT] = {};
-      float inner = 0.0f;
-      {
-        f32x4 R[RT], dO[RT];
+      load_column<RT>(rv, A.v.row(t0, h), A.v.st, vcol, n - 1);
+      load_column<RT>(ro, A.d_o.row(t0, h), A.d_o.st, vcol, n - 1);
+      load_state<DT>(rs, ps, z.dk, z.dv, vcol);
+      load_state<DT>(rd, pd, z.dk, z.dv, vcol);
+    }
+    fetch_done();
+    __syncthreads();
+    if (wave < DV / 16) {
+      f32x4 N[RT] = {}, dN[RT] = {}, dU[RT] = {}, ks0[RT] = {}, dO[RT];
+      float inner = 0.0f, w_sum = 0.0f;
+      if (!full)
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int t = 16 * i + 4 * lg + r;
-            const bool in = live && t < n;
-            R[i][r] = in ? to_f32(A.v.row(t0 + t, h)[col]) : 0.0f;
-            dO[i][r] = in ? to_f32(A.d_o.row(t0 + t, h)[col]) : 0.0f;
-          }
-        f32x4 ks0[RT] = {};
-#pragma unroll
-        for (int ks = 0; ks < KD; ++ks) {
-          f32x4 a[2], b[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int d = 32 * ks + 16 * u + 4 * lg + r;
-              const bool in = live && d < z.dk;
-              const int64_t at = unit * size + static_cast<int64_t>(d) * z.dv + col;
-              a[u][r] = in ? A.states[at] : 0.0f;
-              b[u][r] = in ? A.ds[at] : 0.0f;
-              inner = __builtin_fmaf(a[u][r], b[u][r], inner);
-            }
-          const Frag<kW> fs = frag_of<kW>(a[0], a[1]), fd = frag_of<kW>(b[0], b[1]);
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const Frag<kIn> f = KImg::load(lds + kK, i, ks);
-            mm<kW>(ks0[i], f, fs);
-            mm<kW>(dU[i], f, fd);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          ks0[i] *= gate4(gate, C, kEG, 16 * i + 4 * lg);
-          dU[i] *= gate4(gate, C, kRest, 16 * i + 4 * lg);
-          R[i] -= ks0[i];
-          N[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-#pragma unroll
-        for (int kt = 0; kt < KC; ++kt) {
-          const Frag<kW> f = frag_of<kW>(R[2 * kt], R[2 * kt + 1]);
-#pragma unroll
-          for (int i = 2 * kt; i < RT; ++i) mm<kW>(N[i], SqImg::load(lds + kB, i, kt), f);
-        }
-        // w, before P^T dO joins dU
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const f32x4 b = gate4(gate, C, kBeta, 16 * i + 4 * lg);
+        for (int i = 0; i < DT; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float w = row16_tree(b[r] * N[i][r] * dU[i][r]);
-            if (c == 0) red_w[wave * C + 16 * i + 4 * lg + r] = w;
+            const bool in = live && rho(i, 4 * lg + r) < z.dk;
+            rs[i][r] = in ? rs[i][r] : 0.0f;
+            rd[i][r] = in ? rd[i][r] : 0.0f;
           }
-        }
 #pragma unroll
-        for (int kt = 0; kt < KC; ++kt) {
-          const Frag<kIn> f = frag_of<kIn>(dO[2 * kt], dO[2 * kt + 1]);
+      for (int ks = 0; ks < KD; ++ks) {
+        f32x4 a[2], b[2];
 #pragma unroll
-          for (int j = 0; j < RT && j < 2 * kt + 2; ++j) mm<kW>(dU[j], SqImg::load(lds + kA, j, kt), f);
-        }
-#pragma unroll
-        for (int kt = 0; kt < KC; ++kt) {
-          const f32x4 b0 = gate4(gate, C, kBeta, 32 * kt + 4 * lg), b1 = gate4(gate, C, kBeta, 32 * kt + 16 + 4 * lg);
-          const Frag<kW> f = frag_of<kW>(dU[2 * kt] * b0, dU[2 * kt + 1] * b1);
-#pragma unroll
-          for (int j = 0; j < RT && j < 2 * kt + 2; ++j) mm<kW>(dN[j], SqImg::load(lds + kC, j, kt), f);
-        }
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float b = row16_tree(dU[i][r] * N[i][r]), m = row16_tree(dN[i][r] * ks0[i][r]);
-            const int t = 16 * i + 4 * lg + r;
-            if (c == 0) {
-              red_b[wave * C + t] = b;
-              red_n[wave * C + t] = m;
-            }
-            VImg::store1(lds + kN, t, col, N[i][r]);
-            VImg::store1(lds + kDN, t, col, dN[i][r]);
+            a[u][r] = rs[2 * ks + u][r];
+            b[u][r] = rd[2 * ks + u][r];
+            inner = __builtin_fmaf(a[u][r], b[u][r], inner);
           }
+        const Frag<kW> fs = frag_of<kW>(a[0], a[1]), fd = frag_of<kW>(b[0], b[1]);
+        Frag<kIn> f[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kIn, kIn>(lds, i * KD + ks);
+        mm_tiles<kW, 0, RT>(ks0, f, fs);
+        mm_tiles<kW, 0, RT>(dU, f, fd);
+        step();
       }
+      {
+        f32x4 R[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          ks0[i] *= gate4(gate, C, kEG, rho(i, 4 * lg));
+          dU[i] *= gate4(gate, C, kRest, rho(i, 4 * lg));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            R[i][r] = live ? to_f32(rv[i][r]) - ks0[i][r] : 0.0f;
+            dO[i][r] = live ? to_f32(ro[i][r]) : 0.0f;
+          }
+        }
+        static_for<KC>([&](auto kt) {
+          const Frag<kW> f = frag_of<kW>(R[2 * kt.value], R[2 * kt.value + 1]);
+          Frag<kW> fi[RT];
+#pragma unroll
+          for (int i = 2 * kt.value; i < RT; ++i) fi[i] = lds_frag<kW, kSW>(inv, lower_frag(i, kt.value));
+          mm_tiles<kW, 2 * kt.value, RT>(N, fi, f);
+          step();
+        });
+      }
+      // w, before P^T dO joins dU: its rows' sums with those of dN * K S0, and the sum of all
+      f32x4 wn[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        wn[i] = gate4(gate, C, kBeta, rho(i, 4 * lg)) * N[i] * dU[i];
+        w_sum += (wn[i][0] + wn[i][1]) + (wn[i][2] + wn[i][3]);
+      }
+      static_for<KC>([&](auto kt) {
+        constexpr int to = 2 * kt.value + 2;
+        const Frag<kIn> f = frag_of<kIn>(dO[2 * kt.value], dO[2 * kt.value + 1]);
+        Frag<kW> fp[RT];
+#pragma unroll
+        for (int j = 0; j < to; ++j) fp[j] = lds_frag<kW, kSW>(p_t, upper_frag<KC>(j, kt.value));
+        mm_tiles<kW, 0, to>(dU, fp, f);
+        step();
+      });
+      static_for<KC>([&](auto kt) {
+        constexpr int to = 2 * kt.value + 2;
+        const Frag<kW> f = frag_of<kW>(dU[2 * kt.value] * gate4(gate, C, kBeta, rho(2 * kt.value, 4 * lg)),
+                                       dU[2 * kt.value + 1] * gate4(gate, C, kBeta, rho(2 * kt.value + 1, 4 * lg)));
+        Frag<kW> fi[RT];
+#pragma unroll
+        for (int j = 0; j < to; ++j) fi[j] = lds_frag<kW, kSW>(inv_t, upper_frag<KC>(j, kt.value));
+        mm_tiles<kW, 0, to>(dN, fi, f);
+        step();
+      });
+      // rows t = rho(i, 4 lg + r) of the images lie in lane slots 16 (v / 8) + 4 lg + r of tile i
+      char* to_n = lds + oN * 1024 + (col >> 5) * kW * 1024 + (16 * ((col >> 3) & 3) + 4 * lg) * 16 + (col & 7) * 2;
+      char* to_dn = to_n + nV * 1024;
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float b = row16_tree(dU[i][r] * N[i][r]), m = row16_tree(dN[i][r] * ks0[i][r] + wn[i][r]);
+          if (c == 0) {
+            red_b[wave][rho(i, r) + 8 * lg] = b;
+            red_n[wave][rho(i, r) + 8 * lg] = m;
+          }
+          __bf16 x[kW], y[kW];
+          split<kW>(N[i][r], x);
+          split<kW>(dN[i][r], y);
+#pragma unroll
+          for (int p = 0; p < kW; ++p) {
+            *reinterpret_cast<__bf16*>(to_n + (i * KV * kW + p) * 1024 + r * 16) = x[p];
+            *reinterpret_cast<__bf16*>(to_dn + (i * KV * kW + p) * 1024 + r * 16) = y[p];
+          }
+          if (r == 3) step();
+        }
       inner = lanes_sum<64>(inner);
-      if (lane == 0) red_s[wave] = inner;
+      w_sum = lanes_sum<64>(w_sum);
+      if (lane == 0) {
+        red_s[wave] = inner;
+        red_w[wave] = w_sum;
+      }
+    }
+    // the states' rows of this wave's channels, for the last phase
+    const int d = rho(wave, c);
+    f32x4 xs[KV][2], xd[KV][2];
+    if (wave < DT) {
+      const float *row_s = ps + static_cast<int64_t>(d < z.dk ? d : 0) * z.dv, *row_d = pd + static_cast<int64_t>(d < z.dk ? d : 0) * z.dv;
+      const bool whole = z.dv % 4 == 0;
+#pragma unroll
+      for (int kv = 0; kv < KV; ++kv)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          xs[kv][u] = load4(row_s, 32 * kv + 8 * lg + 4 * u, z.dv, whole);
+          xd[kv][u] = load4(row_d, 32 * kv + 8 * lg + 4 * u, z.dv, whole);
+        }
     }
     __syncthreads();
 
-    // The pair tiles: dP, X and what comes of them.
+    // dv: eight channels of a token from the image
+    for (int id = threadIdx.x; id < C * DV / 8; id += kThreads) {
+      const int t = id / (DV / 8), v = id % (DV / 8) * 8;
+      const char* from = lds + oDN * 1024 + image_at<KV, kW>(t, v) * 2;
+      if (t < n && v < z.dv) {
+        f32x4 x{}, y{};
 #pragma unroll
+        for (int p = kW - 1; p >= 0; --p) {
+          const bf16x8 w = *reinterpret_cast<const bf16x8*>(from + p * 1024);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[j] += static_cast<float>(w[j]);
+            y[j] += static_cast<float>(w[4 + j]);
+          }
+        }
+        T* to = A.dv.row(t0 + t, h) + v;
+        store4(to, z.dv - v, x);
+        if (z.dv > v + 4) store4(to + 4, z.dv - v - 4, y);
+      }
+    }
+
+    // The pair tiles, rows j and columns i: D, P, M, then dP, X and what comes of them.
+#pragma unroll 1
     for (int m = 0; m < kMine; ++m) {
       const int p = wave + m * NW;
-      if (p < kPairs) {
-        int i = 0, j = p;
-        while (j > i) j -= ++i;
-        f32x4 x{}, y{};
-        const int row = 16 * i + c;
+      if (p >= kPairs) break;
+      int i, j;
+      pair_of(p, i, j);
+      f32x4 qk{}, kk{}, x{}, y{};
+      const int row = rho(i, c), at0 = rho(j, 4 * lg);
+      const int ti = row < n ? row : n - 1;
+      Frag<kIn> fq[KD], fo[KV];
 #pragma unroll
-        for (int kv = 0; kv < KV; ++kv) {
-          const Frag<kW> f = VImg::load(lds + kN, j, kv);
-          mm<kW>(x, f, VImg::load(lds + kDN, i, kv));
-          mm<kW>(y, f, row_frag<kIn>(A.d_o.row(t0 + (row < n ? row : 0), h), row < n ? z.dv : 0, kv));
+      for (int ks = 0; ks < KD; ++ks) fq[ks] = A.q.template frag<kIn>(A.q.from(t0, hk), A.q.lane_off(ti), ks);
+#pragma unroll
+      for (int kv = 0; kv < KV; ++kv) fo[kv] = A.d_o_rows.template frag<kIn>(A.d_o_rows.from(t0, h), A.d_o_rows.lane_off(ti), kv);
+#pragma unroll
+      for (int kv = 0; kv < KV; ++kv) mm<kW>(x, lds_frag<kW, kW>(lds + oN * 1024, j * KV + kv), lds_frag<kW, kW>(lds + oDN * 1024, i * KV + kv));
+#pragma unroll
+      for (int ks = 0; ks < KD; ++ks) {
+        const Frag<kIn> kj = lds_frag<kIn, kIn>(lds, j * KD + ks);
+        mm<kIn>(kk, kj, lds_frag<kIn, kIn>(lds, i * KD + ks));
+        mm<kIn>(qk, kj, fq[ks]);
+      }
+#pragma unroll
+      for (int kv = 0; kv < KV; ++kv) mm<kW>(y, lds_frag<kW, kW>(lds + oN * 1024, j * KV + kv), fo[kv]);
+      const f32x4 b = gate4(gate, C, kBeta, at0), hj = gate4(gate, C, kGHi, at0), lj = gate4(gate, C, kGLo, at0);
+      const float hi = gate[kGHi * C + row], li = gate[kGLo * C + row];
+      f32x4 pd, zz, ev, mx;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int at = at0 + r;
+        const bool in = at <= row && row < n, off = at < row && row < n;
+        const float dc = in ? decay(hi, li, hj[r], lj[r]) : 0.0f;
+        const float dp = in ? b[r] * y[r] * dc * z.scale : 0.0f, bx = off ? x[r] * dc : 0.0f;
+        pd[r] = dp;
+        zz[r] = -b[r] * bx;
+        mx[r] = bx * kk[r];
+        ev[r] = dp * qk[r] - b[r] * mx[r];
+      }
+      // sums over j (rows of the tile) for row i, over i (its columns) for row j
+      const Halves s16 = halves16((ev[0] + ev[1]) + (ev[2] + ev[3]));
+      const Halves s32 = halves32(s16.a + s16.b);
+      if (lg == 0) row_e[i][j][c] = s32.a + s32.b;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float ce = row16_tree(ev[r]), cx = row16_tree(mx[r]);
+        if (c == 0) {
+          col_e[i][j][4 * lg + r] = ce;
+          col_x[i][j][4 * lg + r] = cx;
         }
-        const f32x4 b = gate4(gate, C, kBeta, 16 * j + 4 * lg);
-        f32x4 pd, zz, ev, mx;
+      }
+      // dP * D with rows i and places j, with rows j and places i; Z + Z^T
+      char* to_a = img_a + image_at<KC, kW>(row, at0) * 2;
+      char* to_b = img_b + image_at<KC, kW>(at0, row) * 2;  // (its rows at0 + r are neighbouring slots)
+      const bool diagonal = i / 2 == j / 2;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int at = 16 * j + 4 * lg + r;
-          pd[r] = at <= row ? b[r] * y[r] * D[m][r] * z.scale : 0.0f;
-          zz[r] = at < row ? -b[r] * x[r] * D[m][r] : 0.0f;
-          mx[r] = at < row ? M[m][r] * x[r] : 0.0f;
-          ev[r] = (at <= row ? b[r] * y[r] * P[m][r] : 0.0f) - b[r] * mx[r];
-        }
-        // sums over j (rows of the tile) for row i, over i (its columns) for row j
-        float s = (ev[0] + ev[1]) + (ev[2] + ev[3]);
-        const Halves s16 = halves16(s);
-        const Halves s32 = halves32(s16.a + s16.b);
-        if (lg == 0) row_e[p * 16 + c] = s32.a + s32.b;
+      for (int r = 0; r < 4; ++r) {
+        __bf16 wp[kW], wz[kW];
+        split<kW>(pd[r], wp);
+        split<kW>(zz[r], wz);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float ce = row16_tree(ev[r]), cx = row16_tree(mx[r]);
-          if (c == 0) {
-            col_e[p * 16 + 4 * lg + r] = ce;
-            col_x[p * 16 + 4 * lg + r] = cx;
-          }
-        }
-        const float w[4] = {pd[0], pd[1], pd[2], pd[3]};
-        SqImg::store4(lds + kA, row, 16 * j + 4 * lg, w);  // dP * D: rows i, places j
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int at = 16 * j + 4 * lg + r;
-          SqImg::store1(lds + kB, at, row, pd[r]);  // rows j, places i
-          if (i != j || at <= row) {
-            SqImg::store1(lds + kC, row, at, zz[r]);
-            SqImg::store1(lds + kC, at, row, zz[r]);
-          }
-          if (i != j) {  // the tiles on the far side of the diagonal
-            SqImg::store1(lds + kA, at, row, 0.0f);
-            SqImg::store1(lds + kB, row, at, 0.0f);
+        for (int w = 0; w < kW; ++w) {
+          *reinterpret_cast<__bf16*>(to_a + w * 1024 + 2 * r) = wp[w];
+          *reinterpret_cast<__bf16*>(to_b + w * 1024 + 16 * r) = wp[w];
+          if (!diagonal || at0 + r <= row) {
+            *reinterpret_cast<__bf16*>(to_a + 2 * nSq * 1024 + w * 1024 + 2 * r) = wz[w];
+            *reinterpret_cast<__bf16*>(to_b + nSq * 1024 + w * 1024 + 16 * r) = wz[w];
           }
         }
       }
@@ -526,78 +446,110 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
 
     // 16 channels of dq and dk
     if (wave < DT) {
+      Frag<kIn> kT[KC], qT[KC], fo[RT], next[RT];
+#pragma unroll
+      for (int kt = 0; kt < KC; ++kt) {
+        const int64_t at = (static_cast<int64_t>(tile) * z.Hk + hk) * (C * DK * kIn);
+        kT[kt] = image_frag<kIn, kIn>(A.k_t + at, wave * KC + kt);
+        qT[kt] = image_frag<kIn, kIn>(A.q_t + at, wave * KC + kt);
+      }
+      f32x4 q[RT];
+      const uint16_t *po = A.d_o_rows.from(t0, h), *pq = A.q.from(t0, hk) + rho(wave, 0);
+      uint32_t off[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int x = rho(i, c), t = x < n ? x : n - 1;
+        off[i] = A.d_o_rows.lane_off(t);
+        fo[i] = A.d_o_rows.template frag<kIn>(po, off[i], 0);
+        q[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = kIn - 1; u >= 0; --u) {
+          const bf16x4 w4 = load_at<bf16x4>(pq + u * A.q.words_at, A.q.lane_off(t));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) q[i][r] += static_cast<float>(w4[r]);
+        }
+      }
       f32x4 a[RT] = {}, b[RT] = {}, s[RT] = {};
-      const int d = 16 * wave + c;
-      const float* ps = A.states + unit * size + static_cast<int64_t>(d < z.dk ? d : 0) * z.dv;
-      const float* pd = A.ds + unit * size + static_cast<int64_t>(d < z.dk ? d : 0) * z.dv;
 #pragma unroll
       for (int kv = 0; kv < KV; ++kv) {
-        const Frag<kW> fs = row_frag<kW>(ps, d < z.dk ? z.dv : 0, kv), fd = row_frag<kW>(pd, d < z.dk ? z.dv : 0, kv);
+        if (!full && d >= z.dk)
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const int t = 16 * i + c;
-          mm<kW>(a[i], fs, row_frag<kIn>(A.d_o.row(t0 + (t < n ? t : 0), h), t < n ? z.dv : 0, kv));
-          mm<kW>(b[i], fs, VImg::load(lds + kDN, i, kv));
-          mm<kW>(s[i], fd, VImg::load(lds + kN, i, kv));
-        }
+          for (int u = 0; u < 2; ++u) xs[kv][u] = xd[kv][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (kv + 1 < KV)
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+            next[i] = A.d_o_rows.template frag<kIn>(po, off[i], kv + 1);
+        const Frag<kW> fs = frag_of<kW>(xs[kv][0], xs[kv][1]), fd = frag_of<kW>(xd[kv][0], xd[kv][1]);
+        Frag<kW> f[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(lds + oDN * 1024, i * KV + kv);
+        mm_tiles<kW, 0, RT, true>(b, f, fs);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(lds + oN * 1024, i * KV + kv);
+        mm_tiles<kW, 0, RT, true>(s, f, fd);
+        mm_tiles<kW, 0, RT, true>(a, fo, fs);
+        if (kv + 1 < KV)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) fo[i] = next[i];
+        step();
       }
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const int t = 16 * i + c;
+        const int t = rho(i, c);
         const float eg = gate[kEG * C + t], w = gate[kRest * C + t] * gate[kBeta * C + t];
         a[i] *= eg * z.scale;
         // this wave's part of dO . (scale e^G Q S0) = q . (its part of dq)
-        Raw4<T> rq;
-        const int m = t < n ? z.dk - 16 * wave - 4 * lg : 0;
-        rq.load(A.q.row(t0 + (m > 0 ? t : 0), hk) + (m > 0 ? 16 * wave + 4 * lg : 0), m);
-        float q[4];
-        rq.get(q);
-        float dot = (q[0] * a[i][0] + q[1] * a[i][1]) + (q[2] * a[i][2] + q[3] * a[i][3]);
-        const Halves h16 = halves16(dot);
+        const Halves h16 = halves16((q[i][0] * a[i][0] + q[i][1] * a[i][1]) + (q[i][2] * a[i][2] + q[i][3] * a[i][3]));
         const Halves h32 = halves32(h16.a + h16.b);
-        if (lg == 0) red_q[wave * C + t] = h32.a + h32.b;
+        if (lg == 0) red_q[wave][t] = h32.a + h32.b;
         dk[i] += s[i] * w - b[i] * eg;
         dq[i] += a[i];
       }
+      static_for<KC>([&](auto kt) {
+        constexpr int at = kt.value;
+        Frag<kW> f[RT];
 #pragma unroll
-      for (int kt = 0; kt < KC; ++kt)
+        for (int i = 2 * at; i < RT; ++i) f[i] = lds_frag<kW, kW>(img_a, i * KC + at);
+        mm_tiles<kW, 2 * at, RT, true>(dq, f, kT[at]);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          if (i >= 2 * kt) mm<kW>(dq[i], kT[kt], SqImg::load(lds + kA, i, kt));
-          if (i < 2 * kt + 2) mm<kW>(dk[i], qT[kt], SqImg::load(lds + kB, i, kt));
-          mm<kW>(dk[i], kT[kt], SqImg::load(lds + kC, i, kt));
-        }
+        for (int i = 0; i < 2 * at + 2; ++i) f[i] = lds_frag<kW, kW>(img_b, i * KC + at);
+        mm_tiles<kW, 0, 2 * at + 2, true>(dk, f, qT[at]);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(img_c, i * KC + at);
+        mm_tiles<kW, 0, RT, true>(dk, f, kT[at]);
+        step();
+      });
     }
     __syncthreads();
 
     // dbeta and dg, by the first wave: a lane per token
     if (wave == 0) {
-      const int t = lane < C ? lane : 0, rt = t / 16, q = t % 16;
+      const int t = lane < C ? lane : 0, rt = rho_tile(t), x = rho_row(t);
       float db = 0.0f, w = 0.0f, dG = 0.0f, inner = 0.0f;
 #pragma unroll
       for (int i = 0; i < DV / 16; ++i) {
-        db += red_b[i * C + t];
-        w += red_w[i * C + t];
-        dG -= red_n[i * C + t];
+        db += red_b[i][t];
+        w += red_w[i];
+        dG -= red_n[i][t];
         inner += red_s[i];
       }
 #pragma unroll
-      for (int i = 0; i < DT; ++i) dG += red_q[i * C + t];
-      dG -= w;
-      for (int j = 0; j <= rt; ++j) dG += row_e[(rt * (rt + 1) / 2 + j) * 16 + q];
-      for (int i = rt; i < RT; ++i) {
-        dG -= col_e[(i * (i + 1) / 2 + rt) * 16 + q];
-        db -= col_x[(i * (i + 1) / 2 + rt) * 16 + q];
+      for (int i = 0; i < DT; ++i) dG += red_q[i][t];
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        if (j / 2 <= rt / 2) dG += row_e[rt][j][x];
+        if (j / 2 >= rt / 2) {
+          dG -= col_e[j][rt][x];
+          db -= col_x[j][rt][x];
+        }
       }
       // the sums from a row to the end, in float64
-      double sum = lane < C ? static_cast<double>(dG) : 0.0, all = lane < C ? static_cast<double>(w) : 0.0;
+      double sum = lane < n ? static_cast<double>(dG) : 0.0;
+      if (lane == C - 1) sum += w + static_cast<double>(gate[kEnd * C]) * inner;
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d);
-      if (lane == C - 1) sum += all + static_cast<double>(gate[kEG * C + C - 1]) * inner;
-#pragma unroll
-      for (int d = 1; d < C; d <<= 1) {
-        const double o = __shfl_down(sum, d);
-        if (lane + d < C) sum += o;
+      for (int o = 1; o < C; o <<= 1) {
+        const double other = __shfl_down(sum, o);
+        if (lane + o < C) sum += other;
       }
       if (lane < n) {
         const bool cut = A.g[(t0 + t) * A.g_ld + h] < -104.0f;
@@ -606,10 +558,11 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
       }
     }
   }
-  if (wave < DT) {
+  if (wave_ < DT) {
+    const int lane = threadIdx.x & 63, n = static_cast<int>(t1 - t0);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const int t = 16 * i + c, d = 16 * wave + 4 * lg;
+      const int t = rho(i, lane & 15), d = rho(wave_, 4 * (lane >> 4));
       if (t < n && d < z.dk) {
         store4(A.dq.row(t0 + t, hk) + d, z.dk - d, dq[i]);
         store4(A.dk.row(t0 + t, hk) + d, z.dk - d, dk[i]);
@@ -618,34 +571,14 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
   }
 }
 
-struct Layout {
-  size_t inverse, gates, ds, all;
-};
-Layout layout_of(const DeltaSizes& z, int dtype) {
-  const int64_t C = dtype == DET_BF16 ? 64 : 32, units = delta_tiles(z.T, z.S, dtype) * z.H;
-  Layout l;
-  l.inverse = DET_WS_HEADER_BYTES;
-  l.gates = l.inverse + static_cast<size_t>(units * C * C) * 4;
-  l.ds = l.gates + align_up(static_cast<size_t>(units * kGateRows * C) * 4, 256);
-  l.all = l.ds + align_up(static_cast<size_t>(units * z.dk * z.dv) * 4, 256);
-  return l;
-}
-
 template <typename T, int DK>
 void launch_chain(const DeltaSizes& z, const ChainArgs<T>& A, hipStream_t st) {
-  int nw = 8;
-  while (nw > 1 && (static_cast<int64_t>(z.S) * z.H * ceil_div(z.dv, 16 * nw) < 256 || 16 * nw >= 2 * z.dv)) nw /= 2;
-  const int n_blocks = static_cast<int>(ceil_div(z.dv, 16 * nw));
-  const dim3 grid(static_cast<uint32_t>(z.H * n_blocks), static_cast<uint32_t>(z.S));
-#define DET_DELTA_CHAIN(NW) \
-  case NW: hipLaunchKernelGGL((delta_chain_kernel<T, DK, NW>), grid, dim3(64 * NW), 0, st, z, A, n_blocks); break;
-  switch (nw) {
-    DET_DELTA_CHAIN(1)
-    DET_DELTA_CHAIN(2)
-    DET_DELTA_CHAIN(4)
-    DET_DELTA_CHAIN(8)
-  }
-#undef DET_DELTA_CHAIN
+  const int64_t chains = static_cast<int64_t>(z.S) * z.H;
+  const int nw = chains >= 256 ? 8 : chains >= 64 ? 4 : 1;  // as in the forward
+  const dim3 grid(static_cast<uint32_t>(z.H * ceil_div(z.dv, 16 * nw)), static_cast<uint32_t>(z.S));
+  if (nw == 8) hipLaunchKernelGGL((delta_chain_kernel<T, DK, 8>), grid, dim3(512), 0, st, z, A);
+  else if (nw == 4) hipLaunchKernelGGL((delta_chain_kernel<T, DK, 4>), grid, dim3(256), 0, st, z, A);
+  else hipLaunchKernelGGL((delta_chain_kernel<T, DK, 1>), grid, dim3(64), 0, st, z, A);
 }
 
 template <typename T, int DK, int DV>
@@ -659,12 +592,12 @@ void launch_grad(const DeltaSizes& z, const GradArgs<T>& A, int dtype, hipStream
 
 using namespace detgrad;
 
-extern "C" int det_delta_rule_bwd_workspace_size(int64_t T, int64_t S, int64_t H, int64_t dk, int64_t dv, int dtype,
+extern "C" int det_delta_rule_bwd_workspace_size(int64_t T, int64_t S, int64_t Hk, int64_t H, int64_t dk, int64_t dv, int dtype,
                                                  size_t* bytes) {
   if (!bytes) return set_error(DET_ERR_INVALID_ARG, "delta_rule_bwd: bytes is NULL");
-  if (int s = delta_check_sizes("delta_rule_bwd", dtype, T, S, 1, H, dk, dv)) return s;
-  const DeltaSizes z{T, (int)S, 1, (int)H, (int)dk, (int)dv, nullptr, 0.0f};
-  *bytes = T == 0 ? 0 : layout_of(z, dtype).all;
+  if (int s = delta_check_sizes("delta_rule_bwd", dtype, T, S, Hk, H, dk, dv)) return s;
+  const DeltaSizes z{T, (int)S, (int)Hk, (int)H, (int)dk, (int)dv, nullptr, 0.0f};
+  *bytes = T == 0 ? 0 : delta_layout(z, dtype, true).all;
   return ok();
 }
 
@@ -697,7 +630,7 @@ extern "C" int det_delta_rule_bwd(const void* d_o, int64_t do_st, int64_t do_sh,
     if (T > 0 && ld > (int64_t(1) << 44) / T) return set_error(DET_ERR_UNSUPPORTED, "%s: g, beta, dg or dbeta is too large", what);
   }
   const DeltaSizes z{T, (int)S, (int)Hk, (int)H, (int)dk, (int)dv, offs, static_cast<float>(scale)};
-  const Layout l = layout_of(z, dtype);
+  const DeltaLayout l = delta_layout(z, dtype, true);
   const size_t need = T ? l.all : 0;
   if (int s = check_workspace(ws, ws_bytes, need)) return s;
   const size_t state = static_cast<size_t>(H * dk * dv) * 4;
@@ -713,23 +646,22 @@ extern "C" int det_delta_rule_bwd(const void* d_o, int64_t do_st, int64_t do_sh,
                      {"dfinal_state", range1d(dfinal_state, S * state)}};
   if (int s = check_buffers(what, outs, 7, ins, 9)) return s;
   const hipStream_t st = as_stream(stream);
-  float *inverse = nullptr, *gate = nullptr, *ds = nullptr;
-  if (T) {
-    char* p = static_cast<char*>(ws);
-    inverse = reinterpret_cast<float*>(p + l.inverse);
-    gate = reinterpret_cast<float*>(p + l.gates);
-    ds = reinterpret_cast<float*>(p + l.ds);
-    delta_prepare(z, dtype, k, k_st, k_sh, g, g_ld, beta, beta_ld, inverse, gate, st);
-  }
+  char* base = static_cast<char*>(ws);  // (no tokens: nothing there is read)
+  DeltaPrepared r{};
+  if (T)
+    r = delta_prepare(z, dtype, true, q, q_st, q_sh, k, k_st, k_sh, d_o, do_st, do_sh, g, g_ld, beta, beta_ld, base, l, st);
+  const auto words = [&](size_t at) { return reinterpret_cast<const uint16_t*>(base + at); };
+  const auto* gate = reinterpret_cast<const float*>(base + l.gates);
+  auto* ds = reinterpret_cast<float*>(base + l.ds);
 #define DET_DELTA_BWD(E)                                                                                               \
   {                                                                                                                    \
-    const Heads<const E> hq{static_cast<const E*>(q), q_st, q_sh}, hk{static_cast<const E*>(k), k_st, k_sh},           \
-        hv{static_cast<const E*>(v), v_st, v_sh}, ho{static_cast<const E*>(d_o), do_st, do_sh};                        \
-    const ChainArgs<E> A{hq, hk, ho, {static_cast<E*>(dv_out), dv_st, dv_sh}, inverse, gate, dfinal_state, ds,         \
+    const Heads<const E> hv{static_cast<const E*>(v), v_st, v_sh}, ho{static_cast<const E*>(d_o), do_st, do_sh};       \
+    const ChainArgs<E> A{r.k, ho, words(l.k_t), words(l.q_t), words(l.inverse_t), words(l.p), gate, dfinal_state, ds,  \
                          dinitial_state};                                                                              \
-    const GradArgs<E> B{hq, hk, hv, ho, {static_cast<E*>(dq), dq_st, dq_sh}, {static_cast<E*>(dk_out), dk_st, dk_sh},  \
-                        static_cast<E*>(dg), static_cast<E*>(dbeta), g, inverse, gate, states, ds, g_ld, dg_ld,        \
-                        dbeta_ld};                                                                                     \
+    const GradArgs<E> B{r.k, r.q, r.d_o, hv, ho, {static_cast<E*>(dq), dq_st, dq_sh},                                  \
+                        {static_cast<E*>(dk_out), dk_st, dk_sh}, {static_cast<E*>(dv_out), dv_st, dv_sh},              \
+                        static_cast<E*>(dg), static_cast<E*>(dbeta), words(l.k_t), words(l.q_t), words(l.inverse),     \
+                        words(l.inverse_t), words(l.p), g, gate, states, ds, g_ld, dg_ld, dbeta_ld};                   \
     if (dk <= 64) launch_chain<E, 64>(z, A, st);                                                                       \
     else launch_chain<E, 128>(z, A, st);                                                                               \
     if (T) {                                                                                                           \

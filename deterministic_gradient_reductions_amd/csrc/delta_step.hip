@@ -47,17 +47,20 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(StepArgs<T> A) {
     return;
   }
   float* p = A.state + (slot * A.H + h) * (static_cast<int64_t>(A.dk) * A.dv);
-  Raw4<float> s[kRows];
+  const bool whole = A.dv % 4 == 0;
+  f32x4 s[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int d = i * kGroups + rg;
-    s[i].load(p + (d < A.dk && nv > 0 ? static_cast<int64_t>(d) * A.dv + col : 0), d < A.dk ? nv : 0);
+    s[i] = load4(p + static_cast<int64_t>(d < A.dk ? d : 0) * A.dv, col, A.dv, whole);
   }
   if (A.slots) {  // an earlier row of this slot: that row's workgroup takes this token
     int before = 0;
     for (int j = threadIdx.x; j < b; j += kThreads) before |= A.slots[j] == slot;
     if (__syncthreads_or(before)) return;
   }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) s[i] = i * kGroups + rg < A.dk ? s[i] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for (int row = b;;) {
     float x = 0.0f, y = 0.0f;
     if (threadIdx.x < kDeltaMaxDim) {
@@ -68,8 +71,7 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(StepArgs<T> A) {
       lk[threadIdx.x] = x;
       lq[threadIdx.x] = y;
     }
-    Raw4<T> rv;
-    rv.load(A.v.row(row, h) + (nv > 0 ? col : 0), nv);
+    const f32x4 v = load4(A.v.row(row, h), col, A.dv, whole);
     const float gt = A.g[row * A.g_ld + h], bt = to_f32(A.beta[row * A.beta_ld + h]);
     const float dot = lanes_sum<64>(x * y);
     if ((threadIdx.x & 63) == 0) dots[threadIdx.x >> 6] = dot;
@@ -83,11 +85,11 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(StepArgs<T> A) {
       const int d = i * kGroups + rg;
       kd[i] = lk[d];
       const float qd = lq[d];
-      s[i].w *= a;
+      s[i] *= a;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        pk[j] = __builtin_fmaf(kd[i], s[i].w[j], pk[j]);
-        pq[j] = __builtin_fmaf(qd, s[i].w[j], pq[j]);
+        pk[j] = __builtin_fmaf(kd[i], s[i][j], pk[j]);
+        pq[j] = __builtin_fmaf(qd, s[i][j], pq[j]);
       }
     }
     part[0][rg][cg] = pk;
@@ -109,8 +111,6 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(StepArgs<T> A) {
       pk += part[0][i][cg];
       pq += part[1][i][cg];
     }
-    float v[4];
-    rv.get(v);
     f32x4 u, o;
     const float kq = dots[0] + dots[1];
 #pragma unroll
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(StepArgs<T> A) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[i].w[j] = __builtin_fmaf(kd[i], u[j], s[i].w[j]);
+      for (int j = 0; j < 4; ++j) s[i][j] = __builtin_fmaf(kd[i], u[j], s[i][j]);
     if (rg == 0 && nv > 0) store4(A.o.row(row, h) + col, nv, o);
     const int to = next_row;
     if (!A.slots || to >= A.B) break;
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(StepArgs<T> A) {
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int d = i * kGroups + rg;
-    if (d < A.dk && nv > 0) store4(p + static_cast<int64_t>(d) * A.dv + col, nv, s[i].w);
+    if (d < A.dk && nv > 0) store4(p + static_cast<int64_t>(d) * A.dv + col, nv, s[i]);
   }
 }
 

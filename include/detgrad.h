@@ -589,7 +589,7 @@ int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t dh
  *       written. o, final_state and states overlap nothing else.
  * No atomic arm. */
 int det_delta_rule_chunks(int64_t T, int64_t S, int dtype, int64_t* chunks);
-int det_delta_rule_workspace_size(int64_t T, int64_t S, int64_t H, int dtype, size_t* bytes);
+int det_delta_rule_workspace_size(int64_t T, int64_t S, int64_t Hk, int64_t H, int64_t dk, int64_t dv, int dtype, size_t* bytes);
 int det_delta_rule(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh, const void* v,
                    int64_t v_st, int64_t v_sh, const float* g, int64_t g_ld, const void* beta, int64_t beta_ld, int dtype,
                    int64_t T, int64_t Hk, int64_t H, int64_t dk, int64_t dv, const int32_t* offs, int64_t S, double scale,
@@ -608,7 +608,8 @@ int det_delta_rule(const void* q, int64_t q_st, int64_t q_sh, const void* k, int
  * decay is 0, has dg = 0. dg, dbeta: [T, H], row strides >= H.
  * ws: det_delta_rule_bwd_workspace_size() bytes; its header is neither read nor
  *     written. */
-int det_delta_rule_bwd_workspace_size(int64_t T, int64_t S, int64_t H, int64_t dk, int64_t dv, int dtype, size_t* bytes);
+int det_delta_rule_bwd_workspace_size(int64_t T, int64_t S, int64_t Hk, int64_t H, int64_t dk, int64_t dv, int dtype,
+                                      size_t* bytes);
 int det_delta_rule_bwd(const void* d_o, int64_t do_st, int64_t do_sh, const void* q, int64_t q_st, int64_t q_sh, const void* k,
                        int64_t k_st, int64_t k_sh, const void* v, int64_t v_st, int64_t v_sh, const float* g, int64_t g_ld,
                        const void* beta, int64_t beta_ld, int dtype, int64_t T, int64_t Hk, int64_t H, int64_t dk, int64_t dv,

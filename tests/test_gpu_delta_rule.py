@@ -258,8 +258,8 @@ def test_replay_under_load_with_poisoned_workspaces(dtype):
     h = make(700, [0, 300, 333, 690], 2, 4, 128, 128, dtype, seed=7)
     d = to_dev(h)
     load, first = SideLoad(64, 4), None
-    need = (dg.det_delta_rule_workspace_size(700, 3, 4, 0 if dtype == BF else 1),
-            dg.det_delta_rule_bwd_workspace_size(700, 3, 4, 128, 128, 0 if dtype == BF else 1))
+    need = (dg.det_delta_rule_workspace_size(700, 3, 2, 4, 128, 128, 0 if dtype == BF else 1),
+            dg.det_delta_rule_bwd_workspace_size(700, 3, 2, 4, 128, 128, 0 if dtype == BF else 1))
     for i in range(8):
         load.kick()
         ws = [torch.full((n // 4,), (math.nan, 3e38, -1.0)[i % 3], device="cuda").view(torch.uint8) for n in need]

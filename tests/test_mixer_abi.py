@@ -113,11 +113,11 @@ def test_sizes():
     assert L.det_delta_rule_chunks(1000, 3, 0, ctypes.byref(n)) == 0 and n.value == 1000 // 64 + 3
     assert L.det_delta_rule_chunks(1000, 3, 1, ctypes.byref(n)) == 0 and n.value == 1000 // 32 + 3
     assert L.det_delta_rule_chunks(1000, 3, 0, None) == INVALID and L.det_delta_rule_chunks(1000, 3, 5, ctypes.byref(n)) == INVALID
-    assert dg.det_delta_rule_workspace_size(0, 3, 4, 0) == 0
-    assert dg.det_delta_rule_workspace_size(1000, 3, 4, 0) >= 256 + 18 * 4 * (64 * 64 + 5 * 64) * 4
-    assert dg.det_delta_rule_bwd_workspace_size(1000, 3, 4, 64, 48, 0) >= 256 + 18 * 4 * (64 * 64 + 5 * 64 + 64 * 48) * 4
-    assert L.det_delta_rule_workspace_size(10, 1, 1, 0, None) == INVALID
-    assert L.det_delta_rule_bwd_workspace_size(10, 1, 1, 200, 8, 0, ctypes.byref(b)) == UNSUPPORTED
+    assert dg.det_delta_rule_workspace_size(0, 3, 2, 4, 64, 48, 0) == 0
+    assert dg.det_delta_rule_workspace_size(1000, 3, 2, 4, 64, 48, 0) >= 256 + 18 * 4 * (64 * 64 * 3 // 4 * 6 + 6 * 64 * 4)
+    assert dg.det_delta_rule_bwd_workspace_size(1000, 3, 2, 4, 64, 48, 0) >= 256 + 18 * 4 * (64 * 64 * 3 // 4 * 18 + 6 * 64 * 4 + 64 * 48 * 4)
+    assert L.det_delta_rule_workspace_size(10, 1, 1, 1, 8, 8, 0, None) == INVALID
+    assert L.det_delta_rule_bwd_workspace_size(10, 1, 1, 1, 200, 8, 0, ctypes.byref(b)) == UNSUPPORTED
     assert dg.det_qk_norm_bwd_workspace_size(0, 4, 2, 64) == 0
     assert dg.det_qk_norm_bwd_workspace_size(1, 4, 2, 64) >= 256 + 2 * 64 * 4
     assert L.det_qk_norm_bwd_workspace_size(10, 4, 2, 2000, ctypes.byref(b)) == UNSUPPORTED
