@@ -149,7 +149,7 @@ _SIGS = {
     "det_block_norm_bwd_workspace_size": ([_I64, _I64, ctypes.POINTER(_SZ)], _INT),
     "det_block_norm_bwd": ([_P, _I64] * 5 + [_I64] + [_P] * 5 + [_INT, _I64, _I64] + [_P, _I64] * 3 +
                            [_P] * 4 + [_SZ, _P], _INT),
-    "det_delta_rule_chunks": ([_I64, _I64, _INT, ctypes.POINTER(_I64)], _INT),
+    "det_delta_rule_states_size": ([_I64] * 4 + [_INT, ctypes.POINTER(_I64), ctypes.POINTER(_I64)], _INT),
     "det_delta_rule_workspace_size": ([_I64] * 6 + [_INT, ctypes.POINTER(_SZ)], _INT),
     "det_delta_rule": ([_P, _I64, _I64] * 3 + [_P, _I64] * 2 + [_INT] + [_I64] * 5 + [_P, _I64, _F64, _P, _P, _I64, _I64] +
                        [_P] * 3 + [_SZ, _P], _INT),
@@ -853,15 +853,21 @@ def _delta_offs(c, offs, dev: int):
 
 
 @functools.lru_cache(maxsize=256)
-def _delta_chunks(T: int, S: int, code: int) -> int:
-    n = _I64()
-    _check(lib().det_delta_rule_chunks(T, S, code, ctypes.byref(n)))
-    return n.value
+def _delta_states(T: int, S: int, dk: int, dv: int, code: int):
+    n, m = _I64(), _I64()
+    _check(lib().det_delta_rule_states_size(T, S, dk, dv, code, ctypes.byref(n), ctypes.byref(m)))
+    return n.value, m.value
 
 
 def det_delta_rule_states_shape(q, v, offs):
-    """The shape [chunks, H, dk, dv] of det_delta_rule's states for these q [T, Hk, dk], v [T, H, dv], offs [S + 1]."""
-    return (_delta_chunks(q.shape[0], offs.shape[0] - 1, _code(_context(), q, "q")), v.shape[1], q.shape[2], v.shape[2])
+    """The shape [chunks, H, floats] of det_delta_rule's states for these q [T, Hk, dk], v [T, H, dv], offs [S + 1]."""
+    n, m = _delta_states(q.shape[0], offs.shape[0] - 1, q.shape[2], v.shape[2], _code(_context(), q, "q"))
+    return n, v.shape[1], m
+
+
+def _delta_saved(c, states, T, S, H, dk, dv, code, dev):
+    n, m = _delta_states(T, S, dk, dv, code)
+    return _flat(states, "states", (n, H, m), c.f32, dev)
 
 
 @functools.lru_cache(maxsize=256)
@@ -883,7 +889,7 @@ def det_delta_rule(q, k, v, g, beta, o, offs, initial_state=None, final_state=No
     code, sh = x[-6], (S, H, dk, dv)
     p = (_flat(initial_state, "initial_state", sh, c.f32, dev), *_heads(o, "o", (T, H, dv), q.dtype, dev),
          _flat(final_state, "final_state", sh, c.f32, dev),
-         None if states is None else _flat(states, "states", (_delta_chunks(T, S, code), H, dk, dv), c.f32, dev))
+         None if states is None else _delta_saved(c, states, T, S, H, dk, dv, code, dev))
     raw = _stream_on(c, dev, stream)
     wp, wn, keep = _scratch(c, det_delta_rule_workspace_size(T, S, Hk, H, dk, dv, code), ws, dev, stream, raw)
     _run(c, dev, lib().det_delta_rule, *x, po, S, max(dk, 1) ** -0.5 if scale is None else scale, *p, wp, wn, raw)
@@ -906,7 +912,7 @@ def det_delta_rule_bwd(do, q, k, v, g, beta, offs, states, dq, dk, dv, dg, dbeta
     S, po = _delta_offs(c, offs, dev)
     code, sh, dt = x[-6], (S, H, nk, nv), q.dtype
     po3 = _heads(do, "do", (T, H, nv), dt, dev)
-    p = (_flat(states, "states", (_delta_chunks(T, S, code), H, nk, nv), c.f32, dev),
+    p = (_delta_saved(c, states, T, S, H, nk, nv, code, dev),
          _flat(dfinal_state, "dfinal_state", sh, c.f32, dev), *_heads(dq, "dq", (T, Hk, nk), dt, dev),
          *_heads(dk, "dk", (T, Hk, nk), dt, dev), *_heads(dv, "dv", (T, H, nv), dt, dev), *_rows(dg, "dg", (T, H), dt, dev),
          *_rows(dbeta, "dbeta", (T, H), dt, dev), _flat(dinitial_state, "dinitial_state", sh, c.f32, dev))

@@ -87,11 +87,11 @@ constexpr int kPrepWaves = 4;
 
 struct PrepOut {
   float* gates;
-  uint16_t *inverse, *inverse_t, *p;
+  uint16_t *inverse, *p;
 };
 
-// BWD: the inverse's image of both triangles and P transposed (rows j, places i), in the
-// words of the states; else the inverse's and P's of the lower one (rows i, places j).
+// The inverse of I + M B and P as images of rows i and places j; BWD: that of I + B M and P
+// transposed (rows j, places i), P in the words of the states too.
 template <typename T, int DK, bool BWD>
 __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSizes z, Rows k, Rows q,
                                                                      const float* __restrict__ g, int64_t g_ld,
@@ -185,13 +185,13 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSiz
 #pragma unroll
     for (int j = 0; j < RT && j / 2 <= i / 2; ++j) {
       const int col = rho(BWD ? j : i, c), row0 = rho(BWD ? i : j, 4 * lg);
-      const float hc = hi[col], lc = lo[col], bc = be[col];
+      const float hc = hi[col], lc = lo[col];
       f32x4 m;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int row = row0 + r, ti = BWD ? row : col, tj = BWD ? col : row;
         const float d = BWD ? decay(hi[row], lo[row], hc, lc) : decay(hc, lc, hi[row], lo[row]);
-        m[r] = tj < ti ? kk[i][j][r] * d * (BWD ? bc : be[row]) : 0.0f;
+        m[r] = tj < ti ? kk[i][j][r] * d * be[row] : 0.0f;  // beta of j, BWD: of i
         qk[i][j][r] = tj <= ti && ti < n ? qk[i][j][r] * d * z.scale : 0.0f;
       }
       if (BWD) {
@@ -273,8 +273,8 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSiz
       for (int r = 0; r < 4; ++r) a[(16 * i + 4 * lg + r) * kLd + 16 * j + c] = X[i][r];
   }
   wave_fence();
-  {
-    uint16_t* to = out.inverse + unit * (kFrags * kW * kFragElems);
+  uint16_t* to = out.inverse + unit * (kFrags * kW * kFragElems);
+  if (!BWD) {
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -282,9 +282,7 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSiz
         const float* p = a + rho(i, c) * kLd + 32 * m + 8 * lg;
         image_put<kW>(to, lower_frag(i, m), frag_of<kW>(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4)));
       }
-  }
-  if (BWD) {
-    uint16_t* to = out.inverse_t + unit * (kFrags * kW * kFragElems);
+  } else {
 #pragma unroll
     for (int j = 0; j < RT; ++j)
 #pragma unroll
@@ -309,7 +307,8 @@ struct FwdArgs {
   Heads<T> o;
   const uint16_t *k_t, *inverse, *p;
   const float *gates, *s0;
-  float *s1, *states;
+  float *s1, *saved;  // the final state; what the backward needs (delta_saved_floats)
+  int image_floats, saved_floats;
 };
 
 // Workgroup (x, s): value head x % H of sequence s; wave w takes the columns
@@ -371,7 +370,7 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaSizes z, FwdArg
     __syncthreads();  // this chunk's fragments are there, the last one's have been read
     fetch_image<nKT, NW>(lds0 + 2 * kBuf, A.k_t + (unit / z.H * z.Hk + hk) * (nKT * kFragElems), wave);
     if (t0 + C < r1) fetch(t0 + C, unit + z.H, buf ^ 1);
-    if (A.states) store_state<DT>(S, A.states + unit * size, z.dk, z.dv, col);
+    if (A.saved) store_state<DT>(S, A.saved + unit * A.saved_floats + A.image_floats, z.dk, z.dv, col);
     const char* img = lds + buf * kBuf;
     const float* gate = reinterpret_cast<const float*>(img + oGate * 1024);
 
@@ -398,14 +397,16 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaSizes z, FwdArg
       o[i] *= e_col;
     }
     // N, then U = beta N
-    f32x4 U[RT] = {};
+    f32x4 U[RT] = {}, nt[RT] = {};  // nt: N with rows v and columns t, for the backward
     static_for<KC>([&](auto kt) {
       const Frag<kW> f = frag_of<kW>(R[2 * kt.value], R[2 * kt.value + 1]);
       Frag<kW> fi[RT];
 #pragma unroll
       for (int i = 2 * kt.value; i < RT; ++i) fi[i] = lds_frag<kW, kW>(img + oInv * 1024, lower_frag(i, kt.value));
       mm_tiles<kW, 2 * kt.value, RT>(U, fi, f);
+      if (A.saved) mm_tiles<kOut, 2 * kt.value, RT, true>(nt, fi, f);
     });
+    if (A.saved) put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
 #pragma unroll
     for (int i = 0; i < RT; ++i) U[i] *= *reinterpret_cast<const f32x4*>(gate + kBeta * C + rho(i, 4 * lg));
     static_for<KC>([&](auto kt) {
@@ -485,7 +486,7 @@ DeltaPrepared prepare(const DeltaSizes& z, int dtype, bool bwd, const void* q, i
   r.k = rows_of<T>(z, dtype, k, k_st, k_sh, z.Hk, z.dk, at(l.k_t), at(l.k_rows), st);
   r.q = rows_of<T>(z, dtype, q, q_st, q_sh, z.Hk, z.dk, bwd ? at(l.q_t) : nullptr, at(l.q_rows), st);
   if (bwd) r.d_o = rows_of<T>(z, dtype, d_o, do_st, do_sh, z.H, z.dv, nullptr, at(l.o_rows), st);
-  const PrepOut out{reinterpret_cast<float*>(ws + l.gates), at(l.inverse), at(l.inverse_t), at(l.p)};
+  const PrepOut out{reinterpret_cast<float*>(ws + l.gates), at(l.inverse), at(l.p)};
   const int64_t units = delta_tiles(z.T, z.S, dtype) * z.H;
   if (z.dk <= 64) launch_prep<T, 64>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, out, units, st);
   else launch_prep<T, 128>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, out, units, st);
@@ -494,11 +495,12 @@ DeltaPrepared prepare(const DeltaSizes& z, int dtype, bool bwd, const void* q, i
 
 template <typename T, int DK>
 void launch_fwd(const DeltaSizes& z, const FwdArgs<T>& A, hipStream_t st) {
-  // the waves of a head in one workgroup, which share its L1 cache, where that leaves a
+  // the waves of a head in one workgroup, which share its fragments, where that leaves a
   // workgroup for each compute unit; else spread out
   const int64_t chains = static_cast<int64_t>(z.S) * z.H;
   const int nw = chains >= 256 ? 8 : chains >= 64 ? 4 : 1;
-  const dim3 grid(static_cast<uint32_t>(z.H * ceil_div(z.dv, 16 * nw)), static_cast<uint32_t>(z.S));
+  const int64_t columns = A.saved ? delta_pad(z.dv) : z.dv;  // (the images' padding is written too)
+  const dim3 grid(static_cast<uint32_t>(z.H * ceil_div(columns, 16 * nw)), static_cast<uint32_t>(z.S));
   if (nw == 8) hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 8>), grid, dim3(512), 0, st, z, A);
   else if (nw == 4) hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 4>), grid, dim3(256), 0, st, z, A);
   else hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 1>), grid, dim3(64), 0, st, z, A);
@@ -519,7 +521,6 @@ DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd) {
   };
   l.gates = take(units * kGateRows * C * 4);
   l.inverse = take(units * square * kStateWords);
-  l.inverse_t = take(bwd ? units * square * kStateWords : 0);
   l.p = take(units * square * p_words);
   l.k_t = take(tiles * z.Hk * C * dk * words * 2);
   l.q_t = take(bwd ? tiles * z.Hk * C * dk * words * 2 : 0);
@@ -527,6 +528,7 @@ DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd) {
   l.q_rows = take(z.T * z.Hk * words * dk * 2);
   l.o_rows = take(bwd ? z.T * z.H * words * dv * 2 : 0);
   l.ds = take(bwd ? units * z.dk * z.dv * 4 : 0);
+  l.dy = take(bwd ? units * delta_image_floats(z.dv, dtype) * 4 : 0);
   l.all = at;
   return l;
 }
@@ -575,10 +577,12 @@ int delta_buf(const char* what, const char* name, const void* p, int64_t T, int6
 
 using namespace detgrad;
 
-extern "C" int det_delta_rule_chunks(int64_t T, int64_t S, int dtype, int64_t* chunks) {
-  if (!chunks) return set_error(DET_ERR_INVALID_ARG, "delta_rule: chunks is NULL");
-  if (int s = delta_check_sizes("delta_rule", dtype, T, S, 1, 1, 1, 1)) return s;
+extern "C" int det_delta_rule_states_size(int64_t T, int64_t S, int64_t dk, int64_t dv, int dtype, int64_t* chunks,
+                                          int64_t* floats) {
+  if (!chunks || !floats) return set_error(DET_ERR_INVALID_ARG, "delta_rule: chunks or floats is NULL");
+  if (int s = delta_check_sizes("delta_rule", dtype, T, S, 1, 1, dk, dv)) return s;
   *chunks = delta_tiles(T, S, dtype);
+  *floats = delta_saved_floats(dk, dv, dtype);
   return ok();
 }
 
@@ -619,7 +623,7 @@ extern "C" int det_delta_rule(const void* q, int64_t q_st, int64_t q_sh, const v
   const size_t state = static_cast<size_t>(H * dk * dv) * 4;
   const Buf outs[] = {bo,
                       {"final_state", range1d(final_state, S * state)},
-                      {"states", range1d(states, delta_tiles(T, S, dtype) * state)},
+                      {"states", range1d(states, delta_tiles(T, S, dtype) * H * delta_saved_floats(dk, dv, dtype) * 4), 16},
                       {"the workspace", range1d(need ? ws : nullptr, ws_bytes)}};
   const Buf ins[] = {bq, bk, bv, buf_rows("g", g, T, H, T > 1 ? g_ld : H, 4),
                      buf_rows("beta", beta, T, H, T > 1 ? beta_ld : H, es),
@@ -637,7 +641,8 @@ extern "C" int det_delta_rule(const void* q, int64_t q_st, int64_t q_sh, const v
                        reinterpret_cast<const uint16_t*>(base + l.k_t),                                             \
                        reinterpret_cast<const uint16_t*>(base + l.inverse),                                         \
                        reinterpret_cast<const uint16_t*>(base + l.p), reinterpret_cast<const float*>(base + l.gates), \
-                       initial_state, final_state, states};                                                         \
+                       initial_state, final_state, states, (int)delta_image_floats(dv, dtype),                      \
+                       (int)delta_saved_floats(dk, dv, dtype)};                                                       \
     if (dk <= 64) launch_fwd<E, 64>(z, A, st);                                                                      \
     else launch_fwd<E, 128>(z, A, st);                                                                              \
   }

@@ -177,6 +177,10 @@ __device__ __forceinline__ constexpr int upper_frag(int j, int kt) {
   return 2 * ((j >> 1) * KC - (j >> 1) * ((j >> 1) - 1) / 2) + (j & 1) * (KC - (j >> 1)) + kt - (j >> 1);
 }
 
+// At the end of one of two ways to load the same: keeps the compiler from joining their
+// loads into one sequence with the addresses of either in registers.
+__device__ __forceinline__ void own_way() { asm volatile("; its own way" ::: "memory"); }
+
 // Four consecutive elements at .. at + 3 of a row of n, those behind it zero, loaded
 // without a branch (loads under one would be waited for one by one): whole rows (n a
 // multiple of four, the same for all) in one access, others element by element.
@@ -188,6 +192,7 @@ __device__ __forceinline__ f32x4 load4(const T* row, int at, int n, bool whole) 
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = row[at + j < n ? at + j : n - 1];
+    own_way();
   }
   f32x4 r;
 #pragma unroll
@@ -260,6 +265,27 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// Results with rows v0 + 4 g + r and columns rho(i, c) as a part of an image with rows t and
+// places v (kv fragments of 32 per row tile), zeros from place dv on, nothing behind the image's.
+template <int RT, int NP>
+__device__ __forceinline__ void put_image(const f32x4 (&x)[RT], uint16_t* image, int v0, int dv, int kv) {
+  const int lane = threadIdx.x & 63, c = lane & 15, v = v0 + 4 * (lane >> 4);
+  if (v0 >= 32 * kv) return;
+  // places v .. v + 3 of row tile 0, row c
+  uint16_t* to = image + (v >> 5) * NP * kFragElems + (16 * ((v >> 3) & 3) + c) * 8 + (v & 7);
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    uint32_t a[NP], b[NP];
+    split2<NP>(v < dv ? x[i][0] : 0.0f, v + 1 < dv ? x[i][1] : 0.0f, a);
+    split2<NP>(v + 2 < dv ? x[i][2] : 0.0f, v + 3 < dv ? x[i][3] : 0.0f, b);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const uint64_t w = a[p] | static_cast<uint64_t>(b[p]) << 32;
+      __builtin_memcpy(to + (i * kv * NP + p) * kFragElems, &w, 8);
+    }
+  }
+}
+
 // A [T, heads, dim] tensor with unit innermost stride.
 template <typename T>
 struct Heads {
@@ -288,6 +314,7 @@ __device__ __forceinline__ void load_column(T (&v)[RT][4], const T* rows, int64_
         const int t = rho(i, 4 * g + r);
         v[i][r] = rows[(t < last ? t : last) * st + col];
       }
+    own_way();
   }
 }
 // The elements d = rho(i, 4 g + r) < dk (others: the first row's) of column col of a [dk, dv] state.
@@ -309,6 +336,7 @@ __device__ __forceinline__ void load_state(float (&v)[DT][4], const float* state
         const int d = rho(i, 4 * g + r);
         v[i][r] = load_at<float>(state, static_cast<uint32_t>((d < dk ? d : 0) * dv + col) * 4u);
       }
+    own_way();
   }
 }
 template <int DT>
@@ -441,10 +469,20 @@ inline int delta_words(int dtype) { return dtype == DET_BF16 ? DeltaType<uint16_
 inline int64_t delta_tiles(int64_t T, int64_t S, int dtype) { return T / delta_chunk(dtype) + S; }
 inline int delta_pad(int64_t d) { return d <= 64 ? 64 : 128; }
 
-// Where the parts of a workspace lie. The square images: the inverse of I + M B, of both
-// triangles in the backward, and P (transposed in the backward).
+// What a forward leaves for the backward per (chunk, value head): N as an image of rows t and
+// places v in kOut words, then the state in front of the chunk, in floats.
+inline int64_t delta_image_floats(int64_t dv, int dtype) {
+  const int64_t words = dtype == DET_BF16 ? DeltaType<uint16_t>::kOut : DeltaType<float>::kOut;
+  return delta_chunk(dtype) * delta_pad(dv) * words / 2;
+}
+inline int64_t delta_saved_floats(int64_t dk, int64_t dv, int dtype) {
+  return delta_image_floats(dv, dtype) + static_cast<int64_t>(align_up(static_cast<size_t>(dk * dv), 4));
+}
+
+// Where the parts of a workspace lie. The square images: the inverse and P, transposed in
+// the backward; dy: the backward's images as N's.
 struct DeltaLayout {
-  size_t gates, inverse, inverse_t, p, k_rows, q_rows, o_rows, k_t, q_t, ds, all;
+  size_t gates, inverse, p, k_rows, q_rows, o_rows, k_t, q_t, ds, dy, all;
 };
 DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd);
 

@@ -1,23 +1,21 @@
 // det_delta_rule_bwd: the gradients of the gated delta rule, in the chunks and with the
-// notation of its forward. With X = strict(dN N^T), dP = lower(dO U^T) and dS1 the
-// gradient of the state behind the chunk:
+// notation of its forward. With A = (I + B M)^-T, dP = lower(dO U^T), X = strict(dN N^T)
+// and dS1 the gradient of the state behind the chunk:
 //
-//   dU = P^T dO + e^(G_C - G) K dS1,   dN = (I + M B)^-T B dU,   dV = dN
+//   dU = P^T dO + e^(G_C - G) K dS1,   dY = A dU,   dN = B dY,   dV = dN,   dbeta = rowsum(dY * N)
 //   dS0 = e^G_C dS1 + scale (e^G Q)^T dO - (e^G K)^T dN
-//   dQ = scale e^G dO S0^T + scale (dP * D) K
-//   dK = e^(G_C - G) U dS1^T - e^G dN S0^T + scale (dP * D)^T Q + (Z + Z^T) K,   Z = -D * X * beta_col
-//   dbeta = rowsum(dU * N) - colsum(M * X)
-//   dG = rowsum(E) - colsum(E) + rowsum(dO * scale e^G Q S0) - rowsum(dN * e^G K S0) - w,   E = dP * P - M * X * beta_col
-//        and on the chunk's last row sum(w) + e^G_C <S0, dS1>,   w = rowsum(U * e^(G_C - G) K dS1)
+//   dQ = dQ1 + scale (dP * D) K,       dQ1 = scale e^G dO S0^T
+//   dK = dK1 - dK0 + scale (dP * D)^T Q + (Z + Z^T) K,   dK1 = e^(G_C - G) U dS1^T,  dK0 = e^G dN S0^T,  Z = -D * X * beta_col
+//   dG = rowsum(E) - colsum(E) + rowsum(Q * dQ1 - K * dK0 - K * dK1),   E = dP * P - M * X * beta_col
+//        and on the chunk's last row sum(K * dK1) + e^G_C <S0, dS1>
 //   dg = the sums of dG from a row to the chunk's end
 //
 // Nothing is divided by beta or by a decay. After the forward's two preparing kernels
-// (with P and the inverse transposed too) one kernel walks a sequence's chunks backwards
-// as the forward's walks them (16 columns of v per wave, dS in registers) and writes
-// every chunk's dS1, and one takes all chunks side by side: it forms N, dU and dN of its
-// chunk again and the sums over v and over token pairs. There a wave owns 16 columns of
-// v first (N, dN), then tiles of token pairs, then 16 channels of dQ and dK; N, dN and
-// the pair matrices change hands in LDS as images.
+// (with the transposes) one kernel walks a sequence's chunks backwards as the forward's
+// walks them (16 columns of v per wave, dS in registers): it writes dV, every chunk's
+// dS1, and dY as an image, as the forward left N. The last kernel takes all chunks side by
+// side: in it a wave owns tiles of token pairs first, then 16 channels of dQ and dK;
+// the pair matrices change hands in LDS.
 #include "delta.hpp"
 
 namespace detgrad {
@@ -31,16 +29,19 @@ template <typename T>
 struct ChainArgs {
   Rows k;
   Heads<const T> d_o;
+  Heads<T> dv;
   const uint16_t *k_t, *q_t, *inverse_t, *p_t;
   const float *gates, *ds1;
   float *ds, *ds0;  // every chunk's dS1, the initial state's gradient
+  uint16_t* dy;
 };
 
 // Workgroups, waves and buffers as in the forward's chain; K^T and Q^T have one buffer.
 template <typename T, int DK, int NW>
 __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaSizes z, ChainArgs<T> A) {
-  constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
+  constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords, kFrags = KC * (KC + 1);
+  const int DVP = z.dv <= 64 ? 64 : 128;
   constexpr int nRows = RT * KD * kIn, nSq = kFrags * kW, nGate = (kGateRows * C * 4 + 1023) / 1024, nT = DT * KC * kIn;
   constexpr int oInv = nRows, oP = oInv + nSq, oGate = oP + nSq, kBuf = (oGate + nGate) * 1024;
   __shared__ __align__(16) char lds[2 * kBuf + 2 * nT * 1024];
@@ -109,9 +110,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaSizes z, Chai
       for (int j = 0; j < to; ++j) fp[j] = lds_frag<kW, kW>(img + oP * 1024, upper_frag<KC>(j, kt.value));
       mm_tiles<kW, 0, to>(dU, fp, f);
     });
-    f32x4 dN[RT] = {};
-#pragma unroll
-    for (int i = 0; i < RT; ++i) dU[i] *= gate4(gate, C, kBeta, rho(i, 4 * lg));
+    f32x4 dN[RT] = {}, yt[RT] = {};  // dY, and dY with rows v and columns t
     static_for<KC>([&](auto kt) {
       constexpr int to = 2 * kt.value + 2;
       const Frag<kW> f = frag_of<kW>(dU[2 * kt.value], dU[2 * kt.value + 1]);
@@ -119,7 +118,15 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaSizes z, Chai
 #pragma unroll
       for (int j = 0; j < to; ++j) fi[j] = lds_frag<kW, kW>(img + oInv * 1024, upper_frag<KC>(j, kt.value));
       mm_tiles<kW, 0, to>(dN, fi, f);
+      mm_tiles<kOut, 0, to, true>(yt, fi, f);
     });
+    put_image<RT, kOut>(yt, A.dy + unit * (C * DVP * kOut), v0, z.dv, DVP / 32);
+    const int n = r1 - start(ch) < static_cast<uint32_t>(C) ? static_cast<int>(r1 - start(ch)) : C;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int t = rho(i, c);
+      if (t < n) store4(A.dv.row(start(ch) + t, h) + v0 + 4 * lg, z.dv - v0 - 4 * lg, yt[i] * gate[kBeta * C + t]);
+    }
     const float el = gate[kEnd * C];
 #pragma unroll
     for (int i = 0; i < DT; ++i) S[i] *= el;
@@ -127,7 +134,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaSizes z, Chai
     for (int i = 0; i < RT; ++i) {
       const f32x4 eg = gate4(gate, C, kEG, rho(i, 4 * lg));
       dO[i] *= eg * z.scale;
-      dN[i] *= -eg;
+      dN[i] *= -eg * gate4(gate, C, kBeta, rho(i, 4 * lg));
     }
     fetch_done();
     __syncthreads();  // K^T and Q^T are there, and the next chunk's fragments
@@ -149,13 +156,13 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaSizes z, Chai
 
 template <typename T>
 struct GradArgs {
-  Rows k, q, d_o_rows;
-  Heads<const T> v, d_o;
-  Heads<T> dq, dk, dv;
+  Rows k, q, d_o;
+  Heads<T> dq, dk;
   T *dg, *dbeta;
-  const uint16_t *k_t, *q_t, *inverse, *inverse_t, *p_t;
-  const float *g, *gates, *states, *ds;
+  const uint16_t *k_t, *q_t, *dy;
+  const float *g, *gates, *saved, *ds;
   int64_t g_ld, dg_ld, dbeta_ld;
+  int image_floats, saved_floats;
 };
 
 // No instruction is moved over this: what a step loads is not loaded steps before, in
@@ -168,28 +175,22 @@ __device__ __forceinline__ void pair_of(int p, int& i, int& j) {
   j = p < 4 ? p & 1 : (p - 4) & 3;
 }
 
-// Workgroup (tile, hk): one chunk of one key head, its value heads in turn. What the
-// products over channels and the chunk's squares need comes to LDS, the rest of a
-// phase's operands to registers all at once, a phase ahead where there is room: the
-// kernel's time goes into memory's latency otherwise (3583 us against ... at 16384
-// tokens of 32 heads, 128 x 128).
+// Workgroup (tile, hk): one chunk of one key head, its value heads in turn. N, dY, K and
+// dO come to LDS past the registers, the states' rows into registers meanwhile.
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(4 * (DK > DV ? DK : DV), DK > DV ? DK / 64 : DV / 64) void delta_grad_kernel(DeltaSizes z,
-                                                                                                       GradArgs<T> A) {
-  constexpr int kIn = DeltaType<T>::kIn, kW = DeltaType<T>::kOut, kSW = kStateWords, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
+__global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(DeltaSizes z, GradArgs<T> A) {
+  constexpr int kIn = DeltaType<T>::kIn, kW = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int NW = (DK > DV ? DK : DV) / 16, RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, KV = DV / 32;
   constexpr int kFrags = KC * (KC + 1), kPairs = 2 * kFrags, kMine = (kPairs + NW - 1) / NW;  // pair tiles, of a wave
   // 1024-byte fragments of the images
-  constexpr int nRows = RT * KD * kIn, nV = RT * KV * kW, nSq = RT * KC * kW, nTri = kFrags * kSW, nGate = (kGateRows * C * 4 + 1023) / 1024;
-  // the pair matrices take the place of the inverses and of P
-  constexpr int nShared = 3 * nSq > 3 * nTri ? 3 * nSq : 3 * nTri;
-  constexpr int oN = nRows, oDN = oN + nV, oS = oDN + nV, oGate = oS + nShared, nAll = oGate + nGate;
-  __shared__ __align__(16) char lds[nAll * 1024];
-  __shared__ float red_b[NW][C], red_n[NW][C], red_q[NW][C], red_s[NW], red_w[NW];
-  __shared__ float row_e[RT][RT][16], col_e[RT][RT][16], col_x[RT][RT][16];
+  constexpr int nK = RT * KD * kIn, nO = RT * KV * kIn, nV = RT * KV * kW, nTri = kFrags * kW, nSq = RT * KC * kW,
+                nGate = (kGateRows * C * 4 + 1023) / 1024;
+  constexpr int oO = nK, oN = oO + nO, oY = oN + nV, oA = oY + nV, oB = oA + nTri, oZ = oB + nTri, oGate = oZ + nSq;
+  __shared__ __align__(16) char lds[(oGate + nGate) * 1024];
+  __shared__ float red_q[NW][C], red_s[NW], red_w[NW], diag[C];
+  __shared__ float row_e[RT][RT][16], col_e[RT][RT][16];
   const float* gate = reinterpret_cast<const float*>(lds + oGate * 1024);
-  char *img_a = lds + oS * 1024, *img_b = img_a + nSq * 1024, *img_c = img_b + nSq * 1024;
-  const char *inv = img_a, *inv_t = img_a + nTri * 1024, *p_t = inv_t + nTri * 1024;
+  char *img_a = lds + oA * 1024, *img_b = lds + oB * 1024, *img_z = lds + oZ * 1024;
   const uint32_t lds0 = lds_address(lds);
   const int wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tile = blockIdx.x;
@@ -198,8 +199,6 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV), DK > DV ? DK / 64 : DV / 6
   uint32_t t0, t1, s0, s1;
   if (!segment_tile<1>(z.offs, z.S, static_cast<uint32_t>(z.T), kLogC, tile, e, t0, t1, s0, s1)) return;
   const int size = z.dk * z.dv;
-  const bool full = z.dk == DK && z.dv == DV;  // no padded channel
-  constexpr int kThreads = 64 * NW;
   fetch_rows<RT, KD, kIn, NW>(lds0, A.k, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
   f32x4 dq[RT] = {}, dk[RT] = {};  // rows d, columns t
 
@@ -207,169 +206,42 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV), DK > DV ? DK / 64 : DV / 6
     const int wave = here(wave_), lane = here_lane(threadIdx.x) & 63, c = lane & 15, lg = lane >> 4;
     const int n = here(static_cast<int>(t1 - t0));
     const int64_t unit = static_cast<int64_t>(tile) * z.H + h;
-    const float *ps = A.states + unit * size, *pd = A.ds + unit * size;
+    const float *saved = A.saved + unit * A.saved_floats, *ps = saved + A.image_floats, *pd = A.ds + unit * size;
     __syncthreads();  // the last head's images and sums have been read
-    fetch_image<nTri, NW>(lds0 + oS * 1024, A.inverse + unit * (nTri * kFragElems), wave);
-    fetch_image<nTri, NW>(lds0 + (oS + nTri) * 1024, A.inverse_t + unit * (nTri * kFragElems), wave);
-    fetch_image<nTri, NW>(lds0 + (oS + 2 * nTri) * 1024, A.p_t + unit * (nTri * kFragElems), wave);
+    fetch_image<nV, NW>(lds0 + oN * 1024, reinterpret_cast<const uint16_t*>(saved), wave);
+    fetch_image<nV, NW>(lds0 + oY * 1024, A.dy + unit * (nV * kFragElems), wave);
+    fetch_rows<RT, KV, kIn, NW>(lds0 + oO * 1024, A.d_o, t0, n - 1, h, wave);
     fetch_image<nGate, NW>(lds0 + oGate * 1024, reinterpret_cast<const uint16_t*>(A.gates + unit * (kGateRows * C)), wave);
-
-    // 16 columns of v: N, dU, dN
-    const int col = 16 * wave + c, vcol = col < z.dv ? col : z.dv - 1;
-    const bool live = col < z.dv;
-    T rv[RT][4], ro[RT][4];
-    float rs[DT][4], rd[DT][4];
-    if (wave < DV / 16) {
-      load_column<RT>(rv, A.v.row(t0, h), A.v.st, vcol, n - 1);
-      load_column<RT>(ro, A.d_o.row(t0, h), A.d_o.st, vcol, n - 1);
-      load_state<DT>(rs, ps, z.dk, z.dv, vcol);
-      load_state<DT>(rd, pd, z.dk, z.dv, vcol);
-    }
-    fetch_done();
-    __syncthreads();
-    if (wave < DV / 16) {
-      f32x4 N[RT] = {}, dN[RT] = {}, dU[RT] = {}, ks0[RT] = {}, dO[RT];
-      float inner = 0.0f, w_sum = 0.0f;
-      if (!full)
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const bool in = live && rho(i, 4 * lg + r) < z.dk;
-            rs[i][r] = in ? rs[i][r] : 0.0f;
-            rd[i][r] = in ? rd[i][r] : 0.0f;
-          }
-#pragma unroll
-      for (int ks = 0; ks < KD; ++ks) {
-        f32x4 a[2], b[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            a[u][r] = rs[2 * ks + u][r];
-            b[u][r] = rd[2 * ks + u][r];
-            inner = __builtin_fmaf(a[u][r], b[u][r], inner);
-          }
-        const Frag<kW> fs = frag_of<kW>(a[0], a[1]), fd = frag_of<kW>(b[0], b[1]);
-        Frag<kIn> f[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kIn, kIn>(lds, i * KD + ks);
-        mm_tiles<kW, 0, RT>(ks0, f, fs);
-        mm_tiles<kW, 0, RT>(dU, f, fd);
-        step();
-      }
-      {
-        f32x4 R[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          ks0[i] *= gate4(gate, C, kEG, rho(i, 4 * lg));
-          dU[i] *= gate4(gate, C, kRest, rho(i, 4 * lg));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            R[i][r] = live ? to_f32(rv[i][r]) - ks0[i][r] : 0.0f;
-            dO[i][r] = live ? to_f32(ro[i][r]) : 0.0f;
-          }
-        }
-        static_for<KC>([&](auto kt) {
-          const Frag<kW> f = frag_of<kW>(R[2 * kt.value], R[2 * kt.value + 1]);
-          Frag<kW> fi[RT];
-#pragma unroll
-          for (int i = 2 * kt.value; i < RT; ++i) fi[i] = lds_frag<kW, kSW>(inv, lower_frag(i, kt.value));
-          mm_tiles<kW, 2 * kt.value, RT>(N, fi, f);
-          step();
-        });
-      }
-      // w, before P^T dO joins dU: its rows' sums with those of dN * K S0, and the sum of all
-      f32x4 wn[RT];
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        wn[i] = gate4(gate, C, kBeta, rho(i, 4 * lg)) * N[i] * dU[i];
-        w_sum += (wn[i][0] + wn[i][1]) + (wn[i][2] + wn[i][3]);
-      }
-      static_for<KC>([&](auto kt) {
-        constexpr int to = 2 * kt.value + 2;
-        const Frag<kIn> f = frag_of<kIn>(dO[2 * kt.value], dO[2 * kt.value + 1]);
-        Frag<kW> fp[RT];
-#pragma unroll
-        for (int j = 0; j < to; ++j) fp[j] = lds_frag<kW, kSW>(p_t, upper_frag<KC>(j, kt.value));
-        mm_tiles<kW, 0, to>(dU, fp, f);
-        step();
-      });
-      static_for<KC>([&](auto kt) {
-        constexpr int to = 2 * kt.value + 2;
-        const Frag<kW> f = frag_of<kW>(dU[2 * kt.value] * gate4(gate, C, kBeta, rho(2 * kt.value, 4 * lg)),
-                                       dU[2 * kt.value + 1] * gate4(gate, C, kBeta, rho(2 * kt.value + 1, 4 * lg)));
-        Frag<kW> fi[RT];
-#pragma unroll
-        for (int j = 0; j < to; ++j) fi[j] = lds_frag<kW, kSW>(inv_t, upper_frag<KC>(j, kt.value));
-        mm_tiles<kW, 0, to>(dN, fi, f);
-        step();
-      });
-      // rows t = rho(i, 4 lg + r) of the images lie in lane slots 16 (v / 8) + 4 lg + r of tile i
-      char* to_n = lds + oN * 1024 + (col >> 5) * kW * 1024 + (16 * ((col >> 3) & 3) + 4 * lg) * 16 + (col & 7) * 2;
-      char* to_dn = to_n + nV * 1024;
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float b = row16_tree(dU[i][r] * N[i][r]), m = row16_tree(dN[i][r] * ks0[i][r] + wn[i][r]);
-          if (c == 0) {
-            red_b[wave][rho(i, r) + 8 * lg] = b;
-            red_n[wave][rho(i, r) + 8 * lg] = m;
-          }
-          __bf16 x[kW], y[kW];
-          split<kW>(N[i][r], x);
-          split<kW>(dN[i][r], y);
-#pragma unroll
-          for (int p = 0; p < kW; ++p) {
-            *reinterpret_cast<__bf16*>(to_n + (i * KV * kW + p) * 1024 + r * 16) = x[p];
-            *reinterpret_cast<__bf16*>(to_dn + (i * KV * kW + p) * 1024 + r * 16) = y[p];
-          }
-          if (r == 3) step();
-        }
-      inner = lanes_sum<64>(inner);
-      w_sum = lanes_sum<64>(w_sum);
-      if (lane == 0) {
-        red_s[wave] = inner;
-        red_w[wave] = w_sum;
-      }
-    }
-    // the states' rows of this wave's channels, for the last phase
+    // the states' rows of this wave's channels, for the second phase
     const int d = rho(wave, c);
     f32x4 xs[KV][2], xd[KV][2];
     if (wave < DT) {
-      const float *row_s = ps + static_cast<int64_t>(d < z.dk ? d : 0) * z.dv, *row_d = pd + static_cast<int64_t>(d < z.dk ? d : 0) * z.dv;
-      const bool whole = z.dv % 4 == 0;
+      const uint32_t off = static_cast<uint32_t>((d < z.dk ? d : 0) * z.dv) * 4u;
+      if (z.dv == DV) {
 #pragma unroll
-      for (int kv = 0; kv < KV; ++kv)
+        for (int kv = 0; kv < KV; ++kv)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          xs[kv][u] = load4(row_s, 32 * kv + 8 * lg + 4 * u, z.dv, whole);
-          xd[kv][u] = load4(row_d, 32 * kv + 8 * lg + 4 * u, z.dv, whole);
-        }
-    }
-    __syncthreads();
-
-    // dv: eight channels of a token from the image
-    for (int id = threadIdx.x; id < C * DV / 8; id += kThreads) {
-      const int t = id / (DV / 8), v = id % (DV / 8) * 8;
-      const char* from = lds + oDN * 1024 + image_at<KV, kW>(t, v) * 2;
-      if (t < n && v < z.dv) {
-        f32x4 x{}, y{};
-#pragma unroll
-        for (int p = kW - 1; p >= 0; --p) {
-          const bf16x8 w = *reinterpret_cast<const bf16x8*>(from + p * 1024);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[j] += static_cast<float>(w[j]);
-            y[j] += static_cast<float>(w[4 + j]);
+          for (int u = 0; u < 2; ++u) {
+            xs[kv][u] = load_at<f32x4>(ps + 32 * kv + 4 * u, off + 32 * lg);
+            xd[kv][u] = load_at<f32x4>(pd + 32 * kv + 4 * u, off + 32 * lg);
           }
-        }
-        T* to = A.dv.row(t0 + t, h) + v;
-        store4(to, z.dv - v, x);
-        if (z.dv > v + 4) store4(to + 4, z.dv - v - 4, y);
+      } else {
+#pragma unroll
+        for (int kv = 0; kv < KV; ++kv)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int v = 32 * kv + 8 * lg + 4 * u + r;
+              const float x = load_at<float>(ps, off + 4u * (v < z.dv ? v : 0)), y = load_at<float>(pd, off + 4u * (v < z.dv ? v : 0));
+              xs[kv][u][r] = v < z.dv ? x : 0.0f;
+              xd[kv][u][r] = v < z.dv ? y : 0.0f;
+            }
+        own_way();
       }
     }
+    fetch_done();
+    __syncthreads();
 
     // The pair tiles, rows j and columns i: D, P, M, then dP, X and what comes of them.
 #pragma unroll 1
@@ -380,35 +252,34 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV), DK > DV ? DK / 64 : DV / 6
       pair_of(p, i, j);
       f32x4 qk{}, kk{}, x{}, y{};
       const int row = rho(i, c), at0 = rho(j, 4 * lg);
-      const int ti = row < n ? row : n - 1;
-      Frag<kIn> fq[KD], fo[KV];
+      Frag<kIn> fq[KD];
 #pragma unroll
-      for (int ks = 0; ks < KD; ++ks) fq[ks] = A.q.template frag<kIn>(A.q.from(t0, hk), A.q.lane_off(ti), ks);
+      for (int ks = 0; ks < KD; ++ks) fq[ks] = A.q.template frag<kIn>(A.q.from(t0, hk), A.q.lane_off(row < n ? row : n - 1), ks);
 #pragma unroll
-      for (int kv = 0; kv < KV; ++kv) fo[kv] = A.d_o_rows.template frag<kIn>(A.d_o_rows.from(t0, h), A.d_o_rows.lane_off(ti), kv);
-#pragma unroll
-      for (int kv = 0; kv < KV; ++kv) mm<kW>(x, lds_frag<kW, kW>(lds + oN * 1024, j * KV + kv), lds_frag<kW, kW>(lds + oDN * 1024, i * KV + kv));
+      for (int kv = 0; kv < KV; ++kv) {
+        const Frag<kW> f = lds_frag<kW, kW>(lds + oN * 1024, j * KV + kv);
+        mm<kW>(x, f, lds_frag<kW, kW>(lds + oY * 1024, i * KV + kv));
+        mm<kW>(y, f, lds_frag<kIn, kIn>(lds + oO * 1024, i * KV + kv));
+      }
 #pragma unroll
       for (int ks = 0; ks < KD; ++ks) {
         const Frag<kIn> kj = lds_frag<kIn, kIn>(lds, j * KD + ks);
         mm<kIn>(kk, kj, lds_frag<kIn, kIn>(lds, i * KD + ks));
         mm<kIn>(qk, kj, fq[ks]);
       }
-#pragma unroll
-      for (int kv = 0; kv < KV; ++kv) mm<kW>(y, lds_frag<kW, kW>(lds + oN * 1024, j * KV + kv), fo[kv]);
       const f32x4 b = gate4(gate, C, kBeta, at0), hj = gate4(gate, C, kGHi, at0), lj = gate4(gate, C, kGLo, at0);
-      const float hi = gate[kGHi * C + row], li = gate[kGLo * C + row];
-      f32x4 pd, zz, ev, mx;
+      const float hi = gate[kGHi * C + row], li = gate[kGLo * C + row], bi = gate[kBeta * C + row];
+      f32x4 pd, zz, ev;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int at = at0 + r;
+        if (at == row) diag[row] = x[r];  // dY . N of one token
         const bool in = at <= row && row < n, off = at < row && row < n;
         const float dc = in ? decay(hi, li, hj[r], lj[r]) : 0.0f;
-        const float dp = in ? b[r] * y[r] * dc * z.scale : 0.0f, bx = off ? x[r] * dc : 0.0f;
+        const float dp = in ? b[r] * y[r] * dc * z.scale : 0.0f, bx = off ? b[r] * bi * x[r] * dc : 0.0f;
         pd[r] = dp;
-        zz[r] = -b[r] * bx;
-        mx[r] = bx * kk[r];
-        ev[r] = dp * qk[r] - b[r] * mx[r];
+        zz[r] = -bx;
+        ev[r] = dp * qk[r] - bx * kk[r];
       }
       // sums over j (rows of the tile) for row i, over i (its columns) for row j
       const Halves s16 = halves16((ev[0] + ev[1]) + (ev[2] + ev[3]));
@@ -416,15 +287,14 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV), DK > DV ? DK / 64 : DV / 6
       if (lg == 0) row_e[i][j][c] = s32.a + s32.b;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float ce = row16_tree(ev[r]), cx = row16_tree(mx[r]);
-        if (c == 0) {
-          col_e[i][j][4 * lg + r] = ce;
-          col_x[i][j][4 * lg + r] = cx;
-        }
+        const float ce = row16_tree(ev[r]);
+        if (c == 0) col_e[i][j][4 * lg + r] = ce;
       }
-      // dP * D with rows i and places j, with rows j and places i; Z + Z^T
-      char* to_a = img_a + image_at<KC, kW>(row, at0) * 2;
-      char* to_b = img_b + image_at<KC, kW>(at0, row) * 2;  // (its rows at0 + r are neighbouring slots)
+      // dP * D with rows i and places j, with rows j and places i; Z + Z^T. Row tile i, row c, places at0 .. of
+      // fragment j / 2, and row tile j, rows 4 lg + r, place `row` of fragment i / 2:
+      const int in_a = (16 * lg + c) * 16 + (j & 1) * 8, in_b = (16 * (c >> 2) + 4 * lg) * 16 + (4 * (i & 1) + (c & 3)) * 2;
+      char *to_a = img_a + lower_frag(i, j >> 1) * kW * 1024 + in_a, *to_b = img_b + upper_frag<KC>(j, i >> 1) * kW * 1024 + in_b;
+      char *to_z = img_z + (i * KC + (j >> 1)) * kW * 1024 + in_a, *to_zt = img_z + (j * KC + (i >> 1)) * kW * 1024 + in_b;
       const bool diagonal = i / 2 == j / 2;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -436,8 +306,8 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV), DK > DV ? DK / 64 : DV / 6
           *reinterpret_cast<__bf16*>(to_a + w * 1024 + 2 * r) = wp[w];
           *reinterpret_cast<__bf16*>(to_b + w * 1024 + 16 * r) = wp[w];
           if (!diagonal || at0 + r <= row) {
-            *reinterpret_cast<__bf16*>(to_a + 2 * nSq * 1024 + w * 1024 + 2 * r) = wz[w];
-            *reinterpret_cast<__bf16*>(to_b + nSq * 1024 + w * 1024 + 16 * r) = wz[w];
+            *reinterpret_cast<__bf16*>(to_z + w * 1024 + 2 * r) = wz[w];
+            *reinterpret_cast<__bf16*>(to_zt + w * 1024 + 16 * r) = wz[w];
           }
         }
       }
@@ -446,76 +316,95 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV), DK > DV ? DK / 64 : DV / 6
 
     // 16 channels of dq and dk
     if (wave < DT) {
-      Frag<kIn> kT[KC], qT[KC], fo[RT], next[RT];
+      Frag<kIn> kT[KC], qT[KC];
+      const int64_t at = (static_cast<int64_t>(tile) * z.Hk + hk) * (C * DK * kIn);
 #pragma unroll
       for (int kt = 0; kt < KC; ++kt) {
-        const int64_t at = (static_cast<int64_t>(tile) * z.Hk + hk) * (C * DK * kIn);
         kT[kt] = image_frag<kIn, kIn>(A.k_t + at, wave * KC + kt);
         qT[kt] = image_frag<kIn, kIn>(A.q_t + at, wave * KC + kt);
       }
-      f32x4 q[RT];
-      const uint16_t *po = A.d_o_rows.from(t0, h), *pq = A.q.from(t0, hk) + rho(wave, 0);
-      uint32_t off[RT];
+      bf16x4 wq[RT][kIn];  // four channels of Q of a token
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const int x = rho(i, c), t = x < n ? x : n - 1;
-        off[i] = A.d_o_rows.lane_off(t);
-        fo[i] = A.d_o_rows.template frag<kIn>(po, off[i], 0);
-        q[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const int x = rho(i, c);
+        const uint32_t off = A.q.lane_off(x < n ? x : n - 1);
 #pragma unroll
-        for (int u = kIn - 1; u >= 0; --u) {
-          const bf16x4 w4 = load_at<bf16x4>(pq + u * A.q.words_at, A.q.lane_off(t));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) q[i][r] += static_cast<float>(w4[r]);
-        }
+        for (int u = 0; u < kIn; ++u) wq[i][u] = load_at<bf16x4>(A.q.from(t0, hk) + u * A.q.words_at + rho(wave, 0), off);
       }
       f32x4 a[RT] = {}, b[RT] = {}, s[RT] = {};
+      float inner = 0.0f, w_sum = 0.0f;
 #pragma unroll
       for (int kv = 0; kv < KV; ++kv) {
-        if (!full && d >= z.dk)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) xs[kv][u] = xd[kv][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (kv + 1 < KV)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < RT; ++i)
-            next[i] = A.d_o_rows.template frag<kIn>(po, off[i], kv + 1);
+          for (int r = 0; r < 4; ++r) {
+            xs[kv][u][r] = d < z.dk ? xs[kv][u][r] : 0.0f;
+            xd[kv][u][r] = d < z.dk ? xd[kv][u][r] : 0.0f;
+            inner = __builtin_fmaf(xs[kv][u][r], xd[kv][u][r], inner);
+          }
         const Frag<kW> fs = frag_of<kW>(xs[kv][0], xs[kv][1]), fd = frag_of<kW>(xd[kv][0], xd[kv][1]);
         Frag<kW> f[RT];
+        Frag<kIn> fo[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(lds + oDN * 1024, i * KV + kv);
+        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(lds + oY * 1024, i * KV + kv);
         mm_tiles<kW, 0, RT, true>(b, f, fs);
 #pragma unroll
         for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(lds + oN * 1024, i * KV + kv);
         mm_tiles<kW, 0, RT, true>(s, f, fd);
-        mm_tiles<kW, 0, RT, true>(a, fo, fs);
-        if (kv + 1 < KV)
 #pragma unroll
-          for (int i = 0; i < RT; ++i) fo[i] = next[i];
+        for (int i = 0; i < RT; ++i) fo[i] = lds_frag<kIn, kIn>(lds + oO * 1024, i * KV + kv);
+        mm_tiles<kW, 0, RT, true>(a, fo, fs);
         step();
       }
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         const int t = rho(i, c);
-        const float eg = gate[kEG * C + t], w = gate[kRest * C + t] * gate[kBeta * C + t];
+        const float eg = gate[kEG * C + t], bt = gate[kBeta * C + t];
         a[i] *= eg * z.scale;
-        // this wave's part of dO . (scale e^G Q S0) = q . (its part of dq)
-        const Halves h16 = halves16((q[i][0] * a[i][0] + q[i][1] * a[i][1]) + (q[i][2] * a[i][2] + q[i][3] * a[i][3]));
+        b[i] *= eg * bt;
+        s[i] *= gate[kRest * C + t] * bt;
+        f32x4 q{}, k{};
+#pragma unroll
+        for (int u = kIn - 1; u >= 0; --u) {
+          const bf16x4 wk = *reinterpret_cast<const bf16x4*>(lds + ((i * KD + (wave >> 1)) * kIn + u) * 1024 + (16 * lg + c) * 16 + (wave & 1) * 8);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            q[r] += static_cast<float>(wq[i][u][r]);
+            k[r] += static_cast<float>(wk[r]);
+          }
+        }
+        // this wave's part of Q * dQ1 - K * dK0 - K * dK1 (tokens past the end: K stands for another's, but a, b, s are 0)
+        float dot = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float ks = k[r] * s[i][r];
+          w_sum += ks;
+          dot += __builtin_fmaf(q[r], a[i][r], -__builtin_fmaf(k[r], b[i][r], ks));
+        }
+        const Halves h16 = halves16(dot);
         const Halves h32 = halves32(h16.a + h16.b);
         if (lg == 0) red_q[wave][t] = h32.a + h32.b;
-        dk[i] += s[i] * w - b[i] * eg;
+        dk[i] += s[i] - b[i];
         dq[i] += a[i];
+      }
+      inner = lanes_sum<64>(inner);
+      w_sum = lanes_sum<64>(w_sum);
+      if (lane == 0) {
+        red_s[wave] = inner;
+        red_w[wave] = w_sum;
       }
       static_for<KC>([&](auto kt) {
         constexpr int at = kt.value;
         Frag<kW> f[RT];
 #pragma unroll
-        for (int i = 2 * at; i < RT; ++i) f[i] = lds_frag<kW, kW>(img_a, i * KC + at);
+        for (int i = 2 * at; i < RT; ++i) f[i] = lds_frag<kW, kW>(img_a, lower_frag(i, at));
         mm_tiles<kW, 2 * at, RT, true>(dq, f, kT[at]);
 #pragma unroll
-        for (int i = 0; i < 2 * at + 2; ++i) f[i] = lds_frag<kW, kW>(img_b, i * KC + at);
+        for (int i = 0; i < 2 * at + 2; ++i) f[i] = lds_frag<kW, kW>(img_b, upper_frag<KC>(i, at));
         mm_tiles<kW, 0, 2 * at + 2, true>(dk, f, qT[at]);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(img_c, i * KC + at);
+        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(img_z, i * KC + at);
         mm_tiles<kW, 0, RT, true>(dk, f, kT[at]);
         step();
       });
@@ -525,23 +414,17 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV), DK > DV ? DK / 64 : DV / 6
     // dbeta and dg, by the first wave: a lane per token
     if (wave == 0) {
       const int t = lane < C ? lane : 0, rt = rho_tile(t), x = rho_row(t);
-      float db = 0.0f, w = 0.0f, dG = 0.0f, inner = 0.0f;
+      float w = 0.0f, dG = 0.0f, inner = 0.0f;
 #pragma unroll
-      for (int i = 0; i < DV / 16; ++i) {
-        db += red_b[i][t];
+      for (int i = 0; i < DT; ++i) {
+        dG += red_q[i][t];
         w += red_w[i];
-        dG -= red_n[i][t];
         inner += red_s[i];
       }
 #pragma unroll
-      for (int i = 0; i < DT; ++i) dG += red_q[i][t];
-#pragma unroll
       for (int j = 0; j < RT; ++j) {
         if (j / 2 <= rt / 2) dG += row_e[rt][j][x];
-        if (j / 2 >= rt / 2) {
-          dG -= col_e[j][rt][x];
-          db -= col_x[j][rt][x];
-        }
+        if (j / 2 >= rt / 2) dG -= col_e[j][rt][x];
       }
       // the sums from a row to the end, in float64
       double sum = lane < n ? static_cast<double>(dG) : 0.0;
@@ -554,7 +437,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV), DK > DV ? DK / 64 : DV / 6
       if (lane < n) {
         const bool cut = A.g[(t0 + t) * A.g_ld + h] < -104.0f;
         A.dg[(t0 + t) * A.dg_ld + h] = from_f32<T>(cut ? 0.0f : static_cast<float>(sum));
-        A.dbeta[(t0 + t) * A.dbeta_ld + h] = from_f32<T>(db);
+        A.dbeta[(t0 + t) * A.dbeta_ld + h] = from_f32<T>(diag[t]);
       }
     }
   }
@@ -575,7 +458,7 @@ template <typename T, int DK>
 void launch_chain(const DeltaSizes& z, const ChainArgs<T>& A, hipStream_t st) {
   const int64_t chains = static_cast<int64_t>(z.S) * z.H;
   const int nw = chains >= 256 ? 8 : chains >= 64 ? 4 : 1;  // as in the forward
-  const dim3 grid(static_cast<uint32_t>(z.H * ceil_div(z.dv, 16 * nw)), static_cast<uint32_t>(z.S));
+  const dim3 grid(static_cast<uint32_t>(z.H * (delta_pad(z.dv) / (16 * nw) + (delta_pad(z.dv) < 16 * nw))), static_cast<uint32_t>(z.S));
   if (nw == 8) hipLaunchKernelGGL((delta_chain_kernel<T, DK, 8>), grid, dim3(512), 0, st, z, A);
   else if (nw == 4) hipLaunchKernelGGL((delta_chain_kernel<T, DK, 4>), grid, dim3(256), 0, st, z, A);
   else hipLaunchKernelGGL((delta_chain_kernel<T, DK, 1>), grid, dim3(64), 0, st, z, A);
@@ -642,7 +525,7 @@ extern "C" int det_delta_rule_bwd(const void* d_o, int64_t do_st, int64_t do_sh,
                       {"the workspace", range1d(need ? ws : nullptr, ws_bytes)}};
   const Buf ins[] = {b[0], b[1], b[2], b[3], gates("g", g, g_ld, 4), gates("beta", beta, beta_ld, es),
                      {"offs", range1d(offs, (S + 1) * 4)},
-                     {"states", range1d(states, delta_tiles(T, S, dtype) * state)},
+                     {"states", range1d(states, delta_tiles(T, S, dtype) * H * delta_saved_floats(dk, dv, dtype) * 4), 16},
                      {"dfinal_state", range1d(dfinal_state, S * state)}};
   if (int s = check_buffers(what, outs, 7, ins, 9)) return s;
   const hipStream_t st = as_stream(stream);
@@ -650,18 +533,19 @@ extern "C" int det_delta_rule_bwd(const void* d_o, int64_t do_st, int64_t do_sh,
   DeltaPrepared r{};
   if (T)
     r = delta_prepare(z, dtype, true, q, q_st, q_sh, k, k_st, k_sh, d_o, do_st, do_sh, g, g_ld, beta, beta_ld, base, l, st);
-  const auto words = [&](size_t at) { return reinterpret_cast<const uint16_t*>(base + at); };
+  const auto words = [&](size_t at) { return reinterpret_cast<uint16_t*>(base + at); };
   const auto* gate = reinterpret_cast<const float*>(base + l.gates);
   auto* ds = reinterpret_cast<float*>(base + l.ds);
+  const int image = static_cast<int>(delta_image_floats(dv, dtype)), saved = static_cast<int>(delta_saved_floats(dk, dv, dtype));
 #define DET_DELTA_BWD(E)                                                                                               \
   {                                                                                                                    \
-    const Heads<const E> hv{static_cast<const E*>(v), v_st, v_sh}, ho{static_cast<const E*>(d_o), do_st, do_sh};       \
-    const ChainArgs<E> A{r.k, ho, words(l.k_t), words(l.q_t), words(l.inverse_t), words(l.p), gate, dfinal_state, ds,  \
-                         dinitial_state};                                                                              \
-    const GradArgs<E> B{r.k, r.q, r.d_o, hv, ho, {static_cast<E*>(dq), dq_st, dq_sh},                                  \
-                        {static_cast<E*>(dk_out), dk_st, dk_sh}, {static_cast<E*>(dv_out), dv_st, dv_sh},              \
-                        static_cast<E*>(dg), static_cast<E*>(dbeta), words(l.k_t), words(l.q_t), words(l.inverse),     \
-                        words(l.inverse_t), words(l.p), g, gate, states, ds, g_ld, dg_ld, dbeta_ld};                   \
+    const ChainArgs<E> A{r.k, {static_cast<const E*>(d_o), do_st, do_sh}, {static_cast<E*>(dv_out), dv_st, dv_sh},     \
+                         words(l.k_t), words(l.q_t), words(l.inverse), words(l.p), gate, dfinal_state, ds,             \
+                         dinitial_state, words(l.dy)};                                                                 \
+    const GradArgs<E> B{r.k, r.q, r.d_o, {static_cast<E*>(dq), dq_st, dq_sh},                                          \
+                        {static_cast<E*>(dk_out), dk_st, dk_sh}, static_cast<E*>(dg), static_cast<E*>(dbeta),          \
+                        words(l.k_t), words(l.q_t), words(l.dy), g, gate, states, ds, g_ld, dg_ld, dbeta_ld,           \
+                        image, saved};                                                                                 \
     if (dk <= 64) launch_chain<E, 64>(z, A, st);                                                                       \
     else launch_chain<E, 128>(z, A, st);                                                                               \
     if (T) {                                                                                                           \

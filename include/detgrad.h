@@ -566,10 +566,11 @@ int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t dh
  * non-decreasing (read on the device only); rows of o behind the last sequence are
  * left as they were. Value head h uses key head h / (H / Hk). It starts from
  * initial_state[s] (NULL: zeros) and leaves final_state[s] (unless NULL), also for an
- * empty sequence. states (NULL: not written; needed for the backward) receives the
- * state in front of every chunk of 64 tokens (DET_F32: 32), counted from each
- * sequence's first: det_delta_rule_chunks() of [H, dk, dv], of which those past the
- * last chunk are left as they were.
+ * empty sequence. states (NULL: not written) receives what the backward needs of
+ * every chunk of 64 tokens (DET_F32: 32), counted from each sequence's first: the state
+ * in front of it and what the recurrence took up in it, in a layout of the library's
+ * own, det_delta_rule_states_size() chunks of H times so many floats, of which those past
+ * the last chunk are left as they were; 16-byte aligned.
  * Computed in chunks on the matrix cores with float32 sums and float32 states:
  * inputs of DET_F32 and everything that reaches a state are carried in three bf16
  * words (24 bits), the rest of a DET_BF16 call in two. Any g is allowed; below -1e4
@@ -588,7 +589,7 @@ int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t dh
  * ws:   det_delta_rule_workspace_size() bytes; its header is neither read nor
  *       written. o, final_state and states overlap nothing else.
  * No atomic arm. */
-int det_delta_rule_chunks(int64_t T, int64_t S, int dtype, int64_t* chunks);
+int det_delta_rule_states_size(int64_t T, int64_t S, int64_t dk, int64_t dv, int dtype, int64_t* chunks, int64_t* floats);
 int det_delta_rule_workspace_size(int64_t T, int64_t S, int64_t Hk, int64_t H, int64_t dk, int64_t dv, int dtype, size_t* bytes);
 int det_delta_rule(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh, const void* v,
                    int64_t v_st, int64_t v_sh, const float* g, int64_t g_ld, const void* beta, int64_t beta_ld, int dtype,

@@ -110,12 +110,16 @@ def test_column_ranges_of_one_buffer_are_no_overlap():
 def test_sizes():
     n, b = ctypes.c_int64(), ctypes.c_size_t()
     L = dg.lib()
-    assert L.det_delta_rule_chunks(1000, 3, 0, ctypes.byref(n)) == 0 and n.value == 1000 // 64 + 3
-    assert L.det_delta_rule_chunks(1000, 3, 1, ctypes.byref(n)) == 0 and n.value == 1000 // 32 + 3
-    assert L.det_delta_rule_chunks(1000, 3, 0, None) == INVALID and L.det_delta_rule_chunks(1000, 3, 5, ctypes.byref(n)) == INVALID
+    f = ctypes.c_int64()
+    size = lambda *a: L.det_delta_rule_states_size(*a, ctypes.byref(n), ctypes.byref(f))  # noqa: E731
+    assert size(1000, 3, 64, 48, 0) == 0 and n.value == 1000 // 64 + 3 and f.value >= 64 * 48 + 64 * 48
+    assert size(1000, 3, 63, 47, 1) == 0 and n.value == 1000 // 32 + 3 and f.value % 4 == 0 and f.value >= 63 * 47 + 32 * 47
+    assert L.det_delta_rule_states_size(1000, 3, 64, 48, 0, None, ctypes.byref(f)) == INVALID
+    assert L.det_delta_rule_states_size(1000, 3, 64, 48, 0, ctypes.byref(n), None) == INVALID
+    assert size(1000, 3, 64, 48, 5) == INVALID and size(1000, 3, 64, 129, 0) == UNSUPPORTED
     assert dg.det_delta_rule_workspace_size(0, 3, 2, 4, 64, 48, 0) == 0
     assert dg.det_delta_rule_workspace_size(1000, 3, 2, 4, 64, 48, 0) >= 256 + 18 * 4 * (64 * 64 * 3 // 4 * 6 + 6 * 64 * 4)
-    assert dg.det_delta_rule_bwd_workspace_size(1000, 3, 2, 4, 64, 48, 0) >= 256 + 18 * 4 * (64 * 64 * 3 // 4 * 18 + 6 * 64 * 4 + 64 * 48 * 4)
+    assert dg.det_delta_rule_bwd_workspace_size(1000, 3, 2, 4, 64, 48, 0) >= 256 + 18 * 4 * (64 * 64 * 3 // 4 * 12 + 6 * 64 * 4 + 64 * 48 * 8)
     assert L.det_delta_rule_workspace_size(10, 1, 1, 1, 8, 8, 0, None) == INVALID
     assert L.det_delta_rule_bwd_workspace_size(10, 1, 1, 1, 200, 8, 0, ctypes.byref(b)) == UNSUPPORTED
     assert dg.det_qk_norm_bwd_workspace_size(0, 4, 2, 64) == 0
@@ -146,11 +150,11 @@ def test_binding_refusals():
     refuse(ValueError, f, q, q, v, g, b, v[..., :4], offs)
     refuse(ValueError, f, q, q, v, g, b, v, offs[None])
     refuse(ValueError, f, q, q, v, g, b, v, offs, initial_state=s[:, :2])
-    refuse(ValueError, f, q, q, v, g, b, v, offs, states=torch.zeros(2, 4, 8, 5))
+    refuse(ValueError, f, q, q, v, g, b, v, offs, states=torch.zeros(2, 4, 64 * 64 + 40))
     refuse(ValueError, f, q.transpose(1, 2).contiguous().transpose(1, 2), q, v, g, b, v, offs)
     refuse(ValueError, f, q, q, v, g, b, v.clone(), offs)                        # not on a GPU
-    assert dg.det_delta_rule_states_shape(q, v, offs) == (1, 4, 8, 5)
-    f, st = dg.det_delta_rule_bwd, torch.zeros(1, 4, 8, 5)
+    assert dg.det_delta_rule_states_shape(q, v, offs) == (1, 4, 64 * 64 + 40)
+    f, st = dg.det_delta_rule_bwd, torch.zeros(dg.det_delta_rule_states_shape(q, v, offs))
     refuse(TypeError, f, v.float(), q, q, v, g, b, offs, st, q, q, v, b, b)
     refuse(TypeError, f, v, q, q, v, g, b, offs, st, q, q, v, g, b)
     refuse(ValueError, f, v, q, q, v, g, b, offs, st[:0], q, q, v, b, b)
