@@ -85,20 +85,16 @@ __global__ __launch_bounds__(256) void delta_turn_kernel(DeltaSizes z, Heads<con
 // ------------------------------------------------------------- inverse, P and gates
 constexpr int kPrepWaves = 4;
 
-struct PrepOut {
-  float* gates;
-  uint16_t *inverse, *p;
-};
-
 // The inverse of I + M B and P as images of rows i and places j; BWD: that of I + B M and P
 // transposed (rows j, places i), P in the words of the states too.
 template <typename T, int DK, bool BWD>
 __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSizes z, Rows k, Rows q,
                                                                      const float* __restrict__ g, int64_t g_ld,
                                                                      const T* __restrict__ beta, int64_t beta_ld,
-                                                                     PrepOut out, int64_t units) {
+                                                                     uint16_t* __restrict__ out, int64_t units) {
   constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC, RT = C / 16, KC = C / 32, KS = DK / 32;
-  constexpr int kW = kStateWords, kP = BWD ? kStateWords : DeltaType<T>::kOut, kFrags = KC * (KC + 1);
+  typedef Unit<T, BWD> Rec;
+  constexpr int kW = kStateWords, kP = Rec::kP;
   constexpr int kLd = C + 4;  // 16-byte rows whose starts move through the banks
   __shared__ __align__(16) float lds[kPrepWaves][C * kLd + 3 * C];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
@@ -111,6 +107,7 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSiz
   if (!segment_tile<1>(z.offs, z.S, static_cast<uint32_t>(z.T), kLogC, tile, e, r0, r1, s0, s1)) return;
   const int n = static_cast<int>(r1 - r0);
   float* a = lds[wave];
+  out += unit * Rec::kElems;
   float *hi = a + C * kLd, *lo = hi + C, *be = lo + C;
 
   // the sums of g in float64, kept as two float32 words
@@ -130,7 +127,7 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSiz
     const double last = __shfl(G, C - 1);
     const float h0 = static_cast<float>(G), h1 = static_cast<float>(G - h0);
     const float eg = exp_e(h0) * (1.0f + h1), end = __shfl(eg, C - 1);
-    float* to = out.gates + unit * (kGateRows * C);
+    float* to = reinterpret_cast<float*>(out + Rec::oGate * kFragElems);
     if (lane < C) {
       hi[lane] = h0;
       lo[lane] = h1;
@@ -202,7 +199,7 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSiz
       }
     }
   {
-    uint16_t* to = out.p + unit * (kFrags * kP * kFragElems);
+    uint16_t* to = out + Rec::oP * kFragElems;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -273,7 +270,7 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSiz
       for (int r = 0; r < 4; ++r) a[(16 * i + 4 * lg + r) * kLd + 16 * j + c] = X[i][r];
   }
   wave_fence();
-  uint16_t* to = out.inverse + unit * (kFrags * kW * kFragElems);
+  uint16_t* to = out;
   if (!BWD) {
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -305,8 +302,8 @@ struct FwdArgs {
   Rows k, q;
   Heads<const T> v;
   Heads<T> o;
-  const uint16_t *k_t, *inverse, *p;
-  const float *gates, *s0;
+  const uint16_t *k_t, *units;
+  const float* s0;
   float *s1, *saved;  // the final state; what the backward needs (delta_saved_floats)
   int image_floats, saved_floats;
 };
@@ -314,65 +311,116 @@ struct FwdArgs {
 // Workgroup (x, s): value head x % H of sequence s; wave w takes the columns
 // 16 (NW (x / H) + w) .. of v. Heads run fastest, so the workgroups of one head, which
 // read the same fragments, meet in one of the eight L2 caches. A chunk's fragments
-// come into LDS while the chunk before is worked on; those of K^T, which are needed
-// last, have one buffer.
-template <typename T, int DK, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T> A) {
+// come into LDS while the chunk before is worked on; those that are needed last have
+// one buffer. PAIR: a second wave for the same columns fetches, and forms O from what the
+// first one leaves in LDS of S0 and U; what is left to the first is the chain of states.
+template <typename T, int DK, int NW, bool PAIR>
+__global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T> A) {
+  typedef Unit<T, false> Rec;
   constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
-  constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords, kFrags = KC * (KC + 1);
-  // fragments of a buffer
-  constexpr int nRows = RT * KD * kIn, nInv = kFrags * kW, nP = kFrags * kOut, nGate = (kGateRows * C * 4 + 1023) / 1024,
-                nKT = DT * KC * kIn;
-  constexpr int oQ = nRows, oInv = 2 * nRows, oP = oInv + nInv, oGate = oP + nP, kBuf = (oGate + nGate) * 1024;
-  __shared__ __align__(16) char lds[2 * kBuf + nKT * 1024];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
+  constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
+  // fragments in LDS: two buffers of K, the inverse and the gates, then one of K^T; Q and P with the former or (PAIR) the latter
+  constexpr int nRows = RT * KD * kIn, nKT = DT * KC * kIn, nHead = Rec::oP, nP = Rec::nP, nX = (KD + KC) * kOut;
+  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nRows + nP), oKT = 2 * kBuf, oX = oKT + nKT + (PAIR ? nRows + nP : 0);
+  __shared__ __align__(16) char lds[(oX + (PAIR ? NW * nX : 0)) * 1024];
+  const int lane = threadIdx.x & 63, wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
+  const int wave = PAIR && wave_ >= NW ? wave_ - NW : wave_;
   const int h = blockIdx.x % z.H, hk = h / (z.H / z.Hk), v0 = ((blockIdx.x / z.H) * NW + wave) * 16, s = blockIdx.y;
   const uint32_t lds0 = lds_address(lds);
-  const char* kt_img = lds + 2 * kBuf;
+  char* x = lds + (oX + (PAIR ? wave * nX : 0)) * 1024;  // S0 and U of these columns
   uint32_t r0, r1, first;
   segment_rows(z.offs, s, static_cast<uint32_t>(z.T), kLogC, r0, r1, first);
+  int64_t unit = static_cast<int64_t>(first) * z.H + h;
+  int buf = 0;
+
+  const auto rows_at = [&](uint32_t t0) { return r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C; };
+  const auto fetch_next = [&](uint32_t t0, int64_t unit, int buf) {
+    const uint32_t to = lds0 + buf * kBuf * 1024;
+    const uint16_t* rec = A.units + unit * Rec::kElems;
+    fetch_rows<RT, KD, kIn, NW>(to, A.k, t0, rows_at(t0) - 1, hk, wave);
+    fetch_image<nHead, NW, 4>(to + nRows * 1024, rec, wave);
+    if (!PAIR) {
+      fetch_rows<RT, KD, kIn, NW, 4>(to + (nRows + nHead) * 1024, A.q, t0, rows_at(t0) - 1, hk, wave);
+      fetch_image<nP, NW, 5>(to + (2 * nRows + nHead) * 1024, rec + Rec::oP * kFragElems, wave);
+    }
+  };
+  const auto fetch_now = [&](uint32_t t0, int64_t unit) {
+    fetch_image<nKT, NW>(lds0 + oKT * 1024, A.k_t + (unit / z.H * z.Hk + hk) * (nKT * kFragElems), wave);
+    if (PAIR) {
+      fetch_rows<RT, KD, kIn, NW>(lds0 + (oKT + nKT) * 1024, A.q, t0, rows_at(t0) - 1, hk, wave);
+      fetch_image<nP, NW>(lds0 + (oKT + nKT + nRows) * 1024, A.units + unit * Rec::kElems + Rec::oP * kFragElems, wave);
+    }
+  };
+  // O: rows v, columns t. (Q S0, then the scales, then P U; in PAIR from the second wave.)
+  const auto scale_o = [&](f32x4 (&o)[RT], const float* gate) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) o[i] *= gate[kEG * C + rho(i, c)] * z.scale;
+  };
+
+  if (PAIR && wave_ >= NW) {
+    if (r0 < r1) fetch_next(r0, unit, 0);
+    fetch_done();
+    for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
+      __syncthreads();  // this chunk's fragments are there, the last one's have been read
+      fetch_now(t0, unit);
+      if (t0 + C < r1) fetch_next(t0 + C, unit + z.H, buf ^ 1);
+      fetch_done();
+      __syncthreads();  // as in the first wave; S0 and U are there
+      const char *q_img = lds + (oKT + nKT) * 1024, *p_img = q_img + nRows * 1024;
+      f32x4 o[RT] = {};
+#pragma unroll
+      for (int ks = 0; ks < KD; ++ks) {
+        Frag<kIn> fq[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) fq[i] = lds_frag<kIn, kIn>(q_img, i * KD + ks);
+        mm_tiles<kOut, 0, RT, true>(o, fq, lds_frag<kOut, kOut>(x, ks));
+      }
+      scale_o(o, reinterpret_cast<const float*>(lds + (buf * kBuf + nRows + Rec::oGate) * 1024));
+      static_for<KC>([&](auto kt) {
+        Frag<kOut> fp[RT];
+#pragma unroll
+        for (int i = 2 * kt.value; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(p_img, lower_frag(i, kt.value));
+        mm_tiles<kOut, 2 * kt.value, RT, true>(o, fp, lds_frag<kOut, kOut>(x, KD + kt.value));
+      });
+      store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
+    }
+    return;
+  }
 
   // the state's rows rho(i, 4 lg + r), column v0 + c
   const int col = v0 + c, vcol = col < z.dv ? col : z.dv - 1;
   const int64_t size = static_cast<int64_t>(z.dk) * z.dv, of = (static_cast<int64_t>(s) * z.H + h) * size;
   f32x4 S[DT] = {};
   if (A.s0) {
-    float x[DT][4];
-    load_state<DT>(x, A.s0 + of, z.dk, z.dv, vcol);
+    float y[DT][4];
+    load_state<DT>(y, A.s0 + of, z.dk, z.dv, vcol);
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[i][r] = rho(i, 4 * lg + r) < z.dk ? x[i][r] : 0.0f;
+      for (int r = 0; r < 4; ++r) S[i][r] = rho(i, 4 * lg + r) < z.dk ? y[i][r] : 0.0f;
   }
   T rv[RT][4];
-  const auto fetch = [&](uint32_t t0, int64_t unit, int buf) {
-    const int last = (r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C) - 1;
-    load_column<RT>(rv, A.v.row(t0, h), A.v.st, vcol, last);
-    const uint32_t to = lds0 + buf * kBuf;
-    fetch_rows<RT, KD, kIn, NW>(to, A.k, t0, last, hk, wave);
-    fetch_rows<RT, KD, kIn, NW>(to + oQ * 1024, A.q, t0, last, hk, wave);
-    fetch_image<nInv, NW>(to + oInv * 1024, A.inverse + unit * (nInv * kFragElems), wave);
-    fetch_image<nP, NW>(to + oP * 1024, A.p + unit * (nP * kFragElems), wave);
-    fetch_image<nGate, NW>(to + oGate * 1024, reinterpret_cast<const uint16_t*>(A.gates + unit * (kGateRows * C)), wave);
-  };
-
-  int64_t unit = static_cast<int64_t>(first) * z.H + h;
-  int buf = 0;
-  if (r0 < r1) fetch(r0, unit, 0);
-  fetch_done();
+  const auto load_v = [&](uint32_t t0) { load_column<RT>(rv, A.v.row(t0, h), A.v.st, vcol, rows_at(t0) - 1); };
+  if (r0 < r1) {
+    load_v(r0);
+    if (!PAIR) fetch_next(r0, unit, 0);
+  }
+  if (!PAIR) fetch_done();
   for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
-    const int n = r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C;
     f32x4 R[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) R[i][r] = to_f32(rv[i][r]);
     __syncthreads();  // this chunk's fragments are there, the last one's have been read
-    fetch_image<nKT, NW>(lds0 + 2 * kBuf, A.k_t + (unit / z.H * z.Hk + hk) * (nKT * kFragElems), wave);
-    if (t0 + C < r1) fetch(t0 + C, unit + z.H, buf ^ 1);
+    if (!PAIR) fetch_now(t0, unit);
+    if (t0 + C < r1) {
+      load_v(t0 + C);
+      if (!PAIR) fetch_next(t0 + C, unit + z.H, buf ^ 1);
+    }
     if (A.saved) store_state<DT>(S, A.saved + unit * A.saved_floats + A.image_floats, z.dk, z.dv, col);
-    const char* img = lds + buf * kBuf;
-    const float* gate = reinterpret_cast<const float*>(img + oGate * 1024);
+    const char* img = lds + buf * kBuf * 1024;
+    const float* gate = reinterpret_cast<const float*>(img + (nRows + Rec::oGate) * 1024);
 
     // K S0 (rows t, columns v) and its transposed Q S0 (rows v, columns t)
     f32x4 ks0[RT] = {}, o[RT] = {};
@@ -381,20 +429,22 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaSizes z, FwdArg
       const Frag<kW> f = frag_of<kW>(S[2 * ks], S[2 * ks + 1]);
       Frag<kIn> fk[RT], fq[RT];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        fk[i] = lds_frag<kIn, kIn>(img, i * KD + ks);
-        fq[i] = lds_frag<kIn, kIn>(img + oQ * 1024, i * KD + ks);
+      for (int i = 0; i < RT; ++i) fk[i] = lds_frag<kIn, kIn>(img, i * KD + ks);
+      if (PAIR) {
+        lds_put<kOut>(x, ks, f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) fq[i] = lds_frag<kIn, kIn>(img + (nRows + nHead) * 1024, i * KD + ks);
       }
       mm_tiles<kW, 0, RT>(ks0, fk, f);
-      mm_tiles<kOut, 0, RT, true>(o, fq, f);
+      if (!PAIR) mm_tiles<kOut, 0, RT, true>(o, fq, f);
     }
+    if (!PAIR) scale_o(o, gate);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const f32x4 eg = *reinterpret_cast<const f32x4*>(gate + kEG * C + rho(i, 4 * lg));
-      const float e_col = gate[kEG * C + rho(i, c)] * z.scale;
+      const f32x4 eg = gate4(gate, C, kEG, rho(i, 4 * lg));
 #pragma unroll
       for (int r = 0; r < 4; ++r) R[i][r] = __builtin_fmaf(-eg[r], ks0[i][r], R[i][r]);
-      o[i] *= e_col;
     }
     // N, then U = beta N
     f32x4 U[RT] = {}, nt[RT] = {};  // nt: N with rows v and columns t, for the backward
@@ -402,38 +452,38 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaSizes z, FwdArg
       const Frag<kW> f = frag_of<kW>(R[2 * kt.value], R[2 * kt.value + 1]);
       Frag<kW> fi[RT];
 #pragma unroll
-      for (int i = 2 * kt.value; i < RT; ++i) fi[i] = lds_frag<kW, kW>(img + oInv * 1024, lower_frag(i, kt.value));
+      for (int i = 2 * kt.value; i < RT; ++i) fi[i] = lds_frag<kW, kW>(img + nRows * 1024, lower_frag(i, kt.value));
       mm_tiles<kW, 2 * kt.value, RT>(U, fi, f);
       if (A.saved) mm_tiles<kOut, 2 * kt.value, RT, true>(nt, fi, f);
     });
     if (A.saved) put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
 #pragma unroll
-    for (int i = 0; i < RT; ++i) U[i] *= *reinterpret_cast<const f32x4*>(gate + kBeta * C + rho(i, 4 * lg));
+    for (int i = 0; i < RT; ++i) U[i] *= gate4(gate, C, kBeta, rho(i, 4 * lg));
     static_for<KC>([&](auto kt) {
       const Frag<kOut> f = frag_of<kOut>(U[2 * kt.value], U[2 * kt.value + 1]);
-      Frag<kOut> fp[RT];
+      if (PAIR) {
+        lds_put<kOut>(x, KD + kt.value, f);
+      } else {
+        Frag<kOut> fp[RT];
 #pragma unroll
-      for (int i = 2 * kt.value; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(img + oP * 1024, lower_frag(i, kt.value));
-      mm_tiles<kOut, 2 * kt.value, RT, true>(o, fp, f);
+        for (int i = 2 * kt.value; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(img + (2 * nRows + nHead) * 1024, lower_frag(i, kt.value));
+        mm_tiles<kOut, 2 * kt.value, RT, true>(o, fp, f);
+      }
     });
     const float el = gate[kEnd * C];
 #pragma unroll
     for (int i = 0; i < DT; ++i) S[i] *= el;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) U[i] *= *reinterpret_cast<const f32x4*>(gate + kRest * C + rho(i, 4 * lg));
-    fetch_done();
+    for (int i = 0; i < RT; ++i) U[i] *= gate4(gate, C, kRest, rho(i, 4 * lg));
+    if (!PAIR) fetch_done();
     __syncthreads();  // K^T is there, and the next chunk's fragments
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int t = rho(i, c);
-      if (t < n) store4(A.o.row(t0 + t, h) + v0 + 4 * lg, z.dv - v0 - 4 * lg, o[i]);
-    }
+    if (!PAIR) store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
 #pragma unroll
     for (int kt = 0; kt < KC; ++kt) {
       const Frag<kW> f = frag_of<kW>(U[2 * kt], U[2 * kt + 1]);
       Frag<kIn> fk[DT];
 #pragma unroll
-      for (int i = 0; i < DT; ++i) fk[i] = lds_frag<kIn, kIn>(kt_img, i * KC + kt);
+      for (int i = 0; i < DT; ++i) fk[i] = lds_frag<kIn, kIn>(lds + oKT * 1024, i * KC + kt);
       mm_tiles<kW, 0, DT>(S, fk, f);
     }
   }
@@ -467,7 +517,7 @@ Rows rows_of(const DeltaSizes& z, int dtype, const void* x, int64_t x_st, int64_
 
 template <typename T, int DK>
 void launch_prep(const DeltaSizes& z, bool bwd, const Rows& k, const Rows& q, const float* g, int64_t g_ld, const void* beta,
-                 int64_t beta_ld, const PrepOut& out, int64_t units, hipStream_t st) {
+                 int64_t beta_ld, uint16_t* out, int64_t units, hipStream_t st) {
   const dim3 grid(static_cast<uint32_t>(ceil_div(units, kPrepWaves)));
   if (bwd)
     hipLaunchKernelGGL((delta_prep_kernel<T, DK, true>), grid, dim3(64 * kPrepWaves), 0, st, z, k, q, g, g_ld,
@@ -486,32 +536,29 @@ DeltaPrepared prepare(const DeltaSizes& z, int dtype, bool bwd, const void* q, i
   r.k = rows_of<T>(z, dtype, k, k_st, k_sh, z.Hk, z.dk, at(l.k_t), at(l.k_rows), st);
   r.q = rows_of<T>(z, dtype, q, q_st, q_sh, z.Hk, z.dk, bwd ? at(l.q_t) : nullptr, at(l.q_rows), st);
   if (bwd) r.d_o = rows_of<T>(z, dtype, d_o, do_st, do_sh, z.H, z.dv, nullptr, at(l.o_rows), st);
-  const PrepOut out{reinterpret_cast<float*>(ws + l.gates), at(l.inverse), at(l.p)};
   const int64_t units = delta_tiles(z.T, z.S, dtype) * z.H;
-  if (z.dk <= 64) launch_prep<T, 64>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, out, units, st);
-  else launch_prep<T, 128>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, out, units, st);
+  if (z.dk <= 64) launch_prep<T, 64>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, at(l.units), units, st);
+  else launch_prep<T, 128>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, at(l.units), units, st);
   return r;
 }
 
 template <typename T, int DK>
 void launch_fwd(const DeltaSizes& z, const FwdArgs<T>& A, hipStream_t st) {
-  // the waves of a head in one workgroup, which share its fragments, where that leaves a
-  // workgroup for each compute unit; else spread out
-  const int64_t chains = static_cast<int64_t>(z.S) * z.H;
-  const int nw = chains >= 256 ? 8 : chains >= 64 ? 4 : 1;
+  const int nw = delta_chain_waves(z);
   const int64_t columns = A.saved ? delta_pad(z.dv) : z.dv;  // (the images' padding is written too)
   const dim3 grid(static_cast<uint32_t>(z.H * ceil_div(columns, 16 * nw)), static_cast<uint32_t>(z.S));
-  if (nw == 8) hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 8>), grid, dim3(512), 0, st, z, A);
-  else if (nw == 4) hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 4>), grid, dim3(256), 0, st, z, A);
-  else hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 1>), grid, dim3(64), 0, st, z, A);
+  if (nw == 8) hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 8, false>), grid, dim3(512), 0, st, z, A);
+  else if (nw == 2) hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 2, true>), grid, dim3(256), 0, st, z, A);
+  else hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 1, true>), grid, dim3(128), 0, st, z, A);
 }
 
 }  // namespace
 
 DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd) {
-  const int64_t C = delta_chunk(dtype), KC = C / 32, tiles = delta_tiles(z.T, z.S, dtype), units = tiles * z.H;
-  const int64_t words = delta_words(dtype), dk = delta_pad(z.dk), dv = delta_pad(z.dv), square = KC * (KC + 1) * kFragElems * 2;
-  const int64_t p_words = bwd ? kStateWords : (dtype == DET_BF16 ? DeltaType<uint16_t>::kOut : DeltaType<float>::kOut);
+  const int64_t C = delta_chunk(dtype), tiles = delta_tiles(z.T, z.S, dtype), units = tiles * z.H;
+  const int64_t words = delta_words(dtype), dk = delta_pad(z.dk), dv = delta_pad(z.dv);
+  const int64_t unit = dtype == DET_BF16 ? (bwd ? Unit<uint16_t, true>::kElems : Unit<uint16_t, false>::kElems)
+                                         : (bwd ? Unit<float, true>::kElems : Unit<float, false>::kElems);
   DeltaLayout l{};
   size_t at = DET_WS_HEADER_BYTES;
   const auto take = [&](int64_t bytes) {
@@ -519,9 +566,7 @@ DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd) {
     at += align_up(static_cast<size_t>(bytes), 256);
     return r;
   };
-  l.gates = take(units * kGateRows * C * 4);
-  l.inverse = take(units * square * kStateWords);
-  l.p = take(units * square * p_words);
+  l.units = take(units * unit * 2);
   l.k_t = take(tiles * z.Hk * C * dk * words * 2);
   l.q_t = take(bwd ? tiles * z.Hk * C * dk * words * 2 : 0);
   l.k_rows = take(z.T * z.Hk * words * dk * 2);
@@ -638,9 +683,8 @@ extern "C" int det_delta_rule(const void* q, int64_t q_st, int64_t q_sh, const v
 #define DET_DELTA_FWD(E)                                                                                            \
   {                                                                                                                 \
     const FwdArgs<E> A{r.k, r.q, {static_cast<const E*>(v), v_st, v_sh}, {static_cast<E*>(o), o_st, o_sh},          \
-                       reinterpret_cast<const uint16_t*>(base + l.k_t),                                             \
-                       reinterpret_cast<const uint16_t*>(base + l.inverse),                                         \
-                       reinterpret_cast<const uint16_t*>(base + l.p), reinterpret_cast<const float*>(base + l.gates), \
+                       reinterpret_cast<const uint16_t*>(base + l.k_t),                                         \
+                       reinterpret_cast<const uint16_t*>(base + l.units),                                           \
                        initial_state, final_state, states, (int)delta_image_floats(dv, dtype),                      \
                        (int)delta_saved_floats(dk, dv, dtype)};                                                       \
     if (dk <= 64) launch_fwd<E, 64>(z, A, st);                                                                      \

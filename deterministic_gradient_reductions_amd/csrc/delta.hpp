@@ -164,6 +164,12 @@ __device__ __forceinline__ void image_put(uint16_t* image, int f, const Frag<NP>
 #pragma unroll
   for (int p = 0; p < NP; ++p) __builtin_memcpy(image + (f * NP + p) * kFragElems + (threadIdx.x & 63) * 8, &v.w[p], 16);
 }
+// The first NP words to LDS.
+template <int NP, int N>
+__device__ __forceinline__ void lds_put(char* image, int f, const Frag<N>& v) {
+#pragma unroll
+  for (int p = 0; p < NP; ++p) *reinterpret_cast<bf16x8*>(image + (f * NP + p) * 1024 + (threadIdx.x & 63) * 16) = v.w[p];
+}
 // Where row `row` and place `place` of an operand with KS fragments per row tile lie, in elements (word 0).
 template <int KS, int NP>
 __device__ __forceinline__ int image_at(int row, int place) {
@@ -210,22 +216,36 @@ __device__ __forceinline__ void store4(float* p, int n, const f32x4& v) {
   }
 }
 __device__ __forceinline__ void store4(uint16_t* p, int n, const f32x4& v) {
-  uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    w[i] = static_cast<uint32_t>(from_f32<uint16_t>(v[2 * i])) |
-           (static_cast<uint32_t>(from_f32<uint16_t>(v[2 * i + 1])) << 16);
+  uint32_t a[1], b[1];
+  split2<1>(v[0], v[1], a);
+  split2<1>(v[2], v[3], b);
   if (n >= 4) {
-    __builtin_memcpy(p, w, 8);
+    const uint64_t w = a[0] | static_cast<uint64_t>(b[0]) << 32;
+    __builtin_memcpy(p, &w, 8);
+  } else {
+    if (n > 0) p[0] = static_cast<uint16_t>(a[0]);
+    if (n > 1) p[1] = static_cast<uint16_t>(a[0] >> 16);
+    if (n > 2) p[2] = static_cast<uint16_t>(b[0]);
+  }
+}
+// Results with rows v0 + 4 g + r and columns t = rho(i, c) < n: x[i][r] to place v0 + 4 g + r of row t.
+template <int RT, typename T>
+__device__ __forceinline__ void store_rows(const f32x4 (&x)[RT], T* rows, int64_t st, int v0, int dv, int n) {
+  const int lane = here_lane(threadIdx.x) & 63, c = lane & 15, v = v0 + 4 * (lane >> 4);
+  T* to = rows + rho(0, c) * st + v;
+  if (n == 16 * RT && v0 + 16 <= dv) {  // (the same for all)
+#pragma unroll
+    for (int i = 0; i < RT; ++i) store4(to + rho(i, 0) * st, 4, x[i]);
   } else {
 #pragma unroll
-    for (int j = 0; j < 3; ++j)
-      if (j < n) p[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+    for (int i = 0; i < RT; ++i)
+      if (rho(i, c) < n) store4(to + rho(i, 0) * st, dv - v, x[i]);
   }
 }
 
-// Memory to LDS past the registers: lane l brings the 16 bytes at base + off to `lds` + 16 l
-// (base and lds the same for the wave). In assembly, since the compiler makes every
+// Memory to LDS past the registers: N groups of 64 lanes of 16 bytes; lane l brings those at
+// base + off[j] + 1024 j to `lds` + 1024 j + 16 l (the instruction's offset counts on both
+// sides; base and lds the same for the wave). In assembly, since the compiler makes every
 // read of LDS wait for all such loads, those of a buffer that is only read later
 // too; the wait is fetch_done() and a barrier. It counts only its own loads, of which
 // there are fewer than the hardware counts, so its waits are never too short.
@@ -233,29 +253,41 @@ typedef __attribute__((address_space(3))) void lds_void;
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)p));
 }
-__device__ __forceinline__ void fetch16(uint32_t lds, const void* base, uint32_t off) {
+#define DET_FETCH_HEAD "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\t"
+#define DET_FETCH_TAIL "s_mov_b32 m0, %0"
+template <int N>
+__device__ __forceinline__ void fetch_group(uint32_t lds, const void* base, const uint32_t (&off)[N]) {
+  static_assert(N >= 1 && N <= 4, "offsets up to 4095 bytes");
   uint32_t m0;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %1\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %2, %3\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(m0)
-      : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
-      : "memory");
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  if constexpr (N == 1)
+    asm volatile(DET_FETCH_HEAD DET_FETCH_TAIL : "=&s"(m0) : "s"(lds), "v"(off[0]), "s"(base) : "memory");
+  if constexpr (N == 2)
+    asm volatile(DET_FETCH_HEAD "global_load_lds_dwordx4 %4, %3 offset:1024\n\t" DET_FETCH_TAIL
+                 : "=&s"(m0) : "s"(lds), "v"(off[0]), "s"(base), "v"(off[1]) : "memory");
+  if constexpr (N == 3)
+    asm volatile(DET_FETCH_HEAD "global_load_lds_dwordx4 %4, %3 offset:1024\n\tglobal_load_lds_dwordx4 %5, %3 offset:2*1024\n\t"
+                 DET_FETCH_TAIL : "=&s"(m0) : "s"(lds), "v"(off[0]), "s"(base), "v"(off[1]), "v"(off[2]) : "memory");
+  if constexpr (N == 4)
+    asm volatile(DET_FETCH_HEAD "global_load_lds_dwordx4 %4, %3 offset:1024\n\tglobal_load_lds_dwordx4 %5, %3 offset:2*1024\n\t"
+                 "global_load_lds_dwordx4 %6, %3 offset:3*1024\n\t" DET_FETCH_TAIL
+                 : "=&s"(m0) : "s"(lds), "v"(off[0]), "s"(base), "v"(off[1]), "v"(off[2]), "v"(off[3]) : "memory");
 }
+#undef DET_FETCH_HEAD
+#undef DET_FETCH_TAIL
 __device__ __forceinline__ void fetch_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-// N consecutive fragments of an image, shared out among NW waves.
-template <int N, int NW>
+// N consecutive fragments of an image, four at a time, shared out among NW waves from wave FIRST on.
+template <int N, int NW, int FIRST = 0>
 __device__ __forceinline__ void fetch_image(uint32_t lds, const uint16_t* image, int wave) {
-  const uint32_t off = (threadIdx.x & 63) * 16;
+  const uint32_t l = (threadIdx.x & 63) * 16;
   wave = here(wave);
+  static_for<(N + 3) / 4>([&](auto group) {
+    constexpr int f = 4 * group.value, n = N - f < 4 ? N - f : 4;
+    uint32_t off[n];
 #pragma unroll
-  for (int u = 0; u < (N + NW - 1) / NW; ++u) {
-    const int f = wave + u * NW;
-    if (f < N) fetch16(lds + f * 1024, image + f * kFragElems, off);
-  }
+    for (int j = 0; j < n; ++j) off[j] = l;
+    if (NW == 1 || wave == (group.value + FIRST) % NW) fetch_group<n>(lds + f * 1024, image + f * kFragElems, off);
+  });
 }
 
 // Writes to LDS of this wave's lanes are seen by its other lanes after this (the
@@ -284,6 +316,10 @@ __device__ __forceinline__ void put_image(const f32x4 (&x)[RT], uint16_t* image,
       __builtin_memcpy(to + (i * kv * NP + p) * kFragElems, &w, 8);
     }
   }
+}
+
+__device__ __forceinline__ f32x4 gate4(const float* gate, int C, int row, int at) {
+  return *reinterpret_cast<const f32x4*>(gate + row * C + at);
 }
 
 // A [T, heads, dim] tensor with unit innermost stride.
@@ -384,26 +420,24 @@ struct Rows {
 // The fragments of a chunk's rows t0 + rho(i, c) (the last one again behind it) as an image
 // in LDS, tile by tile, KD places of 32 each, NP words; shared out among NW waves. The rows'
 // strides are below 2^24 elements (as_it_is), so that a chunk spans less than 2^32 bytes.
-template <int RT, int KD, int NP, int NW>
+template <int RT, int KD, int NP, int NW, int FIRST = 0>
 __device__ __forceinline__ void fetch_rows(uint32_t lds, const Rows& x, int64_t t0, int last, int h, int wave) {
-  constexpr int kTile = KD * NP, kAll = RT * kTile;
+  constexpr int kTile = KD * NP, kGroups = (kTile + 3) / 4;
   const int c = here_lane(threadIdx.x) & 15;
   wave = here(wave);
-  const uint16_t* base = x.from(t0, h);
-  uint32_t off[RT];
+  const uint16_t* base = x.from(t0, h) - 2048;  // (the offsets below would be negative)
+  static_for<RT * kGroups>([&](auto group) {
+    constexpr int i = group.value / kGroups, f = 4 * (group.value % kGroups), n = kTile - f < 4 ? kTile - f : 4;
+    if (NW == 1 || wave == (group.value + FIRST) % NW) {
+      const int t = rho(i, c);
+      const uint32_t row = x.lane_off(t < last ? t : last) + 4096u;
+      uint32_t off[n];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int t = rho(i, c);
-    off[i] = x.lane_off(t < last ? t : last);
-  }
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int u = 0; u < kTile; ++u) {
-      constexpr int kEach = (kAll + NW - 1) / NW;  // neighbours for a wave
-      const int f = i * kTile + u;
-      if (wave == f / kEach) fetch16(lds + f * 1024, base + (u % NP) * x.words_at + 32 * (u / NP), off[i]);
+      for (int j = 0; j < n; ++j)
+        off[j] = row + 64u * ((f + j) / NP) - 1024u * j + (NP == 1 ? 0u : (f + j) % NP * 64u * KD);  // words: KD * 32 apart
+      fetch_group<n>(lds + (i * kTile + f) * 1024, base, off);
     }
+  });
 }
 
 // Rows [r0, r1) of segment s and the tiles before it, from the clamped offsets (see
@@ -455,6 +489,15 @@ __device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float
 // and exp(G_C) in every place.
 enum GateRow { kGHi = 0, kGLo = 1, kEG = 2, kRest = 3, kBeta = 4, kEnd = 5, kGateRows = 6 };
 
+// What it leaves per (chunk, value head), in fragments of 1024 bytes: the inverse, those rows, P.
+template <typename T, bool BWD>
+struct Unit {
+  static constexpr int C = 1 << DeltaType<T>::kLogC, KC = C / 32, kFrags = KC * (KC + 1);
+  static constexpr int kP = BWD ? kStateWords : DeltaType<T>::kOut;
+  static constexpr int nInv = kFrags * kStateWords, nGate = (kGateRows * C * 4 + 1023) / 1024, nP = kFrags * kP;
+  static constexpr int oGate = nInv, oP = nInv + nGate, nAll = oP + nP, kElems = nAll * kFragElems;
+};
+
 // Sizes, and what every kernel of a call is given.
 struct DeltaSizes {
   int64_t T;
@@ -469,6 +512,13 @@ inline int delta_words(int dtype) { return dtype == DET_BF16 ? DeltaType<uint16_
 inline int64_t delta_tiles(int64_t T, int64_t S, int dtype) { return T / delta_chunk(dtype) + S; }
 inline int delta_pad(int64_t d) { return d <= 64 ? 64 : 128; }
 
+// The waves of a workgroup of the chains of states: all columns of a head, which share its
+// fragments, where that leaves a workgroup for each compute unit; else spread out, in pairs.
+inline int delta_chain_waves(const DeltaSizes& z) {
+  const int64_t chains = static_cast<int64_t>(z.S) * z.H;
+  return chains >= 192 ? 8 : chains >= 64 ? 2 : 1;
+}
+
 // What a forward leaves for the backward per (chunk, value head): N as an image of rows t and
 // places v in kOut words, then the state in front of the chunk, in floats.
 inline int64_t delta_image_floats(int64_t dv, int dtype) {
@@ -479,10 +529,9 @@ inline int64_t delta_saved_floats(int64_t dk, int64_t dv, int dtype) {
   return delta_image_floats(dv, dtype) + static_cast<int64_t>(align_up(static_cast<size_t>(dk * dv), 4));
 }
 
-// Where the parts of a workspace lie. The square images: the inverse and P, transposed in
-// the backward; dy: the backward's images as N's.
+// Where the parts of a workspace lie. units: a Unit each; dy: the backward's images as N's.
 struct DeltaLayout {
-  size_t gates, inverse, p, k_rows, q_rows, o_rows, k_t, q_t, ds, dy, all;
+  size_t units, k_rows, q_rows, o_rows, k_t, q_t, ds, dy, all;
 };
 DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd);
 

@@ -21,77 +21,191 @@
 namespace detgrad {
 namespace {
 
-__device__ __forceinline__ f32x4 gate4(const float* gate, int C, int row, int at) {
-  return *reinterpret_cast<const f32x4*>(gate + row * C + at);
-}
-
 template <typename T>
 struct ChainArgs {
   Rows k;
   Heads<const T> d_o;
   Heads<T> dv;
-  const uint16_t *k_t, *q_t, *inverse_t, *p_t;
-  const float *gates, *ds1;
+  const uint16_t *k_t, *q_t, *units;
+  const float* ds1;
   float *ds, *ds0;  // every chunk's dS1, the initial state's gradient
   uint16_t* dy;
 };
 
-// Workgroups, waves and buffers as in the forward's chain; K^T and Q^T have one buffer.
-template <typename T, int DK, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaSizes z, ChainArgs<T> A) {
+// Workgroups, waves and buffers as in the forward's chain. PAIR: the second wave fetches,
+// forms P^T dO (a chunk ahead) and scale (e^G Q)^T dO for the first one, and dV and dY's image
+// from what that leaves of dU.
+template <typename T, int DK, int NW, bool PAIR>
+__global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_chain_kernel(DeltaSizes z, ChainArgs<T> A) {
+  typedef Unit<T, true> Rec;
   constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
-  constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords, kFrags = KC * (KC + 1);
-  const int DVP = z.dv <= 64 ? 64 : 128;
-  constexpr int nRows = RT * KD * kIn, nSq = kFrags * kW, nGate = (kGateRows * C * 4 + 1023) / 1024, nT = DT * KC * kIn;
-  constexpr int oInv = nRows, oP = oInv + nSq, oGate = oP + nSq, kBuf = (oGate + nGate) * 1024;
-  __shared__ __align__(16) char lds[2 * kBuf + 2 * nT * 1024];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
+  constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
+  // fragments in LDS: two buffers of K, the inverse and the gates, then one of K^T and Q^T; P with the former or (PAIR) the latter
+  constexpr int nRows = RT * KD * kIn, nT = DT * KC * kIn, nHead = Rec::oP, nP = Rec::nP, nX = KC * kOut + RT + DT;
+  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nP), oKT = 2 * kBuf, oQT = oKT + nT, oPs = oQT + nT, oX = oPs + (PAIR ? nP : 0);
+  __shared__ __align__(16) char lds[(oX + (PAIR ? NW * nX : 0)) * 1024];
+  const int lane = threadIdx.x & 63, wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
+  const int wave = PAIR && wave_ >= NW ? wave_ - NW : wave_;
   const int h = blockIdx.x % z.H, hk = h / (z.H / z.Hk), v0 = ((blockIdx.x / z.H) * NW + wave) * 16, s = blockIdx.y;
+  const int dvp = z.dv <= 64 ? 64 : 128;
   const uint32_t lds0 = lds_address(lds);
-  const char *kt_img = lds + 2 * kBuf, *qt_img = kt_img + nT * 1024;
+  char* x = lds + (oX + (PAIR ? wave * nX : 0)) * 1024;  // dU of these columns
+  f32x4 *x_p = reinterpret_cast<f32x4*>(x + KC * kOut * 1024) + lane, *x_q = x_p + RT * 64;  // tiles of P^T dO, of (e^G Q)^T dO
   uint32_t r0, r1, first;
   segment_rows(z.offs, s, static_cast<uint32_t>(z.T), kLogC, r0, r1, first);
   const int col = v0 + c, vcol = col < z.dv ? col : z.dv - 1;
-  const int64_t size = static_cast<int64_t>(z.dk) * z.dv, of = (static_cast<int64_t>(s) * z.H + h) * size;
-  f32x4 S[DT] = {};
-  if (A.ds1) {
-    float x[DT][4];
-    load_state<DT>(x, A.ds1 + of, z.dk, z.dv, vcol);
-#pragma unroll
-    for (int i = 0; i < DT; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[i][r] = rho(i, 4 * lg + r) < z.dk ? x[i][r] : 0.0f;
-  }
-  T rd[RT][4];
-  const auto fetch = [&](uint32_t t0, int64_t unit, int buf) {
-    const int last = (r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C) - 1;
-    load_column<RT>(rd, A.d_o.row(t0, h), A.d_o.st, vcol, last);
-    const uint32_t to = lds0 + buf * kBuf;
-    fetch_rows<RT, KD, kIn, NW>(to, A.k, t0, last, hk, wave);
-    fetch_image<nSq, NW>(to + oInv * 1024, A.inverse_t + unit * (nSq * kFragElems), wave);
-    fetch_image<nSq, NW>(to + oP * 1024, A.p_t + unit * (nSq * kFragElems), wave);
-    fetch_image<nGate, NW>(to + oGate * 1024, reinterpret_cast<const uint16_t*>(A.gates + unit * (kGateRows * C)), wave);
-  };
   const int chunks = static_cast<int>((r1 - r0 + C - 1) >> kLogC);
-  const auto start = [&](int ch) { return r0 + (static_cast<uint32_t>(ch) << kLogC); };
   int64_t unit = (static_cast<int64_t>(first) + chunks - 1) * z.H + h;
   int buf = 0;
-  if (chunks) fetch(start(chunks - 1), unit, 0);
-  fetch_done();
-  for (int ch = chunks - 1; ch >= 0; --ch, unit -= z.H, buf ^= 1) {
-    f32x4 dU[RT] = {}, dO[RT];
+  T rd[RT][4];
+  f32x4 dO[RT];
+  const auto start = [&](int ch) { return r0 + (static_cast<uint32_t>(ch) << kLogC); };
+  const auto rows_at = [&](int ch) { return r1 - start(ch) < static_cast<uint32_t>(C) ? static_cast<int>(r1 - start(ch)) : C; };
+  const auto load_do = [&](int ch) { load_column<RT>(rd, A.d_o.row(start(ch), h), A.d_o.st, vcol, rows_at(ch) - 1); };
+  const auto take_do = [&] {
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) dO[i][r] = to_f32(rd[i][r]);
+  };
+  const auto fetch_p = [&](uint32_t to, int64_t unit) {
+    fetch_image<nP, NW, 5>(to, A.units + unit * Rec::kElems + Rec::oP * kFragElems, wave);
+  };
+  const auto fetch_next = [&](int ch, int64_t unit, int buf) {
+    const uint32_t to = lds0 + buf * kBuf * 1024;
+    fetch_rows<RT, KD, kIn, NW>(to, A.k, start(ch), rows_at(ch) - 1, hk, wave);
+    fetch_image<nHead, NW, 4>(to + nRows * 1024, A.units + unit * Rec::kElems, wave);
+    if (!PAIR) fetch_p(to + (nRows + nHead) * 1024, unit);
+  };
+  const auto fetch_t = [&](int at, const uint16_t* image, int64_t unit) {
+    fetch_image<nT, NW>(lds0 + at * 1024, image + (unit / z.H * z.Hk + hk) * (nT * kFragElems), wave);
+  };
+  // dU += P^T dO
+  const auto add_p = [&](f32x4 (&dU)[RT], const char* img) {
+    static_for<KC>([&](auto kt) {
+      constexpr int to = 2 * kt.value + 2;
+      const Frag<kIn> f = frag_of<kIn>(dO[2 * kt.value], dO[2 * kt.value + 1]);
+      Frag<kW> fp[RT];
+#pragma unroll
+      for (int j = 0; j < to; ++j) fp[j] = lds_frag<kW, kW>(img, upper_frag<KC>(j, kt.value));
+      mm_tiles<kW, 0, to>(dU, fp, f);
+    });
+  };
+  // S += Q^T or K^T times `x`
+  const auto add_t = [&](f32x4 (&S)[DT], const char* img, const f32x4 (&y)[RT]) {
+#pragma unroll
+    for (int kt = 0; kt < KC; ++kt) {
+      const Frag<kW> f = frag_of<kW>(y[2 * kt], y[2 * kt + 1]);
+      Frag<kIn> ft[DT];
+#pragma unroll
+      for (int i = 0; i < DT; ++i) ft[i] = lds_frag<kIn, kIn>(img, i * KC + kt);
+      mm_tiles<kW, 0, DT>(S, ft, f);
+    }
+  };
+  const auto scale_do = [&](const float* gate) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) dO[i] *= gate4(gate, C, kEG, rho(i, 4 * lg)) * z.scale;
+  };
+  // dV, and dY's image, from dY with rows v and columns t
+  const auto put_y = [&](const f32x4 (&yt)[RT], const float* gate, int ch, int64_t unit) {
+    put_image<RT, kOut>(yt, A.dy + unit * (C * dvp * kOut), v0, z.dv, dvp / 32);
+    f32x4 dv[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) dv[i] = yt[i] * gate[kBeta * C + rho(i, c)];
+    store_rows<RT>(dv, A.dv.row(start(ch), h), A.dv.st, v0, z.dv, rows_at(ch));
+  };
+
+  if (PAIR && wave_ >= NW) {
+    if (chunks) {
+      load_do(chunks - 1);
+      fetch_next(chunks - 1, unit, 0);
+      fetch_t(oQT, A.q_t, unit);
+      fetch_p(lds0 + oPs * 1024, unit);
+      take_do();
+    }
+    fetch_done();
+    __syncthreads();
+    const auto give_p = [&] {
+      f32x4 w[RT] = {};
+      add_p(w, lds + oPs * 1024);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) x_p[i * 64] = w[i];
+    };
+    if (chunks) give_p();
+    for (int ch = chunks - 1; ch >= 0; --ch, unit -= z.H, buf ^= 1) {
+      __syncthreads();  // P^T dO and this chunk's fragments are there, the last one's have been read
+      fetch_t(oKT, A.k_t, unit);
+      if (ch > 0) {
+        fetch_next(ch - 1, unit - z.H, buf ^ 1);
+        fetch_p(lds0 + oPs * 1024, unit - z.H);
+        load_do(ch - 1);
+      }
+      const char* img = lds + buf * kBuf * 1024;
+      const float* gate = reinterpret_cast<const float*>(img + (nRows + Rec::oGate) * 1024);
+      {
+        scale_do(gate);
+        f32x4 w[DT] = {};
+        add_t(w, lds + oQT * 1024, dO);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) x_q[i * 64] = w[i];
+      }
+      fetch_done();
+      __syncthreads();  // as in the first wave; dU is there, and Q^T has been read
+      if (ch > 0) fetch_t(oQT, A.q_t, unit - z.H);
+      {
+        f32x4 yt[RT] = {};
+        static_for<KC>([&](auto kt) {
+          constexpr int to = 2 * kt.value + 2;
+          Frag<kOut> fi[RT];
+#pragma unroll
+          for (int j = 0; j < to; ++j) fi[j] = lds_frag<kOut, kW>(img + nRows * 1024, upper_frag<KC>(j, kt.value));
+          mm_tiles<kOut, 0, to, true>(yt, fi, lds_frag<kOut, kOut>(x, kt.value));
+        });
+        put_y(yt, gate, ch, unit);
+      }
+      if (ch > 0) {
+        take_do();
+        give_p();
+      }
+      fetch_done();
+    }
+    return;
+  }
+
+  const int64_t size = static_cast<int64_t>(z.dk) * z.dv, of = (static_cast<int64_t>(s) * z.H + h) * size;
+  f32x4 S[DT] = {};
+  if (A.ds1) {
+    float y[DT][4];
+    load_state<DT>(y, A.ds1 + of, z.dk, z.dv, vcol);
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = rho(i, 4 * lg + r) < z.dk ? y[i][r] : 0.0f;
+  }
+  if (PAIR) {
+    __syncthreads();
+  } else {
+    if (chunks) {
+      load_do(chunks - 1);
+      fetch_next(chunks - 1, unit, 0);
+    }
+    fetch_done();
+  }
+  for (int ch = chunks - 1; ch >= 0; --ch, unit -= z.H, buf ^= 1) {
+    if (!PAIR) take_do();
     __syncthreads();  // this chunk's fragments are there, the last one's have been read
-    const int64_t at = (unit / z.H * z.Hk + hk) * (nT * kFragElems);
-    fetch_image<nT, NW>(lds0 + 2 * kBuf, A.k_t + at, wave);
-    fetch_image<nT, NW>(lds0 + 2 * kBuf + nT * 1024, A.q_t + at, wave);
-    if (ch > 0) fetch(start(ch - 1), unit - z.H, buf ^ 1);
+    if (!PAIR) {
+      fetch_t(oKT, A.k_t, unit);
+      fetch_t(oQT, A.q_t, unit);
+      if (ch > 0) {
+        load_do(ch - 1);
+        fetch_next(ch - 1, unit - z.H, buf ^ 1);
+      }
+    }
     store_state<DT>(S, A.ds + unit * size, z.dk, z.dv, col);
-    const char* img = lds + buf * kBuf;
-    const float* gate = reinterpret_cast<const float*>(img + oGate * 1024);
+    const char* img = lds + buf * kBuf * 1024;
+    const float* gate = reinterpret_cast<const float*>(img + (nRows + Rec::oGate) * 1024);
+    f32x4 dU[RT] = {};
 #pragma unroll
     for (int ks = 0; ks < KD; ++ks) {
       const Frag<kW> f = frag_of<kW>(S[2 * ks], S[2 * ks + 1]);
@@ -102,54 +216,41 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaSizes z, Chai
     }
 #pragma unroll
     for (int i = 0; i < RT; ++i) dU[i] *= gate4(gate, C, kRest, rho(i, 4 * lg));
-    static_for<KC>([&](auto kt) {
-      constexpr int to = 2 * kt.value + 2;
-      const Frag<kIn> f = frag_of<kIn>(dO[2 * kt.value], dO[2 * kt.value + 1]);
-      Frag<kW> fp[RT];
+    if (PAIR) {
 #pragma unroll
-      for (int j = 0; j < to; ++j) fp[j] = lds_frag<kW, kW>(img + oP * 1024, upper_frag<KC>(j, kt.value));
-      mm_tiles<kW, 0, to>(dU, fp, f);
-    });
+      for (int i = 0; i < RT; ++i) dU[i] += x_p[i * 64];
+    } else {
+      add_p(dU, img + (nRows + nHead) * 1024);
+    }
     f32x4 dN[RT] = {}, yt[RT] = {};  // dY, and dY with rows v and columns t
     static_for<KC>([&](auto kt) {
       constexpr int to = 2 * kt.value + 2;
       const Frag<kW> f = frag_of<kW>(dU[2 * kt.value], dU[2 * kt.value + 1]);
+      if (PAIR) lds_put<kOut>(x, kt.value, f);
       Frag<kW> fi[RT];
 #pragma unroll
-      for (int j = 0; j < to; ++j) fi[j] = lds_frag<kW, kW>(img + oInv * 1024, upper_frag<KC>(j, kt.value));
+      for (int j = 0; j < to; ++j) fi[j] = lds_frag<kW, kW>(img + nRows * 1024, upper_frag<KC>(j, kt.value));
       mm_tiles<kW, 0, to>(dN, fi, f);
-      mm_tiles<kOut, 0, to, true>(yt, fi, f);
+      if (!PAIR) mm_tiles<kOut, 0, to, true>(yt, fi, f);
     });
-    put_image<RT, kOut>(yt, A.dy + unit * (C * DVP * kOut), v0, z.dv, DVP / 32);
-    const int n = r1 - start(ch) < static_cast<uint32_t>(C) ? static_cast<int>(r1 - start(ch)) : C;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int t = rho(i, c);
-      if (t < n) store4(A.dv.row(start(ch) + t, h) + v0 + 4 * lg, z.dv - v0 - 4 * lg, yt[i] * gate[kBeta * C + t]);
+    if (!PAIR) {
+      put_y(yt, gate, ch, unit);
+      scale_do(gate);
     }
     const float el = gate[kEnd * C];
 #pragma unroll
     for (int i = 0; i < DT; ++i) S[i] *= el;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const f32x4 eg = gate4(gate, C, kEG, rho(i, 4 * lg));
-      dO[i] *= eg * z.scale;
-      dN[i] *= -eg * gate4(gate, C, kBeta, rho(i, 4 * lg));
-    }
-    fetch_done();
-    __syncthreads();  // K^T and Q^T are there, and the next chunk's fragments
+    for (int i = 0; i < RT; ++i) dN[i] *= -gate4(gate, C, kEG, rho(i, 4 * lg)) * gate4(gate, C, kBeta, rho(i, 4 * lg));
+    if (!PAIR) fetch_done();
+    __syncthreads();  // K^T and Q^T are there (PAIR: K^T, Q^T dO), and the next chunk's fragments
+    if (PAIR) {
 #pragma unroll
-    for (int kt = 0; kt < KC; ++kt) {
-      const Frag<kW> fo = frag_of<kW>(dO[2 * kt], dO[2 * kt + 1]), fn = frag_of<kW>(dN[2 * kt], dN[2 * kt + 1]);
-      Frag<kIn> fq[DT], fk[DT];
-#pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        fq[i] = lds_frag<kIn, kIn>(qt_img, i * KC + kt);
-        fk[i] = lds_frag<kIn, kIn>(kt_img, i * KC + kt);
-      }
-      mm_tiles<kW, 0, DT>(S, fq, fo);
-      mm_tiles<kW, 0, DT>(S, fk, fn);
+      for (int i = 0; i < DT; ++i) S[i] += x_q[i * 64];
+    } else {
+      add_t(S, lds + oQT * 1024, dO);
     }
+    add_t(S, lds + oKT * 1024, dN);
   }
   if (A.ds0) store_state<DT>(S, A.ds0 + of, z.dk, z.dv, col);
 }
@@ -159,8 +260,8 @@ struct GradArgs {
   Rows k, q, d_o;
   Heads<T> dq, dk;
   T *dg, *dbeta;
-  const uint16_t *k_t, *q_t, *dy;
-  const float *g, *gates, *saved, *ds;
+  const uint16_t *k_t, *q_t, *dy, *units;
+  const float *g, *saved, *ds;
   int64_t g_ld, dg_ld, dbeta_ld;
   int image_floats, saved_floats;
 };
@@ -184,7 +285,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
   constexpr int kFrags = KC * (KC + 1), kPairs = 2 * kFrags, kMine = (kPairs + NW - 1) / NW;  // pair tiles, of a wave
   // 1024-byte fragments of the images
   constexpr int nK = RT * KD * kIn, nO = RT * KV * kIn, nV = RT * KV * kW, nTri = kFrags * kW, nSq = RT * KC * kW,
-                nGate = (kGateRows * C * 4 + 1023) / 1024;
+                nGate = Unit<T, true>::nGate;
   constexpr int oO = nK, oN = oO + nO, oY = oN + nV, oA = oY + nV, oB = oA + nTri, oZ = oB + nTri, oGate = oZ + nSq;
   __shared__ __align__(16) char lds[(oGate + nGate) * 1024];
   __shared__ float red_q[NW][C], red_s[NW], red_w[NW], diag[C];
@@ -209,9 +310,9 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
     const float *saved = A.saved + unit * A.saved_floats, *ps = saved + A.image_floats, *pd = A.ds + unit * size;
     __syncthreads();  // the last head's images and sums have been read
     fetch_image<nV, NW>(lds0 + oN * 1024, reinterpret_cast<const uint16_t*>(saved), wave);
-    fetch_image<nV, NW>(lds0 + oY * 1024, A.dy + unit * (nV * kFragElems), wave);
-    fetch_rows<RT, KV, kIn, NW>(lds0 + oO * 1024, A.d_o, t0, n - 1, h, wave);
-    fetch_image<nGate, NW>(lds0 + oGate * 1024, reinterpret_cast<const uint16_t*>(A.gates + unit * (kGateRows * C)), wave);
+    fetch_image<nV, NW, nV / 4>(lds0 + oY * 1024, A.dy + unit * (nV * kFragElems), wave);
+    fetch_rows<RT, KV, kIn, NW, nV / 2>(lds0 + oO * 1024, A.d_o, t0, n - 1, h, wave);
+    fetch_image<nGate, NW, 7>(lds0 + oGate * 1024, A.units + unit * Unit<T, true>::kElems + Unit<T, true>::oGate * kFragElems, wave);
     // the states' rows of this wave's channels, for the second phase
     const int d = rho(wave, c);
     f32x4 xs[KV][2], xd[KV][2];
@@ -456,12 +557,11 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
 
 template <typename T, int DK>
 void launch_chain(const DeltaSizes& z, const ChainArgs<T>& A, hipStream_t st) {
-  const int64_t chains = static_cast<int64_t>(z.S) * z.H;
-  const int nw = chains >= 256 ? 8 : chains >= 64 ? 4 : 1;  // as in the forward
-  const dim3 grid(static_cast<uint32_t>(z.H * (delta_pad(z.dv) / (16 * nw) + (delta_pad(z.dv) < 16 * nw))), static_cast<uint32_t>(z.S));
-  if (nw == 8) hipLaunchKernelGGL((delta_chain_kernel<T, DK, 8>), grid, dim3(512), 0, st, z, A);
-  else if (nw == 4) hipLaunchKernelGGL((delta_chain_kernel<T, DK, 4>), grid, dim3(256), 0, st, z, A);
-  else hipLaunchKernelGGL((delta_chain_kernel<T, DK, 1>), grid, dim3(64), 0, st, z, A);
+  const int nw = delta_chain_waves(z);
+  const dim3 grid(static_cast<uint32_t>(z.H * ceil_div(delta_pad(z.dv), 16 * nw)), static_cast<uint32_t>(z.S));
+  if (nw == 8) hipLaunchKernelGGL((delta_chain_kernel<T, DK, 8, false>), grid, dim3(512), 0, st, z, A);
+  else if (nw == 2) hipLaunchKernelGGL((delta_chain_kernel<T, DK, 2, true>), grid, dim3(256), 0, st, z, A);
+  else hipLaunchKernelGGL((delta_chain_kernel<T, DK, 1, true>), grid, dim3(128), 0, st, z, A);
 }
 
 template <typename T, int DK, int DV>
@@ -534,17 +634,15 @@ extern "C" int det_delta_rule_bwd(const void* d_o, int64_t do_st, int64_t do_sh,
   if (T)
     r = delta_prepare(z, dtype, true, q, q_st, q_sh, k, k_st, k_sh, d_o, do_st, do_sh, g, g_ld, beta, beta_ld, base, l, st);
   const auto words = [&](size_t at) { return reinterpret_cast<uint16_t*>(base + at); };
-  const auto* gate = reinterpret_cast<const float*>(base + l.gates);
   auto* ds = reinterpret_cast<float*>(base + l.ds);
   const int image = static_cast<int>(delta_image_floats(dv, dtype)), saved = static_cast<int>(delta_saved_floats(dk, dv, dtype));
 #define DET_DELTA_BWD(E)                                                                                               \
   {                                                                                                                    \
     const ChainArgs<E> A{r.k, {static_cast<const E*>(d_o), do_st, do_sh}, {static_cast<E*>(dv_out), dv_st, dv_sh},     \
-                         words(l.k_t), words(l.q_t), words(l.inverse), words(l.p), gate, dfinal_state, ds,             \
-                         dinitial_state, words(l.dy)};                                                                 \
+                         words(l.k_t), words(l.q_t), words(l.units), dfinal_state, ds, dinitial_state, words(l.dy)};   \
     const GradArgs<E> B{r.k, r.q, r.d_o, {static_cast<E*>(dq), dq_st, dq_sh},                                          \
                         {static_cast<E*>(dk_out), dk_st, dk_sh}, static_cast<E*>(dg), static_cast<E*>(dbeta),          \
-                        words(l.k_t), words(l.q_t), words(l.dy), g, gate, states, ds, g_ld, dg_ld, dbeta_ld,           \
+                        words(l.k_t), words(l.q_t), words(l.dy), words(l.units), g, states, ds, g_ld, dg_ld, dbeta_ld,  \
                         image, saved};                                                                                 \
     if (dk <= 64) launch_chain<E, 64>(z, A, st);                                                                       \
     else launch_chain<E, 128>(z, A, st);                                                                               \
