@@ -311,17 +311,19 @@ struct FwdArgs {
 // Workgroup (x, s): value head x % H of sequence s; wave w takes the columns
 // 16 (NW (x / H) + w) .. of v. Heads run fastest, so the workgroups of one head, which
 // read the same fragments, meet in one of the eight L2 caches. A chunk's fragments
-// come into LDS while the chunk before is worked on; those that are needed last have
-// one buffer. PAIR: a second wave for the same columns fetches, and forms O from what the
-// first one leaves in LDS of S0 and U; what is left to the first is the chain of states.
+// come into LDS while the chunk before is worked on; those of K^T, which are needed
+// last, have one buffer, if not two. PAIR: a second wave for the same columns fetches, and forms O, a
+// chunk behind, from what the first one leaves in LDS of S0 and U; what is left to the first
+// is the chain of states.
 template <typename T, int DK, int NW, bool PAIR>
-__global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T> A) {
+__global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T> A) {
   typedef Unit<T, false> Rec;
   constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
-  // fragments in LDS: two buffers of K, the inverse and the gates, then one of K^T; Q and P with the former or (PAIR) the latter
+  // fragments in LDS: two buffers of K, the inverse and the gates, Q and P, one of K^T; PAIR: one of Q and P, alone (NW 1): two of K^T
   constexpr int nRows = RT * KD * kIn, nKT = DT * KC * kIn, nHead = Rec::oP, nP = Rec::nP, nX = (KD + KC) * kOut;
-  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nRows + nP), oKT = 2 * kBuf, oX = oKT + nKT + (PAIR ? nRows + nP : 0);
+  constexpr bool ALONE = PAIR && NW == 1;
+  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nRows + nP), oKT = 2 * kBuf, oQ = oKT + (ALONE ? 2 : 1) * nKT, oX = oQ + (PAIR ? nRows + nP : 0);
   __shared__ __align__(16) char lds[(oX + (PAIR ? NW * nX : 0)) * 1024];
   const int lane = threadIdx.x & 63, wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
   const int wave = PAIR && wave_ >= NW ? wave_ - NW : wave_;
@@ -344,46 +346,77 @@ __global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_fwd_kernel(
       fetch_image<nP, NW, 5>(to + (2 * nRows + nHead) * 1024, rec + Rec::oP * kFragElems, wave);
     }
   };
-  const auto fetch_now = [&](uint32_t t0, int64_t unit) {
-    fetch_image<nKT, NW>(lds0 + oKT * 1024, A.k_t + (unit / z.H * z.Hk + hk) * (nKT * kFragElems), wave);
-    if (PAIR) {
-      fetch_rows<RT, KD, kIn, NW>(lds0 + (oKT + nKT) * 1024, A.q, t0, rows_at(t0) - 1, hk, wave);
-      fetch_image<nP, NW>(lds0 + (oKT + nKT + nRows) * 1024, A.units + unit * Rec::kElems + Rec::oP * kFragElems, wave);
-    }
+  const auto fetch_kt = [&](int64_t unit, int buf) {
+    fetch_image<nKT, NW>(lds0 + (oKT + buf * nKT) * 1024, A.k_t + (unit / z.H * z.Hk + hk) * (nKT * kFragElems), wave);
   };
-  // O: rows v, columns t. (Q S0, then the scales, then P U; in PAIR from the second wave.)
-  const auto scale_o = [&](f32x4 (&o)[RT], const float* gate) {
-#pragma unroll
-    for (int i = 0; i < RT; ++i) o[i] *= gate[kEG * C + rho(i, c)] * z.scale;
+  const auto fetch_qp = [&](uint32_t t0, int64_t unit) {
+    fetch_rows<RT, KD, kIn, NW>(lds0 + oQ * 1024, A.q, t0, rows_at(t0) - 1, hk, wave);
+    fetch_image<nP, NW>(lds0 + (oQ + nRows) * 1024, A.units + unit * Rec::kElems + Rec::oP * kFragElems, wave);
   };
 
   if (PAIR && wave_ >= NW) {
-    if (r0 < r1) fetch_next(r0, unit, 0);
-    fetch_done();
-    for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
-      __syncthreads();  // this chunk's fragments are there, the last one's have been read
-      fetch_now(t0, unit);
-      if (t0 + C < r1) fetch_next(t0 + C, unit + z.H, buf ^ 1);
-      fetch_done();
-      __syncthreads();  // as in the first wave; S0 and U are there
-      const char *q_img = lds + (oKT + nKT) * 1024, *p_img = q_img + nRows * 1024;
+    Frag<kOut> xs[KD], xu[KC];
+    float eg[RT];
+    const auto put_o = [&](uint32_t t0, const auto& read) {  // (rows v, columns t)
+      const char *q_img = lds + oQ * 1024, *p_img = q_img + nRows * 1024;
       f32x4 o[RT] = {};
 #pragma unroll
       for (int ks = 0; ks < KD; ++ks) {
         Frag<kIn> fq[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) fq[i] = lds_frag<kIn, kIn>(q_img, i * KD + ks);
-        mm_tiles<kOut, 0, RT, true>(o, fq, lds_frag<kOut, kOut>(x, ks));
+        mm_tiles<kOut, 0, RT, true>(o, fq, xs[ks]);
       }
-      scale_o(o, reinterpret_cast<const float*>(lds + (buf * kBuf + nRows + Rec::oGate) * 1024));
+#pragma unroll
+      for (int i = 0; i < RT; ++i) o[i] *= eg[i];
       static_for<KC>([&](auto kt) {
         Frag<kOut> fp[RT];
 #pragma unroll
         for (int i = 2 * kt.value; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(p_img, lower_frag(i, kt.value));
-        mm_tiles<kOut, 2 * kt.value, RT, true>(o, fp, lds_frag<kOut, kOut>(x, KD + kt.value));
+        mm_tiles<kOut, 2 * kt.value, RT, true>(o, fp, xu[kt.value]);
       });
+      read();
       store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
+    };
+    if (r0 < r1) {
+      fetch_next(r0, unit, 0);
+      if (ALONE) fetch_kt(unit, 0);
     }
+    fetch_done();
+    constexpr int kNext = fetched(KD * kIn, NW, 0, RT) + fetched(nHead, NW, 4) + (ALONE ? fetched(nKT, NW, 0) : 0);
+    for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
+      __syncthreads();  // this chunk's fragments are there, the last one's have been read
+      if (!ALONE) fetch_kt(unit, 0);
+      const bool more = t0 + C < r1;
+      if (more) {
+        fetch_next(t0 + C, unit + z.H, buf ^ 1);
+        if (ALONE) fetch_kt(unit + z.H, buf ^ 1);
+      }
+      // what was fetched before those: K^T, or the last chunk's Q and P
+      if (more) fetch_done_but<kNext>();
+      else fetch_done();
+      const auto next_qp = [&] {
+        lds_read();
+        if (ALONE) fetch_qp(t0, unit);
+      };
+      if (t0 > r0) put_o(t0 - C, next_qp);
+      else next_qp();
+      __syncthreads();  // S0 and U are there
+      if (!ALONE) fetch_qp(t0, unit);
+#pragma unroll
+      for (int ks = 0; ks < KD; ++ks) xs[ks] = lds_frag<kOut, kOut>(x, ks);
+#pragma unroll
+      for (int kt = 0; kt < KC; ++kt) xu[kt] = lds_frag<kOut, kOut>(x, KD + kt);
+      const float* gate = reinterpret_cast<const float*>(lds + (buf * kBuf + nRows + Rec::oGate) * 1024);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) eg[i] = gate[kEG * C + rho(i, c)] * z.scale;
+      lds_read();
+      if (ALONE) fetch_done_but<fetched(KD * kIn, NW, 0, RT) + fetched(nP, NW, 0)>();
+      else fetch_done();
+    }
+    fetch_done();
+    __syncthreads();
+    if (r0 < r1) put_o(r0 + ((r1 - r0 - 1) >> kLogC << kLogC), [] {});
     return;
   }
 
@@ -413,7 +446,7 @@ __global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_fwd_kernel(
 #pragma unroll
       for (int r = 0; r < 4; ++r) R[i][r] = to_f32(rv[i][r]);
     __syncthreads();  // this chunk's fragments are there, the last one's have been read
-    if (!PAIR) fetch_now(t0, unit);
+    if (!PAIR) fetch_kt(unit, 0);
     if (t0 + C < r1) {
       load_v(t0 + C);
       if (!PAIR) fetch_next(t0 + C, unit + z.H, buf ^ 1);
@@ -439,7 +472,9 @@ __global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_fwd_kernel(
       mm_tiles<kW, 0, RT>(ks0, fk, f);
       if (!PAIR) mm_tiles<kOut, 0, RT, true>(o, fq, f);
     }
-    if (!PAIR) scale_o(o, gate);
+    if (!PAIR)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) o[i] *= gate[kEG * C + rho(i, c)] * z.scale;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const f32x4 eg = gate4(gate, C, kEG, rho(i, 4 * lg));
@@ -483,10 +518,11 @@ __global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_fwd_kernel(
       const Frag<kW> f = frag_of<kW>(U[2 * kt], U[2 * kt + 1]);
       Frag<kIn> fk[DT];
 #pragma unroll
-      for (int i = 0; i < DT; ++i) fk[i] = lds_frag<kIn, kIn>(lds + oKT * 1024, i * KC + kt);
+      for (int i = 0; i < DT; ++i) fk[i] = lds_frag<kIn, kIn>(lds + (oKT + (ALONE ? buf * nKT : 0)) * 1024, i * KC + kt);
       mm_tiles<kW, 0, DT>(S, fk, f);
     }
   }
+  if (PAIR) __syncthreads();
   if (A.s1) store_state<DT>(S, A.s1 + of, z.dk, z.dv, col);
 }
 

@@ -276,6 +276,25 @@ __device__ __forceinline__ void fetch_group(uint32_t lds, const void* base, cons
 #undef DET_FETCH_HEAD
 #undef DET_FETCH_TAIL
 __device__ __forceinline__ void fetch_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All but the last N of this wave.
+template <int N>
+__device__ __forceinline__ void fetch_done_but() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N < 63 ? N : 63) : "memory");
+}
+// What this wave has read of LDS is in its registers (a fetch may write there).
+__device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// The fewest fragments that fetch_image brings in one wave, and fetch_rows (RT tiles of N fragments).
+constexpr int fetched(int N, int NW, int first, int RT = 1) {
+  int least = 1 << 20;
+  const int groups = (N + 3) / 4;
+  for (int w = 0; w < NW; ++w) {
+    int n = 0;
+    for (int g = 0; g < RT * groups; ++g)
+      if ((g + first) % NW == w) n += N - 4 * (g % groups) < 4 ? N - 4 * (g % groups) : 4;
+    least = n < least ? n : least;
+  }
+  return least;
+}
 // N consecutive fragments of an image, four at a time, shared out among NW waves from wave FIRST on.
 template <int N, int NW, int FIRST = 0>
 __device__ __forceinline__ void fetch_image(uint32_t lds, const uint16_t* image, int wave) {
@@ -516,7 +535,7 @@ inline int delta_pad(int64_t d) { return d <= 64 ? 64 : 128; }
 // fragments, where that leaves a workgroup for each compute unit; else spread out, in pairs.
 inline int delta_chain_waves(const DeltaSizes& z) {
   const int64_t chains = static_cast<int64_t>(z.S) * z.H;
-  return chains >= 192 ? 8 : chains >= 64 ? 2 : 1;
+  return chains >= 128 ? 8 : chains >= 64 ? 2 : 1;
 }
 
 // What a forward leaves for the backward per (chunk, value head): N as an image of rows t and

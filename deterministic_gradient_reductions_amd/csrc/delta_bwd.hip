@@ -34,15 +34,16 @@ struct ChainArgs {
 
 // Workgroups, waves and buffers as in the forward's chain. PAIR: the second wave fetches,
 // forms P^T dO (a chunk ahead) and scale (e^G Q)^T dO for the first one, and dV and dY's image
-// from what that leaves of dU.
+// from what that leaves of dU; Q^T goes straight into its registers.
 template <typename T, int DK, int NW, bool PAIR>
-__global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_chain_kernel(DeltaSizes z, ChainArgs<T> A) {
+__global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArgs<T> A) {
   typedef Unit<T, true> Rec;
   constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
-  // fragments in LDS: two buffers of K, the inverse and the gates, then one of K^T and Q^T; P with the former or (PAIR) the latter
+  // fragments in LDS: two buffers of K, the inverse, the gates and P, one of K^T and Q^T; PAIR: one of P, none of Q^T, alone (NW 1) two of K^T
   constexpr int nRows = RT * KD * kIn, nT = DT * KC * kIn, nHead = Rec::oP, nP = Rec::nP, nX = KC * kOut + RT + DT;
-  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nP), oKT = 2 * kBuf, oQT = oKT + nT, oPs = oQT + nT, oX = oPs + (PAIR ? nP : 0);
+  constexpr bool ALONE = PAIR && NW == 1;
+  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nP), oKT = 2 * kBuf, oQT = oKT + nT, oPs = oKT + (ALONE ? 2 : 1) * nT, oX = PAIR ? oPs + nP : oQT + nT;
   __shared__ __align__(16) char lds[(oX + (PAIR ? NW * nX : 0)) * 1024];
   const int lane = threadIdx.x & 63, wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
   const int wave = PAIR && wave_ >= NW ? wave_ - NW : wave_;
@@ -91,17 +92,18 @@ __global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_chain_kerne
       mm_tiles<kW, 0, to>(dU, fp, f);
     });
   };
-  // S += Q^T or K^T times `x`
-  const auto add_t = [&](f32x4 (&S)[DT], const char* img, const f32x4 (&y)[RT]) {
+  // S += Q^T or K^T (at(i KC + kt): the fragment of tile i, places 32 kt ..) times y
+  const auto add_t = [&](f32x4 (&S)[DT], const auto& at, const f32x4 (&y)[RT]) {
 #pragma unroll
     for (int kt = 0; kt < KC; ++kt) {
       const Frag<kW> f = frag_of<kW>(y[2 * kt], y[2 * kt + 1]);
       Frag<kIn> ft[DT];
 #pragma unroll
-      for (int i = 0; i < DT; ++i) ft[i] = lds_frag<kIn, kIn>(img, i * KC + kt);
+      for (int i = 0; i < DT; ++i) ft[i] = at(i * KC + kt);
       mm_tiles<kW, 0, DT>(S, ft, f);
     }
   };
+  const auto lds_t = [&](int at) { return [&, at](int i) { return lds_frag<kIn, kIn>(lds + at * 1024, i); }; };
   const auto scale_do = [&](const float* gate) {
 #pragma unroll
     for (int i = 0; i < RT; ++i) dO[i] *= gate4(gate, C, kEG, rho(i, 4 * lg)) * z.scale;
@@ -116,10 +118,16 @@ __global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_chain_kerne
   };
 
   if (PAIR && wave_ >= NW) {
+    Frag<kIn> qt[DT * KC];
+    const auto load_qt = [&](int64_t unit) {
+      const uint16_t* image = A.q_t + (unit / z.H * z.Hk + hk) * (nT * kFragElems);
+#pragma unroll
+      for (int i = 0; i < DT * KC; ++i) qt[i] = image_frag<kIn, kIn>(image, i);
+    };
     if (chunks) {
       load_do(chunks - 1);
+      load_qt(unit);
       fetch_next(chunks - 1, unit, 0);
-      fetch_t(oQT, A.q_t, unit);
       fetch_p(lds0 + oPs * 1024, unit);
       take_do();
     }
@@ -134,40 +142,44 @@ __global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_chain_kerne
     if (chunks) give_p();
     for (int ch = chunks - 1; ch >= 0; --ch, unit -= z.H, buf ^= 1) {
       __syncthreads();  // P^T dO and this chunk's fragments are there, the last one's have been read
-      fetch_t(oKT, A.k_t, unit);
-      if (ch > 0) {
-        fetch_next(ch - 1, unit - z.H, buf ^ 1);
-        fetch_p(lds0 + oPs * 1024, unit - z.H);
-        load_do(ch - 1);
-      }
       const char* img = lds + buf * kBuf * 1024;
       const float* gate = reinterpret_cast<const float*>(img + (nRows + Rec::oGate) * 1024);
+      if (!ALONE) fetch_t(oKT, A.k_t, unit);
+      if (ch > 0) fetch_p(lds0 + oPs * 1024, unit - z.H);
       {
         scale_do(gate);
         f32x4 w[DT] = {};
-        add_t(w, lds + oQT * 1024, dO);
+        add_t(w, [&](int i) { return qt[i]; }, dO);
 #pragma unroll
         for (int i = 0; i < DT; ++i) x_q[i * 64] = w[i];
       }
-      fetch_done();
-      __syncthreads();  // as in the first wave; dU is there, and Q^T has been read
-      if (ch > 0) fetch_t(oQT, A.q_t, unit - z.H);
-      {
-        f32x4 yt[RT] = {};
-        static_for<KC>([&](auto kt) {
-          constexpr int to = 2 * kt.value + 2;
-          Frag<kOut> fi[RT];
-#pragma unroll
-          for (int j = 0; j < to; ++j) fi[j] = lds_frag<kOut, kW>(img + nRows * 1024, upper_frag<KC>(j, kt.value));
-          mm_tiles<kOut, 0, to, true>(yt, fi, lds_frag<kOut, kOut>(x, kt.value));
-        });
-        put_y(yt, gate, ch, unit);
+      if (ch > 0) {
+        load_do(ch - 1);
+        load_qt(unit - z.H);
+        fetch_next(ch - 1, unit - z.H, buf ^ 1);
       }
+      // K^T's and P's; alone this wave needs them only after the barrier
+      const auto done_now = [&] {
+        if (ch > 0) fetch_done_but<fetched(KD * kIn, NW, 0, RT) + fetched(nHead, NW, 4)>();
+        else fetch_done();
+      };
+      if (!ALONE) done_now();
+      __syncthreads();  // dU is there, and what this wave has left
+      if (ALONE) done_now();
+      f32x4 yt[RT] = {};
+      static_for<KC>([&](auto kt) {
+        constexpr int to = 2 * kt.value + 2;
+        Frag<kOut> fi[RT];
+#pragma unroll
+        for (int j = 0; j < to; ++j) fi[j] = lds_frag<kOut, kW>(img + nRows * 1024, upper_frag<KC>(j, kt.value));
+        mm_tiles<kOut, 0, to, true>(yt, fi, lds_frag<kOut, kOut>(x, kt.value));
+      });
       if (ch > 0) {
         take_do();
         give_p();
       }
-      fetch_done();
+      fetch_done();  // (before the stores, which nothing waits for)
+      put_y(yt, gate, ch, unit);
     }
     return;
   }
@@ -183,6 +195,8 @@ __global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_chain_kerne
       for (int r = 0; r < 4; ++r) S[i][r] = rho(i, 4 * lg + r) < z.dk ? y[i][r] : 0.0f;
   }
   if (PAIR) {
+    if (ALONE && chunks) fetch_t(oKT, A.k_t, unit);
+    if (ALONE) fetch_done();
     __syncthreads();
   } else {
     if (chunks) {
@@ -201,6 +215,8 @@ __global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_chain_kerne
         load_do(ch - 1);
         fetch_next(ch - 1, unit - z.H, buf ^ 1);
       }
+    } else if (ALONE && ch > 0) {
+      fetch_t(oKT + (buf ^ 1) * nT, A.k_t, unit - z.H);
     }
     store_state<DT>(S, A.ds + unit * size, z.dk, z.dv, col);
     const char* img = lds + buf * kBuf * 1024;
@@ -248,9 +264,10 @@ __global__ __launch_bounds__(64 * NW * (PAIR ? 2 : 1), 2) void delta_chain_kerne
 #pragma unroll
       for (int i = 0; i < DT; ++i) S[i] += x_q[i * 64];
     } else {
-      add_t(S, lds + oQT * 1024, dO);
+      add_t(S, lds_t(oQT), dO);
     }
-    add_t(S, lds + oKT * 1024, dN);
+    add_t(S, lds_t(oKT + (ALONE ? buf * nT : 0)), dN);
+    if (ALONE) fetch_done();
   }
   if (A.ds0) store_state<DT>(S, A.ds0 + of, z.dk, z.dv, col);
 }
