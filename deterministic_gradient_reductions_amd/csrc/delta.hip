@@ -14,13 +14,12 @@
 // float32 sum over a chunk would lose (two words). g below -1e4 counts as -1e4 (a
 // factor of 0 either way), which keeps -inf out of the differences.
 //
-// Three kernels. Two work on all chunks side by side: one turns K (the backward: Q too)
-// so that tokens are neighbours, and copies what is not of bf16 in whole 16-byte
-// rows; one forms P and the inverse of I + M B (a wave per chunk and head: 16 x 16
-// diagonal blocks by substitution, the blocks below by float32 matrix
-// instructions) and leaves both as fragments. The third walks the chunks of one
-// sequence and value head in order. There a wave owns 16 columns of v, so its part of
-// S, N, U and O depends on no other wave, what one product leaves in its registers is
+// Two or three kernels. One copies K and Q into padded bf16 words where they are not
+// bf16 in whole 16-byte rows already. One forms, for all chunks side by side, P and the
+// inverse of I + M B (a wave per chunk and head: 16 x 16 diagonal blocks by substitution, the
+// blocks below by float32 matrix instructions) and leaves both as fragments. The last walks the
+// chunks of one sequence and value head in order. There a wave owns 16 columns of v, so its
+// part of S, N, U and O depends on no other wave, what one product leaves in its registers is
 // the next one's operand, and the other operands are fragments of 16 bytes per lane,
 // shared by the workgroup through LDS. What is not on the chain of states is formed
 // before it.
@@ -29,13 +28,12 @@
 namespace detgrad {
 namespace {
 
-// ------------------------------------------------------------------ turn and copy
-// Workgroup (tile, head): the chunk's rows of x, turned into an image with rows d and
-// places t (`turned`, unless NULL) and copied into padded words (`rows`, unless NULL).
+// ------------------------------------------------------------------------------- copy
+// Workgroup (tile, head): the chunk's rows of x in padded words.
 template <typename T, int DIM>
-__global__ __launch_bounds__(256) void delta_turn_kernel(DeltaSizes z, Heads<const T> x, int heads, int dim,
-                                                         uint16_t* __restrict__ turned, uint16_t* __restrict__ rows) {
-  constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC, KC = C / 32;
+__global__ __launch_bounds__(256) void delta_copy_kernel(DeltaSizes z, Heads<const T> x, int heads, int dim,
+                                                         uint16_t* __restrict__ rows) {
+  constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   const uint32_t tile = blockIdx.x;
   const int h = blockIdx.y;
   int e;
@@ -43,42 +41,25 @@ __global__ __launch_bounds__(256) void delta_turn_kernel(DeltaSizes z, Heads<con
   if (!segment_tile<1>(z.offs, z.S, static_cast<uint32_t>(z.T), kLogC, tile, e, r0, r1, s0, s1)) return;
   const int n = static_cast<int>(r1 - r0);
   const bool whole = dim % 4 == 0;
-  constexpr int kSize = C * DIM * kIn;
-  if (turned) turned += (static_cast<int64_t>(tile) * heads + h) * kSize;
-  for (int id = threadIdx.x; id < C * DIM / 16; id += 256) {
-    const int t = id / (DIM / 4) * 4, d = id % (DIM / 4) * 4;
-    f32x4 v[4];
+  constexpr int kEach = C * DIM / 4 / 256;
+  f32x4 v[kEach];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = load4(x.row(r0 + (t + j < n ? t + j : 0), h), d, dim, whole);
+  for (int u = 0; u < kEach; ++u) {
+    const int id = threadIdx.x + u * 256, t = id / (DIM / 4), d = id % (DIM / 4) * 4;
+    v[u] = load4(x.row(r0 + (t < n ? t : 0), h), d, dim, whole);
+  }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = t + j < n ? v[j] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    bf16x4 w[kIn][4];  // of row j, then of column j
+  for (int u = 0; u < kEach; ++u) {
+    const int id = threadIdx.x + u * 256, t = id / (DIM / 4), d = id % (DIM / 4) * 4;
+    if (t >= n) continue;
+    uint32_t a[kIn], b[kIn];
+    split2<kIn>(v[u][0], v[u][1], a);
+    split2<kIn>(v[u][2], v[u][3], b);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        __bf16 y[kIn];
-        split<kIn>(v[j][i], y);
-#pragma unroll
-        for (int p = 0; p < kIn; ++p) w[p][j][i] = y[p];
-      }
-    if (rows)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (t + j < n)
-#pragma unroll
-          for (int p = 0; p < kIn; ++p)
-            __builtin_memcpy(rows + ((static_cast<int64_t>(r0 + t + j) * heads + h) * kIn + p) * DIM + d, &w[p][j], 8);
-    if (turned)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint16_t* to = turned + image_at<KC, kIn>(d + i, t);
-#pragma unroll
-        for (int p = 0; p < kIn; ++p) {
-          const bf16x4 u = {w[p][0][i], w[p][1][i], w[p][2][i], w[p][3][i]};
-          __builtin_memcpy(to + p * kFragElems, &u, 8);
-        }
-      }
+    for (int p = 0; p < kIn; ++p) {
+      const uint64_t w = a[p] | static_cast<uint64_t>(b[p]) << 32;
+      __builtin_memcpy(rows + ((static_cast<int64_t>(r0 + t) * heads + h) * kIn + p) * DIM + d, &w, 8);
+    }
   }
 }
 
@@ -137,7 +118,10 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSiz
       to[kEG * C + lane] = lane < n ? eg : 0.0f;
       const double rest = last - G;
       const float q0 = static_cast<float>(rest);
-      to[kRest * C + lane] = exp_e(q0) * (1.0f + static_cast<float>(rest - q0));
+      const float er = exp_e(q0) * (1.0f + static_cast<float>(rest - q0));
+      to[kRest * C + lane] = er;
+      to[kRestBeta * C + lane] = er * b;
+      to[kEGBeta * C + lane] = -eg * b;
       to[kBeta * C + lane] = b;
       to[kEnd * C + lane] = end;
     }
@@ -302,7 +286,7 @@ struct FwdArgs {
   Rows k, q;
   Heads<const T> v;
   Heads<T> o;
-  const uint16_t *k_t, *units;
+  const uint16_t* units;
   const float* s0;
   float *s1, *saved;  // the final state; what the backward needs (delta_saved_floats)
   int image_floats, saved_floats;
@@ -311,25 +295,26 @@ struct FwdArgs {
 // Workgroup (x, s): value head x % H of sequence s; wave w takes the columns
 // 16 (NW (x / H) + w) .. of v. Heads run fastest, so the workgroups of one head, which
 // read the same fragments, meet in one of the eight L2 caches. A chunk's fragments
-// come into LDS while the chunk before is worked on; those of K^T, which are needed
-// last, have one buffer, if not two. PAIR: a second wave for the same columns fetches, and forms O, a
-// chunk behind, from what the first one leaves in LDS of S0 and U; what is left to the first
-// is the chain of states.
+// come into LDS while the chunk before is worked on; K^T is read there from K's rows. PAIR: a
+// second wave for the same columns fetches, and forms O, a chunk behind, from what the first
+// one leaves in LDS of S0 and N; what is left to the first is the chain of states. The
+// state goes from chunk to chunk as itself and as fragments, whose words are made
+// while the matrix instructions of the other half of it run.
 template <typename T, int DK, int NW, bool PAIR>
 __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T> A) {
   typedef Unit<T, false> Rec;
   constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
-  // fragments in LDS: two buffers of K, the inverse and the gates, Q and P, one of K^T; PAIR: one of Q and P, alone (NW 1): two of K^T
-  constexpr int nRows = RT * KD * kIn, nKT = DT * KC * kIn, nHead = Rec::oP, nP = Rec::nP, nX = (KD + KC) * kOut;
   constexpr bool ALONE = PAIR && NW == 1;
-  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nRows + nP), oKT = 2 * kBuf, oQ = oKT + (ALONE ? 2 : 1) * nKT, oX = oQ + (PAIR ? nRows + nP : 0);
+  // fragments in LDS: two buffers of K, the inverse and the gates, Q and P (PAIR: one of these two); V of each wave
+  constexpr int nRows = RT * KD * kIn, nHead = Rec::oP, nP = Rec::nP, nX = KD * kOut + RT;
+  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nRows + nP), oQ = 2 * kBuf, oV = oQ + (PAIR ? nRows + nP : 0), oX = oV + 2 * NW;
   __shared__ __align__(16) char lds[(oX + (PAIR ? NW * nX : 0)) * 1024];
   const int lane = threadIdx.x & 63, wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
   const int wave = PAIR && wave_ >= NW ? wave_ - NW : wave_;
   const int h = blockIdx.x % z.H, hk = h / (z.H / z.Hk), v0 = ((blockIdx.x / z.H) * NW + wave) * 16, s = blockIdx.y;
   const uint32_t lds0 = lds_address(lds);
-  char* x = lds + (oX + (PAIR ? wave * nX : 0)) * 1024;  // S0 and U of these columns
+  char* x = lds + (oX + (PAIR ? wave * nX : 0)) * 1024;  // S0 and N of these columns
   uint32_t r0, r1, first;
   segment_rows(z.offs, s, static_cast<uint32_t>(z.T), kLogC, r0, r1, first);
   int64_t unit = static_cast<int64_t>(first) * z.H + h;
@@ -346,9 +331,6 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
       fetch_image<nP, NW, 5>(to + (2 * nRows + nHead) * 1024, rec + Rec::oP * kFragElems, wave);
     }
   };
-  const auto fetch_kt = [&](int64_t unit, int buf) {
-    fetch_image<nKT, NW>(lds0 + (oKT + buf * nKT) * 1024, A.k_t + (unit / z.H * z.Hk + hk) * (nKT * kFragElems), wave);
-  };
   const auto fetch_qp = [&](uint32_t t0, int64_t unit) {
     fetch_rows<RT, KD, kIn, NW>(lds0 + oQ * 1024, A.q, t0, rows_at(t0) - 1, hk, wave);
     fetch_image<nP, NW>(lds0 + (oQ + nRows) * 1024, A.units + unit * Rec::kElems + Rec::oP * kFragElems, wave);
@@ -356,6 +338,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
 
   if (PAIR && wave_ >= NW) {
     Frag<kOut> xs[KD], xu[KC];
+    f32x4 nt[RT];
     float eg[RT];
     const auto put_o = [&](uint32_t t0, const auto& read) {  // (rows v, columns t)
       const char *q_img = lds + oQ * 1024, *p_img = q_img + nRows * 1024;
@@ -364,7 +347,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
       for (int ks = 0; ks < KD; ++ks) {
         Frag<kIn> fq[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) fq[i] = lds_frag<kIn, kIn>(q_img, i * KD + ks);
+        for (int i = 0; i < RT; ++i) fq[i] = row_frag<kIn>(q_img, i * KD + ks);
         mm_tiles<kOut, 0, RT, true>(o, fq, xs[ks]);
       }
 #pragma unroll
@@ -376,24 +359,18 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
         mm_tiles<kOut, 2 * kt.value, RT, true>(o, fp, xu[kt.value]);
       });
       read();
+      if (A.saved)
+        put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + (unit - z.H) * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
       store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
     };
-    if (r0 < r1) {
-      fetch_next(r0, unit, 0);
-      if (ALONE) fetch_kt(unit, 0);
-    }
+    if (r0 < r1) fetch_next(r0, unit, 0);
     fetch_done();
-    constexpr int kNext = fetched(KD * kIn, NW, 0, RT) + fetched(nHead, NW, 4) + (ALONE ? fetched(nKT, NW, 0) : 0);
     for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
       __syncthreads();  // this chunk's fragments are there, the last one's have been read
-      if (!ALONE) fetch_kt(unit, 0);
       const bool more = t0 + C < r1;
-      if (more) {
-        fetch_next(t0 + C, unit + z.H, buf ^ 1);
-        if (ALONE) fetch_kt(unit + z.H, buf ^ 1);
-      }
-      // what was fetched before those: K^T, or the last chunk's Q and P
-      if (more) fetch_done_but<kNext>();
+      if (more) fetch_next(t0 + C, unit + z.H, buf ^ 1);
+      // the last chunk's Q and P, fetched before those
+      if (more) fetch_done_but<fetched(KD * kIn, NW, 0, RT) + fetched(nHead, NW, 4)>();
       else fetch_done();
       const auto next_qp = [&] {
         lds_read();
@@ -401,13 +378,19 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
       };
       if (t0 > r0) put_o(t0 - C, next_qp);
       else next_qp();
-      __syncthreads();  // S0 and U are there
+      __syncthreads();  // S0 and N are there
       if (!ALONE) fetch_qp(t0, unit);
 #pragma unroll
       for (int ks = 0; ks < KD; ++ks) xs[ks] = lds_frag<kOut, kOut>(x, ks);
-#pragma unroll
-      for (int kt = 0; kt < KC; ++kt) xu[kt] = lds_frag<kOut, kOut>(x, KD + kt);
       const float* gate = reinterpret_cast<const float*>(lds + (buf * kBuf + nRows + Rec::oGate) * 1024);
+      char* xn = x + KD * kOut * 1024;
+#pragma unroll
+      for (int kt = 0; kt < KC; ++kt)
+        xu[kt] = frag_of<kOut>(*lds_tile(xn + 2 * kt * 1024) * gate4(gate, C, kBeta, rho(2 * kt, 4 * lg)),
+                               *lds_tile(xn + (2 * kt + 1) * 1024) * gate4(gate, C, kBeta, rho(2 * kt + 1, 4 * lg)));
+      if (A.saved)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) nt[i] = lds_turned(xn + i * 1024);
 #pragma unroll
       for (int i = 0; i < RT; ++i) eg[i] = gate[kEG * C + rho(i, c)] * z.scale;
       lds_read();
@@ -432,45 +415,53 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[i][r] = rho(i, 4 * lg + r) < z.dk ? y[i][r] : 0.0f;
   }
+  Frag<kW> f[KD];  // of S
+#pragma unroll
+  for (int ks = 0; ks < KD; ++ks) f[ks] = frag_of<kW>(S[2 * ks], S[2 * ks + 1]);
+  char* v_tile = lds + (oV + 2 * wave) * 1024;
+  const bool whole = whole_columns(A.v, v0, z.dv);
   T rv[RT][4];
-  const auto load_v = [&](uint32_t t0) { load_column<RT>(rv, A.v.row(t0, h), A.v.st, vcol, rows_at(t0) - 1); };
+  const auto next_v = [&](uint32_t t0) {
+    lds_read();  // (the last one's)
+    if (whole) fetch_columns<RT>(lds0 + (oV + 2 * wave) * 1024, A.v, t0, h, v0, rows_at(t0) - 1);
+    else load_column<RT>(rv, A.v.row(t0, h), A.v.st, vcol, rows_at(t0) - 1);
+  };
   if (r0 < r1) {
-    load_v(r0);
+    next_v(r0);
     if (!PAIR) fetch_next(r0, unit, 0);
   }
-  if (!PAIR) fetch_done();
+  fetch_done();
   for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
-    f32x4 R[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) R[i][r] = to_f32(rv[i][r]);
     __syncthreads();  // this chunk's fragments are there, the last one's have been read
-    if (!PAIR) fetch_kt(unit, 0);
-    if (t0 + C < r1) {
-      load_v(t0 + C);
-      if (!PAIR) fetch_next(t0 + C, unit + z.H, buf ^ 1);
-    }
+    if (!PAIR && t0 + C < r1) fetch_next(t0 + C, unit + z.H, buf ^ 1);
     if (A.saved) store_state<DT>(S, A.saved + unit * A.saved_floats + A.image_floats, z.dk, z.dv, col);
     const char* img = lds + buf * kBuf * 1024;
     const float* gate = reinterpret_cast<const float*>(img + (nRows + Rec::oGate) * 1024);
+    f32x4 R[RT];
+    if (whole) {
+      take_columns<RT>(R, v_tile, static_cast<const T*>(nullptr));
+    } else {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) R[i][r] = to_f32(rv[i][r]);
+    }
 
     // K S0 (rows t, columns v) and its transposed Q S0 (rows v, columns t)
     f32x4 ks0[RT] = {}, o[RT] = {};
 #pragma unroll
     for (int ks = 0; ks < KD; ++ks) {
-      const Frag<kW> f = frag_of<kW>(S[2 * ks], S[2 * ks + 1]);
       Frag<kIn> fk[RT], fq[RT];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) fk[i] = lds_frag<kIn, kIn>(img, i * KD + ks);
+      for (int i = 0; i < RT; ++i) fk[i] = row_frag<kIn>(img, i * KD + ks);
       if (PAIR) {
-        lds_put<kOut>(x, ks, f);
+        lds_put<kOut>(x, ks, f[ks]);
       } else {
 #pragma unroll
-        for (int i = 0; i < RT; ++i) fq[i] = lds_frag<kIn, kIn>(img + (nRows + nHead) * 1024, i * KD + ks);
+        for (int i = 0; i < RT; ++i) fq[i] = row_frag<kIn>(img + (nRows + nHead) * 1024, i * KD + ks);
       }
-      mm_tiles<kW, 0, RT>(ks0, fk, f);
-      if (!PAIR) mm_tiles<kOut, 0, RT, true>(o, fq, f);
+      mm_tiles<kW, 0, RT>(ks0, fk, f[ks]);
+      if (!PAIR) mm_tiles<kOut, 0, RT, true>(o, fq, f[ks]);
     }
     if (!PAIR)
 #pragma unroll
@@ -481,57 +472,44 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
 #pragma unroll
       for (int r = 0; r < 4; ++r) R[i][r] = __builtin_fmaf(-eg[r], ks0[i][r], R[i][r]);
     }
-    // N, then U = beta N
+    if (t0 + C < r1) next_v(t0 + C);
+    // N
     f32x4 U[RT] = {}, nt[RT] = {};  // nt: N with rows v and columns t, for the backward
     static_for<KC>([&](auto kt) {
-      const Frag<kW> f = frag_of<kW>(R[2 * kt.value], R[2 * kt.value + 1]);
+      const Frag<kW> fr = frag_of<kW>(R[2 * kt.value], R[2 * kt.value + 1]);
       Frag<kW> fi[RT];
 #pragma unroll
       for (int i = 2 * kt.value; i < RT; ++i) fi[i] = lds_frag<kW, kW>(img + nRows * 1024, lower_frag(i, kt.value));
-      mm_tiles<kW, 2 * kt.value, RT>(U, fi, f);
-      if (A.saved) mm_tiles<kOut, 2 * kt.value, RT, true>(nt, fi, f);
+      mm_tiles<kW, 2 * kt.value, RT>(U, fi, fr);
+      if (!PAIR && A.saved) mm_tiles<kOut, 2 * kt.value, RT, true>(nt, fi, fr);
     });
-    if (A.saved) put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
+    if (!PAIR && A.saved) put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
+    if (PAIR) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) U[i] *= gate4(gate, C, kBeta, rho(i, 4 * lg));
-    static_for<KC>([&](auto kt) {
-      const Frag<kOut> f = frag_of<kOut>(U[2 * kt.value], U[2 * kt.value + 1]);
-      if (PAIR) {
-        lds_put<kOut>(x, KD + kt.value, f);
-      } else {
+      for (int i = 0; i < RT; ++i) *lds_tile(x + (KD * kOut + i) * 1024) = U[i];
+    } else {
+      static_for<KC>([&](auto kt) {
+        constexpr int k = 2 * kt.value;
+        const Frag<kOut> fu = frag_of<kOut>(U[k] * gate4(gate, C, kBeta, rho(k, 4 * lg)), U[k + 1] * gate4(gate, C, kBeta, rho(k + 1, 4 * lg)));
         Frag<kOut> fp[RT];
 #pragma unroll
-        for (int i = 2 * kt.value; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(img + (2 * nRows + nHead) * 1024, lower_frag(i, kt.value));
-        mm_tiles<kOut, 2 * kt.value, RT, true>(o, fp, f);
-      }
-    });
+        for (int i = k; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(img + (2 * nRows + nHead) * 1024, lower_frag(i, kt.value));
+        mm_tiles<kOut, k, RT, true>(o, fp, fu);
+      });
+      store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
+    }
     const float el = gate[kEnd * C];
 #pragma unroll
-    for (int i = 0; i < DT; ++i) S[i] *= el;
+    for (int i = 0; i < RT; ++i) U[i] *= gate4(gate, C, kRestBeta, rho(i, 4 * lg));
+    if (PAIR) __syncthreads();  // S0 and N are there
+    Frag<kW> fu[KC];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) U[i] *= gate4(gate, C, kRest, rho(i, 4 * lg));
-    if (!PAIR) fetch_done();
-    __syncthreads();  // K^T is there, and the next chunk's fragments
-    if (!PAIR) store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
-#pragma unroll
-    for (int kt = 0; kt < KC; ++kt) {
-      const Frag<kW> f = frag_of<kW>(U[2 * kt], U[2 * kt + 1]);
-      Frag<kIn> fk[DT];
-#pragma unroll
-      for (int i = 0; i < DT; ++i) fk[i] = lds_frag<kIn, kIn>(lds + (oKT + (ALONE ? buf * nKT : 0)) * 1024, i * KC + kt);
-      mm_tiles<kW, 0, DT>(S, fk, f);
-    }
+    for (int kt = 0; kt < KC; ++kt) fu[kt] = frag_of<kW>(U[2 * kt], U[2 * kt + 1]);
+    next_state<kIn, KC>(S, f, img, fu, el);
+    fetch_done();
   }
   if (PAIR) __syncthreads();
   if (A.s1) store_state<DT>(S, A.s1 + of, z.dk, z.dv, col);
-}
-
-template <typename T, int DIM>
-void launch_turn(const DeltaSizes& z, int dtype, const Heads<const T>& x, int heads, int dim, uint16_t* turned, uint16_t* rows,
-                 hipStream_t st) {
-  if (!turned && !rows) return;
-  const dim3 grid(static_cast<uint32_t>(delta_tiles(z.T, z.S, dtype)), static_cast<uint32_t>(heads));
-  hipLaunchKernelGGL((delta_turn_kernel<T, DIM>), grid, dim3(256), 0, st, z, x, heads, dim, turned, rows);
 }
 
 // Whether the kernels can read a tensor's rows as they are.
@@ -540,13 +518,13 @@ bool as_it_is(const void* p, int64_t st, int64_t sh, int64_t dim) {
 }
 
 template <typename T>
-Rows rows_of(const DeltaSizes& z, int dtype, const void* x, int64_t x_st, int64_t x_sh, int heads, int dim, uint16_t* turned,
-             uint16_t* copy, hipStream_t st) {
-  const bool direct = sizeof(T) == 2 && as_it_is(x, x_st, x_sh, dim);
+Rows rows_of(const DeltaSizes& z, int dtype, const void* x, int64_t x_st, int64_t x_sh, int heads, int dim, uint16_t* copy,
+             hipStream_t st) {
+  if (sizeof(T) == 2 && as_it_is(x, x_st, x_sh, dim)) return {static_cast<const uint16_t*>(x), x_st, x_sh, 0};
   const Heads<const T> h{static_cast<const T*>(x), x_st, x_sh};
-  if (dim <= 64) launch_turn<T, 64>(z, dtype, h, heads, dim, turned, direct ? nullptr : copy, st);
-  else launch_turn<T, 128>(z, dtype, h, heads, dim, turned, direct ? nullptr : copy, st);
-  if (direct) return {static_cast<const uint16_t*>(x), x_st, x_sh, 0};
+  const dim3 grid(static_cast<uint32_t>(delta_tiles(z.T, z.S, dtype)), static_cast<uint32_t>(heads));
+  if (dim <= 64) hipLaunchKernelGGL((delta_copy_kernel<T, 64>), grid, dim3(256), 0, st, z, h, heads, dim, copy);
+  else hipLaunchKernelGGL((delta_copy_kernel<T, 128>), grid, dim3(256), 0, st, z, h, heads, dim, copy);
   const int pad = delta_pad(dim), words = delta_words(dtype);
   return {copy, static_cast<int64_t>(heads) * words * pad, static_cast<int64_t>(words) * pad, pad};
 }
@@ -569,9 +547,9 @@ DeltaPrepared prepare(const DeltaSizes& z, int dtype, bool bwd, const void* q, i
                       const void* beta, int64_t beta_ld, char* ws, const DeltaLayout& l, hipStream_t st) {
   const auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(ws + o); };
   DeltaPrepared r{};
-  r.k = rows_of<T>(z, dtype, k, k_st, k_sh, z.Hk, z.dk, at(l.k_t), at(l.k_rows), st);
-  r.q = rows_of<T>(z, dtype, q, q_st, q_sh, z.Hk, z.dk, bwd ? at(l.q_t) : nullptr, at(l.q_rows), st);
-  if (bwd) r.d_o = rows_of<T>(z, dtype, d_o, do_st, do_sh, z.H, z.dv, nullptr, at(l.o_rows), st);
+  r.k = rows_of<T>(z, dtype, k, k_st, k_sh, z.Hk, z.dk, at(l.k_rows), st);
+  r.q = rows_of<T>(z, dtype, q, q_st, q_sh, z.Hk, z.dk, at(l.q_rows), st);
+  if (bwd) r.d_o = rows_of<T>(z, dtype, d_o, do_st, do_sh, z.H, z.dv, at(l.o_rows), st);
   const int64_t units = delta_tiles(z.T, z.S, dtype) * z.H;
   if (z.dk <= 64) launch_prep<T, 64>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, at(l.units), units, st);
   else launch_prep<T, 128>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, at(l.units), units, st);
@@ -591,7 +569,7 @@ void launch_fwd(const DeltaSizes& z, const FwdArgs<T>& A, hipStream_t st) {
 }  // namespace
 
 DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd) {
-  const int64_t C = delta_chunk(dtype), tiles = delta_tiles(z.T, z.S, dtype), units = tiles * z.H;
+  const int64_t tiles = delta_tiles(z.T, z.S, dtype), units = tiles * z.H;
   const int64_t words = delta_words(dtype), dk = delta_pad(z.dk), dv = delta_pad(z.dv);
   const int64_t unit = dtype == DET_BF16 ? (bwd ? Unit<uint16_t, true>::kElems : Unit<uint16_t, false>::kElems)
                                          : (bwd ? Unit<float, true>::kElems : Unit<float, false>::kElems);
@@ -603,8 +581,6 @@ DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd) {
     return r;
   };
   l.units = take(units * unit * 2);
-  l.k_t = take(tiles * z.Hk * C * dk * words * 2);
-  l.q_t = take(bwd ? tiles * z.Hk * C * dk * words * 2 : 0);
   l.k_rows = take(z.T * z.Hk * words * dk * 2);
   l.q_rows = take(z.T * z.Hk * words * dk * 2);
   l.o_rows = take(bwd ? z.T * z.H * words * dv * 2 : 0);
@@ -719,7 +695,6 @@ extern "C" int det_delta_rule(const void* q, int64_t q_st, int64_t q_sh, const v
 #define DET_DELTA_FWD(E)                                                                                            \
   {                                                                                                                 \
     const FwdArgs<E> A{r.k, r.q, {static_cast<const E*>(v), v_st, v_sh}, {static_cast<E*>(o), o_st, o_sh},          \
-                       reinterpret_cast<const uint16_t*>(base + l.k_t),                                         \
                        reinterpret_cast<const uint16_t*>(base + l.units),                                           \
                        initial_state, final_state, states, (int)delta_image_floats(dv, dtype),                      \
                        (int)delta_saved_floats(dk, dv, dtype)};                                                       \

@@ -87,7 +87,8 @@ __device__ __forceinline__ void split(float x, __bf16 (&w)[NP]) {
     if (p + 1 < NP) x -= static_cast<float>(w[p]);
   }
 }
-// The words of two values side by side (one conversion instruction for both).
+// The words of two values side by side (one conversion instruction for both; taking a word from
+// its value with the dot product instruction instead of unpacking it was slower: 572 for 507 us).
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 template <int NP>
@@ -164,16 +165,44 @@ __device__ __forceinline__ void image_put(uint16_t* image, int f, const Frag<NP>
 #pragma unroll
   for (int p = 0; p < NP; ++p) __builtin_memcpy(image + (f * NP + p) * kFragElems + (threadIdx.x & 63) * 8, &v.w[p], 16);
 }
+// Images of rows as they come from a tensor (fetch_rows): lane 16 g + c of a fragment lies at
+// place 16 g + (c ^ 4 g), which keeps the reads of turned_frag on banks of their own.
+__device__ __forceinline__ int row_place() {
+  const int lane = threadIdx.x & 63;
+  return lane ^ (lane >> 4 << 2);
+}
+template <int NP>
+__device__ __forceinline__ Frag<NP> row_frag(const char* image, int f) {
+  Frag<NP> r;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) r.w[p] = *reinterpret_cast<const bf16x8*>(image + (f * NP + p) * 1024 + row_place() * 16);
+  return r;
+}
+// From an image of rows t and places d (KD fragments per tile), the fragment of rows d, tile j,
+// and places t, 32 kt + 8 g ..: the hardware reads 16 columns of four rows, turned, for the lanes
+// of a group; lane p of it gives the address of four columns, 4 (p % 4) .., of row p / 4.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ s16x4 lds_turned4(const char* p) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+}
+template <int KD, int NP>
+__device__ __forceinline__ Frag<NP> turned_frag(const char* image, int j, int kt) {
+  const int lane = threadIdx.x & 63, p = lane & 15, x = 4 * (lane >> 4) + (p >> 2), g = p & 3;
+  const char* at = image + (2 * kt * KD + (j >> 1)) * NP * 1024 + (16 * g + (x ^ (4 * g))) * 16 + 8 * (j & 1);
+  Frag<NP> r;
+#pragma unroll
+  for (int w = 0; w < NP; ++w) {
+    const s16x4 a = lds_turned4(at + w * 1024), b = lds_turned4(at + (KD * NP + w) * 1024);
+    r.w[w] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  return r;
+}
 // The first NP words to LDS.
 template <int NP, int N>
 __device__ __forceinline__ void lds_put(char* image, int f, const Frag<N>& v) {
 #pragma unroll
   for (int p = 0; p < NP; ++p) *reinterpret_cast<bf16x8*>(image + (f * NP + p) * 1024 + (threadIdx.x & 63) * 16) = v.w[p];
-}
-// Where row `row` and place `place` of an operand with KS fragments per row tile lie, in elements (word 0).
-template <int KS, int NP>
-__device__ __forceinline__ int image_at(int row, int place) {
-  return (rho_tile(row) * KS + (place >> 5)) * NP * kFragElems + (16 * ((place >> 3) & 3) + rho_row(row)) * 8 + (place & 7);
 }
 // Square images [C][C] of lower (rows i, places j <= i) or upper (rows j, places i >= j)
 // triangles leave out the fragments that hold nothing else: their numbers.
@@ -341,6 +370,17 @@ __device__ __forceinline__ f32x4 gate4(const float* gate, int C, int row, int at
   return *reinterpret_cast<const f32x4*>(gate + row * C + at);
 }
 
+// A result tile (rows 4 g + r, column c) in 1024 bytes of LDS, and back with rows and columns changed.
+__device__ __forceinline__ f32x4* lds_tile(char* at) { return reinterpret_cast<f32x4*>(at) + (threadIdx.x & 63); }
+__device__ __forceinline__ f32x4 lds_turned(const char* at) {
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const char* p = at + (16 * (c >> 2) + 4 * g) * 16 + (c & 3) * 4;
+  f32x4 v;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] = *reinterpret_cast<const float*>(p + 16 * r);
+  return v;
+}
+
 // A [T, heads, dim] tensor with unit innermost stride.
 template <typename T>
 struct Heads {
@@ -442,7 +482,7 @@ struct Rows {
 template <int RT, int KD, int NP, int NW, int FIRST = 0>
 __device__ __forceinline__ void fetch_rows(uint32_t lds, const Rows& x, int64_t t0, int last, int h, int wave) {
   constexpr int kTile = KD * NP, kGroups = (kTile + 3) / 4;
-  const int c = here_lane(threadIdx.x) & 15;
+  const int c = here_lane(row_place()) & 15;
   wave = here(wave);
   const uint16_t* base = x.from(t0, h) - 2048;  // (the offsets below would be negative)
   static_for<RT * kGroups>([&](auto group) {
@@ -457,6 +497,46 @@ __device__ __forceinline__ void fetch_rows(uint32_t lds, const Rows& x, int64_t 
       fetch_group<n>(lds + (i * kTile + f) * 1024, base, off);
     }
   });
+}
+
+// 16 columns from v0 on of a chunk's rows (RT tiles) in LDS, 2048 bytes of [row][column], for this
+// wave: where `whole_columns`, the rows' strides and starts being whole 16 bytes.
+template <typename T>
+__device__ __forceinline__ bool whole_columns(const Heads<const T>& x, int v0, int dv) {
+  return v0 + 16 <= dv && x.st < (1 << 24) && ((reinterpret_cast<uintptr_t>(x.p) | x.st * sizeof(T) | x.sh * sizeof(T)) & 15) == 0;
+}
+template <int RT, typename T>
+__device__ __forceinline__ void fetch_columns(uint32_t lds, const Heads<const T>& x, int64_t t0, int h, int v0, int last) {
+  constexpr int kLanes = sizeof(T);  // of a row
+  static_assert(16 * RT * 16 * sizeof(T) == 2048, "two loads");
+  const int lane = here_lane(threadIdx.x) & 63;
+  const char* base = reinterpret_cast<const char*>(x.row(t0, h) + v0) - 4096;
+  uint32_t off[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int t = j * (64 / kLanes) + lane / kLanes;
+    off[j] = static_cast<uint32_t>(t < last ? t : last) * static_cast<uint32_t>(x.st * sizeof(T)) + lane % kLanes * 16 + 4096 - 1024 * j;
+  }
+  fetch_group<2>(lds, base, off);
+}
+// The elements of rows rho(i, 4 g + r), column v0 + c, of that.
+template <int RT>
+__device__ __forceinline__ void take_columns(f32x4 (&v)[RT], const char* lds, const float*) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[i][r] = *reinterpret_cast<const float*>(lds + rho(i, r) * 64 + (lane >> 4) * 8 * 64 + (lane & 15) * 4);
+}
+template <int RT>
+__device__ __forceinline__ void take_columns(f32x4 (&v)[RT], const char* lds, const uint16_t*) {
+  const int lane = threadIdx.x & 63, p = lane & 15;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const s16x4 w = lds_turned4(lds + (rho(i, 0) + 8 * (lane >> 4) + (p >> 2)) * 32 + (p & 3) * 8);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[i][r] = to_f32(static_cast<uint16_t>(w[r]));
+  }
 }
 
 // Rows [r0, r1) of segment s and the tiles before it, from the clamped offsets (see
@@ -483,6 +563,26 @@ __device__ __forceinline__ void segment_rows(const int32_t* __restrict__ offs, i
   }
 }
 
+// S = el S + X^T y, from X's rows in LDS (`image`) and the fragments of y, and S's own
+// fragments: in two halves, so that the words of one are made under the products of the other.
+template <int NP, int KC, int DT, int N>
+__device__ __forceinline__ void next_state(f32x4 (&S)[DT], Frag<N> (&f)[DT / 2], const char* image, const Frag<N> (&y)[KC], float el) {
+#pragma unroll
+  for (int i = 0; i < DT; ++i) S[i] *= el;
+  static_for<2>([&](auto half) {
+    constexpr int from = half.value * DT / 2, to = from + DT / 2;
+#pragma unroll
+    for (int kt = 0; kt < KC; ++kt) {
+      Frag<NP> ft[DT];
+#pragma unroll
+      for (int i = from; i < to; ++i) ft[i] = turned_frag<DT / 2, NP>(image, i, kt);
+      mm_tiles<N, from, to>(S, ft, y[kt]);
+    }
+#pragma unroll
+    for (int i = from; i < to; i += 2) f[i / 2] = frag_of<N>(S[i], S[i + 1]);
+  });
+}
+
 // Tokens per chunk, words of an input, words of what only reaches outputs of the
 // input's type. float32 takes half the chunk: its operands have three words.
 template <typename T>
@@ -504,9 +604,9 @@ __device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float
 }
 
 // Rows of C floats that the preparing kernel leaves per (chunk, value head): the running
-// sum G of g in two words, exp(G) and beta (0 behind the sequence's end), exp(G_C - G),
-// and exp(G_C) in every place.
-enum GateRow { kGHi = 0, kGLo = 1, kEG = 2, kRest = 3, kBeta = 4, kEnd = 5, kGateRows = 6 };
+// of g in two words, exp(G) and beta (0 behind the sequence's end), exp(G_C - G),
+// exp(G_C) in every place, and the products exp(G_C - G) beta and -exp(G) beta.
+enum GateRow { kGHi = 0, kGLo = 1, kEG = 2, kRest = 3, kBeta = 4, kEnd = 5, kRestBeta = 6, kEGBeta = 7, kGateRows = 8 };
 
 // What it leaves per (chunk, value head), in fragments of 1024 bytes: the inverse, those rows, P.
 template <typename T, bool BWD>
@@ -550,7 +650,7 @@ inline int64_t delta_saved_floats(int64_t dk, int64_t dv, int dtype) {
 
 // Where the parts of a workspace lie. units: a Unit each; dy: the backward's images as N's.
 struct DeltaLayout {
-  size_t units, k_rows, q_rows, o_rows, k_t, q_t, ds, dy, all;
+  size_t units, k_rows, q_rows, o_rows, ds, dy, all;
 };
 DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd);
 

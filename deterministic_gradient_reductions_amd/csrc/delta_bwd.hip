@@ -10,8 +10,8 @@
 //        and on the chunk's last row sum(K * dK1) + e^G_C <S0, dS1>
 //   dg = the sums of dG from a row to the chunk's end
 //
-// Nothing is divided by beta or by a decay. After the forward's two preparing kernels
-// (with the transposes) one kernel walks a sequence's chunks backwards as the forward's
+// Nothing is divided by beta or by a decay. After the forward's preparing
+// kernels (with the transposes of P and the inverse) one walks a sequence's chunks backwards as the forward's
 // walks them (16 columns of v per wave, dS in registers): it writes dV, every chunk's
 // dS1, and dY as an image, as the forward left N. The last kernel takes all chunks side by
 // side: in it a wave owns tiles of token pairs first, then 16 channels of dQ and dK;
@@ -23,10 +23,10 @@ namespace {
 
 template <typename T>
 struct ChainArgs {
-  Rows k;
+  Rows k, q;
   Heads<const T> d_o;
   Heads<T> dv;
-  const uint16_t *k_t, *q_t, *units;
+  const uint16_t* units;
   const float* ds1;
   float *ds, *ds0;  // every chunk's dS1, the initial state's gradient
   uint16_t* dy;
@@ -34,79 +34,88 @@ struct ChainArgs {
 
 // Workgroups, waves and buffers as in the forward's chain. PAIR: the second wave fetches,
 // forms P^T dO (a chunk ahead) and scale (e^G Q)^T dO for the first one, and dV and dY's image
-// from what that leaves of dU; Q^T goes straight into its registers.
+// from what that leaves of dY.
 template <typename T, int DK, int NW, bool PAIR>
 __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArgs<T> A) {
   typedef Unit<T, true> Rec;
   constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
-  // fragments in LDS: two buffers of K, the inverse, the gates and P, one of K^T and Q^T; PAIR: one of P, none of Q^T, alone (NW 1) two of K^T
-  constexpr int nRows = RT * KD * kIn, nT = DT * KC * kIn, nHead = Rec::oP, nP = Rec::nP, nX = KC * kOut + RT + DT;
   constexpr bool ALONE = PAIR && NW == 1;
-  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nP), oKT = 2 * kBuf, oQT = oKT + nT, oPs = oKT + (ALONE ? 2 : 1) * nT, oX = PAIR ? oPs + nP : oQT + nT;
+  // fragments in LDS: two buffers of K, the inverse and the gates, P and Q (PAIR: one of these two); dO of each wave
+  constexpr int nRows = RT * KD * kIn, nHead = Rec::oP, nP = Rec::nP, nX = 2 * RT + DT;
+  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nP + nRows), oPs = 2 * kBuf, oQ = oPs + nP;
+  constexpr int oO = PAIR ? oQ + nRows : 2 * kBuf, oX = oO + 2 * NW;
   __shared__ __align__(16) char lds[(oX + (PAIR ? NW * nX : 0)) * 1024];
   const int lane = threadIdx.x & 63, wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
   const int wave = PAIR && wave_ >= NW ? wave_ - NW : wave_;
   const int h = blockIdx.x % z.H, hk = h / (z.H / z.Hk), v0 = ((blockIdx.x / z.H) * NW + wave) * 16, s = blockIdx.y;
   const int dvp = z.dv <= 64 ? 64 : 128;
   const uint32_t lds0 = lds_address(lds);
-  char* x = lds + (oX + (PAIR ? wave * nX : 0)) * 1024;  // dU of these columns
-  f32x4 *x_p = reinterpret_cast<f32x4*>(x + KC * kOut * 1024) + lane, *x_q = x_p + RT * 64;  // tiles of P^T dO, of (e^G Q)^T dO
+  char* x = lds + (oX + (PAIR ? wave * nX : 0)) * 1024;  // dY of these columns
+  f32x4 *x_p = lds_tile(x + RT * 1024), *x_q = x_p + RT * 64;  // tiles of P^T dO, of scale (e^G Q)^T dO
   uint32_t r0, r1, first;
   segment_rows(z.offs, s, static_cast<uint32_t>(z.T), kLogC, r0, r1, first);
   const int col = v0 + c, vcol = col < z.dv ? col : z.dv - 1;
   const int chunks = static_cast<int>((r1 - r0 + C - 1) >> kLogC);
   int64_t unit = (static_cast<int64_t>(first) + chunks - 1) * z.H + h;
   int buf = 0;
+  const char* o_tile = lds + (oO + 2 * wave) * 1024;
+  const bool whole = whole_columns(A.d_o, v0, z.dv);
   T rd[RT][4];
   f32x4 dO[RT];
   const auto start = [&](int ch) { return r0 + (static_cast<uint32_t>(ch) << kLogC); };
   const auto rows_at = [&](int ch) { return r1 - start(ch) < static_cast<uint32_t>(C) ? static_cast<int>(r1 - start(ch)) : C; };
-  const auto load_do = [&](int ch) { load_column<RT>(rd, A.d_o.row(start(ch), h), A.d_o.st, vcol, rows_at(ch) - 1); };
+  const auto next_do = [&](int ch) {
+    lds_read();  // (the last one's)
+    if (whole) fetch_columns<RT>(lds0 + (oO + 2 * wave) * 1024, A.d_o, start(ch), h, v0, rows_at(ch) - 1);
+    else load_column<RT>(rd, A.d_o.row(start(ch), h), A.d_o.st, vcol, rows_at(ch) - 1);
+  };
   const auto take_do = [&] {
+    if (whole) {
+      take_columns<RT>(dO, o_tile, static_cast<const T*>(nullptr));
+    } else {
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+      for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) dO[i][r] = to_f32(rd[i][r]);
+        for (int r = 0; r < 4; ++r) dO[i][r] = to_f32(rd[i][r]);
+    }
   };
   const auto fetch_p = [&](uint32_t to, int64_t unit) {
     fetch_image<nP, NW, 5>(to, A.units + unit * Rec::kElems + Rec::oP * kFragElems, wave);
   };
+  const auto fetch_q = [&](uint32_t to, int ch) { fetch_rows<RT, KD, kIn, NW, 4>(to, A.q, start(ch), rows_at(ch) - 1, hk, wave); };
   const auto fetch_next = [&](int ch, int64_t unit, int buf) {
     const uint32_t to = lds0 + buf * kBuf * 1024;
     fetch_rows<RT, KD, kIn, NW>(to, A.k, start(ch), rows_at(ch) - 1, hk, wave);
     fetch_image<nHead, NW, 4>(to + nRows * 1024, A.units + unit * Rec::kElems, wave);
-    if (!PAIR) fetch_p(to + (nRows + nHead) * 1024, unit);
-  };
-  const auto fetch_t = [&](int at, const uint16_t* image, int64_t unit) {
-    fetch_image<nT, NW>(lds0 + at * 1024, image + (unit / z.H * z.Hk + hk) * (nT * kFragElems), wave);
+    if (!PAIR) {
+      fetch_p(to + (nRows + nHead) * 1024, unit);
+      fetch_q(to + (nRows + nHead + nP) * 1024, ch);
+    }
   };
   // dU += P^T dO
   const auto add_p = [&](f32x4 (&dU)[RT], const char* img) {
     static_for<KC>([&](auto kt) {
       constexpr int to = 2 * kt.value + 2;
-      const Frag<kIn> f = frag_of<kIn>(dO[2 * kt.value], dO[2 * kt.value + 1]);
+      const Frag<kIn> fo = frag_of<kIn>(dO[2 * kt.value], dO[2 * kt.value + 1]);
       Frag<kW> fp[RT];
 #pragma unroll
       for (int j = 0; j < to; ++j) fp[j] = lds_frag<kW, kW>(img, upper_frag<KC>(j, kt.value));
-      mm_tiles<kW, 0, to>(dU, fp, f);
+      mm_tiles<kW, 0, to>(dU, fp, fo);
     });
   };
-  // S += Q^T or K^T (at(i KC + kt): the fragment of tile i, places 32 kt ..) times y
-  const auto add_t = [&](f32x4 (&S)[DT], const auto& at, const f32x4 (&y)[RT]) {
-#pragma unroll
-    for (int kt = 0; kt < KC; ++kt) {
-      const Frag<kW> f = frag_of<kW>(y[2 * kt], y[2 * kt + 1]);
-      Frag<kIn> ft[DT];
-#pragma unroll
-      for (int i = 0; i < DT; ++i) ft[i] = at(i * KC + kt);
-      mm_tiles<kW, 0, DT>(S, ft, f);
-    }
-  };
-  const auto lds_t = [&](int at) { return [&, at](int i) { return lds_frag<kIn, kIn>(lds + at * 1024, i); }; };
-  const auto scale_do = [&](const float* gate) {
+  // S += scale (e^G Q)^T dO
+  const auto add_q = [&](f32x4 (&S)[DT], const char* img, const float* gate) {
 #pragma unroll
     for (int i = 0; i < RT; ++i) dO[i] *= gate4(gate, C, kEG, rho(i, 4 * lg)) * z.scale;
+#pragma unroll
+    for (int kt = 0; kt < KC; ++kt) {
+      const Frag<kW> fo = frag_of<kW>(dO[2 * kt], dO[2 * kt + 1]);
+      Frag<kIn> ft[DT];
+#pragma unroll
+      for (int i = 0; i < DT; ++i) ft[i] = turned_frag<KD, kIn>(img, i, kt);
+      mm_tiles<kW, 0, DT>(S, ft, fo);
+    }
   };
   // dV, and dY's image, from dY with rows v and columns t
   const auto put_y = [&](const f32x4 (&yt)[RT], const float* gate, int ch, int64_t unit) {
@@ -118,18 +127,11 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
   };
 
   if (PAIR && wave_ >= NW) {
-    Frag<kIn> qt[DT * KC];
-    const auto load_qt = [&](int64_t unit) {
-      const uint16_t* image = A.q_t + (unit / z.H * z.Hk + hk) * (nT * kFragElems);
-#pragma unroll
-      for (int i = 0; i < DT * KC; ++i) qt[i] = image_frag<kIn, kIn>(image, i);
-    };
     if (chunks) {
-      load_do(chunks - 1);
-      load_qt(unit);
+      next_do(chunks - 1);
       fetch_next(chunks - 1, unit, 0);
       fetch_p(lds0 + oPs * 1024, unit);
-      take_do();
+      fetch_q(lds0 + oQ * 1024, chunks - 1);
     }
     fetch_done();
     __syncthreads();
@@ -139,41 +141,39 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
 #pragma unroll
       for (int i = 0; i < RT; ++i) x_p[i * 64] = w[i];
     };
-    if (chunks) give_p();
+    if (chunks) {
+      take_do();
+      give_p();
+    }
     for (int ch = chunks - 1; ch >= 0; --ch, unit -= z.H, buf ^= 1) {
+      lds_read();
       __syncthreads();  // P^T dO and this chunk's fragments are there, the last one's have been read
       const char* img = lds + buf * kBuf * 1024;
       const float* gate = reinterpret_cast<const float*>(img + (nRows + Rec::oGate) * 1024);
-      if (!ALONE) fetch_t(oKT, A.k_t, unit);
-      if (ch > 0) fetch_p(lds0 + oPs * 1024, unit - z.H);
-      {
-        scale_do(gate);
-        f32x4 w[DT] = {};
-        add_t(w, [&](int i) { return qt[i]; }, dO);
-#pragma unroll
-        for (int i = 0; i < DT; ++i) x_q[i * 64] = w[i];
-      }
       if (ch > 0) {
-        load_do(ch - 1);
-        load_qt(unit - z.H);
+        fetch_p(lds0 + oPs * 1024, unit - z.H);
+        next_do(ch - 1);
         fetch_next(ch - 1, unit - z.H, buf ^ 1);
       }
-      // K^T's and P's; alone this wave needs them only after the barrier
+      {
+        f32x4 w[DT] = {};
+        add_q(w, lds + oQ * 1024, gate);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) x_q[i * 64] = w[i];
+        lds_read();
+      }
+      // P's and dO's; alone this wave needs them only after the barrier
       const auto done_now = [&] {
         if (ch > 0) fetch_done_but<fetched(KD * kIn, NW, 0, RT) + fetched(nHead, NW, 4)>();
         else fetch_done();
       };
       if (!ALONE) done_now();
-      __syncthreads();  // dU is there, and what this wave has left
+      __syncthreads();  // dY is there, and what this wave has left; Q has been read
       if (ALONE) done_now();
-      f32x4 yt[RT] = {};
-      static_for<KC>([&](auto kt) {
-        constexpr int to = 2 * kt.value + 2;
-        Frag<kOut> fi[RT];
+      if (ch > 0) fetch_q(lds0 + oQ * 1024, ch - 1);
+      f32x4 yt[RT];
 #pragma unroll
-        for (int j = 0; j < to; ++j) fi[j] = lds_frag<kOut, kW>(img + nRows * 1024, upper_frag<KC>(j, kt.value));
-        mm_tiles<kOut, 0, to, true>(yt, fi, lds_frag<kOut, kOut>(x, kt.value));
-      });
+      for (int i = 0; i < RT; ++i) yt[i] = lds_turned(x + i * 1024);
       if (ch > 0) {
         take_do();
         give_p();
@@ -194,29 +194,23 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[i][r] = rho(i, 4 * lg + r) < z.dk ? y[i][r] : 0.0f;
   }
+  Frag<kW> f[KD];  // of S
+#pragma unroll
+  for (int ks = 0; ks < KD; ++ks) f[ks] = frag_of<kW>(S[2 * ks], S[2 * ks + 1]);
   if (PAIR) {
-    if (ALONE && chunks) fetch_t(oKT, A.k_t, unit);
-    if (ALONE) fetch_done();
     __syncthreads();
   } else {
     if (chunks) {
-      load_do(chunks - 1);
+      next_do(chunks - 1);
       fetch_next(chunks - 1, unit, 0);
     }
     fetch_done();
   }
   for (int ch = chunks - 1; ch >= 0; --ch, unit -= z.H, buf ^= 1) {
-    if (!PAIR) take_do();
     __syncthreads();  // this chunk's fragments are there, the last one's have been read
     if (!PAIR) {
-      fetch_t(oKT, A.k_t, unit);
-      fetch_t(oQT, A.q_t, unit);
-      if (ch > 0) {
-        load_do(ch - 1);
-        fetch_next(ch - 1, unit - z.H, buf ^ 1);
-      }
-    } else if (ALONE && ch > 0) {
-      fetch_t(oKT + (buf ^ 1) * nT, A.k_t, unit - z.H);
+      if (ch > 0) fetch_next(ch - 1, unit - z.H, buf ^ 1);
+      take_do();
     }
     store_state<DT>(S, A.ds + unit * size, z.dk, z.dv, col);
     const char* img = lds + buf * kBuf * 1024;
@@ -224,11 +218,10 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
     f32x4 dU[RT] = {};
 #pragma unroll
     for (int ks = 0; ks < KD; ++ks) {
-      const Frag<kW> f = frag_of<kW>(S[2 * ks], S[2 * ks + 1]);
       Frag<kIn> fk[RT];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) fk[i] = lds_frag<kIn, kIn>(img, i * KD + ks);
-      mm_tiles<kW, 0, RT>(dU, fk, f);
+      for (int i = 0; i < RT; ++i) fk[i] = row_frag<kIn>(img, i * KD + ks);
+      mm_tiles<kW, 0, RT>(dU, fk, f[ks]);
     }
 #pragma unroll
     for (int i = 0; i < RT; ++i) dU[i] *= gate4(gate, C, kRest, rho(i, 4 * lg));
@@ -237,37 +230,41 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
       for (int i = 0; i < RT; ++i) dU[i] += x_p[i * 64];
     } else {
       add_p(dU, img + (nRows + nHead) * 1024);
+      if (ch > 0) next_do(ch - 1);
     }
     f32x4 dN[RT] = {}, yt[RT] = {};  // dY, and dY with rows v and columns t
     static_for<KC>([&](auto kt) {
       constexpr int to = 2 * kt.value + 2;
-      const Frag<kW> f = frag_of<kW>(dU[2 * kt.value], dU[2 * kt.value + 1]);
-      if (PAIR) lds_put<kOut>(x, kt.value, f);
+      const Frag<kW> fu = frag_of<kW>(dU[2 * kt.value], dU[2 * kt.value + 1]);
       Frag<kW> fi[RT];
 #pragma unroll
       for (int j = 0; j < to; ++j) fi[j] = lds_frag<kW, kW>(img + nRows * 1024, upper_frag<KC>(j, kt.value));
-      mm_tiles<kW, 0, to>(dN, fi, f);
-      if (!PAIR) mm_tiles<kOut, 0, to, true>(yt, fi, f);
+      mm_tiles<kW, 0, to>(dN, fi, fu);
+      if (!PAIR) mm_tiles<kOut, 0, to, true>(yt, fi, fu);
     });
-    if (!PAIR) {
-      put_y(yt, gate, ch, unit);
-      scale_do(gate);
-    }
     const float el = gate[kEnd * C];
+    if (PAIR) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) *lds_tile(x + i * 1024) = dN[i];
+    } else {
+      put_y(yt, gate, ch, unit);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) dN[i] *= gate4(gate, C, kEGBeta, rho(i, 4 * lg));
+    Frag<kW> fn[KC];
+#pragma unroll
+    for (int kt = 0; kt < KC; ++kt) fn[kt] = frag_of<kW>(dN[2 * kt], dN[2 * kt + 1]);
 #pragma unroll
     for (int i = 0; i < DT; ++i) S[i] *= el;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) dN[i] *= -gate4(gate, C, kEG, rho(i, 4 * lg)) * gate4(gate, C, kBeta, rho(i, 4 * lg));
-    if (!PAIR) fetch_done();
-    __syncthreads();  // K^T and Q^T are there (PAIR: K^T, Q^T dO), and the next chunk's fragments
     if (PAIR) {
+      __syncthreads();  // the second wave's part of dS is there
 #pragma unroll
       for (int i = 0; i < DT; ++i) S[i] += x_q[i * 64];
     } else {
-      add_t(S, lds_t(oQT), dO);
+      add_q(S, img + (nRows + nHead + nP) * 1024, gate);
     }
-    add_t(S, lds_t(oKT + (ALONE ? buf * nT : 0)), dN);
-    if (ALONE) fetch_done();
+    next_state<kIn, KC>(S, f, img, fn, 1.0f);
+    if (!PAIR) fetch_done();
   }
   if (A.ds0) store_state<DT>(S, A.ds0 + of, z.dk, z.dv, col);
 }
@@ -277,7 +274,7 @@ struct GradArgs {
   Rows k, q, d_o;
   Heads<T> dq, dk;
   T *dg, *dbeta;
-  const uint16_t *k_t, *q_t, *dy, *units;
+  const uint16_t *dy, *units;
   const float *g, *saved, *ds;
   int64_t g_ld, dg_ld, dbeta_ld;
   int image_floats, saved_floats;
@@ -303,7 +300,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
   // 1024-byte fragments of the images
   constexpr int nK = RT * KD * kIn, nO = RT * KV * kIn, nV = RT * KV * kW, nTri = kFrags * kW, nSq = RT * KC * kW,
                 nGate = Unit<T, true>::nGate;
-  constexpr int oO = nK, oN = oO + nO, oY = oN + nV, oA = oY + nV, oB = oA + nTri, oZ = oB + nTri, oGate = oZ + nSq;
+  constexpr int oQ = nK, oO = 2 * nK, oN = oO + nO, oY = oN + nV, oA = oY + nV, oB = oA + nTri, oZ = oB + nTri, oGate = oZ + nSq;
   __shared__ __align__(16) char lds[(oGate + nGate) * 1024];
   __shared__ float red_q[NW][C], red_s[NW], red_w[NW], diag[C];
   __shared__ float row_e[RT][RT][16], col_e[RT][RT][16];
@@ -318,6 +315,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
   if (!segment_tile<1>(z.offs, z.S, static_cast<uint32_t>(z.T), kLogC, tile, e, t0, t1, s0, s1)) return;
   const int size = z.dk * z.dv;
   fetch_rows<RT, KD, kIn, NW>(lds0, A.k, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
+  fetch_rows<RT, KD, kIn, NW, 4>(lds0 + oQ * 1024, A.q, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
   f32x4 dq[RT] = {}, dk[RT] = {};  // rows d, columns t
 
   for (int h = hk * group; h < (hk + 1) * group; ++h) {
@@ -370,20 +368,17 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
       pair_of(p, i, j);
       f32x4 qk{}, kk{}, x{}, y{};
       const int row = rho(i, c), at0 = rho(j, 4 * lg);
-      Frag<kIn> fq[KD];
-#pragma unroll
-      for (int ks = 0; ks < KD; ++ks) fq[ks] = A.q.template frag<kIn>(A.q.from(t0, hk), A.q.lane_off(row < n ? row : n - 1), ks);
 #pragma unroll
       for (int kv = 0; kv < KV; ++kv) {
         const Frag<kW> f = lds_frag<kW, kW>(lds + oN * 1024, j * KV + kv);
         mm<kW>(x, f, lds_frag<kW, kW>(lds + oY * 1024, i * KV + kv));
-        mm<kW>(y, f, lds_frag<kIn, kIn>(lds + oO * 1024, i * KV + kv));
+        mm<kW>(y, f, row_frag<kIn>(lds + oO * 1024, i * KV + kv));
       }
 #pragma unroll
       for (int ks = 0; ks < KD; ++ks) {
-        const Frag<kIn> kj = lds_frag<kIn, kIn>(lds, j * KD + ks);
-        mm<kIn>(kk, kj, lds_frag<kIn, kIn>(lds, i * KD + ks));
-        mm<kIn>(qk, kj, fq[ks]);
+        const Frag<kIn> kj = row_frag<kIn>(lds, j * KD + ks);
+        mm<kIn>(kk, kj, row_frag<kIn>(lds, i * KD + ks));
+        mm<kIn>(qk, kj, row_frag<kIn>(lds + oQ * 1024, i * KD + ks));
       }
       const f32x4 b = gate4(gate, C, kBeta, at0), hj = gate4(gate, C, kGHi, at0), lj = gate4(gate, C, kGLo, at0);
       const float hi = gate[kGHi * C + row], li = gate[kGLo * C + row], bi = gate[kBeta * C + row];
@@ -434,21 +429,6 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
 
     // 16 channels of dq and dk
     if (wave < DT) {
-      Frag<kIn> kT[KC], qT[KC];
-      const int64_t at = (static_cast<int64_t>(tile) * z.Hk + hk) * (C * DK * kIn);
-#pragma unroll
-      for (int kt = 0; kt < KC; ++kt) {
-        kT[kt] = image_frag<kIn, kIn>(A.k_t + at, wave * KC + kt);
-        qT[kt] = image_frag<kIn, kIn>(A.q_t + at, wave * KC + kt);
-      }
-      bf16x4 wq[RT][kIn];  // four channels of Q of a token
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const int x = rho(i, c);
-        const uint32_t off = A.q.lane_off(x < n ? x : n - 1);
-#pragma unroll
-        for (int u = 0; u < kIn; ++u) wq[i][u] = load_at<bf16x4>(A.q.from(t0, hk) + u * A.q.words_at + rho(wave, 0), off);
-      }
       f32x4 a[RT] = {}, b[RT] = {}, s[RT] = {};
       float inner = 0.0f, w_sum = 0.0f;
 #pragma unroll
@@ -471,7 +451,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
         for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(lds + oN * 1024, i * KV + kv);
         mm_tiles<kW, 0, RT, true>(s, f, fd);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) fo[i] = lds_frag<kIn, kIn>(lds + oO * 1024, i * KV + kv);
+        for (int i = 0; i < RT; ++i) fo[i] = row_frag<kIn>(lds + oO * 1024, i * KV + kv);
         mm_tiles<kW, 0, RT, true>(a, fo, fs);
         step();
       }
@@ -485,10 +465,11 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
         f32x4 q{}, k{};
 #pragma unroll
         for (int u = kIn - 1; u >= 0; --u) {
-          const bf16x4 wk = *reinterpret_cast<const bf16x4*>(lds + ((i * KD + (wave >> 1)) * kIn + u) * 1024 + (16 * lg + c) * 16 + (wave & 1) * 8);
+          const char* row = lds + ((i * KD + (wave >> 1)) * kIn + u) * 1024 + row_place() * 16 + (wave & 1) * 8;
+          const bf16x4 wk = *reinterpret_cast<const bf16x4*>(row), wq = *reinterpret_cast<const bf16x4*>(row + oQ * 1024);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            q[r] += static_cast<float>(wq[i][u][r]);
+            q[r] += static_cast<float>(wq[r]);
             k[r] += static_cast<float>(wk[r]);
           }
         }
@@ -514,16 +495,17 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
       }
       static_for<KC>([&](auto kt) {
         constexpr int at = kt.value;
+        const Frag<kIn> kT = turned_frag<KD, kIn>(lds, wave, at), qT = turned_frag<KD, kIn>(lds + oQ * 1024, wave, at);
         Frag<kW> f[RT];
 #pragma unroll
         for (int i = 2 * at; i < RT; ++i) f[i] = lds_frag<kW, kW>(img_a, lower_frag(i, at));
-        mm_tiles<kW, 2 * at, RT, true>(dq, f, kT[at]);
+        mm_tiles<kW, 2 * at, RT, true>(dq, f, kT);
 #pragma unroll
         for (int i = 0; i < 2 * at + 2; ++i) f[i] = lds_frag<kW, kW>(img_b, upper_frag<KC>(i, at));
-        mm_tiles<kW, 0, 2 * at + 2, true>(dk, f, qT[at]);
+        mm_tiles<kW, 0, 2 * at + 2, true>(dk, f, qT);
 #pragma unroll
         for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(img_z, i * KC + at);
-        mm_tiles<kW, 0, RT, true>(dk, f, kT[at]);
+        mm_tiles<kW, 0, RT, true>(dk, f, kT);
         step();
       });
     }
@@ -655,11 +637,12 @@ extern "C" int det_delta_rule_bwd(const void* d_o, int64_t do_st, int64_t do_sh,
   const int image = static_cast<int>(delta_image_floats(dv, dtype)), saved = static_cast<int>(delta_saved_floats(dk, dv, dtype));
 #define DET_DELTA_BWD(E)                                                                                               \
   {                                                                                                                    \
-    const ChainArgs<E> A{r.k, {static_cast<const E*>(d_o), do_st, do_sh}, {static_cast<E*>(dv_out), dv_st, dv_sh},     \
-                         words(l.k_t), words(l.q_t), words(l.units), dfinal_state, ds, dinitial_state, words(l.dy)};   \
+    const ChainArgs<E> A{r.k, r.q, {static_cast<const E*>(d_o), do_st, do_sh},                                         \
+                         {static_cast<E*>(dv_out), dv_st, dv_sh}, words(l.units), dfinal_state, ds, dinitial_state,    \
+                         words(l.dy)};                                                                                 \
     const GradArgs<E> B{r.k, r.q, r.d_o, {static_cast<E*>(dq), dq_st, dq_sh},                                          \
                         {static_cast<E*>(dk_out), dk_st, dk_sh}, static_cast<E*>(dg), static_cast<E*>(dbeta),          \
-                        words(l.k_t), words(l.q_t), words(l.dy), words(l.units), g, states, ds, g_ld, dg_ld, dbeta_ld,  \
+                        words(l.dy), words(l.units), g, states, ds, g_ld, dg_ld, dbeta_ld,  \
                         image, saved};                                                                                 \
     if (dk <= 64) launch_chain<E, 64>(z, A, st);                                                                       \
     else launch_chain<E, 128>(z, A, st);                                                                               \
