@@ -306,9 +306,9 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
   constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
   constexpr bool ALONE = PAIR && NW == 1;
-  // fragments in LDS: two buffers of K, the inverse and the gates, Q and P (PAIR: one of these two); V of each wave
+  // fragments in LDS: two buffers of K, the inverse and the gates, Q and P (PAIR: one of these two); V of each wave (PAIR: two)
   constexpr int nRows = RT * KD * kIn, nHead = Rec::oP, nP = Rec::nP, nX = KD * kOut + RT;
-  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nRows + nP), oQ = 2 * kBuf, oV = oQ + (PAIR ? nRows + nP : 0), oX = oV + 2 * NW;
+  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nRows + nP), oQ = 2 * kBuf, oV = oQ + (PAIR ? nRows + nP : 0), oX = oV + (PAIR ? 4 : 2) * NW;
   __shared__ __align__(16) char lds[(oX + (PAIR ? NW * nX : 0)) * 1024];
   const int lane = threadIdx.x & 63, wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
   const int wave = PAIR && wave_ >= NW ? wave_ - NW : wave_;
@@ -320,6 +320,8 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
   int64_t unit = static_cast<int64_t>(first) * z.H + h;
   int buf = 0;
 
+  const bool whole = whole_columns(A.v, v0, z.dv);
+  const auto v_tile = [&](int buf) { return (oV + 2 * (PAIR ? 2 * wave + buf : wave)) * 1024; };
   const auto rows_at = [&](uint32_t t0) { return r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C; };
   const auto fetch_next = [&](uint32_t t0, int64_t unit, int buf) {
     const uint32_t to = lds0 + buf * kBuf * 1024;
@@ -363,12 +365,21 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
         put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + (unit - z.H) * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
       store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
     };
-    if (r0 < r1) fetch_next(r0, unit, 0);
+    const auto fetch_v = [&](uint32_t t0, int buf) {
+      if (whole) fetch_columns<RT>(lds0 + v_tile(buf), A.v, t0, h, v0, rows_at(t0) - 1);
+    };
+    if (r0 < r1) {
+      fetch_next(r0, unit, 0);
+      fetch_v(r0, 0);
+    }
     fetch_done();
     for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
       __syncthreads();  // this chunk's fragments are there, the last one's have been read
       const bool more = t0 + C < r1;
-      if (more) fetch_next(t0 + C, unit + z.H, buf ^ 1);
+      if (more) {
+        fetch_next(t0 + C, unit + z.H, buf ^ 1);
+        fetch_v(t0 + C, buf ^ 1);
+      }
       // the last chunk's Q and P, fetched before those
       if (more) fetch_done_but<fetched(KD * kIn, NW, 0, RT) + fetched(nHead, NW, 4)>();
       else fetch_done();
@@ -418,33 +429,37 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
   Frag<kW> f[KD];  // of S
 #pragma unroll
   for (int ks = 0; ks < KD; ++ks) f[ks] = frag_of<kW>(S[2 * ks], S[2 * ks + 1]);
-  char* v_tile = lds + (oV + 2 * wave) * 1024;
-  const bool whole = whole_columns(A.v, v0, z.dv);
   T rv[RT][4];
   const auto next_v = [&](uint32_t t0) {
-    lds_read();  // (the last one's)
-    if (whole) fetch_columns<RT>(lds0 + (oV + 2 * wave) * 1024, A.v, t0, h, v0, rows_at(t0) - 1);
-    else load_column<RT>(rv, A.v.row(t0, h), A.v.st, vcol, rows_at(t0) - 1);
+    if (!whole) {
+      load_column<RT>(rv, A.v.row(t0, h), A.v.st, vcol, rows_at(t0) - 1);
+    } else if (!PAIR) {
+      lds_read();  // (the last one's)
+      fetch_columns<RT>(lds0 + v_tile(0), A.v, t0, h, v0, rows_at(t0) - 1);
+    }
   };
   if (r0 < r1) {
     next_v(r0);
     if (!PAIR) fetch_next(r0, unit, 0);
   }
-  fetch_done();
+  if (!PAIR) fetch_done();
   for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
     __syncthreads();  // this chunk's fragments are there, the last one's have been read
     if (!PAIR && t0 + C < r1) fetch_next(t0 + C, unit + z.H, buf ^ 1);
-    if (A.saved) store_state<DT>(S, A.saved + unit * A.saved_floats + A.image_floats, z.dk, z.dv, col);
     const char* img = lds + buf * kBuf * 1024;
     const float* gate = reinterpret_cast<const float*>(img + (nRows + Rec::oGate) * 1024);
     f32x4 R[RT];
     if (whole) {
-      take_columns<RT>(R, v_tile, static_cast<const T*>(nullptr));
+      take_columns<RT>(R, lds + v_tile(buf), static_cast<const T*>(nullptr));
     } else {
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) R[i][r] = to_f32(rv[i][r]);
+    }
+    if (A.saved && v0 < z.dv) {
+      lds_read();
+      store_block<DT>(S, A.saved + unit * A.saved_floats + A.image_floats + v0 * z.dk, z.dk, PAIR ? x + KD * kOut * 1024 : lds + v_tile(0));
     }
 
     // K S0 (rows t, columns v) and its transposed Q S0 (rows v, columns t)
@@ -506,7 +521,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
 #pragma unroll
     for (int kt = 0; kt < KC; ++kt) fu[kt] = frag_of<kW>(U[2 * kt], U[2 * kt + 1]);
     next_state<kIn, KC>(S, f, img, fu, el);
-    fetch_done();
+    if (!PAIR) fetch_done();
   }
   if (PAIR) __syncthreads();
   if (A.s1) store_state<DT>(S, A.s1 + of, z.dk, z.dv, col);
@@ -584,7 +599,7 @@ DeltaLayout delta_layout(const DeltaSizes& z, int dtype, bool bwd) {
   l.k_rows = take(z.T * z.Hk * words * dk * 2);
   l.q_rows = take(z.T * z.Hk * words * dk * 2);
   l.o_rows = take(bwd ? z.T * z.H * words * dv * 2 : 0);
-  l.ds = take(bwd ? units * z.dk * z.dv * 4 : 0);
+  l.ds = take(bwd ? units * delta_block_floats(z.dk, z.dv) * 4 : 0);
   l.dy = take(bwd ? units * delta_image_floats(z.dv, dtype) * 4 : 0);
   l.all = at;
   return l;

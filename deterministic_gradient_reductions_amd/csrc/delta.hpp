@@ -456,6 +456,22 @@ __device__ __forceinline__ void store_state(const f32x4 (&v)[DT], float* state, 
   }
 }
 
+// The same for a state between kernels: [dv / 16][dk][16], of which a wave's columns are one block, so that
+// it is stored in whole lines; turned in 2048 bytes of LDS (32 stores of 4 bytes took most of a chunk).
+template <int DT>
+__device__ __forceinline__ void store_block(const f32x4 (&v)[DT], float* block, int dk, char* scratch) {
+  const int lane = here_lane(threadIdx.x) & 63, c = lane & 15;
+#pragma unroll
+  for (int i = 0; i < DT; ++i) {
+    char* tile = scratch + (i & 1) * 1024;
+    *lds_tile(tile) = v[i];
+    wave_fence();
+    const f32x4 w = lds_turned(tile);
+    wave_fence();
+    if (rho(i, c) < dk) *reinterpret_cast<f32x4*>(block + rho(i, c) * 16 + 4 * (lane >> 4)) = w;
+  }
+}
+
 // The rows of a [T, heads, dim] operand in bf16 words: a bf16 tensor itself where its
 // rows start on 16-byte borders and dim is the kernels' own, else a copy [T, heads, words, dim]
 // padded with zeros.
@@ -578,8 +594,20 @@ __device__ __forceinline__ void next_state(f32x4 (&S)[DT], Frag<N> (&f)[DT / 2],
       for (int i = from; i < to; ++i) ft[i] = turned_frag<DT / 2, NP>(image, i, kt);
       mm_tiles<N, from, to>(S, ft, y[kt]);
     }
+    if constexpr (half.value == 0) {
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
 #pragma unroll
-    for (int i = from; i < to; i += 2) f[i / 2] = frag_of<N>(S[i], S[i + 1]);
+      for (int i = 0; i < from; i += 2) f[i / 2] = frag_of<N>(S[i], S[i + 1]);
+      // an instruction of the matrix cores, then four others, in turn
+      static_for<KC * DT / 2 * N * (N + 1) / 2>([](auto) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = from; i < to; i += 2) f[i / 2] = frag_of<N>(S[i], S[i + 1]);
+    }
   });
 }
 
@@ -639,14 +667,13 @@ inline int delta_chain_waves(const DeltaSizes& z) {
 }
 
 // What a forward leaves for the backward per (chunk, value head): N as an image of rows t and
-// places v in kOut words, then the state in front of the chunk, in floats.
+// places v in kOut words, then the state in front of the chunk in blocks of 16 columns, in floats.
 inline int64_t delta_image_floats(int64_t dv, int dtype) {
   const int64_t words = dtype == DET_BF16 ? DeltaType<uint16_t>::kOut : DeltaType<float>::kOut;
   return delta_chunk(dtype) * delta_pad(dv) * words / 2;
 }
-inline int64_t delta_saved_floats(int64_t dk, int64_t dv, int dtype) {
-  return delta_image_floats(dv, dtype) + static_cast<int64_t>(align_up(static_cast<size_t>(dk * dv), 4));
-}
+inline int64_t delta_block_floats(int64_t dk, int64_t dv) { return dk * static_cast<int64_t>(align_up(static_cast<size_t>(dv), 16)); }
+inline int64_t delta_saved_floats(int64_t dk, int64_t dv, int dtype) { return delta_image_floats(dv, dtype) + delta_block_floats(dk, dv); }
 
 // Where the parts of a workspace lie. units: a Unit each; dy: the backward's images as N's.
 struct DeltaLayout {

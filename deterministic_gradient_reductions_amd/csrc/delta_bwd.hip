@@ -28,8 +28,9 @@ struct ChainArgs {
   Heads<T> dv;
   const uint16_t* units;
   const float* ds1;
-  float *ds, *ds0;  // every chunk's dS1, the initial state's gradient
+  float *ds, *ds0;  // every chunk's dS1 in blocks, the initial state's gradient
   uint16_t* dy;
+  int ds_floats;
 };
 
 // Workgroups, waves and buffers as in the forward's chain. PAIR: the second wave fetches,
@@ -59,7 +60,7 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
   const int chunks = static_cast<int>((r1 - r0 + C - 1) >> kLogC);
   int64_t unit = (static_cast<int64_t>(first) + chunks - 1) * z.H + h;
   int buf = 0;
-  const char* o_tile = lds + (oO + 2 * wave) * 1024;
+  char* o_tile = lds + (oO + 2 * wave) * 1024;
   const bool whole = whole_columns(A.d_o, v0, z.dv);
   T rd[RT][4];
   f32x4 dO[RT];
@@ -212,7 +213,10 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
       if (ch > 0) fetch_next(ch - 1, unit - z.H, buf ^ 1);
       take_do();
     }
-    store_state<DT>(S, A.ds + unit * size, z.dk, z.dv, col);
+    if (v0 < z.dv) {
+      if (!PAIR) lds_read();
+      store_block<DT>(S, A.ds + unit * A.ds_floats + v0 * z.dk, z.dk, PAIR ? x : o_tile);
+    }
     const char* img = lds + buf * kBuf * 1024;
     const float* gate = reinterpret_cast<const float*>(img + (nRows + Rec::oGate) * 1024);
     f32x4 dU[RT] = {};
@@ -277,7 +281,7 @@ struct GradArgs {
   const uint16_t *dy, *units;
   const float *g, *saved, *ds;
   int64_t g_ld, dg_ld, dbeta_ld;
-  int image_floats, saved_floats;
+  int image_floats, saved_floats, ds_floats;
 };
 
 // No instruction is moved over this: what a step loads is not loaded steps before, in
@@ -313,7 +317,6 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
   int e;
   uint32_t t0, t1, s0, s1;
   if (!segment_tile<1>(z.offs, z.S, static_cast<uint32_t>(z.T), kLogC, tile, e, t0, t1, s0, s1)) return;
-  const int size = z.dk * z.dv;
   fetch_rows<RT, KD, kIn, NW>(lds0, A.k, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
   fetch_rows<RT, KD, kIn, NW, 4>(lds0 + oQ * 1024, A.q, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
   f32x4 dq[RT] = {}, dk[RT] = {};  // rows d, columns t
@@ -322,7 +325,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
     const int wave = here(wave_), lane = here_lane(threadIdx.x) & 63, c = lane & 15, lg = lane >> 4;
     const int n = here(static_cast<int>(t1 - t0));
     const int64_t unit = static_cast<int64_t>(tile) * z.H + h;
-    const float *saved = A.saved + unit * A.saved_floats, *ps = saved + A.image_floats, *pd = A.ds + unit * size;
+    const float *saved = A.saved + unit * A.saved_floats, *ps = saved + A.image_floats, *pd = A.ds + unit * A.ds_floats;
     __syncthreads();  // the last head's images and sums have been read
     fetch_image<nV, NW>(lds0 + oN * 1024, reinterpret_cast<const uint16_t*>(saved), wave);
     fetch_image<nV, NW, nV / 4>(lds0 + oY * 1024, A.dy + unit * (nV * kFragElems), wave);
@@ -332,28 +335,16 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
     const int d = rho(wave, c);
     f32x4 xs[KV][2], xd[KV][2];
     if (wave < DT) {
-      const uint32_t off = static_cast<uint32_t>((d < z.dk ? d : 0) * z.dv) * 4u;
-      if (z.dv == DV) {
+      // (every load stays in its block; what lies behind dk or dv is masked below)
 #pragma unroll
-        for (int kv = 0; kv < KV; ++kv)
+      for (int kv = 0; kv < KV; ++kv) {
+        const int block = 2 * kv + (lg >> 1);
+        const uint32_t off = static_cast<uint32_t>(((16 * block < z.dv ? block : 0) * z.dk + (d < z.dk ? d : 0)) * 16 + 8 * (lg & 1)) * 4u;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            xs[kv][u] = load_at<f32x4>(ps + 32 * kv + 4 * u, off + 32 * lg);
-            xd[kv][u] = load_at<f32x4>(pd + 32 * kv + 4 * u, off + 32 * lg);
-          }
-      } else {
-#pragma unroll
-        for (int kv = 0; kv < KV; ++kv)
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int v = 32 * kv + 8 * lg + 4 * u + r;
-              const float x = load_at<float>(ps, off + 4u * (v < z.dv ? v : 0)), y = load_at<float>(pd, off + 4u * (v < z.dv ? v : 0));
-              xs[kv][u][r] = v < z.dv ? x : 0.0f;
-              xd[kv][u][r] = v < z.dv ? y : 0.0f;
-            }
-        own_way();
+        for (int u = 0; u < 2; ++u) {
+          xs[kv][u] = load_at<f32x4>(ps + 4 * u, off);
+          xd[kv][u] = load_at<f32x4>(pd + 4 * u, off);
+        }
       }
     }
     fetch_done();
@@ -437,8 +428,9 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            xs[kv][u][r] = d < z.dk ? xs[kv][u][r] : 0.0f;
-            xd[kv][u][r] = d < z.dk ? xd[kv][u][r] : 0.0f;
+            const bool in = d < z.dk && 32 * kv + 8 * lg + 4 * u + r < z.dv;
+            xs[kv][u][r] = in ? xs[kv][u][r] : 0.0f;
+            xd[kv][u][r] = in ? xd[kv][u][r] : 0.0f;
             inner = __builtin_fmaf(xs[kv][u][r], xd[kv][u][r], inner);
           }
         const Frag<kW> fs = frag_of<kW>(xs[kv][0], xs[kv][1]), fd = frag_of<kW>(xd[kv][0], xd[kv][1]);
@@ -634,16 +626,17 @@ extern "C" int det_delta_rule_bwd(const void* d_o, int64_t do_st, int64_t do_sh,
     r = delta_prepare(z, dtype, true, q, q_st, q_sh, k, k_st, k_sh, d_o, do_st, do_sh, g, g_ld, beta, beta_ld, base, l, st);
   const auto words = [&](size_t at) { return reinterpret_cast<uint16_t*>(base + at); };
   auto* ds = reinterpret_cast<float*>(base + l.ds);
-  const int image = static_cast<int>(delta_image_floats(dv, dtype)), saved = static_cast<int>(delta_saved_floats(dk, dv, dtype));
+  const int image = static_cast<int>(delta_image_floats(dv, dtype)), saved = static_cast<int>(delta_saved_floats(dk, dv, dtype)),
+            block = static_cast<int>(delta_block_floats(dk, dv));
 #define DET_DELTA_BWD(E)                                                                                               \
   {                                                                                                                    \
     const ChainArgs<E> A{r.k, r.q, {static_cast<const E*>(d_o), do_st, do_sh},                                         \
                          {static_cast<E*>(dv_out), dv_st, dv_sh}, words(l.units), dfinal_state, ds, dinitial_state,    \
-                         words(l.dy)};                                                                                 \
+                         words(l.dy), block};                                                                          \
     const GradArgs<E> B{r.k, r.q, r.d_o, {static_cast<E*>(dq), dq_st, dq_sh},                                          \
                         {static_cast<E*>(dk_out), dk_st, dk_sh}, static_cast<E*>(dg), static_cast<E*>(dbeta),          \
                         words(l.dy), words(l.units), g, states, ds, g_ld, dg_ld, dbeta_ld,  \
-                        image, saved};                                                                                 \
+                        image, saved, block};                                                                          \
     if (dk <= 64) launch_chain<E, 64>(z, A, st);                                                                       \
     else launch_chain<E, 128>(z, A, st);                                                                               \
     if (T) {                                                                                                           \

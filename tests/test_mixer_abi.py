@@ -150,10 +150,10 @@ def test_binding_refusals():
     refuse(ValueError, f, q, q, v, g, b, v[..., :4], offs)
     refuse(ValueError, f, q, q, v, g, b, v, offs[None])
     refuse(ValueError, f, q, q, v, g, b, v, offs, initial_state=s[:, :2])
-    refuse(ValueError, f, q, q, v, g, b, v, offs, states=torch.zeros(2, 4, 64 * 64 + 40))
+    refuse(ValueError, f, q, q, v, g, b, v, offs, states=torch.zeros(2, 4, 64 * 64 + 128))
     refuse(ValueError, f, q.transpose(1, 2).contiguous().transpose(1, 2), q, v, g, b, v, offs)
     refuse(ValueError, f, q, q, v, g, b, v.clone(), offs)                        # not on a GPU
-    assert dg.det_delta_rule_states_shape(q, v, offs) == (1, 4, 64 * 64 + 40)
+    assert dg.det_delta_rule_states_shape(q, v, offs) == (1, 4, 64 * 64 + 128)
     f, st = dg.det_delta_rule_bwd, torch.zeros(dg.det_delta_rule_states_shape(q, v, offs))
     refuse(TypeError, f, v.float(), q, q, v, g, b, offs, st, q, q, v, b, b)
     refuse(TypeError, f, v, q, q, v, g, b, offs, st, q, q, v, g, b)
