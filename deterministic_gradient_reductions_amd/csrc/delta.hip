@@ -293,57 +293,86 @@ struct FwdArgs {
 };
 
 // Workgroup (x, s): value head x % H of sequence s; wave w takes the columns
-// 16 (NW (x / H) + w) .. of v. Heads run fastest, so the workgroups of one head, which
+// 16 (8 (x / H) + w) .. of v. Heads run fastest, so the workgroups of one head, which
 // read the same fragments, meet in one of the eight L2 caches. A chunk's fragments
-// come into LDS while the chunk before is worked on; K^T is read there from K's rows. PAIR: a
-// second wave for the same columns fetches, and forms O, a chunk behind, from what the first
-// one leaves in LDS of S0 and N; what is left to the first is the chain of states. The
-// state goes from chunk to chunk as itself and as fragments, whose words are made
+// come into LDS while the chunk before is worked on; K^T is read there from K's rows.
+//
+// TEAM: 16 columns and three waves. The first is left with the chain of states; the second forms
+// O, a chunk behind, from what that leaves in LDS of S0 and N; the third fetches. (A wave
+// that does all waits for its own loads to be taken: 3.2 us a chunk where the team needs 2.0.)
+//
+// The state goes from chunk to chunk as itself and as fragments, whose words are made
 // while the matrix instructions of the other half of it run.
-template <typename T, int DK, int NW, bool PAIR>
+template <typename T, int DK, bool TEAM>
 __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T> A) {
   typedef Unit<T, false> Rec;
   constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
-  constexpr bool ALONE = PAIR && NW == 1;
-  // fragments in LDS: two buffers of K, the inverse and the gates, Q and P (PAIR: one of these two); V of each wave (PAIR: two)
+  constexpr int NW = TEAM ? 1 : 8;
+  // fragments in LDS: two buffers of K, the inverse and the gates, Q and P; V of each wave (TEAM: two); S0 and N for the team
   constexpr int nRows = RT * KD * kIn, nHead = Rec::oP, nP = Rec::nP, nX = KD * kOut + RT;
-  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nRows + nP), oQ = 2 * kBuf, oV = oQ + (PAIR ? nRows + nP : 0), oX = oV + (PAIR ? 4 : 2) * NW;
-  __shared__ __align__(16) char lds[(oX + (PAIR ? NW * nX : 0)) * 1024];
+  constexpr int oQ = nRows + nHead, oP = oQ + nRows, kBuf = oP + nP, oV = 2 * kBuf, oX = oV + (TEAM ? 4 : 2 * NW);
+  __shared__ __align__(16) char lds[(oX + (TEAM ? nX : 0)) * 1024];
   const int lane = threadIdx.x & 63, wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
-  const int wave = PAIR && wave_ >= NW ? wave_ - NW : wave_;
+  const int role = TEAM ? wave_ : 0, wave = TEAM ? 0 : wave_;
   const int h = blockIdx.x % z.H, hk = h / (z.H / z.Hk), v0 = ((blockIdx.x / z.H) * NW + wave) * 16, s = blockIdx.y;
   const uint32_t lds0 = lds_address(lds);
-  char* x = lds + (oX + (PAIR ? wave * nX : 0)) * 1024;  // S0 and N of these columns
+  char* x = lds + oX * 1024;
   uint32_t r0, r1, first;
   segment_rows(z.offs, s, static_cast<uint32_t>(z.T), kLogC, r0, r1, first);
   int64_t unit = static_cast<int64_t>(first) * z.H + h;
   int buf = 0;
 
   const bool whole = whole_columns(A.v, v0, z.dv);
-  const auto v_tile = [&](int buf) { return (oV + 2 * (PAIR ? 2 * wave + buf : wave)) * 1024; };
+  const auto v_tile = [&](int buf) { return (oV + 2 * (TEAM ? buf : wave)) * 1024; };
   const auto rows_at = [&](uint32_t t0) { return r1 - t0 < static_cast<uint32_t>(C) ? static_cast<int>(r1 - t0) : C; };
   const auto fetch_next = [&](uint32_t t0, int64_t unit, int buf) {
     const uint32_t to = lds0 + buf * kBuf * 1024;
     const uint16_t* rec = A.units + unit * Rec::kElems;
     fetch_rows<RT, KD, kIn, NW>(to, A.k, t0, rows_at(t0) - 1, hk, wave);
     fetch_image<nHead, NW, 4>(to + nRows * 1024, rec, wave);
-    if (!PAIR) {
-      fetch_rows<RT, KD, kIn, NW, 4>(to + (nRows + nHead) * 1024, A.q, t0, rows_at(t0) - 1, hk, wave);
-      fetch_image<nP, NW, 5>(to + (2 * nRows + nHead) * 1024, rec + Rec::oP * kFragElems, wave);
-    }
   };
-  const auto fetch_qp = [&](uint32_t t0, int64_t unit) {
-    fetch_rows<RT, KD, kIn, NW>(lds0 + oQ * 1024, A.q, t0, rows_at(t0) - 1, hk, wave);
-    fetch_image<nP, NW>(lds0 + (oQ + nRows) * 1024, A.units + unit * Rec::kElems + Rec::oP * kFragElems, wave);
+  const auto fetch_qp = [&](uint32_t t0, int64_t unit, int buf) {
+    const uint32_t to = lds0 + buf * kBuf * 1024;
+    fetch_rows<RT, KD, kIn, NW, 4>(to + oQ * 1024, A.q, t0, rows_at(t0) - 1, hk, wave);
+    fetch_image<nP, NW, 5>(to + oP * 1024, A.units + unit * Rec::kElems + Rec::oP * kFragElems, wave);
+  };
+  const auto fetch_v = [&](uint32_t t0, int buf) {
+    if (whole) fetch_columns<RT>(lds0 + v_tile(buf), A.v, t0, h, v0, rows_at(t0) - 1);
   };
 
-  if (PAIR && wave_ >= NW) {
+  if (role == 2) {
+    if (r0 < r1) {
+      fetch_next(r0, unit, 0);
+      fetch_v(r0, 0);
+      fetch_qp(r0, unit, 0);
+    }
+    fetch_done();
+    for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
+      __syncthreads();  // this chunk's fragments are there, the last one's have been read, but Q and P
+      const bool more = t0 + C < r1;
+      if (more) {
+        fetch_next(t0 + C, unit + z.H, buf ^ 1);
+        fetch_v(t0 + C, buf ^ 1);
+      }
+      __syncthreads();  // S0 and N are there, the last chunk's Q and P have been read
+      if (more) {
+        fetch_qp(t0 + C, unit + z.H, buf ^ 1);
+        fetch_done_but<nRows + nP>();
+      } else {
+        fetch_done();
+      }
+    }
+    __syncthreads();
+    return;
+  }
+
+  if (role == 1) {
     Frag<kOut> xs[KD], xu[KC];
     f32x4 nt[RT];
     float eg[RT];
-    const auto put_o = [&](uint32_t t0, const auto& read) {  // (rows v, columns t)
-      const char *q_img = lds + oQ * 1024, *p_img = q_img + nRows * 1024;
+    const auto put_o = [&](uint32_t t0, int64_t unit, int buf) {  // (rows v, columns t)
+      const char *q_img = lds + (buf * kBuf + oQ) * 1024, *p_img = lds + (buf * kBuf + oP) * 1024;
       f32x4 o[RT] = {};
 #pragma unroll
       for (int ks = 0; ks < KD; ++ks) {
@@ -360,37 +389,14 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
         for (int i = 2 * kt.value; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(p_img, lower_frag(i, kt.value));
         mm_tiles<kOut, 2 * kt.value, RT, true>(o, fp, xu[kt.value]);
       });
-      read();
-      if (A.saved)
-        put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + (unit - z.H) * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
+      if (A.saved) put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
       store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
     };
-    const auto fetch_v = [&](uint32_t t0, int buf) {
-      if (whole) fetch_columns<RT>(lds0 + v_tile(buf), A.v, t0, h, v0, rows_at(t0) - 1);
-    };
-    if (r0 < r1) {
-      fetch_next(r0, unit, 0);
-      fetch_v(r0, 0);
-    }
-    fetch_done();
     for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
-      __syncthreads();  // this chunk's fragments are there, the last one's have been read
-      const bool more = t0 + C < r1;
-      if (more) {
-        fetch_next(t0 + C, unit + z.H, buf ^ 1);
-        fetch_v(t0 + C, buf ^ 1);
-      }
-      // the last chunk's Q and P, fetched before those
-      if (more) fetch_done_but<fetched(KD * kIn, NW, 0, RT) + fetched(nHead, NW, 4)>();
-      else fetch_done();
-      const auto next_qp = [&] {
-        lds_read();
-        if (ALONE) fetch_qp(t0, unit);
-      };
-      if (t0 > r0) put_o(t0 - C, next_qp);
-      else next_qp();
+      __syncthreads();
+      if (t0 > r0) put_o(t0 - C, unit - z.H, buf ^ 1);
+      lds_read();
       __syncthreads();  // S0 and N are there
-      if (!ALONE) fetch_qp(t0, unit);
 #pragma unroll
       for (int ks = 0; ks < KD; ++ks) xs[ks] = lds_frag<kOut, kOut>(x, ks);
       const float* gate = reinterpret_cast<const float*>(lds + (buf * kBuf + nRows + Rec::oGate) * 1024);
@@ -405,12 +411,9 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
 #pragma unroll
       for (int i = 0; i < RT; ++i) eg[i] = gate[kEG * C + rho(i, c)] * z.scale;
       lds_read();
-      if (ALONE) fetch_done_but<fetched(KD * kIn, NW, 0, RT) + fetched(nP, NW, 0)>();
-      else fetch_done();
     }
-    fetch_done();
     __syncthreads();
-    if (r0 < r1) put_o(r0 + ((r1 - r0 - 1) >> kLogC << kLogC), [] {});
+    if (r0 < r1) put_o(r0 + ((r1 - r0 - 1) >> kLogC << kLogC), unit - z.H, buf ^ 1);
     return;
   }
 
@@ -433,19 +436,25 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
   const auto next_v = [&](uint32_t t0) {
     if (!whole) {
       load_column<RT>(rv, A.v.row(t0, h), A.v.st, vcol, rows_at(t0) - 1);
-    } else if (!PAIR) {
+    } else if (!TEAM) {
       lds_read();  // (the last one's)
-      fetch_columns<RT>(lds0 + v_tile(0), A.v, t0, h, v0, rows_at(t0) - 1);
+      fetch_v(t0, 0);
     }
   };
   if (r0 < r1) {
     next_v(r0);
-    if (!PAIR) fetch_next(r0, unit, 0);
+    if (!TEAM) {
+      fetch_next(r0, unit, 0);
+      fetch_qp(r0, unit, 0);
+    }
   }
-  if (!PAIR) fetch_done();
+  if (!TEAM) fetch_done();
   for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
     __syncthreads();  // this chunk's fragments are there, the last one's have been read
-    if (!PAIR && t0 + C < r1) fetch_next(t0 + C, unit + z.H, buf ^ 1);
+    if (!TEAM && t0 + C < r1) {
+      fetch_next(t0 + C, unit + z.H, buf ^ 1);
+      fetch_qp(t0 + C, unit + z.H, buf ^ 1);
+    }
     const char* img = lds + buf * kBuf * 1024;
     const float* gate = reinterpret_cast<const float*>(img + (nRows + Rec::oGate) * 1024);
     f32x4 R[RT];
@@ -459,7 +468,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
     }
     if (A.saved && v0 < z.dv) {
       lds_read();
-      store_block<DT>(S, A.saved + unit * A.saved_floats + A.image_floats + v0 * z.dk, z.dk, PAIR ? x + KD * kOut * 1024 : lds + v_tile(0));
+      store_block<DT>(S, A.saved + unit * A.saved_floats + A.image_floats + v0 * z.dk, z.dk, TEAM ? x + KD * kOut * 1024 : lds + v_tile(0));
     }
 
     // K S0 (rows t, columns v) and its transposed Q S0 (rows v, columns t)
@@ -469,16 +478,16 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
       Frag<kIn> fk[RT], fq[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) fk[i] = row_frag<kIn>(img, i * KD + ks);
-      if (PAIR) {
+      if (TEAM) {
         lds_put<kOut>(x, ks, f[ks]);
       } else {
 #pragma unroll
-        for (int i = 0; i < RT; ++i) fq[i] = row_frag<kIn>(img + (nRows + nHead) * 1024, i * KD + ks);
+        for (int i = 0; i < RT; ++i) fq[i] = row_frag<kIn>(img + oQ * 1024, i * KD + ks);
       }
       mm_tiles<kW, 0, RT>(ks0, fk, f[ks]);
-      if (!PAIR) mm_tiles<kOut, 0, RT, true>(o, fq, f[ks]);
+      if (!TEAM) mm_tiles<kOut, 0, RT, true>(o, fq, f[ks]);
     }
-    if (!PAIR)
+    if (!TEAM)
 #pragma unroll
       for (int i = 0; i < RT; ++i) o[i] *= gate[kEG * C + rho(i, c)] * z.scale;
 #pragma unroll
@@ -496,10 +505,10 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
 #pragma unroll
       for (int i = 2 * kt.value; i < RT; ++i) fi[i] = lds_frag<kW, kW>(img + nRows * 1024, lower_frag(i, kt.value));
       mm_tiles<kW, 2 * kt.value, RT>(U, fi, fr);
-      if (!PAIR && A.saved) mm_tiles<kOut, 2 * kt.value, RT, true>(nt, fi, fr);
+      if (!TEAM && A.saved) mm_tiles<kOut, 2 * kt.value, RT, true>(nt, fi, fr);
     });
-    if (!PAIR && A.saved) put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
-    if (PAIR) {
+    if (!TEAM && A.saved) put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
+    if (TEAM) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) *lds_tile(x + (KD * kOut + i) * 1024) = U[i];
     } else {
@@ -508,7 +517,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
         const Frag<kOut> fu = frag_of<kOut>(U[k] * gate4(gate, C, kBeta, rho(k, 4 * lg)), U[k + 1] * gate4(gate, C, kBeta, rho(k + 1, 4 * lg)));
         Frag<kOut> fp[RT];
 #pragma unroll
-        for (int i = k; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(img + (2 * nRows + nHead) * 1024, lower_frag(i, kt.value));
+        for (int i = k; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(img + oP * 1024, lower_frag(i, kt.value));
         mm_tiles<kOut, k, RT, true>(o, fp, fu);
       });
       store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
@@ -516,14 +525,14 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
     const float el = gate[kEnd * C];
 #pragma unroll
     for (int i = 0; i < RT; ++i) U[i] *= gate4(gate, C, kRestBeta, rho(i, 4 * lg));
-    if (PAIR) __syncthreads();  // S0 and N are there
+    if (TEAM) __syncthreads();  // S0 and N are there
     Frag<kW> fu[KC];
 #pragma unroll
     for (int kt = 0; kt < KC; ++kt) fu[kt] = frag_of<kW>(U[2 * kt], U[2 * kt + 1]);
     next_state<kIn, KC>(S, f, img, fu, el);
-    if (!PAIR) fetch_done();
+    if (!TEAM) fetch_done();
   }
-  if (PAIR) __syncthreads();
+  if (TEAM) __syncthreads();
   if (A.s1) store_state<DT>(S, A.s1 + of, z.dk, z.dv, col);
 }
 
@@ -573,12 +582,11 @@ DeltaPrepared prepare(const DeltaSizes& z, int dtype, bool bwd, const void* q, i
 
 template <typename T, int DK>
 void launch_fwd(const DeltaSizes& z, const FwdArgs<T>& A, hipStream_t st) {
-  const int nw = delta_chain_waves(z);
+  const bool teams = delta_teams(z);
   const int64_t columns = A.saved ? delta_pad(z.dv) : z.dv;  // (the images' padding is written too)
-  const dim3 grid(static_cast<uint32_t>(z.H * ceil_div(columns, 16 * nw)), static_cast<uint32_t>(z.S));
-  if (nw == 8) hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 8, false>), grid, dim3(512), 0, st, z, A);
-  else if (nw == 2) hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 2, true>), grid, dim3(256), 0, st, z, A);
-  else hipLaunchKernelGGL((delta_fwd_kernel<T, DK, 1, true>), grid, dim3(128), 0, st, z, A);
+  const dim3 grid(static_cast<uint32_t>(z.H * ceil_div(columns, teams ? 16 : 128)), static_cast<uint32_t>(z.S));
+  if (teams) hipLaunchKernelGGL((delta_fwd_kernel<T, DK, true>), grid, dim3(192), 0, st, z, A);
+  else hipLaunchKernelGGL((delta_fwd_kernel<T, DK, false>), grid, dim3(512), 0, st, z, A);
 }
 
 }  // namespace

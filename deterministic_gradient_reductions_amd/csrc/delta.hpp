@@ -312,18 +312,6 @@ __device__ __forceinline__ void fetch_done_but() {
 }
 // What this wave has read of LDS is in its registers (a fetch may write there).
 __device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-// The fewest fragments that fetch_image brings in one wave, and fetch_rows (RT tiles of N fragments).
-constexpr int fetched(int N, int NW, int first, int RT = 1) {
-  int least = 1 << 20;
-  const int groups = (N + 3) / 4;
-  for (int w = 0; w < NW; ++w) {
-    int n = 0;
-    for (int g = 0; g < RT * groups; ++g)
-      if ((g + first) % NW == w) n += N - 4 * (g % groups) < 4 ? N - 4 * (g % groups) : 4;
-    least = n < least ? n : least;
-  }
-  return least;
-}
 // N consecutive fragments of an image, four at a time, shared out among NW waves from wave FIRST on.
 template <int N, int NW, int FIRST = 0>
 __device__ __forceinline__ void fetch_image(uint32_t lds, const uint16_t* image, int wave) {
@@ -659,12 +647,9 @@ inline int delta_words(int dtype) { return dtype == DET_BF16 ? DeltaType<uint16_
 inline int64_t delta_tiles(int64_t T, int64_t S, int dtype) { return T / delta_chunk(dtype) + S; }
 inline int delta_pad(int64_t d) { return d <= 64 ? 64 : 128; }
 
-// The waves of a workgroup of the chains of states: all columns of a head, which share its
-// fragments, where that leaves a workgroup for each compute unit; else spread out, in pairs.
-inline int delta_chain_waves(const DeltaSizes& z) {
-  const int64_t chains = static_cast<int64_t>(z.S) * z.H;
-  return chains >= 128 ? 8 : chains >= 64 ? 2 : 1;
-}
+// The workgroups of the chains of states: all columns of a head in eight waves, which share its
+// fragments, where there is a head for every fourth compute unit; else 16 columns in a team.
+inline bool delta_teams(const DeltaSizes& z) { return static_cast<int64_t>(z.S) * z.H < 64; }
 
 // What a forward leaves for the backward per (chunk, value head): N as an image of rows t and
 // places v in kOut words, then the state in front of the chunk in blocks of 16 columns, in floats.

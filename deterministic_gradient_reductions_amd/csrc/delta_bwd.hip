@@ -33,26 +33,25 @@ struct ChainArgs {
   int ds_floats;
 };
 
-// Workgroups, waves and buffers as in the forward's chain. PAIR: the second wave fetches,
-// forms P^T dO (a chunk ahead) and scale (e^G Q)^T dO for the first one, and dV and dY's image
-// from what that leaves of dY.
-template <typename T, int DK, int NW, bool PAIR>
+// Workgroups, waves and buffers as in the forward's chain. TEAM: the second wave forms P^T dO
+// (a chunk ahead) and scale (e^G Q)^T dO for the first one, and dV and dY's image from what
+// that leaves of dY.
+template <typename T, int DK, bool TEAM>
 __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArgs<T> A) {
   typedef Unit<T, true> Rec;
   constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
-  constexpr bool ALONE = PAIR && NW == 1;
-  // fragments in LDS: two buffers of K, the inverse and the gates, P and Q (PAIR: one of these two); dO of each wave
+  constexpr int NW = TEAM ? 1 : 8;
+  // fragments in LDS: two buffers of K, the inverse and the gates, P and Q; dO of each wave (TEAM: two); what the team hands on
   constexpr int nRows = RT * KD * kIn, nHead = Rec::oP, nP = Rec::nP, nX = 2 * RT + DT;
-  constexpr int kBuf = nRows + nHead + (PAIR ? 0 : nP + nRows), oPs = 2 * kBuf, oQ = oPs + nP;
-  constexpr int oO = PAIR ? oQ + nRows : 2 * kBuf, oX = oO + 2 * NW;
-  __shared__ __align__(16) char lds[(oX + (PAIR ? NW * nX : 0)) * 1024];
+  constexpr int oP = nRows + nHead, oQ = oP + nP, kBuf = oQ + nRows, oO = 2 * kBuf, oX = oO + (TEAM ? 4 : 2 * NW);
+  __shared__ __align__(16) char lds[(oX + (TEAM ? nX : 0)) * 1024];
   const int lane = threadIdx.x & 63, wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
-  const int wave = PAIR && wave_ >= NW ? wave_ - NW : wave_;
+  const int role = TEAM ? wave_ : 0, wave = TEAM ? 0 : wave_;
   const int h = blockIdx.x % z.H, hk = h / (z.H / z.Hk), v0 = ((blockIdx.x / z.H) * NW + wave) * 16, s = blockIdx.y;
   const int dvp = z.dv <= 64 ? 64 : 128;
   const uint32_t lds0 = lds_address(lds);
-  char* x = lds + (oX + (PAIR ? wave * nX : 0)) * 1024;  // dY of these columns
+  char* x = lds + (TEAM ? oX : 0) * 1024;  // dY of these columns
   f32x4 *x_p = lds_tile(x + RT * 1024), *x_q = x_p + RT * 64;  // tiles of P^T dO, of scale (e^G Q)^T dO
   uint32_t r0, r1, first;
   segment_rows(z.offs, s, static_cast<uint32_t>(z.T), kLogC, r0, r1, first);
@@ -60,20 +59,21 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
   const int chunks = static_cast<int>((r1 - r0 + C - 1) >> kLogC);
   int64_t unit = (static_cast<int64_t>(first) + chunks - 1) * z.H + h;
   int buf = 0;
-  char* o_tile = lds + (oO + 2 * wave) * 1024;
+  const auto o_tile = [&](int buf) { return (oO + 2 * (TEAM ? buf : wave)) * 1024; };
   const bool whole = whole_columns(A.d_o, v0, z.dv);
   T rd[RT][4];
   f32x4 dO[RT];
   const auto start = [&](int ch) { return r0 + (static_cast<uint32_t>(ch) << kLogC); };
   const auto rows_at = [&](int ch) { return r1 - start(ch) < static_cast<uint32_t>(C) ? static_cast<int>(r1 - start(ch)) : C; };
-  const auto next_do = [&](int ch) {
-    lds_read();  // (the last one's)
-    if (whole) fetch_columns<RT>(lds0 + (oO + 2 * wave) * 1024, A.d_o, start(ch), h, v0, rows_at(ch) - 1);
-    else load_column<RT>(rd, A.d_o.row(start(ch), h), A.d_o.st, vcol, rows_at(ch) - 1);
+  const auto fetch_do = [&](int ch, int buf) {
+    if (whole) fetch_columns<RT>(lds0 + o_tile(buf), A.d_o, start(ch), h, v0, rows_at(ch) - 1);
   };
-  const auto take_do = [&] {
+  const auto load_do = [&](int ch) {
+    if (!whole) load_column<RT>(rd, A.d_o.row(start(ch), h), A.d_o.st, vcol, rows_at(ch) - 1);
+  };
+  const auto take_do = [&](int buf) {
     if (whole) {
-      take_columns<RT>(dO, o_tile, static_cast<const T*>(nullptr));
+      take_columns<RT>(dO, lds + o_tile(buf), static_cast<const T*>(nullptr));
     } else {
 #pragma unroll
       for (int i = 0; i < RT; ++i)
@@ -81,18 +81,14 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
         for (int r = 0; r < 4; ++r) dO[i][r] = to_f32(rd[i][r]);
     }
   };
-  const auto fetch_p = [&](uint32_t to, int64_t unit) {
-    fetch_image<nP, NW, 5>(to, A.units + unit * Rec::kElems + Rec::oP * kFragElems, wave);
+  const auto fetch_p = [&](int64_t unit, int buf) {
+    fetch_image<nP, NW, 5>(lds0 + (buf * kBuf + oP) * 1024, A.units + unit * Rec::kElems + Rec::oP * kFragElems, wave);
   };
-  const auto fetch_q = [&](uint32_t to, int ch) { fetch_rows<RT, KD, kIn, NW, 4>(to, A.q, start(ch), rows_at(ch) - 1, hk, wave); };
   const auto fetch_next = [&](int ch, int64_t unit, int buf) {
     const uint32_t to = lds0 + buf * kBuf * 1024;
     fetch_rows<RT, KD, kIn, NW>(to, A.k, start(ch), rows_at(ch) - 1, hk, wave);
     fetch_image<nHead, NW, 4>(to + nRows * 1024, A.units + unit * Rec::kElems, wave);
-    if (!PAIR) {
-      fetch_p(to + (nRows + nHead) * 1024, unit);
-      fetch_q(to + (nRows + nHead + nP) * 1024, ch);
-    }
+    fetch_rows<RT, KD, kIn, NW, 4>(to + oQ * 1024, A.q, start(ch), rows_at(ch) - 1, hk, wave);
   };
   // dU += P^T dO
   const auto add_p = [&](f32x4 (&dU)[RT], const char* img) {
@@ -127,59 +123,68 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
     store_rows<RT>(dv, A.dv.row(start(ch), h), A.dv.st, v0, z.dv, rows_at(ch));
   };
 
-  if (PAIR && wave_ >= NW) {
+  if (role == 2) {
     if (chunks) {
-      next_do(chunks - 1);
       fetch_next(chunks - 1, unit, 0);
-      fetch_p(lds0 + oPs * 1024, unit);
-      fetch_q(lds0 + oQ * 1024, chunks - 1);
+      fetch_p(unit, 0);
+      fetch_do(chunks - 1, 0);
     }
     fetch_done();
+    __syncthreads();  // the last chunk's fragments are there
+    if (chunks > 1) {
+      fetch_p(unit - z.H, 1);
+      fetch_do(chunks - 2, 1);
+    }
+    for (int ch = chunks - 1; ch >= 0; --ch, unit -= z.H, buf ^= 1) {
+      __syncthreads();  // this chunk's fragments are there, the one's behind it have been read
+      if (ch > 0) {
+        fetch_next(ch - 1, unit - z.H, buf ^ 1);
+        fetch_done_but<2 * nRows + nHead>();  // (the next chunk's P and dO are there)
+      }
+      __syncthreads();
+      if (ch > 1) {  // (this chunk's P and dO have been read)
+        fetch_p(unit - 2 * z.H, buf);
+        fetch_do(ch - 2, buf);
+        if (whole) fetch_done_but<nP + 2>();
+        else fetch_done_but<nP>();
+      } else {
+        fetch_done();
+      }
+    }
+    return;
+  }
+  if (role == 1) {
     __syncthreads();
-    const auto give_p = [&] {
+    const auto give_p = [&](int buf) {
       f32x4 w[RT] = {};
-      add_p(w, lds + oPs * 1024);
+      add_p(w, lds + (buf * kBuf + oP) * 1024);
 #pragma unroll
       for (int i = 0; i < RT; ++i) x_p[i * 64] = w[i];
     };
     if (chunks) {
-      take_do();
-      give_p();
+      load_do(chunks - 1);
+      take_do(0);
+      give_p(0);
     }
     for (int ch = chunks - 1; ch >= 0; --ch, unit -= z.H, buf ^= 1) {
       lds_read();
-      __syncthreads();  // P^T dO and this chunk's fragments are there, the last one's have been read
+      __syncthreads();  // P^T dO is there
       const char* img = lds + buf * kBuf * 1024;
       const float* gate = reinterpret_cast<const float*>(img + (nRows + Rec::oGate) * 1024);
-      if (ch > 0) {
-        fetch_p(lds0 + oPs * 1024, unit - z.H);
-        next_do(ch - 1);
-        fetch_next(ch - 1, unit - z.H, buf ^ 1);
-      }
-      {
-        f32x4 w[DT] = {};
-        add_q(w, lds + oQ * 1024, gate);
+      if (ch > 0) load_do(ch - 1);
+      f32x4 w[DT] = {};
+      add_q(w, img + oQ * 1024, gate);
 #pragma unroll
-        for (int i = 0; i < DT; ++i) x_q[i * 64] = w[i];
-        lds_read();
-      }
-      // P's and dO's; alone this wave needs them only after the barrier
-      const auto done_now = [&] {
-        if (ch > 0) fetch_done_but<fetched(KD * kIn, NW, 0, RT) + fetched(nHead, NW, 4)>();
-        else fetch_done();
-      };
-      if (!ALONE) done_now();
-      __syncthreads();  // dY is there, and what this wave has left; Q has been read
-      if (ALONE) done_now();
-      if (ch > 0) fetch_q(lds0 + oQ * 1024, ch - 1);
+      for (int i = 0; i < DT; ++i) x_q[i * 64] = w[i];
+      lds_read();
+      __syncthreads();  // dY is there, and what this wave has left
       f32x4 yt[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) yt[i] = lds_turned(x + i * 1024);
       if (ch > 0) {
-        take_do();
-        give_p();
+        take_do(buf ^ 1);
+        give_p(buf ^ 1);
       }
-      fetch_done();  // (before the stores, which nothing waits for)
       put_y(yt, gate, ch, unit);
     }
     return;
@@ -198,24 +203,29 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
   Frag<kW> f[KD];  // of S
 #pragma unroll
   for (int ks = 0; ks < KD; ++ks) f[ks] = frag_of<kW>(S[2 * ks], S[2 * ks + 1]);
-  if (PAIR) {
+  if (TEAM) {
     __syncthreads();
   } else {
     if (chunks) {
-      next_do(chunks - 1);
+      load_do(chunks - 1);
+      fetch_do(chunks - 1, 0);
       fetch_next(chunks - 1, unit, 0);
+      fetch_p(unit, 0);
     }
     fetch_done();
   }
   for (int ch = chunks - 1; ch >= 0; --ch, unit -= z.H, buf ^= 1) {
     __syncthreads();  // this chunk's fragments are there, the last one's have been read
-    if (!PAIR) {
-      if (ch > 0) fetch_next(ch - 1, unit - z.H, buf ^ 1);
-      take_do();
+    if (!TEAM) {
+      if (ch > 0) {
+        fetch_next(ch - 1, unit - z.H, buf ^ 1);
+        fetch_p(unit - z.H, buf ^ 1);
+      }
+      take_do(0);
     }
     if (v0 < z.dv) {
-      if (!PAIR) lds_read();
-      store_block<DT>(S, A.ds + unit * A.ds_floats + v0 * z.dk, z.dk, PAIR ? x : o_tile);
+      if (!TEAM) lds_read();
+      store_block<DT>(S, A.ds + unit * A.ds_floats + v0 * z.dk, z.dk, TEAM ? x : lds + o_tile(0));
     }
     const char* img = lds + buf * kBuf * 1024;
     const float* gate = reinterpret_cast<const float*>(img + (nRows + Rec::oGate) * 1024);
@@ -229,12 +239,16 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
     }
 #pragma unroll
     for (int i = 0; i < RT; ++i) dU[i] *= gate4(gate, C, kRest, rho(i, 4 * lg));
-    if (PAIR) {
+    if (TEAM) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) dU[i] += x_p[i * 64];
     } else {
-      add_p(dU, img + (nRows + nHead) * 1024);
-      if (ch > 0) next_do(ch - 1);
+      add_p(dU, img + oP * 1024);
+      if (ch > 0) {
+        lds_read();  // (this chunk's dO)
+        load_do(ch - 1);
+        fetch_do(ch - 1, 0);
+      }
     }
     f32x4 dN[RT] = {}, yt[RT] = {};  // dY, and dY with rows v and columns t
     static_for<KC>([&](auto kt) {
@@ -244,10 +258,10 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
 #pragma unroll
       for (int j = 0; j < to; ++j) fi[j] = lds_frag<kW, kW>(img + nRows * 1024, upper_frag<KC>(j, kt.value));
       mm_tiles<kW, 0, to>(dN, fi, fu);
-      if (!PAIR) mm_tiles<kOut, 0, to, true>(yt, fi, fu);
+      if (!TEAM) mm_tiles<kOut, 0, to, true>(yt, fi, fu);
     });
     const float el = gate[kEnd * C];
-    if (PAIR) {
+    if (TEAM) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) *lds_tile(x + i * 1024) = dN[i];
     } else {
@@ -260,15 +274,15 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
     for (int kt = 0; kt < KC; ++kt) fn[kt] = frag_of<kW>(dN[2 * kt], dN[2 * kt + 1]);
 #pragma unroll
     for (int i = 0; i < DT; ++i) S[i] *= el;
-    if (PAIR) {
+    if (TEAM) {
       __syncthreads();  // the second wave's part of dS is there
 #pragma unroll
       for (int i = 0; i < DT; ++i) S[i] += x_q[i * 64];
     } else {
-      add_q(S, img + (nRows + nHead + nP) * 1024, gate);
+      add_q(S, img + oQ * 1024, gate);
     }
     next_state<kIn, KC>(S, f, img, fn, 1.0f);
-    if (!PAIR) fetch_done();
+    if (!TEAM) fetch_done();
   }
   if (A.ds0) store_state<DT>(S, A.ds0 + of, z.dk, z.dv, col);
 }
@@ -548,11 +562,10 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
 
 template <typename T, int DK>
 void launch_chain(const DeltaSizes& z, const ChainArgs<T>& A, hipStream_t st) {
-  const int nw = delta_chain_waves(z);
-  const dim3 grid(static_cast<uint32_t>(z.H * ceil_div(delta_pad(z.dv), 16 * nw)), static_cast<uint32_t>(z.S));
-  if (nw == 8) hipLaunchKernelGGL((delta_chain_kernel<T, DK, 8, false>), grid, dim3(512), 0, st, z, A);
-  else if (nw == 2) hipLaunchKernelGGL((delta_chain_kernel<T, DK, 2, true>), grid, dim3(256), 0, st, z, A);
-  else hipLaunchKernelGGL((delta_chain_kernel<T, DK, 1, true>), grid, dim3(128), 0, st, z, A);
+  const bool teams = delta_teams(z);
+  const dim3 grid(static_cast<uint32_t>(z.H * (teams ? delta_pad(z.dv) / 16 : 1)), static_cast<uint32_t>(z.S));
+  if (teams) hipLaunchKernelGGL((delta_chain_kernel<T, DK, true>), grid, dim3(192), 0, st, z, A);
+  else hipLaunchKernelGGL((delta_chain_kernel<T, DK, false>), grid, dim3(512), 0, st, z, A);
 }
 
 template <typename T, int DK, int DV>
