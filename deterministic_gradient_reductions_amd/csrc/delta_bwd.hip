@@ -360,8 +360,10 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
           xd[kv][u] = load_at<f32x4>(pd + 4 * u, off);
         }
       }
+      fetch_done_but<4 * KV>();  // (the states' rows are still on their way)
+    } else {
+      fetch_done();
     }
-    fetch_done();
     __syncthreads();
 
     // The pair tiles, rows j and columns i: D, P, M, then dP, X and what comes of them.
