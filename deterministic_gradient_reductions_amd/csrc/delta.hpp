@@ -186,17 +186,21 @@ __device__ __forceinline__ s16x4 lds_turned4(const char* p) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
 }
-template <int KD, int NP>
-__device__ __forceinline__ Frag<NP> turned_frag(const char* image, int j, int kt) {
+template <int NP>
+__device__ __forceinline__ Frag<NP> turned_frag(const char* image, int j, int frag0, int frag1) {  // (of the two row tiles)
   const int lane = threadIdx.x & 63, p = lane & 15, x = 4 * (lane >> 4) + (p >> 2), g = p & 3;
-  const char* at = image + (2 * kt * KD + (j >> 1)) * NP * 1024 + (16 * g + (x ^ (4 * g))) * 16 + 8 * (j & 1);
+  const char* at = image + (16 * g + (x ^ (4 * g))) * 16 + 8 * (j & 1);
   Frag<NP> r;
 #pragma unroll
   for (int w = 0; w < NP; ++w) {
-    const s16x4 a = lds_turned4(at + w * 1024), b = lds_turned4(at + (KD * NP + w) * 1024);
+    const s16x4 a = lds_turned4(at + (frag0 * NP + w) * 1024), b = lds_turned4(at + (frag1 * NP + w) * 1024);
     r.w[w] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   }
   return r;
+}
+template <int KD, int NP>
+__device__ __forceinline__ Frag<NP> turned_frag(const char* image, int j, int kt) {
+  return turned_frag<NP>(image, j, 2 * kt * KD + (j >> 1), (2 * kt + 1) * KD + (j >> 1));
 }
 // The first NP words to LDS.
 template <int NP, int N>

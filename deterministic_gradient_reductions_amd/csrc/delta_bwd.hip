@@ -316,14 +316,13 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
   constexpr int NW = (DK > DV ? DK : DV) / 16, RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, KV = DV / 32;
   constexpr int kFrags = KC * (KC + 1), kPairs = 2 * kFrags, kMine = (kPairs + NW - 1) / NW;  // pair tiles, of a wave
   // 1024-byte fragments of the images
-  constexpr int nK = RT * KD * kIn, nO = RT * KV * kIn, nV = RT * KV * kW, nTri = kFrags * kW, nSq = RT * KC * kW,
+  constexpr int nK = RT * KD * kIn, nO = RT * KV * kIn, nV = RT * KV * kW, nTri = kFrags * kW,
                 nGate = Unit<T, true>::nGate;
-  constexpr int oQ = nK, oO = 2 * nK, oN = oO + nO, oY = oN + nV, oA = oY + nV, oB = oA + nTri, oZ = oB + nTri, oGate = oZ + nSq;
-  __shared__ __align__(16) char lds[(oGate + nGate) * 1024];
+  constexpr int oQ = nK, oO = 2 * nK, oN = oO + nO, oY = oN + nV, oA = oY + nV, oZ = oA + nTri, oGate = oZ + nTri;
+  __shared__ __align__(16) char lds[(oGate + 2 * nGate) * 1024];
   __shared__ float red_q[NW][C], red_s[NW], red_w[NW], diag[C];
   __shared__ float row_e[RT][RT][16], col_e[RT][RT][16];
-  const float* gate = reinterpret_cast<const float*>(lds + oGate * 1024);
-  char *img_a = lds + oA * 1024, *img_b = lds + oB * 1024, *img_z = lds + oZ * 1024;
+  char *img_a = lds + oA * 1024, *img_z = lds + oZ * 1024;
   const uint32_t lds0 = lds_address(lds);
   const int wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tile = blockIdx.x;
@@ -334,17 +333,24 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
   fetch_rows<RT, KD, kIn, NW>(lds0, A.k, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
   fetch_rows<RT, KD, kIn, NW, 4>(lds0 + oQ * 1024, A.q, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
   f32x4 dq[RT] = {}, dk[RT] = {};  // rows d, columns t
+  f32x4 qk[kMine], kk[kMine];      // of this wave's pair tiles
+  const auto fetch_head = [&](int h, int buf) {
+    const int wave = here(wave_), n = here(static_cast<int>(t1 - t0));
+    const int64_t unit = static_cast<int64_t>(tile) * z.H + h;
+    fetch_image<nV, NW>(lds0 + oN * 1024, reinterpret_cast<const uint16_t*>(A.saved + unit * A.saved_floats), wave);
+    fetch_image<nV, NW, nV / 4>(lds0 + oY * 1024, A.dy + unit * (nV * kFragElems), wave);
+    fetch_rows<RT, KV, kIn, NW, nV / 2>(lds0 + oO * 1024, A.d_o, t0, n - 1, h, wave);
+    fetch_image<nGate, NW, 7>(lds0 + (oGate + buf * nGate) * 1024, A.units + unit * Unit<T, true>::kElems + Unit<T, true>::oGate * kFragElems, wave);
+  };
+  const int h0 = hk * group;
+  fetch_head(h0, 0);
 
-  for (int h = hk * group; h < (hk + 1) * group; ++h) {
+  for (int h = h0; h < h0 + group; ++h) {
     const int wave = here(wave_), lane = here_lane(threadIdx.x) & 63, c = lane & 15, lg = lane >> 4;
     const int n = here(static_cast<int>(t1 - t0));
     const int64_t unit = static_cast<int64_t>(tile) * z.H + h;
-    const float *saved = A.saved + unit * A.saved_floats, *ps = saved + A.image_floats, *pd = A.ds + unit * A.ds_floats;
-    __syncthreads();  // the last head's images and sums have been read
-    fetch_image<nV, NW>(lds0 + oN * 1024, reinterpret_cast<const uint16_t*>(saved), wave);
-    fetch_image<nV, NW, nV / 4>(lds0 + oY * 1024, A.dy + unit * (nV * kFragElems), wave);
-    fetch_rows<RT, KV, kIn, NW, nV / 2>(lds0 + oO * 1024, A.d_o, t0, n - 1, h, wave);
-    fetch_image<nGate, NW, 7>(lds0 + oGate * 1024, A.units + unit * Unit<T, true>::kElems + Unit<T, true>::oGate * kFragElems, wave);
+    const float *ps = A.saved + unit * A.saved_floats + A.image_floats, *pd = A.ds + unit * A.ds_floats;
+    const float* gate = reinterpret_cast<const float*>(lds + (oGate + ((h - h0) & 1) * nGate) * 1024);
     // the states' rows of this wave's channels, for the second phase
     const int d = rho(wave, c);
     f32x4 xs[KV][2], xd[KV][2];
@@ -367,13 +373,13 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
     __syncthreads();
 
     // The pair tiles, rows j and columns i: D, P, M, then dP, X and what comes of them.
-#pragma unroll 1
-    for (int m = 0; m < kMine; ++m) {
+    static_for<kMine>([&](auto mine) {
+      constexpr int m = mine.value;
       const int p = wave + m * NW;
-      if (p >= kPairs) break;
+      if (p >= kPairs) return;
       int i, j;
       pair_of(p, i, j);
-      f32x4 qk{}, kk{}, x{}, y{};
+      f32x4 x{}, y{};
       const int row = rho(i, c), at0 = rho(j, 4 * lg);
 #pragma unroll
       for (int kv = 0; kv < KV; ++kv) {
@@ -381,11 +387,14 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
         mm<kW>(x, f, lds_frag<kW, kW>(lds + oY * 1024, i * KV + kv));
         mm<kW>(y, f, row_frag<kIn>(lds + oO * 1024, i * KV + kv));
       }
+      if (h == h0) {
+        qk[m] = kk[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int ks = 0; ks < KD; ++ks) {
-        const Frag<kIn> kj = row_frag<kIn>(lds, j * KD + ks);
-        mm<kIn>(kk, kj, row_frag<kIn>(lds, i * KD + ks));
-        mm<kIn>(qk, kj, row_frag<kIn>(lds + oQ * 1024, i * KD + ks));
+        for (int ks = 0; ks < KD; ++ks) {
+          const Frag<kIn> kj = row_frag<kIn>(lds, j * KD + ks);
+          mm<kIn>(kk[m], kj, row_frag<kIn>(lds, i * KD + ks));
+          mm<kIn>(qk[m], kj, row_frag<kIn>(lds + oQ * 1024, i * KD + ks));
+        }
       }
       const f32x4 b = gate4(gate, C, kBeta, at0), hj = gate4(gate, C, kGHi, at0), lj = gate4(gate, C, kGLo, at0);
       const float hi = gate[kGHi * C + row], li = gate[kGLo * C + row], bi = gate[kBeta * C + row];
@@ -399,7 +408,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
         const float dp = in ? b[r] * y[r] * dc * z.scale : 0.0f, bx = off ? b[r] * bi * x[r] * dc : 0.0f;
         pd[r] = dp;
         zz[r] = -bx;
-        ev[r] = dp * qk[r] - bx * kk[r];
+        ev[r] = dp * qk[m][r] - bx * kk[m][r];
       }
       // sums over j (rows of the tile) for row i, over i (its columns) for row j
       const Halves s16 = halves16((ev[0] + ev[1]) + (ev[2] + ev[3]));
@@ -410,28 +419,19 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
         const float ce = row16_tree(ev[r]);
         if (c == 0) col_e[i][j][4 * lg + r] = ce;
       }
-      // dP * D with rows i and places j, with rows j and places i; Z + Z^T. Row tile i, row c, places at0 .. of
-      // fragment j / 2, and row tile j, rows 4 lg + r, place `row` of fragment i / 2:
-      const int in_a = (16 * lg + c) * 16 + (j & 1) * 8, in_b = (16 * (c >> 2) + 4 * lg) * 16 + (4 * (i & 1) + (c & 3)) * 2;
-      char *to_a = img_a + lower_frag(i, j >> 1) * kW * 1024 + in_a, *to_b = img_b + upper_frag<KC>(j, i >> 1) * kW * 1024 + in_b;
-      char *to_z = img_z + (i * KC + (j >> 1)) * kW * 1024 + in_a, *to_zt = img_z + (j * KC + (i >> 1)) * kW * 1024 + in_b;
-      const bool diagonal = i / 2 == j / 2;
+      // dP * D and Z as images of rows i and places j: row tile i, row c, places at0 .. of fragment j / 2
+      const int to = lower_frag(i, j >> 1) * kW * 1024 + row_place() * 16 + (j & 1) * 8;
+      uint32_t w0[kW], w1[kW], w2[kW], w3[kW];
+      split2<kW>(pd[0], pd[1], w0);
+      split2<kW>(pd[2], pd[3], w1);
+      split2<kW>(zz[0], zz[1], w2);
+      split2<kW>(zz[2], zz[3], w3);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        __bf16 wp[kW], wz[kW];
-        split<kW>(pd[r], wp);
-        split<kW>(zz[r], wz);
-#pragma unroll
-        for (int w = 0; w < kW; ++w) {
-          *reinterpret_cast<__bf16*>(to_a + w * 1024 + 2 * r) = wp[w];
-          *reinterpret_cast<__bf16*>(to_b + w * 1024 + 16 * r) = wp[w];
-          if (!diagonal || at0 + r <= row) {
-            *reinterpret_cast<__bf16*>(to_z + w * 1024 + 2 * r) = wz[w];
-            *reinterpret_cast<__bf16*>(to_zt + w * 1024 + 16 * r) = wz[w];
-          }
-        }
+      for (int w = 0; w < kW; ++w) {
+        *reinterpret_cast<uint64_t*>(img_a + to + w * 1024) = w0[w] | static_cast<uint64_t>(w1[w]) << 32;
+        *reinterpret_cast<uint64_t*>(img_z + to + w * 1024) = w2[w] | static_cast<uint64_t>(w3[w]) << 32;
       }
-    }
+    });
     __syncthreads();
 
     // 16 channels of dq and dk
@@ -501,19 +501,27 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
         red_s[wave] = inner;
         red_w[wave] = w_sum;
       }
+    }
+    __syncthreads();  // N, dY and dO have been read
+    if (h + 1 < h0 + group) fetch_head(h + 1, (h + 1 - h0) & 1);
+    if (wave < DT) {
       static_for<KC>([&](auto kt) {
         constexpr int at = kt.value;
         const Frag<kIn> kT = turned_frag<KD, kIn>(lds, wave, at), qT = turned_frag<KD, kIn>(lds + oQ * 1024, wave, at);
         Frag<kW> f[RT];
 #pragma unroll
-        for (int i = 2 * at; i < RT; ++i) f[i] = lds_frag<kW, kW>(img_a, lower_frag(i, at));
+        for (int i = 2 * at; i < RT; ++i) f[i] = row_frag<kW>(img_a, lower_frag(i, at));
         mm_tiles<kW, 2 * at, RT, true>(dq, f, kT);
 #pragma unroll
-        for (int i = 0; i < 2 * at + 2; ++i) f[i] = lds_frag<kW, kW>(img_b, upper_frag<KC>(i, at));
+        for (int i = 2 * at; i < RT; ++i) f[i] = row_frag<kW>(img_z, lower_frag(i, at));
+        mm_tiles<kW, 2 * at, RT, true>(dk, f, kT);
+        step();
+#pragma unroll
+        for (int j = 0; j < 2 * at + 2; ++j) f[j] = turned_frag<kW>(img_a, j, lower_frag(2 * at, j >> 1), lower_frag(2 * at + 1, j >> 1));
         mm_tiles<kW, 0, 2 * at + 2, true>(dk, f, qT);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(img_z, i * KC + at);
-        mm_tiles<kW, 0, RT, true>(dk, f, kT);
+        for (int j = 0; j < 2 * at + 2; ++j) f[j] = turned_frag<kW>(img_z, j, lower_frag(2 * at, j >> 1), lower_frag(2 * at + 1, j >> 1));
+        mm_tiles<kW, 0, 2 * at + 2, true>(dk, f, kT);
         step();
       });
     }
