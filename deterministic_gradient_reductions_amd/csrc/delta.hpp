@@ -651,9 +651,12 @@ inline int delta_words(int dtype) { return dtype == DET_BF16 ? DeltaType<uint16_
 inline int64_t delta_tiles(int64_t T, int64_t S, int dtype) { return T / delta_chunk(dtype) + S; }
 inline int delta_pad(int64_t d) { return d <= 64 ? 64 : 128; }
 
-// The workgroups of the chains of states: all columns of a head in eight waves, which share its
-// fragments, where there is a head for every fourth compute unit; else 16 columns in a team.
-inline bool delta_teams(const DeltaSizes& z) { return static_cast<int64_t>(z.S) * z.H < 64; }
+// The workgroups of the chains of states: eight waves for all columns of a head, which share its
+// fragments, or a team of three waves for 16 columns. A team's chunk takes 2.2 us, the eight waves'
+// 5.9 to 6.5 us, but there are eight times as many teams for the compute units. 8192 tokens in all, 32 heads of
+// 128 x 128, bf16, teams and eight waves: one sequence 336 and 780 us, two 324 and 425 us, three
+// 338 and 313 us, eight 341 and 168 us; with the backward's states and the backward the same way round.
+inline bool delta_teams(const DeltaSizes& z) { return static_cast<int64_t>(z.S) * z.H <= 80; }
 
 // What a forward leaves for the backward per (chunk, value head): N as an image of rows t and
 // places v in kOut words, then the state in front of the chunk in blocks of 16 columns, in floats.
