@@ -50,6 +50,7 @@ __device__ __forceinline__ int channel(const QkPlan& P, int p, int s) {
 // A lane's eight pairs of a row.
 struct Spot {
   int p0, off[2];  // first pair; first channels of the two runs of eight
+  bool live;       // there are any of them
   bool fast;       // both runs lie in the row as they stand
   bool split;      // the runs are the two sides (else sixteen neighbours)
 };
@@ -59,12 +60,15 @@ __device__ __forceinline__ Spot spot_of(const QkPlan& P) {
   s.split = P.halves && s.p0 < P.half;
   s.off[0] = s.split ? s.p0 : 2 * s.p0;
   s.off[1] = s.split ? s.p0 + P.half : 2 * s.p0 + 8;
+  s.live = 2 * s.p0 < P.D;
   s.fast = s.split ? s.p0 + 8 <= P.half : 2 * s.p0 + 16 <= P.D;
+  if (!s.live) s.off[0] = s.off[1] = 0;  // (loaded, not used)
   return s;
 }
 
-// The lane's pairs of a row as they are in memory: in the fast case one of the two
-// forms below, else element by element.
+// The lane's pairs of a row as they are in memory: in the fast case one of the two forms
+// below, else element by element; loads under a branch of the lane's own would be waited
+// for one by one. What a lane has not is zero.
 template <typename T, int MODE>
 struct Row {
   Raw8<T> r[2];
@@ -79,11 +83,11 @@ struct Row {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int d = channel(P, s.p0 + j, e);
-          slow[MODE == kMixed ? 2 * j + e : 0] = d < P.D ? row[d] : T{};
+          slow[MODE == kMixed ? 2 * j + e : 0] = row[d < P.D ? d : 0];
         }
     }
   }
-  __device__ __forceinline__ void get(const Spot& s, float (&a)[8], float (&b)[8]) const {
+  __device__ __forceinline__ void get(const QkPlan& P, const Spot& s, float (&a)[8], float (&b)[8]) const {
     float x[8], y[8];
     r[0].get(x);
     r[1].get(y);
@@ -97,15 +101,17 @@ struct Row {
         a[j] = na;
         b[j] = nb;
       } else {
-        a[j] = s.fast ? (s.split ? x[j] : na) : to_f32(slow[2 * j]);
-        b[j] = s.fast ? (s.split ? y[j] : nb) : to_f32(slow[2 * j + 1]);
+        a[j] = s.fast ? (s.split ? x[j] : na) : channel(P, s.p0 + j, 0) < P.D ? to_f32(slow[2 * j]) : 0.0f;
+        b[j] = s.fast ? (s.split ? y[j] : nb) : channel(P, s.p0 + j, 1) < P.D ? to_f32(slow[2 * j + 1]) : 0.0f;
       }
+      if (MODE != kMixed && !s.live) a[j] = b[j] = 0.0f;
     }
   }
 };
 
 template <int MODE, typename T>
 __device__ __forceinline__ void put_row(T* row, const QkPlan& P, const Spot& s, const float (&a)[8], const float (&b)[8]) {
+  if (MODE != kMixed && !s.live) return;
   if (MODE != kMixed || s.fast) {
     float x[8], y[8];
 #pragma unroll
@@ -233,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkPlan P, Heads<const
         Row<T, MODE> row;
         float a[8], b[8];
         row.load(in.row(t0 + t, h), P, s);
-        row.get(s, a, b);
+        row.get(P, s, a, b);
         if (P.norm != DET_NORM_NONE) {
           float m = 0.0f;
 #pragma unroll
@@ -258,7 +264,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkPlan P, Heads<const
 }
 
 template <typename T, int MODE>
-__global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkPlan P, Heads<const T> dyq, Heads<const T> q, Heads<T> dq,
+__global__ __launch_bounds__(kThreads, MODE == kMixed ? 2 : 4) void qk_norm_bwd_kernel(QkPlan P, Heads<const T> dyq, Heads<const T> q, Heads<T> dq,
                                                                int Hq, const float* __restrict__ w_q, Heads<const T> dyk,
                                                                Heads<const T> k, Heads<T> dk, int Hk,
                                                                const float* __restrict__ w_k, float* __restrict__ slots) {
@@ -289,8 +295,8 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkPlan P, Heads<c
         float a[8], b[8], da[8], db[8];
         rx.load(in.row(t0 + t, h), P, s);
         rd.load(dy.row(t0 + t, h), P, s);
-        rx.get(s, a, b);
-        rd.get(s, da, db);
+        rx.get(P, s, a, b);
+        rd.get(P, s, da, db);
         if (s.p0 < P.half) turn_pairs(turns + t * row_pairs + s.p0, -1.0f, da, db);
         float r = 1.0f;
         if (P.norm != DET_NORM_NONE) {
@@ -376,26 +382,32 @@ int lanes_for(int64_t D) {
   while (16 * l < D) l *= 2;
   return l;
 }
-int64_t groups_for(int64_t T, int64_t tokens, bool bwd) {
-  const int64_t most = bwd ? 1024 : 4096, n = ceil_div(T, tokens);
-  return n < most ? n : most;
+// Workgroups: as many as are at work at once (the backward leaves a slot for each).
+int64_t most_groups(bool bwd) { return bwd ? 1024 : 4096; }
+// Tokens of a workgroup's turn: one round of its lanes at least while every compute unit has a
+// workgroup, up to four while there are 1024, and the same number of turns for all; their
+// sines have to fit. (8191 tokens of 18 heads, backward: one turn of 8 tokens for each of 1024
+// workgroups, all at work at once, 30 us; 1171 turns of 7 tokens, three workgroups to a compute
+// unit, 39 us.)
+int64_t tokens_for(int64_t T, int64_t D, int64_t heads, bool bwd) {
+  const int64_t rows = kThreads / lanes_for(D), room = kTurns / (8 * lanes_for(D));
+  const auto lower = [](int64_t a, int64_t b) { return a < b ? a : b; };
+  int64_t n = lower(ceil_div(4 * rows, heads), ceil_div(T, 1024));
+  const int64_t one = lower(rows / heads, T / 256);
+  n = lower(n > one ? n : one, room);
+  if (n < 1) n = 1;
+  const int64_t turns = ceil_div(ceil_div(T, n), most_groups(bwd));
+  return turns > 1 ? lower(n, ceil_div(T, most_groups(bwd) * turns)) : n;
 }
-// Tokens of a workgroup's turn: enough rows for two or more rounds of its lanes, as long
-// as half the compute units' workgroups remain, and their sines fit.
-int64_t tokens_for(int64_t T, int64_t D, int64_t heads) {
-  const int64_t rows = kThreads / lanes_for(D);
-  int64_t n = ceil_div(4 * rows, heads);
-  const int64_t few = T < 1024 ? 1 : T / 1024;
-  if (n > few) n = few;
-  const int64_t most = kTurns / (8 * lanes_for(D));
-  if (n > most) n = most;
-  return n < 1 ? 1 : n;
+int64_t groups_for(int64_t T, int64_t tokens, bool bwd) {
+  const int64_t n = ceil_div(T, tokens);
+  return n < most_groups(bwd) ? n : most_groups(bwd);
 }
 size_t ws_bytes_for(int64_t T, int64_t D, int64_t heads) {
   return T == 0 || D == 0 || heads == 0
              ? 0
              : DET_WS_HEADER_BYTES +
-                   align_up(static_cast<size_t>(groups_for(T, tokens_for(T, D, heads), true) * 2 * D) * 4, 256);
+                   align_up(static_cast<size_t>(groups_for(T, tokens_for(T, D, heads, true), true) * 2 * D) * 4, 256);
 }
 
 int check_sizes(const char* what, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R) {
@@ -409,7 +421,7 @@ int check_sizes(const char* what, int64_t T, int64_t Hq, int64_t Hk, int64_t D, 
 
 // The checks that both directions share, and the plan.
 int make_plan(const char* what, int dtype, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int norm, double eps, const int32_t* pos,
-              int64_t pos_ld, int64_t axes, const float* inv_freq, const int32_t* axis, int64_t R, int pairs, QkPlan& P) {
+              int64_t pos_ld, int64_t axes, const float* inv_freq, const int32_t* axis, int64_t R, int pairs, bool bwd, QkPlan& P) {
   if (int s = check_float_dtype(what, dtype)) return s;
   if (norm != DET_NORM_NONE && norm != DET_NORM_RMS && norm != DET_NORM_L2)
     return set_error(DET_ERR_INVALID_ARG, "%s: unknown norm %d", what, norm);
@@ -424,15 +436,15 @@ int make_plan(const char* what, int dtype, int64_t T, int64_t Hq, int64_t Hk, in
     if (axes > 1 && pos_ld > (int64_t(1) << 44) / axes) return set_error(DET_ERR_UNSUPPORTED, "%s: pos is too large", what);
   }
   const int lanes = lanes_for(D);
-  P = QkPlan{T, (int)D, (int)(R / 2), lanes, (int)tokens_for(T, D, Hq + Hk > 0 ? Hq + Hk : 1), kThreads / lanes, norm,
+  P = QkPlan{T, (int)D, (int)(R / 2), lanes, (int)tokens_for(T, D, Hq + Hk > 0 ? Hq + Hk : 1, bwd), kThreads / lanes, norm,
              pairs == DET_PAIRS_HALVES, past_caches(T * (Hq + Hk) * D * static_cast<int64_t>(dtype_size(dtype))),
              static_cast<float>(eps), norm == DET_NORM_RMS ? static_cast<float>(1.0 / (D > 0 ? D : 1)) : 1.0f,
              pos, axis, axes > 1 ? pos_ld : 0, (int)axes, inv_freq};
   return DET_OK;
 }
-// Whether every lane of a row owns runs of one kind, whole.
+// Whether every lane of a row owns runs of one kind, whole, if any.
 int mode_of(const QkPlan& P) {
-  if (P.D != 16 * P.lanes) return kMixed;
+  if (P.D % 16) return kMixed;
   if (P.halves && P.half) return 2 * P.half == P.D ? kHalves : kMixed;
   return kNeighbours;
 }
@@ -459,7 +471,7 @@ extern "C" int det_qk_norm(const void* q, int64_t q_st, int64_t q_sh, int64_t Hq
   const char* what = "qk_norm";
   if (int s = check_sizes(what, T, Hq, Hk, D, R)) return s;
   QkPlan P;
-  if (int s = make_plan(what, dtype, T, Hq, Hk, D, norm, eps, pos, pos_ld, axes, inv_freq, axis, R, pairs, P)) return s;
+  if (int s = make_plan(what, dtype, T, Hq, Hk, D, norm, eps, pos, pos_ld, axes, inv_freq, axis, R, pairs, false, P)) return s;
   if (T == 0 || D == 0 || Hq + Hk == 0) return ok();
   if ((Hq && (!q || !q_out)) || (Hk && (!k || !k_out))) return set_error(DET_ERR_INVALID_ARG, "%s: NULL pointer", what);
   const size_t es = dtype_size(dtype);
@@ -505,7 +517,7 @@ extern "C" int det_qk_norm_bwd(const void* dq_out, int64_t dqo_st, int64_t dqo_s
   const char* what = "qk_norm_bwd";
   if (int s = check_sizes(what, T, Hq, Hk, D, R)) return s;
   QkPlan P;
-  if (int s = make_plan(what, dtype, T, Hq, Hk, D, norm, eps, pos, pos_ld, axes, inv_freq, axis, R, pairs, P)) return s;
+  if (int s = make_plan(what, dtype, T, Hq, Hk, D, norm, eps, pos, pos_ld, axes, inv_freq, axis, R, pairs, true, P)) return s;
   if ((w_q != nullptr) != (dw_q != nullptr) || (w_k != nullptr) != (dw_k != nullptr))
     return set_error(DET_ERR_INVALID_ARG, "%s: w_q goes with dw_q, w_k with dw_k", what);
   if (T == 0 || D == 0 || Hq + Hk == 0) return ok();
