@@ -23,6 +23,11 @@
 // the next one's operand, and the other operands are fragments of 16 bytes per lane,
 // shared by the workgroup through LDS. What is not on the chain of states is formed
 // before it.
+//
+// 32768 tokens of one sequence, 32 heads of 128 x 128, bf16: 190 us for P and the inverses (2.8 TB/s
+// written) and 1130 us for the chains, 2.2 us a chunk, of which the 132 matrix instructions of the wave
+// that carries the state are 0.9 us. 16384 tokens of 8 sequences, with what the backward needs: 115 and
+// 508 us (0.94 GB written).
 #include "delta.hpp"
 
 namespace detgrad {
@@ -299,7 +304,7 @@ struct FwdArgs {
 //
 // TEAM: 16 columns and three waves. The first is left with the chain of states; the second forms
 // O, a chunk behind, from what that leaves in LDS of S0 and N; the third fetches. (A wave
-// that does all waits for its own loads to be taken: 3.2 us a chunk where the team needs 2.0.)
+// that does all of it waits for its loads to be taken: 5.8 us a chunk where the team needs 2.2.)
 //
 // The state goes from chunk to chunk as itself and as fragments, whose words are made
 // while the matrix instructions of the other half of it run.

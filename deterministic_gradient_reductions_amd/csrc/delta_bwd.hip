@@ -10,12 +10,17 @@
 //        and on the chunk's last row sum(K * dK1) + e^G_C <S0, dS1>
 //   dg = the sums of dG from a row to the chunk's end
 //
-// Nothing is divided by beta or by a decay. After the forward's preparing
-// kernels (with the transposes of P and the inverse) one walks a sequence's chunks backwards as the forward's
+// Nothing is divided by beta or by a decay. After the forward's preparing kernels (with the
+// transposes of P and the inverse) one walks a sequence's chunks backwards as the forward's
 // walks them (16 columns of v per wave, dS in registers): it writes dV, every chunk's
 // dS1, and dY as an image, as the forward left N. The last kernel takes all chunks side by
 // side: in it a wave owns tiles of token pairs first, then 16 channels of dQ and dK;
 // the pair matrices change hands in LDS.
+//
+// 16384 tokens in 8 sequences, 32 heads of 128 x 128, bf16: the chains 517 us, bound by memory
+// (0.94 GB written) while all run and by the longest one after; the last kernel 569 us for 1.7 GB read.
+// There N, dY and dO arrive before the pair tiles and the states' rows under them (643 -> 588 us),
+// and the next head's under the last products (569 us).
 #include "delta.hpp"
 
 namespace detgrad {
