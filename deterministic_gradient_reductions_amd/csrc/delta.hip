@@ -501,18 +501,25 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
 #pragma unroll
       for (int r = 0; r < 4; ++r) R[i][r] = __builtin_fmaf(-eg[r], ks0[i][r], R[i][r]);
     }
-    if (t0 + C < r1) next_v(t0 + C);
+    if (TEAM && t0 + C < r1) next_v(t0 + C);
     // N
-    f32x4 U[RT] = {}, nt[RT] = {};  // nt: N with rows v and columns t, for the backward
+    f32x4 U[RT] = {};
     static_for<KC>([&](auto kt) {
       const Frag<kW> fr = frag_of<kW>(R[2 * kt.value], R[2 * kt.value + 1]);
       Frag<kW> fi[RT];
 #pragma unroll
       for (int i = 2 * kt.value; i < RT; ++i) fi[i] = lds_frag<kW, kW>(img + nRows * 1024, lower_frag(i, kt.value));
       mm_tiles<kW, 2 * kt.value, RT>(U, fi, fr);
-      if (!TEAM && A.saved) mm_tiles<kOut, 2 * kt.value, RT, true>(nt, fi, fr);
     });
-    if (!TEAM && A.saved) put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
+    if (!TEAM) {
+      if (A.saved) {
+        f32x4 nt[RT];  // with rows v and columns t
+        lds_read();
+        turn_tiles<RT>(nt, U, lds + v_tile(0));
+        put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
+      }
+      if (t0 + C < r1) next_v(t0 + C);
+    }
     if (TEAM) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) *lds_tile(x + (KD * kOut + i) * 1024) = U[i];

@@ -373,6 +373,19 @@ __device__ __forceinline__ f32x4 lds_turned(const char* at) {
   return v;
 }
 
+// The tiles of a result with rows and columns changed, in 2048 bytes of this wave.
+template <int RT>
+__device__ __forceinline__ void turn_tiles(f32x4 (&y)[RT], const f32x4 (&x)[RT], char* scratch) {
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    char* tile = scratch + (i & 1) * 1024;
+    *lds_tile(tile) = x[i];
+    wave_fence();
+    y[i] = lds_turned(tile);
+    wave_fence();
+  }
+}
+
 // A [T, heads, dim] tensor with unit innermost stride.
 template <typename T>
 struct Heads {

@@ -248,14 +248,12 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
 #pragma unroll
       for (int i = 0; i < RT; ++i) dU[i] += x_p[i * 64];
     } else {
-      add_p(dU, img + oP * 1024);
-      if (ch > 0) {
-        lds_read();  // (this chunk's dO)
-        load_do(ch - 1);
-        fetch_do(ch - 1, 0);
-      }
+      f32x4 w[RT] = {};  // (summed by itself, as the team does)
+      add_p(w, img + oP * 1024);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) dU[i] += w[i];
     }
-    f32x4 dN[RT] = {}, yt[RT] = {};  // dY, and dY with rows v and columns t
+    f32x4 dN[RT] = {};  // dY
     static_for<KC>([&](auto kt) {
       constexpr int to = 2 * kt.value + 2;
       const Frag<kW> fu = frag_of<kW>(dU[2 * kt.value], dU[2 * kt.value + 1]);
@@ -263,14 +261,21 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
 #pragma unroll
       for (int j = 0; j < to; ++j) fi[j] = lds_frag<kW, kW>(img + nRows * 1024, upper_frag<KC>(j, kt.value));
       mm_tiles<kW, 0, to>(dN, fi, fu);
-      if (!TEAM) mm_tiles<kOut, 0, to, true>(yt, fi, fu);
     });
     const float el = gate[kEnd * C];
     if (TEAM) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) *lds_tile(x + i * 1024) = dN[i];
     } else {
+      f32x4 yt[RT];
+      lds_read();
+      turn_tiles<RT>(yt, dN, lds + o_tile(0));
       put_y(yt, gate, ch, unit);
+      if (ch > 0) {
+        lds_read();
+        load_do(ch - 1);
+        fetch_do(ch - 1, 0);
+      }
     }
 #pragma unroll
     for (int i = 0; i < RT; ++i) dN[i] *= gate4(gate, C, kEGBeta, rho(i, 4 * lg));
@@ -284,7 +289,10 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
 #pragma unroll
       for (int i = 0; i < DT; ++i) S[i] += x_q[i * 64];
     } else {
-      add_q(S, img + oQ * 1024, gate);
+      f32x4 w[DT] = {};
+      add_q(w, img + oQ * 1024, gate);
+#pragma unroll
+      for (int i = 0; i < DT; ++i) S[i] += w[i];
     }
     next_state<kIn, KC>(S, f, img, fn, 1.0f);
     if (!TEAM) fetch_done();

@@ -576,9 +576,10 @@ int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t dh
  * words (24 bits), the rest of a DET_BF16 call in two. Any g is allowed; below -1e4
  * it counts as -1e4 (a decay of 0 either way), -inf included. The recurrence is as
  * stable as its decays and keys are: with g <= 0, keys of length at most 1 and beta
- * in [0, 2] no intermediate grows. NaN and infinities spread to what they touch
- * (and to the rest of their chunk). Every sum has one order: the same bits from run
- * to run.
+ * in [0, 2] no intermediate grows. NaN and infinities (float32 values above 3.38e38
+ * among them) spread to what they touch and to the rest of their chunk. Every sum has
+ * one order: the same bits from run to run, and for a sequence whatever others the
+ * call holds.
  *
  * q, k: [T, Hk, dk], v, o: [T, H, dv] of dtype (DET_BF16 or DET_F32), strides of
  *       tokens (_st) and heads (_sh) in elements: whole tokens that do not overlap

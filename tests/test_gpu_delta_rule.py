@@ -122,6 +122,73 @@ def test_many_sequences():
     check(500, [0] + offs, 1, 1, 32, 32, F32, seed=3)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hk,H,dk,dv,extra", [(3, 6, 128, 128, 0), (6, 6, 64, 64, 0), (2, 6, 100, 90, 0), (6, 6, 64, 128, 5), (6, 6, 128, 50, 0)])
+def test_many_chains(Hk, H, dk, dv, extra, dtype):
+    """More sequences and heads than take the form for few."""
+    offs = [0, 0, 1, 65, 66, 130, 197, 240, 241, 300, 330, 331, 333, 395, 400, 470]
+    check(475, offs, Hk, H, dk, dv, dtype, extra=extra, seed=dk)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv,extra", [(128, 128, 0), (64, 50, 3)])
+def test_both_forms_give_the_same_bits(dk, dv, extra, dtype):
+    """Each sequence alone (few chains) gives its rows of a packed call of many."""
+    offs = [0, 150, 150, 214, 300, 301, 330, 400, 401, 402, 430]
+    h = make(430, offs, 9, 9, dk, dv, dtype, seed=12)
+    d = to_dev(h, extra)
+    f = fwd(d)
+    r = bwd(d, f)
+    for s in (0, 1, 3, 4, 6):
+        a, b = offs[s:s + 2]
+        e = {n: x[a:b] for n, x in d.items() if n in X + ("do",)}
+        e.update(offs=torch.tensor([0, b - a], dtype=torch.int32).cuda(), s0=d["s0"][s:s + 1].contiguous(),
+                 ds1=d["ds1"][s:s + 1].contiguous())
+        g = fwd(e)
+        q = bwd(e, g)
+        assert torch.equal(g["o"], f["o"][a:b]) and torch.equal(g["s1"][0], f["s1"][s]), s
+        for n in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert torch.equal(q[n], r[n][a:b]), (s, n)
+        assert torch.equal(q["ds0"][0], r["ds0"][s]), s
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H", [2, 90])
+def test_values_at_any_place(H, dtype):
+    """Rows of v and do whose starts or strides are not whole 16 bytes, and tokens far apart, give the same bits."""
+    h = make(140, [0, 75, 140], H, H, 64, 48, dtype, seed=13)
+    d = to_dev(h)
+    f = fwd(d)
+    r = bwd(d, f)
+
+    def wide(x):
+        y = torch.zeros((140, 1 << 18), dtype=x.dtype, device="cuda")[:, 8:8 + x[0].numel()].unflatten(1, x.shape[1:])
+        return y.copy_(x)
+    for e in (dict(d, v=spaced(h["v"], 3), do=spaced(h["do"], 5)), dict(d, q=wide(d["q"]), k=wide(d["k"]), v=wide(d["v"]), do=wide(d["do"]))):
+        g = fwd(e, out=dict(f, o=spaced(torch.full_like(h["v"], 7.0), 1), s1=f["s1"].clone(), states=f["states"].clone()))
+        assert torch.equal(g["o"], f["o"]) and torch.equal(g["s1"], f["s1"])
+        for n, x in bwd(e, g).items():
+            assert torch.equal(x, r[n]), n
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_offsets_past_32_bits(dtype):
+    """Tokens 2^24 elements and more apart: the last ones lie past 2^32 bytes."""
+    T, H = 140 if dtype == BF else 70, 2
+    h = make(T, [0, T], 1, H, 64, 64, dtype, seed=14)
+    d = to_dev(h)
+    f = fwd(d)
+    r = bwd(d, f)
+
+    def far(x, extra=8):
+        return torch.empty((T, (1 << 24) + extra), dtype=x.dtype, device="cuda")[:, :x[0].numel()].unflatten(1, x.shape[1:])
+    e = dict(d, **{n: far(d[n]).copy_(d[n]) for n in ("q", "k", "v", "do")})
+    g = fwd(e, out=dict(f, o=far(d["v"]), s1=f["s1"].clone(), states=f["states"].clone()))
+    assert torch.equal(g["o"], f["o"]) and torch.equal(g["s1"], f["s1"])
+    for n, x in bwd(e, g, out=dict(r, dq=far(d["q"]), dk=far(d["k"]), dv=far(d["v"]))).items():
+        assert torch.equal(x, r[n]), n
+
+
 def test_no_tokens():
     d, f = check(0, [0, 0, 0], 1, 2, 16, 16, F32)
     assert torch.equal(f["s1"], d["s0"])
