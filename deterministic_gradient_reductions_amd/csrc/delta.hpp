@@ -362,17 +362,20 @@ __device__ __forceinline__ f32x4 gate4(const float* gate, int C, int row, int at
   return *reinterpret_cast<const f32x4*>(gate + row * C + at);
 }
 
-// A result tile (rows 4 g + r, column c) in 1024 bytes of LDS, and back with rows and columns changed.
-__device__ __forceinline__ f32x4* lds_tile(char* at) { return reinterpret_cast<f32x4*>(at) + (threadIdx.x & 63); }
+// A result tile (rows 4 g + r, column c) in 1024 bytes of LDS, and back with rows and columns changed;
+// lane 16 g + c at place 16 g + (c ^ g), so that the latter reads every bank once.
+__device__ __forceinline__ f32x4* lds_tile(char* at) {
+  const int lane = threadIdx.x & 63;
+  return reinterpret_cast<f32x4*>(at) + (lane ^ (lane >> 4));
+}
 __device__ __forceinline__ f32x4 lds_turned(const char* at) {
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const char* p = at + (16 * (c >> 2) + 4 * g) * 16 + (c & 3) * 4;
   f32x4 v;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) v[r] = *reinterpret_cast<const float*>(p + 16 * r);
+  for (int r = 0; r < 4; ++r) v[r] = *reinterpret_cast<const float*>(p + 16 * (r ^ (c >> 2)));
   return v;
 }
-
 // The tiles of a result with rows and columns changed, in 2048 bytes of this wave.
 template <int RT>
 __device__ __forceinline__ void turn_tiles(f32x4 (&y)[RT], const f32x4 (&x)[RT], char* scratch) {

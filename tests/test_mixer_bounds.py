@@ -152,10 +152,11 @@ def test_turned_tile():
     """lds_tile, lds_turned: a result tile back with rows and columns changed."""
     tile = np.zeros(256, np.int64)
     for r in range(4):
-        tile[LANE * 4 + r] = (4 * G + r) * 16 + C
+        tile[(LANE ^ (LANE >> 4)) * 4 + r] = (4 * G + r) * 16 + C
     for r in range(4):
-        at = (16 * (C >> 2) + 4 * G) * 16 + (C & 3) * 4 + 16 * r
+        at = (16 * (C >> 2) + 4 * G) * 16 + (C & 3) * 4 + 16 * (r ^ (C >> 2))
         assert np.array_equal(tile[at // 4], C * 16 + 4 * G + r)
+        assert sorted(at // 4 % 64) == list(range(64))   # every bank once
 
 
 @pytest.mark.parametrize("RT,kv,NP", [(4, 4, 2), (4, 2, 2), (2, 4, 3), (2, 2, 3)])
