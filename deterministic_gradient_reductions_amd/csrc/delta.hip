@@ -34,36 +34,46 @@ namespace detgrad {
 namespace {
 
 // ------------------------------------------------------------------------------- copy
-// Workgroup (tile, head): the chunk's rows of x in padded words.
-template <typename T, int DIM>
-__global__ __launch_bounds__(256) void delta_copy_kernel(DeltaSizes z, Heads<const T> x, int heads, int dim,
-                                                         uint16_t* __restrict__ rows) {
-  constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
+// Up to three tensors of a call that the kernels cannot read as they are.
+template <typename T>
+struct Copies {
+  Heads<const T> x[3];
+  uint16_t* rows[3];
+  int heads[3], dim[3], pad[3], n;
+};
+// Workgroup (tile, head, tensor): the chunk's rows in padded words. (One launch for all of them: a
+// launch is 6 us where there is little to copy.)
+template <typename T>
+__global__ __launch_bounds__(256) void delta_copy_kernel(DeltaSizes z, Copies<T> A) {
+  constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC, kEach = 2;
   const uint32_t tile = blockIdx.x;
-  const int h = blockIdx.y;
+  const int h = blockIdx.y, heads = A.heads[blockIdx.z], dim = A.dim[blockIdx.z], pad = A.pad[blockIdx.z];
+  const Heads<const T> x = A.x[blockIdx.z];
+  uint16_t* rows = A.rows[blockIdx.z];
   int e;
   uint32_t r0, r1, s0, s1;
-  if (!segment_tile<1>(z.offs, z.S, static_cast<uint32_t>(z.T), kLogC, tile, e, r0, r1, s0, s1)) return;
-  const int n = static_cast<int>(r1 - r0);
+  if (h >= heads || !segment_tile<1>(z.offs, z.S, static_cast<uint32_t>(z.T), kLogC, tile, e, r0, r1, s0, s1)) return;
+  const int n = static_cast<int>(r1 - r0), log_row = pad == 64 ? 4 : 5;  // of groups of four channels
   const bool whole = dim % 4 == 0;
-  constexpr int kEach = C * DIM / 4 / 256;
-  f32x4 v[kEach];
+  for (int id0 = threadIdx.x; id0 < C << log_row; id0 += kEach * 256) {
+    f32x4 v[kEach];
 #pragma unroll
-  for (int u = 0; u < kEach; ++u) {
-    const int id = threadIdx.x + u * 256, t = id / (DIM / 4), d = id % (DIM / 4) * 4;
-    v[u] = load4(x.row(r0 + (t < n ? t : 0), h), d, dim, whole);
-  }
+    for (int u = 0; u < kEach; ++u) {
+      const int t = (id0 + u * 256) >> log_row, d = 4 * ((id0 + u * 256) & ((1 << log_row) - 1));
+      v[u] = load4(x.row(r0 + (t < n ? t : 0), h), d, dim, whole);
+    }
 #pragma unroll
-  for (int u = 0; u < kEach; ++u) {
-    const int id = threadIdx.x + u * 256, t = id / (DIM / 4), d = id % (DIM / 4) * 4;
-    if (t >= n) continue;
-    uint32_t a[kIn], b[kIn];
-    split2<kIn>(v[u][0], v[u][1], a);
-    split2<kIn>(v[u][2], v[u][3], b);
+    for (int u = 0; u < kEach; ++u) {
+      const int t = (id0 + u * 256) >> log_row, d = 4 * ((id0 + u * 256) & ((1 << log_row) - 1));
+      if (t >= n) continue;
+      uint32_t a[kIn], b[kIn];
+      split2<kIn>(v[u][0], v[u][1], a);
+      split2<kIn>(v[u][2], v[u][3], b);
 #pragma unroll
-    for (int p = 0; p < kIn; ++p) {
-      const uint64_t w = a[p] | static_cast<uint64_t>(b[p]) << 32;
-      __builtin_memcpy(rows + ((static_cast<int64_t>(r0 + t) * heads + h) * kIn + p) * DIM + d, &w, 8);
+      for (int p = 0; p < kIn; ++p) {
+        const uint64_t w = a[p] | static_cast<uint64_t>(b[p]) << 32;
+        __builtin_memcpy(rows + ((static_cast<int64_t>(r0 + t) * heads + h) * kIn + p) * pad + d, &w, 8);
+      }
     }
   }
 }
@@ -553,15 +563,16 @@ bool as_it_is(const void* p, int64_t st, int64_t sh, int64_t dim) {
   return dim == delta_pad(dim) && aligned(p, 16) && st % 8 == 0 && sh % 8 == 0 && st < (1 << 24);
 }
 
+// The rows of a tensor, from a copy that joins `all` where need be.
 template <typename T>
-Rows rows_of(const DeltaSizes& z, int dtype, const void* x, int64_t x_st, int64_t x_sh, int heads, int dim, uint16_t* copy,
-             hipStream_t st) {
+Rows rows_of(Copies<T>& all, int dtype, const void* x, int64_t x_st, int64_t x_sh, int heads, int dim, uint16_t* copy) {
   if (sizeof(T) == 2 && as_it_is(x, x_st, x_sh, dim)) return {static_cast<const uint16_t*>(x), x_st, x_sh, 0};
-  const Heads<const T> h{static_cast<const T*>(x), x_st, x_sh};
-  const dim3 grid(static_cast<uint32_t>(delta_tiles(z.T, z.S, dtype)), static_cast<uint32_t>(heads));
-  if (dim <= 64) hipLaunchKernelGGL((delta_copy_kernel<T, 64>), grid, dim3(256), 0, st, z, h, heads, dim, copy);
-  else hipLaunchKernelGGL((delta_copy_kernel<T, 128>), grid, dim3(256), 0, st, z, h, heads, dim, copy);
-  const int pad = delta_pad(dim), words = delta_words(dtype);
+  const int pad = delta_pad(dim), words = delta_words(dtype), i = all.n++;
+  all.x[i] = {static_cast<const T*>(x), x_st, x_sh};
+  all.rows[i] = copy;
+  all.heads[i] = heads;
+  all.dim[i] = dim;
+  all.pad[i] = pad;
   return {copy, static_cast<int64_t>(heads) * words * pad, static_cast<int64_t>(words) * pad, pad};
 }
 
@@ -583,9 +594,14 @@ DeltaPrepared prepare(const DeltaSizes& z, int dtype, bool bwd, const void* q, i
                       const void* beta, int64_t beta_ld, char* ws, const DeltaLayout& l, hipStream_t st) {
   const auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(ws + o); };
   DeltaPrepared r{};
-  r.k = rows_of<T>(z, dtype, k, k_st, k_sh, z.Hk, z.dk, at(l.k_rows), st);
-  r.q = rows_of<T>(z, dtype, q, q_st, q_sh, z.Hk, z.dk, at(l.q_rows), st);
-  if (bwd) r.d_o = rows_of<T>(z, dtype, d_o, do_st, do_sh, z.H, z.dv, at(l.o_rows), st);
+  Copies<T> all{};
+  r.k = rows_of<T>(all, dtype, k, k_st, k_sh, z.Hk, z.dk, at(l.k_rows));
+  r.q = rows_of<T>(all, dtype, q, q_st, q_sh, z.Hk, z.dk, at(l.q_rows));
+  if (bwd) r.d_o = rows_of<T>(all, dtype, d_o, do_st, do_sh, z.H, z.dv, at(l.o_rows));
+  if (all.n) {
+    const dim3 grid(static_cast<uint32_t>(delta_tiles(z.T, z.S, dtype)), static_cast<uint32_t>(bwd ? z.H : z.Hk), static_cast<uint32_t>(all.n));
+    hipLaunchKernelGGL(delta_copy_kernel<T>, grid, dim3(256), 0, st, z, all);
+  }
   const int64_t units = delta_tiles(z.T, z.S, dtype) * z.H;
   if (z.dk <= 64) launch_prep<T, 64>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, at(l.units), units, st);
   else launch_prep<T, 128>(z, bwd, r.k, r.q, g, g_ld, beta, beta_ld, at(l.units), units, st);
