@@ -79,14 +79,6 @@ __device__ __forceinline__ void mm_tiles(f32x4 (&acc)[N], const Frag<NA> (&a)[N]
                         : __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t].w[i], b.w[s - i], acc[t], 0, 0, 0);
 }
 
-template <int NP>
-__device__ __forceinline__ void split(float x, __bf16 (&w)[NP]) {
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    w[p] = static_cast<__bf16>(x);
-    if (p + 1 < NP) x -= static_cast<float>(w[p]);
-  }
-}
 // The words of two values side by side (one conversion instruction for both; taking a word from
 // its value with the dot product instruction instead of unpacking it was slower: 572 for 507 us).
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -142,15 +134,7 @@ __device__ __forceinline__ V load_at(const void* base, uint32_t off) {
 
 // Images: fragments one after the other, each NP words of 64 lanes of 16 bytes.
 constexpr int kFragElems = 64 * 8;
-template <int NP, int STORED>
-__device__ __forceinline__ Frag<NP> image_frag(const uint16_t* image, int f) {
-  static_assert(NP <= STORED, "more words than the image has");
-  Frag<NP> r;
-#pragma unroll
-  for (int p = 0; p < NP; ++p) r.w[p] = load_at<bf16x8>(image + (f * STORED + p) * kFragElems, (threadIdx.x & 63) * 16);
-  return r;
-}
-// The same from LDS.
+// One of them, its first NP words, from LDS.
 template <int NP, int STORED>
 __device__ __forceinline__ Frag<NP> lds_frag(const char* image, int f) {
   static_assert(NP <= STORED, "more words than the image has");

@@ -286,6 +286,32 @@ def test_nan_stays_in_its_sequence_and_head():
         assert torch.equal(o[90:], f["o"][90:]) and torch.equal(o[:, 0], f["o"][:, 0]), name
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H", [2, 45])
+def test_nan_outside_the_sequences_and_in_another(H, dtype):
+    """What lies in front of, behind and in other sequences or heads changes no bit, in either form of the chains."""
+    h = make(230, [7, 90, 200], H, H, 64, 48, dtype, seed=15)
+    d = to_dev(h)
+    f = fwd(d)
+    r = bwd(d, f)
+    e = {n: x.clone() if torch.is_tensor(x) else x for n, x in d.items()}
+    for name in ("q", "k", "v", "g", "beta", "do"):
+        e[name][:7] = math.nan
+        e[name][200:] = math.inf
+    f2 = fwd(e)
+    r2 = bwd(e, f2)
+    for x, y in zip([f["o"], f["s1"]] + list(r.values()), [f2["o"], f2["s1"]] + list(r2.values())):
+        assert torch.equal(x, y)
+    e["v"][40, 1] = math.nan
+    e["do"][50, 1] = math.inf
+    f2 = fwd(e)
+    r2 = bwd(e, f2)
+    assert torch.isnan(f2["o"][40:90, 1]).all() and torch.equal(f2["o"][90:], f["o"][90:]) and torch.equal(f2["o"][:, 0], f["o"][:, 0])
+    assert torch.equal(f2["s1"][1], f["s1"][1]) and torch.equal(f2["s1"][0, 0], f["s1"][0, 0])
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(r2[n][90:], r[n][90:]) and torch.equal(r2[n][:, 0], r[n][:, 0]), n
+
+
 def test_gradients_against_differences():
     """Central differences of sum(o do) + sum(s1 ds1) of the kernels along random directions. Their step's own error is
     what the float64 differences of the same step are off; each of the two values has rounding errors of at most
