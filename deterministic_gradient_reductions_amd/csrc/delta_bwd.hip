@@ -18,7 +18,7 @@
 // the pair matrices change hands in LDS.
 //
 // 16384 tokens in 8 sequences, 32 heads of 128 x 128, bf16: the chains 430 to 570 us, bound by memory
-// (0.94 GB written) while all run and by the longest one after; the last kernel 570 us for 1.7 GB read.
+// (0.94 GB written) while all run and by the longest one after; the last kernel 560 us for 1.7 GB read.
 // There N, dY and dO arrive before the pair tiles and the states' rows under them (643 -> 588 us),
 // and the next head's under the last products (569 us).
 #include "delta.hpp"
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
     // the states' rows of this wave's channels, for the second phase
     const int d = rho(wave, c);
     f32x4 xs[KV][2], xd[KV][2];
-    if (wave < DT) {
+    if (DT == NW || wave < DT) {
       // (every load stays in its block; what lies behind dk or dv is masked below)
 #pragma unroll
       for (int kv = 0; kv < KV; ++kv) {
@@ -448,7 +448,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
     __syncthreads();
 
     // 16 channels of dq and dk
-    if (wave < DT) {
+    if (DT == NW || wave < DT) {
       f32x4 a[RT] = {}, b[RT] = {}, s[RT] = {};
       float inner = 0.0f, w_sum = 0.0f;
 #pragma unroll
@@ -517,7 +517,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
     }
     __syncthreads();  // N, dY and dO have been read
     if (h + 1 < h0 + group) fetch_head(h + 1, (h + 1 - h0) & 1);
-    if (wave < DT) {
+    if (DT == NW || wave < DT) {
       static_for<KC>([&](auto kt) {
         constexpr int at = kt.value;
         const Frag<kIn> kT = turned_frag<KD, kIn>(lds, wave, at), qT = turned_frag<KD, kIn>(lds + oQ * 1024, wave, at);
@@ -570,7 +570,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
       }
     }
   }
-  if (wave_ < DT) {
+  if (DT == NW || wave_ < DT) {
     const int lane = threadIdx.x & 63, n = static_cast<int>(t1 - t0);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
