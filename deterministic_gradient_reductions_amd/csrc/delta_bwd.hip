@@ -18,9 +18,9 @@
 // the pair matrices change hands in LDS.
 //
 // 16384 tokens in 8 sequences, 32 heads of 128 x 128, bf16: the chains 430 to 570 us, bound by memory
-// (0.94 GB written) while all run and by the longest one after; the last kernel 560 us for 1.7 GB read.
+// (0.94 GB written) while all run and by the longest one after; the last kernel 560 to 600 us for 1.7 GB read.
 // There N, dY and dO arrive before the pair tiles and the states' rows under them (643 -> 588 us),
-// and the next head's under the last products (569 us).
+// and the next head's under the last products (-> 569 us).
 #include "delta.hpp"
 
 namespace detgrad {
