@@ -6,9 +6,13 @@
 //   dS0 = e^G_C dS1 + scale (e^G Q)^T dO - (e^G K)^T dN
 //   dQ = dQ1 + scale (dP * D) K,       dQ1 = scale e^G dO S0^T
 //   dK = dK1 - dK0 + scale (dP * D)^T Q + (Z + Z^T) K,   dK1 = e^(G_C - G) U dS1^T,  dK0 = e^G dN S0^T,  Z = -D * X * beta_col
-//   dG = rowsum(E) - colsum(E) + rowsum(Q * dQ1 - K * dK0 - K * dK1),   E = dP * P - M * X * beta_col
-//        and on the chunk's last row sum(K * dK1) + e^G_C <S0, dS1>
-//   dg = the sums of dG from a row to the chunk's end
+//   dg_t = sum_{i >= t > j} E_ij + sum_{i >= t} (q_i dQ1_i - k_i dK0_i) + sum_{j < t} k_j dK1_j + e^G_C <S0, dS1>,
+//          E = dP * P - M * X * beta_col
+//
+// Every term of dg_t has e^g_t as a factor, since the decays between its two tokens (or states) pass t, so dg keeps its
+// digits relative to itself however fast a head forgets. (As the sums from t on of what each row of G takes up, E's
+// row sum less its column sum and so on, it is terms without that factor which cancel: what float32 leaves
+// of them was more than dg from g of about -8 on.)
 //
 // Nothing is divided by beta or by a decay. After the forward's preparing kernels (with the
 // transposes of P and the inverse) one walks a sequence's chunks backwards as the forward's
@@ -306,8 +310,8 @@ struct GradArgs {
   Heads<T> dq, dk;
   T *dg, *dbeta;
   const uint16_t *dy, *units;
-  const float *g, *saved, *ds;
-  int64_t g_ld, dg_ld, dbeta_ld;
+  const float *saved, *ds;
+  int64_t dg_ld, dbeta_ld;
   int image_floats, saved_floats, ds_floats;
 };
 
@@ -333,8 +337,11 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
                 nGate = Unit<T, true>::nGate;
   constexpr int oQ = nK, oO = 2 * nK, oN = oO + nO, oY = oN + nV, oA = oY + nV, oZ = oA + nTri, oGate = oZ + nTri;
   __shared__ __align__(16) char lds[(oGate + 2 * nGate) * 1024];
-  __shared__ float red_q[NW][C], red_s[NW], red_w[NW], diag[C];
-  __shared__ float row_e[RT][RT][16], col_e[RT][RT][16];
+  __shared__ float red_q[NW][C], red_w[NW][C], red_s[NW], diag[C];
+  // E's sums over four columns j from 4 m on, per row (padded: rows start on banks of their own); its crossing sums with
+  // j in t's own four, per row tile; and with j before them
+  constexpr int kRuns = C / 4, kRunLd = kRuns + 4;
+  __shared__ __align__(16) float run_e[C][kRunLd], near_e[RT][C], far_e[C];
   char *img_a = lds + oA * 1024, *img_z = lds + oZ * 1024;
   const uint32_t lds0 = lds_address(lds);
   const int wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -421,16 +428,16 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
         const float dp = in ? b[r] * y[r] * dc * z.scale : 0.0f, bx = off ? b[r] * bi * x[r] * dc : 0.0f;
         pd[r] = dp;
         zz[r] = -bx;
-        ev[r] = dp * qk[m][r] - bx * kk[m][r];
+        ev[r] = off ? dp * qk[m][r] - bx * kk[m][r] : 0.0f;  // (no token's pair with itself crosses a t)
       }
-      // sums over j (rows of the tile) for row i, over i (its columns) for row j
-      const Halves s16 = halves16((ev[0] + ev[1]) + (ev[2] + ev[3]));
-      const Halves s32 = halves32(s16.a + s16.b);
-      if (lg == 0) row_e[i][j][c] = s32.a + s32.b;
+      // a lane's four columns j are one run: t behind them takes them all, t among them those before it
+      run_e[row][at0 >> 2] = (ev[0] + ev[1]) + (ev[2] + ev[3]);
+      float before = ev[0];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float ce = row16_tree(ev[r]);
-        if (c == 0) col_e[i][j][4 * lg + r] = ce;
+      for (int r = 1; r < 4; ++r) {
+        const float ne = row16_tree(row >= at0 + r ? before : 0.0f);
+        if (c == 0) near_e[i][at0 + r] = ne;
+        before += ev[r];
       }
       // dP * D and Z as images of rows i and places j: row tile i, row c, places at0 .. of fragment j / 2
       const int to = lower_frag(i, j >> 1) * kW * 1024 + row_place() * 16 + (j & 1) * 8;
@@ -447,10 +454,26 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
     });
     __syncthreads();
 
+    // E's crossing sums for the t of a run, a lane per row i: its runs before that one, summed over the rows from t on
+    for (int m = wave; m < kRuns; m += NW) {
+      float p = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kRuns; u += 4) {
+        const f32x4 w = *reinterpret_cast<const f32x4*>(&run_e[lane & (C - 1)][u]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p += u + r < m ? w[r] : 0.0f;
+      }
+      f32x4 t;
+      t[3] = lanes_sum<64>(lane >= 4 * m + 4 && lane < C ? p : 0.0f);
+#pragma unroll
+      for (int r = 3; r >= 0; --r) t[r] = (r < 3 ? t[r + 1] : t[3]) + readlane(p, 4 * m + r);
+      if (lane == 0) *reinterpret_cast<f32x4*>(&far_e[4 * m]) = t;
+    }
+
     // 16 channels of dq and dk
     if (DT == NW || wave < DT) {
       f32x4 a[RT] = {}, b[RT] = {}, s[RT] = {};
-      float inner = 0.0f, w_sum = 0.0f;
+      float inner = 0.0f;
 #pragma unroll
       for (int kv = 0; kv < KV; ++kv) {
 #pragma unroll
@@ -494,26 +517,24 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
             k[r] += static_cast<float>(wk[r]);
           }
         }
-        // this wave's part of Q * dQ1 - K * dK0 - K * dK1 (tokens past the end: K stands for another's, but a, b, s are 0)
-        float dot = 0.0f;
+        // this wave's part of Q * dQ1 - K * dK0 and of K * dK1 (tokens past the end: K stands for another's, but a, b, s are 0)
+        float dot = 0.0f, dot_w = 0.0f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float ks = k[r] * s[i][r];
-          w_sum += ks;
-          dot += __builtin_fmaf(q[r], a[i][r], -__builtin_fmaf(k[r], b[i][r], ks));
+          dot_w = __builtin_fmaf(k[r], s[i][r], dot_w);
+          dot += __builtin_fmaf(q[r], a[i][r], -(k[r] * b[i][r]));
         }
-        const Halves h16 = halves16(dot);
-        const Halves h32 = halves32(h16.a + h16.b);
-        if (lg == 0) red_q[wave][t] = h32.a + h32.b;
+        const Halves h16 = halves16(dot), w16 = halves16(dot_w);
+        const Halves h32 = halves32(h16.a + h16.b), w32 = halves32(w16.a + w16.b);
+        if (lg == 0) {
+          red_q[wave][t] = h32.a + h32.b;
+          red_w[wave][t] = w32.a + w32.b;
+        }
         dk[i] += s[i] - b[i];
         dq[i] += a[i];
       }
       inner = lanes_sum<64>(inner);
-      w_sum = lanes_sum<64>(w_sum);
-      if (lane == 0) {
-        red_s[wave] = inner;
-        red_w[wave] = w_sum;
-      }
+      if (lane == 0) red_s[wave] = inner;
     }
     __syncthreads();  // N, dY and dO have been read
     if (h + 1 < h0 + group) fetch_head(h + 1, (h + 1 - h0) & 1);
@@ -542,30 +563,29 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
 
     // dbeta and dg, by the first wave: a lane per token
     if (wave == 0) {
-      const int t = lane < C ? lane : 0, rt = rho_tile(t), x = rho_row(t);
-      float w = 0.0f, dG = 0.0f, inner = 0.0f;
+      const int t = lane < C ? lane : 0, rt = rho_tile(t);
+      float q = 0.0f, w = 0.0f, inner = 0.0f, ce = far_e[t];
 #pragma unroll
       for (int i = 0; i < DT; ++i) {
-        dG += red_q[i][t];
-        w += red_w[i];
+        q += red_q[i][t];
+        w += red_w[i][t];
         inner += red_s[i];
       }
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        if (j / 2 <= rt / 2) dG += row_e[rt][j][x];
-        if (j / 2 >= rt / 2) dG -= col_e[j][rt][x];
-      }
-      // the sums from a row to the end, in float64
-      double sum = lane < n ? static_cast<double>(dG) : 0.0;
-      if (lane == C - 1) sum += w + static_cast<double>(gate[kEnd * C]) * inner;
+      for (int i = 0; i < RT; ++i)
+        if (i / 2 >= rt / 2 && (t & 3)) ce += near_e[i][t];
+      // the rows' sums from t to the end, and those before t (taking a row off a sum with it would not leave them), in float64
+      const float w0 = __shfl_up(w, 1);
+      double from = lane < n ? static_cast<double>(q) : 0.0, to = lane > 0 && lane < n ? static_cast<double>(w0) : 0.0;
 #pragma unroll
       for (int o = 1; o < C; o <<= 1) {
-        const double other = __shfl_down(sum, o);
-        if (lane + o < C) sum += other;
+        const double f = __shfl_down(from, o), g = __shfl_up(to, o);
+        if (lane + o < C) from += f;
+        if (lane >= o) to += g;
       }
       if (lane < n) {
-        const bool cut = A.g[(t0 + t) * A.g_ld + h] < -104.0f;
-        A.dg[(t0 + t) * A.dg_ld + h] = from_f32<T>(cut ? 0.0f : static_cast<float>(sum));
+        const double dg = from + to + ce + static_cast<double>(gate[kEnd * C]) * inner;
+        A.dg[(t0 + t) * A.dg_ld + h] = from_f32<T>(static_cast<float>(dg));
         A.dbeta[(t0 + t) * A.dbeta_ld + h] = from_f32<T>(diag[t]);
       }
     }
@@ -671,7 +691,7 @@ extern "C" int det_delta_rule_bwd(const void* d_o, int64_t do_st, int64_t do_sh,
                          words(l.dy), block};                                                                          \
     const GradArgs<E> B{r.k, r.q, r.d_o, {static_cast<E*>(dq), dq_st, dq_sh},                                          \
                         {static_cast<E*>(dk_out), dk_st, dk_sh}, static_cast<E*>(dg), static_cast<E*>(dbeta),          \
-                        words(l.dy), words(l.units), g, states, ds, g_ld, dg_ld, dbeta_ld,  \
+                        words(l.dy), words(l.units), states, ds, dg_ld, dbeta_ld,           \
                         image, saved, block};                                                                          \
     if (dk <= 64) launch_chain<E, 64>(z, A, st);                                                                       \
     else launch_chain<E, 128>(z, A, st);                                                                               \

@@ -606,8 +606,9 @@ int det_delta_rule(const void* q, int64_t q_st, int64_t q_sh, const void* k, int
  *
  * overwritten; rows behind the last sequence are left as they were. dq, dk, dv, dg
  * and dbeta are of dtype (dg is what det_colsum takes next to an a of that type),
- * dfinal_state and dinitial_state [S, H, dk, dv] float32. A token with g < -104, whose
- * decay is 0, has dg = 0. dg, dbeta: [T, H], row strides >= H.
+ * dfinal_state and dinitial_state [S, H, dk, dv] float32. Every term that a token's dg
+ * is summed from has the token's decay exp(g) as a factor: dg keeps its digits however small
+ * the decay, and is 0 where that is (g < -104). dg, dbeta: [T, H], row strides >= H.
  * ws: det_delta_rule_bwd_workspace_size() bytes; its header is neither read nor
  *     written. */
 int det_delta_rule_bwd_workspace_size(int64_t T, int64_t S, int64_t Hk, int64_t H, int64_t dk, int64_t dv, int dtype,

@@ -101,6 +101,39 @@ def delta_bwd(do, x, ds1, group):
     return r, mags
 
 
+# ------------------------------------------------------------- dg, token by token
+def delta_dg_mag(x, do, s0, ds1):
+    """dg's magnitude [T, H] from `x`, what delta() kept: dg of token t is <dS', exp(g) S> of the gradient and the state
+    on its two sides, and a chunk forms it as the sum of the products of what either is made of, each with the decays
+    between the two, that of t among them. By Cauchy-Schwarz these are at most the product of two sums of norms, of the
+    terms of S_{t-1} (the first state, k u^T with |u| <= beta (|v| + |k| |S'|)) and of dS'_t (the last gradient, scale
+    q do^T, k dN^T with |dN| <= beta |k| |dS|), each decayed up to its side of t."""
+    q, k, v, g, beta, scale = (x[n] for n in ("q", "k", "v", "g", "beta", "scale"))
+    T, H = v.shape[:2]
+    norm = lambda s: s.flatten(1).norm(dim=1)  # noqa: E731
+    zero = torch.zeros(H).double()
+    mag, before, sums, grads = torch.zeros(T, H).double(), {}, {}, {}
+    for s, t, st, kept, n, u in x["tape"]:
+        if s not in sums:
+            sums[s] = norm(s0[s].double()) if s0 is not None else zero
+        before[t] = g[t].exp() * sums[s]
+        un = beta[t] * (v[t].norm(dim=1) + k[t].norm(dim=1) * norm(kept))
+        sums[s] = before[t] + k[t].norm(dim=1) * un
+    ds = {}
+    for s, t, st, kept, n, u in reversed(x["tape"]):
+        if s not in ds:
+            ds[s] = ds1[s].double() if ds1 is not None else torch.zeros_like(st)
+            grads[s] = norm(ds[s])
+        d = ds[s] + scale * q[t][:, :, None] * do[t].double()[:, None, :]
+        kn = k[t].norm(dim=1)
+        after = grads[s] + abs(scale) * q[t].norm(dim=1) * do[t].double().norm(dim=1) + kn * beta[t] * kn * norm(d)
+        mag[t] = before[t] * after
+        grads[s] = g[t].exp() * after
+        d = d - k[t][:, :, None] * (beta[t][:, None] * (k[t][:, :, None] * d).sum(1))[:, None, :]
+        ds[s] = d * g[t].exp()[:, None, None]
+    return mag
+
+
 # ------------------------------------------------------------ query and key norms
 def turns(pos, inv_freq, axis):
     """cos and sin [T, 1, R / 2], from angles with 64 bits of fraction (the product of 31 and 24 bits, exactly); an axis
@@ -163,4 +196,4 @@ def qk_bwd(dy, x, w, norm, eps, cs, pairs):
     return dx, mag, (d * xh).sum((0, 1)), (dm * xh.abs()).sum((0, 1))
 
 
-__all__ = ["allowed", "assert_close", "bounds", "delta", "delta_bwd", "qk", "qk_bwd", "turn", "turn_mag", "turns"]
+__all__ = ["allowed", "assert_close", "bounds", "delta", "delta_bwd", "delta_dg_mag", "qk", "qk_bwd", "turn", "turn_mag", "turns"]
