@@ -90,7 +90,7 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSiz
                                                                      uint16_t* __restrict__ out, int64_t units) {
   constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC, RT = C / 16, KC = C / 32, KS = DK / 32;
   typedef Unit<T, BWD> Rec;
-  constexpr int kW = kStateWords, kP = Rec::kP;
+  constexpr int kW = kStateWords;
   constexpr int kLd = C + 4;  // 16-byte rows whose starts move through the banks
   __shared__ __align__(16) float lds[kPrepWaves][C * kLd + 3 * C];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
@@ -203,8 +203,8 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void delta_prep_kernel(DeltaSiz
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int m = 0; m < KC; ++m) {
-        if (BWD && m >= i / 2) image_put<kP>(to, upper_frag<KC>(i, m), frag_of<kP>(qk[2 * m][i], qk[2 * m + 1][i]));
-        if (!BWD && m <= i / 2) image_put<kP>(to, lower_frag(i, m), frag_of<kP>(qk[i][2 * m], qk[i][2 * m + 1]));
+        if (BWD && m >= i / 2) image_put<kW>(to, upper_frag<KC>(i, m), frag_of<kW>(qk[2 * m][i], qk[2 * m + 1][i]));
+        if (!BWD && m <= i / 2) image_put<kW>(to, lower_frag(i, m), frag_of<kW>(qk[i][2 * m], qk[i][2 * m + 1]));
       }
   }
   wave_fence();
@@ -321,11 +321,11 @@ struct FwdArgs {
 template <typename T, int DK, bool TEAM>
 __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T> A) {
   typedef Unit<T, false> Rec;
-  constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
+  constexpr int kIn = DeltaType<T>::kIn, kGrad = DeltaType<T>::kGrad, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
   constexpr int NW = TEAM ? 1 : 8;
   // fragments in LDS: two buffers of K, the inverse and the gates, Q and P; V of each wave (TEAM: two); S0 and N for the team
-  constexpr int nRows = RT * KD * kIn, nHead = Rec::oP, nP = Rec::nP, nX = KD * kOut + RT;
+  constexpr int nRows = RT * KD * kIn, nHead = Rec::oP, nP = Rec::nP, nX = KD * kW + RT;
   constexpr int oQ = nRows + nHead, oP = oQ + nRows, kBuf = oP + nP, oV = 2 * kBuf, oX = oV + (TEAM ? 4 : 2 * NW);
   __shared__ __align__(16) char lds[(oX + (TEAM ? nX : 0)) * 1024];
   const int lane = threadIdx.x & 63, wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, lg = lane >> 4;
@@ -383,7 +383,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
   }
 
   if (role == 1) {
-    Frag<kOut> xs[KD], xu[KC];
+    Frag<kW> xs[KD], xu[KC];
     f32x4 nt[RT];
     float eg[RT];
     const auto put_o = [&](uint32_t t0, int64_t unit, int buf) {  // (rows v, columns t)
@@ -394,17 +394,17 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
         Frag<kIn> fq[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) fq[i] = row_frag<kIn>(q_img, i * KD + ks);
-        mm_tiles<kOut, 0, RT, true>(o, fq, xs[ks]);
+        mm_tiles<kW, 0, RT, true>(o, fq, xs[ks]);
       }
 #pragma unroll
       for (int i = 0; i < RT; ++i) o[i] *= eg[i];
       static_for<KC>([&](auto kt) {
-        Frag<kOut> fp[RT];
+        Frag<kW> fp[RT];
 #pragma unroll
-        for (int i = 2 * kt.value; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(p_img, lower_frag(i, kt.value));
-        mm_tiles<kOut, 2 * kt.value, RT, true>(o, fp, xu[kt.value]);
+        for (int i = 2 * kt.value; i < RT; ++i) fp[i] = lds_frag<kW, kW>(p_img, lower_frag(i, kt.value));
+        mm_tiles<kW, 2 * kt.value, RT, true>(o, fp, xu[kt.value]);
       });
-      if (A.saved) put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
+      if (A.saved) put_image<RT, kGrad>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
       store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
     };
     for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
@@ -413,12 +413,12 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
       lds_read();
       __syncthreads();  // S0 and N are there
 #pragma unroll
-      for (int ks = 0; ks < KD; ++ks) xs[ks] = lds_frag<kOut, kOut>(x, ks);
+      for (int ks = 0; ks < KD; ++ks) xs[ks] = lds_frag<kW, kW>(x, ks);
       const float* gate = reinterpret_cast<const float*>(lds + (buf * kBuf + nRows + Rec::oGate) * 1024);
-      char* xn = x + KD * kOut * 1024;
+      char* xn = x + KD * kW * 1024;
 #pragma unroll
       for (int kt = 0; kt < KC; ++kt)
-        xu[kt] = frag_of<kOut>(*lds_tile(xn + 2 * kt * 1024) * gate4(gate, C, kBeta, rho(2 * kt, 4 * lg)),
+        xu[kt] = frag_of<kW>(*lds_tile(xn + 2 * kt * 1024) * gate4(gate, C, kBeta, rho(2 * kt, 4 * lg)),
                                *lds_tile(xn + (2 * kt + 1) * 1024) * gate4(gate, C, kBeta, rho(2 * kt + 1, 4 * lg)));
       if (A.saved)
 #pragma unroll
@@ -483,7 +483,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
     }
     if (A.saved && v0 < z.dv) {
       lds_read();
-      store_block<DT>(S, A.saved + unit * A.saved_floats + A.image_floats + v0 * z.dk, z.dk, TEAM ? x + KD * kOut * 1024 : lds + v_tile(0));
+      store_block<DT>(S, A.saved + unit * A.saved_floats + A.image_floats + v0 * z.dk, z.dk, TEAM ? x + KD * kW * 1024 : lds + v_tile(0));
     }
 
     // K S0 (rows t, columns v) and its transposed Q S0 (rows v, columns t)
@@ -494,13 +494,13 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
 #pragma unroll
       for (int i = 0; i < RT; ++i) fk[i] = row_frag<kIn>(img, i * KD + ks);
       if (TEAM) {
-        lds_put<kOut>(x, ks, f[ks]);
+        lds_put<kW>(x, ks, f[ks]);
       } else {
 #pragma unroll
         for (int i = 0; i < RT; ++i) fq[i] = row_frag<kIn>(img + oQ * 1024, i * KD + ks);
       }
       mm_tiles<kW, 0, RT>(ks0, fk, f[ks]);
-      if (!TEAM) mm_tiles<kOut, 0, RT, true>(o, fq, f[ks]);
+      if (!TEAM) mm_tiles<kW, 0, RT, true>(o, fq, f[ks]);
     }
     if (!TEAM)
 #pragma unroll
@@ -526,21 +526,21 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
         f32x4 nt[RT];  // with rows v and columns t
         lds_read();
         turn_tiles<RT>(nt, U, lds + v_tile(0));
-        put_image<RT, kOut>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
+        put_image<RT, kGrad>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
       }
       if (t0 + C < r1) next_v(t0 + C);
     }
     if (TEAM) {
 #pragma unroll
-      for (int i = 0; i < RT; ++i) *lds_tile(x + (KD * kOut + i) * 1024) = U[i];
+      for (int i = 0; i < RT; ++i) *lds_tile(x + (KD * kW + i) * 1024) = U[i];
     } else {
       static_for<KC>([&](auto kt) {
         constexpr int k = 2 * kt.value;
-        const Frag<kOut> fu = frag_of<kOut>(U[k] * gate4(gate, C, kBeta, rho(k, 4 * lg)), U[k + 1] * gate4(gate, C, kBeta, rho(k + 1, 4 * lg)));
-        Frag<kOut> fp[RT];
+        const Frag<kW> fu = frag_of<kW>(U[k] * gate4(gate, C, kBeta, rho(k, 4 * lg)), U[k + 1] * gate4(gate, C, kBeta, rho(k + 1, 4 * lg)));
+        Frag<kW> fp[RT];
 #pragma unroll
-        for (int i = k; i < RT; ++i) fp[i] = lds_frag<kOut, kOut>(img + oP * 1024, lower_frag(i, kt.value));
-        mm_tiles<kOut, k, RT, true>(o, fp, fu);
+        for (int i = k; i < RT; ++i) fp[i] = lds_frag<kW, kW>(img + oP * 1024, lower_frag(i, kt.value));
+        mm_tiles<kW, k, RT, true>(o, fp, fu);
       });
       store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
     }

@@ -48,7 +48,7 @@ struct ChainArgs {
 template <typename T, int DK, bool TEAM>
 __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArgs<T> A) {
   typedef Unit<T, true> Rec;
-  constexpr int kIn = DeltaType<T>::kIn, kOut = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
+  constexpr int kIn = DeltaType<T>::kIn, kGrad = DeltaType<T>::kGrad, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
   constexpr int NW = TEAM ? 1 : 8;
   // fragments in LDS: two buffers of K, the inverse and the gates, P and Q; dO of each wave (TEAM: two); what the team hands on
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
   };
   // dV, and dY's image, from dY with rows v and columns t
   const auto put_y = [&](const f32x4 (&yt)[RT], const float* gate, int ch, int64_t unit) {
-    put_image<RT, kOut>(yt, A.dy + unit * (C * dvp * kOut), v0, z.dv, dvp / 32);
+    put_image<RT, kGrad>(yt, A.dy + unit * (C * dvp * kGrad), v0, z.dv, dvp / 32);
     f32x4 dv[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) dv[i] = yt[i] * gate[kBeta * C + rho(i, c)];
@@ -329,7 +329,7 @@ __device__ __forceinline__ void pair_of(int p, int& i, int& j) {
 // dO come to LDS past the registers, the states' rows into registers meanwhile.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(DeltaSizes z, GradArgs<T> A) {
-  constexpr int kIn = DeltaType<T>::kIn, kW = DeltaType<T>::kOut, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
+  constexpr int kIn = DeltaType<T>::kIn, kW = DeltaType<T>::kGrad, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int NW = (DK > DV ? DK : DV) / 16, RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, KV = DV / 32;
   constexpr int kFrags = KC * (KC + 1), kPairs = 2 * kFrags, kMine = (kPairs + NW - 1) / NW;  // pair tiles, of a wave
   // 1024-byte fragments of the images
