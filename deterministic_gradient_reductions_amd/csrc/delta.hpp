@@ -603,21 +603,20 @@ __device__ __forceinline__ void next_state(f32x4 (&S)[DT], Frag<N> (&f)[DT / 2],
   });
 }
 
-// Tokens per chunk, words of an input, words of what the last kernel of a backward reads beside the
-// states. float32 takes half the chunk: its operands have three words.
+// Tokens per chunk, words of an input. float32 takes half the chunk: its operands have three words.
 template <typename T>
 struct DeltaType;
 template <>
 struct DeltaType<uint16_t> {
-  static constexpr int kLogC = 6, kIn = 1, kGrad = 2;
+  static constexpr int kLogC = 6, kIn = 1;
 };
 template <>
 struct DeltaType<float> {
-  static constexpr int kLogC = 5, kIn = 3, kGrad = 3;
+  static constexpr int kLogC = 5, kIn = 3;
 };
-// Words of everything else: of what reaches a float32 state, whose errors stay, and of what reaches o. (o of a
-// bf16 call in two words, 16 bits: 0.35 % of its values were another bf16 value than the rounded exact one, now 0.01 to
-// 0.03 % as from float32; 32768 tokens 1254 and 1293 us.)
+// Words of everything else, states and what is only ever rounded to bf16 alike. (o of a bf16 call in two words, 16 bits:
+// 0.35 % of its values were another bf16 value than the rounded exact one, in three 0.01 to 0.03 % as from float32;
+// 32768 tokens 1254 and 1293 us. The gradients: see delta_bwd.hip.)
 constexpr int kStateWords = 3;
 
 // exp(hi + lo) of a difference of two-word sums
@@ -660,11 +659,8 @@ inline int delta_pad(int64_t d) { return d <= 64 ? 64 : 128; }
 inline bool delta_teams(const DeltaSizes& z) { return static_cast<int64_t>(z.S) * z.H <= 80; }
 
 // What a forward leaves for the backward per (chunk, value head): N as an image of rows t and
-// places v in kGrad words, then the state in front of the chunk in blocks of 16 columns, in floats.
-inline int64_t delta_image_floats(int64_t dv, int dtype) {
-  const int64_t words = dtype == DET_BF16 ? DeltaType<uint16_t>::kGrad : DeltaType<float>::kGrad;
-  return delta_chunk(dtype) * delta_pad(dv) * words / 2;
-}
+// places v in kStateWords words, then the state in front of the chunk in blocks of 16 columns, in floats.
+inline int64_t delta_image_floats(int64_t dv, int dtype) { return delta_chunk(dtype) * delta_pad(dv) * kStateWords / 2; }
 inline int64_t delta_block_floats(int64_t dk, int64_t dv) { return dk * static_cast<int64_t>(align_up(static_cast<size_t>(dv), 16)); }
 inline int64_t delta_saved_floats(int64_t dk, int64_t dv, int dtype) { return delta_image_floats(dv, dtype) + delta_block_floats(dk, dv); }
 

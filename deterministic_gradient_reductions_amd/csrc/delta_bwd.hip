@@ -21,10 +21,11 @@
 // side: in it a wave owns tiles of token pairs first, then 16 channels of dQ and dK;
 // the pair matrices change hands in LDS.
 //
-// 16384 tokens in 8 sequences, 32 heads of 128 x 128, bf16: the chains 430 to 570 us, bound by memory
-// (0.94 GB written) while all run and by the longest one after; the last kernel 560 to 600 us for 1.7 GB read.
-// There N, dY and dO arrive before the pair tiles and the states' rows under them (643 -> 588 us),
-// and the next head's under the last products (-> 569 us).
+// 16384 tokens in 8 sequences, 32 heads of 128 x 128, bf16: the chains 450 to 600 us, bound by memory
+// (1.0 GB written) while all run and by the longest one after; the last kernel 700 to 800 us for 2.0 GB read.
+// There N, dY and dO arrive before the pair tiles and the states' rows under them, and most of the next head's under
+// the last products. (N, dY, the pair matrices and the states in two words, 16 bits, took 560 to 650 us, but 0.3 to 0.4 %
+// of dq, dk and dbeta were another bf16 value than the rounded exact one; in three as many as from float32, 0.01 to 0.03 %.)
 #include "delta.hpp"
 
 namespace detgrad {
@@ -48,7 +49,7 @@ struct ChainArgs {
 template <typename T, int DK, bool TEAM>
 __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArgs<T> A) {
   typedef Unit<T, true> Rec;
-  constexpr int kIn = DeltaType<T>::kIn, kGrad = DeltaType<T>::kGrad, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
+  constexpr int kIn = DeltaType<T>::kIn, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, kW = kStateWords;
   constexpr int NW = TEAM ? 1 : 8;
   // fragments in LDS: two buffers of K, the inverse and the gates, P and Q; dO of each wave (TEAM: two); what the team hands on
@@ -125,7 +126,7 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
   };
   // dV, and dY's image, from dY with rows v and columns t
   const auto put_y = [&](const f32x4 (&yt)[RT], const float* gate, int ch, int64_t unit) {
-    put_image<RT, kGrad>(yt, A.dy + unit * (C * dvp * kGrad), v0, z.dv, dvp / 32);
+    put_image<RT, kW>(yt, A.dy + unit * (C * dvp * kW), v0, z.dv, dvp / 32);
     f32x4 dv[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) dv[i] = yt[i] * gate[kBeta * C + rho(i, c)];
@@ -327,15 +328,22 @@ __device__ __forceinline__ void pair_of(int p, int& i, int& j) {
 
 // Workgroup (tile, hk): one chunk of one key head, its value heads in turn. N, dY, K and
 // dO come to LDS past the registers, the states' rows into registers meanwhile.
+//
+// For a bf16 call's 128 channels of v LDS has no room for the pair matrices beside N, dY and dO. There (kShare) they wait
+// in registers and take the place of dO and of the end of dY, whose next ones come after them.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(DeltaSizes z, GradArgs<T> A) {
-  constexpr int kIn = DeltaType<T>::kIn, kW = DeltaType<T>::kGrad, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
+  constexpr int kIn = DeltaType<T>::kIn, kW = kStateWords, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
   constexpr int NW = (DK > DV ? DK : DV) / 16, RT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32, KV = DV / 32;
   constexpr int kFrags = KC * (KC + 1), kPairs = 2 * kFrags, kMine = (kPairs + NW - 1) / NW;  // pair tiles, of a wave
   // 1024-byte fragments of the images
   constexpr int nK = RT * KD * kIn, nO = RT * KV * kIn, nV = RT * KV * kW, nTri = kFrags * kW,
                 nGate = Unit<T, true>::nGate;
-  constexpr int oQ = nK, oO = 2 * nK, oN = oO + nO, oY = oN + nV, oA = oY + nV, oZ = oA + nTri, oGate = oZ + nTri;
+  constexpr bool kShare = 2 * nK + nO + 2 * nV + 2 * nTri + 2 * nGate > 148;
+  constexpr int oQ = nK, oN = 2 * nK, oY = oN + nV, oO = oY + nV, oA = oO + nO - (kShare ? 2 * nTri : 0), oZ = oA + nTri,
+                oGate = oZ + nTri;
+  constexpr int kEarly = kShare ? oA - oY : nV;  // of dY's fragments
+  static_assert(!kShare || (2 * nTri >= nO && kEarly > 0), "dO and an end of dY");
   __shared__ __align__(16) char lds[(oGate + 2 * nGate) * 1024];
   __shared__ float red_q[NW][C], red_w[NW][C], red_s[NW], diag[C];
   // E's sums over four columns j from 4 m on, per row (padded: rows start on banks of their own); its crossing sums with
@@ -350,49 +358,75 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
   int e;
   uint32_t t0, t1, s0, s1;
   if (!segment_tile<1>(z.offs, z.S, static_cast<uint32_t>(z.T), kLogC, tile, e, t0, t1, s0, s1)) return;
-  fetch_rows<RT, KD, kIn, NW>(lds0, A.k, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
-  fetch_rows<RT, KD, kIn, NW, 4>(lds0 + oQ * 1024, A.q, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
   f32x4 dq[RT] = {}, dk[RT] = {};  // rows d, columns t
   f32x4 qk[kMine], kk[kMine];      // of this wave's pair tiles
-  const auto fetch_head = [&](int h, int buf) {
-    const int wave = here(wave_), n = here(static_cast<int>(t1 - t0));
+  f32x4 xs[KV][2], xd[KV][2];      // the states' rows of this wave's channels
+  const auto fetch_head = [&](int h) {  // what nothing but N, dY and dO of the head before has to leave
+    const int wave = here(wave_), n = here(static_cast<int>(t1 - t0)), buf = (h - hk * group) & 1;
     const int64_t unit = static_cast<int64_t>(tile) * z.H + h;
     fetch_image<nV, NW>(lds0 + oN * 1024, reinterpret_cast<const uint16_t*>(A.saved + unit * A.saved_floats), wave);
-    fetch_image<nV, NW, nV / 4>(lds0 + oY * 1024, A.dy + unit * (nV * kFragElems), wave);
-    fetch_rows<RT, KV, kIn, NW, nV / 2>(lds0 + oO * 1024, A.d_o, t0, n - 1, h, wave);
+    fetch_image<kEarly, NW, nV / 4>(lds0 + oY * 1024, A.dy + unit * (nV * kFragElems), wave);
+    if (!kShare) fetch_rows<RT, KV, kIn, NW, nV / 2>(lds0 + oO * 1024, A.d_o, t0, n - 1, h, wave);
     fetch_image<nGate, NW, 7>(lds0 + (oGate + buf * nGate) * 1024, A.units + unit * Unit<T, true>::kElems + Unit<T, true>::oGate * kFragElems, wave);
   };
+  const auto fetch_late = [&](int h) {  // what the pair matrices have to leave
+    if constexpr (kShare) {
+      const int wave = here(wave_), n = here(static_cast<int>(t1 - t0));
+      const int64_t unit = static_cast<int64_t>(tile) * z.H + h;
+      fetch_image<nV - kEarly, NW>(lds0 + (oY + kEarly) * 1024, A.dy + unit * (nV * kFragElems) + kEarly * kFragElems, wave);
+      fetch_rows<RT, KV, kIn, NW, (nV - kEarly) / 4>(lds0 + oO * 1024, A.d_o, t0, n - 1, h, wave);
+    }
+  };
+  const auto load_states = [&](int h) {
+    const int wave = here(wave_), lane = here_lane(threadIdx.x) & 63, c = lane & 15, lg = lane >> 4;
+    if (DT != NW && wave >= DT) return;
+    const int64_t unit = static_cast<int64_t>(tile) * z.H + h;
+    const float *ps = A.saved + unit * A.saved_floats + A.image_floats, *pd = A.ds + unit * A.ds_floats;
+    const int d = rho(wave, c);
+    // (every load stays in its block; what lies behind dk or dv is masked below)
+#pragma unroll
+    for (int kv = 0; kv < KV; ++kv) {
+      const int block = 2 * kv + (lg >> 1);
+      const uint32_t off = static_cast<uint32_t>(((16 * block < z.dv ? block : 0) * z.dk + (d < z.dk ? d : 0)) * 16 + 8 * (lg & 1)) * 4u;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        xs[kv][u] = load_at<f32x4>(ps + 4 * u, off);
+        xd[kv][u] = load_at<f32x4>(pd + 4 * u, off);
+      }
+    }
+  };
+  // dP * D and Z of a pair tile as images of rows i and places j: row tile i, row c, places 4 lg .. of fragment j / 2
+  const auto put_pairs = [&](int i, int j, const f32x4& ps, const f32x4& pz) {
+    const int to = lower_frag(i, j >> 1) * kW * 1024 + row_place() * 16 + (j & 1) * 8;
+    uint32_t w0[kW], w1[kW], w2[kW], w3[kW];
+    split2<kW>(ps[0], ps[1], w0);
+    split2<kW>(ps[2], ps[3], w1);
+    split2<kW>(pz[0], pz[1], w2);
+    split2<kW>(pz[2], pz[3], w3);
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      *reinterpret_cast<uint64_t*>(img_a + to + w * 1024) = w0[w] | static_cast<uint64_t>(w1[w]) << 32;
+      *reinterpret_cast<uint64_t*>(img_z + to + w * 1024) = w2[w] | static_cast<uint64_t>(w3[w]) << 32;
+    }
+  };
   const int h0 = hk * group;
-  fetch_head(h0, 0);
+  fetch_rows<RT, KD, kIn, NW>(lds0, A.k, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
+  fetch_rows<RT, KD, kIn, NW, 4>(lds0 + oQ * 1024, A.q, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
+  fetch_head(h0);
+  fetch_late(h0);
 
   for (int h = h0; h < h0 + group; ++h) {
     const int wave = here(wave_), lane = here_lane(threadIdx.x) & 63, c = lane & 15, lg = lane >> 4;
-    const int n = here(static_cast<int>(t1 - t0));
-    const int64_t unit = static_cast<int64_t>(tile) * z.H + h;
-    const float *ps = A.saved + unit * A.saved_floats + A.image_floats, *pd = A.ds + unit * A.ds_floats;
+    const int n = here(static_cast<int>(t1 - t0)), d = rho(wave, c);
     const float* gate = reinterpret_cast<const float*>(lds + (oGate + ((h - h0) & 1) * nGate) * 1024);
-    // the states' rows of this wave's channels, for the second phase
-    const int d = rho(wave, c);
-    f32x4 xs[KV][2], xd[KV][2];
-    if (DT == NW || wave < DT) {
-      // (every load stays in its block; what lies behind dk or dv is masked below)
-#pragma unroll
-      for (int kv = 0; kv < KV; ++kv) {
-        const int block = 2 * kv + (lg >> 1);
-        const uint32_t off = static_cast<uint32_t>(((16 * block < z.dv ? block : 0) * z.dk + (d < z.dk ? d : 0)) * 16 + 8 * (lg & 1)) * 4u;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          xs[kv][u] = load_at<f32x4>(ps + 4 * u, off);
-          xd[kv][u] = load_at<f32x4>(pd + 4 * u, off);
-        }
-      }
-      fetch_done_but<4 * KV>();  // (the states' rows are still on their way)
-    } else {
-      fetch_done();
-    }
+    const bool more = h + 1 < h0 + group;
+    load_states(h);
+    if (DT == NW || wave < DT) fetch_done_but<4 * KV>();  // (the states' rows are still on their way)
+    else fetch_done();
     __syncthreads();
 
     // The pair tiles, rows j and columns i: D, P, M, then dP, X and what comes of them.
+    f32x4 pd[kMine], zz[kMine];
     static_for<kMine>([&](auto mine) {
       constexpr int m = mine.value;
       const int p = wave + m * NW;
@@ -418,7 +452,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
       }
       const f32x4 b = gate4(gate, C, kBeta, at0), hj = gate4(gate, C, kGHi, at0), lj = gate4(gate, C, kGLo, at0);
       const float hi = gate[kGHi * C + row], li = gate[kGLo * C + row], bi = gate[kBeta * C + row];
-      f32x4 pd, zz, ev;
+      f32x4 ps, pz, ev;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int at = at0 + r;
@@ -426,8 +460,8 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
         const bool in = at <= row && row < n, off = at < row && row < n;
         const float dc = in ? decay(hi, li, hj[r], lj[r]) : 0.0f;
         const float dp = in ? b[r] * y[r] * dc * z.scale : 0.0f, bx = off ? b[r] * bi * x[r] * dc : 0.0f;
-        pd[r] = dp;
-        zz[r] = -bx;
+        ps[r] = dp;
+        pz[r] = -bx;
         ev[r] = off ? dp * qk[m][r] - bx * kk[m][r] : 0.0f;  // (no token's pair with itself crosses a t)
       }
       // a lane's four columns j are one run: t behind them takes them all, t among them those before it
@@ -439,36 +473,13 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
         if (c == 0) near_e[i][at0 + r] = ne;
         before += ev[r];
       }
-      // dP * D and Z as images of rows i and places j: row tile i, row c, places at0 .. of fragment j / 2
-      const int to = lower_frag(i, j >> 1) * kW * 1024 + row_place() * 16 + (j & 1) * 8;
-      uint32_t w0[kW], w1[kW], w2[kW], w3[kW];
-      split2<kW>(pd[0], pd[1], w0);
-      split2<kW>(pd[2], pd[3], w1);
-      split2<kW>(zz[0], zz[1], w2);
-      split2<kW>(zz[2], zz[3], w3);
-#pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        *reinterpret_cast<uint64_t*>(img_a + to + w * 1024) = w0[w] | static_cast<uint64_t>(w1[w]) << 32;
-        *reinterpret_cast<uint64_t*>(img_z + to + w * 1024) = w2[w] | static_cast<uint64_t>(w3[w]) << 32;
+      if (kShare) {
+        pd[m] = ps;
+        zz[m] = pz;
+      } else {
+        put_pairs(i, j, ps, pz);
       }
     });
-    __syncthreads();
-
-    // E's crossing sums for the t of a run, a lane per row i: its runs before that one, summed over the rows from t on
-    for (int m = wave; m < kRuns; m += NW) {
-      float p = 0.0f;
-#pragma unroll
-      for (int u = 0; u < kRuns; u += 4) {
-        const f32x4 w = *reinterpret_cast<const f32x4*>(&run_e[lane & (C - 1)][u]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) p += u + r < m ? w[r] : 0.0f;
-      }
-      f32x4 t;
-      t[3] = lanes_sum<64>(lane >= 4 * m + 4 && lane < C ? p : 0.0f);
-#pragma unroll
-      for (int r = 3; r >= 0; --r) t[r] = (r < 3 ? t[r + 1] : t[3]) + readlane(p, 4 * m + r);
-      if (lane == 0) *reinterpret_cast<f32x4*>(&far_e[4 * m]) = t;
-    }
 
     // 16 channels of dq and dk
     if (DT == NW || wave < DT) {
@@ -485,15 +496,21 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
             xd[kv][u][r] = in ? xd[kv][u][r] : 0.0f;
             inner = __builtin_fmaf(xs[kv][u][r], xd[kv][u][r], inner);
           }
-        const Frag<kW> fs = frag_of<kW>(xs[kv][0], xs[kv][1]), fd = frag_of<kW>(xd[kv][0], xd[kv][1]);
+        const Frag<kW> fd = frag_of<kW>(xd[kv][0], xd[kv][1]);
+        Frag<kW> f[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(lds + oN * 1024, i * KV + kv);
+        mm_tiles<kW, 0, RT, true>(s, f, fd);
+        step();
+      }
+#pragma unroll
+      for (int kv = 0; kv < KV; ++kv) {
+        const Frag<kW> fs = frag_of<kW>(xs[kv][0], xs[kv][1]);
         Frag<kW> f[RT];
         Frag<kIn> fo[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(lds + oY * 1024, i * KV + kv);
         mm_tiles<kW, 0, RT, true>(b, f, fs);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) f[i] = lds_frag<kW, kW>(lds + oN * 1024, i * KV + kv);
-        mm_tiles<kW, 0, RT, true>(s, f, fd);
 #pragma unroll
         for (int i = 0; i < RT; ++i) fo[i] = row_frag<kIn>(lds + oO * 1024, i * KV + kv);
         mm_tiles<kW, 0, RT, true>(a, fo, fs);
@@ -536,8 +553,37 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
       inner = lanes_sum<64>(inner);
       if (lane == 0) red_s[wave] = inner;
     }
+
     __syncthreads();  // N, dY and dO have been read
-    if (h + 1 < h0 + group) fetch_head(h + 1, (h + 1 - h0) & 1);
+    if (more) fetch_head(h + 1);
+    if constexpr (kShare) {
+      static_for<kMine>([&](auto mine) {
+        constexpr int m = mine.value;
+        const int p = wave + m * NW;
+        if (p >= kPairs) return;
+        int i, j;
+        pair_of(p, i, j);
+        put_pairs(i, j, pd[m], zz[m]);
+      });
+      __syncthreads();  // the pair matrices are there
+    }
+
+    // E's crossing sums for the t of a run, a lane per row i: its runs before that one, summed over the rows from t on
+    for (int m = wave; m < kRuns; m += NW) {
+      float p = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kRuns; u += 4) {
+        const f32x4 w = *reinterpret_cast<const f32x4*>(&run_e[lane & (C - 1)][u]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p += u + r < m ? w[r] : 0.0f;
+      }
+      f32x4 t;
+      t[3] = lanes_sum<64>(lane >= 4 * m + 4 && lane < C ? p : 0.0f);
+#pragma unroll
+      for (int r = 3; r >= 0; --r) t[r] = (r < 3 ? t[r + 1] : t[3]) + readlane(p, 4 * m + r);
+      if (lane == 0) *reinterpret_cast<f32x4*>(&far_e[4 * m]) = t;
+    }
+
     if (DT == NW || wave < DT) {
       static_for<KC>([&](auto kt) {
         constexpr int at = kt.value;
@@ -560,6 +606,7 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
       });
     }
     __syncthreads();
+    if (more) fetch_late(h + 1);
 
     // dbeta and dg, by the first wave: a lane per token
     if (wave == 0) {

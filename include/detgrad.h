@@ -572,8 +572,8 @@ int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t dh
  * own, det_delta_rule_states_size() chunks of H times so many floats, of which those past
  * the last chunk are left as they were; 16-byte aligned.
  * Computed in chunks on the matrix cores with float32 sums and float32 states:
- * inputs of DET_F32 and everything that reaches a state or o are carried in three bf16
- * words (24 bits), what the gradients of a DET_BF16 call are formed from at last in two. Any g is allowed; below -1e4
+ * every value but inputs of DET_BF16 is carried in three bf16 words (24 bits), so that
+ * outputs of DET_BF16 are float32 results rounded once. Any g is allowed; below -1e4
  * it counts as -1e4 (a decay of 0 either way), -inf included. The recurrence is as
  * stable as its decays and keys are: with g <= 0, keys of length at most 1 and beta
  * in [0, 2] no intermediate grows. NaN and infinities (float32 values above 3.38e38

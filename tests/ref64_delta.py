@@ -19,7 +19,7 @@ import torch
 from tests.ref64 import assert_close, bounds
 
 #: Roundings of one chunk on an output's path: sums over 128 channels and three times over 64 tokens, their
-#: operands' words (three, or what reaches only a bf16 output two: 2^-17 of it, far below its half step).
+#: operands' words.
 PER_CHUNK = 128 + 3 * 64 + 16
 
 

@@ -11,9 +11,6 @@ from tests.test_gpu_delta_rule import BF, F32, X, bwd, fwd, make, to_dev
 
 pytestmark = pytest.mark.gpu
 
-#: Roundings to two bf16 words (2^-17 of the value) on dg's path of a bf16 call: N, dY, S0 and dS1, each in two products.
-WORDS = 8
-
 
 def gates(kind, T, H, gen):
     if kind == "resets":     # kept otherwise: every eleventh token or so forgets, and neighbours do
@@ -30,8 +27,6 @@ def limits(dtype, mag, want, chunks, dv):
     the norm of all the magnitude is what products over dv channels have, whose signs are random here as are their
     errors': 1 / sqrt(dv) of the bound by norms."""
     sd = R.allowed(chunks) / 8.0 * 2.0 ** -24 * mag
-    if dtype == BF:
-        sd = sd + math.sqrt(WORDS) * 2.0 ** -17 * mag
     rounded = torch.finfo(dtype).eps / 2 * want.abs() + 2.0 ** -126
     return 8.0 * sd + rounded, (2.0 / math.sqrt(dv) * sd + rounded).norm().item()
 

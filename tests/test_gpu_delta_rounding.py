@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from tests import ref64_delta as R
-from tests.test_gpu_delta_rule import BF, X, fwd, make, to_dev
+from tests.test_gpu_delta_rule import BF, X, bwd, fwd, make, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,8 @@ def test_outputs_are_rounded_once(Hk, H, dk, dv, offs, g_scale):
     e = {n: x.float() if torch.is_tensor(x) and x.dtype == BF else x for n, x in d.items()}
     o, s1, _, kept = R.delta(*(h[n] for n in X), offs, h["s0"], dk ** -0.5)
     moved(fwd(d)["o"], fwd(e)["o"], o, "o")
+    # and its gradients
+    want, _ = R.delta_bwd(h["do"], kept, h["ds1"], H // Hk)
+    r, r32 = bwd(d, fwd(d)), bwd(e, fwd(e))
+    for name in ("dv", "dq", "dk", "dbeta", "dg"):
+        moved(r[name], r32[name], want[name], name)

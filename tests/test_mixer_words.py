@@ -1,0 +1,47 @@
+"""CPU replay of where the delta rule's kernels hold their operands in LDS, with three words for all but bf16 inputs
+(the same names as in their sources)."""
+import pytest
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("DK", [64, 128])
+def test_chains_fit(bf16, DK):
+    kIn, C = (1, 64) if bf16 else (3, 32)
+    RT, KC, KD, DT = C // 16, C // 32, DK // 32, DK // 16
+    tri, gates = 3 * KC * (KC + 1), -(-8 * C * 4 // 1024)
+    rows, head = RT * KD * kIn, tri + gates
+    buf = 2 * rows + head + tri
+    assert 2 * buf + max(4 + 3 * KD + RT, 4 + 2 * RT + DT, 16) <= 160
+    # the counted waits: at most 63 loads of a wave
+    assert rows + tri <= 63 and 2 * rows + head <= 63 and tri + 2 <= 63
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("DK", [64, 128])
+@pytest.mark.parametrize("DV", [64, 128])
+def test_gradients_fit_and_share(bf16, DK, DV):
+    kIn, C = (1, 64) if bf16 else (3, 32)
+    RT, KC, KD, KV, NW = C // 16, C // 32, DK // 32, DV // 32, max(DK, DV) // 16
+    nK, nO, nV, nTri, nGate = RT * KD * kIn, RT * KV * kIn, RT * KV * 3, KC * (KC + 1) * 3, -(-8 * C * 4 // 1024)
+    share = 2 * nK + nO + 2 * nV + 2 * nTri + 2 * nGate > 148
+    assert share == (bf16 and DV == 128)
+    oN = 2 * nK
+    oY = oN + nV
+    oO = oY + nV
+    oA = oO + nO - (2 * nTri if share else 0)
+    oZ = oA + nTri
+    oGate = oZ + nTri
+    early = oA - oY if share else nV
+    floats = 2 * NW * C + NW + C + C * (C // 4 + 4) + RT * C + C
+    assert (oGate + 2 * nGate) * 1024 + 4 * floats + 64 <= 163840
+    # fragments that a fetch of the next head may write while the pair matrices are read: none of theirs
+    first = set(range(oN, oN + nV)) | set(range(oY, oY + early)) | (set() if share else set(range(oO, oO + nO)))
+    late = (set(range(oY + early, oY + nV)) | set(range(oO, oO + nO))) if share else set()
+    pairs = set(range(oA, oA + 2 * nTri))
+    assert not first & pairs and not first & late
+    assert first | late == set(range(oN, oO + nO))
+    if share:
+        assert pairs <= late
+    else:
+        assert not pairs & set(range(0, oO + nO))
+    assert not (pairs | late) & set(range(oGate, oGate + 2 * nGate)) and not pairs & set(range(0, 2 * nK))
