@@ -404,7 +404,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
         for (int i = 2 * kt.value; i < RT; ++i) fp[i] = lds_frag<kW, kW>(p_img, lower_frag(i, kt.value));
         mm_tiles<kW, 2 * kt.value, RT, true>(o, fp, xu[kt.value]);
       });
-      if (A.saved) put_image<RT, kW>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
+      if (A.saved) put_image<RT>(nt, A.saved + unit * A.saved_floats, v0, z.dv, z.dv <= 64 ? 2 : 4);
       store_rows<RT>(o, A.o.row(t0, h), A.o.st, v0, z.dv, rows_at(t0));
     };
     for (uint32_t t0 = r0; t0 < r1; t0 += C, unit += z.H, buf ^= 1) {
@@ -526,7 +526,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaSizes z, FwdArgs<T>
         f32x4 nt[RT];  // with rows v and columns t
         lds_read();
         turn_tiles<RT>(nt, U, lds + v_tile(0));
-        put_image<RT, kW>(nt, reinterpret_cast<uint16_t*>(A.saved + unit * A.saved_floats), v0, z.dv, z.dv <= 64 ? 2 : 4);
+        put_image<RT>(nt, A.saved + unit * A.saved_floats, v0, z.dv, z.dv <= 64 ? 2 : 4);
       }
       if (t0 + C < r1) next_v(t0 + C);
     }

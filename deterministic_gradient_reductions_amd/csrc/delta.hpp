@@ -321,24 +321,21 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Results with rows v0 + 4 g + r and columns rho(i, c) as a part of an image with rows t and
-// places v (kv fragments of 32 per row tile), zeros from place dv on, nothing behind the image's.
-template <int RT, int NP>
-__device__ __forceinline__ void put_image(const f32x4 (&x)[RT], uint16_t* image, int v0, int dv, int kv) {
+// Results with rows v0 + 4 g + r and columns rho(i, c) as a part of a float32 image with rows t and
+// places v (kv fragments of 32 per row tile), zeros from place dv on, nothing behind the image's. A fragment is the first
+// four of its 64 lanes' eight places, then the others, so that it is stored and loaded in whole lines.
+constexpr int kFragFloats = 64 * 8;
+template <int RT>
+__device__ __forceinline__ void put_image(const f32x4 (&x)[RT], float* image, int v0, int dv, int kv) {
   const int lane = threadIdx.x & 63, c = lane & 15, v = v0 + 4 * (lane >> 4);
   if (v0 >= 32 * kv) return;
-  // places v .. v + 3 of row tile 0, row c
-  uint16_t* to = image + (v >> 5) * NP * kFragElems + (16 * ((v >> 3) & 3) + c) * 8 + (v & 7);
+  float* to = image + (v >> 5) * kFragFloats + ((v >> 2) & 1) * 256 + (16 * ((v >> 3) & 3) + c) * 4;
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
-    uint32_t a[NP], b[NP];
-    split2<NP>(v < dv ? x[i][0] : 0.0f, v + 1 < dv ? x[i][1] : 0.0f, a);
-    split2<NP>(v + 2 < dv ? x[i][2] : 0.0f, v + 3 < dv ? x[i][3] : 0.0f, b);
+    f32x4 y;
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const uint64_t w = a[p] | static_cast<uint64_t>(b[p]) << 32;
-      __builtin_memcpy(to + (i * kv * NP + p) * kFragElems, &w, 8);
-    }
+    for (int r = 0; r < 4; ++r) y[r] = v + r < dv ? x[i][r] : 0.0f;
+    *reinterpret_cast<f32x4*>(to + i * kv * kFragFloats) = y;
   }
 }
 
@@ -658,9 +655,9 @@ inline int delta_pad(int64_t d) { return d <= 64 ? 64 : 128; }
 // 338 and 313 us, eight 341 and 168 us; with the backward's states and the backward the same way round.
 inline bool delta_teams(const DeltaSizes& z) { return static_cast<int64_t>(z.S) * z.H <= 80; }
 
-// What a forward leaves for the backward per (chunk, value head): N as an image of rows t and
-// places v in kStateWords words, then the state in front of the chunk in blocks of 16 columns, in floats.
-inline int64_t delta_image_floats(int64_t dv, int dtype) { return delta_chunk(dtype) * delta_pad(dv) * kStateWords / 2; }
+// What a forward leaves for the backward per (chunk, value head), in floats: N as an image of rows t and
+// places v, then the state in front of the chunk in blocks of 16 columns.
+inline int64_t delta_image_floats(int64_t dv, int dtype) { return delta_chunk(dtype) * delta_pad(dv); }
 inline int64_t delta_block_floats(int64_t dk, int64_t dv) { return dk * static_cast<int64_t>(align_up(static_cast<size_t>(dv), 16)); }
 inline int64_t delta_saved_floats(int64_t dk, int64_t dv, int dtype) { return delta_image_floats(dv, dtype) + delta_block_floats(dk, dv); }
 

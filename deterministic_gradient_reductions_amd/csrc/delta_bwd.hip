@@ -39,7 +39,7 @@ struct ChainArgs {
   const uint16_t* units;
   const float* ds1;
   float *ds, *ds0;  // every chunk's dS1 in blocks, the initial state's gradient
-  uint16_t* dy;
+  float* dy;
   int ds_floats;
 };
 
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaSizes z, ChainArg
   };
   // dV, and dY's image, from dY with rows v and columns t
   const auto put_y = [&](const f32x4 (&yt)[RT], const float* gate, int ch, int64_t unit) {
-    put_image<RT, kW>(yt, A.dy + unit * (C * dvp * kW), v0, z.dv, dvp / 32);
+    put_image<RT>(yt, A.dy + unit * (C * dvp), v0, z.dv, dvp / 32);
     f32x4 dv[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) dv[i] = yt[i] * gate[kBeta * C + rho(i, c)];
@@ -310,8 +310,8 @@ struct GradArgs {
   Rows k, q, d_o;
   Heads<T> dq, dk;
   T *dg, *dbeta;
-  const uint16_t *dy, *units;
-  const float *saved, *ds;
+  const uint16_t* units;
+  const float *dy, *saved, *ds;
   int64_t dg_ld, dbeta_ld;
   int image_floats, saved_floats, ds_floats;
 };
@@ -326,11 +326,12 @@ __device__ __forceinline__ void pair_of(int p, int& i, int& j) {
   j = p < 4 ? p & 1 : (p - 4) & 3;
 }
 
-// Workgroup (tile, hk): one chunk of one key head, its value heads in turn. N, dY, K and
-// dO come to LDS past the registers, the states' rows into registers meanwhile.
+// Workgroup (tile, hk): one chunk of one key head, its value heads in turn. K, Q and dO come to LDS past the
+// registers, the states' rows into registers meanwhile. N and dY are float32 in memory (two thirds of their words) and
+// pass the registers, where each of their fragments becomes words once, under the last products of the head before.
 //
 // For a bf16 call's 128 channels of v LDS has no room for the pair matrices beside N, dY and dO. There (kShare) they wait
-// in registers and take the place of dO and of the end of dY, whose next ones come after them.
+// in registers and take the place of dY, whose next one waits in registers for them.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(DeltaSizes z, GradArgs<T> A) {
   constexpr int kIn = DeltaType<T>::kIn, kW = kStateWords, kLogC = DeltaType<T>::kLogC, C = 1 << kLogC;
@@ -340,10 +341,10 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
   constexpr int nK = RT * KD * kIn, nO = RT * KV * kIn, nV = RT * KV * kW, nTri = kFrags * kW,
                 nGate = Unit<T, true>::nGate;
   constexpr bool kShare = 2 * nK + nO + 2 * nV + 2 * nTri + 2 * nGate > 148;
-  constexpr int oQ = nK, oN = 2 * nK, oY = oN + nV, oO = oY + nV, oA = oO + nO - (kShare ? 2 * nTri : 0), oZ = oA + nTri,
-                oGate = oZ + nTri;
-  constexpr int kEarly = kShare ? oA - oY : nV;  // of dY's fragments
-  static_assert(!kShare || (2 * nTri >= nO && kEarly > 0), "dO and an end of dY");
+  constexpr int oQ = nK, oN = 2 * nK, oO = oN + nV, oY = oO + nO, oA = kShare ? oY : oY + nV, oZ = oA + nTri,
+                oGate = kShare ? oY + nV : oZ + nTri;
+  static_assert(2 * nTri <= nV || !kShare, "the pair matrices in dY's place");
+  constexpr int nF = RT * KV, kEach = (nF + NW - 1) / NW;  // fragments of N and of dY, of a wave
   __shared__ __align__(16) char lds[(oGate + 2 * nGate) * 1024];
   __shared__ float red_q[NW][C], red_w[NW][C], red_s[NW], diag[C];
   // E's sums over four columns j from 4 m on, per row (padded: rows start on banks of their own); its crossing sums with
@@ -361,20 +362,31 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
   f32x4 dq[RT] = {}, dk[RT] = {};  // rows d, columns t
   f32x4 qk[kMine], kk[kMine];      // of this wave's pair tiles
   f32x4 xs[KV][2], xd[KV][2];      // the states' rows of this wave's channels
-  const auto fetch_head = [&](int h) {  // what nothing but N, dY and dO of the head before has to leave
+  typedef f32x4 Mine[kEach][2];  // this wave's fragments of N or dY
+  const auto fetch_head = [&](int h, Mine& rn, Mine& ry) {
     const int wave = here(wave_), n = here(static_cast<int>(t1 - t0)), buf = (h - hk * group) & 1;
+    const uint32_t at = static_cast<uint32_t>(here_lane(threadIdx.x) & 63) * 16u;
     const int64_t unit = static_cast<int64_t>(tile) * z.H + h;
-    fetch_image<nV, NW>(lds0 + oN * 1024, reinterpret_cast<const uint16_t*>(A.saved + unit * A.saved_floats), wave);
-    fetch_image<kEarly, NW, nV / 4>(lds0 + oY * 1024, A.dy + unit * (nV * kFragElems), wave);
-    if (!kShare) fetch_rows<RT, KV, kIn, NW, nV / 2>(lds0 + oO * 1024, A.d_o, t0, n - 1, h, wave);
+    const float *pn = A.saved + unit * A.saved_floats, *py = A.dy + unit * (nF * kFragFloats);
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int f = wave + u * NW;
+      if (nF % NW && f >= nF) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        rn[u][e] = load_at<f32x4>(pn + f * kFragFloats + e * 256, at);
+        ry[u][e] = load_at<f32x4>(py + f * kFragFloats + e * 256, at);
+      }
+    }
+    fetch_rows<RT, KV, kIn, NW>(lds0 + oO * 1024, A.d_o, t0, n - 1, h, wave);
     fetch_image<nGate, NW, 7>(lds0 + (oGate + buf * nGate) * 1024, A.units + unit * Unit<T, true>::kElems + Unit<T, true>::oGate * kFragElems, wave);
   };
-  const auto fetch_late = [&](int h) {  // what the pair matrices have to leave
-    if constexpr (kShare) {
-      const int wave = here(wave_), n = here(static_cast<int>(t1 - t0));
-      const int64_t unit = static_cast<int64_t>(tile) * z.H + h;
-      fetch_image<nV - kEarly, NW>(lds0 + (oY + kEarly) * 1024, A.dy + unit * (nV * kFragElems) + kEarly * kFragElems, wave);
-      fetch_rows<RT, KV, kIn, NW, (nV - kEarly) / 4>(lds0 + oO * 1024, A.d_o, t0, n - 1, h, wave);
+  const auto put_words = [&](int at, const Mine& x) {
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int f = here(wave_) + u * NW;
+      if (nF % NW && f >= nF) continue;
+      lds_put<kW>(lds + at * 1024, f, frag_of<kW>(x[u][0], x[u][1]));
     }
   };
   const auto load_states = [&](int h) {
@@ -412,8 +424,12 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
   const int h0 = hk * group;
   fetch_rows<RT, KD, kIn, NW>(lds0, A.k, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
   fetch_rows<RT, KD, kIn, NW, 4>(lds0 + oQ * 1024, A.q, t0, static_cast<int>(t1 - t0) - 1, hk, wave_);
-  fetch_head(h0);
-  fetch_late(h0);
+  {
+    Mine rn, ry;
+    fetch_head(h0, rn, ry);
+    put_words(oN, rn);
+    put_words(oY, ry);
+  }
 
   for (int h = h0; h < h0 + group; ++h) {
     const int wave = here(wave_), lane = here_lane(threadIdx.x) & 63, c = lane & 15, lg = lane >> 4;
@@ -555,7 +571,8 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
     }
 
     __syncthreads();  // N, dY and dO have been read
-    if (more) fetch_head(h + 1);
+    Mine rn = {}, ry = {};  // (no values of the head before, which would stay in registers all the way)
+    if (more) fetch_head(h + 1, rn, ry);
     if constexpr (kShare) {
       static_for<kMine>([&](auto mine) {
         constexpr int m = mine.value;
@@ -605,8 +622,12 @@ __global__ __launch_bounds__(4 * (DK > DV ? DK : DV)) void delta_grad_kernel(Del
         step();
       });
     }
+    if (more) {
+      put_words(oN, rn);
+      if (!kShare) put_words(oY, ry);
+    }
     __syncthreads();
-    if (more) fetch_late(h + 1);
+    if (kShare && more) put_words(oY, ry);
 
     // dbeta and dg, by the first wave: a lane per token
     if (wave == 0) {
@@ -735,10 +756,10 @@ extern "C" int det_delta_rule_bwd(const void* d_o, int64_t do_st, int64_t do_sh,
   {                                                                                                                    \
     const ChainArgs<E> A{r.k, r.q, {static_cast<const E*>(d_o), do_st, do_sh},                                         \
                          {static_cast<E*>(dv_out), dv_st, dv_sh}, words(l.units), dfinal_state, ds, dinitial_state,    \
-                         words(l.dy), block};                                                                          \
+                         reinterpret_cast<float*>(base + l.dy), block};                                                \
     const GradArgs<E> B{r.k, r.q, r.d_o, {static_cast<E*>(dq), dq_st, dq_sh},                                          \
                         {static_cast<E*>(dk_out), dk_st, dk_sh}, static_cast<E*>(dg), static_cast<E*>(dbeta),          \
-                        words(l.dy), words(l.units), states, ds, dg_ld, dbeta_ld,           \
+                        words(l.units), reinterpret_cast<const float*>(base + l.dy), states, ds, dg_ld, dbeta_ld,      \
                         image, saved, block};                                                                          \
     if (dk <= 64) launch_chain<E, 64>(z, A, st);                                                                       \
     else launch_chain<E, 128>(z, A, st);                                                                               \

@@ -26,22 +26,15 @@ def test_gradients_fit_and_share(bf16, DK, DV):
     share = 2 * nK + nO + 2 * nV + 2 * nTri + 2 * nGate > 148
     assert share == (bf16 and DV == 128)
     oN = 2 * nK
-    oY = oN + nV
-    oO = oY + nV
-    oA = oO + nO - (2 * nTri if share else 0)
+    oO = oN + nV
+    oY = oO + nO
+    oA = oY if share else oY + nV
     oZ = oA + nTri
-    oGate = oZ + nTri
-    early = oA - oY if share else nV
+    oGate = oY + nV if share else oZ + nTri
     floats = 2 * NW * C + NW + C + C * (C // 4 + 4) + RT * C + C
     assert (oGate + 2 * nGate) * 1024 + 4 * floats + 64 <= 163840
-    # fragments that a fetch of the next head may write while the pair matrices are read: none of theirs
-    first = set(range(oN, oN + nV)) | set(range(oY, oY + early)) | (set() if share else set(range(oO, oO + nO)))
-    late = (set(range(oY + early, oY + nV)) | set(range(oO, oO + nO))) if share else set()
+    # what comes for the next head while the pair matrices are read: none of theirs
+    n, y, o = range(oN, oN + nV), range(oY, oY + nV), range(oO, oO + nO)
     pairs = set(range(oA, oA + 2 * nTri))
-    assert not first & pairs and not first & late
-    assert first | late == set(range(oN, oO + nO))
-    if share:
-        assert pairs <= late
-    else:
-        assert not pairs & set(range(0, oO + nO))
-    assert not (pairs | late) & set(range(oGate, oGate + 2 * nGate)) and not pairs & set(range(0, 2 * nK))
+    assert not pairs & (set(n) | set(o) | set(range(2 * nK)) | set(range(oGate, oGate + 2 * nGate)))
+    assert pairs <= set(y) if share else not pairs & set(y)
