@@ -24,10 +24,10 @@
 // shared by the workgroup through LDS. What is not on the chain of states is formed
 // before it.
 //
-// 32768 tokens of one sequence, 32 heads of 128 x 128, bf16: 190 us for P and the inverses (0.27 GB
-// read and 0.52 GB written, 4.1 TB/s) and 1130 us for the chains, 2.2 us a chunk, of which the 132 matrix instructions of the wave
-// that carries the state are 0.9 us. 16384 tokens of 8 sequences, with what the backward needs: 115 and
-// 430 to 570 us, by the longest (0.94 GB written, 4.9 TB/s in all while all chains run).
+// 32768 tokens of one sequence, 32 heads of 128 x 128, bf16: 1301 us, most of it the chains, 2.2 us a chunk, of which the
+// 132 matrix instructions of the wave that carries the state are 0.9 us. Under a profiler, whose passes are slower (1434 us
+// in all): 214 us for P and the inverses (0.27 GB read and 0.64 GB written) and 1221 us for the chains. There, too, 16384
+// tokens of 8 sequences with what the backward needs take 127 and 450 to 640 us, by the longest (0.97 GB written).
 #include "delta.hpp"
 
 namespace detgrad {

@@ -650,9 +650,15 @@ inline int delta_pad(int64_t d) { return d <= 64 ? 64 : 128; }
 
 // The workgroups of the chains of states: eight waves for all columns of a head, which share its
 // fragments, or a team of three waves for 16 columns. A team's chunk takes 2.2 us, the eight waves'
-// 5.9 to 6.5 us, but there are eight times as many teams for the compute units. 8192 tokens in all, 32 heads of
-// 128 x 128, bf16, teams and eight waves: one sequence 336 and 780 us, two 324 and 425 us, three
-// 338 and 313 us, eight 341 and 168 us; with the backward's states and the backward the same way round.
+// 5.9 to 6.5 us, but there are eight times as many teams for the compute units. Whole calls of 32 heads with sequences of
+// equal length, teams and eight waves, us:
+//   8192 tokens, 128 x 128, bf16, forward: one sequence 372 and 927, two 352 and 505, three 368 and 380, eight 373 and 200;
+//     with the backward's states 510 and 1088, 512 and 611, 533 and 473, 531 and 263; backward, two and three: 877 and
+//     988, 886 and 838
+//   4096 tokens, 128 x 128, float32, forward: two 380 and 509, three 387 and 392, eight 403 and 257
+//   64 x 64 halves the teams, which are better up to about 160 chains there: forward of 8192 tokens in bf16, three 201 and
+//     281, four 164 and 221, five 197 and 201, eight 170 and 151
+// The bound is that of 128 columns for all. The lengths are on the device: sequences without tokens count too.
 inline bool delta_teams(const DeltaSizes& z) { return static_cast<int64_t>(z.S) * z.H <= 80; }
 
 // What a forward leaves for the backward per (chunk, value head), in floats: N as an image of rows t and

@@ -21,9 +21,9 @@
 // side: in it a wave owns tiles of token pairs first, then 16 channels of dQ and dK;
 // the pair matrices change hands in LDS.
 //
-// 16384 tokens in 8 sequences, 32 heads of 128 x 128, bf16: the chains 450 to 600 us, bound by memory
-// (1.0 GB written) while all run and by the longest one after; the last kernel 700 to 800 us for 2.0 GB read.
-// There N, dY and dO arrive before the pair tiles and the states' rows under them, and most of the next head's under
+// 16384 tokens in 8 sequences, 32 heads of 128 x 128, bf16: the chains 440 to 580 us, bound by memory
+// (0.97 GB written) while all run and by the longest one after; the last kernel 710 to 800 us for 1.9 GB read.
+// There N, dY and dO arrive before the pair tiles and the states' rows under them, and the next head's under
 // the last products. (N, dY, the pair matrices and the states in two words, 16 bits, took 560 to 650 us, but 0.3 to 0.4 %
 // of dq, dk and dbeta were another bf16 value than the rounded exact one; in three as many as from float32, 0.01 to 0.03 %.)
 #include "delta.hpp"

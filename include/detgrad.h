@@ -570,7 +570,10 @@ int det_block_norm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t dh
  * every chunk of 64 tokens (DET_F32: 32), counted from each sequence's first: the state
  * in front of it and what the recurrence took up in it, in a layout of the library's
  * own, det_delta_rule_states_size() chunks of H times so many floats, of which those past
- * the last chunk are left as they were; 16-byte aligned.
+ * the last chunk are left as they were; 16-byte aligned. They are large (dk = dv = 128: 96 KiB
+ * a chunk and head for DET_BF16, 80 KiB for DET_F32; 0.83 GB for 16384 tokens of 8 sequences and 32
+ * heads): a second forward call with states right in front of the backward gives the same
+ * bits as states kept from the first.
  * Computed in chunks on the matrix cores with float32 sums and float32 states:
  * every value but inputs of DET_BF16 is carried in three bf16 words (24 bits), so that
  * outputs of DET_BF16 are float32 results rounded once. Any g is allowed; below -1e4
